@@ -131,6 +131,9 @@ enum {
                                          -DMOE_CHECKED): a computed index failed its
                                          check and the access was skipped */
 
+#define MOE_DEV_ERR_NAN_LOGIT 16      /* moe_router_topk met a NaN logit (or a NaN biased
+                                         score): that expert was treated as masked */
+
 typedef struct moe_shape {
   int64_t T; /* tokens (>= 0) */
   int64_t H; /* hidden size (multiple of 128) */
@@ -480,6 +483,181 @@ MOE_API moe_status moe_quantize_fp8_blocks(const void* w, int64_t G, int64_t N, 
  * block scale = E4M3(amax/(6*global)), code = E2M1(x/(block*global)). */
 MOE_API moe_status moe_quantize_nvfp4_rows(const void* x, int64_t R, int64_t Kd, const float* global,
                                    void* packed, void* scales, void* stream);
+
+/* -------------------------------------------- operators around the layer */
+
+/* Element types of the operators below. */
+enum {
+  MOE_ELEM_F32 = 0,
+  MOE_ELEM_BF16 = 1,
+  MOE_ELEM_F16 = 2
+};
+
+/* A row-major matrix on the device: element (r, c) at data[r * stride + c],
+ * stride in elements, at least the number of columns when there is more than
+ * one row.  Where a call takes a const moe_rows*, NULL (or NULL data) means an
+ * optional matrix that is absent. */
+typedef struct moe_rows {
+  void* data;
+  int64_t stride;
+} moe_rows;
+
+/* ------------------------------------------------------------- layer norm */
+
+typedef struct moe_norm {
+  int64_t rows;        /* >= 0 */
+  int64_t H;           /* columns, 1 .. 2^20 */
+  int32_t dtype;       /* MOE_ELEM_* of the row matrices */
+  int32_t param_dtype; /* MOE_ELEM_* of weight and bias: dtype, or MOE_ELEM_F32 */
+  float eps;           /* finite, >= 0 */
+} moe_norm;
+
+/* Layer norm of every row, with the residual sum in front of it when there is
+ * one (the norm before the router and the dispatch of a pre-norm MoE block):
+ *   h[r]    = x[r] + residual[r], rounded to dtype (x[r] without a residual)
+ *   mean[r] = sum_c h[r][c] / H,  rstd[r] = 1 / sqrt(sum_c (h[r][c] - mean[r])^2 / H + eps)
+ *   y[r]    = (h[r] - mean[r]) * rstd[r] * weight + bias, rounded to dtype
+ * Sums, statistics and the formula are fp32; the variance is taken about the
+ * mean, not from a sum of squares.  weight, bias: device [H] of param_dtype, or
+ * NULL (1 and 0).  sum: h (optional; may be x or residual itself, with the same
+ * stride, and must not overlap them otherwise); it needs a residual.  mean,
+ * rstd: device fp32 [rows], each optional; the backward pass reads both.  y
+ * must not overlap an input.  Any row stride and any alignment of an element;
+ * 16-byte aligned rows (base, stride, H) take the 128-bit path. */
+MOE_API moe_status moe_layer_norm(const moe_norm* norm, const moe_rows* x, const moe_rows* residual,
+                                  const void* weight, const void* bias, const moe_rows* y, const moe_rows* sum,
+                                  float* mean, float* rstd, void* stream);
+
+/* Device workspace bytes of moe_layer_norm_backward (host only): fp32 partial
+ * sums of the weight's and the bias's gradients. */
+MOE_API moe_status moe_layer_norm_workspace_size(int64_t rows, int64_t H, size_t* bytes_out);
+
+/* Backward of moe_layer_norm.  With xhat = (h - mean) * rstd, u = grad_y * weight:
+ *   grad_x[r]   = rstd[r] * (u[r] - sum_c u[r][c] / H - xhat[r] * sum_c (u[r][c] * xhat[r][c]) / H)
+ *                 (+ grad_sum[r] when given), rounded to dtype once
+ *   grad_weight = sum_r grad_y[r] * xhat[r],  grad_bias = sum_r grad_y[r]   (fp32 [H])
+ * h is the row the forward pass normalised (its sum output when it had a
+ * residual); grad_sum, the gradient that reaches that sum by the residual
+ * stream.  grad_x is then the gradient of x and of the residual alike.
+ * mean, rstd: fp32 [rows] from the forward pass.  grad_weight, grad_bias: each
+ * optional, overwritten; both sums are formed in an order fixed by the shape
+ * and the device's SM count, without atomics, so repeated calls agree bit for
+ * bit.  workspace (used when either is wanted): device, 16-byte aligned, of at
+ * least moe_layer_norm_workspace_size bytes, no initialisation; calls that
+ * share one must not overlap on the GPU.  grad_x may be grad_y or grad_sum
+ * itself (same stride) and must not overlap an input otherwise. */
+MOE_API moe_status moe_layer_norm_backward(const moe_norm* norm, const moe_rows* grad_y, const moe_rows* h,
+                                           const void* weight, const float* mean, const float* rstd,
+                                           const moe_rows* grad_sum, const moe_rows* grad_x, float* grad_weight,
+                                           float* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------------- router */
+
+/* Score functions of the router. */
+enum {
+  MOE_SCORE_SOFTMAX = 0, /* softmax over the token's experts */
+  MOE_SCORE_SIGMOID = 1  /* sigmoid of each logit */
+};
+
+typedef struct moe_router {
+  int64_t T;            /* tokens (>= 0, T*E < 2^40) */
+  int64_t E;            /* experts (1..1024) */
+  int64_t K;            /* routes per token (1..128, K <= E) */
+  int32_t logits_dtype; /* MOE_ELEM_* */
+  int32_t score;        /* MOE_SCORE_* */
+  int32_t renormalize;  /* nonzero: the chosen scores are divided by their sum */
+  float scale;          /* the weights' last factor (finite) */
+} moe_router;
+
+/* Top-k router: from the logits to the routing map and the probabilities that
+ * moe_preprocess, moe_dispatch_permute and moe_combine_unpermute read.  For
+ * every token the K experts of the largest selection score are chosen, ties to
+ * the lowest expert; the score is the logit, and with select_bias (device fp32
+ * [E], or NULL) logit + bias for MOE_SCORE_SOFTMAX and sigmoid(logit) + bias for
+ * MOE_SCORE_SIGMOID, in fp32.  The bias takes part in the selection alone.  With
+ * s the softmax over all experts of the token or the sigmoid, the weights are
+ *   w(e) = scale * s(e)   or, renormalized,   scale * s(e) / sum over the chosen of s
+ * in fp32.  An expert whose logit (or biased score) is -inf is masked: it is
+ * never chosen and takes no part in the softmax; a NaN is treated the same way
+ * and reported (MOE_DEV_ERR_NAN_LOGIT is or-ed into *status when status is not
+ * NULL).  A +inf logit takes the whole softmax (shared evenly among several).  A
+ * token with fewer than K experts left has that many routes, maybe none.
+ * map_format MOE_ROUTING_DENSE_I16: map int16 [T][K], the chosen ids ascending,
+ * then -1; probs fp32 [T][K], 0 beside -1.  MOE_ROUTING_SPARSE_BOOL: map uint8
+ * [T][E], probs fp32 [T][E], 0 off the map.  Both give the same slots: slot k is
+ * the k-th chosen expert in ascending order.  logits: rows of logits_dtype. */
+MOE_API moe_status moe_router_topk(const moe_router* router, const moe_rows* logits, const float* select_bias,
+                                   int32_t map_format, void* map, float* probs, int32_t* status, void* stream);
+
+/* Backward of moe_router_topk: the gradient of the logits from the gradients of
+ * the probabilities (the layout of map_format, as moe_dispatch_backward writes
+ * grad_probs; entries off the map or beside -1 are ignored).  The choice itself
+ * has no gradient.  With g the gradients of the chosen weights, 0 elsewhere:
+ *   softmax:               grad(e) = scale * s(e) * (g(e) - sum over the chosen of g s)
+ *   sigmoid:               grad(e) = scale * s(e) * (1 - s(e)) * g(e)
+ *   renormalized, n = s / sum over the chosen of s, for the chosen (0 elsewhere):
+ *     grad(e) = scale * n(e) * d(e) * (g(e) - sum of g n),  d = 1 (softmax), 1 - s(e) (sigmoid)
+ * grad_logits: rows of logits_dtype, rounded once; every entry is written.  The
+ * ids of a token's dense map must differ; ids outside [-1, E) are ignored. */
+MOE_API moe_status moe_router_topk_backward(const moe_router* router, const moe_rows* logits, int32_t map_format,
+                                            const void* map, const float* grad_probs, const moe_rows* grad_logits,
+                                            void* stream);
+
+/* ------------------------- matrix-vector products with 4-bit weights ------ */
+
+/* Weights of four bits with a scale per group of consecutive elements of a row:
+ *   w[n][k] = (q[n][k] - z[n][k / group]) * scale[n][k / group]
+ * codes: two per byte, even k in the low nibble, [N][Kd/2]; scales: [N][G] of
+ * dtype, G = ceil(Kd / group); zeros: the z as codes are packed, [N][ceil(G/2)]
+ * bytes, or NULL for z = 8.  Several matrices follow one another. */
+typedef struct moe_w4 {
+  int64_t N;          /* rows of a matrix (output features), 1 .. 2^24 */
+  int64_t Kd;         /* columns (input features), a multiple of 32, <= 2^20 */
+  int32_t group;      /* 32, 64 or 128 */
+  int32_t dtype;      /* MOE_ELEM_BF16 or MOE_ELEM_F16: scales, inputs and outputs */
+  const void* codes;  /* device, 16-byte aligned */
+  const void* scales; /* device */
+  const void* zeros;  /* device or NULL */
+} moe_w4;
+
+/* What follows the product. */
+enum {
+  MOE_W4_NONE = 0,
+  MOE_W4_SWIGLU = 1 /* rows 0..N/2-1 are up, N/2..N-1 gate (the w3_w1 order of
+                       moe_grouped_mlp): silu(gate) * up, N/2 output features */
+};
+
+/* y[m] = act( W x[m] ) (+ addend[m]), rounded to dtype once: products of few
+ * tokens with one weight matrix (a shared expert or a projection of a decode
+ * step).  (q - z) and x are exact operands of tensor-core products summed in
+ * fp32 per group; each group's sum is scaled in fp32.  x: M rows of Kd (16-byte
+ * aligned, stride a multiple of 8); y: M rows of N (N/2 with SwiGLU; N must be
+ * even); addend: optional, as y (it may be y itself), only without SwiGLU.  y
+ * must not overlap x.  Any M >= 0; the weights are read once per 32 tokens. */
+MOE_API moe_status moe_w4_matvec(const moe_w4* w, int64_t M, const moe_rows* x, int32_t activation,
+                                 const moe_rows* addend, const moe_rows* y, void* stream);
+
+/* The same per expert over dispatched rows, for decode batches: w holds E
+ * matrices, x is the dispatched buffer (capacity rows of Kd) and for every
+ * routed row r of expert e below the capacity
+ *   y[r] = act( W[e] x[r] ).
+ * shape: T, E and K are read (H and I are not).  Pad rows are neither read nor
+ * written, nor are rows at or beyond the capacity.  Two calls run FC1 with
+ * SwiGLU and FC2 of an expert MLP between moe_dispatch_permute and
+ * moe_combine_unpermute. */
+MOE_API moe_status moe_grouped_w4_matvec(const moe_handle_dev* handle, const moe_shape* shape,
+                                         const moe_layout* layout, const moe_w4* w, const moe_rows* x,
+                                         int32_t activation, const moe_rows* y, void* stream);
+
+/* Rows [R][Kd] of dtype (contiguous) -> codes, scales and (when zeros is not
+ * NULL) zero points in the layout of moe_w4.  Without zeros: scale = amax / 7
+ * rounded to dtype, q = rint(w / scale) + 8 clamped to [0, 15].  With zeros, over
+ * the group's range widened to hold 0: scale = (max - min) / 15 rounded to
+ * dtype, z = rint(-min / scale), q = rint(w / scale) + z, both clamped to
+ * [0, 15].  A scale that rounds to 0 becomes 1.  fp32 arithmetic, ties to even.
+ * A one-time weight preparation step. */
+MOE_API moe_status moe_quantize_w4_rows(const void* w, int64_t R, int64_t Kd, int32_t group, int32_t dtype,
+                                        void* codes, void* scales, void* zeros, void* stream);
 
 /* ------------------------------------------------------------ buffer ring */
 

@@ -50,6 +50,17 @@ DEV_ERR_BAD_EXPERT = 1
 DEV_ERR_TOO_MANY_ROUTES = 2
 DEV_ERR_TIMEOUT = 4
 DEV_ERR_BOUNDS = 8  # bounds-checked builds only
+DEV_ERR_NAN_LOGIT = 16
+
+ELEM_F32 = 0
+ELEM_BF16 = 1
+ELEM_F16 = 2
+
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+
+W4_NONE = 0
+W4_SWIGLU = 1
 
 
 class _Shape(ctypes.Structure):
@@ -73,6 +84,26 @@ class _HandleDev(ctypes.Structure):
 class _Nvfp4Globals(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("fc1_input_scale", "fc2_input_scale", "w13_scale_2",
                                                "w2_scale_2")]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("H", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class _Router(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("logits_dtype", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class _W4(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("Kd", ctypes.c_int64), ("group", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
 # Every symbol include/moe.h declares, with its ctypes signature.
@@ -116,6 +147,19 @@ _SIGNATURES = {
                                          ctypes.POINTER(_HandleDev), _P, ctypes.c_size_t, ctypes.c_int64, _P],
     "moe_quantize_fp8_blocks": [_P, _I64, _I64, _I64, _P, _P, _P],
     "moe_quantize_nvfp4_rows": [_P, _I64, _I64, _P, _P, _P, _P],
+    "moe_layer_norm": [ctypes.POINTER(_Norm), ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _P, _P,
+                       ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _P, _P, _P],
+    "moe_layer_norm_workspace_size": [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_layer_norm_backward": [ctypes.POINTER(_Norm), ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _P, _P, _P,
+                                ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_router_topk": [ctypes.POINTER(_Router), ctypes.POINTER(_Rows), _P, ctypes.c_int32, _P, _P, _P, _P],
+    "moe_router_topk_backward": [ctypes.POINTER(_Router), ctypes.POINTER(_Rows), ctypes.c_int32, _P, _P,
+                                 ctypes.POINTER(_Rows), _P],
+    "moe_w4_matvec": [ctypes.POINTER(_W4), _I64, ctypes.POINTER(_Rows), ctypes.c_int32, ctypes.POINTER(_Rows),
+                      ctypes.POINTER(_Rows), _P],
+    "moe_grouped_w4_matvec": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout),
+                              ctypes.POINTER(_W4), ctypes.POINTER(_Rows), ctypes.c_int32, ctypes.POINTER(_Rows), _P],
+    "moe_quantize_w4_rows": [_P, _I64, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P],
     "moe_ring_create": [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_P)],
     "moe_ring_acquire": [_P, _P, ctypes.POINTER(ctypes.c_int32)],
     "moe_ring_release": [_P, ctypes.c_int32, _P],
@@ -415,6 +459,205 @@ def moe_quantize_nvfp4_rows(x: torch.Tensor, global_scale: torch.Tensor, packed:
     R = x.numel() // Kd
     _check(_lib.moe_quantize_nvfp4_rows(_ptr(x), R, Kd, _ptr(global_scale), _ptr(packed), _ptr(scales),
                                         _stream(stream)), "moe_quantize_nvfp4_rows")
+
+
+# ------------------------------------------- operators around the layer
+
+_ELEM = {torch.float32: ELEM_F32, torch.bfloat16: ELEM_BF16, torch.float16: ELEM_F16}
+
+
+def _elem(t: torch.Tensor) -> int:
+    if t.dtype not in _ELEM:
+        raise ValueError(f"float32, bfloat16 or float16 tensor expected, got {t.dtype}")
+    return _ELEM[t.dtype]
+
+
+def _rows(t: Optional[torch.Tensor], name: str, rows: int, cols: int, dtype: torch.dtype):
+    """A 2-D tensor with unit column stride as a moe_rows; rows may lie apart."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name}: device tensor expected")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: shape {(rows, cols)} expected, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: adjacent columns expected (stride(1) == 1)")
+    return ctypes.byref(_Rows(t.data_ptr(), t.stride(0) if rows > 1 else cols))
+
+
+def _dense(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
+    """A contiguous tensor of this shape and type as a pointer."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: 2-D tensor expected")
+    return t.shape
+
+
+def _norm_desc(x: torch.Tensor, weight, bias, eps: float):
+    rows, H = _matrix(x, "x")
+    params = [p for p in (weight, bias) if p is not None]
+    pdtype = params[0].dtype if params else x.dtype
+    if any(p.dtype != pdtype for p in params):
+        raise ValueError("weight and bias: one dtype expected")
+    if pdtype not in (x.dtype, torch.float32):
+        raise ValueError(f"weight, bias: {x.dtype} or float32 expected, got {pdtype}")
+    return _Norm(rows, H, _elem(x), _ELEM[pdtype], eps), rows, H, pdtype
+
+
+def moe_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], eps: float,
+                   y: torch.Tensor, residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                   mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y = layer_norm(x + residual) * weight + bias per row of x [rows, H]; sum_out
+    takes the residual sum, mean and rstd (float [rows]) what the backward reads."""
+    n, rows, H, pdtype = _norm_desc(x, weight, bias, eps)
+    _check(_lib.moe_layer_norm(ctypes.byref(n), _rows(x, "x", rows, H, x.dtype),
+                               _rows(residual, "residual", rows, H, x.dtype), _dense(weight, "weight", (H,), pdtype),
+                               _dense(bias, "bias", (H,), pdtype), _rows(y, "y", rows, H, x.dtype),
+                               _rows(sum_out, "sum_out", rows, H, x.dtype),
+                               _dense(mean, "mean", (rows,), torch.float32),
+                               _dense(rstd, "rstd", (rows,), torch.float32), _stream(stream)), "moe_layer_norm")
+
+
+def moe_layer_norm_workspace_size(rows: int, H: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.moe_layer_norm_workspace_size(rows, H, ctypes.byref(out)), "moe_layer_norm_workspace_size")
+    return out.value
+
+
+def moe_layer_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor],
+                            mean: torch.Tensor, rstd: torch.Tensor, grad_x: torch.Tensor,
+                            grad_weight: Optional[torch.Tensor] = None, grad_bias: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, grad_sum: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """Gradients of moe_layer_norm; h is the normalised row matrix (x, or sum_out
+    where there was a residual) and grad_sum the gradient that reaches it past
+    the norm.  workspace is needed for grad_weight / grad_bias (float [H])."""
+    n, rows, H, pdtype = _norm_desc(h, weight, None, 0.0)
+    f32 = torch.float32
+    _check(_lib.moe_layer_norm_backward(
+        ctypes.byref(n), _rows(grad_y, "grad_y", rows, H, h.dtype), _rows(h, "h", rows, H, h.dtype),
+        _dense(weight, "weight", (H,), pdtype), _dense(mean, "mean", (rows,), f32), _dense(rstd, "rstd", (rows,), f32),
+        _rows(grad_sum, "grad_sum", rows, H, h.dtype), _rows(grad_x, "grad_x", rows, H, h.dtype),
+        _dense(grad_weight, "grad_weight", (H,), f32), _dense(grad_bias, "grad_bias", (H,), f32), _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)),
+        "moe_layer_norm_backward")
+
+
+@dataclasses.dataclass(frozen=True)
+class Router:
+    """Top-k router over E experts: score SCORE_SOFTMAX or SCORE_SIGMOID; with
+    renormalize the chosen scores are divided by their sum; scale multiplies the
+    weights last (see moe_router in moe.h)."""
+    E: int
+    K: int
+    score: int = SCORE_SOFTMAX
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def c(self, T: int, dtype: int):
+        return _Router(T, self.E, self.K, dtype, self.score, 1 if self.renormalize else 0, self.scale)
+
+    def map_shape(self, fmt: int, T: int):
+        return (T, self.E) if fmt == ROUTING_SPARSE_BOOL else (T, self.K)
+
+
+_MAP_DTYPE = {ROUTING_DENSE_I16: torch.int16, ROUTING_SPARSE_BOOL: torch.uint8}
+
+
+def _map(routing: Routing, router: Router, T: int):
+    if routing.format not in _MAP_DTYPE:
+        raise ValueError("unknown routing format")
+    return _dense(routing.map, "routing.map", router.map_shape(routing.format, T), _MAP_DTYPE[routing.format])
+
+
+def moe_router_topk(router: Router, logits: torch.Tensor, routing: Routing,
+                    select_bias: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """Writes routing.map and routing.probs (both required) from logits [T, E];
+    status (int32 [1], optional) collects DEV_ERR_NAN_LOGIT."""
+    T, _ = _matrix(logits, "logits")
+    probs = _dense(routing.probs, "routing.probs", router.map_shape(routing.format, T), torch.float32)
+    _check(_lib.moe_router_topk(ctypes.byref(router.c(T, _elem(logits))),
+                                _rows(logits, "logits", T, router.E, logits.dtype),
+                                _dense(select_bias, "select_bias", (router.E,), torch.float32), routing.format,
+                                _map(routing, router, T), probs, _dense(status, "status", (1,), torch.int32),
+                                _stream(stream)), "moe_router_topk")
+
+
+def moe_router_topk_backward(router: Router, logits: torch.Tensor, routing: Routing, grad_probs: torch.Tensor,
+                             grad_logits: torch.Tensor, stream=None) -> None:
+    """grad_logits [T, E] from grad_probs in the layout of routing.map."""
+    T, _ = _matrix(logits, "logits")
+    _check(_lib.moe_router_topk_backward(
+        ctypes.byref(router.c(T, _elem(logits))), _rows(logits, "logits", T, router.E, logits.dtype), routing.format,
+        _map(routing, router, T),
+        _dense(grad_probs, "grad_probs", router.map_shape(routing.format, T), torch.float32),
+        _rows(grad_logits, "grad_logits", T, router.E, logits.dtype), _stream(stream)), "moe_router_topk_backward")
+
+
+@dataclasses.dataclass
+class W4Weight:
+    """4-bit weights with group scales: codes uint8 [N, Kd/2] (or [E, N, Kd/2], one
+    matrix per expert), scales bfloat16 / float16 [.., N, ceil(Kd/group)], zeros
+    uint8 [.., N, ceil(ceil(Kd/group)/2)] or None (z = 8); see moe_w4 in moe.h."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: Optional[torch.Tensor]
+    group: int
+
+    def c(self, lead=()):
+        if self.codes.dim() != len(lead) + 2 or self.group < 1:
+            raise ValueError(f"codes: {len(lead) + 2}-D tensor expected, got {tuple(self.codes.shape)}")
+        N, Kd = self.codes.shape[-2], self.codes.shape[-1] * 2
+        G = (Kd + self.group - 1) // self.group
+        return _W4(N, Kd, self.group, _elem(self.scales),
+                   _dense(self.codes, "codes", (*lead, N, Kd // 2), torch.uint8),
+                   _dense(self.scales, "scales", (*lead, N, G), self.scales.dtype),
+                   _dense(self.zeros, "zeros", (*lead, N, (G + 1) // 2), torch.uint8)), N, Kd
+
+
+def moe_w4_matvec(weight: W4Weight, x: torch.Tensor, y: torch.Tensor, activation: int = W4_NONE,
+                  addend: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y [M, N or N/2] = act(x [M, Kd] . W^T) (+ addend)."""
+    w, N, Kd = weight.c()
+    M, _ = _matrix(x, "x")
+    dt, n_out = weight.scales.dtype, N // 2 if activation == W4_SWIGLU else N
+    _check(_lib.moe_w4_matvec(ctypes.byref(w), M, _rows(x, "x", M, Kd, dt), activation,
+                              _rows(addend, "addend", M, n_out, dt), _rows(y, "y", M, n_out, dt), _stream(stream)),
+           "moe_w4_matvec")
+
+
+def moe_grouped_w4_matvec(handle: Handle, shape: Shape, layout: Layout, weight: W4Weight, x: torch.Tensor,
+                          y: torch.Tensor, activation: int = W4_NONE, stream=None) -> None:
+    """moe_w4_matvec of every dispatched row x [cap, Kd] with its expert's matrix, into y [cap, N or N/2]."""
+    w, N, Kd = weight.c((shape.E,))
+    dt, n_out = weight.scales.dtype, N // 2 if activation == W4_SWIGLU else N
+    _check(_lib.moe_grouped_w4_matvec(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()),
+                                      ctypes.byref(w), _rows(x, "x", layout.capacity, Kd, dt), activation,
+                                      _rows(y, "y", layout.capacity, n_out, dt), _stream(stream)),
+           "moe_grouped_w4_matvec")
+
+
+def moe_quantize_w4_rows(w: torch.Tensor, group: int, codes: torch.Tensor, scales: torch.Tensor,
+                         zeros: Optional[torch.Tensor] = None, stream=None) -> None:
+    """w [.., Kd] (bfloat16 / float16) -> the tensors of a W4Weight."""
+    lead, Kd = tuple(w.shape[:-1]), w.shape[-1]
+    R = w.numel() // Kd if Kd else 0
+    G = (Kd + group - 1) // group if group > 0 else 0
+    _check(_lib.moe_quantize_w4_rows(_ptr(w), R, Kd, group, _elem(w),
+                                     _dense(codes, "codes", (*lead, Kd // 2), torch.uint8),
+                                     _dense(scales, "scales", (*lead, G), w.dtype),
+                                     _dense(zeros, "zeros", (*lead, (G + 1) // 2), torch.uint8), _stream(stream)),
+           "moe_quantize_w4_rows")
 
 
 class Ring:

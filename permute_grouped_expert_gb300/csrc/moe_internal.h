@@ -83,6 +83,25 @@ cudaError_t launch_combine_mx(const moe_handle_dev& h, const moe_shape& s, int32
 cudaError_t launch_quantize_mx_rows(const void* x, int64_t R, int64_t H, int32_t format, void* codes, void* scales,
                                     cudaStream_t st);
 
+// Operators around the layer: layer norm (layer_norm.cu), router (router.cu),
+// 4-bit matrix-vector products (w4_matvec.cu).  Optional matrices are NULL.
+size_t layer_norm_workspace_bytes(int64_t rows, int64_t H);
+cudaError_t launch_layer_norm(const moe_norm& n, const moe_rows& x, const moe_rows* res, const void* w, const void* b,
+                              const moe_rows& y, const moe_rows* sum, float* mean, float* rstd, cudaStream_t st);
+cudaError_t launch_layer_norm_backward(const moe_norm& n, const moe_rows& gy, const moe_rows& h, const void* w,
+                                       const float* mean, const float* rstd, const moe_rows* gsum, const moe_rows& gx,
+                                       float* gw, float* gb, void* workspace, cudaStream_t st);
+cudaError_t launch_router_topk(const moe_router& r, const moe_rows& logits, const float* bias, int32_t format,
+                               void* map, float* probs, int32_t* status, cudaStream_t st);
+cudaError_t launch_router_topk_backward(const moe_router& r, const moe_rows& logits, int32_t format, const void* map,
+                                        const float* grad_probs, const moe_rows& grad_logits, cudaStream_t st);
+cudaError_t launch_w4_matvec(const moe_w4& w, int64_t M, const moe_rows& x, int32_t activation,
+                             const moe_rows* addend, const moe_rows& y, cudaStream_t st);
+cudaError_t launch_grouped_w4_matvec(const moe_handle_dev& h, const moe_shape& s, const moe_layout& l, const moe_w4& w,
+                                     const moe_rows& x, int32_t activation, const moe_rows& y, cudaStream_t st);
+cudaError_t launch_quantize_w4_rows(const void* w, int64_t R, int64_t Kd, int32_t group, int32_t dtype, void* codes,
+                                    void* scales, void* zeros, cudaStream_t st);
+
 int device_sm_count();
 
 // Runs a per-device setup step (a kernel attribute such as its dynamic
