@@ -43,6 +43,7 @@ struct W4Params {
   const int32_t* counts;
   const int32_t* offsets;
   int E;
+  bool every;  // blockIdx.y is the expert; else it counts the experts that have rows
   int64_t cap;
 };
 
@@ -58,7 +59,7 @@ struct Pair<__nv_bfloat16> {
     return *reinterpret_cast<uint32_t*>(&r);
   }
   static MOE_DEVICE void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -74,7 +75,7 @@ struct Pair<__half> {
     return *reinterpret_cast<uint32_t*>(&r);
   }
   static MOE_DEVICE void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -92,6 +93,11 @@ MOE_DEVICE uint32_t code_pair(uint32_t w, int i, uint32_t zz) {
 template <typename T>
 MOE_DEVICE uint32_t zero_pair(uint32_t z) {
   return Pair<T>::kMagic | z << Pair<T>::kShift | z << (16 + Pair<T>::kShift);
+}
+
+template <typename T>
+MOE_DEVICE float scale_bits(uint16_t b) {
+  return to_float(*reinterpret_cast<T*>(&b));
 }
 
 // The a-th expert with rows below the capacity, or -1; every thread calls it.
@@ -115,110 +121,210 @@ MOE_DEVICE int nth_active_expert(const W4Params& p, int a) {
   return -1;
 }
 
-// GROUP: elements a scale; NT: tiles of 8 tokens a pass; RT: 2 with SwiGLU (up, gate)
-template <typename T, int GROUP, int NT, int RT>
-__global__ void __launch_bounds__(kThreads) w4_matvec_kernel(W4Params p) {
-  constexpr int LK = GROUP / 4;  // k values a lane takes of a group, for each of its two rows
-  constexpr int W = LK / 8;      // 32-bit words they fill
-  __shared__ float red[kWarps][RT][NT * 8][kTokStride];
+// A warp's tile of codes for one step: 32 weight rows x 128 k (64 bytes a row)
+// in shared memory, 16-byte chunks exchanged by row so that the fragment reads
+// of every group size touch each bank once.
+constexpr int kStepK = 128;
+constexpr int kRowBytes = kStepK / 2;
+constexpr int kWarpRows = 32;
+constexpr int kStageBytes = kWarpRows * kRowBytes;
+constexpr int kStages = 6;
+
+MOE_DEVICE int chunk_at(int row, int chunk) {
+  return row * kRowBytes + ((chunk ^ ((row >> 1 & 1) << 1 | (row >> 2 & 1))) << 4);
+}
+
+MOE_DEVICE void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+MOE_DEVICE void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+MOE_DEVICE void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// GROUP: elements a scale; NT: tiles of 8 tokens a pass.  wk warps of a CTA
+// share the K steps of the same 32 weight rows: neighbouring rows, or with
+// SwiGLU the up and the gate rows of 16 features.
+template <typename T, int GROUP, int NT, bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int wk) {
+  constexpr int U = kStepK / GROUP;                    // groups a step
+  constexpr int W = GROUP / 32;                        // 32-bit code words a lane takes of a group and row
+  constexpr int kFeatures = SWIGLU ? 16 : kWarpRows;   // output features of a warp's rows
+  extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gr = lane >> 2, c = lane & 3;
-  const int64_t n_out = RT == 2 ? p.N / 2 : p.N;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int blocks = kWarps / wk;  // row blocks of a CTA
+  const int64_t n_out = SWIGLU ? p.N / 2 : p.N;
+  const int64_t cta_n0 = (int64_t)blockIdx.x * blocks * kFeatures;
+  const int64_t n0 = cta_n0 + (warp / wk) * kFeatures;
+  const int split = warp % wk;
 
   int64_t first = 0, M = p.M, e = 0;
   if (p.counts) {
-    const int a = nth_active_expert(p, blockIdx.y);
-    if (a < 0) return;
-    e = a;
-    first = p.offsets[a];
-    M = min64(first + p.counts[a], p.cap) - first;
+    e = p.every ? (int)blockIdx.y : nth_active_expert(p, blockIdx.y);
+    if (e < 0) return;
+    first = p.offsets[e];
+    M = min64(first + p.counts[e], p.cap) - first;
+    if (M <= 0) return;
   }
   const uint8_t* codes = p.codes + e * p.N * (p.Kd / 2);
-  const T* scales = static_cast<const T*>(p.scales) + e * p.N * p.G;
+  const uint16_t* scales = static_cast<const uint16_t*>(p.scales) + e * p.N * p.G;
   const uint8_t* zeros = p.zeros ? p.zeros + e * p.N * p.zero_bytes : nullptr;
   const T* x = static_cast<const T*>(p.x) + first * p.sx;
 
-  int64_t row[RT][2];
+  // Row r of the warp's tile is weight row n0 + r, with SwiGLU row n0 + r of the
+  // up half and n0 + r - 16 of the gate half; rows past the end are read again
+  // and not stored.  Lane (gr, c) copies chunk c of rows gr, gr + 8, ... and
+  // holds the products of the same rows: offsets from the tile's first row.
+  const int64_t last = n_out - 1 - n0;
+  uint32_t rel[4];
 #pragma unroll
-  for (int rt = 0; rt < RT; rt++)
+  for (int q = 0; q < 4; q++) {
+    const int r = SWIGLU ? (q & 1) * 8 + gr : q * 8 + gr;
+    rel[q] = (uint32_t)min64(r, last);
+  }
+  const uint32_t row_bytes = (uint32_t)(p.Kd / 2), G = (uint32_t)p.G, zero_bytes = (uint32_t)p.zero_bytes;
+  const uint8_t* codes_at[2];
+  const uint16_t* scales_at[2];
+  const uint8_t* zeros_at[2];
 #pragma unroll
-    for (int h = 0; h < 2; h++) row[rt][h] = min64(n0 + gr + 8 * h, n_out - 1) + rt * n_out;  // past the end: unused
+  for (int rt = 0; rt < 2; rt++) {
+    const int64_t r0 = n0 + (SWIGLU && rt ? n_out : 0);
+    codes_at[rt] = codes + r0 * row_bytes;
+    scales_at[rt] = scales + r0 * G;
+    zeros_at[rt] = zeros ? zeros + r0 * zero_bytes : nullptr;
+  }
+
+  uint8_t* ring = smem + warp * (kStages * kStageBytes);
+  const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
+  const int steps = (int)((p.Kd + kStepK - 1) / kStepK);
+  const int mine = n0 < n_out && split < steps ? (steps - split + wk - 1) / wk : 0;
+
+  auto fill = [&](int it) {
+    if (it < mine) {
+      const int step = split + it * wk;
+      const bool in = (int64_t)step * kStepK + c * 32 < p.Kd;  // Kd is a multiple of 32, a chunk 32 elements
+      const uint32_t dst = ring_u32 + (it % kStages) * kStageBytes;
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        cp_async16(dst + chunk_at(q * 8 + gr, c),
+                   codes_at[q >> 1] + (in ? rel[q] * row_bytes + (uint32_t)(step * kRowBytes + c * 16) : 0u), in);
+    }
+    cp_async_commit();
+  };
 
   for (int64_t t0 = 0; t0 < M; t0 += 8 * NT) {
-    float acc[RT][NT][4] = {};
-    for (int64_t g = warp; g < p.G; g += kWarps) {
-      const int64_t k = g * GROUP + c * LK;
-      const bool in = k < p.Kd;  // the last group may be short by whole lanes
-      uint32_t w[RT][2][W];
-      float s[RT][2];
-      uint32_t zz[RT][2];
+    float acc[2][NT][4] = {};
 #pragma unroll
-      for (int rt = 0; rt < RT; rt++)
+    for (int i = 0; i < kStages - 1; i++) fill(i);
+    for (int it = 0; it < mine; it++) {
+      const int step = split + it * wk;
+      // scales and zero points of this step, while its codes arrive
+      uint16_t sc[4][U];
+      uint8_t zp[4][U];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(codes + (row[rt][h] * p.Kd + k) / 2);
+      for (int q = 0; q < 4; q++)
 #pragma unroll
-          for (int j = 0; j < W; j++) w[rt][h][j] = in ? src[j] : 0u;
-          s[rt][h] = to_float(scales[row[rt][h] * p.G + g]);
-          const uint32_t z = zeros ? zeros[row[rt][h] * p.zero_bytes + g / 2] >> (4 * (g & 1)) & 15u : 8u;
-          zz[rt][h] = zero_pair<T>(z);
+        for (int u = 0; u < U; u++) {
+          const uint32_t g = step * U + u;
+          sc[q][u] = g < G ? scales_at[q >> 1][rel[q] * G + g] : (uint16_t)0;
+          zp[q][u] = zeros && g < G ? zeros_at[q >> 1][rel[q] * zero_bytes + g / 2] : (uint8_t)0x88;
         }
-      float part[RT][NT][4] = {};
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      fill(it + kStages - 1);  // into the stage every lane has left
+      const uint8_t* tile = ring + (it % kStages) * kStageBytes;
 #pragma unroll
-      for (int j = 0; j < W; j++) {
-        uint32_t a[RT][2][4];
+      for (int u = 0; u < U; u++) {
+        uint32_t w[4][W], zz[4];
 #pragma unroll
-        for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            // fragment order: row gr, row gr + 8, then both again at the next pair
-            a[rt][i >> 1][(i & 1) * 2] = code_pair<T>(w[rt][0][j], i, zz[rt][0]);
-            a[rt][i >> 1][(i & 1) * 2 + 1] = code_pair<T>(w[rt][1][j], i, zz[rt][1]);
+        for (int q = 0; q < 4; q++) {
+          const int r = q * 8 + gr;
+          if (W == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + chunk_at(r, c));
+            w[q][0] = v.x, w[q][1 % W] = v.y, w[q][2 % W] = v.z, w[q][3 % W] = v.w;
+          } else if (W == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(tile + chunk_at(r, 2 * u + (c >> 1)) + (c & 1) * 8);
+            w[q][0] = v.x, w[q][1 % W] = v.y;
+          } else {
+            w[q][0] = *reinterpret_cast<const uint32_t*>(tile + chunk_at(r, u) + c * 4);
           }
+          zz[q] = zero_pair<T>(zp[q][u] >> (4 * ((step * U + u) & 1)) & 15u);
+        }
+        const int k = (step * U + u) * GROUP + c * (GROUP / 4);
+        float part[2][NT][4] = {};
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-          if (nt > 0 && t0 + nt * 8 >= M) break;  // the same for the whole CTA
-          const int64_t tok = t0 + nt * 8 + gr;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (in && tok < M) v = *reinterpret_cast<const uint4*>(x + tok * p.sx + k + j * 8);
-          const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
-          const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
+        for (int j = 0; j < W; j++) {
+          uint32_t a[2][2][4];
 #pragma unroll
-          for (int rt = 0; rt < RT; rt++) {
-            Pair<T>::mma(part[rt][nt], a[rt][0], b0, b1);
-            Pair<T>::mma(part[rt][nt], a[rt][1], b2, b3);
+          for (int rt = 0; rt < 2; rt++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              // fragment order: row gr, row gr + 8, then both again at the next pair
+              a[rt][i >> 1][(i & 1) * 2] = code_pair<T>(w[2 * rt][j], i, zz[2 * rt]);
+              a[rt][i >> 1][(i & 1) * 2 + 1] = code_pair<T>(w[2 * rt + 1][j], i, zz[2 * rt + 1]);
+            }
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            if (nt > 0 && t0 + nt * 8 >= M) break;  // the same for the whole CTA
+            const int64_t tok = t0 + nt * 8 + gr;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (k < p.Kd && tok < M) v = *reinterpret_cast<const uint4*>(x + tok * p.sx + k + j * 8);
+            const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
+            const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
+#pragma unroll
+            for (int rt = 0; rt < 2; rt++) {
+              Pair<T>::mma(part[rt][nt], a[rt][0], b0, b1);
+              Pair<T>::mma(part[rt][nt], a[rt][1], b2, b3);
+            }
           }
         }
+#pragma unroll
+        for (int rt = 0; rt < 2; rt++)
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              acc[rt][nt][i] = fmaf(scale_bits<T>(sc[2 * rt + (i >> 1)][u]), part[rt][nt][i], acc[rt][nt][i]);
       }
-#pragma unroll
-      for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) acc[rt][nt][i] = fmaf(s[rt][i >> 1], part[rt][nt][i], acc[rt][nt][i]);
     }
+    cp_async_wait<0>();
+    __syncwarp();
 
+    // partial tiles through the warps' rings: [tile][token][row]
+    constexpr int kTile = NT * 8 * kTokStride;
+    static_assert(2 * kTile * (int)sizeof(float) <= kStages * kStageBytes, "a partial tile fits the ring");
+    float* red = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int rt = 0; rt < RT; rt++)
+    for (int rt = 0; rt < 2; rt++)
 #pragma unroll
       for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) red[warp][rt][nt * 8 + 2 * c + (i & 1)][gr + 8 * (i >> 1)] = acc[rt][nt][i];
+        for (int i = 0; i < 4; i++)
+          red[rt * kTile + (nt * 8 + 2 * c + (i & 1)) * kTokStride + gr + 8 * (i >> 1)] = acc[rt][nt][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * 8 * NT; i += kThreads) {
-      const int r = i & 15, tt = i >> 4;
-      const int64_t tok = t0 + tt, n = n0 + r;
-      if (tok >= M || n >= n_out) continue;
-      float v[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; rt++) {
-        v[rt] = red[0][rt][tt][r];
-#pragma unroll
-        for (int k = 1; k < kWarps; k++) v[rt] += red[k][rt][tt][r];
+    const int features = blocks * kFeatures;
+    const int toks = (int)min64(M - t0, 8 * NT);
+    for (int i = threadIdx.x; i < features * toks; i += kThreads) {
+      const int f = i % features, tt = i / features, r = f % kFeatures;
+      const int64_t n = cta_n0 + f, tok = t0 + tt;
+      if (n >= n_out) continue;
+      const float* base = reinterpret_cast<const float*>(smem + (f / kFeatures) * wk * (kStages * kStageBytes));
+      auto total = [&](int rt) {
+        const float* at = base + rt * kTile + tt * kTokStride + (r & 15);
+        float v = at[0];
+        for (int k = 1; k < wk; k++) v += at[k * (kStages * kStageBytes / 4)];
+        return v;
+      };
+      float o;
+      if (SWIGLU) {
+        const float gate = total(1);
+        o = gate / (1.0f + expf(-gate)) * total(0);
+      } else {
+        o = total(r >> 4);
       }
-      float o = v[0];
-      if (RT == 2) o = v[RT - 1] / (1.0f + expf(-v[RT - 1])) * v[0];
       if (p.addend) o += to_float(static_cast<const T*>(p.addend)[(first + tok) * p.sadd + n]);
       static_cast<T*>(p.y)[(first + tok) * p.sy + n] = from_float<T>(o);
     }
@@ -266,30 +372,37 @@ __global__ void __launch_bounds__(kThreads) quantize_w4_kernel(const T* w, int64
   }
 }
 
+template <typename T, int GROUP, int NT, bool SWIGLU>
+cudaError_t launch(const W4Params& p, int wk, dim3 grid, cudaStream_t st) {
+  constexpr int kSmem = kWarps * kStages * kStageBytes;
+  static PerDeviceOnce once;
+  cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(w4_matvec_kernel<T, GROUP, NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  w4_matvec_kernel<T, GROUP, NT, SWIGLU><<<grid, kThreads, kSmem, st>>>(p, wk);
+  return cudaGetLastError();
+}
+
 template <typename T, int GROUP, int NT>
-void run_rt(const W4Params& p, bool swiglu, dim3 grid, cudaStream_t st) {
-  if (swiglu)
-    w4_matvec_kernel<T, GROUP, NT, 2><<<grid, kThreads, 0, st>>>(p);
-  else
-    w4_matvec_kernel<T, GROUP, NT, 1><<<grid, kThreads, 0, st>>>(p);
+cudaError_t run_act(const W4Params& p, bool swiglu, int wk, dim3 grid, cudaStream_t st) {
+  return swiglu ? launch<T, GROUP, NT, true>(p, wk, grid, st) : launch<T, GROUP, NT, false>(p, wk, grid, st);
 }
 
 template <typename T, int GROUP>
-void run_nt(const W4Params& p, int64_t tokens, bool swiglu, dim3 grid, cudaStream_t st) {
-  if (tokens <= 8)
-    run_rt<T, GROUP, 1>(p, swiglu, grid, st);
-  else if (tokens <= 16)
-    run_rt<T, GROUP, 2>(p, swiglu, grid, st);
-  else
-    run_rt<T, GROUP, 4>(p, swiglu, grid, st);
+cudaError_t run_nt(const W4Params& p, int64_t tokens, bool swiglu, int wk, dim3 grid, cudaStream_t st) {
+  if (tokens <= 8) return run_act<T, GROUP, 1>(p, swiglu, wk, grid, st);
+  if (tokens <= 16) return run_act<T, GROUP, 2>(p, swiglu, wk, grid, st);
+  return run_act<T, GROUP, 4>(p, swiglu, wk, grid, st);
 }
 
 template <typename T>
-void run_group(const W4Params& p, int group, int64_t tokens, bool swiglu, dim3 grid, cudaStream_t st) {
+cudaError_t run_group(const W4Params& p, int group, int64_t tokens, bool swiglu, int wk, dim3 grid, cudaStream_t st) {
   switch (group) {
-    case 32: run_nt<T, 32>(p, tokens, swiglu, grid, st); break;
-    case 64: run_nt<T, 64>(p, tokens, swiglu, grid, st); break;
-    default: run_nt<T, 128>(p, tokens, swiglu, grid, st); break;
+    case 32: return run_nt<T, 32>(p, tokens, swiglu, wk, grid, st);
+    case 64: return run_nt<T, 64>(p, tokens, swiglu, wk, grid, st);
+    default: return run_nt<T, 128>(p, tokens, swiglu, wk, grid, st);
   }
 }
 
@@ -309,17 +422,17 @@ W4Params base_params(const moe_w4& w, const moe_rows& x, const moe_rows& y) {
   return p;
 }
 
-// tokens: a bound on the rows of one matrix
+// tokens: the rows a matrix is expected to meet; matrices: those that have rows
 cudaError_t run(const moe_w4& w, const W4Params& p, int64_t tokens, int64_t matrices, int32_t activation,
                 cudaStream_t st) {
   const bool swiglu = activation == MOE_W4_SWIGLU;
-  const int64_t n_out = swiglu ? w.N / 2 : w.N;
-  const dim3 grid((unsigned)((n_out + 15) / 16), (unsigned)matrices);
-  if (w.dtype == MOE_ELEM_BF16)
-    run_group<__nv_bfloat16>(p, w.group, tokens, swiglu, grid, st);
-  else
-    run_group<__half>(p, w.group, tokens, swiglu, grid, st);
-  return cudaGetLastError();
+  const int64_t blocks = (w.N + kWarpRows - 1) / kWarpRows;  // row blocks of a matrix
+  const int64_t want = (int64_t)device_sm_count() * 2 * kWarps;  // warps that fill the device
+  int wk = 1;
+  while (wk < kWarps && blocks * matrices * wk < want) wk *= 2;
+  const dim3 grid((unsigned)((blocks * wk + kWarps - 1) / kWarps), (unsigned)matrices);
+  return w.dtype == MOE_ELEM_BF16 ? run_group<__nv_bfloat16>(p, w.group, tokens, swiglu, wk, grid, st)
+                                  : run_group<__half>(p, w.group, tokens, swiglu, wk, grid, st);
 }
 
 }  // namespace
@@ -340,8 +453,10 @@ cudaError_t launch_grouped_w4_matvec(const moe_handle_dev& h, const moe_shape& s
   p.E = (int)s.E;
   p.cap = l.capacity;
   const int64_t routes = s.T * s.K;
+  p.every = routes >= s.E;
   // a token's routes go to different experts, so an expert has at most T rows
-  return run(w, p, s.T, routes < s.E ? routes : s.E, activation, st);
+  const int64_t mean_rows = (routes + s.E - 1) / s.E;
+  return run(w, p, s.T <= 8 ? s.T : mean_rows <= 12 ? 16 : s.T, routes < s.E ? routes : s.E, activation, st);
 }
 
 cudaError_t launch_quantize_w4_rows(const void* w, int64_t R, int64_t Kd, int32_t group, int32_t dtype, void* codes,
