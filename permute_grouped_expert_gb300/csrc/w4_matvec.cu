@@ -43,6 +43,7 @@ struct W4Params {
   const int32_t* counts;
   const int32_t* offsets;
   int E;
+  uint32_t magic;  // Pair<T>::kMagic: as a run-time value it stays in a register, and mask-and-set is one instruction
   bool every;  // blockIdx.y is the expert; else it counts the experts that have rows
   int64_t cap;
 };
@@ -84,10 +85,12 @@ struct Pair<__half> {
 
 // Codes (i, i + 4) of a word as two T's, less 16 + z: exactly q - z.
 template <typename T>
-MOE_DEVICE uint32_t code_pair(uint32_t w, int i, uint32_t zz) {
+MOE_DEVICE uint32_t code_pair(uint32_t w, int i, uint32_t magic, uint32_t zz) {
   const int s = Pair<T>::kShift - 4 * i;
   const uint32_t v = s >= 0 ? w << s : w >> -s;
-  return Pair<T>::sub((v & Pair<T>::kMask) | Pair<T>::kMagic, zz);
+  uint32_t b;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(v), "n"(Pair<T>::kMask), "r"(magic));  // (v & mask) | magic
+  return Pair<T>::sub(b, zz);
 }
 
 template <typename T>
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
   constexpr int W = GROUP / 32;                        // 32-bit code words a lane takes of a group and row
   constexpr int kFeatures = SWIGLU ? 16 : kWarpRows;   // output features of a warp's rows
   extern __shared__ __align__(128) uint8_t smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   const int gr = lane >> 2, c = lane & 3;
   const int blocks = kWarps / wk;  // row blocks of a CTA
   const int64_t n_out = SWIGLU ? p.N / 2 : p.N;
@@ -197,16 +200,17 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
     zeros_at[rt] = zeros ? zeros + r0 * zero_bytes : nullptr;
   }
 
+  const uint32_t magic = p.magic;
   uint8_t* ring = smem + warp * (kStages * kStageBytes);
   const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
   const int steps = (int)((p.Kd + kStepK - 1) / kStepK);
   const int mine = n0 < n_out && split < steps ? (steps - split + wk - 1) / wk : 0;
 
-  auto fill = [&](int it) {
+  auto fill = [&](int it, int stage) {
     if (it < mine) {
       const int step = split + it * wk;
       const bool in = (int64_t)step * kStepK + c * 32 < p.Kd;  // Kd is a multiple of 32, a chunk 32 elements
-      const uint32_t dst = ring_u32 + (it % kStages) * kStageBytes;
+      const uint32_t dst = ring_u32 + stage * kStageBytes;
 #pragma unroll
       for (int q = 0; q < 4; q++)
         cp_async16(dst + chunk_at(q * 8 + gr, c),
@@ -218,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
   for (int64_t t0 = 0; t0 < M; t0 += 8 * NT) {
     float acc[2][NT][4] = {};
 #pragma unroll
-    for (int i = 0; i < kStages - 1; i++) fill(i);
+    for (int i = 0; i < kStages - 1; i++) fill(i, i);
+    int stage = 0, free_stage = kStages - 1;
     for (int it = 0; it < mine; it++) {
       const int step = split + it * wk;
       // scales and zero points of this step, while its codes arrive
@@ -234,8 +239,10 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
         }
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      fill(it + kStages - 1);  // into the stage every lane has left
-      const uint8_t* tile = ring + (it % kStages) * kStageBytes;
+      fill(it + kStages - 1, free_stage);  // the stage every lane has left
+      const uint8_t* tile = ring + stage * kStageBytes;
+      free_stage = stage;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
       for (int u = 0; u < U; u++) {
         uint32_t w[4][W], zz[4];
@@ -263,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
 #pragma unroll
             for (int i = 0; i < 4; i++) {
               // fragment order: row gr, row gr + 8, then both again at the next pair
-              a[rt][i >> 1][(i & 1) * 2] = code_pair<T>(w[2 * rt][j], i, zz[2 * rt]);
-              a[rt][i >> 1][(i & 1) * 2 + 1] = code_pair<T>(w[2 * rt + 1][j], i, zz[2 * rt + 1]);
+              a[rt][i >> 1][(i & 1) * 2] = code_pair<T>(w[2 * rt][j], i, magic, zz[2 * rt]);
+              a[rt][i >> 1][(i & 1) * 2 + 1] = code_pair<T>(w[2 * rt + 1][j], i, magic, zz[2 * rt + 1]);
             }
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
@@ -411,6 +418,7 @@ W4Params base_params(const moe_w4& w, const moe_rows& x, const moe_rows& y) {
   p.codes = static_cast<const uint8_t*>(w.codes);
   p.scales = w.scales;
   p.zeros = static_cast<const uint8_t*>(w.zeros);
+  p.magic = w.dtype == MOE_ELEM_BF16 ? Pair<__nv_bfloat16>::kMagic : Pair<__half>::kMagic;
   p.N = w.N;
   p.Kd = w.Kd;
   p.G = (w.Kd + w.group - 1) / w.group;
