@@ -5,17 +5,25 @@
 //   y[m][n] = act( sum_k (q[n][k] - z[n][k / group]) scale[n][k / group] x[m][k] )
 //
 // The products are m16n8k16 tensor-core products of 16 weight rows with 8
-// tokens.  A nibble becomes a 16-bit float without a conversion: placed in the
-// top mantissa bits of a number whose exponent is 2^4 it reads 16 + q, and
-// 16 + z is taken off exactly, so both operands are exact and a group's sum
-// is rounded in fp32 only; its scale is applied to that sum in fp32.  A sum over
-// k may take k in any order, so a lane's eight nibbles of one 32-bit word form
-// the pairs (i, i + 4) that two masks give at once, and the token values are
-// paired the same way.
+// tokens, f16 operands and fp32 sums.  What bounds them is not the tensor cores
+// but the instructions that make operands of nibbles, so a nibble is used where
+// it lies: masked out of a word at bits 0-3 of a half it reads as the
+// subnormal q 2^-24, at bits 4-7 as q 2^-20, both exact, which is five
+// instructions for a word of eight codes.  The factor 16 between them, and the
+// order that two masks give (codes i and i + 4 of a word form a pair), are put
+// on the tokens' side once: the CTA stages the tokens in fragment order, each
+// 128 elements of a token multiplied by the power of two that brings their
+// largest to [2^14, 2^15).  An element keeps all its bits down to 2^-24 of the
+// largest, and below that errs by 2^-35 of it.  With f that factor,
+//   sum (q - z) x = (sum q 2^-24 f x - z sum 2^-24 f x) 2^24 / f
+// whose second sum is staged with the tokens; a group's difference is scaled
+// and added up in fp32.  A token with an infinity or a NaN gives NaN.
 //
-// A CTA takes 16 output features (with SwiGLU the up and the gate rows of 16)
-// and its warps share the groups of K; partial sums meet in shared memory in
-// warp order.
+// A warp takes 32 weight rows (with SwiGLU the up and the gate rows of 16
+// features) whose codes stream through its own ring in shared memory.  Where
+// rows are few the CTAs of a cluster share the K steps of the same rows, so that
+// each stages its part of the tokens only, and then the warps of a CTA; partial
+// sums meet in (distributed) shared memory in a fixed order.
 #include "block_common.cuh"
 #include "moe_internal.h"
 
@@ -43,60 +51,18 @@ struct W4Params {
   const int32_t* counts;
   const int32_t* offsets;
   int E;
-  uint32_t magic;  // Pair<T>::kMagic: as a run-time value it stays in a register, and mask-and-set is one instruction
   bool every;  // blockIdx.y is the expert; else it counts the experts that have rows
   int64_t cap;
 };
 
-template <typename T>
-struct Pair;  // how 4-bit codes become pairs of T
-
-template <>
-struct Pair<__nv_bfloat16> {
-  static constexpr uint32_t kMagic = 0x41804180u, kMask = 0x00780078u;
-  static constexpr int kShift = 3;  // bits below a nibble in the mantissa
-  static MOE_DEVICE uint32_t sub(uint32_t a, uint32_t b) {
-    __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<uint32_t*>(&r);
-  }
-  static MOE_DEVICE void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-};
-
-template <>
-struct Pair<__half> {
-  static constexpr uint32_t kMagic = 0x4C004C00u, kMask = 0x03C003C0u;
-  static constexpr int kShift = 6;
-  static MOE_DEVICE uint32_t sub(uint32_t a, uint32_t b) {
-    __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<uint32_t*>(&r);
-  }
-  static MOE_DEVICE void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-};
-
-// Codes (i, i + 4) of a word as two T's, less 16 + z: exactly q - z.
-template <typename T>
-MOE_DEVICE uint32_t code_pair(uint32_t w, int i, uint32_t magic, uint32_t zz) {
-  const int s = Pair<T>::kShift - 4 * i;
-  const uint32_t v = s >= 0 ? w << s : w >> -s;
-  uint32_t b;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(v), "n"(Pair<T>::kMask), "r"(magic));  // (v & mask) | magic
-  return Pair<T>::sub(b, zz);
+MOE_DEVICE void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T>
-MOE_DEVICE uint32_t zero_pair(uint32_t z) {
-  return Pair<T>::kMagic | z << Pair<T>::kShift | z << (16 + Pair<T>::kShift);
-}
+// The integer 0..15 as a float.
+MOE_DEVICE float small_float(uint32_t v) { return __uint_as_float(0x4B000000u | v) - 8388608.0f; }
 
 template <typename T>
 MOE_DEVICE float scale_bits(uint16_t b) {
@@ -131,7 +97,17 @@ constexpr int kStepK = 128;
 constexpr int kRowBytes = kStepK / 2;
 constexpr int kWarpRows = 32;
 constexpr int kStageBytes = kWarpRows * kRowBytes;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
+constexpr int kRingBytes = kStages * kStageBytes;
+// Staged tokens: per step and token 128 f16 and, for each group, the sum of
+// what they hold and the factor that undoes their scaling.
+constexpr int kTokenBytes = 32 * 1024;
+constexpr int kSmemBytes = kWarps * kRingBytes + kTokenBytes;
+
+// Steps of `toks` tokens that fit: a multiple of wk, at least wk (host and device).
+__host__ __device__ constexpr int token_chunk(int toks, int groups, int wk) {
+  return kTokenBytes / (toks * kStepK * 2 + (toks + 1) / 2 * 2 * groups * 8) / wk * wk;
+}
 
 MOE_DEVICE int chunk_at(int row, int chunk) {
   return row * kRowBytes + ((chunk ^ ((row >> 1 & 1) << 1 | (row >> 2 & 1))) << 4);
@@ -147,11 +123,92 @@ MOE_DEVICE void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// GROUP: elements a scale; NT: tiles of 8 tokens a pass.  wk warps of a CTA
-// share the K steps of the same 32 weight rows: neighbouring rows, or with
-// SwiGLU the up and the gate rows of 16 features.
+// Stages steps [s0, s1) of `toks` tokens (x: the first of them).  Half a warp
+// takes a token's step, eight elements a lane.  frag: 16 bytes at
+// ((step * 4 + word) * toks + token) * 4 + lane-of-quad, the pairs (0, 4),
+// (1, 5) / 16, (2, 6), (3, 7) / 16 of the eight k of that code word.  aux:
+// {sum, factor} at (step * groups + group) * even(toks) + token.
+template <typename T, int GROUP>
+MOE_DEVICE void stage_tokens(const T* x, int64_t sx, int64_t Kd, int toks, int s0, int s1, uint4* frag, float2* aux) {
+  constexpr int U = kStepK / GROUP;
+  const int half = threadIdx.x >> 4, k8 = threadIdx.x & 15;
+  const int j = GROUP == 128 ? k8 & 3 : GROUP == 64 ? (k8 >> 3) * 2 + (k8 & 1) : k8 >> 2;
+  const int c = GROUP == 128 ? k8 >> 2 : GROUP == 64 ? k8 >> 1 & 3 : k8 & 3;
+  const int even = (toks + 1) & ~1;
+  const int units = (s1 - s0) * toks;
+  constexpr int kBatch = 4;  // units a half-warp has in flight
+  constexpr int kHalves = kThreads / 16;
+  for (int first = 0; first < units; first += kBatch * kHalves) {  // every lane stays: shuffles below
+    union {
+      uint4 v;
+      T e[8];
+    } in[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; b++) {
+      const int unit = first + b * kHalves + half, s = unit / toks, tok = unit - s * toks;
+      const int64_t k = (int64_t)(s0 + s) * kStepK + k8 * 8;
+      in[b].v = make_uint4(0, 0, 0, 0);
+      if (unit < units && k < Kd) in[b].v = *reinterpret_cast<const uint4*>(x + tok * sx + k);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; b++) {
+      if (first + b * kHalves >= units) break;  // the same for the whole CTA
+      const int unit = first + b * kHalves + half, s = unit / toks, tok = unit - s * toks;
+      float f[8], top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        f[i] = to_float(in[b].e[i]);
+        top = fmaxf(top, fabsf(f[i]));
+      }
+#pragma unroll
+      for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      // 2^(14 - E) for top in [2^E, 2^(E+1)); E held where both it and its inverse are normal
+      const int E = top > 0.0f ? min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127) : 14;
+      const float up = __uint_as_float((uint32_t)(127 + 14 - E) << 23);
+      const float up16 = up * 0.0625f;
+      __half2 h[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float m = i & 1 ? up16 : up;
+        h[i] = __floats2half2_rn(f[i] * m, f[i + 4] * m);
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float2 v = __half22float2(h[i]);
+        sum = fmaf(v.x + v.y, i & 1 ? 16.0f : 1.0f, sum);
+      }
+#pragma unroll
+      for (int d = GROUP / 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (unit < units) {
+        frag[((s * 4 + j) * toks + tok) * 4 + c] = *reinterpret_cast<uint4*>(h);
+        if (k8 % (GROUP / 8) == 0)
+          aux[(s * U + k8 / (GROUP / 8)) * even + tok] =
+              make_float2(sum * 0x1p-24f, __uint_as_float((uint32_t)(127 + 12 - 14 + E) << 23));
+      }
+    }
+  }
+}
+
+MOE_DEVICE void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The float at this CTA's shared address `at`, read from the CTA of this rank.
+MOE_DEVICE float ld_cluster(const float* at, int rank) {
+  uint32_t a;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// GROUP: elements a scale; NT: tiles of 8 tokens a pass.  A warp holds 32
+// weight rows: neighbouring rows, or with SwiGLU the up and the gate rows of 16
+// features.  The K steps of a row are shared by the ck CTAs of a cluster, a
+// run of steps each, and in a CTA by wk warps, every wk-th step each.
 template <typename T, int GROUP, int NT, bool SWIGLU>
-__global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int wk) {
+__global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int ck, int wk) {
   constexpr int U = kStepK / GROUP;                    // groups a step
   constexpr int W = GROUP / 32;                        // 32-bit code words a lane takes of a group and row
   constexpr int kFeatures = SWIGLU ? 16 : kWarpRows;   // output features of a warp's rows
@@ -160,7 +217,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
   const int gr = lane >> 2, c = lane & 3;
   const int blocks = kWarps / wk;  // row blocks of a CTA
   const int64_t n_out = SWIGLU ? p.N / 2 : p.N;
-  const int64_t cta_n0 = (int64_t)blockIdx.x * blocks * kFeatures;
+  const int rank = blockIdx.x % ck;  // clusters lie along x
+  const int64_t cta_n0 = (int64_t)(blockIdx.x / ck) * blocks * kFeatures;
   const int64_t n0 = cta_n0 + (warp / wk) * kFeatures;
   const int split = warp % wk;
 
@@ -200,15 +258,16 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
     zeros_at[rt] = zeros ? zeros + r0 * zero_bytes : nullptr;
   }
 
-  const uint32_t magic = p.magic;
-  uint8_t* ring = smem + warp * (kStages * kStageBytes);
+  uint8_t* ring = smem + warp * kRingBytes;
   const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
-  const int steps = (int)((p.Kd + kStepK - 1) / kStepK);
+  uint4* frag = reinterpret_cast<uint4*>(smem + kWarps * kRingBytes);
+  const int all_steps = (int)((p.Kd + kStepK - 1) / kStepK), run = (all_steps + ck - 1) / ck;
+  const int begin = min(rank * run, all_steps), steps = min(run, all_steps - begin);  // this CTA's
   const int mine = n0 < n_out && split < steps ? (steps - split + wk - 1) / wk : 0;
 
   auto fill = [&](int it, int stage) {
     if (it < mine) {
-      const int step = split + it * wk;
+      const int step = begin + split + it * wk;
       const bool in = (int64_t)step * kStepK + c * 32 < p.Kd;  // Kd is a multiple of 32, a chunk 32 elements
       const uint32_t dst = ring_u32 + stage * kStageBytes;
 #pragma unroll
@@ -220,81 +279,104 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
   };
 
   for (int64_t t0 = 0; t0 < M; t0 += 8 * NT) {
+    const int toks = (int)min64(M - t0, 8 * NT), even = (toks + 1) & ~1;
+    const int chunk = min(token_chunk(toks, U, wk), run);
+    float2* aux = reinterpret_cast<float2*>(frag + chunk * toks * 16);
     float acc[2][NT][4] = {};
 #pragma unroll
     for (int i = 0; i < kStages - 1; i++) fill(i, i);
     int stage = 0, free_stage = kStages - 1;
-    for (int it = 0; it < mine; it++) {
-      const int step = split + it * wk;
-      // scales and zero points of this step, while its codes arrive
-      uint16_t sc[4][U];
-      uint8_t zp[4][U];
+    int it = 0;
+    for (int s0 = begin; s0 < begin + steps; s0 += chunk) {
+      const int s1 = min(s0 + chunk, begin + steps);
+      if (s0 > begin) __syncthreads();  // the last chunk has been read
+      stage_tokens<T, GROUP>(x + t0 * p.sx, p.sx, p.Kd, toks, s0, s1, frag, aux);
+      __syncthreads();
+      for (; it < mine; it++) {
+        const int step = begin + split + it * wk;
+        if (step >= s1) break;
+        // scales and zero points of this step, while its codes arrive
+        uint16_t sc[4][U];
+        uint8_t zp[4][U];
 #pragma unroll
-      for (int q = 0; q < 4; q++)
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+          for (int u = 0; u < U; u++) {
+            const uint32_t g = step * U + u;
+            sc[q][u] = g < G ? scales_at[q >> 1][rel[q] * G + g] : (uint16_t)0;
+            zp[q][u] = zeros && g < G ? zeros_at[q >> 1][rel[q] * zero_bytes + g / 2] : (uint8_t)0x88;
+          }
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        fill(it + kStages - 1, free_stage);  // the stage every lane has left
+        const uint8_t* tile = ring + stage * kStageBytes;
+        free_stage = stage;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
         for (int u = 0; u < U; u++) {
-          const uint32_t g = step * U + u;
-          sc[q][u] = g < G ? scales_at[q >> 1][rel[q] * G + g] : (uint16_t)0;
-          zp[q][u] = zeros && g < G ? zeros_at[q >> 1][rel[q] * zero_bytes + g / 2] : (uint8_t)0x88;
-        }
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      fill(it + kStages - 1, free_stage);  // the stage every lane has left
-      const uint8_t* tile = ring + stage * kStageBytes;
-      free_stage = stage;
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+          uint32_t w[4][W];
 #pragma unroll
-      for (int u = 0; u < U; u++) {
-        uint32_t w[4][W], zz[4];
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const int r = q * 8 + gr;
-          if (W == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(tile + chunk_at(r, c));
-            w[q][0] = v.x, w[q][1 % W] = v.y, w[q][2 % W] = v.z, w[q][3 % W] = v.w;
-          } else if (W == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(tile + chunk_at(r, 2 * u + (c >> 1)) + (c & 1) * 8);
-            w[q][0] = v.x, w[q][1 % W] = v.y;
-          } else {
-            w[q][0] = *reinterpret_cast<const uint32_t*>(tile + chunk_at(r, u) + c * 4);
-          }
-          zz[q] = zero_pair<T>(zp[q][u] >> (4 * ((step * U + u) & 1)) & 15u);
-        }
-        const int k = (step * U + u) * GROUP + c * (GROUP / 4);
-        float part[2][NT][4] = {};
-#pragma unroll
-        for (int j = 0; j < W; j++) {
-          uint32_t a[2][2][4];
-#pragma unroll
-          for (int rt = 0; rt < 2; rt++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              // fragment order: row gr, row gr + 8, then both again at the next pair
-              a[rt][i >> 1][(i & 1) * 2] = code_pair<T>(w[2 * rt][j], i, magic, zz[2 * rt]);
-              a[rt][i >> 1][(i & 1) * 2 + 1] = code_pair<T>(w[2 * rt + 1][j], i, magic, zz[2 * rt + 1]);
+          for (int q = 0; q < 4; q++) {
+            const int r = q * 8 + gr;
+            if (W == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(tile + chunk_at(r, c));
+              w[q][0] = v.x, w[q][1 % W] = v.y, w[q][2 % W] = v.z, w[q][3 % W] = v.w;
+            } else if (W == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(tile + chunk_at(r, 2 * u + (c >> 1)) + (c & 1) * 8);
+              w[q][0] = v.x, w[q][1 % W] = v.y;
+            } else {
+              w[q][0] = *reinterpret_cast<const uint32_t*>(tile + chunk_at(r, u) + c * 4);
             }
+          }
+          float part[2][NT][4] = {};
+#pragma unroll
+          for (int j = 0; j < W; j++) {
+            // fragment order: row gr, row gr + 8, then both again at the next pair
+            uint32_t a[2][2][4];
+#pragma unroll
+            for (int rt = 0; rt < 2; rt++)
+#pragma unroll
+              for (int h = 0; h < 2; h++) {
+                const uint32_t v = w[2 * rt + h][j], v8 = v >> 8;
+                a[rt][0][h] = v & 0x000F000Fu;
+                a[rt][0][2 + h] = v & 0x00F000F0u;
+                a[rt][1][h] = v8 & 0x000F000Fu;
+                a[rt][1][2 + h] = v8 & 0x00F000F0u;
+              }
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              if (nt > 0 && nt * 8 >= toks) break;  // the same for the whole CTA
+              const int tok = min(nt * 8 + gr, toks - 1);  // columns past the last token are not stored
+              const uint4 b = frag[(((step - s0) * 4 + u * W + j) * toks + tok) * 4 + c];
+#pragma unroll
+              for (int rt = 0; rt < 2; rt++) {
+                mma_f16(part[rt][nt], a[rt][0], b.x, b.y);
+                mma_f16(part[rt][nt], a[rt][1], b.z, b.w);
+              }
+            }
+          }
+          float s[4], z[4];
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            s[q] = scale_bits<T>(sc[q][u]) * 4096.0f;  // with the staged factor 2^12 / f: 2^24 / f
+            z[q] = small_float(zp[q][u] >> (4 * ((step * U + u) & 1)) & 15u);
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
-            if (nt > 0 && t0 + nt * 8 >= M) break;  // the same for the whole CTA
-            const int64_t tok = t0 + nt * 8 + gr;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (k < p.Kd && tok < M) v = *reinterpret_cast<const uint4*>(x + tok * p.sx + k + j * 8);
-            const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
-            const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
+            if (nt > 0 && nt * 8 >= toks) break;
+            // {sum, factor} of tokens 2 c and 2 c + 1
+            const float4 xs = *reinterpret_cast<const float4*>(
+                aux + ((step - s0) * U + u) * even + min(nt * 8 + 2 * c, even - 2));
 #pragma unroll
-            for (int rt = 0; rt < 2; rt++) {
-              Pair<T>::mma(part[rt][nt], a[rt][0], b0, b1);
-              Pair<T>::mma(part[rt][nt], a[rt][1], b2, b3);
-            }
+            for (int rt = 0; rt < 2; rt++)
+#pragma unroll
+              for (int i = 0; i < 4; i++) {
+                const int q = 2 * rt + (i >> 1);
+                const float v = fmaf(-z[q], i & 1 ? xs.z : xs.x, part[rt][nt][i]) * (i & 1 ? xs.w : xs.y);
+                acc[rt][nt][i] = fmaf(s[q], v, acc[rt][nt][i]);
+              }
           }
         }
-#pragma unroll
-        for (int rt = 0; rt < 2; rt++)
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              acc[rt][nt][i] = fmaf(scale_bits<T>(sc[2 * rt + (i >> 1)][u]), part[rt][nt][i], acc[rt][nt][i]);
       }
     }
     cp_async_wait<0>();
@@ -302,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
 
     // partial tiles through the warps' rings: [tile][token][row]
     constexpr int kTile = NT * 8 * kTokStride;
-    static_assert(2 * kTile * (int)sizeof(float) <= kStages * kStageBytes, "a partial tile fits the ring");
+    static_assert(2 * kTile * (int)sizeof(float) <= kRingBytes, "a partial tile fits the ring");
     float* red = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int rt = 0; rt < 2; rt++)
@@ -311,18 +393,28 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
 #pragma unroll
         for (int i = 0; i < 4; i++)
           red[rt * kTile + (nt * 8 + 2 * c + (i & 1)) * kTokStride + gr + 8 * (i >> 1)] = acc[rt][nt][i];
-    __syncthreads();
-    const int features = blocks * kFeatures;
-    const int toks = (int)min64(M - t0, 8 * NT);
+    // every CTA of the cluster finishes its share of the features
+    const int features = blocks * kFeatures / ck;
+    if (ck > 1)
+      cluster_barrier();
+    else
+      __syncthreads();
     for (int i = threadIdx.x; i < features * toks; i += kThreads) {
-      const int f = i % features, tt = i / features, r = f % kFeatures;
+      const int f = rank * features + i % features, tt = i / features, r = f % kFeatures;
       const int64_t n = cta_n0 + f, tok = t0 + tt;
       if (n >= n_out) continue;
-      const float* base = reinterpret_cast<const float*>(smem + (f / kFeatures) * wk * (kStages * kStageBytes));
+      const float* base = reinterpret_cast<const float*>(smem + (f / kFeatures) * wk * kRingBytes);
       auto total = [&](int rt) {
         const float* at = base + rt * kTile + tt * kTokStride + (r & 15);
-        float v = at[0];
-        for (int k = 1; k < wk; k++) v += at[k * (kStages * kStageBytes / 4)];
+        float part[8], v = 0.0f;
+        for (int k = 0; k < wk; k++) {  // the reads of a round are in flight together
+#pragma unroll
+          for (int q = 0; q < 8; q++)
+            if (q < ck) part[q] = ck > 1 ? ld_cluster(at + k * (kRingBytes / 4), q) : at[k * (kRingBytes / 4)];
+#pragma unroll
+          for (int q = 0; q < 8; q++)
+            if (q < ck) v += part[q];
+        }
         return v;
       };
       float o;
@@ -335,7 +427,10 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
       if (p.addend) o += to_float(static_cast<const T*>(p.addend)[(first + tok) * p.sadd + n]);
       static_cast<T*>(p.y)[(first + tok) * p.sy + n] = from_float<T>(o);
     }
-    __syncthreads();
+    if (ck > 1)
+      cluster_barrier();  // nobody leaves, or fills its ring again, while it is read
+    else
+      __syncthreads();
   }
 }
 
@@ -379,37 +474,51 @@ __global__ void __launch_bounds__(kThreads) quantize_w4_kernel(const T* w, int64
   }
 }
 
+struct Split {
+  int ck, wk;  // CTAs of a cluster and warps of a CTA that share a row's K
+};
+
 template <typename T, int GROUP, int NT, bool SWIGLU>
-cudaError_t launch(const W4Params& p, int wk, dim3 grid, cudaStream_t st) {
-  constexpr int kSmem = kWarps * kStages * kStageBytes;
+cudaError_t launch(const W4Params& p, Split sp, dim3 grid, cudaStream_t st) {
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
     return cudaFuncSetAttribute(w4_matvec_kernel<T, GROUP, NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSmem);
+                                kSmemBytes);
   });
   if (e != cudaSuccess) return e;
-  w4_matvec_kernel<T, GROUP, NT, SWIGLU><<<grid, kThreads, kSmem, st>>>(p, wk);
-  return cudaGetLastError();
+  cudaLaunchAttribute cluster = {};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = (unsigned)sp.ck;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = sp.ck > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, w4_matvec_kernel<T, GROUP, NT, SWIGLU>, p, sp.ck, sp.wk);
 }
 
 template <typename T, int GROUP, int NT>
-cudaError_t run_act(const W4Params& p, bool swiglu, int wk, dim3 grid, cudaStream_t st) {
-  return swiglu ? launch<T, GROUP, NT, true>(p, wk, grid, st) : launch<T, GROUP, NT, false>(p, wk, grid, st);
+cudaError_t run_act(const W4Params& p, bool swiglu, Split sp, dim3 grid, cudaStream_t st) {
+  return swiglu ? launch<T, GROUP, NT, true>(p, sp, grid, st) : launch<T, GROUP, NT, false>(p, sp, grid, st);
 }
 
 template <typename T, int GROUP>
-cudaError_t run_nt(const W4Params& p, int64_t tokens, bool swiglu, int wk, dim3 grid, cudaStream_t st) {
-  if (tokens <= 8) return run_act<T, GROUP, 1>(p, swiglu, wk, grid, st);
-  if (tokens <= 16) return run_act<T, GROUP, 2>(p, swiglu, wk, grid, st);
-  return run_act<T, GROUP, 4>(p, swiglu, wk, grid, st);
+cudaError_t run_nt(const W4Params& p, int64_t tokens, bool swiglu, Split sp, dim3 grid, cudaStream_t st) {
+  if (tokens <= 8) return run_act<T, GROUP, 1>(p, swiglu, sp, grid, st);
+  if (tokens <= 16) return run_act<T, GROUP, 2>(p, swiglu, sp, grid, st);
+  return run_act<T, GROUP, 4>(p, swiglu, sp, grid, st);
 }
 
 template <typename T>
-cudaError_t run_group(const W4Params& p, int group, int64_t tokens, bool swiglu, int wk, dim3 grid, cudaStream_t st) {
+cudaError_t run_group(const W4Params& p, int group, int64_t tokens, bool swiglu, Split sp, dim3 grid,
+                      cudaStream_t st) {
   switch (group) {
-    case 32: return run_nt<T, 32>(p, tokens, swiglu, wk, grid, st);
-    case 64: return run_nt<T, 64>(p, tokens, swiglu, wk, grid, st);
-    default: return run_nt<T, 128>(p, tokens, swiglu, wk, grid, st);
+    case 32: return run_nt<T, 32>(p, tokens, swiglu, sp, grid, st);
+    case 64: return run_nt<T, 64>(p, tokens, swiglu, sp, grid, st);
+    default: return run_nt<T, 128>(p, tokens, swiglu, sp, grid, st);
   }
 }
 
@@ -418,7 +527,6 @@ W4Params base_params(const moe_w4& w, const moe_rows& x, const moe_rows& y) {
   p.codes = static_cast<const uint8_t*>(w.codes);
   p.scales = w.scales;
   p.zeros = static_cast<const uint8_t*>(w.zeros);
-  p.magic = w.dtype == MOE_ELEM_BF16 ? Pair<__nv_bfloat16>::kMagic : Pair<__half>::kMagic;
   p.N = w.N;
   p.Kd = w.Kd;
   p.G = (w.Kd + w.group - 1) / w.group;
@@ -436,11 +544,17 @@ cudaError_t run(const moe_w4& w, const W4Params& p, int64_t tokens, int64_t matr
   const bool swiglu = activation == MOE_W4_SWIGLU;
   const int64_t blocks = (w.N + kWarpRows - 1) / kWarpRows;  // row blocks of a matrix
   const int64_t want = (int64_t)device_sm_count() * 2 * kWarps;  // warps that fill the device
-  int wk = 1;
-  while (wk < kWarps && blocks * matrices * wk < want) wk *= 2;
-  const dim3 grid((unsigned)((blocks * wk + kWarps - 1) / kWarps), (unsigned)matrices);
-  return w.dtype == MOE_ELEM_BF16 ? run_group<__nv_bfloat16>(p, w.group, tokens, swiglu, wk, grid, st)
-                                  : run_group<__half>(p, w.group, tokens, swiglu, wk, grid, st);
+  const int64_t steps = (w.Kd + kStepK - 1) / kStepK;
+  const int groups = kStepK / w.group, toks = tokens <= 8 ? 8 : tokens <= 16 ? 16 : 32;  // a pass
+  Split sp = {1, 1};
+  while (sp.ck < 8 && blocks * matrices * sp.ck < want && steps >= 2 * sp.ck) sp.ck *= 2;
+  // a chunk of staged tokens holds a step of every warp of a row block
+  while (sp.wk < kWarps && blocks * matrices * sp.ck * sp.wk < want && steps >= 2 * sp.ck * sp.wk &&
+         token_chunk(toks, groups, sp.wk * 2) > 0)
+    sp.wk *= 2;
+  const dim3 grid((unsigned)((blocks * sp.wk + kWarps - 1) / kWarps * sp.ck), (unsigned)matrices);
+  return w.dtype == MOE_ELEM_BF16 ? run_group<__nv_bfloat16>(p, w.group, tokens, swiglu, sp, grid, st)
+                                  : run_group<__half>(p, w.group, tokens, swiglu, sp, grid, st);
 }
 
 }  // namespace
