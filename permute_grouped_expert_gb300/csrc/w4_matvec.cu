@@ -47,6 +47,7 @@ struct W4Params {
   void* y;
   int64_t sy;
   int64_t M;  // tokens, without experts
+  bool vector_scales, vector_zeros;  // eight groups of any row are one aligned 16-byte / 4-byte piece
   // one matrix per expert
   const int32_t* counts;
   const int32_t* offsets;
@@ -99,61 +100,79 @@ constexpr int kWarpRows = 32;
 constexpr int kStageBytes = kWarpRows * kRowBytes;
 constexpr int kStages = 5;
 constexpr int kRingBytes = kStages * kStageBytes;
+// Scales and zero points stream with the codes, eight groups of the 32 rows at
+// a time (16 and 4 bytes a row), into slots enough for the steps in flight.
+constexpr int kSlotBytes = kWarpRows * (16 + 4);
+__host__ __device__ constexpr int scale_slots(int group) { return group == 128 ? 2 : 4; }
 // Staged tokens: per step and token 128 f16 and, for each group, the sum of
 // what they hold and the factor that undoes their scaling.
-constexpr int kTokenBytes = 32 * 1024;
-constexpr int kSmemBytes = kWarps * kRingBytes + kTokenBytes;
-
-// Steps of `toks` tokens that fit: a multiple of wk, at least wk (host and device).
-__host__ __device__ constexpr int token_chunk(int toks, int groups, int wk) {
-  return kTokenBytes / (toks * kStepK * 2 + (toks + 1) / 2 * 2 * groups * 8) / wk * wk;
+constexpr int kSmemBytes = 115456;  // two CTAs fill an SM's shared memory
+__host__ __device__ constexpr int token_bytes(int group) {
+  return kSmemBytes - kWarps * (kRingBytes + scale_slots(group) * kSlotBytes);
 }
+// Steps of `toks` tokens that fit (host and device).
+__host__ __device__ constexpr int token_chunk(int toks, int group) {
+  return token_bytes(group) / (toks * kStepK * 2 + (toks + 1) / 2 * 2 * (kStepK / group) * 8);
+}
+static_assert(token_chunk(32, 32) > 0, "a pass of any size makes progress");
 
 MOE_DEVICE int chunk_at(int row, int chunk) {
   return row * kRowBytes + ((chunk ^ ((row >> 1 & 1) << 1 | (row >> 2 & 1))) << 4);
 }
 
-MOE_DEVICE void cp_async16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
-               : "memory");
+MOE_DEVICE void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 MOE_DEVICE void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+MOE_DEVICE void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int N>
 MOE_DEVICE void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Where lane-of-quad c of a token finds the tokens' 16 bytes for code word j of
+// a step, from the step's and token's 256 bytes: the words of odd tokens change
+// places in pairs, so that a quarter-warp's read of two tokens meets every bank
+// once.
+MOE_DEVICE int frag_at(int tok, int j, int c) { return (j ^ (tok & 1)) * 4 + c; }
+
 // Stages steps [s0, s1) of `toks` tokens (x: the first of them).  Half a warp
 // takes a token's step, eight elements a lane.  frag: 16 bytes at
-// ((step * 4 + word) * toks + token) * 4 + lane-of-quad, the pairs (0, 4),
-// (1, 5) / 16, (2, 6), (3, 7) / 16 of the eight k of that code word.  aux:
-// {sum, factor} at (step * groups + group) * even(toks) + token.
+// (step * toks + token) * 16 + frag_at: the pairs (0, 4), (1, 5) / 16, (2, 6),
+// (3, 7) / 16 of the eight k of that code word.  aux: {sum, factor} at
+// (step * groups + group) * even(toks) + token.
 template <typename T, int GROUP>
 MOE_DEVICE void stage_tokens(const T* x, int64_t sx, int64_t Kd, int toks, int s0, int s1, uint4* frag, float2* aux) {
   constexpr int U = kStepK / GROUP;
-  const int half = threadIdx.x >> 4, k8 = threadIdx.x & 15;
+  constexpr int kBatch = 4;  // units a half-warp has in flight
+  constexpr int kHalves = kThreads / 16;
+  const int k8 = threadIdx.x & 15;
   const int j = GROUP == 128 ? k8 & 3 : GROUP == 64 ? (k8 >> 3) * 2 + (k8 & 1) : k8 >> 2;
   const int c = GROUP == 128 ? k8 >> 2 : GROUP == 64 ? k8 >> 1 & 3 : k8 & 3;
   const int even = (toks + 1) & ~1;
-  const int units = (s1 - s0) * toks;
-  constexpr int kBatch = 4;  // units a half-warp has in flight
-  constexpr int kHalves = kThreads / 16;
-  for (int first = 0; first < units; first += kBatch * kHalves) {  // every lane stays: shuffles below
+  const int rounds = ((s1 - s0) * toks + kHalves - 1) / kHalves;
+  const int ds = kHalves / toks, dt = kHalves % toks;  // one round further
+  int s = (threadIdx.x >> 4) / toks, tok = (threadIdx.x >> 4) % toks;
+  for (int first = 0; first < rounds; first += kBatch) {  // every lane stays: shuffles below
     union {
       uint4 v;
       T e[8];
     } in[kBatch];
+    int ss = s, tt = tok;
 #pragma unroll
     for (int b = 0; b < kBatch; b++) {
-      const int unit = first + b * kHalves + half, s = unit / toks, tok = unit - s * toks;
-      const int64_t k = (int64_t)(s0 + s) * kStepK + k8 * 8;
+      const int64_t k = (int64_t)(s0 + ss) * kStepK + k8 * 8;
       in[b].v = make_uint4(0, 0, 0, 0);
-      if (unit < units && k < Kd) in[b].v = *reinterpret_cast<const uint4*>(x + tok * sx + k);
+      if (s0 + ss < s1 && k < Kd) in[b].v = *reinterpret_cast<const uint4*>(x + tt * sx + k);
+      ss += ds;
+      tt += dt;
+      if (tt >= toks) tt -= toks, ss++;
     }
 #pragma unroll
     for (int b = 0; b < kBatch; b++) {
-      if (first + b * kHalves >= units) break;  // the same for the whole CTA
-      const int unit = first + b * kHalves + half, s = unit / toks, tok = unit - s * toks;
+      if (first + b >= rounds) break;  // the same for the whole CTA
       float f[8], top = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
@@ -180,12 +199,15 @@ MOE_DEVICE void stage_tokens(const T* x, int64_t sx, int64_t Kd, int toks, int s
       }
 #pragma unroll
       for (int d = GROUP / 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (unit < units) {
-        frag[((s * 4 + j) * toks + tok) * 4 + c] = *reinterpret_cast<uint4*>(h);
+      if (s0 + s < s1) {
+        frag[(s * toks + tok) * 16 + frag_at(tok, j, c)] = *reinterpret_cast<uint4*>(h);
         if (k8 % (GROUP / 8) == 0)
           aux[(s * U + k8 / (GROUP / 8)) * even + tok] =
               make_float2(sum * 0x1p-24f, __uint_as_float((uint32_t)(127 + 12 - 14 + E) << 23));
       }
+      s += ds;
+      tok += dt;
+      if (tok >= toks) tok -= toks, s++;
     }
   }
 }
@@ -206,25 +228,25 @@ MOE_DEVICE float ld_cluster(const float* at, int rank) {
 // GROUP: elements a scale; NT: tiles of 8 tokens a pass.  A warp holds 32
 // weight rows: neighbouring rows, or with SwiGLU the up and the gate rows of 16
 // features.  The K steps of a row are shared by the ck CTAs of a cluster, a
-// run of steps each, and in a CTA by wk warps, every wk-th step each.
+// run of steps each.
 template <typename T, int GROUP, int NT, bool SWIGLU>
-__global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int ck, int wk) {
+__global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int ck) {
   constexpr int U = kStepK / GROUP;                    // groups a step
   constexpr int W = GROUP / 32;                        // 32-bit code words a lane takes of a group and row
   constexpr int kFeatures = SWIGLU ? 16 : kWarpRows;   // output features of a warp's rows
+  constexpr int kSlots = scale_slots(GROUP);
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   const int gr = lane >> 2, c = lane & 3;
-  const int blocks = kWarps / wk;  // row blocks of a CTA
   const int64_t n_out = SWIGLU ? p.N / 2 : p.N;
   const int rank = blockIdx.x % ck;  // clusters lie along x
-  const int64_t cta_n0 = (int64_t)(blockIdx.x / ck) * blocks * kFeatures;
-  const int64_t n0 = cta_n0 + (warp / wk) * kFeatures;
-  const int split = warp % wk;
+  const int64_t cta_n0 = (int64_t)(blockIdx.x / ck) * kWarps * kFeatures;
+  const int64_t n0 = cta_n0 + warp * kFeatures;
 
   int64_t first = 0, M = p.M, e = 0;
   if (p.counts) {
-    e = p.every ? (int)blockIdx.y : nth_active_expert(p, blockIdx.y);
+    // (a shuffle tells the compiler that the expert is the whole warp's)
+    e = __shfl_sync(0xffffffffu, p.every ? (int)blockIdx.y : nth_active_expert(p, blockIdx.y), 0);
     if (e < 0) return;
     first = p.offsets[e];
     M = min64(first + p.counts[e], p.cap) - first;
@@ -235,17 +257,20 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
   const uint8_t* zeros = p.zeros ? p.zeros + e * p.N * p.zero_bytes : nullptr;
   const T* x = static_cast<const T*>(p.x) + first * p.sx;
 
+  uint8_t* ring = smem + warp * kRingBytes;
+  uint8_t* slots = smem + kWarps * kRingBytes + warp * kSlots * kSlotBytes;
+  uint4* frag = reinterpret_cast<uint4*>(smem + kWarps * (kRingBytes + kSlots * kSlotBytes));
+  const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t slots_u32 = (uint32_t)__cvta_generic_to_shared(slots);
+  const int all_steps = (int)((p.Kd + kStepK - 1) / kStepK), run = (all_steps + ck - 1) / ck;
+  const int begin = min(rank * run, all_steps), end = min(begin + run, all_steps);  // this CTA's steps
+  const int mine = n0 < n_out ? end : begin;                                      // this warp's end
+
   // Row r of the warp's tile is weight row n0 + r, with SwiGLU row n0 + r of the
-  // up half and n0 + r - 16 of the gate half; rows past the end are read again
-  // and not stored.  Lane (gr, c) copies chunk c of rows gr, gr + 8, ... and
-  // holds the products of the same rows: offsets from the tile's first row.
-  const int64_t last = n_out - 1 - n0;
-  uint32_t rel[4];
-#pragma unroll
-  for (int q = 0; q < 4; q++) {
-    const int r = SWIGLU ? (q & 1) * 8 + gr : q * 8 + gr;
-    rel[q] = (uint32_t)min64(r, last);
-  }
+  // up half and n0 + r - 16 of the gate half.  Lane (gr, c) copies chunk c of
+  // rows gr + 8 q and holds the products of the same rows.  A row past the last
+  // (its products are not stored) reads the last.  Addresses are a base of the
+  // whole warp, which moves with the steps, and a lane's 32-bit offset.
   const uint32_t row_bytes = (uint32_t)(p.Kd / 2), G = (uint32_t)p.G, zero_bytes = (uint32_t)p.zero_bytes;
   const uint8_t* codes_at[2];
   const uint16_t* scales_at[2];
@@ -255,77 +280,107 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
     const int64_t r0 = n0 + (SWIGLU && rt ? n_out : 0);
     codes_at[rt] = codes + r0 * row_bytes;
     scales_at[rt] = scales + r0 * G;
-    zeros_at[rt] = zeros ? zeros + r0 * zero_bytes : nullptr;
+    zeros_at[rt] = zeros + r0 * zero_bytes;
   }
-
-  uint8_t* ring = smem + warp * kRingBytes;
-  const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
-  uint4* frag = reinterpret_cast<uint4*>(smem + kWarps * kRingBytes);
-  const int all_steps = (int)((p.Kd + kStepK - 1) / kStepK), run = (all_steps + ck - 1) / ck;
-  const int begin = min(rank * run, all_steps), steps = min(run, all_steps - begin);  // this CTA's
-  const int mine = n0 < n_out && split < steps ? (steps - split + wk - 1) / wk : 0;
-
-  auto fill = [&](int it, int stage) {
-    if (it < mine) {
-      const int step = begin + split + it * wk;
-      const bool in = (int64_t)step * kStepK + c * 32 < p.Kd;  // Kd is a multiple of 32, a chunk 32 elements
-      const uint32_t dst = ring_u32 + stage * kStageBytes;
+  uint32_t code_to[4];
 #pragma unroll
-      for (int q = 0; q < 4; q++)
-        cp_async16(dst + chunk_at(q * 8 + gr, c),
-                   codes_at[q >> 1] + (in ? rel[q] * row_bytes + (uint32_t)(step * kRowBytes + c * 16) : 0u), in);
+  for (int q = 0; q < 4; q++) {
+    const uint32_t r = (uint32_t)min64(SWIGLU ? (q & 1) * 8 + gr : q * 8 + gr, max64(n_out - 1 - n0, 0));
+    code_to[q] = r * row_bytes + c * 16;
+  }
+  // this lane's row of scales and zero points
+  const uint32_t srow = (uint32_t)min64(SWIGLU ? lane & 15 : lane, max64(n_out - 1 - n0, 0));
+  const uint16_t* scale_src = scales_at[SWIGLU ? lane >> 4 : 0] + srow * G;
+  const uint8_t* zero_src = zeros_at[SWIGLU ? lane >> 4 : 0] + srow * zero_bytes;
+  const int at0 = chunk_at(gr, c);  // rows gr + 8 q lie 8 q rows further
+
+  auto fill = [&](int step, int stage) {
+    if (step < mine) {
+      // Kd is a multiple of 32, a chunk 32 elements; what a chunk past the end holds meets zeros
+      if (c * 32 < (int)p.Kd - step * kStepK) {
+        const uint32_t dst = ring_u32 + stage * kStageBytes + at0;
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+          cp_async16(dst + q * 8 * kRowBytes, codes_at[SWIGLU ? q >> 1 : 0] + (int64_t)step * kRowBytes + code_to[q]);
+      }
+      if (step == begin || step * U % 8 == 0) {
+        const uint32_t g0 = step * U & ~7, slot = (g0 >> 3) % kSlots * kSlotBytes;
+        if (p.vector_scales) {
+          cp_async16(slots_u32 + slot + lane * 16, scale_src + g0);
+        } else {
+          uint16_t* to = reinterpret_cast<uint16_t*>(slots + slot + lane * 16);
+          for (int i = 0; i < 8; i++) to[i] = g0 + i < G ? scale_src[g0 + i] : (uint16_t)0;
+        }
+        if (zeros) {
+          if (p.vector_zeros) {
+            cp_async4(slots_u32 + slot + kWarpRows * 16 + lane * 4, zero_src + (g0 >> 1));
+          } else {
+            uint8_t* to = slots + slot + kWarpRows * 16 + lane * 4;
+            for (int i = 0; i < 4; i++) to[i] = (g0 >> 1) + i < zero_bytes ? zero_src[(g0 >> 1) + i] : (uint8_t)0;
+          }
+        }
+      }
     }
     cp_async_commit();
   };
 
   for (int64_t t0 = 0; t0 < M; t0 += 8 * NT) {
     const int toks = (int)min64(M - t0, 8 * NT), even = (toks + 1) & ~1;
-    const int chunk = min(token_chunk(toks, U, wk), run);
+    const int chunk = min(token_chunk(toks, GROUP), run);
     float2* aux = reinterpret_cast<float2*>(frag + chunk * toks * 16);
     float acc[2][NT][4] = {};
 #pragma unroll
-    for (int i = 0; i < kStages - 1; i++) fill(i, i);
+    for (int i = 0; i < kStages - 1; i++) fill(begin + i, i);
+    // a lane's tokens in a staged step: words of even and of odd index, see frag_at
+    uint32_t tok_to[NT][2], sum_to[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      const int tok = min(nt * 8 + gr, toks - 1);  // columns past the last token are not stored
+      tok_to[nt][0] = tok * 256 + frag_at(tok, 0, c) * 16;
+      tok_to[nt][1] = tok * 256 + frag_at(tok, 1, c) * 16;
+      sum_to[nt] = min(nt * 8 + 2 * c, even - 2) * 8;
+    }
     int stage = 0, free_stage = kStages - 1;
-    int it = 0;
-    for (int s0 = begin; s0 < begin + steps; s0 += chunk) {
-      const int s1 = min(s0 + chunk, begin + steps);
+    for (int s0 = begin; s0 < end; s0 += chunk) {
+      const int s1 = min(s0 + chunk, end);
       if (s0 > begin) __syncthreads();  // the last chunk has been read
       stage_tokens<T, GROUP>(x + t0 * p.sx, p.sx, p.Kd, toks, s0, s1, frag, aux);
       __syncthreads();
-      for (; it < mine; it++) {
-        const int step = begin + split + it * wk;
-        if (step >= s1) break;
-        // scales and zero points of this step, while its codes arrive
-        uint16_t sc[4][U];
-        uint8_t zp[4][U];
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-#pragma unroll
-          for (int u = 0; u < U; u++) {
-            const uint32_t g = step * U + u;
-            sc[q][u] = g < G ? scales_at[q >> 1][rel[q] * G + g] : (uint16_t)0;
-            zp[q][u] = zeros && g < G ? zeros_at[q >> 1][rel[q] * zero_bytes + g / 2] : (uint8_t)0x88;
-          }
+      const uint8_t* tokens = reinterpret_cast<const uint8_t*>(frag);
+      const uint8_t* sums = reinterpret_cast<const uint8_t*>(aux);
+      for (int step = s0; step < min(s1, mine); step++) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
-        fill(it + kStages - 1, free_stage);  // the stage every lane has left
+        fill(step + kStages - 1, free_stage);  // the stage every lane has left
         const uint8_t* tile = ring + stage * kStageBytes;
         free_stage = stage;
         stage = stage + 1 == kStages ? 0 : stage + 1;
+        const uint8_t* slot = slots + (step * U >> 3) % kSlots * kSlotBytes;
 #pragma unroll
         for (int u = 0; u < U; u++) {
+          const int g = (step * U + u) & 7;
+          float s[4], z[4];
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            s[q] = scale_bits<T>(*reinterpret_cast<const uint16_t*>(slot + (gr + 8 * q) * 16 + g * 2));
+            z[q] = 8.0f;
+          }
+          if (zeros)
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+              z[q] = small_float(slot[kWarpRows * 16 + (gr + 8 * q) * 4 + (g >> 1)] >> (4 * (g & 1)) & 15u);
           uint32_t w[4][W];
 #pragma unroll
           for (int q = 0; q < 4; q++) {
-            const int r = q * 8 + gr;
+            const uint8_t* t = tile + q * 8 * kRowBytes;
             if (W == 4) {
-              const uint4 v = *reinterpret_cast<const uint4*>(tile + chunk_at(r, c));
+              const uint4 v = *reinterpret_cast<const uint4*>(t + at0);
               w[q][0] = v.x, w[q][1 % W] = v.y, w[q][2 % W] = v.z, w[q][3 % W] = v.w;
             } else if (W == 2) {
-              const uint2 v = *reinterpret_cast<const uint2*>(tile + chunk_at(r, 2 * u + (c >> 1)) + (c & 1) * 8);
+              const uint2 v = *reinterpret_cast<const uint2*>(t + chunk_at(gr, 2 * u + (c >> 1)) + (c & 1) * 8);
               w[q][0] = v.x, w[q][1 % W] = v.y;
             } else {
-              w[q][0] = *reinterpret_cast<const uint32_t*>(tile + chunk_at(r, u) + c * 4);
+              w[q][0] = *reinterpret_cast<const uint32_t*>(t + chunk_at(gr, u) + c * 4);
             }
           }
           float part[2][NT][4] = {};
@@ -343,11 +398,11 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
                 a[rt][1][h] = v8 & 0x000F000Fu;
                 a[rt][1][2 + h] = v8 & 0x00F000F0u;
               }
+            const int word = u * W + j;
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
               if (nt > 0 && nt * 8 >= toks) break;  // the same for the whole CTA
-              const int tok = min(nt * 8 + gr, toks - 1);  // columns past the last token are not stored
-              const uint4 b = frag[(((step - s0) * 4 + u * W + j) * toks + tok) * 4 + c];
+              const uint4 b = *reinterpret_cast<const uint4*>(tokens + tok_to[nt][word & 1] + (word & 2) * 64);
 #pragma unroll
               for (int rt = 0; rt < 2; rt++) {
                 mma_f16(part[rt][nt], a[rt][0], b.x, b.y);
@@ -355,18 +410,11 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
               }
             }
           }
-          float s[4], z[4];
-#pragma unroll
-          for (int q = 0; q < 4; q++) {
-            s[q] = scale_bits<T>(sc[q][u]) * 4096.0f;  // with the staged factor 2^12 / f: 2^24 / f
-            z[q] = small_float(zp[q][u] >> (4 * ((step * U + u) & 1)) & 15u);
-          }
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
             if (nt > 0 && nt * 8 >= toks) break;
             // {sum, factor} of tokens 2 c and 2 c + 1
-            const float4 xs = *reinterpret_cast<const float4*>(
-                aux + ((step - s0) * U + u) * even + min(nt * 8 + 2 * c, even - 2));
+            const float4 xs = *reinterpret_cast<const float4*>(sums + u * even * 8 + sum_to[nt]);
 #pragma unroll
             for (int rt = 0; rt < 2; rt++)
 #pragma unroll
@@ -377,6 +425,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
               }
           }
         }
+        tokens += toks * 256;
+        sums += U * even * 8;
       }
     }
     cp_async_wait<0>();
@@ -392,29 +442,28 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
       for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int i = 0; i < 4; i++)
-          red[rt * kTile + (nt * 8 + 2 * c + (i & 1)) * kTokStride + gr + 8 * (i >> 1)] = acc[rt][nt][i];
+          red[rt * kTile + (nt * 8 + 2 * c + (i & 1)) * kTokStride + gr + 8 * (i >> 1)] =
+              acc[rt][nt][i] * 0x1p12f;  // with the staged factor 2^12 / f: 2^24 / f
     // every CTA of the cluster finishes its share of the features
-    const int features = blocks * kFeatures / ck;
+    const int features = kWarps * kFeatures / ck, log_features = 31 - __clz(features);  // powers of two
     if (ck > 1)
       cluster_barrier();
     else
       __syncthreads();
     for (int i = threadIdx.x; i < features * toks; i += kThreads) {
-      const int f = rank * features + i % features, tt = i / features, r = f % kFeatures;
+      const int f = rank * features + (i & (features - 1)), tt = i >> log_features, r = f % kFeatures;
       const int64_t n = cta_n0 + f, tok = t0 + tt;
       if (n >= n_out) continue;
-      const float* base = reinterpret_cast<const float*>(smem + (f / kFeatures) * wk * kRingBytes);
+      const float* base = reinterpret_cast<const float*>(smem + (f / kFeatures) * kRingBytes);
       auto total = [&](int rt) {
         const float* at = base + rt * kTile + tt * kTokStride + (r & 15);
         float part[8], v = 0.0f;
-        for (int k = 0; k < wk; k++) {  // the reads of a round are in flight together
 #pragma unroll
-          for (int q = 0; q < 8; q++)
-            if (q < ck) part[q] = ck > 1 ? ld_cluster(at + k * (kRingBytes / 4), q) : at[k * (kRingBytes / 4)];
+        for (int q = 0; q < 8; q++)  // in flight together
+          if (q < ck) part[q] = ck > 1 ? ld_cluster(at, q) : *at;
 #pragma unroll
-          for (int q = 0; q < 8; q++)
-            if (q < ck) v += part[q];
-        }
+        for (int q = 0; q < 8; q++)
+          if (q < ck) v += part[q];
         return v;
       };
       float o;
@@ -474,12 +523,8 @@ __global__ void __launch_bounds__(kThreads) quantize_w4_kernel(const T* w, int64
   }
 }
 
-struct Split {
-  int ck, wk;  // CTAs of a cluster and warps of a CTA that share a row's K
-};
-
 template <typename T, int GROUP, int NT, bool SWIGLU>
-cudaError_t launch(const W4Params& p, Split sp, dim3 grid, cudaStream_t st) {
+cudaError_t launch(const W4Params& p, int ck, dim3 grid, cudaStream_t st) {
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
     return cudaFuncSetAttribute(w4_matvec_kernel<T, GROUP, NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -488,7 +533,7 @@ cudaError_t launch(const W4Params& p, Split sp, dim3 grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster = {};
   cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = (unsigned)sp.ck;
+  cluster.val.clusterDim.x = (unsigned)ck;
   cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -496,29 +541,29 @@ cudaError_t launch(const W4Params& p, Split sp, dim3 grid, cudaStream_t st) {
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cfg.attrs = &cluster;
-  cfg.numAttrs = sp.ck > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, w4_matvec_kernel<T, GROUP, NT, SWIGLU>, p, sp.ck, sp.wk);
+  cfg.numAttrs = ck > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, w4_matvec_kernel<T, GROUP, NT, SWIGLU>, p, ck);
 }
 
 template <typename T, int GROUP, int NT>
-cudaError_t run_act(const W4Params& p, bool swiglu, Split sp, dim3 grid, cudaStream_t st) {
-  return swiglu ? launch<T, GROUP, NT, true>(p, sp, grid, st) : launch<T, GROUP, NT, false>(p, sp, grid, st);
+cudaError_t run_act(const W4Params& p, bool swiglu, int ck, dim3 grid, cudaStream_t st) {
+  return swiglu ? launch<T, GROUP, NT, true>(p, ck, grid, st) : launch<T, GROUP, NT, false>(p, ck, grid, st);
 }
 
 template <typename T, int GROUP>
-cudaError_t run_nt(const W4Params& p, int64_t tokens, bool swiglu, Split sp, dim3 grid, cudaStream_t st) {
-  if (tokens <= 8) return run_act<T, GROUP, 1>(p, swiglu, sp, grid, st);
-  if (tokens <= 16) return run_act<T, GROUP, 2>(p, swiglu, sp, grid, st);
-  return run_act<T, GROUP, 4>(p, swiglu, sp, grid, st);
+cudaError_t run_nt(const W4Params& p, int64_t tokens, bool swiglu, int ck, dim3 grid, cudaStream_t st) {
+  if (tokens <= 8) return run_act<T, GROUP, 1>(p, swiglu, ck, grid, st);
+  if (tokens <= 16) return run_act<T, GROUP, 2>(p, swiglu, ck, grid, st);
+  return run_act<T, GROUP, 4>(p, swiglu, ck, grid, st);
 }
 
 template <typename T>
-cudaError_t run_group(const W4Params& p, int group, int64_t tokens, bool swiglu, Split sp, dim3 grid,
+cudaError_t run_group(const W4Params& p, int group, int64_t tokens, bool swiglu, int ck, dim3 grid,
                       cudaStream_t st) {
   switch (group) {
-    case 32: return run_nt<T, 32>(p, tokens, swiglu, sp, grid, st);
-    case 64: return run_nt<T, 64>(p, tokens, swiglu, sp, grid, st);
-    default: return run_nt<T, 128>(p, tokens, swiglu, sp, grid, st);
+    case 32: return run_nt<T, 32>(p, tokens, swiglu, ck, grid, st);
+    case 64: return run_nt<T, 64>(p, tokens, swiglu, ck, grid, st);
+    default: return run_nt<T, 128>(p, tokens, swiglu, ck, grid, st);
   }
 }
 
@@ -531,6 +576,8 @@ W4Params base_params(const moe_w4& w, const moe_rows& x, const moe_rows& y) {
   p.Kd = w.Kd;
   p.G = (w.Kd + w.group - 1) / w.group;
   p.zero_bytes = (p.G + 1) / 2;
+  p.vector_scales = p.G % 8 == 0 && (reinterpret_cast<uintptr_t>(w.scales) & 15) == 0;
+  p.vector_zeros = p.zero_bytes % 4 == 0 && (reinterpret_cast<uintptr_t>(w.zeros) & 3) == 0;
   p.x = x.data;
   p.sx = x.stride;
   p.y = y.data;
@@ -545,16 +592,11 @@ cudaError_t run(const moe_w4& w, const W4Params& p, int64_t tokens, int64_t matr
   const int64_t blocks = (w.N + kWarpRows - 1) / kWarpRows;  // row blocks of a matrix
   const int64_t want = (int64_t)device_sm_count() * 2 * kWarps;  // warps that fill the device
   const int64_t steps = (w.Kd + kStepK - 1) / kStepK;
-  const int groups = kStepK / w.group, toks = tokens <= 8 ? 8 : tokens <= 16 ? 16 : 32;  // a pass
-  Split sp = {1, 1};
-  while (sp.ck < 8 && blocks * matrices * sp.ck < want && steps >= 2 * sp.ck) sp.ck *= 2;
-  // a chunk of staged tokens holds a step of every warp of a row block
-  while (sp.wk < kWarps && blocks * matrices * sp.ck * sp.wk < want && steps >= 2 * sp.ck * sp.wk &&
-         token_chunk(toks, groups, sp.wk * 2) > 0)
-    sp.wk *= 2;
-  const dim3 grid((unsigned)((blocks * sp.wk + kWarps - 1) / kWarps * sp.ck), (unsigned)matrices);
-  return w.dtype == MOE_ELEM_BF16 ? run_group<__nv_bfloat16>(p, w.group, tokens, swiglu, sp, grid, st)
-                                  : run_group<__half>(p, w.group, tokens, swiglu, sp, grid, st);
+  int ck = 1;  // CTAs that share a row's K
+  while (ck < 8 && blocks * matrices * ck < want && steps >= 2 * ck) ck *= 2;
+  const dim3 grid((unsigned)((blocks + kWarps - 1) / kWarps * ck), (unsigned)matrices);
+  return w.dtype == MOE_ELEM_BF16 ? run_group<__nv_bfloat16>(p, w.group, tokens, swiglu, ck, grid, st)
+                                  : run_group<__half>(p, w.group, tokens, swiglu, ck, grid, st);
 }
 
 }  // namespace
