@@ -31,8 +31,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kQuantThreads = 256;
+constexpr int kQuantWarps = kQuantThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr int kTokStride = 20;  // floats between tokens of a partial tile: conflict-free fragment stores
 
 struct W4Params {
@@ -62,6 +63,13 @@ MOE_DEVICE void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same with sums that start at zero.
+MOE_DEVICE void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // The integer 0..15 as a float.
 MOE_DEVICE float small_float(uint32_t v) { return __uint_as_float(0x4B000000u | v) - 8388608.0f; }
 
@@ -74,7 +82,7 @@ MOE_DEVICE float scale_bits(uint16_t b) {
 MOE_DEVICE int nth_active_expert(const W4Params& p, int a) {
   __shared__ unsigned words[32];
   const int lane = threadIdx.x & 31;
-  for (int base = 0; base < p.E; base += kThreads) {
+  for (int base = 0; base < p.E; base += (int)blockDim.x) {
     const int e = base + threadIdx.x;
     const bool on = e < p.E && p.counts[e] > 0 && p.offsets[e] < p.cap;
     const unsigned m = __ballot_sync(0xffffffffu, on);
@@ -98,23 +106,28 @@ constexpr int kStepK = 128;
 constexpr int kRowBytes = kStepK / 2;
 constexpr int kWarpRows = 32;
 constexpr int kStageBytes = kWarpRows * kRowBytes;
-constexpr int kStages = 5;
-constexpr int kRingBytes = kStages * kStageBytes;
 // Scales and zero points stream with the codes, eight groups of the 32 rows at
 // a time (16 and 4 bytes a row), into slots enough for the steps in flight.
 constexpr int kSlotBytes = kWarpRows * (16 + 4);
 __host__ __device__ constexpr int scale_slots(int group) { return group == 128 ? 2 : 4; }
 // Staged tokens: per step and token 128 f16 and, for each group, the sum of
 // what they hold and the factor that undoes their scaling.
-constexpr int kSmemBytes = 115456;  // two CTAs fill an SM's shared memory
-__host__ __device__ constexpr int token_bytes(int group) {
-  return kSmemBytes - kWarps * (kRingBytes + scale_slots(group) * kSlotBytes);
-}
-// Steps of `toks` tokens that fit (host and device).
-__host__ __device__ constexpr int token_chunk(int toks, int group) {
-  return token_bytes(group) / (toks * kStepK * 2 + (toks + 1) / 2 * 2 * (kStepK / group) * 8);
-}
-static_assert(token_chunk(32, 32) > 0, "a pass of any size makes progress");
+// How a CTA shares an SM (host and device).
+template <int GROUP, int NT>
+struct Plan {
+  static constexpr int kWarps = NT == 1 ? 8 : 16, kThreads = 32 * kWarps;
+  static constexpr int kCtas = NT == 1 ? 3 : 1;  // CTAs of an SM
+  static constexpr int kStages = NT == 1 ? 3 : 5;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kSlots = scale_slots(GROUP);
+  static constexpr int kSmemBytes = 228 * 1024 / kCtas / 128 * 128 - 1024 - 128;  // less what the system and statics take
+  static constexpr int kTokenBytes = kSmemBytes - kWarps * (kRingBytes + kSlots * kSlotBytes);
+  // steps of `toks` tokens that fit
+  static MOE_DEVICE int chunk(int toks) {
+    return kTokenBytes / (toks * kStepK * 2 + (toks + 1) / 2 * 2 * (kStepK / GROUP) * 8);
+  }
+  static_assert(kTokenBytes >= 8 * NT * (kStepK * 2 + kStepK / GROUP * 8), "a pass makes progress");
+};
 
 MOE_DEVICE int chunk_at(int row, int chunk) {
   return row * kRowBytes + ((chunk ^ ((row >> 1 & 1) << 1 | (row >> 2 & 1))) << 4);
@@ -143,7 +156,7 @@ MOE_DEVICE int frag_at(int tok, int j, int c) { return (j ^ (tok & 1)) * 4 + c; 
 // (step * toks + token) * 16 + frag_at: the pairs (0, 4), (1, 5) / 16, (2, 6),
 // (3, 7) / 16 of the eight k of that code word.  aux: {sum, factor} at
 // (step * groups + group) * even(toks) + token.
-template <typename T, int GROUP>
+template <typename T, int GROUP, int kThreads>
 MOE_DEVICE void stage_tokens(const T* x, int64_t sx, int64_t Kd, int toks, int s0, int s1, uint4* frag, float2* aux) {
   constexpr int U = kStepK / GROUP;
   constexpr int kBatch = 4;  // units a half-warp has in flight
@@ -191,19 +204,14 @@ MOE_DEVICE void stage_tokens(const T* x, int64_t sx, int64_t Kd, int toks, int s
         const float m = i & 1 ? up16 : up;
         h[i] = __floats2half2_rn(f[i] * m, f[i + 4] * m);
       }
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float2 v = __half22float2(h[i]);
-        sum = fmaf(v.x + v.y, i & 1 ? 16.0f : 1.0f, sum);
-      }
+      float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
 #pragma unroll
       for (int d = GROUP / 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (s0 + s < s1) {
         frag[(s * toks + tok) * 16 + frag_at(tok, j, c)] = *reinterpret_cast<uint4*>(h);
         if (k8 % (GROUP / 8) == 0)
           aux[(s * U + k8 / (GROUP / 8)) * even + tok] =
-              make_float2(sum * 0x1p-24f, __uint_as_float((uint32_t)(127 + 12 - 14 + E) << 23));
+              make_float2(sum * (up * 0x1p-24f), __uint_as_float((uint32_t)(127 + 12 - 14 + E) << 23));
       }
       s += ds;
       tok += dt;
@@ -230,11 +238,12 @@ MOE_DEVICE float ld_cluster(const float* at, int rank) {
 // features.  The K steps of a row are shared by the ck CTAs of a cluster, a
 // run of steps each.
 template <typename T, int GROUP, int NT, bool SWIGLU>
-__global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int ck) {
+__global__ void __launch_bounds__(Plan<GROUP, NT>::kThreads, Plan<GROUP, NT>::kCtas) w4_matvec_kernel(W4Params p, int ck) {
   constexpr int U = kStepK / GROUP;                    // groups a step
   constexpr int W = GROUP / 32;                        // 32-bit code words a lane takes of a group and row
   constexpr int kFeatures = SWIGLU ? 16 : kWarpRows;   // output features of a warp's rows
-  constexpr int kSlots = scale_slots(GROUP);
+  using P = Plan<GROUP, NT>;
+  constexpr int kWarps = P::kWarps, kThreads = P::kThreads, kSlots = P::kSlots, kStages = P::kStages, kRingBytes = P::kRingBytes;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   const int gr = lane >> 2, c = lane & 3;
@@ -326,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
 
   for (int64_t t0 = 0; t0 < M; t0 += 8 * NT) {
     const int toks = (int)min64(M - t0, 8 * NT), even = (toks + 1) & ~1;
-    const int chunk = min(token_chunk(toks, GROUP), run);
+    const int chunk = min(P::chunk(toks), run);
     float2* aux = reinterpret_cast<float2*>(frag + chunk * toks * 16);
     float acc[2][NT][4] = {};
 #pragma unroll
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
     for (int s0 = begin; s0 < end; s0 += chunk) {
       const int s1 = min(s0 + chunk, end);
       if (s0 > begin) __syncthreads();  // the last chunk has been read
-      stage_tokens<T, GROUP>(x + t0 * p.sx, p.sx, p.Kd, toks, s0, s1, frag, aux);
+      stage_tokens<T, GROUP, kThreads>(x + t0 * p.sx, p.sx, p.Kd, toks, s0, s1, frag, aux);
       __syncthreads();
       const uint8_t* tokens = reinterpret_cast<const uint8_t*>(frag);
       const uint8_t* sums = reinterpret_cast<const uint8_t*>(aux);
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
               w[q][0] = *reinterpret_cast<const uint32_t*>(t + chunk_at(gr, u) + c * 4);
             }
           }
-          float part[2][NT][4] = {};
+          float part[2][NT][4];
 #pragma unroll
           for (int j = 0; j < W; j++) {
             // fragment order: row gr, row gr + 8, then both again at the next pair
@@ -405,7 +414,10 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
               const uint4 b = *reinterpret_cast<const uint4*>(tokens + tok_to[nt][word & 1] + (word & 2) * 64);
 #pragma unroll
               for (int rt = 0; rt < 2; rt++) {
-                mma_f16(part[rt][nt], a[rt][0], b.x, b.y);
+                if (j == 0)
+                  mma_f16_first(part[rt][nt], a[rt][0], b.x, b.y);
+                else
+                  mma_f16(part[rt][nt], a[rt][0], b.x, b.y);
                 mma_f16(part[rt][nt], a[rt][1], b.z, b.w);
               }
             }
@@ -444,25 +456,25 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
         for (int i = 0; i < 4; i++)
           red[rt * kTile + (nt * 8 + 2 * c + (i & 1)) * kTokStride + gr + 8 * (i >> 1)] =
               acc[rt][nt][i] * 0x1p12f;  // with the staged factor 2^12 / f: 2^24 / f
-    // every CTA of the cluster finishes its share of the features
-    const int features = kWarps * kFeatures / ck, log_features = 31 - __clz(features);  // powers of two
+    // every CTA of the cluster finishes a share of the outputs
+    constexpr int kCtaFeatures = kWarps * kFeatures;
     if (ck > 1)
       cluster_barrier();
     else
       __syncthreads();
-    for (int i = threadIdx.x; i < features * toks; i += kThreads) {
-      const int f = rank * features + (i & (features - 1)), tt = i >> log_features, r = f % kFeatures;
+    for (int i = rank * kThreads + threadIdx.x; i < kCtaFeatures * toks; i += ck * kThreads) {
+      const int f = i % kCtaFeatures, tt = i / kCtaFeatures, r = f % kFeatures;
       const int64_t n = cta_n0 + f, tok = t0 + tt;
       if (n >= n_out) continue;
       const float* base = reinterpret_cast<const float*>(smem + (f / kFeatures) * kRingBytes);
       auto total = [&](int rt) {
         const float* at = base + rt * kTile + tt * kTokStride + (r & 15);
-        float part[8], v = 0.0f;
+        float part[kMaxCluster], v = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 8; q++)  // in flight together
+        for (int q = 0; q < kMaxCluster; q++)  // in flight together
           if (q < ck) part[q] = ck > 1 ? ld_cluster(at, q) : *at;
 #pragma unroll
-        for (int q = 0; q < 8; q++)
+        for (int q = 0; q < kMaxCluster; q++)
           if (q < ck) v += part[q];
         return v;
       };
@@ -485,11 +497,11 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(W4Params p, int 
 
 // One warp per row and pair of groups (the two zero points of a byte).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) quantize_w4_kernel(const T* w, int64_t R, int64_t Kd, int group, int64_t G,
+__global__ void __launch_bounds__(kQuantThreads) quantize_w4_kernel(const T* w, int64_t R, int64_t Kd, int group, int64_t G,
                                                                uint8_t* codes, T* scales, uint8_t* zeros) {
   const int lane = threadIdx.x & 31;
   const int64_t pairs = (G + 1) / 2, items = R * pairs;
-  for (int64_t it = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * kWarps) {
+  for (int64_t it = (int64_t)blockIdx.x * kQuantWarps + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * kQuantWarps) {
     const int64_t r = it / pairs, g0 = it % pairs * 2;
     uint32_t zbyte = 0;
     for (int64_t g = g0; g < g0 + 2 && g < G; g++) {
@@ -524,46 +536,72 @@ __global__ void __launch_bounds__(kThreads) quantize_w4_kernel(const T* w, int64
 }
 
 template <typename T, int GROUP, int NT, bool SWIGLU>
-cudaError_t launch(const W4Params& p, int ck, dim3 grid, cudaStream_t st) {
-  static PerDeviceOnce once;
-  cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(w4_matvec_kernel<T, GROUP, NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSmemBytes);
-  });
-  if (e != cudaSuccess) return e;
+cudaError_t launch(const W4Params& p, int64_t matrices, cudaStream_t st) {
+  using P = Plan<GROUP, NT>;
   cudaLaunchAttribute cluster = {};
   cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = (unsigned)ck;
   cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = st;
+  cfg.blockDim = dim3(P::kThreads);
+  cfg.dynamicSmemBytes = P::kSmemBytes;
   cfg.attrs = &cluster;
+
+  // clusters of each size that run at once: a cluster stays within one group of
+  // SMs, so that some sizes leave SMs empty
+  static PerDeviceOnce once;
+  static int at_once[PerDeviceOnce::kMaxDevices][kMaxCluster + 1];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run([&] {
+    cudaError_t r = cudaFuncSetAttribute(w4_matvec_kernel<T, GROUP, NT, SWIGLU>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmemBytes);
+    cfg.numAttrs = 1;
+    for (int k = 1; k <= kMaxCluster && r == cudaSuccess; k++) {
+      cluster.val.clusterDim.x = (unsigned)k;
+      cfg.gridDim = dim3((unsigned)k);
+      r = cudaOccupancyMaxActiveClusters(&at_once[dev][k], w4_matvec_kernel<T, GROUP, NT, SWIGLU>, &cfg);
+    }
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  // CTAs that share a row's K: as many as shorten the longest chain of steps,
+  // counting what a CTA spends around its steps as kOverhead of them
+  constexpr int64_t kOverhead = 8;
+  const int64_t ctas = (p.N + kWarpRows * P::kWarps - 1) / (kWarpRows * P::kWarps), steps = (p.Kd + kStepK - 1) / kStepK;
+  int ck = 1;
+  int64_t best = 0;
+  for (int k = 1; k <= kMaxCluster && k <= steps; k++) {
+    if (at_once[dev][k] < 1) continue;
+    const int64_t cost =
+        (ctas * matrices + at_once[dev][k] - 1) / at_once[dev][k] * ((steps + k - 1) / k + kOverhead);
+    if (k == 1 || cost < best) best = cost, ck = k;
+  }
+  cluster.val.clusterDim.x = (unsigned)ck;
+  cfg.gridDim = dim3((unsigned)(ctas * ck), (unsigned)matrices);
+  cfg.stream = st;
   cfg.numAttrs = ck > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, w4_matvec_kernel<T, GROUP, NT, SWIGLU>, p, ck);
 }
 
 template <typename T, int GROUP, int NT>
-cudaError_t run_act(const W4Params& p, bool swiglu, int ck, dim3 grid, cudaStream_t st) {
-  return swiglu ? launch<T, GROUP, NT, true>(p, ck, grid, st) : launch<T, GROUP, NT, false>(p, ck, grid, st);
+cudaError_t run_act(const W4Params& p, bool swiglu, int64_t matrices, cudaStream_t st) {
+  return swiglu ? launch<T, GROUP, NT, true>(p, matrices, st) : launch<T, GROUP, NT, false>(p, matrices, st);
 }
 
 template <typename T, int GROUP>
-cudaError_t run_nt(const W4Params& p, int64_t tokens, bool swiglu, int ck, dim3 grid, cudaStream_t st) {
-  if (tokens <= 8) return run_act<T, GROUP, 1>(p, swiglu, ck, grid, st);
-  if (tokens <= 16) return run_act<T, GROUP, 2>(p, swiglu, ck, grid, st);
-  return run_act<T, GROUP, 4>(p, swiglu, ck, grid, st);
+cudaError_t run_nt(const W4Params& p, int64_t tokens, bool swiglu, int64_t matrices, cudaStream_t st) {
+  if (tokens <= 8) return run_act<T, GROUP, 1>(p, swiglu, matrices, st);
+  if (tokens <= 16) return run_act<T, GROUP, 2>(p, swiglu, matrices, st);
+  return run_act<T, GROUP, 4>(p, swiglu, matrices, st);
 }
 
 template <typename T>
-cudaError_t run_group(const W4Params& p, int group, int64_t tokens, bool swiglu, int ck, dim3 grid,
-                      cudaStream_t st) {
+cudaError_t run_group(const W4Params& p, int group, int64_t tokens, bool swiglu, int64_t matrices, cudaStream_t st) {
   switch (group) {
-    case 32: return run_nt<T, 32>(p, tokens, swiglu, ck, grid, st);
-    case 64: return run_nt<T, 64>(p, tokens, swiglu, ck, grid, st);
-    default: return run_nt<T, 128>(p, tokens, swiglu, ck, grid, st);
+    case 32: return run_nt<T, 32>(p, tokens, swiglu, matrices, st);
+    case 64: return run_nt<T, 64>(p, tokens, swiglu, matrices, st);
+    default: return run_nt<T, 128>(p, tokens, swiglu, matrices, st);
   }
 }
 
@@ -589,14 +627,8 @@ W4Params base_params(const moe_w4& w, const moe_rows& x, const moe_rows& y) {
 cudaError_t run(const moe_w4& w, const W4Params& p, int64_t tokens, int64_t matrices, int32_t activation,
                 cudaStream_t st) {
   const bool swiglu = activation == MOE_W4_SWIGLU;
-  const int64_t blocks = (w.N + kWarpRows - 1) / kWarpRows;  // row blocks of a matrix
-  const int64_t want = (int64_t)device_sm_count() * 2 * kWarps;  // warps that fill the device
-  const int64_t steps = (w.Kd + kStepK - 1) / kStepK;
-  int ck = 1;  // CTAs that share a row's K
-  while (ck < 8 && blocks * matrices * ck < want && steps >= 2 * ck) ck *= 2;
-  const dim3 grid((unsigned)((blocks + kWarps - 1) / kWarps * ck), (unsigned)matrices);
-  return w.dtype == MOE_ELEM_BF16 ? run_group<__nv_bfloat16>(p, w.group, tokens, swiglu, ck, grid, st)
-                                  : run_group<__half>(p, w.group, tokens, swiglu, ck, grid, st);
+  return w.dtype == MOE_ELEM_BF16 ? run_group<__nv_bfloat16>(p, w.group, tokens, swiglu, matrices, st)
+                                  : run_group<__half>(p, w.group, tokens, swiglu, matrices, st);
 }
 
 }  // namespace
@@ -619,21 +651,22 @@ cudaError_t launch_grouped_w4_matvec(const moe_handle_dev& h, const moe_shape& s
   const int64_t routes = s.T * s.K;
   p.every = routes >= s.E;
   // a token's routes go to different experts, so an expert has at most T rows
+  // a pass holds twice the mean rows of an expert: few experts need a second
   const int64_t mean_rows = (routes + s.E - 1) / s.E;
-  return run(w, p, s.T <= 8 ? s.T : mean_rows <= 12 ? 16 : s.T, routes < s.E ? routes : s.E, activation, st);
+  return run(w, p, s.T < 2 * mean_rows ? s.T : 2 * mean_rows, routes < s.E ? routes : s.E, activation, st);
 }
 
 cudaError_t launch_quantize_w4_rows(const void* w, int64_t R, int64_t Kd, int32_t group, int32_t dtype, void* codes,
                                     void* scales, void* zeros, cudaStream_t st) {
   const int64_t G = (Kd + group - 1) / group, items = R * ((G + 1) / 2);
-  const int64_t cap = (int64_t)device_sm_count() * (2048 / kThreads), blocks = (items + kWarps - 1) / kWarps;
+  const int64_t cap = (int64_t)device_sm_count() * (2048 / kQuantThreads), blocks = (items + kQuantWarps - 1) / kQuantWarps;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   if (dtype == MOE_ELEM_BF16)
-    quantize_w4_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(
+    quantize_w4_kernel<__nv_bfloat16><<<grid, kQuantThreads, 0, st>>>(
         static_cast<const __nv_bfloat16*>(w), R, Kd, group, G, static_cast<uint8_t*>(codes),
         static_cast<__nv_bfloat16*>(scales), static_cast<uint8_t*>(zeros));
   else
-    quantize_w4_kernel<__half><<<grid, kThreads, 0, st>>>(static_cast<const __half*>(w), R, Kd, group, G,
+    quantize_w4_kernel<__half><<<grid, kQuantThreads, 0, st>>>(static_cast<const __half*>(w), R, Kd, group, G,
                                                           static_cast<uint8_t*>(codes), static_cast<__half*>(scales),
                                                           static_cast<uint8_t*>(zeros));
   return cudaGetLastError();
