@@ -616,8 +616,8 @@ typedef struct moe_w4 {
   int32_t group;      /* 32, 64 or 128 */
   int32_t dtype;      /* MOE_ELEM_BF16 or MOE_ELEM_F16: scales, inputs and outputs */
   const void* codes;  /* device, 16-byte aligned */
-  const void* scales; /* device */
-  const void* zeros;  /* device or NULL */
+  const void* scales; /* device, 16-byte aligned */
+  const void* zeros;  /* device, 16-byte aligned, or NULL */
 } moe_w4;
 
 /* What follows the product. */
@@ -629,8 +629,11 @@ enum {
 
 /* y[m] = act( W x[m] ) (+ addend[m]), rounded to dtype once: products of few
  * tokens with one weight matrix (a shared expert or a projection of a decode
- * step).  (q - z) and x are exact operands of tensor-core products summed in
- * fp32 per group; each group's sum is scaled in fp32.  x: M rows of Kd (16-byte
+ * step).  Each group's sums of q x and of x are formed in fp32 (the first on the
+ * tensor cores from exact operands: 128 elements of a token at a time are
+ * brought to f16's range by a power of two, which keeps all bits of an element
+ * down to 2^-24 of the largest), and their difference is scaled in fp32.  A
+ * token that holds an infinity or a NaN gives NaN.  x: M rows of Kd (16-byte
  * aligned, stride a multiple of 8); y: M rows of N (N/2 with SwiGLU; N must be
  * even); addend: optional, as y (it may be y itself), only without SwiGLU.  y
  * must not overlap x.  Any M >= 0; the weights are read once per 32 tokens. */

@@ -79,7 +79,9 @@ moe_status check_w4(const moe_w4* w) {
   if (!w || w->N < 1 || w->N > (1 << 24) || w->Kd < 32 || w->Kd > (1 << 20) || w->Kd % 32) return MOE_ERR_INVALID_ARG;
   if (w->group != 32 && w->group != 64 && w->group != 128) return MOE_ERR_INVALID_ARG;
   if (w->dtype != MOE_ELEM_BF16 && w->dtype != MOE_ELEM_F16) return MOE_ERR_INVALID_ARG;
-  if (!w->codes || !aligned_to(w->codes, 16) || !w->scales || !aligned_to(w->scales, 2)) return MOE_ERR_INVALID_ARG;
+  if (!w->codes || !aligned_to(w->codes, 16) || !w->scales || !aligned_to(w->scales, 16) ||
+      !aligned_to(w->zeros, 16))
+    return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
