@@ -70,6 +70,134 @@ __global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(NormParams p) 
   }
 }
 
+// 16 bytes of a row as fp32.
+template <typename T>
+struct Vec {
+  static constexpr int kN = 16 / sizeof(T);
+  T e[kN];
+};
+
+template <typename T>
+MOE_DEVICE void load_vec(float (&out)[Vec<T>::kN], const T* p) {
+  union {
+    uint4 v;
+    Vec<T> t;
+  } u;
+  u.v = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::kN; i++) out[i] = to_float(u.t.e[i]);
+}
+
+template <typename T>
+MOE_DEVICE void store_vec(T* p, const float (&in)[Vec<T>::kN]) {
+  union {
+    uint4 v;
+    Vec<T> t;
+  } u;
+#pragma unroll
+  for (int i = 0; i < Vec<T>::kN; i++) u.t.e[i] = from_float<T>(in[i]);
+  *reinterpret_cast<uint4*>(p) = u.v;
+}
+
+// Parameters of the same columns: fp32 or the rows' type.
+template <typename T, typename P>
+MOE_DEVICE void load_params(float (&out)[Vec<T>::kN], const P* p) {
+  constexpr int kPieces = Vec<T>::kN * (int)sizeof(P) / 16;  // 1, or 2 for fp32 beside 16-bit rows
+#pragma unroll
+  for (int k = 0; k < kPieces; k++) {
+    float part[Vec<P>::kN];
+    load_vec<P>(part, p + k * Vec<P>::kN);
+#pragma unroll
+    for (int i = 0; i < Vec<P>::kN; i++) out[k * Vec<P>::kN + i] = part[i];
+  }
+}
+
+// Rows of 16-byte vectors held in registers between the mean, the variance and
+// the result, so that the row is read once.  kTeam threads take a row, V vectors
+// each: a warp up to 32 V vectors, else a whole CTA.
+template <typename T, typename P, int V, int TEAM>
+__global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM) layer_norm_vec_kernel(NormParams p) {
+  constexpr int N = Vec<T>::kN;
+  constexpr int kTeams = TEAM == 32 ? kThreads / 32 : 1;
+  __shared__ float2 red[2][TEAM == 32 ? 1 : TEAM / 32];
+  const P* w = static_cast<const P*>(p.w);
+  const P* b = static_cast<const P*>(p.b);
+  const int t = threadIdx.x % TEAM;
+  const int nvec = (int)(p.H / N);
+  for (int64_t r = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; r < p.rows; r += (int64_t)gridDim.x * kTeams) {
+    const T* x = static_cast<const T*>(p.x) + r * p.sx;
+    const T* res = p.res ? static_cast<const T*>(p.res) + r * p.sres : nullptr;
+    T* sum = p.sum ? static_cast<T*>(p.sum) + r * p.ssum : nullptr;
+    T* y = static_cast<T*>(p.y) + r * p.sy;
+    float h[V][N];
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      const int i = v * TEAM + t;
+      if (i < nvec) {
+        load_vec<T>(h[v], x + i * N);
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; k++) h[v][k] = 0.0f;
+      }
+    }
+    if (res) {
+#pragma unroll
+      for (int v = 0; v < V; v++) {
+        const int i = v * TEAM + t;
+        if (i < nvec) {
+          float a[N];
+          load_vec<T>(a, res + i * N);
+#pragma unroll
+          for (int k = 0; k < N; k++) h[v][k] = to_float(from_float<T>(h[v][k] + a[k]));
+          if (sum) store_vec<T>(sum + i * N, h[v]);
+        }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++)
+#pragma unroll
+      for (int k = 0; k < N; k++) s += h[v][k];
+    const float mean = (TEAM == 32 ? warp_sum(s) : block_sum2(s, 0.0f, red[0]).x) / (float)p.H;
+    float q = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      const bool in = v * TEAM + t < nvec;
+#pragma unroll
+      for (int k = 0; k < N; k++) {
+        h[v][k] -= mean;
+        if (in) q = fmaf(h[v][k], h[v][k], q);
+      }
+    }
+    const float var = (TEAM == 32 ? warp_sum(q) : block_sum2(q, 0.0f, red[1]).x) / (float)p.H;
+    const float rstd = 1.0f / sqrtf(var + p.eps);
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      const int i = v * TEAM + t;
+      if (i < nvec) {
+        float g[N];
+#pragma unroll
+        for (int k = 0; k < N; k++) h[v][k] *= rstd;
+        if (w) {
+          load_params<T, P>(g, w + i * N);
+#pragma unroll
+          for (int k = 0; k < N; k++) h[v][k] *= g[k];
+        }
+        if (b) {
+          load_params<T, P>(g, b + i * N);
+#pragma unroll
+          for (int k = 0; k < N; k++) h[v][k] += g[k];
+        }
+        store_vec<T>(y + i * N, h[v]);
+      }
+    }
+    if (t == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+  }
+}
+
 struct NormBwdParams {
   int64_t rows, H;
   int64_t sgy, sh, sgsum, sgx;
@@ -140,17 +268,181 @@ __global__ void __launch_bounds__(kThreads) layer_norm_bwd_cols_kernel(NormBwdPa
   }
 }
 
-// Adds the chunks' partial sums up in order.
-__global__ void __launch_bounds__(kThreads) layer_norm_bwd_finish_kernel(NormBwdParams p) {
-  const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (c >= p.H) return;
-  float sw = 0.0f, sb = 0.0f;
-  for (int64_t k = 0; k < p.chunks; k++) {
-    sw += p.pw[k * p.H + c];
-    sb += p.pb[k * p.H + c];
+MOE_DEVICE void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Sums of two values over a team of `warps` warps, known to its threads; one
+// barrier.  Halves of a warp reduce one value each.  `red`: a float2 per warp,
+// not written again before the team's next barrier but one.
+MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, int barrier) {
+  const int lane = threadIdx.x & 31;
+  const bool low = lane < 16;
+  auto halves = [&](float x, float y) {  // lanes 0-15: sum of x over the warp, 16-31: of y
+    float v = (low ? x : y) + __shfl_xor_sync(0xffffffffu, low ? y : x, 16);
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+  };
+  float v = halves(a, b);
+  if (warps > 1) {
+    if ((lane & 15) == 0) reinterpret_cast<float*>(red + warp)[low ? 0 : 1] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
+    const float2 t = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
+    v = halves(t.x, t.y);
   }
-  if (p.gw) p.gw[c] = sw;
-  if (p.gb) p.gb[c] = sb;
+  return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+}
+
+// Rows of 16-byte vectors: one pass that forms gx and a CTA's partial sums of
+// gw and gb.  A team of threads takes a row, V vectors a thread, and keeps the
+// sums of its columns in registers over the rows it meets; its next rows are on
+// their way into a ring of kStages that is each thread's own, so that only the
+// two sums of a row need a barrier.
+template <typename T, typename P, int V, int STAGES>
+__global__ void __launch_bounds__(1024, 1) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
+  constexpr int N = Vec<T>::kN;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 red[2][32];
+  const int team = threadIdx.x / team_threads, teams = blockDim.x / team_threads, t = threadIdx.x % team_threads;
+  const int warp = t >> 5, warps = team_threads >> 5;
+  const int nvec = (int)(p.H / N);
+  const int64_t step = (int64_t)gridDim.x * teams;
+  const int64_t first = (int64_t)blockIdx.x * teams + team;
+  const P* w = static_cast<const P*>(p.w);
+  // ring: [stage][matrix][vector of the thread][thread]
+  const uint32_t own = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+  const int matrices = p.gsum ? 3 : 2;
+  const int vec_bytes = blockDim.x * 16, matrix_bytes = V * vec_bytes, stage_bytes = matrices * matrix_bytes;
+
+  auto fill = [&](int64_t r, int stage) {
+    if (r < p.rows) {
+      const T* gy = static_cast<const T*>(p.gy) + r * p.sgy;
+      const T* h = static_cast<const T*>(p.h) + r * p.sh;
+      const T* gs = static_cast<const T*>(p.gsum) + r * p.sgsum;
+      const uint32_t dst = own + stage * stage_bytes;
+#pragma unroll
+      for (int v = 0; v < V; v++) {
+        const int i = v * team_threads + t;
+        if (i < nvec) {
+          cp_async16(dst + v * vec_bytes, gy + i * N);
+          cp_async16(dst + matrix_bytes + v * vec_bytes, h + i * N);
+          if (p.gsum) cp_async16(dst + 2 * matrix_bytes + v * vec_bytes, gs + i * N);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto staged = [&](int stage, int matrix, int v, float(&out)[N]) {
+    load_vec<T>(out, reinterpret_cast<const T*>(smem + threadIdx.x * 16 + stage * stage_bytes + matrix * matrix_bytes +
+                                                v * vec_bytes));
+  };
+
+  float wv[V][N], aw[V][N] = {}, ab[V][N] = {};
+#pragma unroll
+  for (int v = 0; v < V; v++) {
+    const int i = v * team_threads + t;
+#pragma unroll
+    for (int k = 0; k < N; k++) wv[v][k] = 1.0f;
+    if (w && i < nvec) load_params<T, P>(wv[v], w + i * N);
+  }
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; i++) fill(first + i * step, i);
+  float mean = 0.0f, rstd = 0.0f;
+  if (first < p.rows) mean = p.mean[first], rstd = p.rstd[first];
+  int stage = 0, phase = 0;
+  for (int64_t r = first; r < p.rows; r += step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    fill(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);  // the stage of the row before
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    if (r + step < p.rows) next_mean = p.mean[r + step], next_rstd = p.rstd[r + step];
+    float su = 0.0f, sx = 0.0f;
+    float u[V][N], xhat[V][N];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      if (v * team_threads + t >= nvec) continue;
+      staged(stage, 0, v, u[v]);
+      staged(stage, 1, v, xhat[v]);
+#pragma unroll
+      for (int k = 0; k < N; k++) {
+        xhat[v][k] = (xhat[v][k] - mean) * rstd;
+        aw[v][k] = fmaf(u[v][k], xhat[v][k], aw[v][k]);
+        ab[v][k] += u[v][k];
+        u[v][k] *= wv[v][k];
+        su += u[v][k];
+        sx = fmaf(u[v][k], xhat[v][k], sx);
+      }
+    }
+    const float2 sums = team_sum2(su, sx, red[phase] + team * warps, warp, warps, team + 1);
+    const float mu = sums.x / (float)p.H, mx = sums.y / (float)p.H;
+    T* gx = static_cast<T*>(p.gx) + r * p.sgx;
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      const int i = v * team_threads + t;
+      if (i >= nvec) continue;
+      float o[N];
+#pragma unroll
+      for (int k = 0; k < N; k++) o[k] = rstd * (u[v][k] - mu - xhat[v][k] * mx);
+      if (p.gsum) {
+        float g[N];
+        staged(stage, 2, v, g);
+#pragma unroll
+        for (int k = 0; k < N; k++) o[k] += g[k];
+      }
+      store_vec<T>(gx + i * N, o);
+    }
+    mean = next_mean;
+    rstd = next_rstd;
+    phase ^= 1;
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+  }
+  if (!p.gw && !p.gb) return;
+
+  // the CTA's partial sums: teams added up in order through the ring's memory
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int sum = 0; sum < 2; sum++) {
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; v++)
+#pragma unroll
+      for (int k = 0; k < N; k++) part[(v * N + k) * blockDim.x + threadIdx.x] = sum ? ab[v][k] : aw[v][k];
+    __syncthreads();
+    float* out = (sum ? p.pb : p.pw) + blockIdx.x * p.H;
+    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+      const int i = c / N, at = (i / team_threads * N + c % N) * blockDim.x + i % team_threads;
+      float s = 0.0f;
+      for (int k = 0; k < teams; k++) s += part[at + k * team_threads];
+      out[c] = s;
+    }
+  }
+}
+
+// Adds the chunks' partial sums up: 32 columns a CTA, each warp every eighth
+// chunk, the warps in order.
+__global__ void __launch_bounds__(kThreads) layer_norm_bwd_finish_kernel(NormBwdParams p) {
+  __shared__ float2 part[kWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float sw = 0.0f, sb = 0.0f;
+  if (c < p.H) {
+#pragma unroll 4
+    for (int64_t k = warp; k < p.chunks; k += kWarps) {
+      sw += p.pw[k * p.H + c];
+      sb += p.pb[k * p.H + c];
+    }
+  }
+  part[warp][lane] = make_float2(sw, sb);
+  __syncthreads();
+  if (warp == 0 && c < p.H) {
+    for (int i = 1; i < kWarps; i++) {
+      sw += part[i][lane].x;
+      sb += part[i][lane].y;
+    }
+    if (p.gw) p.gw[c] = sw;
+    if (p.gb) p.gb[c] = sb;
+  }
 }
 
 constexpr int64_t kMaxChunks = 304;
@@ -165,17 +457,86 @@ unsigned row_grid(int64_t rows) {
   return (unsigned)(rows < cap ? rows : cap);
 }
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Rows that start on 16 bytes and hold whole 16-byte vectors.
+bool vector_rows(const void* p, int64_t stride, int64_t rows, int bytes) {
+  return aligned16(p) && (rows <= 1 || stride * bytes % 16 == 0);
+}
+
+template <typename T, typename P, int V, int TEAM>
+void run_vec(const NormParams& p, cudaStream_t st) {
+  constexpr int kTeams = TEAM == 32 ? kThreads / 32 : 1, kBlock = TEAM == 32 ? kThreads : TEAM;
+  const int64_t blocks = (p.rows + kTeams - 1) / kTeams, cap = (int64_t)device_sm_count() * (2048 / kBlock);
+  layer_norm_vec_kernel<T, P, V, TEAM><<<(unsigned)(blocks < cap ? blocks : cap), kBlock, 0, st>>>(p);
+}
+
 template <typename T, typename P>
 cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
-  layer_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
+  const int b = sizeof(T);
+  const int64_t nvec = p.H * b / 16;
+  const bool vec = p.H * b % 16 == 0 && vector_rows(p.x, p.sx, p.rows, b) && vector_rows(p.res, p.sres, p.rows, b) &&
+                   vector_rows(p.sum, p.ssum, p.rows, b) && vector_rows(p.y, p.sy, p.rows, b) && aligned16(p.w) &&
+                   aligned16(p.b);
+  if (!vec || nvec > 4096)
+    layer_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
+  else if (nvec <= 32)
+    run_vec<T, P, 1, 32>(p, st);
+  else if (nvec <= 64)
+    run_vec<T, P, 2, 32>(p, st);
+  else if (nvec <= 128)
+    run_vec<T, P, 4, 32>(p, st);
+  else if (nvec <= 256)
+    run_vec<T, P, 2, 128>(p, st);
+  else if (nvec <= 512)
+    run_vec<T, P, 2, 256>(p, st);
+  else if (nvec <= 1024)
+    run_vec<T, P, 2, 512>(p, st);
+  else if (nvec <= 2048)
+    run_vec<T, P, 2, 1024>(p, st);
+  else
+    run_vec<T, P, 4, 1024>(p, st);
+  return cudaGetLastError();
+}
+
+template <typename T, typename P, int V, int STAGES>
+cudaError_t run_bwd_vec(NormBwdParams p, cudaStream_t st) {
+  static PerDeviceOnce once;
+  cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, V, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                1024 * 16 * 3 * V * STAGES);
+  });
+  if (e != cudaSuccess) return e;
+  const int nvec = (int)(p.H * sizeof(T) / 16);
+  const int team = ((nvec + V - 1) / V + 31) / 32 * 32;
+  int teams = 1024 / team < 15 ? 1024 / team : 15;  // named barriers 1 to 15
+  while (teams > 1 && p.rows < (int64_t)teams * device_sm_count()) teams--;
+  const int64_t blocks = (p.rows + teams - 1) / teams, sms = device_sm_count();
+  p.chunks = blocks < sms ? blocks : sms;
+  if (p.chunks > kMaxChunks) p.chunks = kMaxChunks;
+  const int block = team * teams;
+  const int ring = block * 16 * (p.gsum ? 3 : 2) * V * STAGES, part = block * 16 / (int)sizeof(T) * 4 * V;
+  p.pb = p.pw + p.chunks * p.H;
+  layer_norm_bwd_vec_kernel<T, P, V, STAGES><<<(unsigned)p.chunks, block, ring > part ? ring : part, st>>>(p, team);
+  if (p.gw || p.gb) layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, typename P>
-cudaError_t run_backward(const NormBwdParams& p, cudaStream_t st) {
+cudaError_t run_backward(NormBwdParams p, cudaStream_t st) {
+  const int b = sizeof(T);
+  const int64_t nvec = p.H * b / 16;
+  const bool vec = p.rows > 0 && p.H * b % 16 == 0 && vector_rows(p.gy, p.sgy, p.rows, b) &&
+                   vector_rows(p.h, p.sh, p.rows, b) && vector_rows(p.gsum, p.sgsum, p.rows, b) &&
+                   vector_rows(p.gx, p.sgx, p.rows, b) && aligned16(p.w);
+  if (vec && nvec <= 1024) return run_bwd_vec<T, P, 1, 4>(p, st);
+  if (vec && nvec <= 2048) return run_bwd_vec<T, P, 2, 2>(p, st);
+  p.chunks = bwd_chunks(p.rows);
+  p.rows_per_chunk = (p.rows + p.chunks - 1) / p.chunks;
+  p.pb = p.pw + p.chunks * p.H;
   if (p.gw || p.gb) {
     layer_norm_bwd_cols_kernel<T><<<dim3((unsigned)((p.H + 31) / 32), (unsigned)p.chunks), kThreads, 0, st>>>(p);
-    layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
+    layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kThreads, 0, st>>>(p);
   }
   if (p.rows > 0) layer_norm_bwd_rows_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
   return cudaGetLastError();
@@ -184,7 +545,9 @@ cudaError_t run_backward(const NormBwdParams& p, cudaStream_t st) {
 }  // namespace
 
 size_t layer_norm_workspace_bytes(int64_t rows, int64_t H) {
-  return (size_t)bwd_chunks(rows) * (size_t)H * 2 * sizeof(float);
+  // a partial sum per chunk of rows or per CTA, whichever kernel runs
+  const int64_t n = rows < 1 ? 1 : rows < kMaxChunks ? rows : kMaxChunks;
+  return (size_t)n * (size_t)H * 2 * sizeof(float);
 }
 
 cudaError_t launch_layer_norm(const moe_norm& n, const moe_rows& x, const moe_rows* res, const void* w, const void* b,
@@ -230,10 +593,7 @@ cudaError_t launch_layer_norm_backward(const moe_norm& n, const moe_rows& gy, co
   p.rstd = rstd;
   p.gw = gw;
   p.gb = gb;
-  p.chunks = bwd_chunks(n.rows);
-  p.rows_per_chunk = (n.rows + p.chunks - 1) / p.chunks;
   p.pw = static_cast<float*>(workspace);
-  p.pb = p.pw ? p.pw + p.chunks * n.H : nullptr;
   const bool f32_params = n.param_dtype == MOE_ELEM_F32;
   switch (n.dtype) {
     case MOE_ELEM_F32: return run_backward<float, float>(p, st);
