@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -147,18 +148,15 @@ _SIGNATURES = {
                                          ctypes.POINTER(_HandleDev), _P, ctypes.c_size_t, ctypes.c_int64, _P],
     "moe_quantize_fp8_blocks": [_P, _I64, _I64, _I64, _P, _P, _P],
     "moe_quantize_nvfp4_rows": [_P, _I64, _I64, _P, _P, _P, _P],
-    "moe_layer_norm": [ctypes.POINTER(_Norm), ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _P, _P,
-                       ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _P, _P, _P],
+    # descriptors (moe_norm, moe_router, moe_w4, moe_rows) by address
+    "moe_layer_norm": [_P] * 10,
     "moe_layer_norm_workspace_size": [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
-    "moe_layer_norm_backward": [ctypes.POINTER(_Norm), ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _P, _P, _P,
-                                ctypes.POINTER(_Rows), ctypes.POINTER(_Rows), _P, _P, _P, ctypes.c_size_t, _P],
-    "moe_router_topk": [ctypes.POINTER(_Router), ctypes.POINTER(_Rows), _P, ctypes.c_int32, _P, _P, _P, _P],
-    "moe_router_topk_backward": [ctypes.POINTER(_Router), ctypes.POINTER(_Rows), ctypes.c_int32, _P, _P,
-                                 ctypes.POINTER(_Rows), _P],
-    "moe_w4_matvec": [ctypes.POINTER(_W4), _I64, ctypes.POINTER(_Rows), ctypes.c_int32, ctypes.POINTER(_Rows),
-                      ctypes.POINTER(_Rows), _P],
-    "moe_grouped_w4_matvec": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout),
-                              ctypes.POINTER(_W4), ctypes.POINTER(_Rows), ctypes.c_int32, ctypes.POINTER(_Rows), _P],
+    "moe_layer_norm_backward": [_P] * 11 + [ctypes.c_size_t, _P],
+    "moe_router_topk": [_P, _P, _P, ctypes.c_int32, _P, _P, _P, _P],
+    "moe_router_topk_backward": [_P, _P, ctypes.c_int32, _P, _P, _P, _P],
+    "moe_w4_matvec": [_P, _I64, _P, ctypes.c_int32, _P, _P, _P],
+    "moe_grouped_w4_matvec": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _P, _P,
+                              ctypes.c_int32, _P, _P],
     "moe_quantize_w4_rows": [_P, _I64, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P],
     "moe_ring_create": [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_P)],
     "moe_ring_acquire": [_P, _P, ctypes.POINTER(ctypes.c_int32)],
@@ -207,10 +205,11 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        # the handle of torch.cuda.current_stream() without building the stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # ------------------------------------------------------------ public types
@@ -472,28 +471,44 @@ def _elem(t: torch.Tensor) -> int:
     return _ELEM[t.dtype]
 
 
-def _rows(t: Optional[torch.Tensor], name: str, rows: int, cols: int, dtype: torch.dtype):
-    """A 2-D tensor with unit column stride as a moe_rows; rows may lie apart."""
-    if t is None:
-        return None
+# The descriptors of a call are packed into one buffer (moe_norm, moe_router or
+# moe_w4, then moe_rows after moe_rows) and passed by address: a few C structs
+# built one by one cost more time than a small kernel takes.
+_ROWS_BYTES = 16
+
+
+def _address(buf: bytearray) -> int:
+    return ctypes.addressof(ctypes.c_char.from_buffer(buf))
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype):
+    """Address and row stride of a 2-D tensor with unit column stride; its rows may lie apart."""
     if not t.is_cuda:
         raise ValueError(f"{name}: device tensor expected")
-    if tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name}: shape {(rows, cols)} expected, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
-    if cols > 1 and t.stride(1) != 1:
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
         raise ValueError(f"{name}: adjacent columns expected (stride(1) == 1)")
-    return ctypes.byref(_Rows(t.data_ptr(), t.stride(0) if rows > 1 else cols))
+    return t.data_ptr(), row if shape[0] > 1 else shape[1]
+
+
+_ABSENT = (0, 0)
 
 
 def _dense(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
-    """A contiguous tensor of this shape and type as a pointer."""
+    """Address of a contiguous tensor of this shape and type."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    if not t.is_cuda:
+        raise ValueError(f"{name}: device tensor expected")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor expected")
+    return t.data_ptr()
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -502,15 +517,15 @@ def _matrix(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _norm_desc(x: torch.Tensor, weight, bias, eps: float):
-    rows, H = _matrix(x, "x")
-    params = [p for p in (weight, bias) if p is not None]
-    pdtype = params[0].dtype if params else x.dtype
-    if any(p.dtype != pdtype for p in params):
-        raise ValueError("weight and bias: one dtype expected")
-    if pdtype not in (x.dtype, torch.float32):
-        raise ValueError(f"weight, bias: {x.dtype} or float32 expected, got {pdtype}")
-    return _Norm(rows, H, _elem(x), _ELEM[pdtype], eps), rows, H, pdtype
+def _param_dtype(x: torch.Tensor, weight, bias) -> torch.dtype:
+    dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
+    if dtype is not x.dtype and dtype is not torch.float32:
+        raise ValueError(f"weight, bias: {x.dtype} or float32 expected, got {dtype}")
+    return dtype
+
+
+_NORM_CALL = struct.Struct("=qqiif4x" + "qq" * 4)  # moe_norm, then four moe_rows
+_NORM_ROWS = 32
 
 
 def moe_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], eps: float,
@@ -518,13 +533,19 @@ def moe_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Option
                    mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None) -> None:
     """y = layer_norm(x + residual) * weight + bias per row of x [rows, H]; sum_out
     takes the residual sum, mean and rstd (float [rows]) what the backward reads."""
-    n, rows, H, pdtype = _norm_desc(x, weight, bias, eps)
-    _check(_lib.moe_layer_norm(ctypes.byref(n), _rows(x, "x", rows, H, x.dtype),
-                               _rows(residual, "residual", rows, H, x.dtype), _dense(weight, "weight", (H,), pdtype),
-                               _dense(bias, "bias", (H,), pdtype), _rows(y, "y", rows, H, x.dtype),
-                               _rows(sum_out, "sum_out", rows, H, x.dtype),
-                               _dense(mean, "mean", (rows,), torch.float32),
-                               _dense(rstd, "rstd", (rows,), torch.float32), _stream(stream)), "moe_layer_norm")
+    shape, dtype = _matrix(x, "x"), x.dtype
+    pdtype = _param_dtype(x, weight, bias)
+    buf = bytearray(_NORM_CALL.size)
+    _NORM_CALL.pack_into(buf, 0, *shape, _elem(x), _ELEM[pdtype], eps, *_rows(x, "x", shape, dtype),
+                         *(_ABSENT if residual is None else _rows(residual, "residual", shape, dtype)),
+                         *_rows(y, "y", shape, dtype),
+                         *(_ABSENT if sum_out is None else _rows(sum_out, "sum_out", shape, dtype)))
+    a = _address(buf)
+    r = a + _NORM_ROWS
+    _check(_lib.moe_layer_norm(a, r, r + _ROWS_BYTES, _dense(weight, "weight", shape[1:], pdtype),
+                               _dense(bias, "bias", shape[1:], pdtype), r + 2 * _ROWS_BYTES, r + 3 * _ROWS_BYTES,
+                               _dense(mean, "mean", shape[:1], torch.float32),
+                               _dense(rstd, "rstd", shape[:1], torch.float32), _stream(stream)), "moe_layer_norm")
 
 
 def moe_layer_norm_workspace_size(rows: int, H: int) -> int:
@@ -541,14 +562,23 @@ def moe_layer_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: Optio
     """Gradients of moe_layer_norm; h is the normalised row matrix (x, or sum_out
     where there was a residual) and grad_sum the gradient that reaches it past
     the norm.  workspace is needed for grad_weight / grad_bias (float [H])."""
-    n, rows, H, pdtype = _norm_desc(h, weight, None, 0.0)
-    f32 = torch.float32
+    shape, dtype, f32 = _matrix(h, "h"), h.dtype, torch.float32
+    pdtype = _param_dtype(h, weight, None)
+    buf = bytearray(_NORM_CALL.size)
+    _NORM_CALL.pack_into(buf, 0, *shape, _elem(h), _ELEM[pdtype], 0.0, *_rows(grad_y, "grad_y", shape, dtype),
+                         *_rows(h, "h", shape, dtype),
+                         *(_ABSENT if grad_sum is None else _rows(grad_sum, "grad_sum", shape, dtype)),
+                         *_rows(grad_x, "grad_x", shape, dtype))
+    a = _address(buf)
+    r = a + _NORM_ROWS
+    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace: contiguous device tensor expected")
     _check(_lib.moe_layer_norm_backward(
-        ctypes.byref(n), _rows(grad_y, "grad_y", rows, H, h.dtype), _rows(h, "h", rows, H, h.dtype),
-        _dense(weight, "weight", (H,), pdtype), _dense(mean, "mean", (rows,), f32), _dense(rstd, "rstd", (rows,), f32),
-        _rows(grad_sum, "grad_sum", rows, H, h.dtype), _rows(grad_x, "grad_x", rows, H, h.dtype),
-        _dense(grad_weight, "grad_weight", (H,), f32), _dense(grad_bias, "grad_bias", (H,), f32), _ptr(workspace),
-        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)),
+        a, r, r + _ROWS_BYTES, _dense(weight, "weight", shape[1:], pdtype), _dense(mean, "mean", shape[:1], f32),
+        _dense(rstd, "rstd", shape[:1], f32), r + 2 * _ROWS_BYTES, r + 3 * _ROWS_BYTES,
+        _dense(grad_weight, "grad_weight", shape[1:], f32), _dense(grad_bias, "grad_bias", shape[1:], f32),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
         "moe_layer_norm_backward")
 
 
@@ -563,20 +593,29 @@ class Router:
     renormalize: bool = True
     scale: float = 1.0
 
-    def c(self, T: int, dtype: int):
-        return _Router(T, self.E, self.K, dtype, self.score, 1 if self.renormalize else 0, self.scale)
-
     def map_shape(self, fmt: int, T: int):
         return (T, self.E) if fmt == ROUTING_SPARSE_BOOL else (T, self.K)
 
 
 _MAP_DTYPE = {ROUTING_DENSE_I16: torch.int16, ROUTING_SPARSE_BOOL: torch.uint8}
+_ROUTER_CALL = struct.Struct("=qqqiiif" + "qq" * 2)  # moe_router, then two moe_rows
+_ROUTER_ROWS = 40
 
 
-def _map(routing: Routing, router: Router, T: int):
+def _router_call(router: Router, logits: torch.Tensor, routing: Routing, grad_logits: Optional[torch.Tensor]):
+    """(buffer, its address, address of the map, shape of the map)"""
+    shape = _matrix(logits, "logits")
+    if shape[1] != router.E:
+        raise ValueError(f"logits: {router.E} columns expected, got {shape[1]}")
     if routing.format not in _MAP_DTYPE:
         raise ValueError("unknown routing format")
-    return _dense(routing.map, "routing.map", router.map_shape(routing.format, T), _MAP_DTYPE[routing.format])
+    buf = bytearray(_ROUTER_CALL.size)
+    _ROUTER_CALL.pack_into(buf, 0, shape[0], router.E, router.K, _elem(logits), router.score,
+                           1 if router.renormalize else 0, router.scale, *_rows(logits, "logits", shape, logits.dtype),
+                           *(_ABSENT if grad_logits is None else
+                             _rows(grad_logits, "grad_logits", shape, logits.dtype)))
+    map_shape = router.map_shape(routing.format, shape[0])
+    return buf, _address(buf), _dense(routing.map, "routing.map", map_shape, _MAP_DTYPE[routing.format]), map_shape
 
 
 def moe_router_topk(router: Router, logits: torch.Tensor, routing: Routing,
@@ -584,24 +623,19 @@ def moe_router_topk(router: Router, logits: torch.Tensor, routing: Routing,
                     stream=None) -> None:
     """Writes routing.map and routing.probs (both required) from logits [T, E];
     status (int32 [1], optional) collects DEV_ERR_NAN_LOGIT."""
-    T, _ = _matrix(logits, "logits")
-    probs = _dense(routing.probs, "routing.probs", router.map_shape(routing.format, T), torch.float32)
-    _check(_lib.moe_router_topk(ctypes.byref(router.c(T, _elem(logits))),
-                                _rows(logits, "logits", T, router.E, logits.dtype),
-                                _dense(select_bias, "select_bias", (router.E,), torch.float32), routing.format,
-                                _map(routing, router, T), probs, _dense(status, "status", (1,), torch.int32),
-                                _stream(stream)), "moe_router_topk")
+    buf, a, map_, map_shape = _router_call(router, logits, routing, None)
+    _check(_lib.moe_router_topk(a, a + _ROUTER_ROWS, _dense(select_bias, "select_bias", (router.E,), torch.float32),
+                                routing.format, map_, _dense(routing.probs, "routing.probs", map_shape, torch.float32),
+                                _dense(status, "status", (1,), torch.int32), _stream(stream)), "moe_router_topk")
 
 
 def moe_router_topk_backward(router: Router, logits: torch.Tensor, routing: Routing, grad_probs: torch.Tensor,
                              grad_logits: torch.Tensor, stream=None) -> None:
     """grad_logits [T, E] from grad_probs in the layout of routing.map."""
-    T, _ = _matrix(logits, "logits")
-    _check(_lib.moe_router_topk_backward(
-        ctypes.byref(router.c(T, _elem(logits))), _rows(logits, "logits", T, router.E, logits.dtype), routing.format,
-        _map(routing, router, T),
-        _dense(grad_probs, "grad_probs", router.map_shape(routing.format, T), torch.float32),
-        _rows(grad_logits, "grad_logits", T, router.E, logits.dtype), _stream(stream)), "moe_router_topk_backward")
+    buf, a, map_, map_shape = _router_call(router, logits, routing, grad_logits)
+    _check(_lib.moe_router_topk_backward(a, a + _ROUTER_ROWS, routing.format, map_,
+                                         _dense(grad_probs, "grad_probs", map_shape, torch.float32),
+                                         a + _ROUTER_ROWS + _ROWS_BYTES, _stream(stream)), "moe_router_topk_backward")
 
 
 @dataclasses.dataclass
@@ -614,37 +648,48 @@ class W4Weight:
     zeros: Optional[torch.Tensor]
     group: int
 
-    def c(self, lead=()):
-        if self.codes.dim() != len(lead) + 2 or self.group < 1:
-            raise ValueError(f"codes: {len(lead) + 2}-D tensor expected, got {tuple(self.codes.shape)}")
-        N, Kd = self.codes.shape[-2], self.codes.shape[-1] * 2
-        G = (Kd + self.group - 1) // self.group
-        return _W4(N, Kd, self.group, _elem(self.scales),
-                   _dense(self.codes, "codes", (*lead, N, Kd // 2), torch.uint8),
-                   _dense(self.scales, "scales", (*lead, N, G), self.scales.dtype),
-                   _dense(self.zeros, "zeros", (*lead, N, (G + 1) // 2), torch.uint8)), N, Kd
+
+_W4_CALL = struct.Struct("=qqiiQQQ" + "qq" * 3)  # moe_w4, then three moe_rows
+_W4_ROWS = 48
+
+
+def _w4_call(weight: W4Weight, lead: tuple, x: torch.Tensor, y: torch.Tensor, activation: int,
+             addend: Optional[torch.Tensor], rows: int):
+    """(buffer, its address): the weight, x, addend, y"""
+    shape, dtype = weight.codes.shape, weight.scales.dtype
+    if len(shape) != len(lead) + 2 or weight.group < 1:
+        raise ValueError(f"codes: {len(lead) + 2}-D tensor expected, got {tuple(shape)}")
+    N, Kd = shape[-2], shape[-1] * 2
+    G = -(-Kd // weight.group)
+    y_shape = (rows, N // 2 if activation == W4_SWIGLU else N)
+    buf = bytearray(_W4_CALL.size)
+    _W4_CALL.pack_into(buf, 0, N, Kd, weight.group, _elem(weight.scales),
+                       _dense(weight.codes, "codes", (*lead, N, shape[-1]), torch.uint8),
+                       _dense(weight.scales, "scales", (*lead, N, G), dtype),
+                       _dense(weight.zeros, "zeros", (*lead, N, (G + 1) // 2), torch.uint8) or 0,
+                       *_rows(x, "x", (rows, Kd), dtype),
+                       *(_ABSENT if addend is None else _rows(addend, "addend", y_shape, dtype)),
+                       *_rows(y, "y", y_shape, dtype))
+    return buf, _address(buf)
 
 
 def moe_w4_matvec(weight: W4Weight, x: torch.Tensor, y: torch.Tensor, activation: int = W4_NONE,
                   addend: Optional[torch.Tensor] = None, stream=None) -> None:
     """y [M, N or N/2] = act(x [M, Kd] . W^T) (+ addend)."""
-    w, N, Kd = weight.c()
-    M, _ = _matrix(x, "x")
-    dt, n_out = weight.scales.dtype, N // 2 if activation == W4_SWIGLU else N
-    _check(_lib.moe_w4_matvec(ctypes.byref(w), M, _rows(x, "x", M, Kd, dt), activation,
-                              _rows(addend, "addend", M, n_out, dt), _rows(y, "y", M, n_out, dt), _stream(stream)),
+    M = _matrix(x, "x")[0]
+    buf, a = _w4_call(weight, (), x, y, activation, addend, M)
+    r = a + _W4_ROWS
+    _check(_lib.moe_w4_matvec(a, M, r, activation, r + _ROWS_BYTES, r + 2 * _ROWS_BYTES, _stream(stream)),
            "moe_w4_matvec")
 
 
 def moe_grouped_w4_matvec(handle: Handle, shape: Shape, layout: Layout, weight: W4Weight, x: torch.Tensor,
                           y: torch.Tensor, activation: int = W4_NONE, stream=None) -> None:
     """moe_w4_matvec of every dispatched row x [cap, Kd] with its expert's matrix, into y [cap, N or N/2]."""
-    w, N, Kd = weight.c((shape.E,))
-    dt, n_out = weight.scales.dtype, N // 2 if activation == W4_SWIGLU else N
-    _check(_lib.moe_grouped_w4_matvec(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()),
-                                      ctypes.byref(w), _rows(x, "x", layout.capacity, Kd, dt), activation,
-                                      _rows(y, "y", layout.capacity, n_out, dt), _stream(stream)),
-           "moe_grouped_w4_matvec")
+    buf, a = _w4_call(weight, (shape.E,), x, y, activation, None, layout.capacity)
+    r = a + _W4_ROWS
+    _check(_lib.moe_grouped_w4_matvec(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), a, r,
+                                      activation, r + 2 * _ROWS_BYTES, _stream(stream)), "moe_grouped_w4_matvec")
 
 
 def moe_quantize_w4_rows(w: torch.Tensor, group: int, codes: torch.Tensor, scales: torch.Tensor,
