@@ -444,6 +444,8 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
           for (int q = 0; q < 4; q++) {
             s[q] = scale_bits<T>(*reinterpret_cast<const uint16_t*>(slot + scale_to[q >> 1] +
                                                                     (q & 1) * 8 * P::kScalePitch + g * 2));
+            // a group past the end: its place in the slot was not filled
+            if (!ALIGNED && U > 1 && step * U + u >= (int)G) s[q] = 0.0f;
             z[q] = 8.0f;
           }
           if (p.zeros)

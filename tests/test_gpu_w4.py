@@ -66,6 +66,22 @@ def test_every_code_and_zero_point_is_exact(dtype, group):
     assert torch.equal(bu.f64(y), bu.w4_dequant(codes, scales, None, group).T)
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 13, 30])
+def test_nothing_is_left_from_an_earlier_call(M, group):
+    """A product whose last group and last rows are short, right after one that filled the GPU's shared memory with
+    NaN scales and NaN tokens."""
+    moe = moe_mod()
+    codes, scales, zeros = bu.w4_random(8192, 4096, group, HF, True, seed=1)
+    dirty = (codes | 0xFF, torch.full_like(scales, float("nan")), zeros)
+    w = bu.w4_random(99, 8224, group, HF, True, seed=2)
+    x = bu.randn(M, 8224, seed=3, dtype=HF)
+    ref, tol = bu.w4_product(x, bu.w4_dequant(*w, group), group, dtype=HF)
+    for _ in range(3):
+        assert bool(torch.isnan(product(moe, torch.full((M, 4096), float("nan"), dtype=HF), dirty, group=group)).all())
+        bu.assert_within(product(moe, x, w, group=group), ref, tol)
+
+
 @pytest.mark.parametrize("M", [1, 4, 11, 20])
 def test_strided_rows_and_addend_in_place(M):
     moe = moe_mod()
