@@ -1,13 +1,15 @@
 // router.cu -- top-k router of the MoE layer (logits -> routing map and
 // probabilities) and the gradient of its logits.
 //
-// One warp per token; lane l holds experts l, l + 32, ... in registers.  The
-// selection finds the K-th largest score exactly: scores become unsigned keys
-// of the same order, and the threshold is built bit by bit from the count of
-// keys at or above a candidate.  Everything above it is chosen, and the lowest
-// experts among those equal to it fill the rest, so ties, masked experts and
-// rows with fewer than K experts left need no case of their own, and ids come
-// out ascending.  Scores and sums are fp32 in a fixed order.
+// A group of L lanes takes a token, V neighbouring experts a lane (E <= V L), so
+// that a warp works on 32 / L tokens at once.  The selection looks for a
+// threshold that exactly K scores reach: it shrinks an interval by the counts
+// at its ends, reading the scores' order from the scores themselves, and stops at
+// the first count that is K, after four or five steps on spread scores.  Where
+// scores are equal no threshold has that count; the interval then closes on one
+// value by bisection of its bit pattern, everything above it is chosen and the
+// lowest experts among those equal to it fill the rest.  Ids come out ascending.
+// Scores and sums are fp32 in a fixed order.
 #include "block_common.cuh"
 #include "moe_internal.h"
 
@@ -23,6 +25,7 @@ struct RouterParams {
   int64_t T, stride;
   int E, K;
   int score, renorm, format;
+  bool vector_in, vector_out;  // rows of logits / of a sparse map are whole aligned vectors
   float scale;
   const void* logits;
   const float* bias;
@@ -31,12 +34,12 @@ struct RouterParams {
   int32_t* status;
 };
 
-// Unsigned key in the order of the floats (+0 and -0 equal); 0 for -inf and NaN.
-MOE_DEVICE uint32_t score_key(float v) {
-  if (!(v > -INFINITY)) return 0;
-  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 -> +0
+// Unsigned key in the order of the floats, and the float of a key.
+MOE_DEVICE uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+MOE_DEVICE float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 // exp(l - top), with the limit 1 where l is top (both may be +inf).
 MOE_DEVICE float exp_below(float l, float top) { return l == top ? 1.0f : expf(l - top); }
@@ -54,100 +57,254 @@ MOE_DEVICE float sigmoid_rest(float l) {
   return z / (1.0f + z);
 }
 
-template <typename T, int V>  // V values a lane: E <= 32 V
+// Over the L lanes of a group.
+template <int L>
+MOE_DEVICE int group_add(int v) {
+  if (L == 32) return __reduce_add_sync(kAll, v);
+#pragma unroll
+  for (int d = L / 2; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+template <int L>
+MOE_DEVICE float group_add(float v) {
+#pragma unroll
+  for (int d = L / 2; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+template <int L>
+MOE_DEVICE float group_max(float v) {
+#pragma unroll
+  for (int d = L / 2; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+// Sum over the lanes of the group below this one.
+template <int L>
+MOE_DEVICE int group_below(int v) {
+  const int lane = threadIdx.x % L;
+  int s = v;
+#pragma unroll
+  for (int d = 1; d < L; d <<= 1) {
+    const int up = __shfl_up_sync(kAll, s, d, L);
+    if (lane >= d) s += up;
+  }
+  return s - v;
+}
+
+// V neighbouring values of a row from e0, -inf past its end.
+template <typename T, int V>
+MOE_DEVICE void load_scores(float (&l)[V], const T* row, int e0, int E, bool vector) {
+  constexpr int N = 16 / sizeof(T);
+  if (vector) {
+#pragma unroll
+    for (int j = 0; j < V; j += N) {
+      union {
+        uint4 v;
+        T e[N];
+      } u;
+      if (e0 + j < E) u.v = *reinterpret_cast<const uint4*>(row + e0 + j);
+#pragma unroll
+      for (int i = 0; i < N; i++) l[j + i] = e0 + j < E ? to_float(u.e[i]) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j++) l[j] = e0 + j < E ? to_float(row[e0 + j]) : -INFINITY;
+  }
+}
+
+template <int V>
+MOE_DEVICE int count_from(const float (&s)[V], float v) {
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < V; j++) n += s[j] >= v;
+  return n;
+}
+
+// Bit j: expert e0 + j is chosen.  `live` scores are above -inf, at least one;
+// `top` is the largest.
+template <int V, int L>
+MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float top) {
+  float low = INFINITY;
+#pragma unroll
+  for (int j = 0; j < V; j++)
+    if (s[j] > -INFINITY) low = fminf(low, s[j]);
+  low = -group_max<L>(-low);
+  // counts: n_lo >= K scores reach lo, n_hi < K reach hi; the choice is exact once a count is K
+  float lo = low, hi = top;
+  int n_lo = live, n_hi = group_add<L>(count_from<V>(s, top));
+  bool exact = live <= K, found = exact || n_hi >= K;
+  if (!exact && n_hi >= K) lo = top, n_lo = n_hi, exact = n_hi == K;
+  for (int it = 0; it < 12; it++) {
+    if (__all_sync(kAll, found)) break;
+    float part = ((float)(K - n_hi) + 0.5f) / (float)(n_lo - n_hi + 1);
+    part = fminf(fmaxf(part, 0.0625f), 0.9375f);
+    const float mid = hi - (hi - lo) * part;
+    const int n = group_add<L>(count_from<V>(s, mid));
+    if (found || !(mid > lo && mid < hi)) continue;
+    if (n >= K)
+      lo = mid, n_lo = n, exact = found = n == K;
+    else
+      hi = mid, n_hi = n;
+  }
+  if (!__all_sync(kAll, found)) {  // equal, infinite or very uneven scores
+    uint32_t klo = key_of(lo), khi = key_of(hi);
+    if (found) khi = klo + 1;
+    while (__any_sync(kAll, khi - klo > 1)) {
+      const uint32_t kmid = klo + (khi - klo) / 2;
+      const int n = group_add<L>(count_from<V>(s, of_key(kmid)));
+      if (khi - klo <= 1) continue;
+      if (n >= K)
+        klo = kmid, n_lo = n;
+      else
+        khi = kmid;
+    }
+    if (!found) lo = of_key(klo), exact = n_lo == K;
+  }
+  uint32_t on = 0;
+#pragma unroll
+  for (int j = 0; j < V; j++) on |= (uint32_t)(s[j] >= lo) << j;
+  if (!__all_sync(kAll, exact)) {
+    uint32_t above = 0;
+#pragma unroll
+    for (int j = 0; j < V; j++) above |= (uint32_t)(s[j] > lo) << j;
+    uint32_t equal = on & ~above;
+    int room = K - group_add<L>(__popc(above)) - group_below<L>(__popc(equal));
+    if (!exact) {
+      for (; equal && room > 0; room--) {
+        above |= equal & -equal;
+        equal &= equal - 1;
+      }
+      on = above;
+    }
+  }
+  // the interval may start at the lowest live score, masked ones are below it
+  return on;
+}
+
+template <typename T, int V, int L>
 __global__ void __launch_bounds__(kThreads) router_topk_kernel(RouterParams p) {
-  const int lane = threadIdx.x & 31;
-  const unsigned below = lanemask_lt();
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < p.T; t += (int64_t)gridDim.x * kWarps) {
-    const T* row = static_cast<const T*>(p.logits) + t * p.stride;
-    float l[V];
-    uint32_t key[V];
+  constexpr int kTokens = 32 / L;               // tokens of a warp
+  constexpr int kChosen = V * L < 128 ? V * L : 128;  // K at the most
+  __shared__ float logit_of[kWarps][kTokens][kChosen];
+  __shared__ int16_t id_of[kWarps][kTokens][kChosen];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = lane % L, e0 = at * V;
+  float* chosen_logit = logit_of[warp][lane / L];
+  int16_t* chosen_id = id_of[warp][lane / L];
+  const bool softmax = p.score == MOE_SCORE_SOFTMAX, divide = softmax || p.renorm;
+
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; t0 < p.T;
+       t0 += (int64_t)gridDim.x * kWarps * kTokens) {
+    const int64_t t = t0 + lane / L;
+    const bool real = t < p.T;
+    const T* row = static_cast<const T*>(p.logits) + (real ? t : t0) * p.stride;
+    float s[V];
+    load_scores<T, V>(s, row, e0, p.E, p.vector_in);
     bool bad = false;
+    int live = 0;
+    float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      const int e = j * 32 + lane;
-      l[j] = e < p.E ? to_float(row[e]) : -INFINITY;
-      bad |= l[j] != l[j];
-      if (l[j] != l[j]) l[j] = -INFINITY;
-      float s = l[j];
-      if (p.bias && e < p.E && s > -INFINITY) {
-        s = (p.score == MOE_SCORE_SIGMOID ? sigmoid_scaled(s, 0.0f) : s) + p.bias[e];
-        bad |= s != s;
-        if (!(s > -INFINITY)) l[j] = -INFINITY;
+      bad |= s[j] != s[j];
+      if (p.bias && s[j] > -INFINITY) {  // (false past the end of the row)
+        s[j] = (softmax ? s[j] : sigmoid_scaled(s[j], 0.0f)) + p.bias[e0 + j];
+        bad |= s[j] != s[j];
       }
-      key[j] = score_key(s);
+      if (!(s[j] > -INFINITY)) s[j] = -INFINITY;
+      live += s[j] > -INFINITY;
+      top = fmaxf(top, s[j]);
     }
     if (bad && p.status) atomicOr(p.status, MOE_DEV_ERR_NAN_LOGIT);
-
-    // the K-th largest key (0 when fewer than K experts are left)
-    uint32_t thr = 0;
-    for (int b = 31; b >= 0; b--) {
-      const uint32_t cand = thr | (1u << b);
-      int n = 0;
+    live = group_add<L>(live);
+    top = group_max<L>(top);
+    uint32_t on = select_top<V, L>(s, p.K, live, top);
+    uint32_t alive = 0;
 #pragma unroll
-      for (int j = 0; j < V; j++) n += key[j] >= cand;
-      if (__reduce_add_sync(kAll, n) >= p.K) thr = cand;
+    for (int j = 0; j < V; j++) alive |= (uint32_t)(s[j] > -INFINITY) << j;
+    on &= alive;
+
+    // logits again where the scores are not
+    if (p.bias) {
+      load_scores<T, V>(s, row, e0, p.E, p.vector_in);
+      top = -INFINITY;  // of the logits that take part
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        if (!(alive >> j & 1)) s[j] = -INFINITY;
+        if ((on >> j & 1) || !p.renorm) top = fmaxf(top, s[j]);
+      }
+      top = group_max<L>(top);
     }
-    int above = 0;
-#pragma unroll
-    for (int j = 0; j < V; j++) above += key[j] > thr;
-    int ties = thr ? p.K - (int)__reduce_add_sync(kAll, above) : 0;
+    const float m = p.renorm ? fminf(top, 0.0f) : 0.0f;
+    auto weight = [&](float l) { return softmax ? exp_below(l, top) : sigmoid_scaled(l, m); };
 
-    // chosen experts in ascending order, and the largest logit among them
-    unsigned chosen[V];
-    float top = -INFINITY, top_all = -INFINITY;
+    float z = 0.0f;
+    if (softmax && !p.renorm) {  // every live expert takes part in the sum
+#pragma unroll
+      for (int j = 0; j < V; j++)
+        if (s[j] > -INFINITY) z += exp_below(s[j], top);
+      z = group_add<L>(z);
+    }
+    // the chosen in ascending order through shared memory, L at a time
+    const int first = group_below<L>(__popc(on)), count = group_add<L>(__popc(on));
+    int slot = first;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      const bool eq = thr && key[j] == thr;
-      const unsigned eqs = __ballot_sync(kAll, eq);
-      const bool on = key[j] > thr || (eq && __popc(eqs & below) < ties);
-      ties -= min(ties, __popc(eqs));
-      chosen[j] = __ballot_sync(kAll, on);
-      if (on) top = fmaxf(top, l[j]);
-      top_all = fmaxf(top_all, l[j]);
-    }
-    top = warp_max(top);
-    top_all = warp_max(top_all);
-
-    const float m = fminf(top, 0.0f);
-    float z = 0.0f, w[V];
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-      const bool on = chosen[j] >> lane & 1;
-      if (p.score == MOE_SCORE_SOFTMAX) {
-        w[j] = l[j] > -INFINITY ? exp_below(l[j], p.renorm ? top : top_all) : 0.0f;
-        z += on || !p.renorm ? w[j] : 0.0f;
-      } else {
-        w[j] = on ? sigmoid_scaled(l[j], p.renorm ? m : 0.0f) : 0.0f;
-        z += w[j];
+      if (on >> j & 1) {
+        chosen_logit[slot] = s[j];
+        chosen_id[slot] = (int16_t)(e0 + j);
+        slot++;
       }
     }
-    z = warp_sum(z);
-    const bool divide = p.score == MOE_SCORE_SOFTMAX || p.renorm;
-    int slot = 0;
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-      const bool on = chosen[j] >> lane & 1;
-      const int e = j * 32 + lane;
-      const float v = p.scale * (divide ? w[j] / z : w[j]);
-      if (p.format == MOE_ROUTING_DENSE_I16) {
-        if (on) {
-          const int64_t k = t * p.K + slot + __popc(chosen[j] & below);
-          static_cast<int16_t*>(p.map)[k] = (int16_t)e;
-          p.probs[k] = v;
-        }
-        slot += __popc(chosen[j]);
-      } else if (e < p.E) {
-        static_cast<uint8_t*>(p.map)[t * p.E + e] = on;
-        p.probs[t * p.E + e] = on ? v : 0.0f;
-      }
+    __syncwarp();
+    for (int k = at; k < count; k += L) {
+      const float w = weight(chosen_logit[k]);
+      chosen_logit[k] = w;
+      if (p.renorm) z += w;
     }
+    if (p.renorm) z = group_add<L>(z);
+    const float f = divide ? p.scale / z : p.scale;  // (z is 0 where nothing is chosen)
+    __syncwarp();
     if (p.format == MOE_ROUTING_DENSE_I16) {
-      for (int k = slot + lane; k < p.K; k += 32) {
-        static_cast<int16_t*>(p.map)[t * p.K + k] = -1;
-        p.probs[t * p.K + k] = 0.0f;
+      if (real) {
+        for (int k = at; k < p.K; k += L) {
+          const bool in = k < count;
+          static_cast<int16_t*>(p.map)[t * p.K + k] = in ? chosen_id[k] : (int16_t)-1;
+          p.probs[t * p.K + k] = in ? chosen_logit[k] * f : 0.0f;
+        }
+      }
+    } else {
+      slot = first;
+#pragma unroll
+      for (int j = 0; j < V; j++) s[j] = on >> j & 1 ? chosen_logit[slot++] * f : 0.0f;
+      if (real) {
+        uint8_t* map = static_cast<uint8_t*>(p.map) + t * p.E;
+        float* probs = p.probs + t * p.E;
+        if (p.vector_out) {
+#pragma unroll
+          for (int j = 0; j < V; j += 8) {
+            if (e0 + j >= p.E) continue;
+            uint2 b = make_uint2(0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              b.x |= (on >> (j + i) & 1) << (8 * i);
+              b.y |= (on >> (j + 4 + i) & 1) << (8 * i);
+            }
+            *reinterpret_cast<uint2*>(map + e0 + j) = b;
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+              *reinterpret_cast<float4*>(probs + e0 + j + i) =
+                  make_float4(s[j + i], s[j + i + 1], s[j + i + 2], s[j + i + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; j++) {
+            if (e0 + j >= p.E) continue;
+            map[e0 + j] = on >> j & 1;
+            probs[e0 + j] = s[j];
+          }
+        }
       }
     }
+    __syncwarp();  // before the next token's chosen
   }
 }
 
@@ -155,130 +312,189 @@ struct RouterBwdParams {
   int64_t T, stride, gstride;
   int E, K;
   int score, renorm, format;
+  bool vector_in, vector_out, vector_map;
   float scale;
   const void *logits, *map;
   const float* gp;
   void* gl;
 };
 
-template <typename T, int V>
+// Marks an expert without a gradient in a staged row (a NaN no computation makes).
+constexpr uint32_t kNoGradient = 0xffa5c3e7u;
+
+template <typename T, int V, int L>
 __global__ void __launch_bounds__(kThreads) router_bwd_kernel(RouterBwdParams p) {
-  extern __shared__ float smem[];  // dense maps: a row of gradients and one of marks per warp
+  constexpr int kTokens = 32 / L, N = 16 / sizeof(T);
+  __shared__ uint4 staged[kWarps][kTokens * V * L / 4];  // dense maps: gradients by expert
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* grow = smem + warp * 2 * p.E;
-  float* mark = grow + p.E;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += (int64_t)gridDim.x * kWarps) {
-    const T* row = static_cast<const T*>(p.logits) + t * p.stride;
+  const int at = lane % L, e0 = at * V;
+  uint4* mine = staged[warp] + lane * (V / 4);  // this lane's experts
+  uint32_t* grow = reinterpret_cast<uint32_t*>(staged[warp] + lane / L * L * (V / 4));
+  const bool softmax = p.score == MOE_SCORE_SOFTMAX;
+
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; t0 < p.T;
+       t0 += (int64_t)gridDim.x * kWarps * kTokens) {
+    const int64_t t = t0 + lane / L;
+    const bool real = t < p.T;
+    const T* row = static_cast<const T*>(p.logits) + (real ? t : t0) * p.stride;
+    float l[V], g[V];
+    load_scores<T, V>(l, row, e0, p.E, p.vector_in);
+    uint32_t on = 0;
     if (p.format == MOE_ROUTING_DENSE_I16) {
-      for (int e = lane; e < p.E; e += 32) mark[e] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V / 4; j++) mine[j] = make_uint4(kNoGradient, kNoGradient, kNoGradient, kNoGradient);
       __syncwarp();
-      for (int k = lane; k < p.K; k += 32) {
-        const int e = static_cast<const int16_t*>(p.map)[t * p.K + k];
-        if (e >= 0 && e < p.E) {
-          grow[e] = p.gp[t * p.K + k];
-          mark[e] = 1.0f;
+      if (real) {
+        for (int k = at; k < p.K; k += L) {
+          const int e = static_cast<const int16_t*>(p.map)[t * p.K + k];
+          const float v = p.gp[t * p.K + k];
+          if (e >= 0 && e < p.E) grow[e] = __float_as_uint(v);
         }
       }
       __syncwarp();
+#pragma unroll
+      for (int j = 0; j < V / 4; j++) {
+        const uint4 v = mine[j];
+        const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          on |= (uint32_t)(b[i] != kNoGradient) << (4 * j + i);
+          g[4 * j + i] = __uint_as_float(b[i]);
+        }
+      }
+      __syncwarp();
+    } else {
+      const uint8_t* map = static_cast<const uint8_t*>(p.map) + (real ? t : t0) * p.E;
+      const float* gp = p.gp + (real ? t : t0) * p.E;
+      if (p.vector_map) {
+#pragma unroll
+        for (int j = 0; j < V; j += 8) {
+          if (e0 + j >= p.E) continue;
+          const uint2 b = *reinterpret_cast<const uint2*>(map + e0 + j);
+#pragma unroll
+          for (int i = 0; i < 8; i++) on |= (uint32_t)(((i < 4 ? b.x : b.y) >> (8 * (i & 3)) & 0xffu) != 0) << (j + i);
+#pragma unroll
+          for (int i = 0; i < 8; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(gp + e0 + j + i);
+            g[j + i] = v.x, g[j + i + 1] = v.y, g[j + i + 2] = v.z, g[j + i + 3] = v.w;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+          if (e0 + j >= p.E) continue;
+          on |= (uint32_t)(map[e0 + j] != 0) << j;
+          g[j] = gp[e0 + j];
+        }
+      }
     }
-    float l[V], g[V];
-    unsigned on = 0;
-    float top = -INFINITY, top_on = -INFINITY;
+    float top = -INFINITY;  // of the logits that take part
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      const int e = j * 32 + lane;
-      l[j] = e < p.E ? to_float(row[e]) : -INFINITY;
-      if (l[j] != l[j]) l[j] = -INFINITY;
-      bool c = false;
-      if (e < p.E)
-        c = p.format == MOE_ROUTING_DENSE_I16 ? mark[e] != 0.0f
-                                              : static_cast<const uint8_t*>(p.map)[t * p.E + e] != 0;
-      c = c && l[j] > -INFINITY;  // a masked expert has no gradient
-      g[j] = 0.0f;
-      if (c) g[j] = p.format == MOE_ROUTING_DENSE_I16 ? grow[e] : p.gp[t * p.E + e];
-      on |= (unsigned)c << j;
-      top = fmaxf(top, l[j]);
-      if (c) top_on = fmaxf(top_on, l[j]);
+      if (!(l[j] > -INFINITY)) {  // masked, NaN, or past the end of the row: no gradient
+        l[j] = -INFINITY;
+        on &= ~(1u << j);
+      }
+      if (!(on >> j & 1)) g[j] = 0.0f;
+      if ((on >> j & 1) || (softmax && !p.renorm)) top = fmaxf(top, l[j]);
     }
-    top = warp_max(top);
-    top_on = warp_max(top_on);
+    top = group_max<L>(top);
+    const float m = p.renorm ? fminf(top, 0.0f) : 0.0f;
     // n: the score each expert takes part with; z its sum; dot = sum of g n
     float n[V], z = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; j++) {
       const bool c = on >> j & 1;
-      if (p.score == MOE_SCORE_SOFTMAX)
-        n[j] = (c || !p.renorm) && l[j] > -INFINITY ? exp_below(l[j], p.renorm ? top_on : top) : 0.0f;
-      else
-        n[j] = c ? sigmoid_scaled(l[j], p.renorm ? fminf(top_on, 0.0f) : 0.0f) : 0.0f;
+      n[j] = 0.0f;
+      if (softmax) {
+        if ((c || !p.renorm) && l[j] > -INFINITY) n[j] = exp_below(l[j], top);
+      } else if (c) {
+        n[j] = sigmoid_scaled(l[j], m);
+      }
       z += n[j];
       dot = fmaf(g[j], n[j], dot);
     }
-    const bool divide = p.score == MOE_SCORE_SOFTMAX || p.renorm;
     float inv = 1.0f;
-    if (divide) {
-      z = warp_sum(z);
-      dot = warp_sum(dot);
+    if (softmax || p.renorm) {
+      z = group_add<L>(z);
+      dot = group_add<L>(dot);
       inv = z > 0.0f ? 1.0f / z : 0.0f;
       dot *= inv;
     } else {
       dot = 0.0f;
     }
-    T* out = static_cast<T*>(p.gl) + t * p.gstride;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      const int e = j * 32 + lane;
       float v = 0.0f;
       if (n[j] != 0.0f) {
         v = p.scale * (n[j] * inv) * (g[j] - dot);
-        if (p.score == MOE_SCORE_SIGMOID) v *= sigmoid_rest(l[j]);
+        if (!softmax) v *= sigmoid_rest(l[j]);
       }
-      if (e < p.E) out[e] = from_float<T>(v);
+      g[j] = v;
     }
-    __syncwarp();
+    if (!real) continue;
+    T* out = static_cast<T*>(p.gl) + t * p.gstride + e0;
+    if (p.vector_out) {
+#pragma unroll
+      for (int j = 0; j < V; j += N) {
+        union {
+          uint4 v;
+          T e[N];
+        } u;
+#pragma unroll
+        for (int i = 0; i < N; i++) u.e[i] = from_float<T>(g[j + i]);
+        if (e0 + j < p.E) *reinterpret_cast<uint4*>(out + j) = u.v;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j++)
+        if (e0 + j < p.E) out[j] = from_float<T>(g[j]);
+    }
   }
 }
 
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <int L>
 unsigned token_grid(int64_t T) {
-  const int64_t blocks = (T + kWarps - 1) / kWarps, cap = (int64_t)device_sm_count() * (2048 / kThreads);
+  const int64_t per_block = kWarps * (32 / L);
+  const int64_t blocks = (T + per_block - 1) / per_block, cap = (int64_t)device_sm_count() * (2048 / kThreads);
   return (unsigned)(blocks < cap ? blocks : cap);
 }
 
+// Eight experts a lane and as few lanes a token as hold them, up to a warp; more
+// experts a lane beyond 256.
+#define MOE_ROUTER_SHAPE(RUN)         \
+  do {                                \
+    if (p.E <= 8) RUN(8, 1);          \
+    else if (p.E <= 16) RUN(8, 2);    \
+    else if (p.E <= 32) RUN(8, 4);    \
+    else if (p.E <= 64) RUN(8, 8);    \
+    else if (p.E <= 128) RUN(8, 16);  \
+    else if (p.E <= 256) RUN(8, 32);  \
+    else if (p.E <= 512) RUN(16, 32); \
+    else RUN(32, 32);                 \
+  } while (0)
+
 template <typename T>
 void run_topk(const RouterParams& p, cudaStream_t st) {
-  const unsigned grid = token_grid(p.T);
-  if (p.E <= 64)
-    router_topk_kernel<T, 2><<<grid, kThreads, 0, st>>>(p);
-  else if (p.E <= 128)
-    router_topk_kernel<T, 4><<<grid, kThreads, 0, st>>>(p);
-  else if (p.E <= 256)
-    router_topk_kernel<T, 8><<<grid, kThreads, 0, st>>>(p);
-  else if (p.E <= 512)
-    router_topk_kernel<T, 16><<<grid, kThreads, 0, st>>>(p);
-  else
-    router_topk_kernel<T, 32><<<grid, kThreads, 0, st>>>(p);
-}
-
-template <typename T, int V>
-cudaError_t run_bwd_v(const RouterBwdParams& p, cudaStream_t st) {
-  const size_t smem = p.format == MOE_ROUTING_DENSE_I16 ? (size_t)kWarps * 2 * p.E * sizeof(float) : 0;
-  static PerDeviceOnce once;  // E = 1024: 64 KB
-  cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(router_bwd_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kWarps * 2 * 1024 * (int)sizeof(float));
-  });
-  if (e != cudaSuccess) return e;
-  router_bwd_kernel<T, V><<<token_grid(p.T), kThreads, smem, st>>>(p);
-  return cudaGetLastError();
+#define RUN(V, L) router_topk_kernel<T, V, L><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+  MOE_ROUTER_SHAPE(RUN);
+#undef RUN
 }
 
 template <typename T>
-cudaError_t run_bwd(const RouterBwdParams& p, cudaStream_t st) {
-  if (p.E <= 64) return run_bwd_v<T, 2>(p, st);
-  if (p.E <= 128) return run_bwd_v<T, 4>(p, st);
-  if (p.E <= 256) return run_bwd_v<T, 8>(p, st);
-  if (p.E <= 512) return run_bwd_v<T, 16>(p, st);
-  return run_bwd_v<T, 32>(p, st);
+void run_bwd(const RouterBwdParams& p, cudaStream_t st) {
+#define RUN(V, L) router_bwd_kernel<T, V, L><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+  MOE_ROUTER_SHAPE(RUN);
+#undef RUN
+}
+
+int elem_bytes(int32_t dtype) { return dtype == MOE_ELEM_F32 ? 4 : 2; }
+
+// Rows of E elements that are whole 16-byte vectors.
+bool vector_rows(const moe_rows& m, int64_t E, int bytes) {
+  return E * bytes % 16 == 0 && E % 8 == 0 && m.stride * bytes % 16 == 0 && aligned(m.data, 16);
 }
 
 }  // namespace
@@ -299,6 +515,8 @@ cudaError_t launch_router_topk(const moe_router& r, const moe_rows& logits, cons
   p.map = map;
   p.probs = probs;
   p.status = status;
+  p.vector_in = vector_rows(logits, r.E, elem_bytes(r.logits_dtype));
+  p.vector_out = r.E % 8 == 0 && aligned(map, 8) && aligned(probs, 16);
   switch (r.logits_dtype) {
     case MOE_ELEM_F32: run_topk<float>(p, st); break;
     case MOE_ELEM_BF16: run_topk<__nv_bfloat16>(p, st); break;
@@ -323,11 +541,16 @@ cudaError_t launch_router_topk_backward(const moe_router& r, const moe_rows& log
   p.gp = grad_probs;
   p.gl = grad_logits.data;
   p.gstride = grad_logits.stride;
+  const int b = elem_bytes(r.logits_dtype);
+  p.vector_in = vector_rows(logits, r.E, b);
+  p.vector_out = vector_rows(grad_logits, r.E, b);
+  p.vector_map = r.E % 8 == 0 && aligned(map, 8) && aligned(grad_probs, 16);
   switch (r.logits_dtype) {
-    case MOE_ELEM_F32: return run_bwd<float>(p, st);
-    case MOE_ELEM_BF16: return run_bwd<__nv_bfloat16>(p, st);
-    default: return run_bwd<__half>(p, st);
+    case MOE_ELEM_F32: run_bwd<float>(p, st); break;
+    case MOE_ELEM_BF16: run_bwd<__nv_bfloat16>(p, st); break;
+    default: run_bwd<__half>(p, st); break;
   }
+  return cudaGetLastError();
 }
 
 }  // namespace moe
