@@ -10,6 +10,8 @@
 // value by bisection of its bit pattern, everything above it is chosen and the
 // lowest experts among those equal to it fill the rest.  Ids come out ascending.
 // Scores and sums are fp32 in a fixed order.
+#include <type_traits>
+
 #include "block_common.cuh"
 #include "moe_internal.h"
 
@@ -24,7 +26,7 @@ constexpr unsigned kAll = 0xffffffffu;
 struct RouterParams {
   int64_t T, stride;
   int E, K;
-  int score, renorm, format;
+  int renorm, format;
   bool vector_in, vector_out;  // rows of logits / of a sparse map are whole aligned vectors
   float scale;
   const void* logits;
@@ -42,19 +44,18 @@ MOE_DEVICE uint32_t key_of(float v) {
 MOE_DEVICE float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 // exp(l - top), with the limit 1 where l is top (both may be +inf).
-MOE_DEVICE float exp_below(float l, float top) { return l == top ? 1.0f : expf(l - top); }
+MOE_DEVICE float exp_below(float l, float top) { return expf(l == top ? 0.0f : l - top); }
 
 // sigmoid(l) * exp(-m) for m = min(largest l, 0): the common factor keeps the
 // ratio of two sigmoids when both are far below the smallest float.
 MOE_DEVICE float sigmoid_scaled(float l, float m) {
-  return l >= 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - m) / (1.0f + expf(l));
+  return __fdividef(l >= 0.0f ? 1.0f : expf(l - m), 1.0f + expf(-fabsf(l)));
 }
 
 // 1 - sigmoid(l)
 MOE_DEVICE float sigmoid_rest(float l) {
-  if (l < 0.0f) return 1.0f / (1.0f + expf(l));
-  const float z = expf(-l);
-  return z / (1.0f + z);
+  const float e = expf(-fabsf(l));
+  return __fdividef(l < 0.0f ? 1.0f : e, 1.0f + e);
 }
 
 // Over the L lanes of a group.
@@ -119,33 +120,30 @@ MOE_DEVICE int count_from(const float (&s)[V], float v) {
   return n;
 }
 
-// Bit j: expert e0 + j is chosen.  `live` scores are above -inf, at least one;
-// `top` is the largest.
+// Bit j: expert e0 + j is chosen.  `live` scores are above -inf; `low` and `top`
+// are the smallest and the largest of them (+inf and -inf if there is none).
 template <int V, int L>
-MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float top) {
-  float low = INFINITY;
-#pragma unroll
-  for (int j = 0; j < V; j++)
-    if (s[j] > -INFINITY) low = fminf(low, s[j]);
-  low = -group_max<L>(-low);
+MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float low, float top) {
   // counts: n_lo >= K scores reach lo, n_hi < K reach hi; the choice is exact once a count is K
   float lo = low, hi = top;
   int n_lo = live, n_hi = group_add<L>(count_from<V>(s, top));
   bool exact = live <= K, found = exact || n_hi >= K;
   if (!exact && n_hi >= K) lo = top, n_lo = n_hi, exact = n_hi == K;
-  for (int it = 0; it < 12; it++) {
-    if (__all_sync(kAll, found)) break;
-    float part = ((float)(K - n_hi) + 0.5f) / (float)(n_lo - n_hi + 1);
-    part = fminf(fmaxf(part, 0.0625f), 0.9375f);
-    const float mid = hi - (hi - lo) * part;
+  // a token's lanes agree; other tokens of the warp go on
+  auto all_found = [&] { return L == 32 ? found : (bool)__all_sync(kAll, found); };
+  for (int it = 0; it < 12 && !all_found(); it++) {
+    // the place of the K-th score if those between the ends were spread evenly
+    const float part = __fdividef((float)(K - n_hi) + 0.5f, (float)(n_lo - n_hi + 1));
+    const float mid = hi - (hi - lo) * fminf(fmaxf(part, 0.0625f), 0.9375f);
     const int n = group_add<L>(count_from<V>(s, mid));
-    if (found || !(mid > lo && mid < hi)) continue;
-    if (n >= K)
-      lo = mid, n_lo = n, exact = found = n == K;
-    else
-      hi = mid, n_hi = n;
+    if (!found && mid > lo && mid < hi) {
+      if (n >= K)
+        lo = mid, n_lo = n, exact = found = n == K;
+      else
+        hi = mid, n_hi = n;
+    }
   }
-  if (!__all_sync(kAll, found)) {  // equal, infinite or very uneven scores
+  if (!all_found()) {  // equal, infinite or very uneven scores
     uint32_t klo = key_of(lo), khi = key_of(hi);
     if (found) khi = klo + 1;
     while (__any_sync(kAll, khi - klo > 1)) {
@@ -161,11 +159,11 @@ MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float top) 
   }
   uint32_t on = 0;
 #pragma unroll
-  for (int j = 0; j < V; j++) on |= (uint32_t)(s[j] >= lo) << j;
-  if (!__all_sync(kAll, exact)) {
+  for (int j = 0; j < V; j++) on |= s[j] >= lo ? 1u << j : 0u;
+  if (!(L == 32 ? exact : (bool)__all_sync(kAll, exact))) {
     uint32_t above = 0;
 #pragma unroll
-    for (int j = 0; j < V; j++) above |= (uint32_t)(s[j] > lo) << j;
+    for (int j = 0; j < V; j++) above |= s[j] > lo ? 1u << j : 0u;
     uint32_t equal = on & ~above;
     int room = K - group_add<L>(__popc(above)) - group_below<L>(__popc(equal));
     if (!exact) {
@@ -176,21 +174,21 @@ MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float top) 
       on = above;
     }
   }
-  // the interval may start at the lowest live score, masked ones are below it
   return on;
 }
 
-template <typename T, int V, int L>
+template <typename T, int V, int L, int SCORE>
 __global__ void __launch_bounds__(kThreads) router_topk_kernel(RouterParams p) {
-  constexpr int kTokens = 32 / L;               // tokens of a warp
+  constexpr int kTokens = 32 / L;                     // tokens of a warp
   constexpr int kChosen = V * L < 128 ? V * L : 128;  // K at the most
-  __shared__ float logit_of[kWarps][kTokens][kChosen];
+  constexpr bool kSoftmax = SCORE == MOE_SCORE_SOFTMAX;
+  __shared__ float weight_of[kWarps][kTokens][kChosen];
   __shared__ int16_t id_of[kWarps][kTokens][kChosen];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int at = lane % L, e0 = at * V;
-  float* chosen_logit = logit_of[warp][lane / L];
+  float* chosen_weight = weight_of[warp][lane / L];
   int16_t* chosen_id = id_of[warp][lane / L];
-  const bool softmax = p.score == MOE_SCORE_SOFTMAX, divide = softmax || p.renorm;
+  const bool divide = kSoftmax || p.renorm;
 
   for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; t0 < p.T;
        t0 += (int64_t)gridDim.x * kWarps * kTokens) {
@@ -200,81 +198,85 @@ __global__ void __launch_bounds__(kThreads) router_topk_kernel(RouterParams p) {
     float s[V];
     load_scores<T, V>(s, row, e0, p.E, p.vector_in);
     bool bad = false;
-    int live = 0;
-    float top = -INFINITY;
+    float low = INFINITY, top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; j++) {
       bad |= s[j] != s[j];
       if (p.bias && s[j] > -INFINITY) {  // (false past the end of the row)
-        s[j] = (softmax ? s[j] : sigmoid_scaled(s[j], 0.0f)) + p.bias[e0 + j];
+        s[j] = (kSoftmax ? s[j] : sigmoid_scaled(s[j], 0.0f)) + p.bias[e0 + j];
         bad |= s[j] != s[j];
       }
-      if (!(s[j] > -INFINITY)) s[j] = -INFINITY;
-      live += s[j] > -INFINITY;
+      s[j] = fmaxf(s[j], -INFINITY);  // NaN: masked
+      if (e0 + j < p.E) low = fminf(low, s[j]);
       top = fmaxf(top, s[j]);
     }
     if (bad && p.status) atomicOr(p.status, MOE_DEV_ERR_NAN_LOGIT);
-    live = group_add<L>(live);
+    low = -group_max<L>(-low);
     top = group_max<L>(top);
-    uint32_t on = select_top<V, L>(s, p.K, live, top);
-    uint32_t alive = 0;
-#pragma unroll
-    for (int j = 0; j < V; j++) alive |= (uint32_t)(s[j] > -INFINITY) << j;
-    on &= alive;
-
-    // logits again where the scores are not
-    if (p.bias) {
-      load_scores<T, V>(s, row, e0, p.E, p.vector_in);
-      top = -INFINITY;  // of the logits that take part
+    int live = p.E;
+    if (__any_sync(kAll, low == -INFINITY)) {  // some experts are masked
+      low = INFINITY;
+      live = 0;
 #pragma unroll
       for (int j = 0; j < V; j++) {
-        if (!(alive >> j & 1)) s[j] = -INFINITY;
-        if ((on >> j & 1) || !p.renorm) top = fmaxf(top, s[j]);
+        live += s[j] > -INFINITY;
+        low = fminf(low, s[j] > -INFINITY ? s[j] : INFINITY);
+      }
+      live = group_add<L>(live);
+      low = -group_max<L>(-low);
+    }
+    const uint32_t on = select_top<V, L>(s, p.K, live, low, top);
+
+    // the chosen ids in ascending order through shared memory
+    const int first = group_below<L>(__popc(on)), count = group_add<L>(__popc(on));
+    int slot = first;
+    for (uint32_t left = on; left; left &= left - 1) chosen_id[slot++] = (int16_t)(e0 + __ffs(left) - 1);
+    __syncwarp();
+
+    // weights, L of the chosen at a time; the largest logit that takes part is
+    // `top` itself, and looked for where the scores are not the logits
+    float z = 0.0f;
+    if (p.bias) {
+      top = -INFINITY;
+      if (kSoftmax && !p.renorm) {
+#pragma unroll
+        for (int j = 0; j < V; j++)
+          if (s[j] > -INFINITY) top = fmaxf(top, to_float(row[e0 + j]));
+      } else {
+        for (int k = at; k < count; k += L) top = fmaxf(top, to_float(row[chosen_id[k]]));
       }
       top = group_max<L>(top);
     }
-    const float m = p.renorm ? fminf(top, 0.0f) : 0.0f;
-    auto weight = [&](float l) { return softmax ? exp_below(l, top) : sigmoid_scaled(l, m); };
-
-    float z = 0.0f;
-    if (softmax && !p.renorm) {  // every live expert takes part in the sum
+    if (kSoftmax && !p.renorm) {  // every live expert takes part in the sum
 #pragma unroll
-      for (int j = 0; j < V; j++)
-        if (s[j] > -INFINITY) z += exp_below(s[j], top);
-      z = group_add<L>(z);
-    }
-    // the chosen in ascending order through shared memory, L at a time
-    const int first = group_below<L>(__popc(on)), count = group_add<L>(__popc(on));
-    int slot = first;
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-      if (on >> j & 1) {
-        chosen_logit[slot] = s[j];
-        chosen_id[slot] = (int16_t)(e0 + j);
-        slot++;
+      for (int j = 0; j < V; j++) {
+        float l = s[j];
+        if (p.bias && l > -INFINITY) l = to_float(row[e0 + j]);
+        z += s[j] > -INFINITY ? exp_below(l, top) : 0.0f;
       }
     }
-    __syncwarp();
+    const float m = p.renorm ? fminf(top, 0.0f) : 0.0f;
     for (int k = at; k < count; k += L) {
-      const float w = weight(chosen_logit[k]);
-      chosen_logit[k] = w;
+      const float l = to_float(row[chosen_id[k]]);
+      const float w = kSoftmax ? exp_below(l, top) : sigmoid_scaled(l, m);
+      chosen_weight[k] = w;
       if (p.renorm) z += w;
     }
-    if (p.renorm) z = group_add<L>(z);
-    const float f = divide ? p.scale / z : p.scale;  // (z is 0 where nothing is chosen)
-    __syncwarp();
+    if (divide) z = group_add<L>(z);
+    const float f = divide ? __fdividef(p.scale, z) : p.scale;  // (z is 0 where nothing is chosen)
     if (p.format == MOE_ROUTING_DENSE_I16) {
       if (real) {
         for (int k = at; k < p.K; k += L) {
           const bool in = k < count;
           static_cast<int16_t*>(p.map)[t * p.K + k] = in ? chosen_id[k] : (int16_t)-1;
-          p.probs[t * p.K + k] = in ? chosen_logit[k] * f : 0.0f;
+          p.probs[t * p.K + k] = in ? chosen_weight[k] * f : 0.0f;
         }
       }
     } else {
+      __syncwarp();
       slot = first;
 #pragma unroll
-      for (int j = 0; j < V; j++) s[j] = on >> j & 1 ? chosen_logit[slot++] * f : 0.0f;
+      for (int j = 0; j < V; j++) s[j] = on >> j & 1 ? chosen_weight[slot++] * f : 0.0f;
       if (real) {
         uint8_t* map = static_cast<uint8_t*>(p.map) + t * p.E;
         float* probs = p.probs + t * p.E;
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) router_topk_kernel(RouterParams p) {
 struct RouterBwdParams {
   int64_t T, stride, gstride;
   int E, K;
-  int score, renorm, format;
+  int renorm, format;
   bool vector_in, vector_out, vector_map;
   float scale;
   const void *logits, *map;
@@ -322,7 +324,7 @@ struct RouterBwdParams {
 // Marks an expert without a gradient in a staged row (a NaN no computation makes).
 constexpr uint32_t kNoGradient = 0xffa5c3e7u;
 
-template <typename T, int V, int L>
+template <typename T, int V, int L, int SCORE>
 __global__ void __launch_bounds__(kThreads) router_bwd_kernel(RouterBwdParams p) {
   constexpr int kTokens = 32 / L, N = 16 / sizeof(T);
   __shared__ uint4 staged[kWarps][kTokens * V * L / 4];  // dense maps: gradients by expert
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(RouterBwdParams p)
   const int at = lane % L, e0 = at * V;
   uint4* mine = staged[warp] + lane * (V / 4);  // this lane's experts
   uint32_t* grow = reinterpret_cast<uint32_t*>(staged[warp] + lane / L * L * (V / 4));
-  const bool softmax = p.score == MOE_SCORE_SOFTMAX;
+  constexpr bool kSoftmax = SCORE == MOE_SCORE_SOFTMAX;
 
   for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; t0 < p.T;
        t0 += (int64_t)gridDim.x * kWarps * kTokens) {
@@ -388,15 +390,17 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(RouterBwdParams p)
         }
       }
     }
-    float top = -INFINITY;  // of the logits that take part
+    // experts that take part: the chosen, with the plain softmax all
+    const bool all = kSoftmax && !p.renorm;
+    float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      if (!(l[j] > -INFINITY)) {  // masked, NaN, or past the end of the row: no gradient
-        l[j] = -INFINITY;
-        on &= ~(1u << j);
-      }
-      if (!(on >> j & 1)) g[j] = 0.0f;
-      if ((on >> j & 1) || (softmax && !p.renorm)) top = fmaxf(top, l[j]);
+      const bool masked = !(l[j] > -INFINITY);  // or NaN, or past the end of the row: no gradient
+      on &= masked ? ~(1u << j) : ~0u;
+      const bool c = on >> j & 1;
+      g[j] = c ? g[j] : 0.0f;
+      l[j] = c || (all && !masked) ? l[j] : -INFINITY;
+      top = fmaxf(top, l[j]);
     }
     top = group_max<L>(top);
     const float m = p.renorm ? fminf(top, 0.0f) : 0.0f;
@@ -404,33 +408,26 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(RouterBwdParams p)
     float n[V], z = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      const bool c = on >> j & 1;
-      n[j] = 0.0f;
-      if (softmax) {
-        if ((c || !p.renorm) && l[j] > -INFINITY) n[j] = exp_below(l[j], top);
-      } else if (c) {
-        n[j] = sigmoid_scaled(l[j], m);
-      }
+      const float v = kSoftmax ? exp_below(l[j], top) : sigmoid_scaled(l[j], m);
+      n[j] = l[j] > -INFINITY ? v : 0.0f;
       z += n[j];
       dot = fmaf(g[j], n[j], dot);
     }
-    float inv = 1.0f;
-    if (softmax || p.renorm) {
+    float inv = p.scale;
+    if (kSoftmax || p.renorm) {
       z = group_add<L>(z);
       dot = group_add<L>(dot);
-      inv = z > 0.0f ? 1.0f / z : 0.0f;
-      dot *= inv;
+      const float r = z > 0.0f ? __fdividef(1.0f, z) : 0.0f;
+      inv *= r;
+      dot *= r;
     } else {
       dot = 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      float v = 0.0f;
-      if (n[j] != 0.0f) {
-        v = p.scale * (n[j] * inv) * (g[j] - dot);
-        if (!softmax) v *= sigmoid_rest(l[j]);
-      }
-      g[j] = v;
+      float v = n[j] * inv * (g[j] - dot);
+      if (!kSoftmax) v *= sigmoid_rest(l[j]);
+      g[j] = n[j] != 0.0f ? v : 0.0f;
     }
     if (!real) continue;
     T* out = static_cast<T*>(p.gl) + t * p.gstride + e0;
@@ -476,18 +473,44 @@ unsigned token_grid(int64_t T) {
     else RUN(32, 32);                 \
   } while (0)
 
-template <typename T>
+template <typename T, int SCORE>
 void run_topk(const RouterParams& p, cudaStream_t st) {
-#define RUN(V, L) router_topk_kernel<T, V, L><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+#define RUN(V, L) router_topk_kernel<T, V, L, SCORE><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
   MOE_ROUTER_SHAPE(RUN);
 #undef RUN
 }
 
-template <typename T>
+template <typename T, int SCORE>
 void run_bwd(const RouterBwdParams& p, cudaStream_t st) {
-#define RUN(V, L) router_bwd_kernel<T, V, L><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+#define RUN(V, L) router_bwd_kernel<T, V, L, SCORE><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
   MOE_ROUTER_SHAPE(RUN);
 #undef RUN
+}
+
+template <int SCORE, typename Params>
+void run_score(int32_t dtype, const Params& p, cudaStream_t st) {
+  constexpr bool kBackward = std::is_same<Params, RouterBwdParams>::value;
+  auto run = [&](auto zero) {
+    using T = decltype(zero);
+    if constexpr (kBackward)
+      run_bwd<T, SCORE>(p, st);
+    else
+      run_topk<T, SCORE>(p, st);
+  };
+  switch (dtype) {
+    case MOE_ELEM_F32: run(0.0f); break;
+    case MOE_ELEM_BF16: run(__nv_bfloat16()); break;
+    default: run(__half()); break;
+  }
+}
+
+template <typename Params>
+cudaError_t run_dtype(const moe_router& r, const Params& p, cudaStream_t st) {
+  if (r.score == MOE_SCORE_SOFTMAX)
+    run_score<MOE_SCORE_SOFTMAX>(r.logits_dtype, p, st);
+  else
+    run_score<MOE_SCORE_SIGMOID>(r.logits_dtype, p, st);
+  return cudaGetLastError();
 }
 
 int elem_bytes(int32_t dtype) { return dtype == MOE_ELEM_F32 ? 4 : 2; }
@@ -505,7 +528,6 @@ cudaError_t launch_router_topk(const moe_router& r, const moe_rows& logits, cons
   p.T = r.T;
   p.E = (int)r.E;
   p.K = (int)r.K;
-  p.score = r.score;
   p.renorm = r.renormalize != 0;
   p.scale = r.scale;
   p.format = format;
@@ -517,12 +539,7 @@ cudaError_t launch_router_topk(const moe_router& r, const moe_rows& logits, cons
   p.status = status;
   p.vector_in = vector_rows(logits, r.E, elem_bytes(r.logits_dtype));
   p.vector_out = r.E % 8 == 0 && aligned(map, 8) && aligned(probs, 16);
-  switch (r.logits_dtype) {
-    case MOE_ELEM_F32: run_topk<float>(p, st); break;
-    case MOE_ELEM_BF16: run_topk<__nv_bfloat16>(p, st); break;
-    default: run_topk<__half>(p, st); break;
-  }
-  return cudaGetLastError();
+  return run_dtype(r, p, st);
 }
 
 cudaError_t launch_router_topk_backward(const moe_router& r, const moe_rows& logits, int32_t format, const void* map,
@@ -531,7 +548,6 @@ cudaError_t launch_router_topk_backward(const moe_router& r, const moe_rows& log
   p.T = r.T;
   p.E = (int)r.E;
   p.K = (int)r.K;
-  p.score = r.score;
   p.renorm = r.renormalize != 0;
   p.scale = r.scale;
   p.format = format;
@@ -545,12 +561,7 @@ cudaError_t launch_router_topk_backward(const moe_router& r, const moe_rows& log
   p.vector_in = vector_rows(logits, r.E, b);
   p.vector_out = vector_rows(grad_logits, r.E, b);
   p.vector_map = r.E % 8 == 0 && aligned(map, 8) && aligned(grad_probs, 16);
-  switch (r.logits_dtype) {
-    case MOE_ELEM_F32: run_bwd<float>(p, st); break;
-    case MOE_ELEM_BF16: run_bwd<__nv_bfloat16>(p, st); break;
-    default: run_bwd<__half>(p, st); break;
-  }
-  return cudaGetLastError();
+  return run_dtype(r, p, st);
 }
 
 }  // namespace moe
