@@ -3,13 +3,13 @@
 //
 // A group of L lanes takes a token, V neighbouring experts a lane (E <= V L), so
 // that a warp works on 32 / L tokens at once.  The selection looks for a
-// threshold that exactly K scores reach: it shrinks an interval by the counts
-// at its ends, reading the scores' order from the scores themselves, and stops at
-// the first count that is K, after four or five steps on spread scores.  Where
-// scores are equal no threshold has that count; the interval then closes on one
+// threshold that exactly K scores reach: it guesses one from the scores' mean and
+// deviation, shrinks an interval by the counts, and stops at the first count
+// that is K.  Where scores are equal no threshold may have that count; the interval then closes on one
 // value by bisection of its bit pattern, everything above it is chosen and the
 // lowest experts among those equal to it fill the rest.  Ids come out ascending.
 // Scores and sums are fp32 in a fixed order.
+#include <cmath>
 #include <type_traits>
 
 #include "block_common.cuh"
@@ -29,6 +29,7 @@ struct RouterParams {
   int renorm, format;
   bool vector_in, vector_out;  // rows of logits / of a sparse map are whole aligned vectors
   float scale;
+  float quantile, spacing;  // of a standard normal sample of E, at the K-th largest
   const void* logits;
   const float* bias;
   void* map;
@@ -122,29 +123,38 @@ MOE_DEVICE int count_from(const float (&s)[V], float v) {
 
 // Bit j: expert e0 + j is chosen.  `live` scores are above -inf; `low` and `top`
 // are the smallest and the largest of them (+inf and -inf if there is none).
+// `guess` is where the K-th score would be, and `step` how far a score is from
+// the next there, if the scores were a normal sample: the first guess then
+// counts K but for a few, and a step by the difference mostly lands on K.
+// Whatever they are, the interval bounds the search.
 template <int V, int L>
-MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float low, float top) {
-  // counts: n_lo >= K scores reach lo, n_hi < K reach hi; the choice is exact once a count is K
+MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float low, float top, float guess, float step) {
+  // counts: n_lo >= K scores reach lo, n_hi < K reach hi (hi is the top, and n_hi
+  // 0, until there is a count below K); the choice is exact once a count is K
   float lo = low, hi = top;
-  int n_lo = live, n_hi = group_add<L>(count_from<V>(s, top));
-  bool exact = live <= K, found = exact || n_hi >= K;
-  if (!exact && n_hi >= K) lo = top, n_lo = n_hi, exact = n_hi == K;
+  int n_lo = live, n_hi = 0;
+  bool exact = live <= K, found = exact;
   // a token's lanes agree; other tokens of the warp go on
   auto all_found = [&] { return L == 32 ? found : (bool)__all_sync(kAll, found); };
+  float mid = K == 1 ? top : fminf(guess, top);
   for (int it = 0; it < 12 && !all_found(); it++) {
-    // the place of the K-th score if those between the ends were spread evenly
-    const float part = __fdividef((float)(K - n_hi) + 0.5f, (float)(n_lo - n_hi + 1));
-    const float mid = hi - (hi - lo) * fminf(fmaxf(part, 0.0625f), 0.9375f);
+    if (!(mid > lo && mid <= hi) || it > 4) {
+      // the place of the K-th score if those between the ends were spread evenly
+      const float part = __fdividef((float)(K - n_hi) + 0.5f, (float)(n_lo - n_hi + 1));
+      mid = hi - (hi - lo) * fminf(fmaxf(part, 0.0625f), 0.9375f);
+    }
     const int n = group_add<L>(count_from<V>(s, mid));
-    if (!found && mid > lo && mid < hi) {
+    if (!found && mid > lo && mid <= hi) {
       if (n >= K)
-        lo = mid, n_lo = n, exact = found = n == K;
+        lo = mid, n_lo = n, exact = n == K;
       else
         hi = mid, n_hi = n;
+      found = exact || lo == top;  // (equal to the top, and not all of them fit)
     }
+    mid += (float)(n - K) * step;
   }
   if (!all_found()) {  // equal, infinite or very uneven scores
-    uint32_t klo = key_of(lo), khi = key_of(hi);
+    uint32_t klo = key_of(lo), khi = key_of(hi) + (n_hi == 0);
     if (found) khi = klo + 1;
     while (__any_sync(kAll, khi - klo > 1)) {
       const uint32_t kmid = klo + (khi - klo) / 2;
@@ -178,7 +188,7 @@ MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float low, 
 }
 
 template <typename T, int V, int L, int SCORE>
-__global__ void __launch_bounds__(kThreads) router_topk_kernel(RouterParams p) {
+__global__ void __launch_bounds__(kThreads, V == 8 ? 5 : 1) router_topk_kernel(RouterParams p) {
   constexpr int kTokens = 32 / L;                     // tokens of a warp
   constexpr int kChosen = V * L < 128 ? V * L : 128;  // K at the most
   constexpr bool kSoftmax = SCORE == MOE_SCORE_SOFTMAX;
@@ -198,34 +208,51 @@ __global__ void __launch_bounds__(kThreads) router_topk_kernel(RouterParams p) {
     float s[V];
     load_scores<T, V>(s, row, e0, p.E, p.vector_in);
     bool bad = false;
-    float low = INFINITY, top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < V; j++) {
-      bad |= s[j] != s[j];
-      if (p.bias && s[j] > -INFINITY) {  // (false past the end of the row)
-        s[j] = (kSoftmax ? s[j] : sigmoid_scaled(s[j], 0.0f)) + p.bias[e0 + j];
-        bad |= s[j] != s[j];
+    for (int j = 0; j < V; j++) bad |= s[j] != s[j];
+    if (p.bias) {
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        if (s[j] > -INFINITY) {  // (false past the end of the row)
+          s[j] = (kSoftmax ? s[j] : sigmoid_scaled(s[j], 0.0f)) + p.bias[e0 + j];
+          bad |= s[j] != s[j];
+        }
       }
-      s[j] = fmaxf(s[j], -INFINITY);  // NaN: masked
-      if (e0 + j < p.E) low = fminf(low, s[j]);
-      top = fmaxf(top, s[j]);
     }
     if (bad && p.status) atomicOr(p.status, MOE_DEV_ERR_NAN_LOGIT);
+    float low = INFINITY, top = -INFINITY, sum = 0.0f, squares = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      s[j] = fmaxf(s[j], -INFINITY);  // NaN: masked
+      const bool in = e0 + j < p.E;
+      low = fminf(low, in ? s[j] : INFINITY);
+      top = fmaxf(top, s[j]);
+      sum += in ? s[j] : 0.0f;
+      squares = fmaf(in ? s[j] : 0.0f, s[j], squares);
+    }
     low = -group_max<L>(-low);
     top = group_max<L>(top);
     int live = p.E;
     if (__any_sync(kAll, low == -INFINITY)) {  // some experts are masked
       low = INFINITY;
       live = 0;
+      sum = squares = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; j++) {
-        live += s[j] > -INFINITY;
-        low = fminf(low, s[j] > -INFINITY ? s[j] : INFINITY);
+        const bool in = s[j] > -INFINITY;
+        live += in;
+        low = fminf(low, in ? s[j] : INFINITY);
+        sum += in ? s[j] : 0.0f;
+        squares = fmaf(in ? s[j] : 0.0f, in ? s[j] : 0.0f, squares);
       }
       live = group_add<L>(live);
       low = -group_max<L>(-low);
     }
-    const uint32_t on = select_top<V, L>(s, p.K, live, low, top);
+    sum = group_add<L>(sum);
+    squares = group_add<L>(squares);
+    const float mean = __fdividef(sum, (float)live);
+    const float dev = sqrtf(fmaxf(__fdividef(squares, (float)live) - mean * mean, 0.0f));
+    const uint32_t on = select_top<V, L>(s, p.K, live, low, top, mean + dev * p.quantile, dev * p.spacing);
 
     // the chosen ids in ascending order through shared memory
     const int first = group_below<L>(__popc(on)), count = group_add<L>(__popc(on));
@@ -537,6 +564,14 @@ cudaError_t launch_router_topk(const moe_router& r, const moe_rows& logits, cons
   p.map = map;
   p.probs = probs;
   p.status = status;
+  // the upper tail's quantile by the rational approximation 26.2.23 of Abramowitz
+  // and Stegun's handbook
+  const float tail = (float)r.K / (float)(r.E + 1), side = tail <= 0.5f ? tail : 1.0f - tail;
+  const float q = std::sqrt(-2.0f * std::log(side));
+  const float x = q - (2.515517f + q * (0.802853f + q * 0.010328f)) /
+                          (1.0f + q * (1.432788f + q * (0.189269f + q * 0.001308f)));
+  p.quantile = tail <= 0.5f ? x : -x;
+  p.spacing = std::exp(0.5f * x * x) * 2.5066283f / (float)r.E;  // 1 / (E density)
   p.vector_in = vector_rows(logits, r.E, elem_bytes(r.logits_dtype));
   p.vector_out = r.E % 8 == 0 && aligned(map, 8) && aligned(probs, 16);
   return run_dtype(r, p, st);
