@@ -7,6 +7,8 @@
 //   gx = rstd (u - sum u / H - xhat sum(u xhat) / H) (+ gsum)
 //   gw = sum over rows of gy xhat,  gb = sum over rows of gy
 // Every sum is fp32: a lane's elements in order, then a fixed shuffle tree.
+#include <type_traits>
+
 #include "block_common.cuh"
 #include "moe_internal.h"
 
@@ -88,17 +90,6 @@ MOE_DEVICE void load_vec(float (&out)[Vec<T>::kN], const T* p) {
   for (int i = 0; i < Vec<T>::kN; i++) out[i] = to_float(u.t.e[i]);
 }
 
-template <typename T>
-MOE_DEVICE void store_vec(T* p, const float (&in)[Vec<T>::kN]) {
-  union {
-    uint4 v;
-    Vec<T> t;
-  } u;
-#pragma unroll
-  for (int i = 0; i < Vec<T>::kN; i++) u.t.e[i] = from_float<T>(in[i]);
-  *reinterpret_cast<uint4*>(p) = u.v;
-}
-
 // Parameters of the same columns: fp32 or the rows' type.
 template <typename T, typename P>
 MOE_DEVICE void load_params(float (&out)[Vec<T>::kN], const P* p) {
@@ -112,86 +103,150 @@ MOE_DEVICE void load_params(float (&out)[Vec<T>::kN], const P* p) {
   }
 }
 
+template <typename T>
+MOE_DEVICE void unpack(float (&out)[Vec<T>::kN], uint4 raw) {
+  union {
+    uint4 v;
+    Vec<T> t;
+  } u;
+  u.v = raw;
+#pragma unroll
+  for (int i = 0; i < Vec<T>::kN; i++) out[i] = to_float(u.t.e[i]);
+}
+
+template <typename T>
+MOE_DEVICE uint4 pack(const float (&in)[Vec<T>::kN]) {
+  union {
+    uint4 v;
+    Vec<T> t;
+  } u;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kN; i++) u.t.e[i] = in[i];
+  } else {  // two at a time
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(in[2 * i], in[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(in[2 * i], in[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    u.v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return u.v;
+}
+
 // Rows of 16-byte vectors held in registers between the mean, the variance and
-// the result, so that the row is read once.  kTeam threads take a row, V vectors
-// each: a warp up to 32 V vectors, else a whole CTA.
-template <typename T, typename P, int V, int TEAM>
-__global__ void __launch_bounds__(TEAM == 32 ? kThreads : TEAM) layer_norm_vec_kernel(NormParams p) {
+// the result, so that the row is read once, V vectors a thread.  LANES threads
+// of a warp take a row; or (0) a CTA does, and its next row is on its way while
+// it reduces and writes this one: two barriers a row would leave the memory idle.
+template <typename T, typename P, int V, int LANES, int THREADS>
+__global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_norm_vec_kernel(NormParams p) {
   constexpr int N = Vec<T>::kN;
-  constexpr int kTeams = TEAM == 32 ? kThreads / 32 : 1;
-  __shared__ float2 red[2][TEAM == 32 ? 1 : TEAM / 32];
+  constexpr bool kAhead = LANES == 0;
+  __shared__ float2 red[2][THREADS / 32];
   const P* w = static_cast<const P*>(p.w);
   const P* b = static_cast<const P*>(p.b);
-  const int t = threadIdx.x % TEAM;
-  const int nvec = (int)(p.H / N);
-  for (int64_t r = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; r < p.rows; r += (int64_t)gridDim.x * kTeams) {
-    const T* x = static_cast<const T*>(p.x) + r * p.sx;
-    const T* res = p.res ? static_cast<const T*>(p.res) + r * p.sres : nullptr;
-    T* sum = p.sum ? static_cast<T*>(p.sum) + r * p.ssum : nullptr;
-    T* y = static_cast<T*>(p.y) + r * p.sy;
-    float h[V][N];
-    float s = 0.0f;
+  const int team = LANES ? LANES : (int)blockDim.x, teams = LANES ? THREADS / LANES : 1;
+  const int t = LANES ? threadIdx.x % LANES : threadIdx.x;
+  const int nvec = (int)(p.H / N), v_step = team * N;
+  auto total = [&](float v, float2* r) {
+    if (!LANES) return block_sum2(v, 0.0f, r).x;
+#pragma unroll
+    for (int d = LANES / 2; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+  };
+  uint4 x_raw[V], res_raw[V];
+  auto fetch = [&](int64_t r) {
+    const T* x = static_cast<const T*>(p.x) + r * p.sx + t * N;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      const int i = v * TEAM + t;
-      if (i < nvec) {
-        load_vec<T>(h[v], x + i * N);
+      x_raw[v] = make_uint4(0, 0, 0, 0);
+      if (v * team + t < nvec) x_raw[v] = *reinterpret_cast<const uint4*>(x + v * v_step);
+    }
+    if (p.res) {
+      const T* res = static_cast<const T*>(p.res) + r * p.sres + t * N;
+#pragma unroll
+      for (int v = 0; v < V; v++)
+        if (v * team + t < nvec) res_raw[v] = *reinterpret_cast<const uint4*>(res + v * v_step);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * teams;
+  if (kAhead) fetch(blockIdx.x);
+  for (int64_t r0 = (int64_t)blockIdx.x * teams; r0 < p.rows; r0 += step) {
+    // a team past the last row takes the last row and stores nothing: its warp shuffles together
+    const int64_t mine = r0 + (LANES ? threadIdx.x / LANES : 0), r = mine < p.rows ? mine : p.rows - 1;
+    const bool real = mine < p.rows;
+    float h[V][N];
+    const T* x = static_cast<const T*>(p.x) + r * p.sx + t * N;
+    const T* res = static_cast<const T*>(p.res) + (p.res ? r * p.sres + t * N : 0);
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      if (kAhead) {
+        unpack<T>(h[v], x_raw[v]);
+      } else if (v * team + t < nvec) {
+        load_vec<T>(h[v], x + v * v_step);
       } else {
 #pragma unroll
         for (int k = 0; k < N; k++) h[v][k] = 0.0f;
       }
     }
-    if (res) {
+    if (p.res) {
+      T* sum = static_cast<T*>(p.sum) + (p.sum ? r * p.ssum + t * N : 0);
 #pragma unroll
       for (int v = 0; v < V; v++) {
-        const int i = v * TEAM + t;
-        if (i < nvec) {
+        if (v * team + t < nvec) {
           float a[N];
-          load_vec<T>(a, res + i * N);
+          if (kAhead)
+            unpack<T>(a, res_raw[v]);
+          else
+            load_vec<T>(a, res + v * v_step);
 #pragma unroll
-          for (int k = 0; k < N; k++) h[v][k] = to_float(from_float<T>(h[v][k] + a[k]));
-          if (sum) store_vec<T>(sum + i * N, h[v]);
+          for (int k = 0; k < N; k++) a[k] += h[v][k];
+          const uint4 packed = pack<T>(a);  // the norm is that of the sum as stored
+          unpack<T>(h[v], packed);
+          if (p.sum && real) *reinterpret_cast<uint4*>(sum + v * v_step) = packed;
         }
       }
     }
+    if (kAhead && r0 + step < p.rows) fetch(r0 + step);
+    float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; v++)
 #pragma unroll
-      for (int k = 0; k < N; k++) s += h[v][k];
-    const float mean = (TEAM == 32 ? warp_sum(s) : block_sum2(s, 0.0f, red[0]).x) / (float)p.H;
+      for (int k = 0; k < N; k++) s += h[v][k];  // 0 past the end
+    const float mean = total(s, red[0]) / (float)p.H;
     float q = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      const bool in = v * TEAM + t < nvec;
+      if (v * team + t < nvec) {
 #pragma unroll
-      for (int k = 0; k < N; k++) {
-        h[v][k] -= mean;
-        if (in) q = fmaf(h[v][k], h[v][k], q);
+        for (int k = 0; k < N; k++) {
+          h[v][k] -= mean;
+          q = fmaf(h[v][k], h[v][k], q);
+        }
       }
     }
-    const float var = (TEAM == 32 ? warp_sum(q) : block_sum2(q, 0.0f, red[1]).x) / (float)p.H;
-    const float rstd = 1.0f / sqrtf(var + p.eps);
+    const float rstd = 1.0f / sqrtf(total(q, red[1]) / (float)p.H + p.eps);
+    T* y = static_cast<T*>(p.y) + r * p.sy + t * N;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      const int i = v * TEAM + t;
-      if (i < nvec) {
-        float g[N];
+      if (v * team + t < nvec && real) {
+        float g[N], c[N];
 #pragma unroll
-        for (int k = 0; k < N; k++) h[v][k] *= rstd;
-        if (w) {
-          load_params<T, P>(g, w + i * N);
+        for (int k = 0; k < N; k++) g[k] = 1.0f, c[k] = 0.0f;
+        if (w) load_params<T, P>(g, w + t * N + v * v_step);
+        if (b) load_params<T, P>(c, b + t * N + v * v_step);
 #pragma unroll
-          for (int k = 0; k < N; k++) h[v][k] *= g[k];
-        }
-        if (b) {
-          load_params<T, P>(g, b + i * N);
-#pragma unroll
-          for (int k = 0; k < N; k++) h[v][k] += g[k];
-        }
-        store_vec<T>(y + i * N, h[v]);
+        for (int k = 0; k < N; k++) g[k] = fmaf(h[v][k] * rstd, g[k], c[k]);
+        *reinterpret_cast<uint4*>(y + v * v_step) = pack<T>(g);
       }
     }
-    if (t == 0) {
+    if (t == 0 && real) {
       if (p.mean) p.mean[r] = mean;
       if (p.rstd) p.rstd[r] = rstd;
     }
@@ -297,11 +352,20 @@ MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, 
 // Rows of 16-byte vectors: one pass that forms gx and a CTA's partial sums of
 // gw and gb.  A team of threads takes a row, V vectors a thread, and keeps the
 // sums of its columns in registers over the rows it meets; its next rows are on
-// their way into a ring of kStages that is each thread's own, so that only the
-// two sums of a row need a barrier.
+// their way into a ring of STAGES that is each thread's own, so that only the
+// two sums of a row need a barrier.  What bounds it is the instructions a row
+// takes: places in the ring are constants, addresses run along, vectors past the
+// end are zeros in the ring and computed with the rest, and the weights stay in
+// registers.  Behind the barrier gy and h are read from the ring again where
+// registers cannot hold them.
+constexpr int kBwdBlock = 512;
+
 template <typename T, typename P, int V, int STAGES>
-__global__ void __launch_bounds__(1024, 1) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
+__global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
   constexpr int N = Vec<T>::kN;
+  constexpr bool kAgain = V * N > 16;  // u, xhat and the weights leave no registers
+  // ring: [stage][matrix][vector of the thread][thread]
+  constexpr int kVec = kBwdBlock * 16, kMatrix = V * kVec, kStage = 3 * kMatrix;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 red[2][32];
   const int team = threadIdx.x / team_threads, teams = blockDim.x / team_threads, t = threadIdx.x % team_threads;
@@ -309,92 +373,118 @@ __global__ void __launch_bounds__(1024, 1) layer_norm_bwd_vec_kernel(NormBwdPara
   const int nvec = (int)(p.H / N);
   const int64_t step = (int64_t)gridDim.x * teams;
   const int64_t first = (int64_t)blockIdx.x * teams + team;
-  const P* w = static_cast<const P*>(p.w);
-  // ring: [stage][matrix][vector of the thread][thread]
-  const uint32_t own = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-  const int matrices = p.gsum ? 3 : 2;
-  const int vec_bytes = blockDim.x * 16, matrix_bytes = V * vec_bytes, stage_bytes = matrices * matrix_bytes;
-
-  auto fill = [&](int64_t r, int stage) {
-    if (r < p.rows) {
-      const T* gy = static_cast<const T*>(p.gy) + r * p.sgy;
-      const T* h = static_cast<const T*>(p.h) + r * p.sh;
-      const T* gs = static_cast<const T*>(p.gsum) + r * p.sgsum;
-      const uint32_t dst = own + stage * stage_bytes;
-#pragma unroll
-      for (int v = 0; v < V; v++) {
-        const int i = v * team_threads + t;
-        if (i < nvec) {
-          cp_async16(dst + v * vec_bytes, gy + i * N);
-          cp_async16(dst + matrix_bytes + v * vec_bytes, h + i * N);
-          if (p.gsum) cp_async16(dst + 2 * matrix_bytes + v * vec_bytes, gs + i * N);
-        }
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto staged = [&](int stage, int matrix, int v, float(&out)[N]) {
-    load_vec<T>(out, reinterpret_cast<const T*>(smem + threadIdx.x * 16 + stage * stage_bytes + matrix * matrix_bytes +
-                                                v * vec_bytes));
-  };
-
-  float wv[V][N], aw[V][N] = {}, ab[V][N] = {};
+  const int rounds = first < p.rows ? (int)((p.rows - first + step - 1) / step) : 0;  // rows of this team
+  const float inv_h = 1.0f / (float)p.H;
+  uint8_t* own = smem + threadIdx.x * 16;
+  const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
+  const int v_step = team_threads * N;
+  bool in[V];
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    const int i = v * team_threads + t;
+    in[v] = v * team_threads + t < nvec;
+    if (!in[v])
+      for (int i = 0; i < 3 * STAGES; i++) *reinterpret_cast<uint4*>(own + i * kMatrix + v * kVec) = make_uint4(0, 0, 0, 0);
+  }
+
+  // where this thread's next copies come from, and where its results go
+  const T* gy = static_cast<const T*>(p.gy) + first * p.sgy + t * N;
+  const T* h = static_cast<const T*>(p.h) + first * p.sh + t * N;
+  const T* gs = static_cast<const T*>(p.gsum) + (p.gsum ? first * p.sgsum + t * N : 0);
+  T* gx = static_cast<T*>(p.gx) + first * p.sgx + t * N;
+  const float *mean_at = p.mean + first, *rstd_at = p.rstd + first;
+  const int64_t gy_step = step * p.sgy, h_step = step * p.sh, gs_step = step * p.sgsum, gx_step = step * p.sgx;
+  int to_fill = rounds;
+  auto fill = [&](uint32_t dst) {
+    if (to_fill > 0) {
+#pragma unroll
+      for (int v = 0; v < V; v++) {
+        if (in[v]) {
+          cp_async16(dst + v * kVec, gy + v * v_step);
+          cp_async16(dst + kMatrix + v * kVec, h + v * v_step);
+          if (p.gsum) cp_async16(dst + 2 * kMatrix + v * kVec, gs + v * v_step);
+        }
+      }
+      gy += gy_step;
+      h += h_step;
+      gs += gs_step;
+    }
+    to_fill--;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  float aw[V][N] = {}, ab[V][N] = {};
+  const P* w = static_cast<const P*>(p.w) + (p.w ? t * N : 0);
+  float wv[V][N];
+#pragma unroll
+  for (int v = 0; v < V; v++) {
 #pragma unroll
     for (int k = 0; k < N; k++) wv[v][k] = 1.0f;
-    if (w && i < nvec) load_params<T, P>(wv[v], w + i * N);
+    if (!kAgain && p.w && in[v]) load_params<T, P>(wv[v], w + v * v_step);
   }
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; i++) fill(first + i * step, i);
+  for (int i = 0; i < STAGES - 1; i++) fill(own_u32 + i * kStage);
   float mean = 0.0f, rstd = 0.0f;
-  if (first < p.rows) mean = p.mean[first], rstd = p.rstd[first];
-  int stage = 0, phase = 0;
-  for (int64_t r = first; r < p.rows; r += step) {
+  if (rounds > 0) mean = *mean_at, rstd = *rstd_at;
+  int stage = 0, phase = 0;  // stage: in bytes
+  for (int left = rounds; left > 0; left--) {
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-    fill(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);  // the stage of the row before
+    fill(own_u32 + (stage == 0 ? (STAGES - 1) * kStage : stage - kStage));  // the stage of the row before
+    mean_at += step;
+    rstd_at += step;
     float next_mean = 0.0f, next_rstd = 0.0f;
-    if (r + step < p.rows) next_mean = p.mean[r + step], next_rstd = p.rstd[r + step];
+    if (left > 1) next_mean = *mean_at, next_rstd = *rstd_at;
+    const uint8_t* at = own + stage;
     float su = 0.0f, sx = 0.0f;
     float u[V][N], xhat[V][N];
+    auto staged = [&](int matrix, int v) {
+      return *reinterpret_cast<const uint4*>(at + matrix * kMatrix + v * kVec);
+    };
+    // u = gy w and xhat of vector v
+    auto form = [&](int v) {
+      unpack<T>(u[v], staged(0, v));
+      unpack<T>(xhat[v], staged(1, v));
+#pragma unroll
+      for (int k = 0; k < N; k++) xhat[v][k] = (xhat[v][k] - mean) * rstd;
+    };
+    auto weigh = [&](int v) {
+      if (kAgain && p.w && in[v]) load_params<T, P>(wv[v], w + v * v_step);
+#pragma unroll
+      for (int k = 0; k < N; k++) u[v][k] *= wv[v][k];
+    };
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      if (v * team_threads + t >= nvec) continue;
-      staged(stage, 0, v, u[v]);
-      staged(stage, 1, v, xhat[v]);
+      form(v);
 #pragma unroll
       for (int k = 0; k < N; k++) {
-        xhat[v][k] = (xhat[v][k] - mean) * rstd;
         aw[v][k] = fmaf(u[v][k], xhat[v][k], aw[v][k]);
         ab[v][k] += u[v][k];
-        u[v][k] *= wv[v][k];
+      }
+      weigh(v);
+#pragma unroll
+      for (int k = 0; k < N; k++) {
         su += u[v][k];
         sx = fmaf(u[v][k], xhat[v][k], sx);
       }
     }
     const float2 sums = team_sum2(su, sx, red[phase] + team * warps, warp, warps, team + 1);
-    const float mu = sums.x / (float)p.H, mx = sums.y / (float)p.H;
-    T* gx = static_cast<T*>(p.gx) + r * p.sgx;
+    const float mu = sums.x * inv_h, mx = sums.y * inv_h;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      const int i = v * team_threads + t;
-      if (i >= nvec) continue;
-      float o[N];
-#pragma unroll
-      for (int k = 0; k < N; k++) o[k] = rstd * (u[v][k] - mu - xhat[v][k] * mx);
-      if (p.gsum) {
-        float g[N];
-        staged(stage, 2, v, g);
-#pragma unroll
-        for (int k = 0; k < N; k++) o[k] += g[k];
+      if (kAgain) {
+        form(v);
+        weigh(v);
       }
-      store_vec<T>(gx + i * N, o);
+      float o[N];
+      unpack<T>(o, p.gsum ? staged(2, v) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+      for (int k = 0; k < N; k++) o[k] = fmaf(rstd, fmaf(-mx, xhat[v][k], u[v][k] - mu), o[k]);
+      if (in[v]) *reinterpret_cast<uint4*>(gx + v * v_step) = pack<T>(o);
     }
+    gx += gx_step;
     mean = next_mean;
     rstd = next_rstd;
     phase ^= 1;
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    stage = stage == (STAGES - 1) * kStage ? 0 : stage + kStage;
   }
   if (!p.gw && !p.gb) return;
 
@@ -464,11 +554,12 @@ bool vector_rows(const void* p, int64_t stride, int64_t rows, int bytes) {
   return aligned16(p) && (rows <= 1 || stride * bytes % 16 == 0);
 }
 
-template <typename T, typename P, int V, int TEAM>
+template <typename T, typename P, int LANES, int THREADS, int V = 4>
 void run_vec(const NormParams& p, cudaStream_t st) {
-  constexpr int kTeams = TEAM == 32 ? kThreads / 32 : 1, kBlock = TEAM == 32 ? kThreads : TEAM;
-  const int64_t blocks = (p.rows + kTeams - 1) / kTeams, cap = (int64_t)device_sm_count() * (2048 / kBlock);
-  layer_norm_vec_kernel<T, P, V, TEAM><<<(unsigned)(blocks < cap ? blocks : cap), kBlock, 0, st>>>(p);
+  const int nvec = (int)(p.H * sizeof(T) / 16);
+  const int block = LANES ? THREADS : ((nvec + V - 1) / V + 31) / 32 * 32, teams = LANES ? THREADS / (LANES + !LANES) : 1;
+  const int64_t blocks = (p.rows + teams - 1) / teams, cap = (int64_t)device_sm_count() * (2048 / block);
+  layer_norm_vec_kernel<T, P, V, LANES, THREADS><<<(unsigned)(blocks < cap ? blocks : cap), block, 0, st>>>(p);
 }
 
 template <typename T, typename P>
@@ -480,44 +571,43 @@ cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
                    aligned16(p.b);
   if (!vec || nvec > 4096)
     layer_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
+  else if (nvec <= 16)
+    run_vec<T, P, 4, 256>(p, st);
   else if (nvec <= 32)
-    run_vec<T, P, 1, 32>(p, st);
+    run_vec<T, P, 8, 256>(p, st);
   else if (nvec <= 64)
-    run_vec<T, P, 2, 32>(p, st);
+    run_vec<T, P, 16, 256>(p, st);
   else if (nvec <= 128)
-    run_vec<T, P, 4, 32>(p, st);
-  else if (nvec <= 256)
-    run_vec<T, P, 2, 128>(p, st);
-  else if (nvec <= 512)
-    run_vec<T, P, 2, 256>(p, st);
+    run_vec<T, P, 32, 256>(p, st);
   else if (nvec <= 1024)
-    run_vec<T, P, 2, 512>(p, st);
+    run_vec<T, P, 0, 512, 2>(p, st);
   else if (nvec <= 2048)
-    run_vec<T, P, 2, 1024>(p, st);
+    run_vec<T, P, 0, 1024, 2>(p, st);
   else
-    run_vec<T, P, 4, 1024>(p, st);
+    run_vec<T, P, 0, 1024, 4>(p, st);
   return cudaGetLastError();
 }
 
 template <typename T, typename P, int V, int STAGES>
 cudaError_t run_bwd_vec(NormBwdParams p, cudaStream_t st) {
+  constexpr int kBlock = kBwdBlock, kRing = kBlock * 16 * 3 * V * STAGES;
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
     return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, V, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                1024 * 16 * 3 * V * STAGES);
+                                kRing);
   });
   if (e != cudaSuccess) return e;
   const int nvec = (int)(p.H * sizeof(T) / 16);
   const int team = ((nvec + V - 1) / V + 31) / 32 * 32;
-  int teams = 1024 / team < 15 ? 1024 / team : 15;  // named barriers 1 to 15
+  int teams = kBlock / team < 15 ? kBlock / team : 15;  // named barriers 1 to 15
   while (teams > 1 && p.rows < (int64_t)teams * device_sm_count()) teams--;
   const int64_t blocks = (p.rows + teams - 1) / teams, sms = device_sm_count();
   p.chunks = blocks < sms ? blocks : sms;
   if (p.chunks > kMaxChunks) p.chunks = kMaxChunks;
   const int block = team * teams;
-  const int ring = block * 16 * (p.gsum ? 3 : 2) * V * STAGES, part = block * 16 / (int)sizeof(T) * 4 * V;
+  static_assert(kRing >= kBlock * 16 / (int)sizeof(T) * 4 * V, "the partial sums fit the ring");
   p.pb = p.pw + p.chunks * p.H;
-  layer_norm_bwd_vec_kernel<T, P, V, STAGES><<<(unsigned)p.chunks, block, ring > part ? ring : part, st>>>(p, team);
+  layer_norm_bwd_vec_kernel<T, P, V, STAGES><<<(unsigned)p.chunks, block, kRing, st>>>(p, team);
   if (p.gw || p.gb) layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
@@ -529,8 +619,8 @@ cudaError_t run_backward(NormBwdParams p, cudaStream_t st) {
   const bool vec = p.rows > 0 && p.H * b % 16 == 0 && vector_rows(p.gy, p.sgy, p.rows, b) &&
                    vector_rows(p.h, p.sh, p.rows, b) && vector_rows(p.gsum, p.sgsum, p.rows, b) &&
                    vector_rows(p.gx, p.sgx, p.rows, b) && aligned16(p.w);
-  if (vec && nvec <= 1024) return run_bwd_vec<T, P, 1, 4>(p, st);
-  if (vec && nvec <= 2048) return run_bwd_vec<T, P, 2, 2>(p, st);
+  if (vec && nvec <= 1024) return run_bwd_vec<T, P, 2, 4>(p, st);
+  if (vec && nvec <= 2048) return run_bwd_vec<T, P, 4, 2>(p, st);
   p.chunks = bwd_chunks(p.rows);
   p.rows_per_chunk = (p.rows + p.chunks - 1) / p.chunks;
   p.pb = p.pw + p.chunks * p.H;
