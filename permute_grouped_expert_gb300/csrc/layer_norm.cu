@@ -330,7 +330,15 @@ MOE_DEVICE void cp_async16(uint32_t dst, const void* src) {
 // Sums of two values over a team of `warps` warps, known to its threads; one
 // barrier.  Halves of a warp reduce one value each.  `red`: a float2 per warp,
 // not written again before the team's next barrier but one.
-MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, int barrier) {
+template <bool PART>
+MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, int barrier, int threads) {
+  if (PART) {  // `threads` lanes, a power of two: the teams of a warp at once
+    for (int d = threads >> 1; d >= 1; d >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, d);
+      b += __shfl_xor_sync(0xffffffffu, b, d);
+    }
+    return make_float2(a, b);
+  }
   const int lane = threadIdx.x & 31;
   const bool low = lane < 16;
   auto halves = [&](float x, float y) {  // lanes 0-15: sum of x over the warp, 16-31: of y
@@ -360,7 +368,7 @@ MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, 
 // registers cannot hold them.
 constexpr int kBwdBlock = 512;
 
-template <typename T, typename P, int V, int STAGES>
+template <typename T, typename P, int V, int STAGES, bool PART>
 __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
   constexpr int N = Vec<T>::kN;
   constexpr bool kAgain = V * N > 16;  // u, xhat and the weights leave no registers
@@ -374,6 +382,9 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   const int64_t step = (int64_t)gridDim.x * teams;
   const int64_t first = (int64_t)blockIdx.x * teams + team;
   const int rounds = first < p.rows ? (int)((p.rows - first + step - 1) / step) : 0;  // rows of this team
+  // PART: teams of a part of a warp shuffle together: they go as many rounds as
+  // the first, and their rounds past the last row are zeros in the ring
+  const int loops = PART ? (int)((p.rows - (first - team) + step - 1) / step) : rounds;
   const float inv_h = 1.0f / (float)p.H;
   uint8_t* own = smem + threadIdx.x * 16;
   const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
@@ -407,6 +418,10 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
       gy += gy_step;
       h += h_step;
       gs += gs_step;
+    } else if (PART) {
+#pragma unroll
+      for (int i = 0; i < 3 * V; i++)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * kVec), "r"(0) : "memory");
     }
     to_fill--;
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -426,13 +441,13 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   float mean = 0.0f, rstd = 0.0f;
   if (rounds > 0) mean = *mean_at, rstd = *rstd_at;
   int stage = 0, phase = 0;  // stage: in bytes
-  for (int left = rounds; left > 0; left--) {
+  for (int round = 0; round < loops; round++) {
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
     fill(own_u32 + (stage == 0 ? (STAGES - 1) * kStage : stage - kStage));  // the stage of the row before
     mean_at += step;
     rstd_at += step;
     float next_mean = 0.0f, next_rstd = 0.0f;
-    if (left > 1) next_mean = *mean_at, next_rstd = *rstd_at;
+    if (round + 1 < rounds) next_mean = *mean_at, next_rstd = *rstd_at;
     const uint8_t* at = own + stage;
     float su = 0.0f, sx = 0.0f;
     float u[V][N], xhat[V][N];
@@ -466,7 +481,7 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
         sx = fmaf(u[v][k], xhat[v][k], sx);
       }
     }
-    const float2 sums = team_sum2(su, sx, red[phase] + team * warps, warp, warps, team + 1);
+    const float2 sums = team_sum2<PART>(su, sx, red[phase] + team * warps, warp, warps, team + 1, team_threads);
     const float mu = sums.x * inv_h, mx = sums.y * inv_h;
 #pragma unroll
     for (int v = 0; v < V; v++) {
@@ -478,7 +493,7 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
       unpack<T>(o, p.gsum ? staged(2, v) : make_uint4(0, 0, 0, 0));
 #pragma unroll
       for (int k = 0; k < N; k++) o[k] = fmaf(rstd, fmaf(-mx, xhat[v][k], u[v][k] - mu), o[k]);
-      if (in[v]) *reinterpret_cast<uint4*>(gx + v * v_step) = pack<T>(o);
+      if (in[v] && (!PART || round < rounds)) *reinterpret_cast<uint4*>(gx + v * v_step) = pack<T>(o);
     }
     gx += gx_step;
     mean = next_mean;
@@ -493,19 +508,29 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int sum = 0; sum < 2; sum++) {
-    __syncthreads();
+    float(&acc)[V][N] = sum ? ab : aw;
+    if (teams > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; v++)
+#pragma unroll
+        for (int k = 0; k < N; k++) part[(v * N + k) * kBwdBlock + threadIdx.x] = acc[v][k];
+      __syncthreads();
+      if (team == 0)
+        for (int j = 1; j < teams; j++)
+#pragma unroll
+          for (int v = 0; v < V; v++)
+#pragma unroll
+            for (int k = 0; k < N; k++) acc[v][k] += part[(v * N + k) * kBwdBlock + j * team_threads + t];
+    }
+    float* out = (sum ? p.pb : p.pw) + blockIdx.x * p.H + t * N;
 #pragma unroll
     for (int v = 0; v < V; v++)
+      if (team == 0 && in[v])
 #pragma unroll
-      for (int k = 0; k < N; k++) part[(v * N + k) * blockDim.x + threadIdx.x] = sum ? ab[v][k] : aw[v][k];
-    __syncthreads();
-    float* out = (sum ? p.pb : p.pw) + blockIdx.x * p.H;
-    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
-      const int i = c / N, at = (i / team_threads * N + c % N) * blockDim.x + i % team_threads;
-      float s = 0.0f;
-      for (int k = 0; k < teams; k++) s += part[at + k * team_threads];
-      out[c] = s;
-    }
+        for (int k = 0; k < N; k += 4)
+          *reinterpret_cast<float4*>(out + v * v_step + k) =
+              make_float4(acc[v][k], acc[v][k + 1], acc[v][k + 2], acc[v][k + 3]);
   }
 }
 
@@ -588,26 +613,27 @@ cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T, typename P, int V, int STAGES>
+template <typename T, typename P, int V, int STAGES, bool PART>
 cudaError_t run_bwd_vec(NormBwdParams p, cudaStream_t st) {
   constexpr int kBlock = kBwdBlock, kRing = kBlock * 16 * 3 * V * STAGES;
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, V, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kRing);
   });
   if (e != cudaSuccess) return e;
   const int nvec = (int)(p.H * sizeof(T) / 16);
-  const int team = ((nvec + V - 1) / V + 31) / 32 * 32;
-  int teams = kBlock / team < 15 ? kBlock / team : 15;  // named barriers 1 to 15
-  while (teams > 1 && p.rows < (int64_t)teams * device_sm_count()) teams--;
+  const int want = (nvec + V - 1) / V;
+  const int team = !PART ? (want + 31) / 32 * 32 : want <= 4 ? 4 : want <= 8 ? 8 : 16, whole = PART ? 32 / team : 1;
+  int teams = team >= 64 && kBlock / team > 15 ? 15 : kBlock / team;  // named barriers 1 to 15
+  while (teams > whole && p.rows < (int64_t)teams * device_sm_count()) teams -= whole;  // whole warps
   const int64_t blocks = (p.rows + teams - 1) / teams, sms = device_sm_count();
   p.chunks = blocks < sms ? blocks : sms;
   if (p.chunks > kMaxChunks) p.chunks = kMaxChunks;
   const int block = team * teams;
   static_assert(kRing >= kBlock * 16 / (int)sizeof(T) * 4 * V, "the partial sums fit the ring");
   p.pb = p.pw + p.chunks * p.H;
-  layer_norm_bwd_vec_kernel<T, P, V, STAGES><<<(unsigned)p.chunks, block, kRing, st>>>(p, team);
+  layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART><<<(unsigned)p.chunks, block, kRing, st>>>(p, team);
   if (p.gw || p.gb) layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
@@ -619,8 +645,9 @@ cudaError_t run_backward(NormBwdParams p, cudaStream_t st) {
   const bool vec = p.rows > 0 && p.H * b % 16 == 0 && vector_rows(p.gy, p.sgy, p.rows, b) &&
                    vector_rows(p.h, p.sh, p.rows, b) && vector_rows(p.gsum, p.sgsum, p.rows, b) &&
                    vector_rows(p.gx, p.sgx, p.rows, b) && aligned16(p.w);
-  if (vec && nvec <= 1024) return run_bwd_vec<T, P, 2, 4>(p, st);
-  if (vec && nvec <= 2048) return run_bwd_vec<T, P, 4, 2>(p, st);
+  if (vec && nvec <= 32) return run_bwd_vec<T, P, 2, 4, true>(p, st);
+  if (vec && nvec <= 1024) return run_bwd_vec<T, P, 2, 4, false>(p, st);
+  if (vec && nvec <= 2048) return run_bwd_vec<T, P, 4, 2, false>(p, st);
   p.chunks = bwd_chunks(p.rows);
   p.rows_per_chunk = (p.rows + p.chunks - 1) / p.chunks;
   p.pb = p.pw + p.chunks * p.H;
