@@ -140,20 +140,83 @@ MOE_DEVICE uint4 pack(const float (&in)[Vec<T>::kN]) {
   return u.v;
 }
 
+// SHIFTED kernels take rows that start anywhere as the aligned 16-byte pieces
+// that hold them: `skip` elements of a row's first piece lie before it.  A team's
+// rows lie a multiple of 16 bytes apart, so that its threads keep their columns.
+// Bit k: element k of the piece whose first column is c0 belongs to the row.
+template <int N>
+MOE_DEVICE uint32_t piece_mask(int c0, int H) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < N; k++) m |= (c0 + k >= 0 && c0 + k < H ? 1u : 0u) << k;
+  return m;
+}
+
+// A piece with zeros outside the row.
+template <typename T, bool SHIFTED>
+MOE_DEVICE uint4 load_piece(const T* p, uint32_t mask) {
+  constexpr int N = Vec<T>::kN;
+  if (!SHIFTED || mask == (1u << N) - 1) return *reinterpret_cast<const uint4*>(p);
+  union {
+    uint4 v;
+    T e[N];
+  } u;
+  u.v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int k = 0; k < N; k++)
+    if (mask >> k & 1) u.e[k] = p[k];
+  return u.v;
+}
+
+template <typename T, bool SHIFTED>
+MOE_DEVICE void store_piece(T* p, uint4 raw, uint32_t mask) {
+  constexpr int N = Vec<T>::kN;
+  if (!SHIFTED || mask == (1u << N) - 1) {
+    *reinterpret_cast<uint4*>(p) = raw;
+    return;
+  }
+  union {
+    uint4 v;
+    T e[N];
+  } u;
+  u.v = raw;
+#pragma unroll
+  for (int k = 0; k < N; k++)
+    if (mask >> k & 1) p[k] = u.e[k];
+}
+
+// Parameters of a piece's columns; p: of its first.
+template <typename T, typename P, bool SHIFTED>
+MOE_DEVICE void piece_params(float (&out)[Vec<T>::kN], const P* p, uint32_t mask) {
+  if (SHIFTED) {
+#pragma unroll
+    for (int k = 0; k < Vec<T>::kN; k++)
+      if (mask >> k & 1) out[k] = to_float(p[k]);
+  } else {
+    load_params<T, P>(out, p);
+  }
+}
+
 // Rows of 16-byte vectors held in registers between the mean, the variance and
 // the result, so that the row is read once, V vectors a thread.  LANES threads
 // of a warp take a row; or (0) a CTA does, and its next row is on its way while
 // it reduces and writes this one: two barriers a row would leave the memory idle.
-template <typename T, typename P, int V, int LANES, int THREADS>
+template <typename T, typename P, int V, int LANES, int THREADS, bool SHIFTED>
 __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_norm_vec_kernel(NormParams p) {
   constexpr int N = Vec<T>::kN;
   constexpr bool kAhead = LANES == 0;
   __shared__ float2 red[2][THREADS / 32];
-  const P* w = static_cast<const P*>(p.w);
-  const P* b = static_cast<const P*>(p.b);
   const int team = LANES ? LANES : (int)blockDim.x, teams = LANES ? THREADS / LANES : 1;
   const int t = LANES ? threadIdx.x % LANES : threadIdx.x;
-  const int nvec = (int)(p.H / N), v_step = team * N;
+  const int64_t first = (int64_t)blockIdx.x * teams + (LANES ? threadIdx.x / LANES : 0);
+  const int skip = SHIFTED ? (int)(first * p.sx % N) : 0;
+  const int nvec = ((int)p.H + skip + N - 1) / N, v_step = team * N;
+  const int c0 = t * N - skip;  // this thread's first column
+  uint32_t mask[V];             // of its pieces
+#pragma unroll
+  for (int v = 0; v < V; v++) mask[v] = SHIFTED ? piece_mask<N>(c0 + v * v_step, (int)p.H) : ~0u;
+  const P* w = static_cast<const P*>(p.w) + (p.w ? c0 : 0);
+  const P* b = static_cast<const P*>(p.b) + (p.b ? c0 : 0);
   auto total = [&](float v, float2* r) {
     if (!LANES) return block_sum2(v, 0.0f, r).x;
 #pragma unroll
@@ -162,54 +225,51 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
   };
   uint4 x_raw[V], res_raw[V];
   auto fetch = [&](int64_t r) {
-    const T* x = static_cast<const T*>(p.x) + r * p.sx + t * N;
+    const T* x = static_cast<const T*>(p.x) + r * p.sx + c0;
 #pragma unroll
     for (int v = 0; v < V; v++) {
       x_raw[v] = make_uint4(0, 0, 0, 0);
-      if (v * team + t < nvec) x_raw[v] = *reinterpret_cast<const uint4*>(x + v * v_step);
+      if (v * team + t < nvec) x_raw[v] = load_piece<T, SHIFTED>(x + v * v_step, mask[v]);
     }
     if (p.res) {
-      const T* res = static_cast<const T*>(p.res) + r * p.sres + t * N;
+      const T* res = static_cast<const T*>(p.res) + r * p.sres + c0;
 #pragma unroll
       for (int v = 0; v < V; v++)
-        if (v * team + t < nvec) res_raw[v] = *reinterpret_cast<const uint4*>(res + v * v_step);
+        if (v * team + t < nvec) res_raw[v] = load_piece<T, SHIFTED>(res + v * v_step, mask[v]);
     }
   };
   const int64_t step = (int64_t)gridDim.x * teams;
   if (kAhead) fetch(blockIdx.x);
   for (int64_t r0 = (int64_t)blockIdx.x * teams; r0 < p.rows; r0 += step) {
-    // a team past the last row takes the last row and stores nothing: its warp shuffles together
-    const int64_t mine = r0 + (LANES ? threadIdx.x / LANES : 0), r = mine < p.rows ? mine : p.rows - 1;
-    const bool real = mine < p.rows;
+    // a team past the last row has no columns: its warp shuffles together
+    const int64_t r = r0 + (LANES ? threadIdx.x / LANES : 0);
+    const int n = r < p.rows ? nvec : 0;
     float h[V][N];
-    const T* x = static_cast<const T*>(p.x) + r * p.sx + t * N;
-    const T* res = static_cast<const T*>(p.res) + (p.res ? r * p.sres + t * N : 0);
+    const T* x = static_cast<const T*>(p.x) + r * p.sx + c0;
+    const T* res = static_cast<const T*>(p.res) + (p.res ? r * p.sres + c0 : 0);
 #pragma unroll
     for (int v = 0; v < V; v++) {
       if (kAhead) {
         unpack<T>(h[v], x_raw[v]);
-      } else if (v * team + t < nvec) {
-        load_vec<T>(h[v], x + v * v_step);
+      } else if (v * team + t < n) {
+        unpack<T>(h[v], load_piece<T, SHIFTED>(x + v * v_step, mask[v]));
       } else {
 #pragma unroll
         for (int k = 0; k < N; k++) h[v][k] = 0.0f;
       }
     }
     if (p.res) {
-      T* sum = static_cast<T*>(p.sum) + (p.sum ? r * p.ssum + t * N : 0);
+      T* sum = static_cast<T*>(p.sum) + (p.sum ? r * p.ssum + c0 : 0);
 #pragma unroll
       for (int v = 0; v < V; v++) {
-        if (v * team + t < nvec) {
+        if (v * team + t < n) {
           float a[N];
-          if (kAhead)
-            unpack<T>(a, res_raw[v]);
-          else
-            load_vec<T>(a, res + v * v_step);
+          unpack<T>(a, kAhead ? res_raw[v] : load_piece<T, SHIFTED>(res + v * v_step, mask[v]));
 #pragma unroll
           for (int k = 0; k < N; k++) a[k] += h[v][k];
           const uint4 packed = pack<T>(a);  // the norm is that of the sum as stored
           unpack<T>(h[v], packed);
-          if (p.sum && real) *reinterpret_cast<uint4*>(sum + v * v_step) = packed;
+          if (p.sum) store_piece<T, SHIFTED>(sum + v * v_step, packed, mask[v]);
         }
       }
     }
@@ -218,35 +278,36 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
 #pragma unroll
     for (int v = 0; v < V; v++)
 #pragma unroll
-      for (int k = 0; k < N; k++) s += h[v][k];  // 0 past the end
+      for (int k = 0; k < N; k++) s += h[v][k];  // 0 outside the row
     const float mean = total(s, red[0]) / (float)p.H;
     float q = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      if (v * team + t < nvec) {
+      if (v * team + t < n) {
 #pragma unroll
         for (int k = 0; k < N; k++) {
           h[v][k] -= mean;
+          if (SHIFTED) h[v][k] = mask[v] >> k & 1 ? h[v][k] : 0.0f;
           q = fmaf(h[v][k], h[v][k], q);
         }
       }
     }
     const float rstd = 1.0f / sqrtf(total(q, red[1]) / (float)p.H + p.eps);
-    T* y = static_cast<T*>(p.y) + r * p.sy + t * N;
+    T* y = static_cast<T*>(p.y) + r * p.sy + c0;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      if (v * team + t < nvec && real) {
+      if (v * team + t < n) {
         float g[N], c[N];
 #pragma unroll
         for (int k = 0; k < N; k++) g[k] = 1.0f, c[k] = 0.0f;
-        if (w) load_params<T, P>(g, w + t * N + v * v_step);
-        if (b) load_params<T, P>(c, b + t * N + v * v_step);
+        if (p.w) piece_params<T, P, SHIFTED>(g, w + v * v_step, mask[v]);
+        if (p.b) piece_params<T, P, SHIFTED>(c, b + v * v_step, mask[v]);
 #pragma unroll
         for (int k = 0; k < N; k++) g[k] = fmaf(h[v][k] * rstd, g[k], c[k]);
-        *reinterpret_cast<uint4*>(y + v * v_step) = pack<T>(g);
+        store_piece<T, SHIFTED>(y + v * v_step, pack<T>(g), mask[v]);
       }
     }
-    if (t == 0 && real) {
+    if (t == 0 && r < p.rows) {
       if (p.mean) p.mean[r] = mean;
       if (p.rstd) p.rstd[r] = rstd;
     }
@@ -323,8 +384,9 @@ __global__ void __launch_bounds__(kThreads) layer_norm_bwd_cols_kernel(NormBwdPa
   }
 }
 
-MOE_DEVICE void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// The first `bytes` of a piece, zeros behind them.
+MOE_DEVICE void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 // Sums of two values over a team of `warps` warps, known to its threads; one
@@ -368,7 +430,7 @@ MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, 
 // registers cannot hold them.
 constexpr int kBwdBlock = 512;
 
-template <typename T, typename P, int V, int STAGES, bool PART>
+template <typename T, typename P, int V, int STAGES, bool PART, bool SHIFTED>
 __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
   constexpr int N = Vec<T>::kN;
   constexpr bool kAgain = V * N > 16;  // u, xhat and the weights leave no registers
@@ -378,9 +440,10 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   __shared__ float2 red[2][32];
   const int team = threadIdx.x / team_threads, teams = blockDim.x / team_threads, t = threadIdx.x % team_threads;
   const int warp = t >> 5, warps = team_threads >> 5;
-  const int nvec = (int)(p.H / N);
   const int64_t step = (int64_t)gridDim.x * teams;
   const int64_t first = (int64_t)blockIdx.x * teams + team;
+  const int skip = SHIFTED ? (int)(first * p.sgy % N) : 0;
+  const int nvec = ((int)p.H + skip + N - 1) / N, c0 = t * N - skip;  // this thread's first column
   const int rounds = first < p.rows ? (int)((p.rows - first + step - 1) / step) : 0;  // rows of this team
   // PART: teams of a part of a warp shuffle together: they go as many rounds as
   // the first, and their rounds past the last row are zeros in the ring
@@ -390,18 +453,20 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
   const int v_step = team_threads * N;
   bool in[V];
+  uint32_t mask[V];  // of this thread's pieces
 #pragma unroll
   for (int v = 0; v < V; v++) {
     in[v] = v * team_threads + t < nvec;
+    mask[v] = SHIFTED ? piece_mask<N>(c0 + v * v_step, (int)p.H) : ~0u;
     if (!in[v])
       for (int i = 0; i < 3 * STAGES; i++) *reinterpret_cast<uint4*>(own + i * kMatrix + v * kVec) = make_uint4(0, 0, 0, 0);
   }
 
   // where this thread's next copies come from, and where its results go
-  const T* gy = static_cast<const T*>(p.gy) + first * p.sgy + t * N;
-  const T* h = static_cast<const T*>(p.h) + first * p.sh + t * N;
-  const T* gs = static_cast<const T*>(p.gsum) + (p.gsum ? first * p.sgsum + t * N : 0);
-  T* gx = static_cast<T*>(p.gx) + first * p.sgx + t * N;
+  const T* gy = static_cast<const T*>(p.gy) + first * p.sgy + c0;
+  const T* h = static_cast<const T*>(p.h) + first * p.sh + c0;
+  const T* gs = static_cast<const T*>(p.gsum) + (p.gsum ? first * p.sgsum + c0 : 0);
+  T* gx = static_cast<T*>(p.gx) + first * p.sgx + c0;
   const float *mean_at = p.mean + first, *rstd_at = p.rstd + first;
   const int64_t gy_step = step * p.sgy, h_step = step * p.sh, gs_step = step * p.sgsum, gx_step = step * p.sgx;
   int to_fill = rounds;
@@ -410,9 +475,11 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
 #pragma unroll
       for (int v = 0; v < V; v++) {
         if (in[v]) {
-          cp_async16(dst + v * kVec, gy + v * v_step);
-          cp_async16(dst + kMatrix + v * kVec, h + v * v_step);
-          if (p.gsum) cp_async16(dst + 2 * kMatrix + v * kVec, gs + v * v_step);
+          // the piece that ends a matrix may be short
+          const int bytes = SHIFTED && to_fill == 1 ? min(16, ((int)p.H - c0 - v * v_step) * (int)sizeof(T)) : 16;
+          cp_async16(dst + v * kVec, gy + v * v_step, bytes);
+          cp_async16(dst + kMatrix + v * kVec, h + v * v_step, bytes);
+          if (p.gsum) cp_async16(dst + 2 * kMatrix + v * kVec, gs + v * v_step, bytes);
         }
       }
       gy += gy_step;
@@ -428,13 +495,13 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   };
 
   float aw[V][N] = {}, ab[V][N] = {};
-  const P* w = static_cast<const P*>(p.w) + (p.w ? t * N : 0);
+  const P* w = static_cast<const P*>(p.w) + (p.w ? c0 : 0);
   float wv[V][N];
 #pragma unroll
   for (int v = 0; v < V; v++) {
 #pragma unroll
     for (int k = 0; k < N; k++) wv[v][k] = 1.0f;
-    if (!kAgain && p.w && in[v]) load_params<T, P>(wv[v], w + v * v_step);
+    if (!kAgain && p.w && in[v]) piece_params<T, P, SHIFTED>(wv[v], w + v * v_step, mask[v]);
   }
 #pragma unroll
   for (int i = 0; i < STAGES - 1; i++) fill(own_u32 + i * kStage);
@@ -460,9 +527,14 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
       unpack<T>(xhat[v], staged(1, v));
 #pragma unroll
       for (int k = 0; k < N; k++) xhat[v][k] = (xhat[v][k] - mean) * rstd;
+      if (SHIFTED && mask[v] != (1u << N) - 1) {  // a neighbour's elements
+#pragma unroll
+        for (int k = 0; k < N; k++)
+          if (!(mask[v] >> k & 1)) u[v][k] = xhat[v][k] = 0.0f;
+      }
     };
     auto weigh = [&](int v) {
-      if (kAgain && p.w && in[v]) load_params<T, P>(wv[v], w + v * v_step);
+      if (kAgain && p.w && in[v]) piece_params<T, P, SHIFTED>(wv[v], w + v * v_step, mask[v]);
 #pragma unroll
       for (int k = 0; k < N; k++) u[v][k] *= wv[v][k];
     };
@@ -493,7 +565,7 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
       unpack<T>(o, p.gsum ? staged(2, v) : make_uint4(0, 0, 0, 0));
 #pragma unroll
       for (int k = 0; k < N; k++) o[k] = fmaf(rstd, fmaf(-mx, xhat[v][k], u[v][k] - mu), o[k]);
-      if (in[v] && (!PART || round < rounds)) *reinterpret_cast<uint4*>(gx + v * v_step) = pack<T>(o);
+      if (in[v] && (!PART || round < rounds)) store_piece<T, SHIFTED>(gx + v * v_step, pack<T>(o), mask[v]);
     }
     gx += gx_step;
     mean = next_mean;
@@ -509,6 +581,21 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
 #pragma unroll
   for (int sum = 0; sum < 2; sum++) {
     float(&acc)[V][N] = sum ? ab : aw;
+    if (SHIFTED) {  // by column: the teams' pieces begin at different ones
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; v++)
+#pragma unroll
+        for (int k = 0; k < N; k++)
+          if (in[v] && mask[v] >> k & 1) part[team * (int)p.H + c0 + v * v_step + k] = acc[v][k];
+      __syncthreads();
+      for (int c = threadIdx.x; c < (int)p.H; c += blockDim.x) {
+        float s = part[c];
+        for (int j = 1; j < teams; j++) s += part[j * (int)p.H + c];
+        (sum ? p.pb : p.pw)[blockIdx.x * p.H + c] = s;
+      }
+      continue;
+    }
     if (teams > 1) {
       __syncthreads();
 #pragma unroll
@@ -579,75 +666,104 @@ bool vector_rows(const void* p, int64_t stride, int64_t rows, int bytes) {
   return aligned16(p) && (rows <= 1 || stride * bytes % 16 == 0);
 }
 
-template <typename T, typename P, int LANES, int THREADS, int V = 4>
+// Rows that start on pieces' elements alike: what the SHIFTED kernels take.
+bool alike(const void* p, int64_t stride, int64_t other, int64_t rows, int n) {
+  return !p || (aligned16(p) && (rows <= 1 || stride % n == other % n));
+}
+
+// CTAs that keep a team's rows a multiple of 16 bytes apart, unless each team has one row.
+int64_t shifted_grid(int64_t grid, int64_t blocks) { return blocks > grid && grid >= 8 ? grid / 8 * 8 : grid; }
+
+template <typename T, typename P, bool SHIFTED, int LANES, int THREADS, int V = 4>
 void run_vec(const NormParams& p, cudaStream_t st) {
-  const int nvec = (int)(p.H * sizeof(T) / 16);
-  const int block = LANES ? THREADS : ((nvec + V - 1) / V + 31) / 32 * 32, teams = LANES ? THREADS / (LANES + !LANES) : 1;
+  const int n = 16 / (int)sizeof(T), pieces = (int)(p.H + (SHIFTED ? n - 1 : 0) + n - 1) / n;
+  const int block = LANES ? THREADS : ((pieces + V - 1) / V + 31) / 32 * 32;
+  const int teams = LANES ? THREADS / (LANES + !LANES) : 1;
   const int64_t blocks = (p.rows + teams - 1) / teams, cap = (int64_t)device_sm_count() * (2048 / block);
-  layer_norm_vec_kernel<T, P, V, LANES, THREADS><<<(unsigned)(blocks < cap ? blocks : cap), block, 0, st>>>(p);
+  const int64_t grid = blocks < cap ? blocks : cap;
+  layer_norm_vec_kernel<T, P, V, LANES, THREADS, SHIFTED>
+      <<<(unsigned)(SHIFTED ? shifted_grid(grid, blocks) : grid), block, 0, st>>>(p);
+}
+
+template <typename T, typename P, bool SHIFTED>
+void run_pieces(const NormParams& p, int64_t pieces, cudaStream_t st) {
+  if (pieces <= 16)
+    run_vec<T, P, SHIFTED, 4, 256>(p, st);
+  else if (pieces <= 32)
+    run_vec<T, P, SHIFTED, 8, 256>(p, st);
+  else if (pieces <= 64)
+    run_vec<T, P, SHIFTED, 16, 256>(p, st);
+  else if (pieces <= 128)
+    run_vec<T, P, SHIFTED, 32, 256>(p, st);
+  else if (pieces <= 1024)
+    run_vec<T, P, SHIFTED, 0, 512, 2>(p, st);
+  else if (pieces <= 2048)
+    run_vec<T, P, SHIFTED, 0, 1024, 2>(p, st);
+  else
+    run_vec<T, P, SHIFTED, 0, 1024, 4>(p, st);
 }
 
 template <typename T, typename P>
 cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
-  const int b = sizeof(T);
-  const int64_t nvec = p.H * b / 16;
+  const int b = sizeof(T), n = 16 / b;
+  const int64_t pieces = (p.H + n - 1) / n;
   const bool vec = p.H * b % 16 == 0 && vector_rows(p.x, p.sx, p.rows, b) && vector_rows(p.res, p.sres, p.rows, b) &&
                    vector_rows(p.sum, p.ssum, p.rows, b) && vector_rows(p.y, p.sy, p.rows, b) && aligned16(p.w) &&
                    aligned16(p.b);
-  if (!vec || nvec > 4096)
-    layer_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
-  else if (nvec <= 16)
-    run_vec<T, P, 4, 256>(p, st);
-  else if (nvec <= 32)
-    run_vec<T, P, 8, 256>(p, st);
-  else if (nvec <= 64)
-    run_vec<T, P, 16, 256>(p, st);
-  else if (nvec <= 128)
-    run_vec<T, P, 32, 256>(p, st);
-  else if (nvec <= 1024)
-    run_vec<T, P, 0, 512, 2>(p, st);
-  else if (nvec <= 2048)
-    run_vec<T, P, 0, 1024, 2>(p, st);
+  const bool shifted = aligned16(p.x) && alike(p.res, p.sres, p.sx, p.rows, n) &&
+                       alike(p.sum, p.ssum, p.sx, p.rows, n) && alike(p.y, p.sy, p.sx, p.rows, n);
+  if (vec && pieces <= 4096)
+    run_pieces<T, P, false>(p, pieces, st);
+  else if (shifted && pieces < 4096)
+    run_pieces<T, P, true>(p, pieces + 1, st);  // a row may touch one more
   else
-    run_vec<T, P, 0, 1024, 4>(p, st);
+    layer_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, typename P, int V, int STAGES, bool PART>
+template <typename T, typename P, int V, int STAGES, bool PART, bool SHIFTED>
 cudaError_t run_bwd_vec(NormBwdParams p, cudaStream_t st) {
   constexpr int kBlock = kBwdBlock, kRing = kBlock * 16 * 3 * V * STAGES;
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART, SHIFTED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kRing);
   });
   if (e != cudaSuccess) return e;
-  const int nvec = (int)(p.H * sizeof(T) / 16);
-  const int want = (nvec + V - 1) / V;
+  constexpr int n = 16 / (int)sizeof(T);
+  const int want = ((int)(p.H + (SHIFTED ? n - 1 : 0) + n - 1) / n + V - 1) / V;
   const int team = !PART ? (want + 31) / 32 * 32 : want <= 4 ? 4 : want <= 8 ? 8 : 16, whole = PART ? 32 / team : 1;
   int teams = team >= 64 && kBlock / team > 15 ? 15 : kBlock / team;  // named barriers 1 to 15
   while (teams > whole && p.rows < (int64_t)teams * device_sm_count()) teams -= whole;  // whole warps
   const int64_t blocks = (p.rows + teams - 1) / teams, sms = device_sm_count();
   p.chunks = blocks < sms ? blocks : sms;
   if (p.chunks > kMaxChunks) p.chunks = kMaxChunks;
+  if (SHIFTED) p.chunks = shifted_grid(p.chunks, blocks);
   const int block = team * teams;
   static_assert(kRing >= kBlock * 16 / (int)sizeof(T) * 4 * V, "the partial sums fit the ring");
   p.pb = p.pw + p.chunks * p.H;
-  layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART><<<(unsigned)p.chunks, block, kRing, st>>>(p, team);
+  layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART, SHIFTED><<<(unsigned)p.chunks, block, kRing, st>>>(p, team);
   if (p.gw || p.gb) layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
+template <typename T, typename P, bool SHIFTED>
+cudaError_t run_bwd_pieces(const NormBwdParams& p, int64_t pieces, cudaStream_t st) {
+  if (pieces <= 32) return run_bwd_vec<T, P, 2, 4, true, SHIFTED>(p, st);
+  if (pieces <= 1024) return run_bwd_vec<T, P, 2, 4, false, SHIFTED>(p, st);
+  return run_bwd_vec<T, P, 4, 2, false, SHIFTED>(p, st);
+}
+
 template <typename T, typename P>
 cudaError_t run_backward(NormBwdParams p, cudaStream_t st) {
-  const int b = sizeof(T);
-  const int64_t nvec = p.H * b / 16;
-  const bool vec = p.rows > 0 && p.H * b % 16 == 0 && vector_rows(p.gy, p.sgy, p.rows, b) &&
-                   vector_rows(p.h, p.sh, p.rows, b) && vector_rows(p.gsum, p.sgsum, p.rows, b) &&
-                   vector_rows(p.gx, p.sgx, p.rows, b) && aligned16(p.w);
-  if (vec && nvec <= 32) return run_bwd_vec<T, P, 2, 4, true>(p, st);
-  if (vec && nvec <= 1024) return run_bwd_vec<T, P, 2, 4, false>(p, st);
-  if (vec && nvec <= 2048) return run_bwd_vec<T, P, 4, 2, false>(p, st);
+  const int b = sizeof(T), n = 16 / b;
+  const int64_t pieces = (p.H + n - 1) / n;
+  const bool vec = p.H * b % 16 == 0 && vector_rows(p.gy, p.sgy, p.rows, b) && vector_rows(p.h, p.sh, p.rows, b) &&
+                   vector_rows(p.gsum, p.sgsum, p.rows, b) && vector_rows(p.gx, p.sgx, p.rows, b) && aligned16(p.w);
+  const bool shifted = aligned16(p.gy) && alike(p.h, p.sh, p.sgy, p.rows, n) &&
+                       alike(p.gsum, p.sgsum, p.sgy, p.rows, n) && alike(p.gx, p.sgx, p.sgy, p.rows, n);
+  if (p.rows > 0 && vec && pieces <= 2048) return run_bwd_pieces<T, P, false>(p, pieces, st);
+  if (p.rows > 0 && shifted && pieces < 2048) return run_bwd_pieces<T, P, true>(p, pieces + 1, st);  // one more
   p.chunks = bwd_chunks(p.rows);
   p.rows_per_chunk = (p.rows + p.chunks - 1) / p.chunks;
   p.pb = p.pw + p.chunks * p.H;
