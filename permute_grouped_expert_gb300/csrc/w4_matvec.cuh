@@ -115,12 +115,13 @@ constexpr int kStageBytes = kWarpRows * kRowBytes;
 // them (two at the most), into slots enough for the steps in flight.  The rest
 // holds staged tokens: per step and token 128 f16 and, for each group, the sum
 // of what they hold and the factor that undoes their scaling.
-template <int GROUP, int NT, int WARPS, bool ALIGNED>
+template <int GROUP, int NT, int WARPS, int KSPLIT, bool ALIGNED>
 struct Plan {
   static constexpr int kGroups = kStepK / GROUP;  // groups of a step
   static constexpr int kWarps = WARPS, kThreads = 32 * kWarps;
-  static constexpr int kCtas = NT == 1 ? 3 : 16 / WARPS;  // CTAs of an SM
-  static constexpr int kStages = NT == 1 ? 3 : 4;
+  static constexpr int kRowBlocks = WARPS / KSPLIT;  // tiles of 32 rows of a CTA; KSPLIT warps share the steps of one
+  static constexpr int kCtas = WARPS == 8 ? (NT == 1 ? 3 : 2) : 1;  // CTAs of an SM
+  static constexpr int kStages = kCtas == 3 ? 3 : 4;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kScalePitch = ALIGNED ? 16 : 32, kZeroPitch = ALIGNED ? 4 : 8;
   static constexpr int kSlotBytes = kWarpRows * (kScalePitch + kZeroPitch);
@@ -130,7 +131,7 @@ struct Plan {
   static constexpr int kSmemBytes = 228 * 1024 / kCtas / 128 * 128 - 1024 - 128;  // less what the system and statics take
   static constexpr int kTokenBytes = kSmemBytes - kWarps * kWarpBytes;
   // steps of `toks` tokens that fit
-  static MOE_DEVICE int chunk(int toks) {
+  static __host__ __device__ int chunk(int toks) {
     return kTokenBytes / (toks * kStepK * 2 + (toks + 1) / 2 * 2 * kGroups * 8);
   }
   static_assert(kTokenBytes >= 8 * NT * (kStepK * 2 + kGroups * 8), "a pass of any size makes progress");
@@ -251,10 +252,11 @@ MOE_DEVICE float ld_cluster(const float* at, int rank) {
 // weight rows: neighbouring rows, or with SwiGLU the up and the gate rows of 16
 // features.  The K steps of a row are shared by the ck CTAs of a cluster, a
 // run of steps each.
-template <typename T, int GROUP, int NT, int WARPS, bool ALIGNED>
-__global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Plan<GROUP, NT, WARPS, ALIGNED>::kCtas)
+template <typename T, int GROUP, int NT, int WARPS, int KSPLIT, bool ALIGNED>
+__global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, KSPLIT, ALIGNED>::kThreads,
+                                  Plan<GROUP, NT, WARPS, KSPLIT, ALIGNED>::kCtas)
     matvec_kernel(Params p, int ck) {
-  using P = Plan<GROUP, NT, WARPS, ALIGNED>;
+  using P = Plan<GROUP, NT, WARPS, KSPLIT, ALIGNED>;
   constexpr int U = P::kGroups;
   constexpr int W = GROUP / 32;  // 32-bit code words a lane takes of a group and row
   constexpr int kWarps = P::kWarps, kThreads = P::kThreads, kStages = P::kStages;
@@ -263,8 +265,8 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
   const int gr = lane >> 2, c = lane & 3;
   const int log_features = p.swiglu ? 4 : 5;  // output features of a warp's rows
   const int rank = blockIdx.x % ck;           // clusters lie along x
-  const int64_t cta_n0 = (int64_t)(blockIdx.x / ck) * kWarps << log_features;
-  const int64_t n0 = cta_n0 + ((int64_t)warp << log_features);
+  const int64_t cta_n0 = (int64_t)(blockIdx.x / ck) * P::kRowBlocks << log_features;
+  const int64_t n0 = cta_n0 + ((int64_t)(warp % P::kRowBlocks) << log_features);
 
   int64_t first = 0, M = p.M, e = 0;
   if (p.counts) {
@@ -284,7 +286,9 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
   const uint32_t slots_u32 = (uint32_t)__cvta_generic_to_shared(slots);
   const int all_steps = (int)((p.Kd + kStepK - 1) / kStepK), run = (all_steps + ck - 1) / ck;
   const int begin = min(rank * run, all_steps), end = min(begin + run, all_steps);  // this CTA's steps
-  const int mine = n0 < p.n_out ? end : begin;                                      // this warp's end
+  const int part = (run + KSPLIT - 1) / KSPLIT;
+  const int my_begin = min(begin + warp / P::kRowBlocks * part, end);               // this warp's
+  const int mine = n0 < p.n_out ? min(my_begin + part, end) : my_begin;
 
   // Row r of the warp's tile is weight row n0 + r below 16, n0 + gate + r - 16
   // from there.  Lane (gr, c) copies chunk c of rows gr + 8 q and holds the
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
   };
   // the eight groups that begin with this step's, where it is the first to need them
   auto fill_scales = [&](int step) {
-    if (step >= mine || (step != begin && step * U % 8 != 0)) return;
+    if (step >= mine || (step != my_begin && step * U % 8 != 0)) return;
     // this lane's row
     const int64_t row = lane < 16 ? row0 + min(lane, max(last, 0)) : row16 + max(min(lane & 15, last16), 0);
     const int64_t scale_row = row * G, zero_row = row * zero_bytes;
@@ -359,10 +363,10 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
     float acc[2][NT][4] = {};
     // the first scales belong to the first group of copies
 #pragma unroll
-    for (int i = 0; i < kStages - 1; i++) fill_scales(begin + i);
+    for (int i = 0; i < kStages - 1; i++) fill_scales(my_begin + i);
 #pragma unroll
     for (int i = 0; i < kStages - 1; i++) {
-      fill_codes(begin + i, i);
+      fill_codes(my_begin + i, i);
       cp_async_commit();
     }
     // a lane's tokens in a staged step: words of even and of odd index, see frag_at
@@ -380,9 +384,11 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
       if (s0 > begin) __syncthreads();  // the last chunk has been read
       stage_tokens<T, GROUP, kThreads>(x + t0 * p.sx, p.sx, p.Kd, toks, s0, s1, frag, aux);
       __syncthreads();
-      const uint8_t* tokens = reinterpret_cast<const uint8_t*>(frag);
-      const uint8_t* sums = reinterpret_cast<const uint8_t*>(aux);
-      for (int step = s0; step < min(s1, mine); step++) {
+      // (with KSPLIT the launch sees to it that one chunk holds all of the CTA's steps)
+      const int from = KSPLIT == 1 ? s0 : my_begin;
+      const uint8_t* tokens = reinterpret_cast<const uint8_t*>(frag) + (from - s0) * toks * 256;
+      const uint8_t* sums = reinterpret_cast<const uint8_t*>(aux) + (from - s0) * U * even * 8;
+      for (int step = from; step < min(s1, mine); step++) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
         fill_codes(step + kStages - 1, free_stage);  // the stage every lane has left
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
           red[rt * P::kTile + (nt * 8 + 2 * c + (i & 1)) * kTokStride + gr + 8 * (i >> 1)] =
               acc[rt][nt][i] * 0x1p12f;  // with the staged factor 2^12 / f: 2^24 / f
     // every CTA of the cluster finishes a share of the outputs
-    const int features = kWarps << log_features, log_cta = 31 - __clz(features);
+    const int features = P::kRowBlocks << log_features, log_cta = 31 - __clz(features);
     if (ck > 1)
       cluster_barrier();
     else
@@ -496,14 +502,22 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
       const float* base = reinterpret_cast<const float*>(smem + (f >> log_features) * P::kRingBytes);
       auto total = [&](int rt) {
         const float* at = base + rt * P::kTile + tt * kTokStride + (r & 15);
-        if (ck == 1) return *at;
-        float part[kMaxCluster], v = 0.0f;
+        constexpr int kNext = P::kRowBlocks * P::kRingBytes / 4;  // to the next part of K
+        float v = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; q++)  // in flight together
-          if (q < ck) part[q] = ld_cluster(at, q);
+        for (int k = 0; k < KSPLIT; k++) {
+          if (ck == 1) {
+            v += at[k * kNext];
+          } else {
+            float part[kMaxCluster];
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; q++)
-          if (q < ck) v += part[q];
+            for (int q = 0; q < kMaxCluster; q++)  // in flight together
+              if (q < ck) part[q] = ld_cluster(at + k * kNext, q);
+#pragma unroll
+            for (int q = 0; q < kMaxCluster; q++)
+              if (q < ck) v += part[q];
+          }
+        }
         return v;
       };
       float o;
@@ -524,9 +538,9 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, ALIGNED>::kThreads, Pla
 }
 
 // One kernel with its launch shape for a problem.
-template <typename T, int GROUP, int NT, int WARPS, bool ALIGNED>
+template <typename T, int GROUP, int NT, int WARPS, int KSPLIT, bool ALIGNED>
 struct Launch {
-  using P = Plan<GROUP, NT, WARPS, ALIGNED>;
+  using P = Plan<GROUP, NT, WARPS, KSPLIT, ALIGNED>;
   cudaLaunchAttribute cluster = {};
   cudaLaunchConfig_t cfg = {};
   int ck = 1;        // CTAs that share a row's K
@@ -541,13 +555,13 @@ struct Launch {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     e = once.run([&] {
-      cudaError_t r = cudaFuncSetAttribute(matvec_kernel<T, GROUP, NT, WARPS, ALIGNED>,
+      cudaError_t r = cudaFuncSetAttribute(matvec_kernel<T, GROUP, NT, WARPS, KSPLIT, ALIGNED>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmemBytes);
       cfg.numAttrs = 1;
       for (int k = 1; k <= kMaxCluster && r == cudaSuccess; k++) {
         cluster.val.clusterDim.x = (unsigned)k;
         cfg.gridDim = dim3((unsigned)k);
-        r = cudaOccupancyMaxActiveClusters(&table[dev][k], matvec_kernel<T, GROUP, NT, WARPS, ALIGNED>, &cfg);
+        r = cudaOccupancyMaxActiveClusters(&table[dev][k], matvec_kernel<T, GROUP, NT, WARPS, KSPLIT, ALIGNED>, &cfg);
       }
       return r;
     });
@@ -567,16 +581,19 @@ struct Launch {
     // In twentieths of a step's time on a full SM: a step on an SM with that many
     // CTAs, each of which stages its tokens, and what a CTA spends around its steps.
     constexpr int64_t kAround = 8 * 20, kAlone = NT == 1 ? 8 : 13;  // (few warps do not speed up in proportion)
-    const int64_t ctas = (p.N + kWarpRows * P::kWarps - 1) / (kWarpRows * P::kWarps), sms = device_sm_count();
+    const int64_t rows = kWarpRows * P::kRowBlocks;
+    const int64_t ctas = (p.N + rows - 1) / rows, sms = device_sm_count();
     const int64_t steps = (p.Kd + kStepK - 1) / kStepK;
     for (int k = 1; k <= kMaxCluster && k <= steps; k++) {
-      if (slots[k] < 1) continue;
+      const int64_t run = (steps + k - 1) / k;
+      if (slots[k] < 1 || (KSPLIT > 1 && run > P::chunk(8 * NT))) continue;
       const int64_t clusters = ctas * matrices, waves = (clusters + slots[k] - 1) / slots[k];
       const int64_t on_sm = waves > 1 ? P::kCtas : (clusters * k + sms - 1) / sms;
       const int64_t step = (20 * on_sm / P::kCtas > kAlone ? 20 * on_sm / P::kCtas : kAlone) + (NT > 1 ? 3 * on_sm : 0);
-      const int64_t c = waves * ((steps + k - 1) / k * step + kAround);
+      const int64_t c = waves * ((run + KSPLIT - 1) / KSPLIT * step + kAround);
       if (cost == 0 || c < cost) cost = c, ck = k;
     }
+    if (cost == 0) cost = INT64_MAX;  // no way to run it
     cluster.val.clusterDim.x = (unsigned)ck;
     cfg.gridDim = dim3((unsigned)(ctas * ck), (unsigned)matrices);
     cfg.numAttrs = ck > 1 ? 1 : 0;
@@ -585,24 +602,28 @@ struct Launch {
 
   cudaError_t run(const Params& p, cudaStream_t st) {
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, matvec_kernel<T, GROUP, NT, WARPS, ALIGNED>, p, ck);
+    return cudaLaunchKernelEx(&cfg, matvec_kernel<T, GROUP, NT, WARPS, KSPLIT, ALIGNED>, p, ck);
   }
 };
 
-// More tokens than eight: CTAs of 16 warps stage them once for 512 weight rows
-// where there are rows enough, CTAs of 8 warps spread fewer rows over more SMs.
+// CTAs of 8 warps, several an SM, are the rule.  CTAs of 16 warps stage more than
+// eight tokens once for 512 weight rows where there are rows enough; where there
+// are few CTAs, 16 warps halve the steps of each tile.
 template <typename T, int GROUP, int NT, bool ALIGNED>
 cudaError_t launch(const Params& p, int64_t matrices, cudaStream_t st) {
-  Launch<T, GROUP, NT, 8, ALIGNED> small;
+  Launch<T, GROUP, NT, 8, 1, ALIGNED> small;
   cudaError_t e = small.plan(p, matrices);
   if (e != cudaSuccess) return e;
+  Launch<T, GROUP, NT, 16, 2, ALIGNED> split;
+  e = split.plan(p, matrices);
+  if (e != cudaSuccess) return e;
   if constexpr (NT > 1) {
-    Launch<T, GROUP, NT, 16, ALIGNED> large;
+    Launch<T, GROUP, NT, 16, 1, ALIGNED> large;
     e = large.plan(p, matrices);
     if (e != cudaSuccess) return e;
-    if (large.cost <= small.cost) return large.run(p, st);
+    if (large.cost <= small.cost && large.cost <= split.cost) return large.run(p, st);
   }
-  return small.run(p, st);
+  return split.cost < small.cost ? split.run(p, st) : small.run(p, st);
 }
 
 template <typename T, bool ALIGNED, int GROUP>
