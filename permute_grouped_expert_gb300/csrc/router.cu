@@ -44,8 +44,13 @@ MOE_DEVICE uint32_t key_of(float v) {
 }
 MOE_DEVICE float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
-// exp(l - top), with the limit 1 where l is top (both may be +inf).
-MOE_DEVICE float exp_below(float l, float top) { return expf(l == top ? 0.0f : l - top); }
+// exp(l - top) for l <= top, 1 where l is top (both may be infinite: the minimum
+// drops a NaN).  What is below 2^-126 of the largest is 0.
+MOE_DEVICE float exp_below(float l, float top) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(l - top, 0.0f) * 1.4426950408889634f));
+  return e;
+}
 
 // sigmoid(l) * exp(-m) for m = min(largest l, 0): the common factor keeps the
 // ratio of two sigmoids when both are far below the smallest float.
@@ -75,9 +80,29 @@ MOE_DEVICE float group_add(float v) {
 }
 template <int L>
 MOE_DEVICE float group_max(float v) {
+  if (L == 32) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+  }
 #pragma unroll
   for (int d = L / 2; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
   return v;
+}
+// Two sums over the group; halves of a warp add one value each.
+template <int L>
+MOE_DEVICE void group_add2(float& a, float& b) {
+  if (L == 32) {
+    const bool lower = (threadIdx.x & 16) == 0;
+    float v = (lower ? a : b) + __shfl_xor_sync(kAll, lower ? b : a, 16);
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    a = __shfl_sync(kAll, v, 0);
+    b = __shfl_sync(kAll, v, 16);
+  } else {
+    a = group_add<L>(a);
+    b = group_add<L>(b);
+  }
 }
 // Sum over the lanes of the group below this one.
 template <int L>
@@ -113,25 +138,43 @@ MOE_DEVICE void load_scores(float (&l)[V], const T* row, int e0, int E, bool vec
   }
 }
 
+// Counts in the low bits of a float: one comparison and one addition a score, of
+// which only the comparison takes the pipe that bounds the kernel.
 template <int V>
 MOE_DEVICE int count_from(const float (&s)[V], float v) {
-  int n = 0;
+  float n[2] = {8388608.0f, 0.0f};  // 2^23
 #pragma unroll
-  for (int j = 0; j < V; j++) n += s[j] >= v;
-  return n;
+  for (int j = 0; j < V; j++) {
+    float one;
+    asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(one) : "f"(s[j]), "f"(v));
+    n[j & 1] += one;
+  }
+  return __float_as_int(n[0] + n[1]) & 0x7fffff;
 }
 
-// Bit j: expert e0 + j is chosen.  `live` scores are above -inf; `low` and `top`
-// are the smallest and the largest of them (+inf and -inf if there is none).
+template <int V>
+MOE_DEVICE uint32_t bits_from(const float (&s)[V], float v) {
+  uint32_t on = 0;
+#pragma unroll
+  for (int j = 0; j < V; j++) on |= s[j] >= v ? 1u << j : 0u;
+  return on;
+}
+
+// The score that the chosen reach, in `lo`; true where more than K scores of a
+// token of the warp reach it, and `on` then tells every token's chosen: bit j,
+// expert e0 + j.  `live` scores are above -inf; `low` and `top` are the smallest
+// and the largest of them (+inf and -inf if there is none).
 // `guess` is where the K-th score would be, and `step` how far a score is from
 // the next there, if the scores were a normal sample: the first guess then
 // counts K but for a few, and a step by the difference mostly lands on K.
 // Whatever they are, the interval bounds the search.
 template <int V, int L>
-MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float low, float top, float guess, float step) {
+MOE_DEVICE bool select_top(const float (&s)[V], int K, int live, float low, float top, float guess, float step,
+                           float& lo, uint32_t& on) {
   // counts: n_lo >= K scores reach lo, n_hi < K reach hi (hi is the top, and n_hi
   // 0, until there is a count below K); the choice is exact once a count is K
-  float lo = low, hi = top;
+  lo = low;
+  float hi = top;
   int n_lo = live, n_hi = 0;
   bool exact = live <= K, found = exact;
   // a token's lanes agree; other tokens of the warp go on
@@ -144,7 +187,7 @@ MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float low, 
       mid = hi - (hi - lo) * fminf(fmaxf(part, 0.0625f), 0.9375f);
     }
     const int n = group_add<L>(count_from<V>(s, mid));
-    if (!found && mid > lo && mid <= hi) {
+    if ((L == 32 || !found) && mid > lo && mid <= hi) {
       if (n >= K)
         lo = mid, n_lo = n, exact = n == K;
       else
@@ -167,37 +210,33 @@ MOE_DEVICE uint32_t select_top(const float (&s)[V], int K, int live, float low, 
     }
     if (!found) lo = of_key(klo), exact = n_lo == K;
   }
-  uint32_t on = 0;
+  if (L == 32 ? exact : (bool)__all_sync(kAll, exact)) return false;
+  on = bits_from<V>(s, lo);
+  uint32_t above = 0;
 #pragma unroll
-  for (int j = 0; j < V; j++) on |= s[j] >= lo ? 1u << j : 0u;
-  if (!(L == 32 ? exact : (bool)__all_sync(kAll, exact))) {
-    uint32_t above = 0;
-#pragma unroll
-    for (int j = 0; j < V; j++) above |= s[j] > lo ? 1u << j : 0u;
-    uint32_t equal = on & ~above;
-    int room = K - group_add<L>(__popc(above)) - group_below<L>(__popc(equal));
-    if (!exact) {
-      for (; equal && room > 0; room--) {
-        above |= equal & -equal;
-        equal &= equal - 1;
-      }
-      on = above;
+  for (int j = 0; j < V; j++) above |= s[j] > lo ? 1u << j : 0u;
+  uint32_t equal = on & ~above;
+  int room = K - group_add<L>(__popc(above)) - group_below<L>(__popc(equal));
+  if (!exact) {
+    for (; equal && room > 0; room--) {
+      above |= equal & -equal;
+      equal &= equal - 1;
     }
+    on = above;
   }
-  return on;
+  return true;
 }
 
 template <typename T, int V, int L, int SCORE>
-__global__ void __launch_bounds__(kThreads, V == 8 ? 5 : 1) router_topk_kernel(RouterParams p) {
+__global__ void __launch_bounds__(kThreads, V == 8 ? 5 : V == 16 ? 3 : 2) router_topk_kernel(RouterParams p) {
   constexpr int kTokens = 32 / L;                     // tokens of a warp
   constexpr int kChosen = V * L < 128 ? V * L : 128;  // K at the most
   constexpr bool kSoftmax = SCORE == MOE_SCORE_SOFTMAX;
-  __shared__ float weight_of[kWarps][kTokens][kChosen];
-  __shared__ int16_t id_of[kWarps][kTokens][kChosen];
+  // a token's chosen: expert and logit, later weight
+  __shared__ uint2 chosen_of[kWarps][kTokens][kChosen];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int at = lane % L, e0 = at * V;
-  float* chosen_weight = weight_of[warp][lane / L];
-  int16_t* chosen_id = id_of[warp][lane / L];
+  uint2* chosen = chosen_of[warp][lane / L];
   const bool divide = kSoftmax || p.renorm;
 
   for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; t0 < p.T;
@@ -207,86 +246,113 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : 1) router_topk_kernel(R
     const T* row = static_cast<const T*>(p.logits) + (real ? t : t0) * p.stride;
     float s[V];
     load_scores<T, V>(s, row, e0, p.E, p.vector_in);
-    bool bad = false;
-#pragma unroll
-    for (int j = 0; j < V; j++) bad |= s[j] != s[j];
     if (p.bias) {
 #pragma unroll
-      for (int j = 0; j < V; j++) {
-        if (s[j] > -INFINITY) {  // (false past the end of the row)
+      for (int j = 0; j < V; j++)
+        if (s[j] > -INFINITY)  // (false past the end of the row)
           s[j] = (kSoftmax ? s[j] : sigmoid_scaled(s[j], 0.0f)) + p.bias[e0 + j];
-          bad |= s[j] != s[j];
-        }
-      }
     }
-    if (bad && p.status) atomicOr(p.status, MOE_DEV_ERR_NAN_LOGIT);
-    float low = INFINITY, top = -INFINITY, sum = 0.0f, squares = 0.0f;
+    // a lane's experts as if all of them were finite, which the squares tell
+    float low = s[0], top = s[0], sum = 0.0f, squares = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      s[j] = fmaxf(s[j], -INFINITY);  // NaN: masked
-      const bool in = e0 + j < p.E;
-      low = fminf(low, in ? s[j] : INFINITY);
+      low = fminf(low, s[j]);
       top = fmaxf(top, s[j]);
-      sum += in ? s[j] : 0.0f;
-      squares = fmaf(in ? s[j] : 0.0f, s[j], squares);
+      sum += s[j];
+      squares = fmaf(s[j], s[j], squares);
     }
-    low = -group_max<L>(-low);
-    top = group_max<L>(top);
+    if (e0 >= p.E) low = INFINITY, sum = squares = 0.0f;
     int live = p.E;
-    if (__any_sync(kAll, low == -INFINITY)) {  // some experts are masked
+    if (__any_sync(kAll, !(squares < INFINITY))) {  // some are masked, past the end, infinite or NaN
+      bool bad = false;
       low = INFINITY;
+      top = -INFINITY;
       live = 0;
       sum = squares = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; j++) {
+        bad |= s[j] != s[j];
         const bool in = s[j] > -INFINITY;
+        s[j] = in ? s[j] : -INFINITY;  // NaN: masked
         live += in;
         low = fminf(low, in ? s[j] : INFINITY);
+        top = fmaxf(top, s[j]);
         sum += in ? s[j] : 0.0f;
         squares = fmaf(in ? s[j] : 0.0f, in ? s[j] : 0.0f, squares);
       }
+      if (bad && p.status) atomicOr(p.status, MOE_DEV_ERR_NAN_LOGIT);
       live = group_add<L>(live);
-      low = -group_max<L>(-low);
     }
-    sum = group_add<L>(sum);
-    squares = group_add<L>(squares);
+    low = -group_max<L>(-low);
+    top = group_max<L>(top);
+    group_add2<L>(sum, squares);
     const float mean = __fdividef(sum, (float)live);
     const float dev = sqrtf(fmaxf(__fdividef(squares, (float)live) - mean * mean, 0.0f));
-    const uint32_t on = select_top<V, L>(s, p.K, live, low, top, mean + dev * p.quantile, dev * p.spacing);
+    float lo;
+    uint32_t on = 0;
+    const bool ties =
+        select_top<V, L>(s, p.K, live, low, top, mean + dev * p.quantile, dev * p.spacing, lo, on);
+    // `bits`: the chosen are marked in `on`
+    const bool bits = V != 8 || ties || p.format == MOE_ROUTING_SPARSE_BOOL;
+    if (bits && !ties) on = bits_from<V>(s, lo);
 
-    // the chosen ids in ascending order through shared memory
-    const int first = group_below<L>(__popc(on)), count = group_add<L>(__popc(on));
+    // the chosen ids in ascending order through shared memory, and the logits
+    // beside them where this lane still has them
+    const int first = group_below<L>(bits ? __popc(on) : count_from<V>(s, lo)), count = min(live, p.K);
+    const bool staged = V == 8 && !p.bias;
     int slot = first;
-    for (uint32_t left = on; left; left &= left - 1) chosen_id[slot++] = (int16_t)(e0 + __ffs(left) - 1);
+    if (!bits) {
+      uint32_t to = (uint32_t)__cvta_generic_to_shared(chosen + first);
+#pragma unroll
+      for (int j = 0; j < V; j++)
+        asm volatile(
+            "{\n.reg .pred on;\n"
+            "setp.ge.f32 on, %2, %3;\n"
+            "@on st.shared.v2.b32 [%0], {%1, %2};\n"
+            "@on add.u32 %0, %0, 8;\n}"
+            : "+r"(to)
+            : "r"(e0 + j), "f"(s[j]), "f"(lo)
+            : "memory");
+    } else if (V == 8) {
+#pragma unroll
+      for (int j = 0; j < V; j++)
+        if (on >> j & 1) chosen[slot++] = make_uint2(e0 + j, __float_as_uint(s[j]));
+    } else {
+      for (uint32_t left = on; left; left &= left - 1) chosen[slot++].x = e0 + __ffs(left) - 1;
+    }
     __syncwarp();
 
     // weights, L of the chosen at a time; the largest logit that takes part is
     // `top` itself, and looked for where the scores are not the logits
     float z = 0.0f;
-    if (p.bias) {
+    if (!p.bias) {
+      if (kSoftmax && !p.renorm) {  // every live expert takes part in the sum
+#pragma unroll
+        for (int j = 0; j < V; j++) z += exp_below(s[j], top);
+      }
+    } else {
       top = -INFINITY;
       if (kSoftmax && !p.renorm) {
 #pragma unroll
-        for (int j = 0; j < V; j++)
-          if (s[j] > -INFINITY) top = fmaxf(top, to_float(row[e0 + j]));
+        for (int j = 0; j < V; j++) {
+          if (s[j] > -INFINITY) s[j] = to_float(row[e0 + j]);
+          top = fmaxf(top, s[j]);
+        }
       } else {
-        for (int k = at; k < count; k += L) top = fmaxf(top, to_float(row[chosen_id[k]]));
+        for (int k = at; k < count; k += L) top = fmaxf(top, to_float(row[chosen[k].x]));
       }
       top = group_max<L>(top);
-    }
-    if (kSoftmax && !p.renorm) {  // every live expert takes part in the sum
+      if (kSoftmax && !p.renorm) {
 #pragma unroll
-      for (int j = 0; j < V; j++) {
-        float l = s[j];
-        if (p.bias && l > -INFINITY) l = to_float(row[e0 + j]);
-        z += s[j] > -INFINITY ? exp_below(l, top) : 0.0f;
+        for (int j = 0; j < V; j++) z += exp_below(s[j], top);
       }
     }
     const float m = p.renorm ? fminf(top, 0.0f) : 0.0f;
     for (int k = at; k < count; k += L) {
-      const float l = to_float(row[chosen_id[k]]);
+      const uint2 c = chosen[k];
+      const float l = staged ? __uint_as_float(c.y) : to_float(row[c.x]);
       const float w = kSoftmax ? exp_below(l, top) : sigmoid_scaled(l, m);
-      chosen_weight[k] = w;
+      chosen[k].y = __float_as_uint(w);
       if (p.renorm) z += w;
     }
     if (divide) z = group_add<L>(z);
@@ -294,16 +360,17 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : 1) router_topk_kernel(R
     if (p.format == MOE_ROUTING_DENSE_I16) {
       if (real) {
         for (int k = at; k < p.K; k += L) {
+          const uint2 c = chosen[k];
           const bool in = k < count;
-          static_cast<int16_t*>(p.map)[t * p.K + k] = in ? chosen_id[k] : (int16_t)-1;
-          p.probs[t * p.K + k] = in ? chosen_weight[k] * f : 0.0f;
+          static_cast<int16_t*>(p.map)[t * p.K + k] = (int16_t)(in ? (int)c.x : -1);
+          p.probs[t * p.K + k] = in ? __uint_as_float(c.y) * f : 0.0f;
         }
       }
     } else {
       __syncwarp();
       slot = first;
 #pragma unroll
-      for (int j = 0; j < V; j++) s[j] = on >> j & 1 ? chosen_weight[slot++] * f : 0.0f;
+      for (int j = 0; j < V; j++) s[j] = on >> j & 1 ? __uint_as_float(chosen[slot++].y) * f : 0.0f;
       if (real) {
         uint8_t* map = static_cast<uint8_t*>(p.map) + t * p.E;
         float* probs = p.probs + t * p.E;
