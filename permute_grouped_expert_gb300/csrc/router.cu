@@ -117,24 +117,26 @@ MOE_DEVICE int group_below(int v) {
   return s - v;
 }
 
-// V neighbouring values of a row from e0, -inf past its end.
+// V values of a row as V / N vectors of N neighbours, the first at e0 and each
+// `gap` after the one before; -inf past the row's end.
 template <typename T, int V>
-MOE_DEVICE void load_scores(float (&l)[V], const T* row, int e0, int E, bool vector) {
+MOE_DEVICE void load_scores(float (&l)[V], const T* row, int e0, int gap, int E, bool vector) {
   constexpr int N = 16 / sizeof(T);
-  if (vector) {
 #pragma unroll
-    for (int j = 0; j < V; j += N) {
+  for (int j = 0; j < V; j += N) {
+    const int e = e0 + j / N * gap;
+    if (vector) {
       union {
         uint4 v;
         T e[N];
       } u;
-      if (e0 + j < E) u.v = *reinterpret_cast<const uint4*>(row + e0 + j);
+      if (e < E) u.v = *reinterpret_cast<const uint4*>(row + e);
 #pragma unroll
-      for (int i = 0; i < N; i++) l[j + i] = e0 + j < E ? to_float(u.e[i]) : -INFINITY;
+      for (int i = 0; i < N; i++) l[j + i] = e < E ? to_float(u.e[i]) : -INFINITY;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i++) l[j + i] = e + i < E ? to_float(row[e + i]) : -INFINITY;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; j++) l[j] = e0 + j < E ? to_float(row[e0 + j]) : -INFINITY;
   }
 }
 
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : V == 16 ? 3 : 2) router
     const bool real = t < p.T;
     const T* row = static_cast<const T*>(p.logits) + (real ? t : t0) * p.stride;
     float s[V];
-    load_scores<T, V>(s, row, e0, p.E, p.vector_in);
+    load_scores<T, V>(s, row, e0, 16 / sizeof(T), p.E, p.vector_in);
     if (p.bias) {
 #pragma unroll
       for (int j = 0; j < V; j++)
@@ -415,53 +417,30 @@ struct RouterBwdParams {
   void* gl;
 };
 
-// Marks an expert without a gradient in a staged row (a NaN no computation makes).
-constexpr uint32_t kNoGradient = 0xffa5c3e7u;
-
-template <typename T, int V, int L, int SCORE>
-__global__ void __launch_bounds__(kThreads) router_bwd_kernel(RouterBwdParams p) {
-  constexpr int kTokens = 32 / L, N = 16 / sizeof(T);
-  __shared__ uint4 staged[kWarps][kTokens * V * L / 4];  // dense maps: gradients by expert
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int at = lane % L, e0 = at * V;
-  uint4* mine = staged[warp] + lane * (V / 4);  // this lane's experts
-  uint32_t* grow = reinterpret_cast<uint32_t*>(staged[warp] + lane / L * L * (V / 4));
+// Gradient where only the chosen take part: a lane takes one of them (or a few),
+// and the row goes out through shared memory, zeros but for theirs.  Of the
+// logits, and of a sparse map's gradients, only those of the chosen are read.
+template <typename T, int V, int L, int SCORE, bool SPARSE>
+__global__ void __launch_bounds__(kThreads, V == 8 ? (SPARSE ? 5 : 4) : 2) router_bwd_chosen_kernel(RouterBwdParams p) {
+  constexpr int kTokens = 32 / L, N = 16 / sizeof(T), kVecs = V / N;
+  constexpr int kEach = SPARSE || V == 8 ? V : 128 / L;  // chosen of a lane at the most
   constexpr bool kSoftmax = SCORE == MOE_SCORE_SOFTMAX;
+  __shared__ uint4 staged[kWarps][kTokens * L * kVecs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane % L;
+  uint4* vecs = staged[warp] + lane / L * (L * kVecs);  // this token's row
+  T* grow = reinterpret_cast<T*>(vecs);
+  int16_t* ids = reinterpret_cast<int16_t*>(vecs);  // before the row
 
   for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; t0 < p.T;
        t0 += (int64_t)gridDim.x * kWarps * kTokens) {
     const int64_t t = t0 + lane / L;
     const bool real = t < p.T;
     const T* row = static_cast<const T*>(p.logits) + (real ? t : t0) * p.stride;
-    float l[V], g[V];
-    load_scores<T, V>(l, row, e0, p.E, p.vector_in);
-    uint32_t on = 0;
-    if (p.format == MOE_ROUTING_DENSE_I16) {
-#pragma unroll
-      for (int j = 0; j < V / 4; j++) mine[j] = make_uint4(kNoGradient, kNoGradient, kNoGradient, kNoGradient);
-      __syncwarp();
-      if (real) {
-        for (int k = at; k < p.K; k += L) {
-          const int e = static_cast<const int16_t*>(p.map)[t * p.K + k];
-          const float v = p.gp[t * p.K + k];
-          if (e >= 0 && e < p.E) grow[e] = __float_as_uint(v);
-        }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < V / 4; j++) {
-        const uint4 v = mine[j];
-        const uint32_t b[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          on |= (uint32_t)(b[i] != kNoGradient) << (4 * j + i);
-          g[4 * j + i] = __uint_as_float(b[i]);
-        }
-      }
-      __syncwarp();
-    } else {
+    int count = real ? p.K : 0;
+    if (SPARSE) {  // the chosen ids in ascending order
       const uint8_t* map = static_cast<const uint8_t*>(p.map) + (real ? t : t0) * p.E;
-      const float* gp = p.gp + (real ? t : t0) * p.E;
+      const int e0 = at * V;
+      uint32_t on = 0;
       if (p.vector_map) {
 #pragma unroll
         for (int j = 0; j < V; j += 8) {
@@ -469,77 +448,172 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(RouterBwdParams p)
           const uint2 b = *reinterpret_cast<const uint2*>(map + e0 + j);
 #pragma unroll
           for (int i = 0; i < 8; i++) on |= (uint32_t)(((i < 4 ? b.x : b.y) >> (8 * (i & 3)) & 0xffu) != 0) << (j + i);
-#pragma unroll
-          for (int i = 0; i < 8; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(gp + e0 + j + i);
-            g[j + i] = v.x, g[j + i + 1] = v.y, g[j + i + 2] = v.z, g[j + i + 3] = v.w;
-          }
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-          if (e0 + j >= p.E) continue;
-          on |= (uint32_t)(map[e0 + j] != 0) << j;
-          g[j] = gp[e0 + j];
-        }
+        for (int j = 0; j < V; j++)
+          if (e0 + j < p.E) on |= (uint32_t)(map[e0 + j] != 0) << j;
       }
+      count = group_add<L>(__popc(on));
+      int slot = group_below<L>(__popc(on));
+      for (; on; on &= on - 1) ids[slot++] = (int16_t)(e0 + __ffs(on) - 1);
+      if (!real) count = 0;
+      __syncwarp();
     }
-    // experts that take part: the chosen, with the plain softmax all
-    const bool all = kSoftmax && !p.renorm;
-    float top = -INFINITY;
+    int e[kEach];
+    float l[kEach], g[kEach], top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < V; j++) {
-      const bool masked = !(l[j] > -INFINITY);  // or NaN, or past the end of the row: no gradient
-      on &= masked ? ~(1u << j) : ~0u;
-      const bool c = on >> j & 1;
-      g[j] = c ? g[j] : 0.0f;
-      l[j] = c || (all && !masked) ? l[j] : -INFINITY;
-      top = fmaxf(top, l[j]);
+    for (int i = 0; i < kEach; i++) {
+      if (i * L >= count) break;
+      const int k = at + i * L;
+      e[i] = -1;
+      if (k < count) e[i] = SPARSE ? ids[k] : static_cast<const int16_t*>(p.map)[t * p.K + k];
+      if (e[i] >= p.E) e[i] = -1;
+      g[i] = e[i] >= 0 ? p.gp[SPARSE ? t * p.E + e[i] : t * p.K + k] : 0.0f;
+      l[i] = e[i] >= 0 ? to_float(row[e[i]]) : -INFINITY;
+      if (!(l[i] > -INFINITY)) e[i] = -1, l[i] = -INFINITY, g[i] = 0.0f;  // masked or NaN
+      top = fmaxf(top, l[i]);
     }
-    top = group_max<L>(top);
+    if (SPARSE) __syncwarp();  // the ids are read
+#pragma unroll
+    for (int j = 0; j < kVecs; j++) vecs[j * L + at] = make_uint4(0, 0, 0, 0);
+    if (kSoftmax || p.renorm) top = group_max<L>(top);
     const float m = p.renorm ? fminf(top, 0.0f) : 0.0f;
-    // n: the score each expert takes part with; z its sum; dot = sum of g n
-    float n[V], z = 0.0f, dot = 0.0f;
+    float n[kEach], z = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; j++) {
-      const float v = kSoftmax ? exp_below(l[j], top) : sigmoid_scaled(l[j], m);
-      n[j] = l[j] > -INFINITY ? v : 0.0f;
-      z += n[j];
-      dot = fmaf(g[j], n[j], dot);
+    for (int i = 0; i < kEach; i++) {
+      if (i * L >= count) break;
+      n[i] = e[i] < 0 ? 0.0f : kSoftmax ? exp_below(l[i], top) : sigmoid_scaled(l[i], m);
+      z += n[i];
+      dot = fmaf(g[i], n[i], dot);
     }
     float inv = p.scale;
-    if (kSoftmax || p.renorm) {
-      z = group_add<L>(z);
-      dot = group_add<L>(dot);
+    if (p.renorm) {
+      group_add2<L>(z, dot);
       const float r = z > 0.0f ? __fdividef(1.0f, z) : 0.0f;
       inv *= r;
       dot *= r;
     } else {
       dot = 0.0f;
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+      if (i * L >= count) break;
+      float v = n[i] * inv * (g[i] - dot);
+      if (!kSoftmax) v *= sigmoid_rest(l[i]);
+      if (e[i] >= 0 && n[i] != 0.0f) grow[e[i]] = from_float<T>(v);
+    }
+    __syncwarp();
+    if (real) {
+      T* out = static_cast<T*>(p.gl) + t * p.gstride;
+      if (p.vector_out) {
+#pragma unroll
+        for (int j = 0; j < kVecs; j++)
+          if ((j * L + at) * N < p.E) reinterpret_cast<uint4*>(out)[j * L + at] = vecs[j * L + at];
+      } else {
+        for (int i = at; i < p.E; i += L) out[i] = grow[i];
+      }
+    }
+    __syncwarp();  // before the next token's row
+  }
+}
+
+// Marks an expert without a gradient in a staged row (a NaN no computation makes).
+constexpr uint32_t kNoGradient = 0xffa5c3e7u;
+
+// Gradient of the plain softmax, where every expert takes part.  A lane takes 16
+// bytes of a row at every L-th place, so that loads and stores are whole lines.
+template <typename T, int V, int L>
+__global__ void __launch_bounds__(kThreads, V == 32 ? 2 : 1) router_bwd_all_kernel(RouterBwdParams p) {
+  constexpr int kTokens = 32 / L, N = 16 / sizeof(T);
+  __shared__ uint4 staged[kWarps][kTokens * V * L / 4];  // dense maps: gradients by expert
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane % L;
+  uint4* token = staged[warp] + lane / L * L * (V / 4);
+  float* row_g = reinterpret_cast<float*>(token);
+  auto expert = [&](int j) { return (j / N * L + at) * N + j % N; };
+
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; t0 < p.T;
+       t0 += (int64_t)gridDim.x * kWarps * kTokens) {
+    const int64_t t = t0 + lane / L;
+    const bool real = t < p.T;
+    float l[V], g[V];
+    load_scores<T, V>(l, static_cast<const T*>(p.logits) + (real ? t : t0) * p.stride, at * N, L * N, p.E, p.vector_in);
+    if (p.format == MOE_ROUTING_DENSE_I16) {
+#pragma unroll
+      for (int j = 0; j < V / 4; j++) token[j * L + at] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+      if (real) {
+        for (int k = at; k < p.K; k += L) {
+          const int e = static_cast<const int16_t*>(p.map)[t * p.K + k];
+          if (e >= 0 && e < p.E) row_g[e] = p.gp[t * p.K + k];
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(row_g + expert(j));
+        g[j] = v.x, g[j + 1] = v.y, g[j + 2] = v.z, g[j + 3] = v.w;
+      }
+      __syncwarp();
+    } else {
+      const uint8_t* map = static_cast<const uint8_t*>(p.map) + (real ? t : t0) * p.E;
+      const float* gp = p.gp + (real ? t : t0) * p.E;
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const int e = expert(j);
+        if (p.vector_map && e < p.E) {
+          const uint32_t b = *reinterpret_cast<const uint32_t*>(map + e);
+          const float4 v = *reinterpret_cast<const float4*>(gp + e);
+          g[j] = b & 0xffu ? v.x : 0.0f;
+          g[j + 1] = b >> 8 & 0xffu ? v.y : 0.0f;
+          g[j + 2] = b >> 16 & 0xffu ? v.z : 0.0f;
+          g[j + 3] = b >> 24 ? v.w : 0.0f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; i++) g[j + i] = e + i < p.E && map[e + i] != 0 ? gp[e + i] : 0.0f;
+        }
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < V; j++) top = fmaxf(top, l[j]);
+    top = group_max<L>(top);
+    // l: the weight each expert takes part with, 0 where it is masked, NaN or past
+    // the row's end; z its sum; dot = sum of g n
+    float z = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-      float v = n[j] * inv * (g[j] - dot);
-      if (!kSoftmax) v *= sigmoid_rest(l[j]);
-      g[j] = n[j] != 0.0f ? v : 0.0f;
+      const bool in = l[j] > -INFINITY;
+      const float n = exp_below(l[j], top);
+      l[j] = in ? n : 0.0f;
+      g[j] = in ? g[j] : 0.0f;
+      z += l[j];
+      dot = fmaf(g[j], l[j], dot);
     }
-    if (!real) continue;
-    T* out = static_cast<T*>(p.gl) + t * p.gstride + e0;
-    if (p.vector_out) {
+    group_add2<L>(z, dot);
+    const float r = z > 0.0f ? __fdividef(1.0f, z) : 0.0f, inv = p.scale * r;
+    dot *= r;
 #pragma unroll
-      for (int j = 0; j < V; j += N) {
+    for (int j = 0; j < V; j++) g[j] = l[j] != 0.0f ? l[j] * inv * (g[j] - dot) : 0.0f;
+    if (!real) continue;
+    T* out = static_cast<T*>(p.gl) + t * p.gstride;
+#pragma unroll
+    for (int j = 0; j < V; j += N) {
+      const int e = expert(j);
+      if (p.vector_out) {
         union {
           uint4 v;
           T e[N];
         } u;
 #pragma unroll
         for (int i = 0; i < N; i++) u.e[i] = from_float<T>(g[j + i]);
-        if (e0 + j < p.E) *reinterpret_cast<uint4*>(out + j) = u.v;
-      }
-    } else {
+        if (e < p.E) *reinterpret_cast<uint4*>(out + e) = u.v;
+      } else {
 #pragma unroll
-      for (int j = 0; j < V; j++)
-        if (e0 + j < p.E) out[j] = from_float<T>(g[j]);
+        for (int i = 0; i < N; i++)
+          if (e + i < p.E) out[e + i] = from_float<T>(g[j + i]);
+      }
     }
   }
 }
@@ -576,7 +650,21 @@ void run_topk(const RouterParams& p, cudaStream_t st) {
 
 template <typename T, int SCORE>
 void run_bwd(const RouterBwdParams& p, cudaStream_t st) {
-#define RUN(V, L) router_bwd_kernel<T, V, L, SCORE><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+#define RUN(V, L) router_bwd_all_kernel<T, V, L><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+    if (!p.renorm) {
+      MOE_ROUTER_SHAPE(RUN);
+      return;
+    }
+  }
+#undef RUN
+#define RUN(V, L) router_bwd_chosen_kernel<T, V, L, SCORE, true><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+  if (p.format == MOE_ROUTING_SPARSE_BOOL) {
+    MOE_ROUTER_SHAPE(RUN);
+    return;
+  }
+#undef RUN
+#define RUN(V, L) router_bwd_chosen_kernel<T, V, L, SCORE, false><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
   MOE_ROUTER_SHAPE(RUN);
 #undef RUN
 }
