@@ -208,8 +208,12 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
   __shared__ float2 red[2][THREADS / 32];
   const int team = LANES ? LANES : (int)blockDim.x, teams = LANES ? THREADS / LANES : 1;
   const int t = LANES ? threadIdx.x % LANES : threadIdx.x;
-  const int64_t first = (int64_t)blockIdx.x * teams + (LANES ? threadIdx.x / LANES : 0);
-  const int skip = SHIFTED ? (int)(first * p.sx % N) : 0;
+  // rows of block number n; SHIFTED: eight apart, so that its rows (and those of
+  // every block that this CTA takes, the grid being a multiple of eight) start alike
+  const int own = LANES ? threadIdx.x / LANES : 0;
+  auto row_of = [&](int64_t n) { return SHIFTED ? ((n >> 3) * teams + own) * 8 + (n & 7) : n * teams + own; };
+  const int64_t blocks = SHIFTED ? (p.rows + 8 * teams - 1) / (8 * teams) * 8 : (p.rows + teams - 1) / teams;
+  const int skip = SHIFTED ? (int)((blockIdx.x & 7) * p.sx % N) : 0;
   const int nvec = ((int)p.H + skip + N - 1) / N, v_step = team * N;
   const int c0 = t * N - skip;  // this thread's first column
   uint32_t mask[V];             // of its pieces
@@ -217,6 +221,7 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
   for (int v = 0; v < V; v++) mask[v] = SHIFTED ? piece_mask<N>(c0 + v * v_step, (int)p.H) : ~0u;
   const P* w = static_cast<const P*>(p.w) + (p.w ? c0 : 0);
   const P* b = static_cast<const P*>(p.b) + (p.b ? c0 : 0);
+  extern __shared__ __align__(16) uint8_t staged[];  // SHIFTED: the parameters as the rows' pieces lie
   auto total = [&](float v, float2* r) {
     if (!LANES) return block_sum2(v, 0.0f, r).x;
 #pragma unroll
@@ -238,11 +243,24 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
         if (v * team + t < nvec) res_raw[v] = load_piece<T, SHIFTED>(res + v * v_step, mask[v]);
     }
   };
-  const int64_t step = (int64_t)gridDim.x * teams;
-  if (kAhead) fetch(blockIdx.x);
-  for (int64_t r0 = (int64_t)blockIdx.x * teams; r0 < p.rows; r0 += step) {
+  if (kAhead && row_of(blockIdx.x) < p.rows) fetch(row_of(blockIdx.x));
+  if (SHIFTED) {
+    P* sw = reinterpret_cast<P*>(staged);
+    P* sb = sw + nvec * N;
+    for (int i = threadIdx.x; i < nvec * N; i += (int)blockDim.x) {
+      const int c = i - skip;
+      const bool in = c >= 0 && c < (int)p.H;
+      sw[i] = in && p.w ? static_cast<const P*>(p.w)[c] : from_float<P>(0.0f);
+      sb[i] = in && p.b ? static_cast<const P*>(p.b)[c] : from_float<P>(0.0f);
+    }
+    w = sw + t * N;
+    b = sb + t * N;
+    __syncthreads();
+  }
+  for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
     // a team past the last row has no columns: its warp shuffles together
-    const int64_t r = r0 + (LANES ? threadIdx.x / LANES : 0);
+    const int64_t r = row_of(block), next = row_of(block + gridDim.x);
+    if (SHIFTED && !LANES && r >= p.rows) break;
     const int n = r < p.rows ? nvec : 0;
     float h[V][N];
     const T* x = static_cast<const T*>(p.x) + r * p.sx + c0;
@@ -273,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
         }
       }
     }
-    if (kAhead && r0 + step < p.rows) fetch(r0 + step);
+    if (kAhead && next < p.rows) fetch(next);
     float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; v++)
@@ -300,8 +318,8 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
         float g[N], c[N];
 #pragma unroll
         for (int k = 0; k < N; k++) g[k] = 1.0f, c[k] = 0.0f;
-        if (p.w) piece_params<T, P, SHIFTED>(g, w + v * v_step, mask[v]);
-        if (p.b) piece_params<T, P, SHIFTED>(c, b + v * v_step, mask[v]);
+        if (p.w) load_params<T, P>(g, w + v * v_step);
+        if (p.b) load_params<T, P>(c, b + v * v_step);
 #pragma unroll
         for (int k = 0; k < N; k++) g[k] = fmaf(h[v][k] * rstd, g[k], c[k]);
         store_piece<T, SHIFTED>(y + v * v_step, pack<T>(g), mask[v]);
@@ -674,33 +692,38 @@ bool alike(const void* p, int64_t stride, int64_t other, int64_t rows, int n) {
 // CTAs that keep a team's rows a multiple of 16 bytes apart, unless each team has one row.
 int64_t shifted_grid(int64_t grid, int64_t blocks) { return blocks > grid && grid >= 8 ? grid / 8 * 8 : grid; }
 
+constexpr int kMaxStaged = 200 * 1024;  // bytes of parameters a CTA stages at the most
+
 template <typename T, typename P, bool SHIFTED, int LANES, int THREADS, int V = 4>
-void run_vec(const NormParams& p, cudaStream_t st) {
+cudaError_t run_vec(const NormParams& p, cudaStream_t st) {
   const int n = 16 / (int)sizeof(T), pieces = (int)(p.H + (SHIFTED ? n - 1 : 0) + n - 1) / n;
   const int block = LANES ? THREADS : ((pieces + V - 1) / V + 31) / 32 * 32;
-  const int teams = LANES ? THREADS / (LANES + !LANES) : 1;
-  const int64_t blocks = (p.rows + teams - 1) / teams, cap = (int64_t)device_sm_count() * (2048 / block);
-  const int64_t grid = blocks < cap ? blocks : cap;
-  layer_norm_vec_kernel<T, P, V, LANES, THREADS, SHIFTED>
-      <<<(unsigned)(SHIFTED ? shifted_grid(grid, blocks) : grid), block, 0, st>>>(p);
+  const int teams = LANES ? THREADS / (LANES + !LANES) : 1, group = SHIFTED ? 8 : 1;
+  const int64_t blocks = (p.rows + group * teams - 1) / (group * teams) * group;
+  const int64_t cap = (int64_t)device_sm_count() * ((LANES ? 2048 : 1024) / block);
+  const int64_t grid = blocks < cap ? blocks : cap / group * group;
+  const int smem = SHIFTED ? pieces * n * (int)sizeof(P) * 2 : 0;
+  if (SHIFTED) {
+    static PerDeviceOnce once;
+    cudaError_t e = once.run([] {
+      return cudaFuncSetAttribute(layer_norm_vec_kernel<T, P, V, LANES, THREADS, SHIFTED>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStaged);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  layer_norm_vec_kernel<T, P, V, LANES, THREADS, SHIFTED><<<(unsigned)grid, block, smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T, typename P, bool SHIFTED>
-void run_pieces(const NormParams& p, int64_t pieces, cudaStream_t st) {
-  if (pieces <= 16)
-    run_vec<T, P, SHIFTED, 4, 256>(p, st);
-  else if (pieces <= 32)
-    run_vec<T, P, SHIFTED, 8, 256>(p, st);
-  else if (pieces <= 64)
-    run_vec<T, P, SHIFTED, 16, 256>(p, st);
-  else if (pieces <= 128)
-    run_vec<T, P, SHIFTED, 32, 256>(p, st);
-  else if (pieces <= 1024)
-    run_vec<T, P, SHIFTED, 0, 512, 2>(p, st);
-  else if (pieces <= 2048)
-    run_vec<T, P, SHIFTED, 0, 1024, 2>(p, st);
-  else
-    run_vec<T, P, SHIFTED, 0, 1024, 4>(p, st);
+cudaError_t run_pieces(const NormParams& p, int64_t pieces, cudaStream_t st) {
+  if (pieces <= 16) return run_vec<T, P, SHIFTED, 4, 256>(p, st);
+  if (pieces <= 32) return run_vec<T, P, SHIFTED, 8, 256>(p, st);
+  if (pieces <= 64) return run_vec<T, P, SHIFTED, 16, 256>(p, st);
+  if (pieces <= 128) return run_vec<T, P, SHIFTED, 32, 256>(p, st);
+  if (pieces <= 1024) return run_vec<T, P, SHIFTED, 0, 512, 2>(p, st);
+  if (pieces <= 2048) return run_vec<T, P, SHIFTED, 0, 1024, 2>(p, st);
+  return run_vec<T, P, SHIFTED, 0, 1024, 4>(p, st);
 }
 
 template <typename T, typename P>
@@ -713,11 +736,10 @@ cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
   const bool shifted = aligned16(p.x) && alike(p.res, p.sres, p.sx, p.rows, n) &&
                        alike(p.sum, p.ssum, p.sx, p.rows, n) && alike(p.y, p.sy, p.sx, p.rows, n);
   if (vec && pieces <= 4096)
-    run_pieces<T, P, false>(p, pieces, st);
-  else if (shifted && pieces < 4096)
-    run_pieces<T, P, true>(p, pieces + 1, st);  // a row may touch one more
-  else
-    layer_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
+    return run_pieces<T, P, false>(p, pieces, st);
+  if (shifted && pieces < 4096 && (pieces + 1) * n * (int64_t)sizeof(P) * 2 <= kMaxStaged)
+    return run_pieces<T, P, true>(p, pieces + 1, st);  // a row may touch one more
+  layer_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
