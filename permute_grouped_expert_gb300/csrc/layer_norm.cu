@@ -485,7 +485,6 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   const T* h = static_cast<const T*>(p.h) + first * p.sh + c0;
   const T* gs = static_cast<const T*>(p.gsum) + (p.gsum ? first * p.sgsum + c0 : 0);
   T* gx = static_cast<T*>(p.gx) + first * p.sgx + c0;
-  const float *mean_at = p.mean + first, *rstd_at = p.rstd + first;
   const int64_t gy_step = step * p.sgy, h_step = step * p.sh, gs_step = step * p.sgsum, gx_step = step * p.sgx;
   int to_fill = rounds;
   auto fill = [&](uint32_t dst) {
@@ -523,16 +522,27 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   }
 #pragma unroll
   for (int i = 0; i < STAGES - 1; i++) fill(own_u32 + i * kStage);
-  float mean = 0.0f, rstd = 0.0f;
-  if (rounds > 0) mean = *mean_at, rstd = *rstd_at;
+  // a row's mean and deviation are a lane's load for a whole batch of rows, a batch
+  // ahead: loaded a row ahead, they were what each row waited for
+  const int batch = PART ? team_threads : 32, lane = t & (batch - 1);
+  float mean_now = 0.0f, rstd_now = 0.0f, mean_next = 0.0f, rstd_next = 0.0f;
+  auto stats = [&](int round, float& m, float& d) {
+    if (round < rounds) m = p.mean[first + round * step], d = p.rstd[first + round * step];
+  };
+  stats(lane, mean_now, rstd_now);
+  stats(batch + lane, mean_next, rstd_next);
   int stage = 0, phase = 0;  // stage: in bytes
   for (int round = 0; round < loops; round++) {
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
     fill(own_u32 + (stage == 0 ? (STAGES - 1) * kStage : stage - kStage));  // the stage of the row before
-    mean_at += step;
-    rstd_at += step;
-    float next_mean = 0.0f, next_rstd = 0.0f;
-    if (round + 1 < rounds) next_mean = *mean_at, next_rstd = *rstd_at;
+    const int place = round & (batch - 1);
+    if (round > 0 && place == 0) {
+      mean_now = mean_next;
+      rstd_now = rstd_next;
+      stats(round + batch + lane, mean_next, rstd_next);
+    }
+    const float mean = __shfl_sync(0xffffffffu, mean_now, place, batch);
+    const float rstd = __shfl_sync(0xffffffffu, rstd_now, place, batch);
     const uint8_t* at = own + stage;
     float su = 0.0f, sx = 0.0f;
     float u[V][N], xhat[V][N];
@@ -586,8 +596,6 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
       if (in[v] && (!PART || round < rounds)) store_piece<T, SHIFTED>(gx + v * v_step, pack<T>(o), mask[v]);
     }
     gx += gx_step;
-    mean = next_mean;
-    rstd = next_rstd;
     phase ^= 1;
     stage = stage == (STAGES - 1) * kStage ? 0 : stage + kStage;
   }
