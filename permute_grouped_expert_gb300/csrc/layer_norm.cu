@@ -511,6 +511,8 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; i++) fill(own_u32 + i * kStage);
   float aw[V][N] = {}, ab[V][N] = {};
   const P* w = static_cast<const P*>(p.w) + (p.w ? c0 : 0);
   float wv[V][N];
@@ -520,8 +522,6 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
     for (int k = 0; k < N; k++) wv[v][k] = 1.0f;
     if (!kAgain && p.w && in[v]) piece_params<T, P, SHIFTED>(wv[v], w + v * v_step, mask[v]);
   }
-#pragma unroll
-  for (int i = 0; i < STAGES - 1; i++) fill(own_u32 + i * kStage);
   // a row's mean and deviation are a lane's load for a whole batch of rows, a batch
   // ahead: loaded a row ahead, they were what each row waited for
   const int batch = PART ? team_threads : 32, lane = t & (batch - 1);
@@ -647,29 +647,33 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   }
 }
 
-// Adds the chunks' partial sums up: 32 columns a CTA, each warp every eighth
-// chunk, the warps in order.
-__global__ void __launch_bounds__(kThreads) layer_norm_bwd_finish_kernel(NormBwdParams p) {
-  __shared__ float2 part[kWarps][32];
+// Adds the chunks' partial sums up: 32 columns a CTA, each warp every 16th chunk
+// (so that a thread's loads are all on their way at once), the warps in order.
+constexpr int kFinishWarps = 16, kFinishLoads = 10;
+
+__global__ void __launch_bounds__(kFinishWarps * 32) layer_norm_bwd_finish_kernel(NormBwdParams p) {
+  __shared__ float2 part[kFinishWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float sw = 0.0f, sb = 0.0f;
+  float2 s = make_float2(0.0f, 0.0f);
   if (c < p.H) {
-#pragma unroll 4
-    for (int64_t k = warp; k < p.chunks; k += kWarps) {
-      sw += p.pw[k * p.H + c];
-      sb += p.pb[k * p.H + c];
+    for (int64_t k0 = warp; k0 < p.chunks; k0 += kFinishWarps * kFinishLoads) {
+      float2 v[kFinishLoads];
+#pragma unroll
+      for (int i = 0; i < kFinishLoads; i++) {
+        const int64_t k = k0 + i * kFinishWarps;
+        v[i] = k < p.chunks ? make_float2(p.pw[k * p.H + c], p.pb[k * p.H + c]) : make_float2(0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < kFinishLoads; i++) s.x += v[i].x, s.y += v[i].y;
     }
   }
-  part[warp][lane] = make_float2(sw, sb);
+  part[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < p.H) {
-    for (int i = 1; i < kWarps; i++) {
-      sw += part[i][lane].x;
-      sb += part[i][lane].y;
-    }
-    if (p.gw) p.gw[c] = sw;
-    if (p.gb) p.gb[c] = sb;
+    for (int i = 1; i < kFinishWarps; i++) s.x += part[i][lane].x, s.y += part[i][lane].y;
+    if (p.gw) p.gw[c] = s.x;
+    if (p.gb) p.gb[c] = s.y;
   }
 }
 
@@ -773,7 +777,7 @@ cudaError_t run_bwd_vec(NormBwdParams p, cudaStream_t st) {
   static_assert(kRing >= kBlock * 16 / (int)sizeof(T) * 4 * V, "the partial sums fit the ring");
   p.pb = p.pw + p.chunks * p.H;
   layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART, SHIFTED><<<(unsigned)p.chunks, block, kRing, st>>>(p, team);
-  if (p.gw || p.gb) layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kThreads, 0, st>>>(p);
+  if (p.gw || p.gb) layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kFinishWarps * 32, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -799,7 +803,7 @@ cudaError_t run_backward(NormBwdParams p, cudaStream_t st) {
   p.pb = p.pw + p.chunks * p.H;
   if (p.gw || p.gb) {
     layer_norm_bwd_cols_kernel<T><<<dim3((unsigned)((p.H + 31) / 32), (unsigned)p.chunks), kThreads, 0, st>>>(p);
-    layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kThreads, 0, st>>>(p);
+    layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kFinishWarps * 32, 0, st>>>(p);
   }
   if (p.rows > 0) layer_norm_bwd_rows_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
   return cudaGetLastError();
