@@ -153,10 +153,25 @@ MOE_DEVICE uint32_t piece_mask(int c0, int H) {
 }
 
 // A piece with zeros outside the row.
+template <typename T>
+MOE_DEVICE uint4 masked_piece(uint4 raw, uint32_t mask) {
+  union {
+    uint4 v;
+    T e[Vec<T>::kN];
+  } u;
+  u.v = raw;
+#pragma unroll
+  for (int k = 0; k < Vec<T>::kN; k++)
+    if (!(mask >> k & 1)) u.e[k] = from_float<T>(0.0f);
+  return u.v;
+}
+
+// A piece with a neighbour's elements, if any, outside the row: what lies there is
+// part of the matrix but behind its last row (`last`), where it is not read.
 template <typename T, bool SHIFTED>
-MOE_DEVICE uint4 load_piece(const T* p, uint32_t mask) {
+MOE_DEVICE uint4 load_piece(const T* p, uint32_t mask, bool last) {
   constexpr int N = Vec<T>::kN;
-  if (!SHIFTED || mask == (1u << N) - 1) return *reinterpret_cast<const uint4*>(p);
+  if (!SHIFTED || !last || mask == (1u << N) - 1) return *reinterpret_cast<const uint4*>(p);
   union {
     uint4 v;
     T e[N];
@@ -229,18 +244,27 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
     return v;
   };
   uint4 x_raw[V], res_raw[V];
-  auto fetch = [&](int64_t r) {
+  bool edge = false;  // a piece of this thread holds elements outside the row
+#pragma unroll
+  for (int v = 0; v < V; v++) edge |= SHIFTED && mask[v] != (1u << N) - 1;
+  auto fetch_x = [&](int64_t r, int n) {
     const T* x = static_cast<const T*>(p.x) + r * p.sx + c0;
 #pragma unroll
     for (int v = 0; v < V; v++) {
       x_raw[v] = make_uint4(0, 0, 0, 0);
-      if (v * team + t < nvec) x_raw[v] = load_piece<T, SHIFTED>(x + v * v_step, mask[v]);
+      if (v * team + t < n) x_raw[v] = load_piece<T, SHIFTED>(x + v * v_step, mask[v], r + 1 == p.rows);
     }
+  };
+  auto fetch_res = [&](int64_t r, int v) {
+    const T* res = static_cast<const T*>(p.res) + r * p.sres + c0 + v * v_step;
+    return load_piece<T, SHIFTED>(res, mask[v], r + 1 == p.rows);
+  };
+  auto fetch = [&](int64_t r) {
+    fetch_x(r, nvec);
     if (p.res) {
-      const T* res = static_cast<const T*>(p.res) + r * p.sres + c0;
 #pragma unroll
       for (int v = 0; v < V; v++)
-        if (v * team + t < nvec) res_raw[v] = load_piece<T, SHIFTED>(res + v * v_step, mask[v]);
+        if (v * team + t < nvec) res_raw[v] = fetch_res(r, v);
     }
   };
   if (kAhead && row_of(blockIdx.x) < p.rows) fetch(row_of(blockIdx.x));
@@ -263,26 +287,21 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
     if (SHIFTED && !LANES && r >= p.rows) break;
     const int n = r < p.rows ? nvec : 0;
     float h[V][N];
-    const T* x = static_cast<const T*>(p.x) + r * p.sx + c0;
-    const T* res = static_cast<const T*>(p.res) + (p.res ? r * p.sres + c0 : 0);
+    if (!kAhead) fetch_x(r, n);
+    if (SHIFTED && edge) {
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-      if (kAhead) {
-        unpack<T>(h[v], x_raw[v]);
-      } else if (v * team + t < n) {
-        unpack<T>(h[v], load_piece<T, SHIFTED>(x + v * v_step, mask[v]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < N; k++) h[v][k] = 0.0f;
-      }
+      for (int v = 0; v < V; v++) x_raw[v] = masked_piece<T>(x_raw[v], mask[v]);
     }
+#pragma unroll
+    for (int v = 0; v < V; v++) unpack<T>(h[v], x_raw[v]);
     if (p.res) {
       T* sum = static_cast<T*>(p.sum) + (p.sum ? r * p.ssum + c0 : 0);
 #pragma unroll
       for (int v = 0; v < V; v++) {
         if (v * team + t < n) {
           float a[N];
-          unpack<T>(a, kAhead ? res_raw[v] : load_piece<T, SHIFTED>(res + v * v_step, mask[v]));
+          const uint4 raw = kAhead ? res_raw[v] : fetch_res(r, v);
+          unpack<T>(a, SHIFTED && edge ? masked_piece<T>(raw, mask[v]) : raw);
 #pragma unroll
           for (int k = 0; k < N; k++) a[k] += h[v][k];
           const uint4 packed = pack<T>(a);  // the norm is that of the sum as stored
@@ -440,26 +459,75 @@ MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, 
 // Rows of 16-byte vectors: one pass that forms gx and a CTA's partial sums of
 // gw and gb.  A team of threads takes a row, V vectors a thread, and keeps the
 // sums of its columns in registers over the rows it meets; its next rows are on
-// their way into a ring of STAGES that is each thread's own, so that only the
-// two sums of a row need a barrier.  What bounds it is the instructions a row
-// takes: places in the ring are constants, addresses run along, vectors past the
-// end are zeros in the ring and computed with the rest, and the weights stay in
-// registers.  Behind the barrier gy and h are read from the ring again where
-// registers cannot hold them.
-constexpr int kBwdBlock = 512;
+// their way into a ring of 8 / V stages that is each thread's own, so that only the
+// two sums of a row need a barrier.  Teams are a part of a warp (kPart), some
+// warps of a CTA (kSome), or a cluster of CTAs (kCluster) for rows that the
+// registers of one cannot hold.  What bounds it is the instructions a row takes:
+// places in the ring are constants, addresses run along, vectors past the end are
+// zeros in the ring and computed with the rest, and the weights stay in registers.
+constexpr int kBwdBlock = 512, kMaxCluster = 4;
+constexpr int kRing = kBwdBlock * 16 * 3 * 8;  // eight vectors a thread of each of three matrices
+enum Team { kPart, kSome, kCluster };
 
-template <typename T, typename P, int V, int STAGES, bool PART, bool SHIFTED>
+MOE_DEVICE uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+MOE_DEVICE uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+MOE_DEVICE void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums of two values over a cluster: every warp leaves its sums in every CTA.
+// `red`: a float2 per warp of the cluster, not written again before its next
+// barrier but one.
+MOE_DEVICE float2 cluster_sum2(float a, float b, float2* red) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, ctas = (int)cluster_size();
+  const bool low = lane < 16;
+  auto halves = [&](float x, float y) {
+    float v = (low ? x : y) + __shfl_xor_sync(0xffffffffu, low ? y : x, 16);
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+  };
+  float v = halves(a, b);
+  if ((lane & 15) < ctas) {
+    const float* to = reinterpret_cast<const float*>(red + cluster_rank() * warps + (threadIdx.x >> 5)) + (low ? 0 : 1);
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(remote)
+                 : "r"((uint32_t)__cvta_generic_to_shared(to)), "r"(lane & 15));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
+  }
+  cluster_barrier();
+  float2 t = make_float2(0.0f, 0.0f);
+  for (int i = lane; i < warps * ctas; i += 32) t.x += red[i].x, t.y += red[i].y;
+  v = halves(t.x, t.y);
+  return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+}
+
+template <typename T, typename P, Team TEAM, int V, bool SHIFTED>
 __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
-  constexpr int N = Vec<T>::kN;
-  constexpr bool kAgain = V * N > 16;  // u, xhat and the weights leave no registers
+  constexpr int N = Vec<T>::kN, STAGES = 8 / V;
+  constexpr bool PART = TEAM == kPart;
   // ring: [stage][matrix][vector of the thread][thread]
   constexpr int kVec = kBwdBlock * 16, kMatrix = V * kVec, kStage = 3 * kMatrix;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 red[2][32];
-  const int team = threadIdx.x / team_threads, teams = blockDim.x / team_threads, t = threadIdx.x % team_threads;
+  __shared__ float2 red[2][TEAM == kCluster ? kMaxCluster * kBwdBlock / 32 : 32];
+  const int ctas = TEAM == kCluster ? (int)cluster_size() : 1, rank = TEAM == kCluster ? (int)cluster_rank() : 0;
+  const int64_t unit = blockIdx.x / ctas, units = gridDim.x / ctas;  // CTA or cluster
+  const int team = threadIdx.x / team_threads, teams = blockDim.x / team_threads;
+  const int t = rank * (int)blockDim.x + threadIdx.x % team_threads;
   const int warp = t >> 5, warps = team_threads >> 5;
-  const int64_t step = (int64_t)gridDim.x * teams;
-  const int64_t first = (int64_t)blockIdx.x * teams + team;
+  const int64_t step = units * teams;
+  const int64_t first = unit * teams + team;
   const int skip = SHIFTED ? (int)(first * p.sgy % N) : 0;
   const int nvec = ((int)p.H + skip + N - 1) / N, c0 = t * N - skip;  // this thread's first column
   const int rounds = first < p.rows ? (int)((p.rows - first + step - 1) / step) : 0;  // rows of this team
@@ -469,12 +537,12 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   const float inv_h = 1.0f / (float)p.H;
   uint8_t* own = smem + threadIdx.x * 16;
   const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
-  const int v_step = team_threads * N;
+  const int v_len = team_threads * ctas, v_step = v_len * N;
   bool in[V];
   uint32_t mask[V];  // of this thread's pieces
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    in[v] = v * team_threads + t < nvec;
+    in[v] = v * v_len + t < nvec;
     mask[v] = SHIFTED ? piece_mask<N>(c0 + v * v_step, (int)p.H) : ~0u;
     if (!in[v])
       for (int i = 0; i < 3 * STAGES; i++) *reinterpret_cast<uint4*>(own + i * kMatrix + v * kVec) = make_uint4(0, 0, 0, 0);
@@ -520,7 +588,7 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   for (int v = 0; v < V; v++) {
 #pragma unroll
     for (int k = 0; k < N; k++) wv[v][k] = 1.0f;
-    if (!kAgain && p.w && in[v]) piece_params<T, P, SHIFTED>(wv[v], w + v * v_step, mask[v]);
+    if (p.w && in[v]) piece_params<T, P, SHIFTED>(wv[v], w + v * v_step, mask[v]);
   }
   // a row's mean and deviation are a lane's load for a whole batch of rows, a batch
   // ahead: loaded a row ahead, they were what each row waited for
@@ -531,7 +599,8 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
   };
   stats(lane, mean_now, rstd_now);
   stats(batch + lane, mean_next, rstd_next);
-  int stage = 0, phase = 0;  // stage: in bytes
+  if (TEAM == kCluster) cluster_barrier();  // its CTAs have started
+  int stage = 0, phase = 0;                 // stage: in bytes
   for (int round = 0; round < loops; round++) {
     asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
     fill(own_u32 + (stage == 0 ? (STAGES - 1) * kStage : stage - kStage));  // the stage of the row before
@@ -549,8 +618,8 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
     auto staged = [&](int matrix, int v) {
       return *reinterpret_cast<const uint4*>(at + matrix * kMatrix + v * kVec);
     };
-    // u = gy w and xhat of vector v
-    auto form = [&](int v) {
+#pragma unroll
+    for (int v = 0; v < V; v++) {
       unpack<T>(u[v], staged(0, v));
       unpack<T>(xhat[v], staged(1, v));
 #pragma unroll
@@ -560,35 +629,24 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
         for (int k = 0; k < N; k++)
           if (!(mask[v] >> k & 1)) u[v][k] = xhat[v][k] = 0.0f;
       }
-    };
-    auto weigh = [&](int v) {
-      if (kAgain && p.w && in[v]) piece_params<T, P, SHIFTED>(wv[v], w + v * v_step, mask[v]);
-#pragma unroll
-      for (int k = 0; k < N; k++) u[v][k] *= wv[v][k];
-    };
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-      form(v);
 #pragma unroll
       for (int k = 0; k < N; k++) {
         aw[v][k] = fmaf(u[v][k], xhat[v][k], aw[v][k]);
         ab[v][k] += u[v][k];
       }
-      weigh(v);
 #pragma unroll
       for (int k = 0; k < N; k++) {
+        u[v][k] *= wv[v][k];
         su += u[v][k];
         sx = fmaf(u[v][k], xhat[v][k], sx);
       }
     }
-    const float2 sums = team_sum2<PART>(su, sx, red[phase] + team * warps, warp, warps, team + 1, team_threads);
+    const float2 sums = TEAM == kCluster ? cluster_sum2(su, sx, red[phase])
+                                         : team_sum2<PART>(su, sx, red[phase] + team * warps, warp, warps, team + 1,
+                                                           team_threads);
     const float mu = sums.x * inv_h, mx = sums.y * inv_h;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      if (kAgain) {
-        form(v);
-        weigh(v);
-      }
       float o[N];
       unpack<T>(o, p.gsum ? staged(2, v) : make_uint4(0, 0, 0, 0));
 #pragma unroll
@@ -607,6 +665,14 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
 #pragma unroll
   for (int sum = 0; sum < 2; sum++) {
     float(&acc)[V][N] = sum ? ab : aw;
+    if (SHIFTED && TEAM == kCluster) {
+#pragma unroll
+      for (int v = 0; v < V; v++)
+#pragma unroll
+        for (int k = 0; k < N; k++)
+          if (in[v] && mask[v] >> k & 1) (sum ? p.pb : p.pw)[unit * p.H + c0 + v * v_step + k] = acc[v][k];
+      continue;
+    }
     if (SHIFTED) {  // by column: the teams' pieces begin at different ones
       __syncthreads();
 #pragma unroll
@@ -618,7 +684,7 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
       for (int c = threadIdx.x; c < (int)p.H; c += blockDim.x) {
         float s = part[c];
         for (int j = 1; j < teams; j++) s += part[j * (int)p.H + c];
-        (sum ? p.pb : p.pw)[blockIdx.x * p.H + c] = s;
+        (sum ? p.pb : p.pw)[unit * p.H + c] = s;
       }
       continue;
     }
@@ -636,7 +702,7 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
 #pragma unroll
             for (int k = 0; k < N; k++) acc[v][k] += part[(v * N + k) * kBwdBlock + j * team_threads + t];
     }
-    float* out = (sum ? p.pb : p.pw) + blockIdx.x * p.H + t * N;
+    float* out = (sum ? p.pb : p.pw) + unit * p.H + t * N;
 #pragma unroll
     for (int v = 0; v < V; v++)
       if (team == 0 && in[v])
@@ -755,37 +821,102 @@ cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T, typename P, int V, int STAGES, bool PART, bool SHIFTED>
-cudaError_t run_bwd_vec(NormBwdParams p, cudaStream_t st) {
-  constexpr int kBlock = kBwdBlock, kRing = kBlock * 16 * 3 * V * STAGES;
-  static PerDeviceOnce once;
-  cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART, SHIFTED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kRing);
-  });
-  if (e != cudaSuccess) return e;
-  constexpr int n = 16 / (int)sizeof(T);
-  const int want = ((int)(p.H + (SHIFTED ? n - 1 : 0) + n - 1) / n + V - 1) / V;
-  const int team = !PART ? (want + 31) / 32 * 32 : want <= 4 ? 4 : want <= 8 ? 8 : 16, whole = PART ? 32 / team : 1;
-  int teams = team >= 64 && kBlock / team > 15 ? 15 : kBlock / team;  // named barriers 1 to 15
-  while (teams > whole && p.rows < (int64_t)teams * device_sm_count()) teams -= whole;  // whole warps
-  const int64_t blocks = (p.rows + teams - 1) / teams, sms = device_sm_count();
-  p.chunks = blocks < sms ? blocks : sms;
-  if (p.chunks > kMaxChunks) p.chunks = kMaxChunks;
-  if (SHIFTED) p.chunks = shifted_grid(p.chunks, blocks);
-  const int block = team * teams;
-  static_assert(kRing >= kBlock * 16 / (int)sizeof(T) * 4 * V, "the partial sums fit the ring");
+// Partial sums of `chunks` units, after the kernel on `chunks` x `ctas` CTAs of them.
+template <typename T, typename P, Team TEAM, int V, bool SHIFTED>
+cudaError_t run_bwd_units(NormBwdParams p, int64_t chunks, int ctas, int block, int team, cudaStream_t st) {
+  static_assert(kRing >= kBwdBlock * 16 / (int)sizeof(T) * 4 * V, "the partial sums fit the ring");
+  p.chunks = chunks;
   p.pb = p.pw + p.chunks * p.H;
-  layer_norm_bwd_vec_kernel<T, P, V, STAGES, PART, SHIFTED><<<(unsigned)p.chunks, block, kRing, st>>>(p, team);
+  cudaLaunchAttribute cluster = {};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = (unsigned)ctas;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(chunks * ctas));
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = kRing;
+  cfg.stream = st;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, layer_norm_bwd_vec_kernel<T, P, TEAM, V, SHIFTED>, p, team);
+  if (e != cudaSuccess) return e;
   if (p.gw || p.gb) layer_norm_bwd_finish_kernel<<<(unsigned)((p.H + 31) / 32), kFinishWarps * 32, 0, st>>>(p);
   return cudaGetLastError();
 }
 
+template <typename T, typename P, Team TEAM, int V, bool SHIFTED>
+cudaError_t allow_ring() {
+  static PerDeviceOnce once;
+  return once.run([] {
+    return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, TEAM, V, SHIFTED>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+  });
+}
+
+template <typename T, typename P, Team TEAM, int V, bool SHIFTED>
+cudaError_t run_bwd_teams(const NormBwdParams& p, int64_t pieces, cudaStream_t st) {
+  cudaError_t e = allow_ring<T, P, TEAM, V, SHIFTED>();
+  if (e != cudaSuccess) return e;
+  constexpr bool kParts = TEAM == kPart;
+  const int want = (int)(pieces + V - 1) / V;
+  const int team = !kParts ? (want + 31) / 32 * 32 : want <= 4 ? 4 : want <= 8 ? 8 : 16, whole = kParts ? 32 / team : 1;
+  int teams = kBwdBlock / team;  // (teams of several warps: at most eight, named barriers 1 to 8)
+  while (teams > whole && p.rows < (int64_t)teams * device_sm_count()) teams -= whole;  // whole warps
+  const int64_t blocks = (p.rows + teams - 1) / teams, sms = device_sm_count();
+  int64_t chunks = blocks < sms ? blocks : sms;
+  if (chunks > kMaxChunks) chunks = kMaxChunks;
+  if (SHIFTED) chunks = shifted_grid(chunks, blocks);
+  return run_bwd_units<T, P, TEAM, V, SHIFTED>(p, chunks, 1, team * teams, team, st);
+}
+
+template <typename T, typename P, int V, bool SHIFTED>
+cudaError_t run_bwd_clusters(const NormBwdParams& p, int64_t pieces, cudaStream_t st) {
+  cudaError_t e = allow_ring<T, P, kCluster, V, SHIFTED>();
+  if (e != cudaSuccess) return e;
+  const int ctas = pieces <= 2 * V * kBwdBlock ? 2 : kMaxCluster;
+  const int want = (int)(pieces + ctas - 1) / ctas, block = ((want + V - 1) / V + 31) / 32 * 32;
+  // as many clusters as run at once: the GPU's parts need not be whole clusters
+  static int at_once[PerDeviceOnce::kMaxDevices][2];
+  static PerDeviceOnce once;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run([&] {
+    cudaError_t r = cudaSuccess;
+    for (int i = 0; i < 2 && r == cudaSuccess; i++) {
+      cudaLaunchAttribute cluster = {};
+      cluster.id = cudaLaunchAttributeClusterDimension;
+      cluster.val.clusterDim.x = 2u << i;
+      cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2u << i);
+      cfg.blockDim = dim3(kBwdBlock);
+      cfg.dynamicSmemBytes = kRing;
+      cfg.attrs = &cluster;
+      cfg.numAttrs = 1;
+      r = cudaOccupancyMaxActiveClusters(&at_once[dev][i], layer_norm_bwd_vec_kernel<T, P, kCluster, V, SHIFTED>, &cfg);
+    }
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  int64_t chunks = at_once[dev][ctas / 4] < 1 ? 1 : at_once[dev][ctas / 4];
+  if (chunks > kMaxChunks) chunks = kMaxChunks;
+  if (chunks > p.rows) chunks = p.rows;
+  if (SHIFTED) chunks = shifted_grid(chunks, p.rows);
+  return run_bwd_units<T, P, kCluster, V, SHIFTED>(p, chunks, ctas, block, block, st);
+}
+
+// Vectors that a thread's registers hold beside the columns' sums.
+template <typename T>
+constexpr int kMostVecs = 16 / Vec<T>::kN;
+
 template <typename T, typename P, bool SHIFTED>
 cudaError_t run_bwd_pieces(const NormBwdParams& p, int64_t pieces, cudaStream_t st) {
-  if (pieces <= 32) return run_bwd_vec<T, P, 2, 4, true, SHIFTED>(p, st);
-  if (pieces <= 1024) return run_bwd_vec<T, P, 2, 4, false, SHIFTED>(p, st);
-  return run_bwd_vec<T, P, 4, 2, false, SHIFTED>(p, st);
+  if (pieces <= 32) return run_bwd_teams<T, P, kPart, 2, SHIFTED>(p, pieces, st);
+  if (pieces <= 2 * kBwdBlock) return run_bwd_teams<T, P, kSome, 2, SHIFTED>(p, pieces, st);
+  if constexpr (kMostVecs<T> > 2)
+    if (pieces <= kMostVecs<T> * kBwdBlock) return run_bwd_teams<T, P, kSome, kMostVecs<T>, SHIFTED>(p, pieces, st);
+  return run_bwd_clusters<T, P, kMostVecs<T>, SHIFTED>(p, pieces, st);
 }
 
 template <typename T, typename P>
@@ -796,8 +927,9 @@ cudaError_t run_backward(NormBwdParams p, cudaStream_t st) {
                    vector_rows(p.gsum, p.sgsum, p.rows, b) && vector_rows(p.gx, p.sgx, p.rows, b) && aligned16(p.w);
   const bool shifted = aligned16(p.gy) && alike(p.h, p.sh, p.sgy, p.rows, n) &&
                        alike(p.gsum, p.sgsum, p.sgy, p.rows, n) && alike(p.gx, p.sgx, p.sgy, p.rows, n);
-  if (p.rows > 0 && vec && pieces <= 2048) return run_bwd_pieces<T, P, false>(p, pieces, st);
-  if (p.rows > 0 && shifted && pieces < 2048) return run_bwd_pieces<T, P, true>(p, pieces + 1, st);  // one more
+  constexpr int64_t kMost = kMaxCluster * kMostVecs<T> * kBwdBlock;
+  if (p.rows > 0 && vec && pieces <= kMost) return run_bwd_pieces<T, P, false>(p, pieces, st);
+  if (p.rows > 0 && shifted && pieces < kMost) return run_bwd_pieces<T, P, true>(p, pieces + 1, st);  // one more
   p.chunks = bwd_chunks(p.rows);
   p.rows_per_chunk = (p.rows + p.chunks - 1) / p.chunks;
   p.pb = p.pw + p.chunks * p.H;

@@ -276,3 +276,42 @@ def test_refusals():
         moe.moe_layer_norm_backward(x, y, w, s, s, y)
     with pytest.raises(moe.MoeError):
         moe.moe_layer_norm_backward(x, y, w, None, s, torch.empty_like(x))
+
+
+@pytest.mark.parametrize("dtype", bu.DTYPES)
+@pytest.mark.parametrize("rows,H", [(3, 8193), (200, 16384), (170, 9001), (90, 16383), (100, 12000), (11, 4100)])
+def test_backward_of_rows_wider_than_a_block(rows, H, dtype):
+    """Rows that clusters share, aligned and not, more of them than clusters and fewer."""
+    test_backward(rows, H, dtype)
+
+
+@pytest.mark.parametrize("rows,H,dtype", [(200000, 8, torch.bfloat16), (100000, 13, torch.float16),
+                                          (170000, 264, torch.bfloat16), (80000, 260, torch.float32)])
+def test_backward_of_many_rows(rows, H, dtype):
+    """More rows a team than the statistics it loads at once, several times over."""
+    moe = moe_mod()
+    x, w, _ = inputs(rows, H, dtype, torch.float32)
+    _, mean, rstd, _ = bu.norm_forward(x, None, None, EPS)
+    mean, rstd = mean.float(), rstd.float()
+    gy = bu.randn(rows, H, seed=11, dtype=dtype)
+    got = backward(moe, gy, x, w, mean, rstd)
+    refs = bu.norm_backward(gy, x, w, mean, rstd, None)
+    tols = bu.norm_backward_tol(gy, x, w, mean, rstd, None, dtype)
+    for name, g, r, t in zip(("gx", "gw", "gb"), got, refs, tols):
+        bu.assert_within(g, r, t, name)
+
+
+@pytest.mark.parametrize("H", [1024, 1001, 5001])
+def test_a_row_of_nans_stays_alone(H):
+    """Unaligned rows share 16-byte pieces: what is wrong in one does not reach the next."""
+    moe = moe_mod()
+    x, w, b = inputs(40, H, torch.bfloat16, torch.bfloat16)
+    x[7] = float("nan")
+    x[20] = float("inf")
+    y, _, mean, rstd = forward(moe, x, w, b, None)
+    gx, _, _ = backward(moe, x, x, w, mean.cpu(), rstd.cpu())
+    bad = torch.zeros(40, dtype=torch.bool)
+    bad[7] = bad[20] = True
+    for out in (y, gx):
+        assert torch.equal(torch.isnan(out).all(1).cpu(), bad)
+        assert torch.equal(torch.isnan(out).any(1).cpu(), bad)
