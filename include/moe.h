@@ -522,8 +522,10 @@ typedef struct moe_norm {
  * NULL (1 and 0).  sum: h (optional; may be x or residual itself, with the same
  * stride, and must not overlap them otherwise); it needs a residual.  mean,
  * rstd: device fp32 [rows], each optional; the backward pass reads both.  y
- * must not overlap an input.  Any row stride and any alignment of an element;
- * 16-byte aligned rows (base, stride, H) take the 128-bit path. */
+ * must not overlap an input.  Rows may begin at any element and lie any distance
+ * of at least H apart; rows that begin alike modulo 16 bytes in every matrix
+ * (16-byte aligned bases, strides that agree modulo 16 bytes) move in 128-bit
+ * pieces, others element by element. */
 MOE_API moe_status moe_layer_norm(const moe_norm* norm, const moe_rows* x, const moe_rows* residual,
                                   const void* weight, const void* bias, const moe_rows* y, const moe_rows* sum,
                                   float* mean, float* rstd, void* stream);
@@ -636,7 +638,8 @@ enum {
  * token that holds an infinity or a NaN gives NaN.  x: M rows of Kd (16-byte
  * aligned, stride a multiple of 8); y: M rows of N (N/2 with SwiGLU; N must be
  * even); addend: optional, as y (it may be y itself), only without SwiGLU.  y
- * must not overlap x.  Any M >= 0; the weights are read once per 32 tokens. */
+ * must not overlap x.  Any M >= 0; the weights are
+ * streamed once for up to 32 tokens, again for the next 32. */
 MOE_API moe_status moe_w4_matvec(const moe_w4* w, int64_t M, const moe_rows* x, int32_t activation,
                                  const moe_rows* addend, const moe_rows* y, void* stream);
 

@@ -7,6 +7,18 @@
 //   gx = rstd (u - sum u / H - xhat sum(u xhat) / H) (+ gsum)
 //   gw = sum over rows of gy xhat,  gb = sum over rows of gy
 // Every sum is fp32: a lane's elements in order, then a fixed shuffle tree.
+//
+// Both passes read and write each row once (forward 2 to 4 values an element,
+// backward 3 or 4), so that HBM is the floor.  Device times on one GB300 (GB/s of
+// that floor beside a copy's 6793):
+//   forward   8192 x 7168 bf16 + residual   76 us, 6180     65536 x 1024   48 us, 5630
+//             4096 x 4096 fp32              26 us, 5200     8000 x 1001    15 us, 2070
+//             one row of 7168               3.4 us
+//   backward  8192 x 7168 bf16 + gsum       75 us, 6240     65536 x 1024   70 us, 5780
+//             4096 x 4096 fp32              35 us, 5720     1531 x 1537 fp32 11.7 us, 2410
+//             2048 x 16384 bf16             64 us, 3160     64 x 7168      7.8 us
+// Calls of a few microseconds are bound by their launches and one row's chain of
+// load, two sums and store.
 #include <type_traits>
 
 #include "block_common.cuh"
@@ -143,6 +155,9 @@ MOE_DEVICE uint4 pack(const float (&in)[Vec<T>::kN]) {
 // SHIFTED kernels take rows that start anywhere as the aligned 16-byte pieces
 // that hold them: `skip` elements of a row's first piece lie before it.  A team's
 // rows lie a multiple of 16 bytes apart, so that its threads keep their columns.
+// Element by element (the any kernels) 8000 x 1001 bf16 took 35 us forward and 49
+// backward; as pieces it takes 15 and 22.  They need rows that start alike in
+// every matrix; what does not is left to the any kernels.
 // Bit k: element k of the piece whose first column is c0 belongs to the row.
 template <int N>
 MOE_DEVICE uint32_t piece_mask(int c0, int H) {
@@ -215,7 +230,9 @@ MOE_DEVICE void piece_params(float (&out)[Vec<T>::kN], const P* p, uint32_t mask
 // Rows of 16-byte vectors held in registers between the mean, the variance and
 // the result, so that the row is read once, V vectors a thread.  LANES threads
 // of a warp take a row; or (0) a CTA does, and its next row is on its way while
-// it reduces and writes this one: two barriers a row would leave the memory idle.
+// it reduces and writes this one: two barriers a row would leave the memory idle
+// (8192 x 7168 bf16 with a residual: 109 us without, 76 with).  Teams of a warp
+// have enough others to wait for: with a ring of their own 8192 x 7168 took 162.
 template <typename T, typename P, int V, int LANES, int THREADS, bool SHIFTED>
 __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_norm_vec_kernel(NormParams p) {
   constexpr int N = Vec<T>::kN;
@@ -465,9 +482,14 @@ MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, 
 // registers of one cannot hold.  What bounds it is the instructions a row takes:
 // places in the ring are constants, addresses run along, vectors past the end are
 // zeros in the ring and computed with the rest, and the weights stay in registers.
-constexpr int kBwdBlock = 512, kMaxCluster = 4;
-constexpr int kRing = kBwdBlock * 16 * 3 * 8;  // eight vectors a thread of each of three matrices
+// Of a cluster's CTAs two share an SM, so that one works while the other waits for
+// its cluster (1024 x 16384 fp32: 47 us, with one of 512 threads 52).
+constexpr int kBwdBlock = 512, kClusterBlock = 256, kMaxCluster = 8;
 enum Team { kPart, kSome, kCluster };
+template <Team TEAM>
+constexpr int kBlockOf = TEAM == kCluster ? kClusterBlock : kBwdBlock;
+template <Team TEAM>
+constexpr int kRing = kBlockOf<TEAM> * 16 * 3 * 8;  // eight vectors a thread of each of three matrices
 
 MOE_DEVICE uint32_t cluster_rank() {
   uint32_t r;
@@ -514,13 +536,13 @@ MOE_DEVICE float2 cluster_sum2(float a, float b, float2* red) {
 }
 
 template <typename T, typename P, Team TEAM, int V, bool SHIFTED>
-__global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
+__global__ void __launch_bounds__(kBlockOf<TEAM>, 512 / kBlockOf<TEAM>) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
   constexpr int N = Vec<T>::kN, STAGES = 8 / V;
   constexpr bool PART = TEAM == kPart;
   // ring: [stage][matrix][vector of the thread][thread]
-  constexpr int kVec = kBwdBlock * 16, kMatrix = V * kVec, kStage = 3 * kMatrix;
+  constexpr int kVec = kBlockOf<TEAM> * 16, kMatrix = V * kVec, kStage = 3 * kMatrix;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 red[2][TEAM == kCluster ? kMaxCluster * kBwdBlock / 32 : 32];
+  __shared__ float2 red[2][TEAM == kCluster ? kMaxCluster * kClusterBlock / 32 : 32];
   const int ctas = TEAM == kCluster ? (int)cluster_size() : 1, rank = TEAM == kCluster ? (int)cluster_rank() : 0;
   const int64_t unit = blockIdx.x / ctas, units = gridDim.x / ctas;  // CTA or cluster
   const int team = threadIdx.x / team_threads, teams = blockDim.x / team_threads;
@@ -693,14 +715,14 @@ __global__ void __launch_bounds__(kBwdBlock, 1) layer_norm_bwd_vec_kernel(NormBw
 #pragma unroll
       for (int v = 0; v < V; v++)
 #pragma unroll
-        for (int k = 0; k < N; k++) part[(v * N + k) * kBwdBlock + threadIdx.x] = acc[v][k];
+        for (int k = 0; k < N; k++) part[(v * N + k) * kBlockOf<TEAM> + threadIdx.x] = acc[v][k];
       __syncthreads();
       if (team == 0)
         for (int j = 1; j < teams; j++)
 #pragma unroll
           for (int v = 0; v < V; v++)
 #pragma unroll
-            for (int k = 0; k < N; k++) acc[v][k] += part[(v * N + k) * kBwdBlock + j * team_threads + t];
+            for (int k = 0; k < N; k++) acc[v][k] += part[(v * N + k) * kBlockOf<TEAM> + j * team_threads + t];
     }
     float* out = (sum ? p.pb : p.pw) + unit * p.H + t * N;
 #pragma unroll
@@ -793,6 +815,12 @@ cudaError_t run_vec(const NormParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// Up to 128 pieces a part of a warp takes a row, so that the narrowest rows leave
+// no lanes idle (65536 x 128 bf16: 19 us with a warp a row, 8.7 so); above, the
+// warps that hold it at two pieces a thread, which leaves registers for the next
+// row.  Four pieces a thread (8192 x 7168: 157 us, against 76) and a warp with
+// eight (4096 x 2048: 11.8, against 10.3) are slower; only rows past 2048 pieces
+// need four.
 template <typename T, typename P, bool SHIFTED>
 cudaError_t run_pieces(const NormParams& p, int64_t pieces, cudaStream_t st) {
   if (pieces <= 16) return run_vec<T, P, SHIFTED, 4, 256>(p, st);
@@ -824,7 +852,7 @@ cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
 // Partial sums of `chunks` units, after the kernel on `chunks` x `ctas` CTAs of them.
 template <typename T, typename P, Team TEAM, int V, bool SHIFTED>
 cudaError_t run_bwd_units(NormBwdParams p, int64_t chunks, int ctas, int block, int team, cudaStream_t st) {
-  static_assert(kRing >= kBwdBlock * 16 / (int)sizeof(T) * 4 * V, "the partial sums fit the ring");
+  static_assert(kRing<TEAM> >= kBlockOf<TEAM> * 16 / (int)sizeof(T) * 4 * V, "the partial sums fit the ring");
   p.chunks = chunks;
   p.pb = p.pw + p.chunks * p.H;
   cudaLaunchAttribute cluster = {};
@@ -834,7 +862,7 @@ cudaError_t run_bwd_units(NormBwdParams p, int64_t chunks, int ctas, int block, 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(chunks * ctas));
   cfg.blockDim = dim3((unsigned)block);
-  cfg.dynamicSmemBytes = kRing;
+  cfg.dynamicSmemBytes = kRing<TEAM>;
   cfg.stream = st;
   cfg.attrs = &cluster;
   cfg.numAttrs = ctas > 1 ? 1 : 0;
@@ -849,7 +877,7 @@ cudaError_t allow_ring() {
   static PerDeviceOnce once;
   return once.run([] {
     return cudaFuncSetAttribute(layer_norm_bwd_vec_kernel<T, P, TEAM, V, SHIFTED>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRing<TEAM>);
   });
 }
 
@@ -873,25 +901,27 @@ template <typename T, typename P, int V, bool SHIFTED>
 cudaError_t run_bwd_clusters(const NormBwdParams& p, int64_t pieces, cudaStream_t st) {
   cudaError_t e = allow_ring<T, P, kCluster, V, SHIFTED>();
   if (e != cudaSuccess) return e;
-  const int ctas = pieces <= 2 * V * kBwdBlock ? 2 : kMaxCluster;
+  int log_ctas = 1;
+  while (pieces > ((int64_t)V * kClusterBlock << log_ctas)) log_ctas++;
+  const int ctas = 1 << log_ctas;
   const int want = (int)(pieces + ctas - 1) / ctas, block = ((want + V - 1) / V + 31) / 32 * 32;
   // as many clusters as run at once: the GPU's parts need not be whole clusters
-  static int at_once[PerDeviceOnce::kMaxDevices][2];
+  static int at_once[PerDeviceOnce::kMaxDevices][4];  // by log2 of the size
   static PerDeviceOnce once;
   int dev = 0;
   e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = once.run([&] {
     cudaError_t r = cudaSuccess;
-    for (int i = 0; i < 2 && r == cudaSuccess; i++) {
+    for (int i = 1; i < 4 && r == cudaSuccess; i++) {
       cudaLaunchAttribute cluster = {};
       cluster.id = cudaLaunchAttributeClusterDimension;
-      cluster.val.clusterDim.x = 2u << i;
+      cluster.val.clusterDim.x = 1u << i;
       cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2u << i);
-      cfg.blockDim = dim3(kBwdBlock);
-      cfg.dynamicSmemBytes = kRing;
+      cfg.gridDim = dim3(1u << i);
+      cfg.blockDim = dim3(kClusterBlock);
+      cfg.dynamicSmemBytes = kRing<kCluster>;
       cfg.attrs = &cluster;
       cfg.numAttrs = 1;
       r = cudaOccupancyMaxActiveClusters(&at_once[dev][i], layer_norm_bwd_vec_kernel<T, P, kCluster, V, SHIFTED>, &cfg);
@@ -899,14 +929,19 @@ cudaError_t run_bwd_clusters(const NormBwdParams& p, int64_t pieces, cudaStream_
     return r;
   });
   if (e != cudaSuccess) return e;
-  int64_t chunks = at_once[dev][ctas / 4] < 1 ? 1 : at_once[dev][ctas / 4];
+  int64_t chunks = at_once[dev][log_ctas] < 1 ? 1 : at_once[dev][log_ctas];
   if (chunks > kMaxChunks) chunks = kMaxChunks;
   if (chunks > p.rows) chunks = p.rows;
   if (SHIFTED) chunks = shifted_grid(chunks, p.rows);
   return run_bwd_units<T, P, kCluster, V, SHIFTED>(p, chunks, ctas, block, block, st);
 }
 
-// Vectors that a thread's registers hold beside the columns' sums.
+// Up to 32 pieces teams are a part of a warp (65536 x 128 bf16: 21 us, with a warp
+// a row 31), up to 1024 some warps at two pieces a thread.  Above, what registers
+// can hold beside the columns' sums decides: fp32 rows go on with four pieces a
+// thread (2048 x 8192: 37 us; clusters 60), 16-bit rows would spill (2048 x 16384:
+// 97 us) and take clusters (64).
+// Vectors that a thread's registers hold beside the columns' sums:
 template <typename T>
 constexpr int kMostVecs = 16 / Vec<T>::kN;
 
@@ -927,7 +962,7 @@ cudaError_t run_backward(NormBwdParams p, cudaStream_t st) {
                    vector_rows(p.gsum, p.sgsum, p.rows, b) && vector_rows(p.gx, p.sgx, p.rows, b) && aligned16(p.w);
   const bool shifted = aligned16(p.gy) && alike(p.h, p.sh, p.sgy, p.rows, n) &&
                        alike(p.gsum, p.sgsum, p.sgy, p.rows, n) && alike(p.gx, p.sgx, p.sgy, p.rows, n);
-  constexpr int64_t kMost = kMaxCluster * kMostVecs<T> * kBwdBlock;
+  constexpr int64_t kMost = kMaxCluster * kMostVecs<T> * kClusterBlock;
   if (p.rows > 0 && vec && pieces <= kMost) return run_bwd_pieces<T, P, false>(p, pieces, st);
   if (p.rows > 0 && shifted && pieces < kMost) return run_bwd_pieces<T, P, true>(p, pieces + 1, st);  // one more
   p.chunks = bwd_chunks(p.rows);

@@ -5,10 +5,19 @@
 // that a warp works on 32 / L tokens at once.  The selection looks for a
 // threshold that exactly K scores reach: it guesses one from the scores' mean and
 // deviation, shrinks an interval by the counts, and stops at the first count
-// that is K.  Where scores are equal no threshold may have that count; the interval then closes on one
-// value by bisection of its bit pattern, everything above it is chosen and the
-// lowest experts among those equal to it fill the rest.  Ids come out ascending.
-// Scores and sums are fp32 in a fixed order.
+// that is K.  Where scores are equal no threshold may have that count; the
+// interval then closes on one value by bisection of its bit pattern, everything
+// above it is chosen and the lowest experts among those equal to it fill the
+// rest.  Ids come out ascending.  Scores and sums are fp32 in a fixed order.
+//
+// The bytes are few (65536 x 256 fp32 logits: 10 us of HBM); what bounds both
+// directions is instructions, and of the forward pass those of the pipe that
+// compares: about 600 a warp for 256 experts, four to five counts among them.
+// Hence no sort, no selection one by one, and one pass for the common case of
+// finite logits.  Device times on one GB300:
+//   65536 x 256 fp32 top-8 45 us, top-36 with the softmax over all 59 us;
+//   65536 x 64 bf16 22 us; 16384 x 1024 top-32 33 us; 64 x 256 3.8 us
+//   gradient 65536 x 256 top-8 27 us (softmax over all 31), 8192 x 256 4.1 us
 #include <cmath>
 #include <type_traits>
 
@@ -419,7 +428,9 @@ struct RouterBwdParams {
 
 // Gradient where only the chosen take part: a lane takes one of them (or a few),
 // and the row goes out through shared memory, zeros but for theirs.  Of the
-// logits, and of a sparse map's gradients, only those of the chosen are read.
+// logits, and of a sparse map's gradients, only those of the chosen are read
+// (16384 x 1024 top-32 fp32: 20 us; as a pass over the row, which the kernel
+// below makes for the plain softmax, 66).
 template <typename T, int V, int L, int SCORE, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, V == 8 ? (SPARSE ? 5 : 4) : 2) router_bwd_chosen_kernel(RouterBwdParams p) {
   constexpr int kTokens = 32 / L, N = 16 / sizeof(T), kVecs = V / N;
@@ -628,7 +639,8 @@ unsigned token_grid(int64_t T) {
 }
 
 // Eight experts a lane and as few lanes a token as hold them, up to a warp; more
-// experts a lane beyond 256.
+// experts a lane beyond 256.  (A warp a token, whatever E: 65536 x 16 47 us, so 7.6;
+// eight experts are two fp32 vectors or one 16-bit vector of a lane.)
 #define MOE_ROUTER_SHAPE(RUN)         \
   do {                                \
     if (p.E <= 8) RUN(8, 1);          \
