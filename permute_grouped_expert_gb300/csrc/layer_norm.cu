@@ -790,7 +790,10 @@ bool alike(const void* p, int64_t stride, int64_t other, int64_t rows, int n) {
 }
 
 // CTAs that keep a team's rows a multiple of 16 bytes apart, unless each team has one row.
-int64_t shifted_grid(int64_t grid, int64_t blocks) { return blocks > grid && grid >= 8 ? grid / 8 * 8 : grid; }
+int64_t shifted_grid(int64_t grid, int64_t blocks) {
+  if (blocks <= 8) return blocks;
+  return grid >= blocks ? blocks : grid < 8 ? 8 : grid / 8 * 8;
+}
 
 constexpr int kMaxStaged = 200 * 1024;  // bytes of parameters a CTA stages at the most
 
@@ -801,7 +804,7 @@ cudaError_t run_vec(const NormParams& p, cudaStream_t st) {
   const int teams = LANES ? THREADS / (LANES + !LANES) : 1, group = SHIFTED ? 8 : 1;
   const int64_t blocks = (p.rows + group * teams - 1) / (group * teams) * group;
   const int64_t cap = (int64_t)device_sm_count() * ((LANES ? 2048 : 1024) / block);
-  const int64_t grid = blocks < cap ? blocks : cap / group * group;
+  const int64_t grid = blocks < cap ? blocks : cap < group ? group : cap / group * group;
   const int smem = SHIFTED ? pieces * n * (int)sizeof(P) * 2 : 0;
   if (SHIFTED) {
     static PerDeviceOnce once;
