@@ -11,9 +11,9 @@
 // Both passes read and write each row once (forward 2 to 4 values an element,
 // backward 3 or 4), so that HBM is the floor.  Device times on one GB300 (GB/s of
 // that floor beside a copy's 6793):
-//   forward   8192 x 7168 bf16 + residual   76 us, 6180     65536 x 1024   48 us, 5630
+//   forward   8192 x 7168 bf16 + residual   73 us, 6400     65536 x 1024   47 us, 5750
 //             4096 x 4096 fp32              26 us, 5200     8000 x 1001    15 us, 2070
-//             one row of 7168               3.4 us
+//             one row of 7168               3.3 us
 //   backward  8192 x 7168 bf16 + gsum       75 us, 6240     65536 x 1024   70 us, 5780
 //             4096 x 4096 fp32              35 us, 5720     1531 x 1537 fp32 11.7 us, 2410
 //             2048 x 16384 bf16             64 us, 3160     64 x 7168      7.8 us
@@ -231,12 +231,16 @@ MOE_DEVICE void piece_params(float (&out)[Vec<T>::kN], const P* p, uint32_t mask
 // the result, so that the row is read once, V vectors a thread.  LANES threads
 // of a warp take a row; or (0) a CTA does, and its next row is on its way while
 // it reduces and writes this one: two barriers a row would leave the memory idle
-// (8192 x 7168 bf16 with a residual: 109 us without, 76 with).  Teams of a warp
+// (8192 x 7168 bf16 with a residual: 109 us without, 76 when it came in).  Teams of a warp
 // have enough others to wait for: with a ring of their own 8192 x 7168 took 162.
 template <typename T, typename P, int V, int LANES, int THREADS, bool SHIFTED>
 __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_norm_vec_kernel(NormParams p) {
   constexpr int N = Vec<T>::kN;
   constexpr bool kAhead = LANES == 0;
+  // vectors past the end are computed with the rest (0, and the first weights) and
+  // not stored, where registers allow: a few branches a row less (8192 x 7168 with a
+  // residual 75.7 -> 73.4 us; 65536 x 1024, which spills, 47.8 -> 52.0)
+  constexpr bool kStraight = LANES == 0 && !SHIFTED;
   __shared__ float2 red[2][THREADS / 32];
   const int team = LANES ? LANES : (int)blockDim.x, teams = LANES ? THREADS / LANES : 1;
   const int t = LANES ? threadIdx.x % LANES : threadIdx.x;
@@ -337,29 +341,30 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
     float q = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      if (v * team + t < n) {
+      const bool in = v * team + t < n;
+      if (!kStraight && !in) continue;
+      const float off = in ? mean : 0.0f;
 #pragma unroll
-        for (int k = 0; k < N; k++) {
-          h[v][k] -= mean;
-          if (SHIFTED) h[v][k] = mask[v] >> k & 1 ? h[v][k] : 0.0f;
-          q = fmaf(h[v][k], h[v][k], q);
-        }
+      for (int k = 0; k < N; k++) {
+        h[v][k] -= off;
+        if (SHIFTED) h[v][k] = mask[v] >> k & 1 ? h[v][k] : 0.0f;
+        q = fmaf(h[v][k], h[v][k], q);
       }
     }
-    const float rstd = 1.0f / sqrtf(total(q, red[1]) / (float)p.H + p.eps);
+    const float rstd = rsqrtf(total(q, red[1]) / (float)p.H + p.eps);
     T* y = static_cast<T*>(p.y) + r * p.sy + c0;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      if (v * team + t < n) {
-        float g[N], c[N];
+      const bool in = v * team + t < n;
+      if (!kStraight && !in) continue;
+      float g[N], c[N];
 #pragma unroll
-        for (int k = 0; k < N; k++) g[k] = 1.0f, c[k] = 0.0f;
-        if (p.w) load_params<T, P>(g, w + v * v_step);
-        if (p.b) load_params<T, P>(c, b + v * v_step);
+      for (int k = 0; k < N; k++) g[k] = 1.0f, c[k] = 0.0f;
+      if (p.w) load_params<T, P>(g, in ? w + v * v_step : static_cast<const P*>(p.w));
+      if (p.b) load_params<T, P>(c, in ? b + v * v_step : static_cast<const P*>(p.b));
 #pragma unroll
-        for (int k = 0; k < N; k++) g[k] = fmaf(h[v][k] * rstd, g[k], c[k]);
-        store_piece<T, SHIFTED>(y + v * v_step, pack<T>(g), mask[v]);
-      }
+      for (int k = 0; k < N; k++) g[k] = fmaf(h[v][k] * rstd, g[k], c[k]);
+      if (in) store_piece<T, SHIFTED>(y + v * v_step, pack<T>(g), mask[v]);
     }
     if (t == 0 && r < p.rows) {
       if (p.mean) p.mean[r] = mean;
@@ -821,8 +826,8 @@ cudaError_t run_vec(const NormParams& p, cudaStream_t st) {
 // Up to 128 pieces a part of a warp takes a row, so that the narrowest rows leave
 // no lanes idle (65536 x 128 bf16: 19 us with a warp a row, 8.7 so); above, the
 // warps that hold it at two pieces a thread, which leaves registers for the next
-// row.  Four pieces a thread (8192 x 7168: 157 us, against 76) and a warp with
-// eight (4096 x 2048: 11.8, against 10.3) are slower; only rows past 2048 pieces
+// row.  Four pieces a thread (8192 x 7168: 157 us, against 76 then) and a warp with
+// eight (4096 x 2048: 11.8, against 10.3 then) are slower; only rows past 2048 pieces
 // need four.
 template <typename T, typename P, bool SHIFTED>
 cudaError_t run_pieces(const NormParams& p, int64_t pieces, cudaStream_t st) {
