@@ -541,7 +541,8 @@ MOE_DEVICE float2 cluster_sum2(float a, float b, float2* red) {
 }
 
 template <typename T, typename P, Team TEAM, int V, bool SHIFTED>
-__global__ void __launch_bounds__(kBlockOf<TEAM>, 512 / kBlockOf<TEAM>) layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
+__global__ void __launch_bounds__(kBlockOf<TEAM>, kBwdBlock / kBlockOf<TEAM>)
+    layer_norm_bwd_vec_kernel(NormBwdParams p, int team_threads) {
   constexpr int N = Vec<T>::kN, STAGES = 8 / V;
   constexpr bool PART = TEAM == kPart;
   // ring: [stage][matrix][vector of the thread][thread]
@@ -572,7 +573,8 @@ __global__ void __launch_bounds__(kBlockOf<TEAM>, 512 / kBlockOf<TEAM>) layer_no
     in[v] = v * v_len + t < nvec;
     mask[v] = SHIFTED ? piece_mask<N>(c0 + v * v_step, (int)p.H) : ~0u;
     if (!in[v])
-      for (int i = 0; i < 3 * STAGES; i++) *reinterpret_cast<uint4*>(own + i * kMatrix + v * kVec) = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 3 * STAGES; i++)
+        *reinterpret_cast<uint4*>(own + i * kMatrix + v * kVec) = make_uint4(0, 0, 0, 0);
   }
 
   // where this thread's next copies come from, and where its results go
