@@ -29,7 +29,7 @@
 //   one token, 4096 x 7168 SwiGLU      10.5 us, 21 %   8192 x 8192   11.3 us, 45 %
 //              32768 x 8192            30.4 us, 67 %
 //   16 / 32 tokens, 8192 x 8192        18 / 31 us      32 tokens, 32768 x 8192   88 us, 24 %
-//   64 tokens top-8 through 256 experts of 4096 x 7168 SwiGLU   590 us, 83 %
+//   64 tokens top-8 through 256 experts of 4096 x 7168 SwiGLU   605 us, 83 %
 // Few rows are bound by the launch, the staging and one pass of the ring (a copy of
 // the same 15 MB takes 6.4 us); long streams of few tokens by HBM; from 16 tokens
 // on by the chains of operand reads and products, which keep the tensor cores 40 %
