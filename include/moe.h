@@ -132,7 +132,7 @@ enum {
                                          check and the access was skipped */
 
 #define MOE_DEV_ERR_NAN_LOGIT 16      /* moe_router_topk met a NaN logit (or a NaN biased
-                                         score): that expert was treated as masked */
+                                         score), which counts as -inf */
 
 typedef struct moe_shape {
   int64_t T; /* tokens (>= 0) */
@@ -579,9 +579,11 @@ typedef struct moe_router {
  * MOE_SCORE_SIGMOID, in fp32.  The bias takes part in the selection alone.  With
  * s the softmax over all experts of the token or the sigmoid, the weights are
  *   w(e) = scale * s(e)   or, renormalized,   scale * s(e) / sum over the chosen of s
- * in fp32.  An expert whose logit (or biased score) is -inf is masked: it is
- * never chosen and takes no part in the softmax; a NaN is treated the same way
- * and reported (MOE_DEV_ERR_NAN_LOGIT is or-ed into *status when status is not
+ * in fp32.  An expert whose logit is -inf is masked: it is never chosen and takes
+ * no part in the softmax.  One whose biased score is -inf is never chosen; its
+ * logit stays in the softmax, as every logit does (the gradient, which knows no
+ * bias, is of these weights).  A NaN logit or biased score is treated as -inf and
+ * reported (MOE_DEV_ERR_NAN_LOGIT is or-ed into *status when status is not
  * NULL).  A +inf logit takes the whole softmax (shared evenly among several).  A
  * token with fewer than K experts left has that many routes, maybe none.
  * map_format MOE_ROUTING_DENSE_I16: map int16 [T][K], the chosen ids ascending,

@@ -344,9 +344,11 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : V == 16 ? 3 : 2) router
     } else {
       top = -INFINITY;
       if (kSoftmax && !p.renorm) {
+        // the bias takes part in the choice alone: an expert that it masks stays in the sum
+        load_scores<T, V>(s, row, e0, 16 / sizeof(T), p.E, p.vector_in);
 #pragma unroll
         for (int j = 0; j < V; j++) {
-          if (s[j] > -INFINITY) s[j] = to_float(row[e0 + j]);
+          s[j] = s[j] == s[j] ? s[j] : -INFINITY;
           top = fmaxf(top, s[j]);
         }
       } else {

@@ -271,3 +271,46 @@ def test_refusals():
     wide = torch.zeros(4, 40, device="cuda")
     with pytest.raises(moe.MoeError):  # the gradient over the logits, shifted
         moe.moe_router_topk_backward(good, wide[:, :16], moe.Routing(0, m), p, wide[:, 8:24])
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,K", [(9, 5, 2), (33, 64, 8), (20, 256, 8), (6, 300, 17), (4, 1000, 40)])
+def test_gradient_with_experts_the_bias_masks(T, E, K, renorm, score, fmt):
+    """Weights and gradient are of the same formula whatever the bias does to the choice: a bias of -inf or NaN keeps
+    an expert from being chosen and leaves its logit in the softmax; logits of -inf are in neither."""
+    moe = moe_mod()
+    scale = 1.0 if renorm else 2.5
+    for dtype in bu.DTYPES:
+        logits = bu.randn(T, E, seed=T + E, dtype=dtype)
+        logits[:, 1] += 3.0  # what the bias masks would have been chosen, and weighs in the sum
+        logits[::2, 3] = float("-inf")
+        bias = bu.randn(E, seed=6, scale=0.5)
+        bias[1], bias[0] = float("-inf"), float("nan")
+        l = logits.float().numpy()
+        m, w, status = topk(moe, logits, K, score, renorm, scale, fmt, bias)
+        assert status == moe.DEV_ERR_NAN_LOGIT
+        on, got = bu.dense_to_full(m, w, E) if fmt == 0 else (m != 0, w.astype(np.float64))
+        assert not on[:, :2].any() and (on.sum(1) == np.minimum(K, (l > -np.inf).sum(1) - 2)).all()
+        live = l > -np.inf
+        want = bu.router_weights(l, live, on, score == 1, renorm, scale)
+        assert (np.abs(got - want) <= bu.router_tol(l, live, want, E)).all()
+        gp = np.where(on, bu.randn(T, E, seed=7).numpy(), 0.0)
+        g = bu.f64(backward(moe, logits, K, score, renorm, scale, fmt, m,
+                            gp if fmt else np.where(m >= 0, np.take_along_axis(gp, np.maximum(m, 0).astype(np.int64),
+                                                                               1), 0.0)))
+        ref = bu.router_backward(l, on, gp, score == 1, renorm, scale)
+        n = bu.router_weights(l, live, on if (score or renorm) else live, score == 1, renorm, 1.0)
+        rel = bu.router_tol(l, live, n, E) / np.maximum(n, 1e-300)
+        mag = scale * n * (np.abs(gp) + (np.abs(gp) * n * on).sum(1, keepdims=True))
+        tol = mag * (3 * np.where(n > 0, rel, 0).max(1, keepdims=True) + 64 * bu.U) + 2.0 ** -126
+        tol = torch.from_numpy(tol) + bu.rounding(torch.from_numpy(ref), dtype)
+        bu.assert_within(g, torch.from_numpy(ref), tol)
+        # the formula of the gradient is the weights': its product with a direction against their differences
+        v = np.where(live, bu.randn(T, E, seed=9).double().numpy(), 0.0)
+        step = 1e-5
+        a, b = (bu.router_weights(np.where(live, l + d * step * v, -np.inf), live, on, score == 1, renorm, scale)
+                for d in (1, -1))
+        num = ((a - b) * gp).sum() / (2 * step)
+        assert abs((ref * v).sum() - num) <= 1e-7 * (1 + np.abs(gp).sum())
