@@ -247,6 +247,7 @@ MOE_DEVICE void stage_tokens(const T* x, int64_t sx, int64_t Kd, int toks, int s
 }
 
 MOE_DEVICE void cluster_barrier() {
+  __syncwarp();  // lanes leave the loops before it at different rounds; the aligned form wants the whole warp
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

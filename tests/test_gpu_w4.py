@@ -101,6 +101,23 @@ def test_strided_rows_and_addend_in_place(M):
     assert bool(torch.isnan(out[:, :5]).all()) and bool(torch.isnan(out[:, 5 + N:]).all())
 
 
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("M,N,Kd", [(1, 257, 7168), (3, 130, 4096), (7, 300, 2048), (11, 70, 7168), (13, 515, 1056),
+                                    (37, 33, 8224), (70, 261, 2048)])
+def test_outputs_that_do_not_fill_a_round(M, N, Kd, group):
+    """Few rows, so that CTAs share K steps, and numbers of outputs that leave some lanes of a warp without one in the
+    last round before the CTAs meet; several passes over the weights where M exceeds 32. Results repeat bit for bit."""
+    moe = moe_mod()
+    w = bu.w4_random(N, Kd, group, BF, True, seed=N)
+    x = bu.randn(M, Kd, seed=M, dtype=BF)
+    for swiglu in (False, True)[:2 - N % 2]:
+        ref, tol = bu.w4_product(x, bu.w4_dequant(*w, group), group, swiglu=swiglu)
+        first = product(moe, x, w, swiglu=swiglu, group=group)
+        bu.assert_within(first, ref, tol)
+        for _ in range(20):
+            assert torch.equal(product(moe, x, w, swiglu=swiglu, group=group), first)
+
+
 def test_nonfinite_tokens_stay_alone():
     moe = moe_mod()
     w = bu.w4_random(40, 256, 128, BF, False, seed=2)
