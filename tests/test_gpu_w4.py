@@ -101,6 +101,27 @@ def test_strided_rows_and_addend_in_place(M):
     assert bool(torch.isnan(out[:, :5]).all()) and bool(torch.isnan(out[:, 5 + N:]).all())
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("scale", [1e38, 3e36, 1e-30, 2e-35])
+def test_tokens_at_the_ends_of_the_range(scale, zeros, group):
+    """bf16 tokens of one sign whose sum over a group is beyond fp32's range, and tiny ones, where the product is an
+    ordinary number."""
+    moe = moe_mod()
+    for M, N, Kd in ((1, 256, 512), (5, 40, 608), (20, 70, 1024)):
+        codes, scales, zp = bu.w4_random(N, Kd, group, BF, zeros, seed=M)
+        # the largest product stays below Kd * 15 * 0.015 * 1e-5 * 2e38 = 4.6e35
+        w = (codes, (scales.float() * (1e-5 if scale > 1 else 100.0)).to(BF), zp)
+        x = ((1.0 + torch.rand(M, Kd, generator=torch.Generator().manual_seed(Kd))) * scale).to(BF)
+        if M > 1:
+            x[1] = -x[1]
+        assert bool(torch.isfinite(x).all())
+        ref, tol = bu.w4_product(x, bu.w4_dequant(*w, group), group)
+        y = product(moe, x, w, group=group)
+        assert bool(torch.isfinite(y).all())
+        bu.assert_within(y, ref, tol)
+
+
 @pytest.mark.parametrize("group", [32, 128])
 @pytest.mark.parametrize("M,N,Kd", [(1, 257, 7168), (3, 130, 4096), (7, 300, 2048), (11, 70, 7168), (13, 515, 1056),
                                     (37, 33, 8224), (70, 261, 2048)])
