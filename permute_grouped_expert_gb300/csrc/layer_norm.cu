@@ -19,10 +19,12 @@
 //             2048 x 16384 bf16             64 us, 3160     64 x 7168      7.8 us
 // Calls of a few microseconds are bound by their launches and one row's chain of
 // load, two sums and store.
+#include <algorithm>
 #include <type_traits>
 
 #include "block_common.cuh"
 #include "moe_internal.h"
+#include "row_pieces.h"
 
 namespace moe {
 
@@ -38,6 +40,7 @@ struct NormParams {
   void *y, *sum;
   float *mean, *rstd;
   float eps;
+  int64_t cut;  // SHIFTED: from this row on pieces may end behind a matrix
 };
 
 // Any width, stride and alignment: one CTA per row, three passes over the row
@@ -181,12 +184,12 @@ MOE_DEVICE uint4 masked_piece(uint4 raw, uint32_t mask) {
   return u.v;
 }
 
-// A piece with a neighbour's elements, if any, outside the row: what lies there is
-// part of the matrix but behind its last row (`last`), where it is not read.
+// A piece with a neighbour's elements, if any, outside the row: they are part of
+// the matrix but in its last rows (`cut`, see first_cut_row), where they are not read.
 template <typename T, bool SHIFTED>
-MOE_DEVICE uint4 load_piece(const T* p, uint32_t mask, bool last) {
+MOE_DEVICE uint4 load_piece(const T* p, uint32_t mask, bool cut) {
   constexpr int N = Vec<T>::kN;
-  if (!SHIFTED || !last || mask == (1u << N) - 1) return *reinterpret_cast<const uint4*>(p);
+  if (!SHIFTED || !cut || mask == (1u << N) - 1) return *reinterpret_cast<const uint4*>(p);
   union {
     uint4 v;
     T e[N];
@@ -273,12 +276,12 @@ __global__ void __launch_bounds__(THREADS, LANES ? 4 : 1024 / THREADS) layer_nor
 #pragma unroll
     for (int v = 0; v < V; v++) {
       x_raw[v] = make_uint4(0, 0, 0, 0);
-      if (v * team + t < n) x_raw[v] = load_piece<T, SHIFTED>(x + v * v_step, mask[v], r + 1 == p.rows);
+      if (v * team + t < n) x_raw[v] = load_piece<T, SHIFTED>(x + v * v_step, mask[v], r >= p.cut);
     }
   };
   auto fetch_res = [&](int64_t r, int v) {
     const T* res = static_cast<const T*>(p.res) + r * p.sres + c0 + v * v_step;
-    return load_piece<T, SHIFTED>(res, mask[v], r + 1 == p.rows);
+    return load_piece<T, SHIFTED>(res, mask[v], r >= p.cut);
   };
   auto fetch = [&](int64_t r) {
     fetch_x(r, nvec);
@@ -843,7 +846,7 @@ cudaError_t run_pieces(const NormParams& p, int64_t pieces, cudaStream_t st) {
 }
 
 template <typename T, typename P>
-cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
+cudaError_t run_forward(NormParams p, cudaStream_t st) {
   const int b = sizeof(T), n = 16 / b;
   const int64_t pieces = (p.H + n - 1) / n;
   const bool vec = p.H * b % 16 == 0 && vector_rows(p.x, p.sx, p.rows, b) && vector_rows(p.res, p.sres, p.rows, b) &&
@@ -853,8 +856,11 @@ cudaError_t run_forward(const NormParams& p, cudaStream_t st) {
                        alike(p.sum, p.ssum, p.sx, p.rows, n) && alike(p.y, p.sy, p.sx, p.rows, n);
   if (vec && pieces <= 4096)
     return run_pieces<T, P, false>(p, pieces, st);
-  if (shifted && pieces < 4096 && (pieces + 1) * n * (int64_t)sizeof(P) * 2 <= kMaxStaged)
+  if (shifted && pieces < 4096 && (pieces + 1) * n * (int64_t)sizeof(P) * 2 <= kMaxStaged) {
+    p.cut = first_cut_row(p.rows, p.sx, n);
+    if (p.res) p.cut = std::min(p.cut, first_cut_row(p.rows, p.sres, n));
     return run_pieces<T, P, true>(p, pieces + 1, st);  // a row may touch one more
+  }
   layer_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }

@@ -315,3 +315,25 @@ def test_a_row_of_nans_stays_alone(H):
     for out in (y, gx):
         assert torch.equal(torch.isnan(out).all(1).cpu(), bad)
         assert torch.equal(torch.isnan(out).any(1).cpu(), bad)
+
+
+@pytest.mark.parametrize("dtype", bu.DTYPES)
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 7, 9])
+def test_rows_narrower_than_a_piece(H, dtype):
+    """Rows that lie close, so that several share 16 bytes and the last ones' pieces end behind the matrix."""
+    moe = moe_mod()
+    for rows in (2, 3, 4, 8, 9, 30, 300):
+        for pad in (0, 1, 2):
+            x, w, b = inputs(rows, H, dtype, dtype)
+            res = bu.randn(rows, H, seed=3, dtype=dtype)
+            views = []
+            for t in (x, res, torch.zeros_like(x)):
+                flat = torch.full((rows * (H + pad) - pad,), float("nan"), dtype=dtype, device="cuda")
+                v = flat.as_strided((rows, H), (H + pad, 1))
+                v.copy_(t)
+                views.append(v)
+            h = (x.float() + res.float()).to(dtype)
+            moe.moe_layer_norm(views[0], w.cuda(), b.cuda(), EPS, views[2], residual=views[1])
+            bu.assert_within(views[2], bu.norm_forward(h, w, b, EPS)[0], bu.norm_forward_tol(h, w, b, EPS, dtype)[0])
+            moe.moe_layer_norm(views[0], w.cuda(), b.cuda(), EPS, views[2])
+            bu.assert_within(views[2], bu.norm_forward(x, w, b, EPS)[0], bu.norm_forward_tol(x, w, b, EPS, dtype)[0])
