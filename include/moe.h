@@ -495,7 +495,7 @@ enum {
 
 /* A row-major matrix on the device: element (r, c) at data[r * stride + c],
  * stride in elements, at least the number of columns when there is more than
- * one row.  Where a call takes a const moe_rows*, NULL (or NULL data) means an
+ * one row; (rows - 1) * stride is at most 2^56.  Where a call takes a const moe_rows*, NULL (or NULL data) means an
  * optional matrix that is absent. */
 typedef struct moe_rows {
   void* data;

@@ -28,12 +28,13 @@ bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool given(const moe_rows* m) { return m && m->data; }
 
-// A row matrix of `rows` x `cols` elements: element-aligned, rows apart.
+// A row matrix of `rows` x `cols` elements: element-aligned, rows apart, of an
+// extent that 64-bit sums of bytes hold.
 bool rows_ok(const moe_rows* m, int64_t rows, int64_t cols, int bytes) {
   if (rows == 0) return m != nullptr;
   if (!given(m) || !aligned_to(m->data, (size_t)bytes)) return false;
   if (rows == 1) return true;
-  return m->stride >= cols && m->stride <= (int64_t(1) << 40);
+  return m->stride >= cols && m->stride <= (int64_t(1) << 40) && rows - 1 <= (int64_t(1) << 56) / m->stride;
 }
 
 // The same matrix: equal base, and equal strides where there is a second row.

@@ -138,3 +138,23 @@ def test_w4_refusals(moe):
     assert grouped(moe._Shape(0, 0, 8, 2, 0), moe._Layout(32, 64)) == moe.MOE_OK
     assert lib.moe_quantize_w4_rows(FAKE, 4, 100, 64, 1, FAKE, FAKE, None, None) == moe.MOE_ERR_INVALID_ARG
     assert lib.moe_quantize_w4_rows(FAKE, 0, 128, 64, 1, FAKE, FAKE, None, None) == moe.MOE_OK
+
+
+def test_matrices_beyond_the_address_space(moe):
+    """Rows times stride that no memory holds (and no 64-bit sum of bytes) are refused, overlapping or not."""
+    lib = moe.library()
+    far, many = 1 << 40, 1 << 39
+    at = lambda i: rows(moe, stride=far, data=0x10000 + 0x1000 * i)
+    bad = moe.MOE_ERR_INVALID_ARG
+    norm = moe._Norm(many, 64, 1, 1, 1e-5)
+    assert lib.moe_layer_norm(byref(norm), at(0), None, None, None, at(1), None, None, None, None) == bad
+    assert lib.moe_layer_norm_backward(byref(norm), at(0), at(1), None, FAKE, FAKE, None, at(2), None, None, None, 0,
+                                       None) == bad
+    router = moe._Router(many // 64, 32, 2, 0, 0, 1, 1.0)
+    assert lib.moe_router_topk(byref(router), at(0), None, 0, FAKE, FAKE, None, None) == bad
+    assert lib.moe_router_topk_backward(byref(router), at(0), 0, FAKE, FAKE, at(1), None) == bad
+    w = moe._W4(16, 256, 64, 1, 0x50000, 0x60000, None)
+    assert lib.moe_w4_matvec(byref(w), 1 << 31, at(0), 0, None, at(1), None) == bad
+    handle = moe._HandleDev(*([FAKE] * 8))
+    assert lib.moe_grouped_w4_matvec(byref(handle), byref(moe._Shape(4, 0, 8, 2, 0)),
+                                     byref(moe._Layout(32, (1 << 31) - 1)), byref(w), at(0), 0, at(1), None) == bad
