@@ -102,6 +102,7 @@ cudaError_t launch_grouped_w4_matvec(const moe_handle_dev& h, const moe_shape& s
   w4::Params p = params(w, s.E, x, activation, y);
   p.counts = h.tokens_per_expert;
   p.offsets = h.padded_offsets;
+  p.status = h.status;
   p.E = (int)s.E;
   p.cap = l.capacity;
   const int64_t routes = s.T * s.K;

@@ -65,6 +65,7 @@ struct Params {
   // one matrix per expert
   const int32_t* counts;
   const int32_t* offsets;
+  int32_t* status;  // of the handle
   int E;
   bool every;  // blockIdx.y is the expert; else it counts the experts that have rows
   int64_t cap;
@@ -289,7 +290,8 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, KSPLIT, ALIGNED>::kThre
     if (e < 0) return;
     first = p.offsets[e];
     M = min64(first + p.counts[e], p.cap) - first;
-    if (M <= 0) return;
+    // (a handle that no preprocess wrote may hold anything: rows stay within [0, cap))
+    if (M <= 0 || !MOE_IN_BOUNDS(71, first, p.cap, p.status) || first < 0) return;
   }
   const T* x = static_cast<const T*>(p.x) + first * p.sx;
 

@@ -214,6 +214,26 @@ def test_experts_below_the_capacity(cut):
     assert torch.equal(short[r], y[r]) and bool((short[~r] == 7.0).all())
 
 
+@pytest.mark.parametrize("T", [1, 30])
+def test_experts_of_a_damaged_handle(T):
+    """A segment that begins before the rows, or has no rows, is left out; the other experts' rows are as ever."""
+    moe = moe_mod()
+    E, K, Kd, N = 40, 2, 128, 40
+    shape, layout, h, w, x = expert_case(moe, T, E, K, 8, Kd, N, 64, BF, True)
+    weight = moe.W4Weight(*(dev(t) for t in w), 64)
+    y = torch.full((layout.capacity, N), 7.0, dtype=BF, device="cuda")
+    moe.moe_grouped_w4_matvec(h, shape, layout, weight, x.cuda(), y)
+    off, cnt = h.padded_offsets.cpu().numpy(), h.tokens_per_expert.cpu().numpy()
+    some = [int(e) for e in np.nonzero(cnt)[0][:2]]
+    h.padded_offsets[some[0]] = -3
+    h.tokens_per_expert[some[1]] = -(1 << 31)
+    got = torch.full_like(y, 7.0)
+    moe.moe_grouped_w4_matvec(h, shape, layout, weight, x.cuda(), got)
+    for e in some:
+        y[off[e]:off[e] + cnt[e]] = 7.0
+    assert torch.equal(got, y)
+
+
 def test_experts_equal_single_matrices():
     """An expert's rows are those of moe_w4_matvec with its matrix: both within the bounds of the definition."""
     moe = moe_mod()
