@@ -337,3 +337,43 @@ def test_rows_narrower_than_a_piece(H, dtype):
             bu.assert_within(views[2], bu.norm_forward(h, w, b, EPS)[0], bu.norm_forward_tol(h, w, b, EPS, dtype)[0])
             moe.moe_layer_norm(views[0], w.cuda(), b.cuda(), EPS, views[2])
             bu.assert_within(views[2], bu.norm_forward(x, w, b, EPS)[0], bu.norm_forward_tol(x, w, b, EPS, dtype)[0])
+
+
+@pytest.mark.parametrize("rows,H,dtype,residual", [
+    (100003, 32, torch.bfloat16, False), (50001, 120, torch.float32, True), (30011, 1000, torch.float16, True),
+    (100003, 13, torch.bfloat16, True), (100003, 51, torch.float32, False), (12007, 1001, torch.bfloat16, True),
+    (3001, 4096, torch.bfloat16, True), (1500, 2050, torch.float16, False), (1600, 1501, torch.float32, True),
+    (1300, 6144, torch.float32, True), (500, 8201, torch.bfloat16, True), (450, 16384, torch.float16, False),
+    (400, 16401, torch.bfloat16, True), (300, 4099, torch.float32, False), (330, 8197, torch.float32, True),
+    (400, 20000, torch.bfloat16, False)])
+def test_forward_of_more_rows_than_run_at_once(rows, H, dtype, residual):
+    """Every kernel's loop over rows, several rows a CTA or team, with the next row on its way."""
+    moe = moe_mod()
+    x, w, b = inputs(rows, H, dtype, torch.float32)
+    res = bu.randn(rows, H, seed=9, dtype=dtype) if residual else None
+    h = (x.float() + res.float()).to(dtype) if residual else x
+    got = forward(moe, x, w, b, res)
+    check_forward(got, h, w, b, EPS, dtype)
+    assert not residual or torch.equal(got[1].cpu(), h)
+
+
+@pytest.mark.parametrize("dtype", bu.DTYPES)
+@pytest.mark.parametrize("rows,H", [(3000, 100), (2600, 513)])
+def test_many_rows_that_start_differently(rows, H, dtype):
+    """Inputs and outputs that share no alignment, element by element, more rows than run at once."""
+    moe = moe_mod()
+    x, w, b = inputs(rows, H, dtype, dtype)
+    gy = bu.randn(rows, H, seed=11, dtype=dtype)
+    _, xv = strided(x, 3, 1)
+    _, yv = strided(x, 2, 5)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    moe.moe_layer_norm(xv, w.cuda(), b.cuda(), EPS, yv, mean=mean, rstd=rstd)
+    check_forward((yv, None, mean, rstd), x, w, b, EPS, dtype)
+    _, gv = strided(gy, 1, 2)
+    ws = torch.empty(moe.moe_layer_norm_workspace_size(rows, H), dtype=torch.uint8, device="cuda")
+    gw, gb = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    moe.moe_layer_norm_backward(gv, xv, w.cuda(), mean, rstd, yv, gw, gb, ws)
+    refs = bu.norm_backward(gy, x, w, mean.cpu(), rstd.cpu(), None)
+    tols = bu.norm_backward_tol(gy, x, w, mean.cpu(), rstd.cpu(), None, dtype)
+    for got, ref, tol in zip((yv, gw, gb), refs, tols):
+        bu.assert_within(got, ref, tol)

@@ -314,3 +314,26 @@ def test_gradient_with_experts_the_bias_masks(T, E, K, renorm, score, fmt):
                 for d in (1, -1))
         num = ((a - b) * gp).sum() / (2 * step)
         assert abs((ref * v).sum() - num) <= 1e-7 * (1 + np.abs(gp).sum())
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E,K,copies", [(7, 2, 400), (64, 8, 100), (100, 6, 60), (256, 8, 31), (256, 36, 31), (300, 17, 30),
+                                        (1000, 40, 30)])
+def test_more_tokens_than_run_at_once(E, K, copies, score):
+    """Every token's routes and gradient are those of the same token in a batch of its own, wherever it lies."""
+    moe = moe_mod()
+    T = 997
+    for dtype, renorm, fmt in ((torch.float32, True, 0), (torch.bfloat16, False, 0), (torch.float16, True, 1),
+                               (torch.float32, False, 1)):
+        base = bu.randn(T, E, seed=E, dtype=dtype)
+        base[5] = float("-inf")
+        base[11::17, 2] = float("-inf")
+        check(moe, base[:200], K, score, renorm)
+        logits = base.repeat(copies, 1)
+        m0, p0, _ = topk(moe, base, K, score, renorm, 1.5, fmt)
+        m, p, _ = topk(moe, logits, K, score, renorm, 1.5, fmt)
+        assert (m.reshape(copies, T, -1) == m0).all() and (p.reshape(copies, T, -1) == p0).all()
+        gp = bu.randn(*m0.shape, seed=7).numpy()
+        g0 = backward(moe, base, K, score, renorm, 1.5, fmt, m0, gp)
+        g = backward(moe, logits, K, score, renorm, 1.5, fmt, m, np.tile(gp, (copies, 1)))
+        assert torch.equal(g.view(copies, T, E), g0.expand(copies, T, E))
