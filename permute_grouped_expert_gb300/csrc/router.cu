@@ -238,7 +238,9 @@ MOE_DEVICE bool select_top(const float (&s)[V], int K, int live, float low, floa
   return true;
 }
 
-template <typename T, int V, int L, int SCORE>
+// BIAS: there is a bias; what it needs would cost the others registers (65536 x 64
+// bf16 22.2 us with one kernel for both, 21.3 so).
+template <typename T, int V, int L, int SCORE, bool BIAS>
 __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : V == 16 ? 3 : 2) router_topk_kernel(RouterParams p) {
   constexpr int kTokens = 32 / L;                     // tokens of a warp
   constexpr int kChosen = V * L < 128 ? V * L : 128;  // K at the most
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : V == 16 ? 3 : 2) router
     const T* row = static_cast<const T*>(p.logits) + (real ? t : t0) * p.stride;
     float s[V];
     load_scores<T, V>(s, row, e0, 16 / sizeof(T), p.E, p.vector_in);
-    if (p.bias) {
+    if (BIAS) {
 #pragma unroll
       for (int j = 0; j < V; j++)
         if (s[j] > -INFINITY)  // (false past the end of the row)
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : V == 16 ? 3 : 2) router
     // the chosen ids in ascending order through shared memory, and the logits
     // beside them where this lane still has them
     const int first = group_below<L>(bits ? __popc(on) : count_from<V>(s, lo)), count = min(live, p.K);
-    const bool staged = V == 8 && !p.bias;
+    const bool staged = V == 8 && !BIAS;
     int slot = first;
     if (!bits) {
       uint32_t to = (uint32_t)__cvta_generic_to_shared(chosen + first);
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : V == 16 ? 3 : 2) router
     // weights, L of the chosen at a time; the largest logit that takes part is
     // `top` itself, and looked for where the scores are not the logits
     float z = 0.0f;
-    if (!p.bias) {
+    if (!BIAS) {
       if (kSoftmax && !p.renorm) {  // every live expert takes part in the sum
 #pragma unroll
         for (int j = 0; j < V; j++) z += exp_below(s[j], top);
@@ -657,7 +659,13 @@ unsigned token_grid(int64_t T) {
 
 template <typename T, int SCORE>
 void run_topk(const RouterParams& p, cudaStream_t st) {
-#define RUN(V, L) router_topk_kernel<T, V, L, SCORE><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+#define RUN(V, L) router_topk_kernel<T, V, L, SCORE, true><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
+  if (p.bias) {
+    MOE_ROUTER_SHAPE(RUN);
+    return;
+  }
+#undef RUN
+#define RUN(V, L) router_topk_kernel<T, V, L, SCORE, false><<<token_grid<L>(p.T), kThreads, 0, st>>>(p)
   MOE_ROUTER_SHAPE(RUN);
 #undef RUN
 }
