@@ -224,16 +224,16 @@ MOE_DEVICE void stage_tokens(const T* x, int64_t sx, int64_t Kd, int toks, int s
       // 2^(14 - E) for top in [2^E, 2^(E+1)); E held where both it and its inverse are normal
       const int E = top > 0.0f ? min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127) : 14;
       const float up = __uint_as_float((uint32_t)(127 + 14 - E) << 23);
-      // scaled before they are added up: a sum of large elements of one sign would leave fp32's range
-#pragma unroll
-      for (int i = 0; i < 8; i++) f[i] *= up;
+      const float up16 = up * 0.0625f;
       __half2 h[4];
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const float m = i & 1 ? 0.0625f : 1.0f;
+        const float m = i & 1 ? up16 : up;
         h[i] = __floats2half2_rn(f[i] * m, f[i + 4] * m);
       }
-      float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+      // of the scaled elements: a sum of large ones of one sign would leave fp32's range
+      auto two = [&](int i) { return fmaf(f[i + 1], up, f[i] * up); };
+      float sum = (two(0) + two(2)) + (two(4) + two(6));
 #pragma unroll
       for (int d = GROUP / 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (s0 + s < s1) {
