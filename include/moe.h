@@ -575,8 +575,9 @@ typedef struct moe_router {
  * moe_preprocess, moe_dispatch_permute and moe_combine_unpermute read.  For
  * every token the K experts of the largest selection score are chosen, ties to
  * the lowest expert; the score is the logit, and with select_bias (device fp32
- * [E], or NULL) logit + bias for MOE_SCORE_SOFTMAX and sigmoid(logit) + bias for
- * MOE_SCORE_SIGMOID, in fp32.  The bias takes part in the selection alone.  With
+ * [E], or NULL) logit + bias for MOE_SCORE_SOFTMAX and 1 / (1 + exp(-logit)) + bias
+ * for MOE_SCORE_SIGMOID, in fp32 and each step rounded to nearest but the
+ * exponential, which is CUDA's expf.  The bias takes part in the selection alone.  With
  * s the softmax over all experts of the token or the sigmoid, the weights are
  *   w(e) = scale * s(e)   or, renormalized,   scale * s(e) / sum over the chosen of s
  * in fp32.  An expert whose logit is -inf is masked: it is never chosen and takes

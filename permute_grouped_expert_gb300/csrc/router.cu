@@ -259,11 +259,11 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? 5 : V == 16 ? 3 : 2) router
     const T* row = static_cast<const T*>(p.logits) + (real ? t : t0) * p.stride;
     float s[V];
     load_scores<T, V>(s, row, e0, 16 / sizeof(T), p.E, p.vector_in);
-    if (BIAS) {
+    if (BIAS) {  // the choice: a quotient rounded correctly, so that near ties fall as in plain fp32
 #pragma unroll
       for (int j = 0; j < V; j++)
         if (s[j] > -INFINITY)  // (false past the end of the row)
-          s[j] = (kSoftmax ? s[j] : sigmoid_scaled(s[j], 0.0f)) + p.bias[e0 + j];
+          s[j] = (kSoftmax ? s[j] : __fdiv_rn(1.0f, 1.0f + expf(-s[j]))) + p.bias[e0 + j];
     }
     // a lane's experts as if all of them were finite, which the squares tell
     float low = s[0], top = s[0], sum = 0.0f, squares = 0.0f;

@@ -337,3 +337,18 @@ def test_more_tokens_than_run_at_once(E, K, copies, score):
         g0 = backward(moe, base, K, score, renorm, 1.5, fmt, m0, gp)
         g = backward(moe, logits, K, score, renorm, 1.5, fmt, m, np.tile(gp, (copies, 1)))
         assert torch.equal(g.view(copies, T, E), g0.expand(copies, T, E))
+
+
+def test_choice_by_biased_sigmoids_is_that_of_fp32():
+    """With a bias the choice goes by 1 / (1 + exp(-logit)) + bias, every step rounded to fp32 once, and equal scores by
+    the lowest expert: near ties, of which there are many among so many tokens, come out as in plain fp32."""
+    moe = moe_mod()
+    for T, E, K in ((60000, 256, 8), (30000, 64, 6), (9000, 1000, 40)):
+        l = bu.randn(T, E, seed=E, scale=3.0).cuda()
+        l[:50] *= 30.0
+        l[T // 2:] = 1e-5 * l[T // 2:] + torch.linspace(-4.0, 4.0, T - T // 2, device="cuda")[:, None]
+        bias = bu.randn(E, seed=1, scale=1e-5).cuda()
+        score = 1.0 / (1.0 + torch.exp(-l)) + bias
+        ids = torch.sort(torch.sort(score, dim=1, descending=True, stable=True).indices[:, :K], dim=1).values
+        m, _, _ = topk(moe, l, K, score=1, bias=bias)
+        assert int((torch.from_numpy(m) != ids.cpu()).any(1).sum()) == 0
