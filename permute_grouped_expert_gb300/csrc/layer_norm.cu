@@ -474,6 +474,7 @@ MOE_DEVICE float2 team_sum2(float a, float b, float2* red, int warp, int warps, 
   float v = halves(a, b);
   if (warps > 1) {
     if ((lane & 15) == 0) reinterpret_cast<float*>(red + warp)[low ? 0 : 1] = v;
+    __syncwarp();  // the barrier's form wants whole warps
     asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
     const float2 t = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
     v = halves(t.x, t.y);

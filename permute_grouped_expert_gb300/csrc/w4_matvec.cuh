@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(Plan<GROUP, NT, WARPS, KSPLIT, ALIGNED>::kThre
         fill_codes(step + kStages - 1, free_stage);  // the stage every lane has left
         fill_scales(step + kStages - 1);
         cp_async_commit();
+        __syncwarp();  // lanes may have copied less than others; the products want the whole warp
         const uint8_t* tile = ring + stage * kStageBytes;
         free_stage = stage;
         stage = stage + 1 == kStages ? 0 : stage + 1;
