@@ -518,7 +518,8 @@ typedef struct moe_norm {
  *   mean[r] = sum_c h[r][c] / H,  rstd[r] = 1 / sqrt(sum_c (h[r][c] - mean[r])^2 / H + eps)
  *   y[r]    = (h[r] - mean[r]) * rstd[r] * weight + bias, rounded to dtype
  * Sums, statistics and the formula are fp32; the variance is taken about the
- * mean, not from a sum of squares.  weight, bias: device [H] of param_dtype, or
+ * mean, not from a sum of squares.  The order of the sums depends on H, the
+ * strides and the alignment, and a row's last bits with it.  weight, bias: device [H] of param_dtype, or
  * NULL (1 and 0).  sum: h (optional; may be x or residual itself, with the same
  * stride, and must not overlap them otherwise); it needs a residual.  mean,
  * rstd: device fp32 [rows], each optional; the backward pass reads both.  y
@@ -637,8 +638,9 @@ enum {
  * step).  Each group's sums of q x and of x are formed in fp32 (the first on the
  * tensor cores from exact operands: 128 elements of a token at a time are
  * brought to f16's range by a power of two, which keeps all bits of an element
- * down to 2^-24 of the largest), and their difference is scaled in fp32.  A
- * token that holds an infinity or a NaN gives NaN.  x: M rows of Kd (16-byte
+ * down to 2^-24 of the largest), and their difference is scaled in fp32, so that
+ * a rounding error is relative to the sum of |q x|.  A token that holds an
+ * infinity or a NaN gives outputs that are not finite.  x: M rows of Kd (16-byte
  * aligned, stride a multiple of 8); y: M rows of N (N/2 with SwiGLU; N must be
  * even); addend: optional, as y (it may be y itself), only without SwiGLU.  y
  * must not overlap x.  Any M >= 0; the weights are

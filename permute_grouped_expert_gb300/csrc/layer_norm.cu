@@ -18,7 +18,10 @@
 //             4096 x 4096 fp32              35 us, 5720     1531 x 1537 fp32 11.7 us, 2410
 //             2048 x 16384 bf16             64 us, 3160     64 x 7168      7.8 us
 // Calls of a few microseconds are bound by their launches and one row's chain of
-// load, two sums and store.
+// load, two sums and store; unaligned rows by their masks and, forward, by spills
+// (below), narrow ones also by the finishing launch backward; forward rows beyond
+// 2048 pieces (2048 x 16384 bf16 34 us, 3940) by one CTA an SM that waits at two
+// barriers a row and spills.
 #include <algorithm>
 #include <type_traits>
 
@@ -230,6 +233,8 @@ MOE_DEVICE void piece_params(float (&out)[Vec<T>::kN], const P* p, uint32_t mask
   }
 }
 
+// rstd is rsqrtf's, within 2 ulp of the any kernels' 1 / sqrtf: a row's last bits
+// depend on which kernel its alignment gives it.
 // Rows of 16-byte vectors held in registers between the mean, the variance and
 // the result, so that the row is read once, V vectors a thread.  LANES threads
 // of a warp take a row; or (0) a CTA does, and its next row is on its way while
@@ -834,7 +839,10 @@ cudaError_t run_vec(const NormParams& p, cudaStream_t st) {
 // warps that hold it at two pieces a thread, which leaves registers for the next
 // row.  Four pieces a thread (8192 x 7168: 157 us, against 76 then) and a warp with
 // eight (4096 x 2048: 11.8, against 10.3 then) are slower; only rows past 2048 pieces
-// need four.
+// need four.  Four 16-bit pieces beside masks and shifted addresses do not fit the 64
+// registers of four CTAs an SM: the unaligned kernels of a part of a warp spill 60
+// to 64 bytes a thread (8000 x 1001 bf16: 15.3 us), those of 1024 threads 236 to 260
+// on aligned rows and 424 to 464 on others.
 template <typename T, typename P, bool SHIFTED>
 cudaError_t run_pieces(const NormParams& p, int64_t pieces, cudaStream_t st) {
   if (pieces <= 16) return run_vec<T, P, SHIFTED, 4, 256>(p, st);

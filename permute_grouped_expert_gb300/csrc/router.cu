@@ -15,9 +15,14 @@
 // compares: about 600 a warp for 256 experts, four to five counts among them.
 // Hence no sort, no selection one by one, and one pass for the common case of
 // finite logits.  Device times on one GB300:
-//   65536 x 256 fp32 top-8 45 us, top-36 with the softmax over all 59 us;
-//   65536 x 64 bf16 22 us; 16384 x 1024 top-32 33 us; 64 x 256 3.8 us
+//   65536 x 256 fp32 top-8 44 us, top-36 with the softmax over all 58 us;
+//   65536 x 64 bf16 21 us; 16384 x 1024 top-32 32 us; 64 x 256 3.8 us
+//   with a bias 65536 x 256 top-8 51 us, by sigmoids 64, softmax over all 54
 //   gradient 65536 x 256 top-8 27 us (softmax over all 31), 8192 x 256 4.1 us
+// The bias reads the chosen logits (softmax over all: the row) a second time.
+// The gradient of 65536 tokens is bound by latency, 57 % of cycles without a warp
+// that can issue: ids, the logits they point to, two sums, the row, a token after
+// the other.
 #include <cmath>
 #include <type_traits>
 
@@ -54,7 +59,10 @@ MOE_DEVICE uint32_t key_of(float v) {
 MOE_DEVICE float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 // exp(l - top) for l <= top, 1 where l is top (both may be infinite: the minimum
-// drops a NaN).  What is below 2^-126 of the largest is 0.
+// drops a NaN).  What is below 2^-126 of the largest is 0.  The rounding of the
+// product makes the relative error grow with the distance, to (top - l) 2^-24 and
+// 2 ulp; expf would hold 2 ulp at several times the instructions.  Over the cases'
+// logits the weights' error to 64 bits is 7e-8, that of a plain fp32 form 6e-8.
 MOE_DEVICE float exp_below(float l, float top) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(l - top, 0.0f) * 1.4426950408889634f));
@@ -62,7 +70,9 @@ MOE_DEVICE float exp_below(float l, float top) {
 }
 
 // sigmoid(l) * exp(-m) for m = min(largest l, 0): the common factor keeps the
-// ratio of two sigmoids when both are far below the smallest float.
+// ratio of two sigmoids when both are far below the smallest float.  The quotients
+// here are approximate ones, 2 ulp for these divisors of 1 to 2 (and for the sums
+// of at most 1024 weights that they are divided by): they weigh, and do not choose.
 MOE_DEVICE float sigmoid_scaled(float l, float m) {
   return __fdividef(l >= 0.0f ? 1.0f : expf(l - m), 1.0f + expf(-fabsf(l)));
 }
@@ -533,9 +543,6 @@ __global__ void __launch_bounds__(kThreads, V == 8 ? (SPARSE ? 5 : 4) : 2) route
     __syncwarp();  // before the next token's row
   }
 }
-
-// Marks an expert without a gradient in a staged row (a NaN no computation makes).
-constexpr uint32_t kNoGradient = 0xffa5c3e7u;
 
 // Gradient of the plain softmax, where every expert takes part.  A lane takes 16
 // bytes of a row at every L-th place, so that loads and stores are whole lines.

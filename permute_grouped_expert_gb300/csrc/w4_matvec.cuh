@@ -16,7 +16,11 @@
 // largest, and below that errs by 2^-35 of it.  With f that factor,
 //   sum (q - z) x = (sum q 2^-24 f x - z sum 2^-24 f x) 2^24 / f
 // whose second sum is staged with the tokens; a group's difference is scaled
-// and added up in fp32.  A token with an infinity or a NaN gives NaN.
+// and added up in fp32.  Codes thus enter uncentred, and the tensor cores may cut
+// where fp32 rounds: the error is relative to sum |q x|, not sum |(q - z) x|, a
+// few 1e-7 of it.  It moves 3 to 5 bf16 outputs in 10000 by a step (2048
+// elements, groups of 128) and their error to 64 bits, 0.0017, in no digit.  A token with an
+// infinity or a NaN gives outputs that are not finite.
 //
 // A warp takes 32 weight rows (with SwiGLU the up and the gate rows of 16
 // features) whose codes stream through its own ring in shared memory.  Where
@@ -26,10 +30,10 @@
 //
 // Device times on one GB300, bf16 tokens and groups of 128 (share of the HBM
 // floor, the weights' bytes at a copy's 6793 GB/s):
-//   one token, 4096 x 7168 SwiGLU      10.5 us, 21 %   8192 x 8192   11.3 us, 45 %
+//   one token, 4096 x 7168 SwiGLU      10.6 us, 20 %   8192 x 8192   11.6 us, 44 %
 //              32768 x 8192            30.4 us, 67 %
-//   16 / 32 tokens, 8192 x 8192        18 / 31 us      32 tokens, 32768 x 8192   88 us, 24 %
-//   64 tokens top-8 through 256 experts of 4096 x 7168 SwiGLU   605 us, 83 %
+//   16 / 32 tokens, 8192 x 8192        18.6 / 31.6 us  32 tokens, 32768 x 8192   89 us, 23 %
+//   64 tokens top-8 through 256 experts of 4096 x 7168 SwiGLU   625 us, 80 %
 // Few rows are bound by the launch, the staging and one pass of the ring (a copy of
 // the same 15 MB takes 6.4 us); long streams of few tokens by HBM; from 16 tokens
 // on by the chains of operand reads and products, which keep the tensor cores 40 %
@@ -221,7 +225,8 @@ MOE_DEVICE void stage_tokens(const T* x, int64_t sx, int64_t Kd, int toks, int s
       }
 #pragma unroll
       for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      // 2^(14 - E) for top in [2^E, 2^(E+1)); E held where both it and its inverse are normal
+      // 2^(14 - E) for top in [2^E, 2^(E+1)); E held where both it and its inverse are
+      // normal (below 2^-100 every bf16, a multiple of 2^-133, is still exact in f16)
       const int E = top > 0.0f ? min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127) : 14;
       const float up = __uint_as_float((uint32_t)(127 + 14 - E) << 23);
       const float up16 = up * 0.0625f;
@@ -597,6 +602,10 @@ struct Launch {
     if (e != cudaSuccess) return e;
     // In twentieths of a step's time on a full SM: a step on an SM with that many
     // CTAs, each of which stages its tokens, and what a CTA spends around its steps.
+    // Fitted to measured times; over 16 shapes (1 to 64 tokens, 1024 to 32768 rows, one
+    // matrix to 256) against every kernel and cluster size: within 2 % of the fastest
+    // but for 32 tokens of 2048 x 7168 (19.0 us, fastest 17.6), 13 of 1024 x 2048 (7.2,
+    // 6.4) and one of 4096 x 7168 with SwiGLU (10.7, 9.9).
     constexpr int64_t kAround = 8 * 20, kAlone = NT == 1 ? 8 : 13;  // (few warps do not speed up in proportion)
     const int64_t rows = kWarpRows * P::kRowBlocks;
     const int64_t ctas = (p.N + rows - 1) / rows, sms = device_sm_count();
@@ -624,10 +633,11 @@ struct Launch {
 };
 
 // CTAs of 8 warps, several an SM, are the rule (64 tokens through 256 experts
-// 634 us; 703 with one CTA an SM).  CTAs of 16 warps stage more than eight tokens
-// once for 512 weight rows where there are rows enough (32 tokens, 32768 x 8192:
-// 88 us, 8 warps 97); where there are few CTAs, 16 warps halve the steps of each
-// tile (13 tokens, 4099 x 8224: 18.1 us, 8 warps 24.3).  The plan's cost decides.
+// 625 us; 852 with 16 warps that share the steps).  CTAs of 16 warps stage more
+// than eight tokens once for 512 weight rows where there are rows enough (32 tokens,
+// 32768 x 8192: 89 us, 8 warps 102); where there are few CTAs, 16 warps halve the
+// steps of each tile (13 tokens, 4099 x 8224: 18.6 us, 8 warps 21.7).  Each side at
+// its best cluster size; the plan's cost decides.
 template <typename T, int GROUP, int NT, bool ALIGNED>
 cudaError_t launch(const Params& p, int64_t matrices, cudaStream_t st) {
   Launch<T, GROUP, NT, 8, 1, ALIGNED> small;
