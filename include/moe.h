@@ -670,6 +670,121 @@ MOE_API moe_status moe_grouped_w4_matvec(const moe_handle_dev* handle, const moe
 MOE_API moe_status moe_quantize_w4_rows(const void* w, int64_t R, int64_t Kd, int32_t group, int32_t dtype,
                                         void* codes, void* scales, void* zeros, void* stream);
 
+/* --------------------------------------------- root-mean-square norm ------ */
+
+/* Root-mean-square norm of every row, with the residual sum in front of it when
+ * there is one, in the rows' type, in 8 bits with scales, or both:
+ *   h[r]    = x[r] + residual[r], rounded to dtype (x[r] without a residual)
+ *   rstd[r] = 1 / sqrt(sum_c h[r][c]^2 / H + eps)
+ *   v[r]    = h[r] * rstd[r] * weight
+ *   y[r]    = v[r], rounded to dtype
+ *   codes, scales: per block of 128 consecutive elements of v[r] (the last may be
+ *             short), scale = amax / 448, 1 for a block of zeros; code =
+ *             E4M3(v / scale), to nearest even, saturating
+ * in fp32.  The codes are those of v itself, not of y.  They and the scales are
+ * what moe_dispatch_permute takes as MOE_DTYPE_FP8_E4M3_B128 (H a multiple of
+ * 128).  norm, weight, sum, rstd and the rules on rows and overlaps: as for
+ * moe_layer_norm.  y: optional where codes are wanted.  codes: device bytes
+ * [rows][H], scales: device fp32 [rows][ceil(H / 128)], both or neither; they
+ * must not overlap anything else.  A NaN in a block makes its scale and codes NaN. */
+MOE_API moe_status moe_rms_norm(const moe_norm* norm, const moe_rows* x, const moe_rows* residual,
+                                const void* weight, const moe_rows* y, const moe_rows* sum, float* rstd,
+                                void* codes, float* scales, void* stream);
+
+/* Device workspace bytes of moe_rms_norm_backward (host only): fp32 partial sums
+ * of the weight's gradient. */
+MOE_API moe_status moe_rms_norm_workspace_size(int64_t rows, int64_t H, size_t* bytes_out);
+
+/* Backward of moe_rms_norm.  With xhat = h * rstd, u = grad_y * weight:
+ *   grad_x[r]   = rstd[r] * (u[r] - xhat[r] * sum_c (u[r][c] * xhat[r][c]) / H)
+ *                 (+ grad_sum[r] when given), rounded to dtype once
+ *   grad_weight = sum_r grad_y[r] * xhat[r]   (fp32 [H], optional, overwritten)
+ * The rounding to 8 bits has no gradient of its own: grad_y is that of v.
+ * Arguments, workspace (moe_rms_norm_workspace_size), determinism and overlaps: as
+ * for moe_layer_norm_backward. */
+MOE_API moe_status moe_rms_norm_backward(const moe_norm* norm, const moe_rows* grad_y, const moe_rows* h,
+                                         const void* weight, const float* rstd, const moe_rows* grad_sum,
+                                         const moe_rows* grad_x, float* grad_weight, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* ------------------- products grouped by expert, forward and backward ------ */
+
+/* One matrix W[e] [N][Kd] per expert, contiguous, E of them one after another. */
+typedef struct moe_gemm {
+  int64_t N;     /* output features, 1 .. 2^20 */
+  int64_t Kd;    /* input features, 1 .. 2^20 (E * N * Kd at most 2^46) */
+  int32_t dtype; /* MOE_ELEM_BF16 or MOE_ELEM_F16: weights and rows */
+} moe_gemm;
+
+/* Device workspace bytes of the three calls below for a layer (host only); one
+ * workspace serves all of them, needs no initialisation, and calls that share
+ * one must not overlap on the GPU. */
+MOE_API moe_status moe_grouped_gemm_workspace_size(const moe_shape* shape, const moe_layout* layout, int64_t N,
+                                                   int64_t Kd, size_t* bytes_out);
+
+/* y[r] = W[e] x[r] for every routed row r of expert e below the capacity: FC1
+ * (whose output moe_swiglu_backward needs, and which moe_grouped_mlp does not
+ * keep) or FC2 of an expert MLP.  Sums in fp32, rounded to dtype once, in an
+ * order fixed by the sizes and the routing: repeated calls agree bit for bit.
+ * x: capacity rows of Kd, y: capacity rows of N.  shape: T, E and K are read.  Pad
+ * rows take no part and are not written, nor are rows at or beyond the capacity;
+ * any segment may be empty.  A NaN or infinity stays in its row.  Rows and weights
+ * may begin at any element; where bases are 16-byte aligned and strides, N and Kd
+ * multiples of 8 the tensor cores' own copies move them.  y overlaps neither x nor
+ * the weights. */
+MOE_API moe_status moe_grouped_gemm(const moe_handle_dev* handle, const moe_shape* shape, const moe_layout* layout,
+                                    const moe_gemm* gemm, const void* weight, const moe_rows* x, const moe_rows* y,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the rows: grad_x[r] = W[e]^T grad_y[r], for the same rows and by
+ * the same rules; grad_y: capacity rows of N, grad_x: of Kd. */
+MOE_API moe_status moe_grouped_gemm_backward_data(const moe_handle_dev* handle, const moe_shape* shape,
+                                                  const moe_layout* layout, const moe_gemm* gemm,
+                                                  const void* weight, const moe_rows* grad_y,
+                                                  const moe_rows* grad_x, void* workspace, size_t workspace_bytes,
+                                                  void* stream);
+
+/* Gradient of the weights:
+ *   grad_weight[e][n][k] = sum over the routed rows r of e below the capacity of
+ *                          grad_y[r][n] * x[r][k]  (+ addend[e][n][k])
+ * Sums in fp32, rounded to grad_dtype (dtype or MOE_ELEM_F32) once; every element
+ * is written, zeros (or the addend) for an expert without rows.  addend: device
+ * fp32, laid out as grad_weight, only with MOE_ELEM_F32; it may be grad_weight
+ * itself, which then gathers the gradients of several steps, and must not overlap
+ * it otherwise.  Pad rows take no part, whatever they hold. */
+MOE_API moe_status moe_grouped_gemm_backward_weight(const moe_handle_dev* handle, const moe_shape* shape,
+                                                    const moe_layout* layout, const moe_gemm* gemm,
+                                                    const moe_rows* x, const moe_rows* grad_y, int32_t grad_dtype,
+                                                    const float* addend, void* grad_weight, void* workspace,
+                                                    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------- SwiGLU of dispatched rows ------ */
+
+/* Between FC1 and FC2 of a training step, for every routed row r below the
+ * capacity, with u = columns 0..I-1 of pre[r] (up) and g = columns I..2I-1 (gate,
+ * the w3_w1 order of moe_grouped_mlp):
+ *   act[r] = p(r) * silu(g) * u,  silu(g) = g / (1 + exp(-g))
+ * in fp32, rounded to dtype once; p(r) = probs[r] (device fp32 [capacity], as
+ * moe_dispatch_permute writes it), or 1 without.  With the probabilities here the
+ * combine is the unweighted one, as with moe_grouped_mlp_ex's fc2_row_probs.
+ * shape: T, E and K are read; handle: token_of and padded_offsets.  pre: capacity
+ * rows of 2 I, act: of I.  Pad rows and rows at or beyond the capacity are neither
+ * read nor written.  act must not overlap pre. */
+MOE_API moe_status moe_swiglu(const moe_handle_dev* handle, const moe_shape* shape, const moe_layout* layout,
+                              int64_t I, int32_t dtype, const moe_rows* pre, const float* probs,
+                              const moe_rows* act, void* stream);
+
+/* Backward of moe_swiglu, s = 1 / (1 + exp(-g)):
+ *   grad_pre[r] = [ga * p * silu(g),  ga * p * u * s * (1 + g * (1 - s))],  ga = grad_act[r]
+ *   grad_probs[r] = sum over the columns of ga * silu(g) * u
+ * for the same rows, in fp32 and each rounded once (grad_probs: device fp32
+ * [capacity], optional).  grad_pre may be pre itself (same stride) and must not
+ * overlap an input otherwise. */
+MOE_API moe_status moe_swiglu_backward(const moe_handle_dev* handle, const moe_shape* shape,
+                                       const moe_layout* layout, int64_t I, int32_t dtype, const moe_rows* pre,
+                                       const float* probs, const moe_rows* grad_act, const moe_rows* grad_pre,
+                                       float* grad_probs, void* stream);
+
 /* ------------------------------------------------------------ buffer ring */
 
 /* Host-side ring of N caller-owned output slots ([REUSE-BUF], Summary and

@@ -102,6 +102,10 @@ class _Router(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class _Gemm(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("Kd", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
 class _W4(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("Kd", ctypes.c_int64), ("group", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
@@ -148,7 +152,7 @@ _SIGNATURES = {
                                          ctypes.POINTER(_HandleDev), _P, ctypes.c_size_t, ctypes.c_int64, _P],
     "moe_quantize_fp8_blocks": [_P, _I64, _I64, _I64, _P, _P, _P],
     "moe_quantize_nvfp4_rows": [_P, _I64, _I64, _P, _P, _P, _P],
-    # descriptors (moe_norm, moe_router, moe_w4, moe_rows) by address
+    # descriptors (moe_norm, moe_router, moe_w4, moe_gemm, moe_rows) by address
     "moe_layer_norm": [_P] * 10,
     "moe_layer_norm_workspace_size": [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
     "moe_layer_norm_backward": [_P] * 11 + [ctypes.c_size_t, _P],
@@ -158,6 +162,21 @@ _SIGNATURES = {
     "moe_grouped_w4_matvec": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _P, _P,
                               ctypes.c_int32, _P, _P],
     "moe_quantize_w4_rows": [_P, _I64, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P],
+    "moe_rms_norm": [_P] * 10,
+    "moe_rms_norm_workspace_size": [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_rms_norm_backward": [_P] * 9 + [ctypes.c_size_t, _P],
+    "moe_grouped_gemm_workspace_size": [ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _I64, _I64,
+                                        ctypes.POINTER(ctypes.c_size_t)],
+    "moe_grouped_gemm": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _P, _P, _P, _P,
+                         _P, ctypes.c_size_t, _P],
+    "moe_grouped_gemm_backward_data": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout),
+                                       _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_grouped_gemm_backward_weight": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout),
+                                         _P, _P, _P, ctypes.c_int32, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_swiglu": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _I64, ctypes.c_int32,
+                   _P, _P, _P, _P],
+    "moe_swiglu_backward": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _I64,
+                            ctypes.c_int32, _P, _P, _P, _P, _P, _P],
     "moe_ring_create": [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_P)],
     "moe_ring_acquire": [_P, _P, ctypes.POINTER(ctypes.c_int32)],
     "moe_ring_release": [_P, ctypes.c_int32, _P],
@@ -703,6 +722,172 @@ def moe_quantize_w4_rows(w: torch.Tensor, group: int, codes: torch.Tensor, scale
                                      _dense(scales, "scales", (*lead, G), w.dtype),
                                      _dense(zeros, "zeros", (*lead, (G + 1) // 2), torch.uint8), _stream(stream)),
            "moe_quantize_w4_rows")
+
+
+# ------------------------------------- root-mean-square norm, expert training
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def moe_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, y: Optional[torch.Tensor],
+                 residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                 rstd: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y = rms_norm(x + residual) * weight per row of x [rows, H], and / or its E4M3
+    codes (float8_e4m3fn or uint8 [rows, H]) with a scale per 128 elements (float
+    [rows, ceil(H / 128)]); sum_out takes the residual sum, rstd (float [rows])
+    what the backward reads."""
+    shape, dtype = _matrix(x, "x"), x.dtype
+    pdtype = _param_dtype(x, weight, None)
+    if codes is not None and codes.dtype not in _CODES:
+        raise ValueError(f"codes: float8_e4m3fn or uint8 expected, got {codes.dtype}")
+    buf = bytearray(_NORM_CALL.size)
+    _NORM_CALL.pack_into(buf, 0, *shape, _elem(x), _ELEM[pdtype], eps, *_rows(x, "x", shape, dtype),
+                         *(_ABSENT if residual is None else _rows(residual, "residual", shape, dtype)),
+                         *(_ABSENT if y is None else _rows(y, "y", shape, dtype)),
+                         *(_ABSENT if sum_out is None else _rows(sum_out, "sum_out", shape, dtype)))
+    a = _address(buf)
+    r = a + _NORM_ROWS
+    _check(_lib.moe_rms_norm(a, r, r + _ROWS_BYTES, _dense(weight, "weight", shape[1:], pdtype), r + 2 * _ROWS_BYTES,
+                             r + 3 * _ROWS_BYTES, _dense(rstd, "rstd", shape[:1], torch.float32),
+                             None if codes is None else _dense(codes, "codes", shape, codes.dtype),
+                             _dense(scales, "scales", (shape[0], -(-shape[1] // 128)), torch.float32),
+                             _stream(stream)), "moe_rms_norm")
+
+
+def moe_rms_norm_workspace_size(rows: int, H: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.moe_rms_norm_workspace_size(rows, H, ctypes.byref(out)), "moe_rms_norm_workspace_size")
+    return out.value
+
+
+def _workspace(workspace: Optional[torch.Tensor]):
+    if workspace is None:
+        return None, 0
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace: contiguous device tensor expected")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def moe_rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor,
+                          grad_x: torch.Tensor, grad_weight: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, grad_sum: Optional[torch.Tensor] = None,
+                          stream=None) -> None:
+    """Gradients of moe_rms_norm; h is the normalised row matrix (x, or sum_out
+    where there was a residual) and grad_sum the gradient that reaches it past
+    the norm.  workspace is needed for grad_weight (float [H])."""
+    shape, dtype, f32 = _matrix(h, "h"), h.dtype, torch.float32
+    pdtype = _param_dtype(h, weight, None)
+    buf = bytearray(_NORM_CALL.size)
+    _NORM_CALL.pack_into(buf, 0, *shape, _elem(h), _ELEM[pdtype], 0.0, *_rows(grad_y, "grad_y", shape, dtype),
+                         *_rows(h, "h", shape, dtype),
+                         *(_ABSENT if grad_sum is None else _rows(grad_sum, "grad_sum", shape, dtype)),
+                         *_rows(grad_x, "grad_x", shape, dtype))
+    a = _address(buf)
+    r = a + _NORM_ROWS
+    _check(_lib.moe_rms_norm_backward(a, r, r + _ROWS_BYTES, _dense(weight, "weight", shape[1:], pdtype),
+                                      _dense(rstd, "rstd", shape[:1], f32), r + 2 * _ROWS_BYTES, r + 3 * _ROWS_BYTES,
+                                      _dense(grad_weight, "grad_weight", shape[1:], f32), *_workspace(workspace),
+                                      _stream(stream)), "moe_rms_norm_backward")
+
+
+def moe_grouped_gemm_workspace_size(shape: Shape, layout: Layout, N: int, Kd: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.moe_grouped_gemm_workspace_size(ctypes.byref(shape.c()), ctypes.byref(layout.c()), N, Kd,
+                                                ctypes.byref(out)), "moe_grouped_gemm_workspace_size")
+    return out.value
+
+
+_GEMM_CALL = struct.Struct("=qqi4x" + "qq" * 2)  # moe_gemm, then two moe_rows
+_GEMM_ROWS = 24
+
+
+def _gemm_call(layout: Layout, N: int, Kd: int, dtype: torch.dtype, rows):
+    """(buffer, its address); rows: (name, tensor, columns) of two row matrices."""
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"bfloat16 or float16 expected, got {dtype}")
+    buf = bytearray(_GEMM_CALL.size)
+    (n0, t0, c0), (n1, t1, c1) = rows
+    _GEMM_CALL.pack_into(buf, 0, N, Kd, _ELEM[dtype], *_rows(t0, n0, (layout.capacity, c0), dtype),
+                         *_rows(t1, n1, (layout.capacity, c1), dtype))
+    return buf, _address(buf)
+
+
+def _expert_matrices(weight: torch.Tensor, name: str, shape: Shape):
+    if weight.dim() != 3 or weight.shape[0] != shape.E:
+        raise ValueError(f"{name}: [{shape.E}, N, Kd] expected, got {tuple(weight.shape)}")
+    return weight.shape[1], weight.shape[2]
+
+
+def moe_grouped_gemm(handle: Handle, shape: Shape, layout: Layout, weight: torch.Tensor, x: torch.Tensor,
+                     y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """y[r] = weight[e] @ x[r] for the routed rows r of expert e: weight [E, N, Kd], x [cap, Kd], y [cap, N]."""
+    N, Kd = _expert_matrices(weight, "weight", shape)
+    buf, a = _gemm_call(layout, N, Kd, weight.dtype, (("x", x, Kd), ("y", y, N)))
+    r = a + _GEMM_ROWS
+    _check(_lib.moe_grouped_gemm(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), a,
+                                 _dense(weight, "weight", weight.shape, weight.dtype), r, r + _ROWS_BYTES,
+                                 *_workspace(workspace), _stream(stream)), "moe_grouped_gemm")
+
+
+def moe_grouped_gemm_backward_data(handle: Handle, shape: Shape, layout: Layout, weight: torch.Tensor,
+                                   grad_y: torch.Tensor, grad_x: torch.Tensor, workspace: torch.Tensor,
+                                   stream=None) -> None:
+    """grad_x[r] = weight[e].T @ grad_y[r] for the routed rows r of expert e: grad_y [cap, N], grad_x [cap, Kd]."""
+    N, Kd = _expert_matrices(weight, "weight", shape)
+    buf, a = _gemm_call(layout, N, Kd, weight.dtype, (("grad_y", grad_y, N), ("grad_x", grad_x, Kd)))
+    r = a + _GEMM_ROWS
+    _check(_lib.moe_grouped_gemm_backward_data(
+        ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), a,
+        _dense(weight, "weight", weight.shape, weight.dtype), r, r + _ROWS_BYTES, *_workspace(workspace),
+        _stream(stream)), "moe_grouped_gemm_backward_data")
+
+
+def moe_grouped_gemm_backward_weight(handle: Handle, shape: Shape, layout: Layout, x: torch.Tensor,
+                                     grad_y: torch.Tensor, grad_weight: torch.Tensor, workspace: torch.Tensor,
+                                     addend: Optional[torch.Tensor] = None, stream=None) -> None:
+    """grad_weight[e] = sum of outer(grad_y[r], x[r]) over the routed rows r of e (+ addend[e]): grad_weight
+    [E, N, Kd] of the rows' type or float; addend float, maybe grad_weight itself."""
+    N, Kd = _expert_matrices(grad_weight, "grad_weight", shape)
+    buf, a = _gemm_call(layout, N, Kd, x.dtype, (("x", x, Kd), ("grad_y", grad_y, N)))
+    r = a + _GEMM_ROWS
+    _check(_lib.moe_grouped_gemm_backward_weight(
+        ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), a, r, r + _ROWS_BYTES,
+        _elem(grad_weight), _dense(addend, "addend", grad_weight.shape, torch.float32),
+        _dense(grad_weight, "grad_weight", grad_weight.shape, grad_weight.dtype), *_workspace(workspace),
+        _stream(stream)), "moe_grouped_gemm_backward_weight")
+
+
+_SWIGLU_CALL = struct.Struct("=" + "qq" * 3)  # three moe_rows
+
+
+def moe_swiglu(handle: Handle, shape: Shape, layout: Layout, pre: torch.Tensor, act: torch.Tensor,
+               probs: Optional[torch.Tensor] = None, stream=None) -> None:
+    """act[r] = probs[r] * silu(gate) * up for the routed rows: pre [cap, 2 I] = up columns, then gate; act [cap, I]."""
+    cap, I = layout.capacity, _matrix(act, "act")[1]
+    buf = bytearray(_SWIGLU_CALL.size)
+    _SWIGLU_CALL.pack_into(buf, 0, *_rows(pre, "pre", (cap, 2 * I), pre.dtype),
+                           *_rows(act, "act", (cap, I), pre.dtype), *_ABSENT)
+    a = _address(buf)
+    _check(_lib.moe_swiglu(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), I, _elem(pre), a,
+                           _dense(probs, "probs", (cap,), torch.float32), a + _ROWS_BYTES, _stream(stream)),
+           "moe_swiglu")
+
+
+def moe_swiglu_backward(handle: Handle, shape: Shape, layout: Layout, pre: torch.Tensor, grad_act: torch.Tensor,
+                        grad_pre: torch.Tensor, probs: Optional[torch.Tensor] = None,
+                        grad_probs: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of moe_swiglu: grad_pre [cap, 2 I] (maybe pre itself) and grad_probs (float [cap])."""
+    cap, I = layout.capacity, _matrix(grad_act, "grad_act")[1]
+    buf = bytearray(_SWIGLU_CALL.size)
+    _SWIGLU_CALL.pack_into(buf, 0, *_rows(pre, "pre", (cap, 2 * I), pre.dtype),
+                           *_rows(grad_act, "grad_act", (cap, I), pre.dtype),
+                           *_rows(grad_pre, "grad_pre", (cap, 2 * I), pre.dtype))
+    a = _address(buf)
+    _check(_lib.moe_swiglu_backward(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), I,
+                                    _elem(pre), a, _dense(probs, "probs", (cap,), torch.float32), a + _ROWS_BYTES,
+                                    a + 2 * _ROWS_BYTES, _dense(grad_probs, "grad_probs", (cap,), torch.float32),
+                                    _stream(stream)), "moe_swiglu_backward")
 
 
 class Ring:

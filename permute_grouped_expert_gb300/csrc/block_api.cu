@@ -1,8 +1,10 @@
 // block_api.cu -- extern "C" entry points of the operators around the layer
-// (layer norm, router, 4-bit matrix-vector products): host-side argument checks
+// (norms, router, 4-bit matrix-vector products, products grouped by expert and
+// SwiGLU of a training step): host-side argument checks
 // (nothing is enqueued when one fails), then the launch.
 #include <cmath>
 
+#include "grouped_gemm.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -94,6 +96,83 @@ moe_status check_w4_call(const moe_w4* w, int64_t rows, const moe_rows* x, int32
   if (rows > 0 && (!aligned_to(x->data, 16) || (rows > 1 && x->stride % 8))) return MOE_ERR_INVALID_ARG;
   if (overlap(x, w->Kd, y, n_out, rows, 2)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
+}
+
+// First byte of a row matrix and the byte behind its last; empty where it is absent.
+struct Bytes {
+  uintptr_t beg = 0, end = 0;
+};
+Bytes bytes_of(const moe_rows* m, int64_t rows, int64_t cols, int bytes) {
+  if (!given(m) || rows == 0) return {};
+  const uintptr_t b = reinterpret_cast<uintptr_t>(m->data);
+  return {b, b + (uintptr_t)(((rows > 1 ? (rows - 1) * m->stride : 0) + cols) * bytes)};
+}
+Bytes bytes_of(const void* p, int64_t bytes) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return p ? Bytes{b, b + (uintptr_t)bytes} : Bytes{};
+}
+bool meet(Bytes a, Bytes b) { return a.beg < b.end && b.beg < a.end; }
+
+// What the calls on dispatched rows read of the routing.
+moe_status check_routed(const moe_handle_dev* h, const moe_shape* s, const moe_layout* l) {
+  if (!h || !h->tokens_per_expert || !h->padded_offsets) return MOE_ERR_INVALID_ARG;
+  if (!s || s->T < 0 || s->E < 1 || s->E > 1024 || s->K < 1 || s->K > 128 || s->K > s->E ||
+      s->T >= (int64_t(1) << 31) / s->K)
+    return MOE_ERR_INVALID_ARG;
+  if (!l || l->capacity < 0 || l->capacity >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status check_gemm(const moe_gemm* g, const moe_shape* s) {
+  if (!g || g->N < 1 || g->N > (1 << 20) || g->Kd < 1 || g->Kd > (1 << 20)) return MOE_ERR_INVALID_ARG;
+  if (g->dtype != MOE_ELEM_BF16 && g->dtype != MOE_ELEM_F16) return MOE_ERR_INVALID_ARG;
+  if (g->N * g->Kd > (int64_t(1) << 46) / s->E) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status check_gemm_workspace(const moe_gemm* g, const moe_shape* s, const moe_layout* l, const void* workspace,
+                                size_t workspace_bytes) {
+  if (!workspace || !aligned_to(workspace, 16)) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < grouped_gemm_workspace_bytes(*s, *l, g->N, g->Kd)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return MOE_OK;
+}
+
+GroupedGemm gemm_args(const moe_handle_dev* h, const moe_shape* s, const moe_layout* l, const moe_gemm* g,
+                      void* workspace) {
+  GroupedGemm p = {};
+  p.offsets = h->padded_offsets;
+  p.counts = h->tokens_per_expert;
+  p.status = h->status;
+  p.E = s->E;
+  p.T = s->T;
+  p.K = s->K;
+  p.cap = l->capacity;
+  p.N = g->N;
+  p.Kd = g->Kd;
+  p.dtype = p.out_dtype = g->dtype;
+  p.workspace = workspace;
+  return p;
+}
+
+// The forward product and the gradient of the rows: `in` of kin columns, `out` of kout.
+moe_status grouped_rows(GemmDir dir, const moe_handle_dev* handle, const moe_shape* shape, const moe_layout* layout,
+                        const moe_gemm* gemm, const void* weight, const moe_rows* in, int64_t kin,
+                        const moe_rows* out, int64_t kout, void* workspace, size_t workspace_bytes, void* stream) {
+  const int64_t cap = layout->capacity, w_bytes = shape->E * gemm->N * gemm->Kd * 2;
+  if (!weight || !aligned_to(weight, 2)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(in, cap, kin, 2) || !rows_ok(out, cap, kout, 2)) return MOE_ERR_INVALID_ARG;
+  if (overlap(in, kin, out, kout, cap, 2) || meet(bytes_of(out, cap, kout, 2), bytes_of(weight, w_bytes)))
+    return MOE_ERR_INVALID_ARG;
+  const moe_status ws = check_gemm_workspace(gemm, shape, layout, workspace, workspace_bytes);
+  if (ws != MOE_OK) return ws;
+  if (shape->T == 0 || cap == 0) return MOE_OK;
+  GroupedGemm p = gemm_args(handle, shape, layout, gemm, workspace);
+  p.a = in->data;
+  p.sa = in->stride;
+  p.b = weight;
+  p.out = out->data;
+  p.sout = out->stride;
+  return finish(launch_grouped_gemm(dir, p, static_cast<cudaStream_t>(stream)));
 }
 
 #define MOE_TRY(expr)              \
@@ -232,6 +311,151 @@ moe_status moe_quantize_w4_rows(const void* w, int64_t R, int64_t Kd, int32_t gr
   if (!w || !codes || !scales || !aligned_to(w, 2) || !aligned_to(scales, 2)) return MOE_ERR_INVALID_ARG;
   return finish(
       launch_quantize_w4_rows(w, R, Kd, group, dtype, codes, scales, zeros, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_rms_norm(const moe_norm* norm, const moe_rows* x, const moe_rows* residual, const void* weight,
+                        const moe_rows* y, const moe_rows* sum, float* rstd, void* codes, float* scales,
+                        void* stream) {
+  MOE_TRY(check_norm(norm));
+  const int b = elem_bytes(norm->dtype), pb = elem_bytes(norm->param_dtype);
+  const int64_t rows = norm->rows, H = norm->H, blocks = (H + 127) / 128;
+  if (!rows_ok(x, rows, H, b)) return MOE_ERR_INVALID_ARG;
+  if (given(y) && !rows_ok(y, rows, H, b)) return MOE_ERR_INVALID_ARG;
+  if (given(residual) && !rows_ok(residual, rows, H, b)) return MOE_ERR_INVALID_ARG;
+  if (given(sum) && (!given(residual) || !rows_ok(sum, rows, H, b))) return MOE_ERR_INVALID_ARG;
+  if ((codes == nullptr) != (scales == nullptr) || (rows > 0 && !given(y) && !codes)) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(weight, pb) || !aligned_to(rstd, 4) || !aligned_to(scales, 4)) return MOE_ERR_INVALID_ARG;
+  if (overlap(y, H, x, H, rows, b) || overlap(y, H, residual, H, rows, b) || overlap(y, H, sum, H, rows, b))
+    return MOE_ERR_INVALID_ARG;
+  if ((overlap(sum, H, x, H, rows, b) && !same_rows(sum, x, rows)) ||
+      (overlap(sum, H, residual, H, rows, b) && !same_rows(sum, residual, rows)))
+    return MOE_ERR_INVALID_ARG;
+  const Bytes c = bytes_of(codes, rows * H), s = bytes_of(scales, rows * blocks * 4);
+  if (meet(c, s)) return MOE_ERR_INVALID_ARG;
+  for (const moe_rows* m : {x, residual, y, sum}) {
+    const Bytes of = bytes_of(m, rows, H, b);
+    if (meet(c, of) || meet(s, of)) return MOE_ERR_INVALID_ARG;
+  }
+  if (rows == 0) return MOE_OK;
+  return finish(launch_rms_norm(*norm, *x, given(residual) ? residual : nullptr, weight, given(y) ? y : nullptr,
+                                given(sum) ? sum : nullptr, rstd, codes, scales, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_rms_norm_workspace_size(int64_t rows, int64_t H, size_t* bytes_out) {
+  if (!bytes_out || rows < 0 || H < 1 || H > (1 << 20)) return MOE_ERR_INVALID_ARG;
+  *bytes_out = rms_norm_workspace_bytes(rows, H);
+  return MOE_OK;
+}
+
+moe_status moe_rms_norm_backward(const moe_norm* norm, const moe_rows* grad_y, const moe_rows* h, const void* weight,
+                                 const float* rstd, const moe_rows* grad_sum, const moe_rows* grad_x,
+                                 float* grad_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_norm(norm));
+  const int b = elem_bytes(norm->dtype), pb = elem_bytes(norm->param_dtype);
+  const int64_t rows = norm->rows, H = norm->H;
+  if (!rows_ok(grad_y, rows, H, b) || !rows_ok(h, rows, H, b) || !rows_ok(grad_x, rows, H, b))
+    return MOE_ERR_INVALID_ARG;
+  if (given(grad_sum) && !rows_ok(grad_sum, rows, H, b)) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && !rstd) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(weight, pb) || !aligned_to(rstd, 4) || !aligned_to(grad_weight, 4)) return MOE_ERR_INVALID_ARG;
+  if (overlap(grad_x, H, h, H, rows, b) ||
+      (overlap(grad_x, H, grad_y, H, rows, b) && !same_rows(grad_x, grad_y, rows)) ||
+      (overlap(grad_x, H, grad_sum, H, rows, b) && !same_rows(grad_x, grad_sum, rows)))
+    return MOE_ERR_INVALID_ARG;
+  if (grad_weight) {
+    if (!workspace || !aligned_to(workspace, 16)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < rms_norm_workspace_bytes(rows, H)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  return finish(launch_rms_norm_backward(*norm, *grad_y, *h, weight, rstd, given(grad_sum) ? grad_sum : nullptr,
+                                         *grad_x, grad_weight, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_grouped_gemm_workspace_size(const moe_shape* shape, const moe_layout* layout, int64_t N, int64_t Kd,
+                                           size_t* bytes_out) {
+  if (!bytes_out || !shape || shape->T < 0 || shape->E < 1 || shape->E > 1024 || shape->K < 1 || !layout ||
+      layout->capacity < 0 || N < 1 || N > (1 << 20) || Kd < 1 || Kd > (1 << 20))
+    return MOE_ERR_INVALID_ARG;
+  *bytes_out = grouped_gemm_workspace_bytes(*shape, *layout, N, Kd);
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm(const moe_handle_dev* handle, const moe_shape* shape, const moe_layout* layout,
+                            const moe_gemm* gemm, const void* weight, const moe_rows* x, const moe_rows* y,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_routed(handle, shape, layout));
+  MOE_TRY(check_gemm(gemm, shape));
+  return grouped_rows(kForward, handle, shape, layout, gemm, weight, x, gemm->Kd, y, gemm->N, workspace,
+                      workspace_bytes, stream);
+}
+
+moe_status moe_grouped_gemm_backward_data(const moe_handle_dev* handle, const moe_shape* shape,
+                                          const moe_layout* layout, const moe_gemm* gemm, const void* weight,
+                                          const moe_rows* grad_y, const moe_rows* grad_x, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_routed(handle, shape, layout));
+  MOE_TRY(check_gemm(gemm, shape));
+  return grouped_rows(kData, handle, shape, layout, gemm, weight, grad_y, gemm->N, grad_x, gemm->Kd, workspace,
+                      workspace_bytes, stream);
+}
+
+moe_status moe_grouped_gemm_backward_weight(const moe_handle_dev* handle, const moe_shape* shape,
+                                            const moe_layout* layout, const moe_gemm* gemm, const moe_rows* x,
+                                            const moe_rows* grad_y, int32_t grad_dtype, const float* addend,
+                                            void* grad_weight, void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+  MOE_TRY(check_routed(handle, shape, layout));
+  MOE_TRY(check_gemm(gemm, shape));
+  if (grad_dtype != gemm->dtype && grad_dtype != MOE_ELEM_F32) return MOE_ERR_INVALID_ARG;
+  const int gb = elem_bytes(grad_dtype);
+  const int64_t cap = layout->capacity, n = shape->E * gemm->N * gemm->Kd;
+  if (!rows_ok(x, cap, gemm->Kd, 2) || !rows_ok(grad_y, cap, gemm->N, 2)) return MOE_ERR_INVALID_ARG;
+  if (!grad_weight || !aligned_to(grad_weight, gb)) return MOE_ERR_INVALID_ARG;
+  if (addend && (grad_dtype != MOE_ELEM_F32 || !aligned_to(addend, 4))) return MOE_ERR_INVALID_ARG;
+  const Bytes gw = bytes_of(grad_weight, n * gb);
+  if (meet(gw, bytes_of(x, cap, gemm->Kd, 2)) || meet(gw, bytes_of(grad_y, cap, gemm->N, 2)) ||
+      (addend != grad_weight && meet(gw, bytes_of(addend, n * 4))))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_gemm_workspace(gemm, shape, layout, workspace, workspace_bytes));
+  GroupedGemm p = gemm_args(handle, shape, layout, gemm, workspace);
+  p.a = grad_y->data;
+  p.sa = grad_y->stride;
+  p.b = x->data;
+  p.sb = x->stride;
+  p.out = grad_weight;
+  p.out_dtype = grad_dtype;
+  p.addend = addend;
+  return finish(launch_grouped_gemm(kWeight, p, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_swiglu(const moe_handle_dev* handle, const moe_shape* shape, const moe_layout* layout, int64_t I,
+                      int32_t dtype, const moe_rows* pre, const float* probs, const moe_rows* act, void* stream) {
+  MOE_TRY(check_routed(handle, shape, layout));
+  const int b = elem_bytes(dtype);
+  const int64_t cap = layout->capacity;
+  if (!b || I < 1 || I > (1 << 20) || !handle->token_of || !aligned_to(probs, 4)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(pre, cap, 2 * I, b) || !rows_ok(act, cap, I, b) || overlap(pre, 2 * I, act, I, cap, b))
+    return MOE_ERR_INVALID_ARG;
+  if (shape->T == 0 || cap == 0) return MOE_OK;
+  return finish(launch_swiglu(*handle, *shape, *layout, I, dtype, *pre, probs, *act,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_swiglu_backward(const moe_handle_dev* handle, const moe_shape* shape, const moe_layout* layout,
+                               int64_t I, int32_t dtype, const moe_rows* pre, const float* probs,
+                               const moe_rows* grad_act, const moe_rows* grad_pre, float* grad_probs, void* stream) {
+  MOE_TRY(check_routed(handle, shape, layout));
+  const int b = elem_bytes(dtype);
+  const int64_t cap = layout->capacity;
+  if (!b || I < 1 || I > (1 << 20) || !handle->token_of || !aligned_to(probs, 4) || !aligned_to(grad_probs, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(pre, cap, 2 * I, b) || !rows_ok(grad_act, cap, I, b) || !rows_ok(grad_pre, cap, 2 * I, b))
+    return MOE_ERR_INVALID_ARG;
+  if (overlap(grad_pre, 2 * I, grad_act, I, cap, b) ||
+      (overlap(grad_pre, 2 * I, pre, 2 * I, cap, b) && !same_rows(grad_pre, pre, cap)))
+    return MOE_ERR_INVALID_ARG;
+  if (shape->T == 0 || cap == 0) return MOE_OK;
+  return finish(launch_swiglu_backward(*handle, *shape, *layout, I, dtype, *pre, probs, *grad_act, *grad_pre,
+                                       grad_probs, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

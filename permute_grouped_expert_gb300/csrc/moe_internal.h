@@ -83,14 +83,27 @@ cudaError_t launch_combine_mx(const moe_handle_dev& h, const moe_shape& s, int32
 cudaError_t launch_quantize_mx_rows(const void* x, int64_t R, int64_t H, int32_t format, void* codes, void* scales,
                                     cudaStream_t st);
 
-// Operators around the layer: layer norm (layer_norm.cu), router (router.cu),
-// 4-bit matrix-vector products (w4_matvec.cu).  Optional matrices are NULL.
+// Operators around the layer: layer norm (layer_norm.cu), root-mean-square norm
+// (rms_norm.cu), router (router.cu), 4-bit matrix-vector products (w4_matvec.cu),
+// SwiGLU of dispatched rows (swiglu.cu).  Optional matrices are NULL.
 size_t layer_norm_workspace_bytes(int64_t rows, int64_t H);
 cudaError_t launch_layer_norm(const moe_norm& n, const moe_rows& x, const moe_rows* res, const void* w, const void* b,
                               const moe_rows& y, const moe_rows* sum, float* mean, float* rstd, cudaStream_t st);
 cudaError_t launch_layer_norm_backward(const moe_norm& n, const moe_rows& gy, const moe_rows& h, const void* w,
                                        const float* mean, const float* rstd, const moe_rows* gsum, const moe_rows& gx,
                                        float* gw, float* gb, void* workspace, cudaStream_t st);
+size_t rms_norm_workspace_bytes(int64_t rows, int64_t H);
+cudaError_t launch_rms_norm(const moe_norm& n, const moe_rows& x, const moe_rows* res, const void* w,
+                            const moe_rows* y, const moe_rows* sum, float* rstd, void* codes, float* scales,
+                            cudaStream_t st);
+cudaError_t launch_rms_norm_backward(const moe_norm& n, const moe_rows& gy, const moe_rows& h, const void* w,
+                                     const float* rstd, const moe_rows* gsum, const moe_rows& gx, float* gw,
+                                     void* workspace, cudaStream_t st);
+cudaError_t launch_swiglu(const moe_handle_dev& h, const moe_shape& s, const moe_layout& l, int64_t I, int32_t dtype,
+                          const moe_rows& pre, const float* probs, const moe_rows& act, cudaStream_t st);
+cudaError_t launch_swiglu_backward(const moe_handle_dev& h, const moe_shape& s, const moe_layout& l, int64_t I,
+                                   int32_t dtype, const moe_rows& pre, const float* probs, const moe_rows& grad_act,
+                                   const moe_rows& grad_pre, float* grad_probs, cudaStream_t st);
 cudaError_t launch_router_topk(const moe_router& r, const moe_rows& logits, const float* bias, int32_t format,
                                void* map, float* probs, int32_t* status, cudaStream_t st);
 cudaError_t launch_router_topk_backward(const moe_router& r, const moe_rows& logits, int32_t format, const void* map,

@@ -1,0 +1,222 @@
+// swiglu.cu -- SwiGLU of dispatched rows between FC1 and FC2, with the routes'
+// probabilities, and its gradient.
+//
+// With u the first I columns of a row, g the others, s = 1 / (1 + exp(-g)), p the
+// row's probability (1 without):
+//   a  = p g s u
+//   gu = ga p g s,  gg = ga p u s (1 + g (1 - s)),  gp = sum over columns of ga g s u
+// in fp32, each result rounded once.  s and 1 - s are formed from exp(-|g|), so that
+// neither overflows or cancels: with z = exp(-|g|), s = (g < 0 ? z : 1) / (1 + z) and
+// 1 - s = (g < 0 ? 1 : z) / (1 + z).
+//
+// Each element is read and written once (3 values forward, 5 backward): HBM bounds
+// both.  A team of threads takes a routed row; pad rows are known by token_of and
+// left alone.
+#include "block_common.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct SwigluParams {
+  const int32_t *offsets, *token_of;
+  int E;
+  int64_t cap, I;
+  int64_t spre, sga, sout;
+  const void *pre, *ga;
+  void* out;  // a, or gu and gg
+  const float* probs;
+  float* gp;
+};
+
+// 16 bytes of a row, or one element where rows are not aligned.
+template <typename T, int N>
+struct Piece {
+  T e[N];
+};
+
+template <typename T, int N>
+MOE_DEVICE void load(float (&v)[N], const T* p) {
+  if constexpr (N == 1) {
+    v[0] = to_float(*p);
+  } else {
+    union {
+      uint4 raw;
+      Piece<T, N> t;
+    } u;
+    u.raw = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = to_float(u.t.e[i]);
+  }
+}
+
+template <typename T, int N>
+MOE_DEVICE void store(T* p, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    *p = from_float<T>(v[0]);
+  } else {
+    union {
+      uint4 raw;
+      Piece<T, N> t;
+    } u;
+#pragma unroll
+    for (int i = 0; i < N; i++) u.t.e[i] = from_float<T>(v[i]);
+    *reinterpret_cast<uint4*>(p) = u.raw;
+  }
+}
+
+struct Gate {
+  float s, c;  // sigmoid, 1 - sigmoid
+};
+
+MOE_DEVICE Gate gate_of(float g) {
+  const float z = expf(-fabsf(g)), r = 1.0f / (1.0f + z);
+  const float zr = z * r;
+  return g < 0.0f ? Gate{zr, r} : Gate{r, zr};
+}
+
+// TEAM threads a row: a warp, or the CTA.
+template <typename T, int N, int TEAM>
+__global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluParams p) {
+  const int64_t rows = min64(p.offsets[p.E], p.cap);
+  const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
+  constexpr int kTeams = kThreads / TEAM;
+  for (int64_t r = (int64_t)blockIdx.x * kTeams + team; r < rows; r += (int64_t)gridDim.x * kTeams) {
+    if (p.token_of[r] < 0) continue;
+    const float prob = p.probs ? p.probs[r] : 1.0f;
+    const T* up = static_cast<const T*>(p.pre) + r * p.spre;
+    const T* gate = up + p.I;
+    T* a = static_cast<T*>(p.out) + r * p.sout;
+#pragma unroll 4
+    for (int64_t c = (int64_t)t * N; c < p.I; c += TEAM * N) {
+      float u[N], g[N];
+      load<T, N>(u, up + c);
+      load<T, N>(g, gate + c);
+#pragma unroll
+      for (int i = 0; i < N; i++) u[i] = prob * (g[i] * gate_of(g[i]).s * u[i]);
+      store<T, N>(a + c, u);
+    }
+  }
+}
+
+template <typename T, int N, int TEAM>
+__global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(SwigluParams p) {
+  __shared__ float2 red[2][kThreads / 32];
+  const int64_t rows = min64(p.offsets[p.E], p.cap);
+  const int team = threadIdx.x / TEAM, t = threadIdx.x % TEAM;
+  constexpr int kTeams = kThreads / TEAM;
+  int phase = 0;
+  for (int64_t r = (int64_t)blockIdx.x * kTeams + team; r < rows; r += (int64_t)gridDim.x * kTeams) {
+    if (p.token_of[r] < 0) continue;
+    const float prob = p.probs ? p.probs[r] : 1.0f;
+    const T* up = static_cast<const T*>(p.pre) + r * p.spre;
+    const T* gate = up + p.I;
+    const T* ga = static_cast<const T*>(p.ga) + r * p.sga;
+    T* gu = static_cast<T*>(p.out) + r * p.sout;
+    T* gg = gu + p.I;
+    float sum = 0.0f;
+#pragma unroll 2
+    for (int64_t c = (int64_t)t * N; c < p.I; c += TEAM * N) {
+      float u[N], g[N], d[N];
+      load<T, N>(u, up + c);
+      load<T, N>(g, gate + c);
+      load<T, N>(d, ga + c);
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        const Gate q = gate_of(g[i]);
+        const float act = g[i] * q.s;
+        sum = fmaf(d[i], act * u[i], sum);
+        d[i] *= prob;
+        g[i] = d[i] * u[i] * (q.s * fmaf(g[i], q.c, 1.0f));
+        u[i] = d[i] * act;
+      }
+      store<T, N>(gu + c, u);
+      store<T, N>(gg + c, g);
+    }
+    if (p.gp) {
+      if (TEAM == 32)
+        sum = warp_sum(sum);
+      else
+        sum = block_sum2(sum, 0.0f, red[phase]).x;
+      phase ^= 1;
+      if (t == 0) p.gp[r] = sum;
+    }
+  }
+}
+
+bool aligned_rows(const void* p, int64_t stride, int64_t rows, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || stride * bytes % 16 == 0);
+}
+
+template <typename T, int N, int TEAM>
+cudaError_t run_team(const SwigluParams& p, bool backward, cudaStream_t st) {
+  const int64_t teams = kThreads / TEAM, blocks = (p.cap + teams - 1) / teams;
+  const int64_t most = (int64_t)device_sm_count() * (2048 / kThreads);
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  if (backward)
+    swiglu_bwd_kernel<T, N, TEAM><<<grid, kThreads, 0, st>>>(p);
+  else
+    swiglu_kernel<T, N, TEAM><<<grid, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int N>
+cudaError_t run_pieces(const SwigluParams& p, int64_t routes, bool backward, cudaStream_t st) {
+  // rows for every SM's CTAs, or rows too short for more than a warp: a warp a row
+  if (routes >= (int64_t)device_sm_count() * 8 || p.I <= 32 * N) return run_team<T, N, 32>(p, backward, st);
+  return run_team<T, N, kThreads>(p, backward, st);
+}
+
+template <typename T>
+cudaError_t run(const SwigluParams& p, int64_t routes, bool backward, cudaStream_t st) {
+  constexpr int b = sizeof(T), N = 16 / b;
+  const bool vec = p.I * b % 16 == 0 && aligned_rows(p.pre, p.spre, p.cap, b) && aligned_rows(p.out, p.sout, p.cap, b) &&
+                   aligned_rows(p.ga, p.sga, p.cap, b);
+  return vec ? run_pieces<T, N>(p, routes, backward, st) : run_pieces<T, 1>(p, routes, backward, st);
+}
+
+cudaError_t dispatch(const SwigluParams& p, int32_t dtype, int64_t routes, bool backward, cudaStream_t st) {
+  switch (dtype) {
+    case MOE_ELEM_F32: return run<float>(p, routes, backward, st);
+    case MOE_ELEM_BF16: return run<__nv_bfloat16>(p, routes, backward, st);
+    default: return run<__half>(p, routes, backward, st);
+  }
+}
+
+SwigluParams params(const moe_handle_dev& h, const moe_shape& s, const moe_layout& l, int64_t I, const moe_rows& pre,
+                    const moe_rows& out, const float* probs) {
+  SwigluParams p = {};
+  p.offsets = h.padded_offsets;
+  p.token_of = h.token_of;
+  p.E = (int)s.E;
+  p.cap = l.capacity;
+  p.I = I;
+  p.pre = pre.data;
+  p.spre = pre.stride;
+  p.out = out.data;
+  p.sout = out.stride;
+  p.probs = probs;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu(const moe_handle_dev& h, const moe_shape& s, const moe_layout& l, int64_t I, int32_t dtype,
+                          const moe_rows& pre, const float* probs, const moe_rows& act, cudaStream_t st) {
+  return dispatch(params(h, s, l, I, pre, act, probs), dtype, s.T * s.K, false, st);
+}
+
+cudaError_t launch_swiglu_backward(const moe_handle_dev& h, const moe_shape& s, const moe_layout& l, int64_t I,
+                                   int32_t dtype, const moe_rows& pre, const float* probs, const moe_rows& grad_act,
+                                   const moe_rows& grad_pre, float* grad_probs, cudaStream_t st) {
+  SwigluParams p = params(h, s, l, I, pre, grad_pre, probs);
+  p.ga = grad_act.data;
+  p.sga = grad_act.stride;
+  p.gp = grad_probs;
+  return dispatch(p, dtype, s.T * s.K, true, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,296 @@
+"""Products grouped by expert on the GPU (forward, gradient of the rows, gradient of the weights) against their
+64-bit definition, and on small whole numbers, whose sums are exact in fp32 in any order, bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import block_util as bu
+import train_util as tu
+from gpu_util import moe_mod
+from train_util import BF, HF, F32
+
+pytestmark = pytest.mark.gpu
+
+# (T, E, K, m, N, Kd): one token to several tiles of rows; widths of one element, odd, of a tile, of several
+SIZES = [(1, 1, 1, 1, 1, 1), (1, 8, 2, 32, 128, 64), (3, 4, 2, 8, 33, 65), (5, 300, 8, 1, 48, 40), (40, 3, 2, 32, 256, 128),
+         (7, 16, 4, 1, 264, 72), (64, 2, 1, 8, 512, 256), (130, 5, 3, 4, 136, 1000), (300, 2, 2, 1, 320, 192),
+         (100, 7, 3, 16, 1001, 77), (700, 3, 1, 32, 128, 520), (33, 1024, 1, 1, 64, 64), (257, 1, 1, 1, 640, 384),
+         (513, 4, 4, 32, 256, 256), (1100, 1, 1, 1, 72, 136)]
+
+
+def matrices(E, N, Kd, dtype, seed, ints=None):
+    g = torch.Generator().manual_seed(seed)
+    if ints is not None:
+        return torch.randint(-ints, ints + 1, (E, N, Kd), generator=g).to(dtype)
+    return (torch.randn(E, N, Kd, generator=g) * Kd ** -0.5).to(dtype)
+
+
+def forward(moe, r, w, x):
+    y = torch.full((r.cap, w.shape[1]), 7.0, dtype=w.dtype, device="cuda")
+    moe.moe_grouped_gemm(r.handle, r.shape, r.layout, w.cuda(), x.cuda(), y, tu.workspace(moe, r, *w.shape[1:]))
+    torch.cuda.synchronize()
+    return y
+
+
+def data(moe, r, w, gy):
+    gx = torch.full((r.cap, w.shape[2]), 7.0, dtype=w.dtype, device="cuda")
+    moe.moe_grouped_gemm_backward_data(r.handle, r.shape, r.layout, w.cuda(), gy.cuda(), gx,
+                                       tu.workspace(moe, r, *w.shape[1:]))
+    torch.cuda.synchronize()
+    return gx
+
+
+def weight(moe, r, gy, x, out_dtype, addend=None):
+    N, Kd = gy.shape[1], x.shape[1]
+    gw = torch.full((r.shape.E, N, Kd), float("nan"), dtype=out_dtype, device="cuda")
+    moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, x.cuda(), gy.cuda(), gw,
+                                         tu.workspace(moe, r, N, Kd), None if addend is None else addend.cuda())
+    torch.cuda.synchronize()
+    return gw
+
+
+def assert_rows(r, got, ref, tol=None):
+    got = got.cpu()
+    assert bool((got[~r.routed] == 7.0).all()), "rows outside the segments were written"
+    if tol is None:
+        assert torch.equal(got[r.routed], ref[r.routed].to(got.dtype))
+    else:
+        bu.assert_within(got[r.routed], ref[r.routed], tol[r.routed])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,E,K,m,N,Kd", SIZES)
+def test_whole_numbers(T, E, K, m, N, Kd, dtype):
+    """Sums of products of whole numbers up to 2 stay below 2^24: every result is the exact sum, rounded once."""
+    moe = moe_mod()
+    r = tu.Routed(moe, T, E, K, m, empty=(0,) if E > K else ())
+    w = matrices(E, N, Kd, dtype, 1, ints=2)
+    x, gy = r.rows(Kd, dtype, 2, ints=2), r.rows(N, dtype, 3, ints=2)
+    assert_rows(r, forward(moe, r, w, x), tu.gemm_forward(r, w, x))
+    assert_rows(r, data(moe, r, w, gy), tu.gemm_data(r, w, gy))
+    gw = tu.gemm_weight(r, gy, x)
+    assert torch.equal(weight(moe, r, gy, x, dtype).cpu(), gw.to(dtype))
+    assert torch.equal(weight(moe, r, gy, x, F32).cpu(), gw.float())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,E,K,m,N,Kd", [(1, 8, 2, 32, 264, 2048), (50, 6, 2, 8, 384, 512), (333, 4, 2, 1, 129, 257),
+                                          (900, 2, 1, 32, 256, 640)])
+def test_against_64_bits(T, E, K, m, N, Kd, dtype):
+    moe = moe_mod()
+    r = tu.Routed(moe, T, E, K, m, seed=4, skew=0.5)
+    w = matrices(E, N, Kd, dtype, 5)
+    x, gy = r.rows(Kd, dtype, 6), r.rows(N, dtype, 7)
+    ref = tu.gemm_forward(r, w, x)
+    assert_rows(r, forward(moe, r, w, x), ref, tu.gemm_tol(ref, tu.gemm_forward(r, w.abs(), x.abs()), Kd, dtype))
+    ref = tu.gemm_data(r, w, gy)
+    assert_rows(r, data(moe, r, w, gy), ref, tu.gemm_tol(ref, tu.gemm_data(r, w.abs(), gy.abs()), N, dtype))
+    ref, most = tu.gemm_weight(r, gy, x), tu.gemm_weight(r, gy.abs(), x.abs())
+    rows = max(n - b for _, b, n in r.segments)
+    for out in (dtype, F32):
+        bu.assert_within(weight(moe, r, gy, x, out), ref, tu.gemm_tol(ref, most, rows, out))
+
+
+@pytest.mark.parametrize("N,Kd", [(128, 192), (264, 136), (33, 50)])
+def test_addend(N, Kd):
+    """The addend joins the fp32 sum; it may be the gradient itself, which then gathers several calls."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 60, 5, 2, 8, empty=(1,))
+    x, gy = r.rows(Kd, BF, 1, ints=2), r.rows(N, BF, 2, ints=2)
+    add = torch.randint(-9, 10, (5, N, Kd), generator=torch.Generator().manual_seed(3)).float()
+    ref = tu.gemm_weight(r, gy, x)
+    assert torch.equal(weight(moe, r, gy, x, F32, add).cpu(), (ref + add).float())
+    gw = add.cuda()
+    ws = tu.workspace(moe, r, N, Kd)
+    for _ in range(3):
+        moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, x.cuda(), gy.cuda(), gw, ws, gw)
+    assert torch.equal(gw.cpu(), (3 * ref + add).float())
+
+
+@pytest.mark.parametrize("N,Kd", [(128, 128), (72, 41)])
+@pytest.mark.parametrize("cut", [0, 1, 17, 70])
+def test_below_the_capacity(cut, N, Kd):
+    """Rows at or beyond the capacity are neither read nor written, and take no part in the weights' gradient."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 50, 4, 2, 8, cap=cut, seed=3)
+    w = matrices(4, N, Kd, BF, 1, ints=2)
+    x, gy = r.rows(Kd, BF, 2, ints=2), r.rows(N, BF, 3, ints=2)
+    assert_rows(r, forward(moe, r, w, x), tu.gemm_forward(r, w, x))
+    assert_rows(r, data(moe, r, w, gy), tu.gemm_data(r, w, gy))
+    assert torch.equal(weight(moe, r, gy, x, F32).cpu(), tu.gemm_weight(r, gy, x).float())
+
+
+@pytest.mark.parametrize("N,Kd", [(128, 256), (40, 24)])
+def test_no_tokens(N, Kd):
+    moe = moe_mod()
+    r = tu.Routed(moe, 0, 3, 1, 8)
+    w = matrices(3, N, Kd, BF, 1)
+    forward(moe, r, w, torch.full((r.cap, Kd), float("nan"), dtype=BF))
+    data(moe, r, w, torch.full((r.cap, N), float("nan"), dtype=BF))
+    nan = lambda c: torch.full((r.cap, c), float("nan"), dtype=BF)
+    assert bool((weight(moe, r, nan(N), nan(Kd), F32) == 0).all())
+    add = matrices(3, N, Kd, F32, 2)
+    assert torch.equal(weight(moe, r, nan(N), nan(Kd), F32, add).cpu(), add)
+
+
+@pytest.mark.parametrize("N,Kd,pad,shift", [(128, 192, 8, 8), (128, 192, 64, 0), (128, 192, 1, 0), (136, 72, 3, 5),
+                                            (65, 31, 7, 1)])
+def test_strides_and_alignment(N, Kd, pad, shift):
+    moe = moe_mod()
+    r = tu.Routed(moe, 90, 3, 2, 4)
+    w = matrices(3, N, Kd, HF, 1, ints=2)
+    x, gy = r.rows(Kd, HF, 2, ints=2), r.rows(N, HF, 3, ints=2)
+
+    def apart(t):
+        buf = torch.full((r.cap, t.shape[1] + pad + shift), 9.0, dtype=HF, device="cuda")
+        v = buf[:, shift:shift + t.shape[1]]
+        v.copy_(t)
+        return buf, v
+
+    def outside(buf, cols):
+        assert bool((buf[:, :shift] == 9.0).all()) and bool((buf[:, shift + cols:] == 9.0).all())
+
+    # the weights one element off their allocation's alignment where rows are off too
+    store = torch.zeros(w.numel() + 8, dtype=HF, device="cuda")
+    wv = store[shift % 8:][:w.numel()].view_as(w)
+    wv.copy_(w)
+    xv, gv = apart(x)[1], apart(gy)[1]
+    ws = tu.workspace(moe, r, N, Kd)
+    yb, yv = apart(torch.full((r.cap, N), 7.0))
+    moe.moe_grouped_gemm(r.handle, r.shape, r.layout, wv, xv, yv, ws)
+    assert_rows(r, yv, tu.gemm_forward(r, w, x))
+    outside(yb, N)
+    gb, gxv = apart(torch.full((r.cap, Kd), 7.0))
+    moe.moe_grouped_gemm_backward_data(r.handle, r.shape, r.layout, wv, gv, gxv, ws)
+    assert_rows(r, gxv, tu.gemm_data(r, w, gy))
+    outside(gb, Kd)
+    gw = torch.empty(3, N, Kd, device="cuda")
+    moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, xv, gv, gw, ws)
+    assert torch.equal(gw.cpu(), tu.gemm_weight(r, gy, x).float())
+
+
+@pytest.mark.parametrize("N,Kd", [(256, 128), (77, 50)])
+def test_nonfinite_rows_and_weights_stay_alone(N, Kd):
+    moe = moe_mod()
+    r = tu.Routed(moe, 80, 4, 2, 8, seed=1)
+    w, x, gy = matrices(4, N, Kd, BF, 1), r.rows(Kd, BF, 2), r.rows(N, BF, 3)
+    seg = [(e, b, n) for e, b, n in r.segments if n - b > 4]
+    (e0, b0, _), (e1, b1, n1) = seg[0], seg[1]
+    y, gx, gw = forward(moe, r, w, x), data(moe, r, w, gy), weight(moe, r, gy, x, F32)
+    bad_x, bad_g, bad_w = x.clone(), gy.clone(), w.clone()
+    bad_x[b0 + 2, 1], bad_g[b0 + 2, 3] = float("nan"), float("inf")
+    bad_w[e1, N - 1, Kd - 1] = float("nan")
+    keep = r.routed.clone()
+    keep[b0 + 2] = False
+    keep[b1:n1] = False
+    keep = keep.cuda()
+    ny, ng = forward(moe, r, bad_w, bad_x), data(moe, r, bad_w, bad_g)
+    assert torch.equal(ny[keep], y[keep]) and torch.equal(ng[keep], gx[keep])
+    assert bool(torch.isnan(ny[b0 + 2]).all()) and bool(torch.isnan(ny[b1:n1, N - 1]).all())
+    assert torch.equal(ny[b1:n1, :N - 1], y[b1:n1, :N - 1])
+    assert bool(torch.isnan(ng[b1:n1, Kd - 1]).all()) and torch.equal(ng[b1:n1, :Kd - 1], gx[b1:n1, :Kd - 1])
+    nw = weight(moe, r, bad_g, bad_x, F32)
+    others = [e for e in range(4) if e != e0]
+    assert torch.equal(nw[others], gw[others])
+    assert bool(torch.isnan(nw[e0][:, 1]).all()) and not bool(torch.isfinite(nw[e0][3]).any())
+
+
+def test_repeated_calls_agree():
+    moe = moe_mod()
+    r = tu.Routed(moe, 500, 8, 3, 32, skew=1.0)
+    w, x, gy = matrices(8, 384, 320, BF, 1), r.rows(320, BF, 2), r.rows(384, BF, 3)
+    first = forward(moe, r, w, x), data(moe, r, w, gy), weight(moe, r, gy, x, F32)
+    for _ in range(5):
+        again = forward(moe, r, w, x), data(moe, r, w, gy), weight(moe, r, gy, x, F32)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("N,Kd", [(128, 128), (30, 24)])
+def test_a_damaged_handle(N, Kd):
+    """A segment that begins before the rows, or has no rows, is left out; the other experts are as ever."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 60, 6, 2, 8)
+    w, x, gy = matrices(6, N, Kd, BF, 1), r.rows(Kd, BF, 2), r.rows(N, BF, 3)
+    y, gw = forward(moe, r, w, x), weight(moe, r, gy, x, F32)
+    some = [e for e, b, n in r.segments if n > b][:2]
+    r.handle.padded_offsets[some[0]] = -3
+    r.handle.tokens_per_expert[some[1]] = -(1 << 31)
+    for e, b, n in r.segments:
+        if e in some:
+            y[b:n] = 7.0
+            gw[e] = 0.0
+    assert torch.equal(forward(moe, r, w, x), y)
+    assert torch.equal(weight(moe, r, gy, x, F32), gw)
+
+
+def test_streams_and_graphs():
+    """Captured and replayed with other inputs and another routing, and on a stream of its own."""
+    moe = moe_mod()
+    T, E, K, m, N, Kd = 120, 6, 2, 8, 256, 192
+    a, b = tu.Routed(moe, T, E, K, m, seed=1), tu.Routed(moe, T, E, K, m, seed=2)
+    w = matrices(E, N, Kd, BF, 1, ints=2)
+    xs, gs = [t.rows(Kd, BF, 3, ints=2) for t in (a, b)], [t.rows(N, BF, 4, ints=2) for t in (a, b)]
+    live = tu.Routed(moe, T, E, K, m, seed=1)
+    wd, x, gy = w.cuda(), xs[0].cuda(), gs[0].cuda()
+    y = torch.zeros(a.cap, N, dtype=BF, device="cuda")
+    gx = torch.zeros(a.cap, Kd, dtype=BF, device="cuda")
+    gw = torch.zeros(E, N, Kd, device="cuda")
+    ws = tu.workspace(moe, a, N, Kd)
+
+    def calls():
+        moe.moe_grouped_gemm(live.handle, a.shape, a.layout, wd, x, y, ws)
+        moe.moe_grouped_gemm_backward_data(live.handle, a.shape, a.layout, wd, gy, gx, ws)
+        moe.moe_grouped_gemm_backward_weight(live.handle, a.shape, a.layout, x, gy, gw, ws)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for r, xv, gv in ((b, xs[1], gs[1]), (a, xs[0], gs[0]), (b, xs[1], gs[1])):
+        x.copy_(xv)
+        gy.copy_(gv)
+        for f in ("padded_offsets", "tokens_per_expert", "token_of"):
+            getattr(live.handle, f).copy_(getattr(r.handle, f))
+        for t in (y, gx):
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_rows(r, y, tu.gemm_forward(r, w, xv))
+        assert_rows(r, gx, tu.gemm_data(r, w, gv))
+        assert torch.equal(gw.cpu(), tu.gemm_weight(r, gv, xv).float())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y.fill_(7.0)
+    side.wait_stream(torch.cuda.current_stream())
+    moe.moe_grouped_gemm(live.handle, a.shape, a.layout, wd, x, y, ws, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert_rows(b, y, tu.gemm_forward(b, w, xs[1]))
+
+
+def test_refusals():
+    moe = moe_mod()
+    r = tu.Routed(moe, 10, 2, 1, 8)
+    w = matrices(2, 64, 32, BF, 1).cuda()
+    x, y = torch.zeros(r.cap, 32, dtype=BF, device="cuda"), torch.zeros(r.cap, 64, dtype=BF, device="cuda")
+    ws = tu.workspace(moe, r, 64, 32)
+    call = lambda w=w, x=x, y=y, ws=ws: moe.moe_grouped_gemm(r.handle, r.shape, r.layout, w, x, y, ws)
+    call()
+    for bad in (dict(w=w[:1]), dict(w=w.float()), dict(x=x.half()), dict(x=y), dict(y=y[:3]), dict(w=w.transpose(1, 2)),
+                dict(x=torch.zeros(r.cap, 64, dtype=BF, device="cuda")[:, ::2]), dict(ws=ws.cpu())):
+        with pytest.raises(ValueError):
+            call(**bad)
+    with pytest.raises(moe.MoeError):
+        call(ws=ws[:16])
+    wide = torch.zeros(r.cap, 96, dtype=BF, device="cuda")
+    with pytest.raises(moe.MoeError):  # y over x
+        call(x=wide[:, :32], y=wide[:, 16:80])
+    gw = torch.zeros(2, 64, 32, dtype=BF, device="cuda")
+    with pytest.raises(moe.MoeError):  # an addend beside a 16-bit gradient
+        moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, x, y, gw, ws, gw.float())
+    with pytest.raises(moe.MoeError):  # a gradient of the other 16-bit type
+        moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, x, y, gw.half(), ws)
+    big = torch.zeros(2 * 64 * 32 + 4, device="cuda")
+    with pytest.raises(moe.MoeError):  # an addend that overlaps the gradient
+        moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, x, y, big[4:].view(2, 64, 32), ws,
+                                             big[:-4].view(2, 64, 32))
