@@ -8,7 +8,7 @@ size_t grouped_gemm_workspace_bytes(const moe_shape& s, const moe_layout& l, int
 }
 
 cudaError_t launch_grouped_gemm(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
-  return launch_grouped_gemm_any(dir, g, st);
+  return grouped_gemm_tc_takes(dir, g) ? launch_grouped_gemm_tc(dir, g, st) : launch_grouped_gemm_any(dir, g, st);
 }
 
 }  // namespace moe

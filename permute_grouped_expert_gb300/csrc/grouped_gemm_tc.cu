@@ -1,0 +1,601 @@
+// grouped_gemm_tc.cu -- products grouped by expert on the tensor cores of pairs of
+// SMs (2-CTA clusters, tcgen05 cta_group::2, operands by TMA, sums in TMEM).
+//
+//   kForward  y[r]  = W x[r]            kData  gx[r] = W^T gy[r]
+//   kWeight   gW    = sum gy[r] x[r]^T (+ addend)
+//
+// Rows' products put the expert's matrix on the M side of the MMA and its rows on
+// the N side: a tile is 256 features (128 a CTA) by up to 256 rows, and an expert's
+// last rows cost what they are, in steps of 32, where rows as M would be filled up
+// to 256.  kData reads W as it lies, its features contiguous (an M-major operand),
+// so that no transposed copy exists.  The weights' gradient has 256 x 256 tiles of
+// the matrix and runs along the expert's rows, both operands with M and N
+// contiguous; its last 16 rows may reach into rows that are not the expert's: those
+// are overwritten with zeros in shared memory between the copy and the MMA (they
+// may hold anything, NaN too).
+//
+// Per CTA, warp-specialised (rank 0 leads the pair):
+//   warp 0      TMA producer of its half of both operands, 64 of the contraction a stage
+//   warp 1      TMEM; on the leader one thread issues the MMAs
+//   warp 2      on the leader: claims tiles and hands their numbers to both CTAs
+//   warp 3      kWeight: zeros behind an expert's last row
+//   warps 4..7  epilogue of this CTA's 128 features, beside the next tile's MMAs
+// Every wait is bounded (MOE_DEV_ERR_TIMEOUT, then a clean exit).
+#include <type_traits>
+
+#include "grouped_gemm.cuh"
+#include "sm100_ptx.cuh"
+#include "tensor_map.h"
+
+namespace moe {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 256;
+constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
+constexpr int kStages = 6, kSlots = 3;
+constexpr int kBand = 8;                                // tiles of a band that share their operands in L2
+constexpr uint32_t kOperand = 128 * BK * 2;             // a CTA's half of an operand: 16 KB
+constexpr uint32_t kBox = 64 * BK * 2;                  // a box of an operand that is not K-major
+constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOutBytes = 32 * 128;                // kWeight: a warp's 32 rows of 128 bytes
+constexpr int kMaxE = 1024;
+constexpr size_t kDynSmem = 1024 + (size_t)kStages * kStageBytes;
+
+struct TcParams {
+  const int32_t *offsets, *counts;
+  int32_t* status;
+  int32_t* next;  // tile counter, or NULL: tiles in turn
+  void* out;
+  const float* addend;
+  int64_t sout;
+  int64_t cap;
+  int E;
+  int features, contraction;  // rows' products
+  int N, Kd;                  // kWeight
+  int mt;                     // tiles of 256 features (kWeight: of N)
+  int kt;                     // kWeight: tiles of 256 of Kd
+};
+
+struct Tile {
+  int e, m, n;         // expert; tile of features; kWeight: tile of Kd
+  int64_t row, end;    // rows [row, end) of the tile, or of the expert (kWeight)
+  int cols;            // columns of the MMA
+};
+
+// Tiles of an expert in bands of kBand along one side, the other side outermost in
+// a band: tiles that run at once share few operands.
+MOE_DEVICE void banded(int local, int along, int across, int& a, int& c) {
+  const int band = local / (kBand * across), in = local - band * kBand * across;
+  const int width = min(kBand, along - band * kBand);
+  c = in / width;
+  a = band * kBand + in - c * width;
+}
+
+// Tiles of rows of an expert with `rows` rows, and rows of each.
+MOE_DEVICE int row_tiles(int64_t rows) { return (int)((rows + BN - 1) / BN); }
+MOE_DEVICE int tile_rows(int64_t rows, int tiles) { return (int)((rows + tiles - 1) / tiles + 31) & ~31; }
+
+template <GemmDir DIR>
+MOE_DEVICE Tile tile_of(int t, const int* prefix, const TcParams& p) {
+  Tile i;
+  int64_t beg, end;
+  if (DIR == kWeight) {
+    const int per = p.mt * p.kt;
+    i.e = t / per;
+    banded(t - i.e * per, p.mt, p.kt, i.m, i.n);
+    gemm_segment(p.offsets, p.counts, p.cap, i.e, beg, end);
+    i.row = beg;
+    i.end = end;
+    i.cols = BN;
+  } else {
+    i.e = expert_of_row(prefix, p.E, t);
+    gemm_segment(p.offsets, p.counts, p.cap, i.e, beg, end);
+    const int tiles = row_tiles(end - beg);
+    banded(t - prefix[i.e], tiles, p.mt, i.n, i.m);
+    i.cols = tile_rows(end - beg, tiles);
+    i.row = beg + (int64_t)i.n * i.cols;
+    i.end = min64(i.row + i.cols, end);
+  }
+  return i;
+}
+
+MOE_DEVICE int blocks_of(const Tile& i, GemmDir dir, const TcParams& p) {
+  return dir == kWeight ? (int)((i.end - i.row + BK - 1) / BK) : (p.contraction + BK - 1) / BK;
+}
+
+// Whether the last stage of a kWeight tile holds rows that are not the expert's
+// within its last 16.
+MOE_DEVICE bool ragged(const Tile& i) { return ((i.end - i.row) & 15) != 0; }
+
+template <typename T>
+MOE_DEVICE uint32_t pack2(float a, float b);
+template <>
+MOE_DEVICE uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+MOE_DEVICE uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+MOE_DEVICE void settle(uint64_t ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < ns) __nanosleep(1000);
+}
+
+// T: 16-bit type of the operands; OUT: of the result.
+template <GemmDir DIR, typename T, typename OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                           const __grid_constant__ CUtensorMap tm_b16, const __grid_constant__ CUtensorMap tm_out,
+                           TcParams p) {
+  constexpr bool kW = DIR == kWeight, kAmn = DIR != kForward, kBmn = kW;
+  extern __shared__ uint8_t dyn_smem[];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tail[kStages], s_tfull[2], s_tempty[2];
+  __shared__ __align__(8) uint64_t s_have[kSlots], s_free[kSlots], s_drain;
+  __shared__ int s_tile[kSlots];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ int s_prefix[kW ? 1 : kMaxE + 1];
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  volatile int* abort_flag = &s_abort;
+
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int s = 0; s < kStages; s++) {
+      // on the leader: its producer (and, kWeight, a second arrival) and both CTAs'
+      // bytes, or both CTAs' warp 3 after the zeros
+      mbar_init(&s_full[s], kW ? 2 : 1);
+      mbar_init(&s_empty[s], 1);  // each CTA's own, by the leader's commit
+      mbar_init(&s_tail[s], 1);   // each CTA's own bytes of a stage that gets zeros
+    }
+    for (int a = 0; a < 2; a++) {
+      mbar_init(&s_tfull[a], 1);
+      mbar_init(&s_tempty[a], 8);  // on the leader: 4 epilogue warps of each CTA
+    }
+    for (int s = 0; s < kSlots; s++) {
+      mbar_init(&s_have[s], 1);
+      mbar_init(&s_free[s], kW ? 13 : 11);  // on the leader: every reader of both CTAs
+    }
+    mbar_init(&s_drain, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) tmem_alloc_pair(&s_tmem, kTmemCols);
+  if (!kW && warp == 0) {
+    int base = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int m = 0;
+      if (e < p.E) {
+        int64_t b, n;
+        gemm_segment(p.offsets, p.counts, p.cap, e, b, n);
+        m = row_tiles(n - b) * p.mt;
+      }
+      int incl = m;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (e < p.E) s_prefix[e] = base + incl - m;
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) s_prefix[p.E] = base;
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem;
+  const int total = kW ? p.E * p.mt * p.kt : s_prefix[p.E];
+
+  // The number of the i-th tile of this pair, -1 behind the last; called by one
+  // thread of each reader, in order.
+  auto next_tile = [&](int i) -> int {
+    if (!p.next) {
+      const int64_t t = cluster + (int64_t)i * clusters;
+      return t < total ? (int)t : -1;
+    }
+    const int s = i % kSlots;
+    if (!mbar_wait_cluster(&s_have[s], (i / kSlots) & 1, abort_flag, p.status)) return -1;
+    const int t = *(volatile int*)&s_tile[s];
+    mbar_arrive_cluster(mapa_shared(smem_u32(&s_free[s]), 0));
+    return t;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued_parity[kStages];
+      bool issued[kStages];
+      for (int s = 0; s < kStages; s++) issued[s] = false;
+      bool ok = true;
+      for (int i = 0; ok; i++) {
+        const int t = next_tile(i);
+        if (t < 0) break;
+        const Tile ti = tile_of<DIR>(t, s_prefix, p);
+        const int nkb = blocks_of(ti, DIR, p);
+        const int f0 = ti.m * BM + (int)rank * 128;             // first feature of this CTA
+        const int half = ti.cols / 2;                           // columns of this CTA
+        const int c0 = kW ? ti.n * BN + (int)rank * 128 : 0;    // kWeight: its first column
+        const uint32_t bytes = kW ? kStageBytes : kOperand + (uint32_t)half * BK * 2;
+        for (int kb = 0; kb < nkb; kb++) {
+          if (!mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + (size_t)stage * kStageBytes;
+          uint8_t* sb = sa + kOperand;
+          const bool tail = kW && kb == nkb - 1 && ragged(ti);
+          uint32_t bar;
+          if (tail) {
+            bar = mapa_shared(smem_u32(&s_tail[stage]), rank);
+            mbar_arrive_expect_tx(&s_tail[stage], bytes);
+          } else {
+            bar = mapa_shared(smem_u32(&s_full[stage]), 0);
+            if (rank == 0) {
+              mbar_arrive_expect_tx(&s_full[stage], 2 * bytes);
+              if (kW) mbar_arrive(&s_full[stage]);
+            }
+          }
+          const int k0 = kb * BK;
+          if (kW) {
+            const int r0 = (int)ti.row + k0;
+            tma_load_2d_pair(sa, &tm_a, f0, r0, bar);
+            tma_load_2d_pair(sa + kBox, &tm_a, f0 + 64, r0, bar);
+            tma_load_2d_pair(sb, &tm_b, c0, r0, bar);
+            tma_load_2d_pair(sb + kBox, &tm_b, c0 + 64, r0, bar);
+          } else {
+            if (DIR == kForward) {
+              tma_load_3d_pair(sa, &tm_a, k0, f0, ti.e, bar);
+            } else {
+              tma_load_3d_pair(sa, &tm_a, f0, k0, ti.e, bar);
+              tma_load_3d_pair(sa + kBox, &tm_a, f0 + 64, k0, ti.e, bar);
+            }
+            const int r0 = (int)ti.row + (int)rank * half;
+            if (half == 128) {
+              tma_load_2d_pair(sb, &tm_b, k0, r0, bar);
+            } else {
+              for (int j = 0; j < half; j += 16) tma_load_2d_pair(sb + j * BK * 2, &tm_b16, k0, r0 + j, bar);
+            }
+          }
+          issued[stage] = !tail;
+          issued_parity[stage] = phase;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        if (rank == 0) {
+          for (int s = 0; s < kStages; s++) {
+            if (!issued[s]) continue;
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(&s_full[s], issued_parity[s]) && globaltimer_ns() - t0 < kWaitLimitNs) {
+            }
+          }
+        }
+        settle(2000000);  // 2 ms: far longer than any single copy takes
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer (leader)
+    if (lane == 0 && rank == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int i = 0; ok; i++) {
+        const int t = next_tile(i);
+        if (t < 0) break;
+        const Tile ti = tile_of<DIR>(t, s_prefix, p);
+        const int nkb = blocks_of(ti, DIR, p);
+        const uint32_t idesc = idesc_16bit(BM, (uint32_t)ti.cols, std::is_same<T, __nv_bfloat16>::value, kAmn, kBmn);
+        if (!mbar_wait_cluster(&s_tempty[acc], acc_phase ^ 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        for (int kb = 0; kb < nkb; kb++) {
+          if (!mbar_wait_cluster(&s_full[stage], phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + (size_t)stage * kStageBytes), sb = sa + kOperand;
+          const uint64_t adesc = kAmn ? smem_desc_sw128_mn(sa, kBox) : smem_desc_sw128(sa);
+          const uint64_t bdesc = kBmn ? smem_desc_sw128_mn(sb, kBox) : smem_desc_sw128(sb);
+          // a step of 16: 32 bytes of K-major rows, or 16 rows of 128 bytes
+          constexpr uint64_t kAstep = kAmn ? 128 : 2, kBstep = kBmn ? 128 : 2;
+          const int left = kW ? (int)(ti.end - ti.row) - kb * BK : p.contraction - kb * BK;
+#pragma unroll
+          for (int k = 0; k < BK / 16; k++)
+            if (k * 16 < left)
+              mma_bf16_pair(d_tmem, adesc + kAstep * k, bdesc + kBstep * k, idesc, (kb | k) != 0 ? 1u : 0u);
+          mma_commit_pair(&s_empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(&s_tfull[acc], 0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (!ok) {
+        mma_commit_pair(&s_drain, 0x1);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&s_drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- tiles (leader)
+    if (lane == 0 && rank == 0 && p.next) {
+      for (int i = 0;; i++) {
+        const int s = i % kSlots;
+        int t = atomicAdd(p.next, 1);
+        if (t >= total) t = -1;
+        if (!mbar_wait_cluster(&s_free[s], ((i / kSlots) & 1) ^ 1, abort_flag, p.status)) break;
+        for (uint32_t r = 0; r < 2; r++) {
+          st_cluster_u32(mapa_shared(smem_u32(&s_tile[s]), r), (uint32_t)t);
+          mbar_arrive_cluster(mapa_shared(smem_u32(&s_have[s]), r));
+        }
+        if (t < 0) break;
+      }
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------- zeros (kWeight)
+    if (kW) {
+      int stage = 0;
+      uint32_t phases = 0;  // bit s: parity of s_tail[s]
+      for (int i = 0;; i++) {
+        int t = 0;
+        if (lane == 0) t = next_tile(i);
+        t = __shfl_sync(0xffffffffu, t, 0);
+        if (t < 0) break;
+        const Tile ti = tile_of<DIR>(t, s_prefix, p);
+        const int nkb = blocks_of(ti, DIR, p);
+        if (nkb && ragged(ti)) {
+          const int s = (stage + nkb - 1) % kStages;
+          int ok = 0;
+          if (lane == 0) ok = mbar_wait(&s_tail[s], (phases >> s) & 1, abort_flag, p.status) ? 1 : 0;
+          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          phases ^= 1u << s;
+          const int rows = (int)(ti.end - ti.row) - (nkb - 1) * BK, stop = (rows + 15) & ~15;
+          uint8_t* base = smem + (size_t)s * kStageBytes;
+          for (int j = lane; j < (stop - rows) * 8 * 4; j += 32) {  // 16 bytes each of the four boxes' rows
+            const int box = j & 3, at = j >> 2;
+            *reinterpret_cast<uint4*>(base + box * kBox + rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_full[s]), 0));
+        }
+        stage = (stage + nkb) % kStages;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    const int lane_base = 32 * (warp & 3);
+    uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (size_t)(warp & 3) * kOutBytes;  // kWeight
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int i = 0;; i++) {
+      int t = 0;
+      if (lane == 0) t = next_tile(i);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      if (t < 0) break;
+      const Tile ti = tile_of<DIR>(t, s_prefix, p);
+      int ok = 0;
+      if (lane == 0) ok = mbar_wait(&s_tfull[acc], acc_phase, abort_flag, p.status) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
+      const int f_warp = ti.m * BM + (int)rank * 128 + lane_base;  // first feature of this warp
+      if constexpr (kW) {
+        // this lane's row of the matrix, 128 bytes at a time through shared memory
+        constexpr int kCols = 128 / (int)sizeof(OUT);
+        const bool none = ti.end == ti.row;
+        const int64_t n = f_warp + lane;
+        const float* add = p.addend ? p.addend + ((int64_t)ti.e * p.N + n) * p.Kd : nullptr;
+        for (int c = 0; c < BN; c += kCols) {
+          const int k0 = ti.n * BN + c;
+          if (k0 >= p.Kd || f_warp >= p.N) break;
+          uint4 chunk[8];
+#pragma unroll
+          for (int h = 0; h < kCols / 32; h++) {
+            float v[32];
+            if (none) {
+#pragma unroll
+              for (int j = 0; j < 32; j++) v[j] = 0.0f;
+            } else {
+              tmem_ld32(taddr + c + h * 32, v);
+            }
+            if constexpr (sizeof(OUT) == 4) {
+              if (add && n < p.N) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                  if (k0 + j < p.Kd) {
+                    const float4 a = *reinterpret_cast<const float4*>(add + k0 + j);
+                    v[j] += a.x;
+                    v[j + 1] += a.y;
+                    v[j + 2] += a.z;
+                    v[j + 3] += a.w;
+                  }
+              }
+#pragma unroll
+              for (int q = 0; q < 8; q++)
+                chunk[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                      __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; q++)
+                chunk[h * 4 + q] = make_uint4(pack2<T>(v[8 * q], v[8 * q + 1]), pack2<T>(v[8 * q + 2], v[8 * q + 3]),
+                                              pack2<T>(v[8 * q + 4], v[8 * q + 5]), pack2<T>(v[8 * q + 6], v[8 * q + 7]));
+            }
+          }
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; q++) *reinterpret_cast<uint4*>(s_out + lane * 128 + ((q ^ (lane & 7)) * 16)) = chunk[q];
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm_out, s_out, k0, f_warp, ti.e);
+            bulk_commit();
+          }
+        }
+      } else {
+        // columns are rows of the result, lanes features: neighbouring lanes exchange
+        // one of two rows, so that each stores two features of one
+        const int f = f_warp + (lane & ~1);
+        const bool odd = lane & 1;
+        T* out = static_cast<T*>(p.out) + f;
+        for (int c = 0; c < ti.cols; c += 32) {
+          float v[32];
+          tmem_ld32(taddr + c, v);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const uint32_t w = odd ? pack2<T>(other, v[j + 1]) : pack2<T>(v[j], other);
+            const int64_t row = ti.row + c + j + (odd ? 1 : 0);
+            if (row < ti.end && f < p.features) *reinterpret_cast<uint32_t*>(out + row * p.sout) = w;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_tempty[acc]), 0));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    if (kW && lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <GemmDir DIR, typename T, typename OUT>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tb16, const CUtensorMap& to,
+                   const TcParams& p, int64_t most_tiles, cudaStream_t st) {
+  constexpr size_t smem = kDynSmem + (DIR == kWeight ? 4 * kOutBytes : 0);
+  static int at_once[PerDeviceOnce::kMaxDevices];
+  static PerDeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run([&] {
+    cudaError_t r = cudaFuncSetAttribute(grouped_gemm_tc_kernel<DIR, T, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (r != cudaSuccess) return r;
+    cudaLaunchAttribute cluster = {};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = 2;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)device_sm_count() / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(&at_once[dev], grouped_gemm_tc_kernel<DIR, T, OUT>, &cfg);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t clusters = at_once[dev] < 1 ? 1 : at_once[dev] < most_tiles ? at_once[dev] : most_tiles;
+  if (p.next && (e = cudaMemsetAsync(p.next, 0, sizeof(int32_t), st)) != cudaSuccess) return e;
+  grouped_gemm_tc_kernel<DIR, T, OUT><<<(unsigned)(2 * clusters), kThreads, smem, st>>>(ta, tb, tb16, to, p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
+  const CUtensorMapDataType type =
+      g.dtype == MOE_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  TcParams p = {};
+  p.offsets = g.offsets;
+  p.counts = g.counts;
+  p.status = g.status;
+  p.out = g.out;
+  p.addend = g.addend;
+  p.sout = g.sout;
+  p.cap = g.cap;
+  p.E = (int)g.E;
+  p.N = (int)g.N;
+  p.Kd = (int)g.Kd;
+  CUtensorMap ta, tb, tb16, to;
+  cudaError_t e;
+  if (dir == kWeight) {
+    p.mt = (int)((g.N + BM - 1) / BM);
+    p.kt = (int)((g.Kd + BN - 1) / BN);
+    p.next = static_cast<int32_t*>(g.workspace);
+    if ((e = make_tensor_map_rows(&ta, g.a, type, g.cap, g.N, g.sa, BK, 64)) != cudaSuccess) return e;
+    if ((e = make_tensor_map_rows(&tb, g.b, type, g.cap, g.Kd, g.sb, BK, 64)) != cudaSuccess) return e;
+    const bool f32 = g.out_dtype == MOE_ELEM_F32;
+    if ((e = make_tensor_map_matrices(&to, g.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, f32 ? 4 : 2, g.E, g.N,
+                                      g.Kd, 32, f32 ? 32 : 64)) != cudaSuccess)
+      return e;
+    const int64_t tiles = g.E * p.mt * p.kt;
+    return f32 ? launch<kWeight, T, float>(ta, tb, tb, to, p, tiles, st)
+               : launch<kWeight, T, T>(ta, tb, tb, to, p, tiles, st);
+  }
+  p.features = (int)(dir == kForward ? g.N : g.Kd);
+  p.contraction = (int)(dir == kForward ? g.Kd : g.N);
+  p.mt = (p.features + BM - 1) / BM;
+  const bool fwd = dir == kForward;
+  if ((e = make_tensor_map_matrices(&ta, g.b, type, 2, g.E, g.N, g.Kd, fwd ? 128 : BK, 64)) != cudaSuccess) return e;
+  if ((e = make_tensor_map_rows(&tb, g.a, type, g.cap, p.contraction, g.sa, 128, BK)) != cudaSuccess) return e;
+  if ((e = make_tensor_map_rows(&tb16, g.a, type, g.cap, p.contraction, g.sa, 16, BK)) != cudaSuccess) return e;
+  const int64_t routes = g.T * g.K;
+  const int64_t tiles = (routes / BN + (routes < g.E ? routes : g.E)) * p.mt;
+  // up to 256 routes no expert has a second tile and every tile costs its weights:
+  // in turn, without the counter and its clearing
+  if (routes > BN) p.next = static_cast<int32_t*>(g.workspace);
+  return fwd ? launch<kForward, T, T>(ta, tb, tb16, tb, p, tiles, st)
+             : launch<kData, T, T>(ta, tb, tb16, tb, p, tiles, st);
+}
+
+}  // namespace
+
+bool grouped_gemm_tc_takes(GemmDir dir, const GroupedGemm& g) {
+  const int64_t tiles = dir == kWeight ? g.E * ((g.N + BM - 1) / BM) * ((g.Kd + BN - 1) / BN)
+                                       : (g.cap / BN + g.E) * (((dir == kForward ? g.N : g.Kd) + BM - 1) / BM);
+  return g.E <= kMaxE && g.cap > 0 && tiles < (int64_t(1) << 30) && g.N % 8 == 0 && g.Kd % 8 == 0 && aligned16(g.a) &&
+         aligned16(g.b) && aligned16(g.out) && aligned16(g.addend) &&
+         (g.cap == 1 || (g.sa % 8 == 0 && (dir == kWeight ? g.sb % 8 == 0 : g.sout % 8 == 0)));
+}
+
+cudaError_t launch_grouped_gemm_tc(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
+  return g.dtype == MOE_ELEM_BF16 ? run<__nv_bfloat16>(dir, g, st) : run<__half>(dir, g, st);
+}
+
+}  // namespace moe

@@ -304,6 +304,89 @@ MOE_DEVICE void tma_load_2d_pair(void* dst, const CUtensorMap* map, int32_t c0, 
       : "memory");
 }
 
+// The same for a box of a 3-D tensor (c2: outermost).
+MOE_DEVICE void tma_load_3d_pair(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster)
+      : "memory");
+}
+
+// Store of a box of a 3-D tensor from shared memory; what lies outside the tensor
+// is left out.  Completion is that of the issuing thread's bulk groups.
+MOE_DEVICE void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+MOE_DEVICE void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+MOE_DEVICE void bulk_wait_read() {  // all but the N newest groups have read their source
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+MOE_DEVICE void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Generic writes to shared memory before, reads by copies and MMAs after.
+MOE_DEVICE void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// mbar_try_wait for arrivals from the other CTA of the cluster.
+MOE_DEVICE bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait for arrivals from the other CTA of the cluster.
+MOE_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; it++) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((it & 63) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        set_status(status, MOE_DEV_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+MOE_DEVICE void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+// Shared-memory matrix descriptor for an operand whose rows run along the
+// contraction: boxes of 64 (M or N) x 128 bytes a row with the 128-byte swizzle,
+// eight rows of the contraction 1024 bytes apart (stride offset), the next 64 of M
+// or N `box_bytes` further (leading offset).
+MOE_DEVICE uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t box_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(box_bytes >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+// Instruction descriptor of a dense kind::f16 MMA with fp32 sums: bf16 or f16
+// operands, each K-major or (a_mn, b_mn) with M or N contiguous.
+__host__ __device__ constexpr uint32_t idesc_16bit(uint32_t M, uint32_t N, bool bf16, bool a_mn, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
 // D[tmem of both CTAs] (+)= A[smem of both CTAs, M = 256] * B[smem of both CTAs, N]^T.
 MOE_DEVICE void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                               uint32_t accumulate) {

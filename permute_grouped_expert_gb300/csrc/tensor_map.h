@@ -39,4 +39,33 @@ inline cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, CUtens
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Row matrix [rows][cols] of 16-bit elements whose rows lie `stride` elements apart.
+inline cudaError_t make_tensor_map_rows(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint64_t rows,
+                                        uint64_t cols, uint64_t stride, uint32_t box_rows, uint32_t box_cols) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {(rows > 1 ? stride : (cols + 7) / 8 * 8) * 2};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Matrices [count][rows][cols], contiguous; boxes within one matrix.
+inline cudaError_t make_tensor_map_matrices(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
+                                            int elem_bytes, uint64_t count, uint64_t rows, uint64_t cols,
+                                            uint32_t box_rows, uint32_t box_cols) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[3] = {cols, rows, count};
+  cuuint64_t strides[2] = {cols * elem_bytes, rows * cols * elem_bytes};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, dtype, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace moe

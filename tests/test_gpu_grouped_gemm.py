@@ -73,6 +73,20 @@ def test_whole_numbers(T, E, K, m, N, Kd, dtype):
     assert torch.equal(weight(moe, r, gy, x, F32).cpu(), gw.float())
 
 
+@pytest.mark.parametrize("T,E,K,m,N,Kd,skew", [(3000, 16, 4, 32, 1024, 512, 0.0), (2500, 3, 1, 8, 2312, 328, 0.0),
+                                               (5000, 40, 2, 1, 520, 264, 1.2)])
+def test_more_tiles_than_run_at_once(T, E, K, m, N, Kd, skew):
+    moe = moe_mod()
+    r = tu.Routed(moe, T, E, K, m, skew=skew)
+    w = matrices(E, N, Kd, BF, 1, ints=2)
+    x, gy = r.rows(Kd, BF, 2, ints=2), r.rows(N, BF, 3, ints=2)
+    assert_rows(r, forward(moe, r, w, x), tu.gemm_forward(r, w, x))
+    assert_rows(r, data(moe, r, w, gy), tu.gemm_data(r, w, gy))
+    gw = tu.gemm_weight(r, gy, x)
+    assert torch.equal(weight(moe, r, gy, x, BF).cpu(), gw.to(BF))
+    assert torch.equal(weight(moe, r, gy, x, F32).cpu(), gw.float())
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("T,E,K,m,N,Kd", [(1, 8, 2, 32, 264, 2048), (50, 6, 2, 8, 384, 512), (333, 4, 2, 1, 129, 257),
                                           (900, 2, 1, 32, 256, 640)])
