@@ -16,7 +16,7 @@
 //
 // Per CTA, warp-specialised (rank 0 leads the pair):
 //   warp 0      TMA producer of its half of both operands, 64 of the contraction a stage
-//   warp 1      TMEM; on the leader one thread issues the MMAs
+//   warp 1      TMEM; on the leader one elected lane issues the MMAs
 //   warp 2      on the leader: claims tiles and hands their numbers to both CTAs
 //   warp 3      kWeight: zeros behind an expert's last row
 //   warps 4..7  epilogue of this CTA's 128 features, beside the next tile's MMAs
@@ -64,6 +64,14 @@ struct Tile {
   int e, m, n;         // expert; tile of features; kWeight: tile of Kd
   int64_t row, end;    // rows [row, end) of the tile, or of the expert (kWeight)
   int cols;            // columns of the MMA
+};
+
+// Maps of the second operand: boxes of 16, 32, .. 128 rows, so that a tile's half of
+// a stage is one copy whatever its rows (as copies of 16 rows, 8192 x 8192 x 8192
+// over experts of about 1024 rows took 1031 us where whole tiles took 717); kWeight:
+// the first alone.
+struct RowMaps {
+  CUtensorMap of[8];
 };
 
 // Tiles of an expert in bands of kBand along one side, the other side outermost in
@@ -132,9 +140,8 @@ MOE_DEVICE void settle(uint64_t ns) {
 // T: 16-bit type of the operands; OUT: of the result.
 template <GemmDir DIR, typename T, typename OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                           const __grid_constant__ CUtensorMap tm_b16, const __grid_constant__ CUtensorMap tm_out,
-                           TcParams p) {
+    grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
+                           const __grid_constant__ CUtensorMap tm_out, TcParams p) {
   constexpr bool kW = DIR == kWeight, kAmn = DIR != kForward, kBmn = kW;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tail[kStages], s_tfull[2], s_tempty[2];
@@ -170,7 +177,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&s_drain, 1);
     fence_barrier_init();
     tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_b.of[0]);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, kTmemCols);
   if (!kW && warp == 0) {
@@ -217,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
-    if (lane == 0) {
+    if (elect_one_lane()) {
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued_parity[kStages];
@@ -257,8 +264,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int r0 = (int)ti.row + k0;
             tma_load_2d_pair(sa, &tm_a, f0, r0, bar);
             tma_load_2d_pair(sa + kBox, &tm_a, f0 + 64, r0, bar);
-            tma_load_2d_pair(sb, &tm_b, c0, r0, bar);
-            tma_load_2d_pair(sb + kBox, &tm_b, c0 + 64, r0, bar);
+            tma_load_2d_pair(sb, &tm_b.of[0], c0, r0, bar);
+            tma_load_2d_pair(sb + kBox, &tm_b.of[0], c0 + 64, r0, bar);
           } else {
             if (DIR == kForward) {
               tma_load_3d_pair(sa, &tm_a, k0, f0, ti.e, bar);
@@ -266,12 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tma_load_3d_pair(sa, &tm_a, f0, k0, ti.e, bar);
               tma_load_3d_pair(sa + kBox, &tm_a, f0 + 64, k0, ti.e, bar);
             }
-            const int r0 = (int)ti.row + (int)rank * half;
-            if (half == 128) {
-              tma_load_2d_pair(sb, &tm_b, k0, r0, bar);
-            } else {
-              for (int j = 0; j < half; j += 16) tma_load_2d_pair(sb + j * BK * 2, &tm_b16, k0, r0 + j, bar);
-            }
+            tma_load_2d_pair(sb, &tm_b.of[half / 16 - 1], k0, (int)ti.row + (int)rank * half, bar);
           }
           issued[stage] = !tail;
           issued_parity[stage] = phase;
@@ -295,7 +297,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer (leader)
-    if (lane == 0 && rank == 0) {
+    // One elected lane waits and issues, the others stay at the end: known to be one,
+    // it needs no care for others that might issue another MMA.
+    if (rank == 0 && elect_one_lane()) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -506,8 +510,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <GemmDir DIR, typename T, typename OUT>
-cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tb16, const CUtensorMap& to,
-                   const TcParams& p, int64_t most_tiles, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, const TcParams& p,
+                   int64_t most_tiles, cudaStream_t st) {
   constexpr size_t smem = kDynSmem + (DIR == kWeight ? 4 * kOutBytes : 0);
   static int at_once[PerDeviceOnce::kMaxDevices];
   static PerDeviceOnce once;
@@ -533,7 +537,7 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorM
   if (e != cudaSuccess) return e;
   const int64_t clusters = at_once[dev] < 1 ? 1 : at_once[dev] < most_tiles ? at_once[dev] : most_tiles;
   if (p.next && (e = cudaMemsetAsync(p.next, 0, sizeof(int32_t), st)) != cudaSuccess) return e;
-  grouped_gemm_tc_kernel<DIR, T, OUT><<<(unsigned)(2 * clusters), kThreads, smem, st>>>(ta, tb, tb16, to, p);
+  grouped_gemm_tc_kernel<DIR, T, OUT><<<(unsigned)(2 * clusters), kThreads, smem, st>>>(ta, tb, to, p);
   return cudaGetLastError();
 }
 
@@ -552,36 +556,37 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
   p.E = (int)g.E;
   p.N = (int)g.N;
   p.Kd = (int)g.Kd;
-  CUtensorMap ta, tb, tb16, to;
+  CUtensorMap ta, to = {};
+  RowMaps tb = {};
   cudaError_t e;
   if (dir == kWeight) {
     p.mt = (int)((g.N + BM - 1) / BM);
     p.kt = (int)((g.Kd + BN - 1) / BN);
     p.next = static_cast<int32_t*>(g.workspace);
     if ((e = make_tensor_map_rows(&ta, g.a, type, g.cap, g.N, g.sa, BK, 64)) != cudaSuccess) return e;
-    if ((e = make_tensor_map_rows(&tb, g.b, type, g.cap, g.Kd, g.sb, BK, 64)) != cudaSuccess) return e;
+    if ((e = make_tensor_map_rows(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK, 64)) != cudaSuccess) return e;
     const bool f32 = g.out_dtype == MOE_ELEM_F32;
     if ((e = make_tensor_map_matrices(&to, g.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, f32 ? 4 : 2, g.E, g.N,
                                       g.Kd, 32, f32 ? 32 : 64)) != cudaSuccess)
       return e;
     const int64_t tiles = g.E * p.mt * p.kt;
-    return f32 ? launch<kWeight, T, float>(ta, tb, tb, to, p, tiles, st)
-               : launch<kWeight, T, T>(ta, tb, tb, to, p, tiles, st);
+    return f32 ? launch<kWeight, T, float>(ta, tb, to, p, tiles, st)
+               : launch<kWeight, T, T>(ta, tb, to, p, tiles, st);
   }
   p.features = (int)(dir == kForward ? g.N : g.Kd);
   p.contraction = (int)(dir == kForward ? g.Kd : g.N);
   p.mt = (p.features + BM - 1) / BM;
   const bool fwd = dir == kForward;
   if ((e = make_tensor_map_matrices(&ta, g.b, type, 2, g.E, g.N, g.Kd, fwd ? 128 : BK, 64)) != cudaSuccess) return e;
-  if ((e = make_tensor_map_rows(&tb, g.a, type, g.cap, p.contraction, g.sa, 128, BK)) != cudaSuccess) return e;
-  if ((e = make_tensor_map_rows(&tb16, g.a, type, g.cap, p.contraction, g.sa, 16, BK)) != cudaSuccess) return e;
   const int64_t routes = g.T * g.K;
+  for (int i = 0; i < 8 && (i == 0 || i * 32 < routes); i++)  // a tile has no more rows than there are routes
+    if ((e = make_tensor_map_rows(&tb.of[i], g.a, type, g.cap, p.contraction, g.sa, 16 * (i + 1), BK)) != cudaSuccess)
+      return e;
   const int64_t tiles = (routes / BN + (routes < g.E ? routes : g.E)) * p.mt;
   // up to 256 routes no expert has a second tile and every tile costs its weights:
   // in turn, without the counter and its clearing
   if (routes > BN) p.next = static_cast<int32_t*>(g.workspace);
-  return fwd ? launch<kForward, T, T>(ta, tb, tb16, tb, p, tiles, st)
-             : launch<kData, T, T>(ta, tb, tb16, tb, p, tiles, st);
+  return fwd ? launch<kForward, T, T>(ta, tb, to, p, tiles, st) : launch<kData, T, T>(ta, tb, to, p, tiles, st);
 }
 
 }  // namespace
