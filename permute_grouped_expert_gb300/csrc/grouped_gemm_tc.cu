@@ -35,7 +35,7 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
-constexpr int kStages = 6, kSlots = 3;
+constexpr int kStages = 6, kSlots = 2;
 constexpr int kBand = 8;                                // tiles of a band that share their operands in L2
 constexpr uint32_t kOperand = 128 * BK * 2;             // a CTA's half of an operand: 16 KB
 constexpr uint32_t kBox = 64 * BK * 2;                  // a box of an operand that is not K-major
@@ -60,10 +60,13 @@ struct TcParams {
   int kt;                     // kWeight: tiles of 256 of Kd
 };
 
-struct Tile {
-  int e, m, n;         // expert; tile of features; kWeight: tile of Kd
-  int64_t row, end;    // rows [row, end) of the tile, or of the expert (kWeight)
-  int cols;            // columns of the MMA
+// A tile as the pair's readers get it.
+struct alignas(16) Tile {
+  int e, m, n;   // expert, -1 behind the last tile; tile of features; kWeight: tile of Kd
+  int row, end;  // rows [row, end) of the tile, or of the expert (kWeight)
+  int cols;      // columns of the MMA
+  int blocks;    // stages along the contraction
+  int pad;
 };
 
 // Maps of the second operand: boxes of 16, 32, .. 128 rows, so that a tile's half of
@@ -87,32 +90,93 @@ MOE_DEVICE void banded(int local, int along, int across, int& a, int& c) {
 MOE_DEVICE int row_tiles(int64_t rows) { return (int)((rows + BN - 1) / BN); }
 MOE_DEVICE int tile_rows(int64_t rows, int tiles) { return (int)((rows + tiles - 1) / tiles + 31) & ~31; }
 
-template <GemmDir DIR>
-MOE_DEVICE Tile tile_of(int t, const int* prefix, const TcParams& p) {
-  Tile i;
-  int64_t beg, end;
-  if (DIR == kWeight) {
-    const int per = p.mt * p.kt;
-    i.e = t / per;
-    banded(t - i.e * per, p.mt, p.kt, i.m, i.n);
-    gemm_segment(p.offsets, p.counts, p.cap, i.e, beg, end);
-    i.row = beg;
-    i.end = end;
-    i.cols = BN;
-  } else {
-    i.e = expert_of_row(prefix, p.E, t);
-    gemm_segment(p.offsets, p.counts, p.cap, i.e, beg, end);
-    const int tiles = row_tiles(end - beg);
-    banded(t - prefix[i.e], tiles, p.mt, i.n, i.m);
-    i.cols = tile_rows(end - beg, tiles);
-    i.row = beg + (int64_t)i.n * i.cols;
-    i.end = min64(i.row + i.cols, end);
+// The order of the tiles.  Experts of up to BN rows cost their matrix's bytes, the
+// others products; one after another they would use HBM and the tensor cores in
+// turn, so the tiles of both kinds are dealt out evenly among each other.
+struct Order {
+  int tiles[2];            // of either kind: 0 products, 1 bytes
+  int experts[2];
+  int before[2][kMaxE];    // tiles of the kind's experts before
+  uint16_t expert[2][kMaxE];
+};
+
+// Filled by one warp.  per: tiles of an expert that has rows (kForward, kData: for
+// each of its tiles of rows); kWeight has tiles without rows too.
+template <bool WEIGHT>
+MOE_DEVICE void make_order(Order& o, const TcParams& p, int per) {
+  constexpr int kAhead = 8;
+  const int lane = threadIdx.x & 31;
+  int tiles[2] = {0, 0}, experts[2] = {0, 0};
+  for (int e0 = 0; e0 < p.E; e0 += 32 * kAhead) {
+    int64_t rows[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) {
+      const int e = e0 + j * 32 + lane;
+      int64_t beg = 0, end = 0;
+      if (e < p.E) gemm_segment(p.offsets, p.counts, p.cap, e, beg, end);
+      rows[j] = end - beg;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) {
+      const int e = e0 + j * 32 + lane;
+      const int mine = e < p.E ? (WEIGHT ? per : row_tiles(rows[j]) * per) : 0;
+      const int kind = rows[j] <= BN;
+      const unsigned some = __ballot_sync(0xffffffffu, mine > 0), second = __ballot_sync(0xffffffffu, mine > 0 && kind);
+      int incl[2] = {kind ? 0 : mine, kind ? mine : 0};
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, incl[0], d), b = __shfl_up_sync(0xffffffffu, incl[1], d);
+        if (lane >= d) incl[0] += a, incl[1] += b;
+      }
+      if (mine > 0) {
+        const unsigned same = kind ? second : some & ~second;
+        const int at = (kind ? experts[1] : experts[0]) + __popc(same & lanemask_lt());
+        o.expert[kind][at] = (uint16_t)e;
+        o.before[kind][at] = (kind ? tiles[1] + incl[1] : tiles[0] + incl[0]) - mine;
+      }
+      tiles[0] += __shfl_sync(0xffffffffu, incl[0], 31);
+      tiles[1] += __shfl_sync(0xffffffffu, incl[1], 31);
+      experts[0] += __popc(some & ~second);
+      experts[1] += __popc(second);
+    }
   }
-  return i;
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < 2; k++) o.tiles[k] = tiles[k], o.experts[k] = experts[k];
+  }
+  __syncwarp();
 }
 
-MOE_DEVICE int blocks_of(const Tile& i, GemmDir dir, const TcParams& p) {
-  return dir == kWeight ? (int)((i.end - i.row + BK - 1) / BK) : (p.contraction + BK - 1) / BK;
+template <GemmDir DIR>
+MOE_DEVICE Tile tile_of(int64_t t, const Order& o, const TcParams& p) {
+  Tile i = {};
+  const int64_t total = (int64_t)o.tiles[0] + o.tiles[1];
+  if (t >= total) {
+    i.e = -1;
+    return i;
+  }
+  const int64_t s = t * o.tiles[1] / total;  // bytes' tiles before t
+  const int kind = (t + 1) * o.tiles[1] / total > s ? 1 : 0;
+  const int at = (int)(kind ? s : t - s);
+  const int x = expert_of_row(o.before[kind], o.experts[kind], at), local = at - o.before[kind][x];
+  int64_t beg, end;
+  i.e = o.expert[kind][x];
+  gemm_segment(p.offsets, p.counts, p.cap, i.e, beg, end);
+  if (DIR == kWeight) {
+    banded(local, p.mt, p.kt, i.m, i.n);
+    i.row = (int)beg;
+    i.end = (int)end;
+    i.cols = BN;
+    i.blocks = (int)((end - beg + BK - 1) / BK);
+  } else {
+    const int tiles = row_tiles(end - beg);
+    banded(local, tiles, p.mt, i.n, i.m);
+    i.cols = tile_rows(end - beg, tiles);
+    i.row = (int)(beg + (int64_t)i.n * i.cols);
+    i.end = (int)min64((int64_t)i.row + i.cols, end);
+    i.blocks = (p.contraction + BK - 1) / BK;
+  }
+  return i;
 }
 
 // Whether the last stage of a kWeight tile holds rows that are not the expert's
@@ -146,10 +210,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tail[kStages], s_tfull[2], s_tempty[2];
   __shared__ __align__(8) uint64_t s_have[kSlots], s_free[kSlots], s_drain;
-  __shared__ int s_tile[kSlots];
+  __shared__ Tile s_tile[kSlots];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int s_prefix[kW ? 1 : kMaxE + 1];
+  __shared__ Order s_order;  // the leader's
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -180,46 +244,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_b.of[0]);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, kTmemCols);
-  if (!kW && warp == 0) {
-    int base = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      int m = 0;
-      if (e < p.E) {
-        int64_t b, n;
-        gemm_segment(p.offsets, p.counts, p.cap, e, b, n);
-        m = row_tiles(n - b) * p.mt;
-      }
-      int incl = m;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
-      if (e < p.E) s_prefix[e] = base + incl - m;
-      base += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) s_prefix[p.E] = base;
-  }
   tc_fence_before();
   __syncwarp();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = s_tmem;
-  const int total = kW ? p.E * p.mt * p.kt : s_prefix[p.E];
 
-  // The number of the i-th tile of this pair, -1 behind the last; called by one
-  // thread of each reader, in order.
-  auto next_tile = [&](int i) -> int {
-    if (!p.next) {
-      const int64_t t = cluster + (int64_t)i * clusters;
-      return t < total ? (int)t : -1;
-    }
+  // The i-th tile of this pair; waits for it, reads it and, once, says so.
+  auto next_tile = [&](int i, Tile& ti) {
     const int s = i % kSlots;
-    if (!mbar_wait_cluster(&s_have[s], (i / kSlots) & 1, abort_flag, p.status)) return -1;
-    const int t = *(volatile int*)&s_tile[s];
-    mbar_arrive_cluster(mapa_shared(smem_u32(&s_free[s]), 0));
-    return t;
+    if (!mbar_wait_cluster(&s_have[s], (i / kSlots) & 1, abort_flag, p.status)) return false;
+    const int4 a = ld_shared_v4(&s_tile[s]), b = ld_shared_v4(reinterpret_cast<const int4*>(&s_tile[s]) + 1);
+    ti.e = a.x, ti.m = a.y, ti.n = a.z, ti.row = a.w;
+    ti.end = b.x, ti.cols = b.y, ti.blocks = b.z;
+    return true;
+  };
+  auto have_read = [&](int i) { mbar_arrive_cluster(mapa_shared(smem_u32(&s_free[i % kSlots]), 0)); };
+  // one thread's, and a whole warp's
+  auto take_tile = [&](int i, Tile& ti) {
+    if (!next_tile(i, ti)) return false;
+    have_read(i);
+    return ti.e >= 0;
+  };
+  auto take_tile_warp = [&](int i, Tile& ti) {
+    if (!__all_sync(0xffffffffu, next_tile(i, ti))) return false;
+    if (lane == 0) have_read(i);
+    return ti.e >= 0;
   };
 
   if (warp == 0) {
@@ -232,10 +282,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int s = 0; s < kStages; s++) issued[s] = false;
       bool ok = true;
       for (int i = 0; ok; i++) {
-        const int t = next_tile(i);
-        if (t < 0) break;
-        const Tile ti = tile_of<DIR>(t, s_prefix, p);
-        const int nkb = blocks_of(ti, DIR, p);
+        Tile ti;
+        if (!take_tile(i, ti)) break;
+        const int nkb = ti.blocks;
         const int f0 = ti.m * BM + (int)rank * 128;             // first feature of this CTA
         const int half = ti.cols / 2;                           // columns of this CTA
         const int c0 = kW ? ti.n * BN + (int)rank * 128 : 0;    // kWeight: its first column
@@ -261,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const int k0 = kb * BK;
           if (kW) {
-            const int r0 = (int)ti.row + k0;
+            const int r0 = ti.row + k0;
             tma_load_2d_pair(sa, &tm_a, f0, r0, bar);
             tma_load_2d_pair(sa + kBox, &tm_a, f0 + 64, r0, bar);
             tma_load_2d_pair(sb, &tm_b.of[0], c0, r0, bar);
@@ -273,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tma_load_3d_pair(sa, &tm_a, f0, k0, ti.e, bar);
               tma_load_3d_pair(sa + kBox, &tm_a, f0 + 64, k0, ti.e, bar);
             }
-            tma_load_2d_pair(sb, &tm_b.of[half / 16 - 1], k0, (int)ti.row + (int)rank * half, bar);
+            tma_load_2d_pair(sb, &tm_b.of[half / 16 - 1], k0, ti.row + (int)rank * half, bar);
           }
           issued[stage] = !tail;
           issued_parity[stage] = phase;
@@ -304,10 +353,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int i = 0; ok; i++) {
-        const int t = next_tile(i);
-        if (t < 0) break;
-        const Tile ti = tile_of<DIR>(t, s_prefix, p);
-        const int nkb = blocks_of(ti, DIR, p);
+        Tile ti;
+        if (!take_tile(i, ti)) break;
+        const int nkb = ti.blocks;
         const uint32_t idesc = idesc_16bit(BM, (uint32_t)ti.cols, std::is_same<T, __nv_bfloat16>::value, kAmn, kBmn);
         if (!mbar_wait_cluster(&s_tempty[acc], acc_phase ^ 1, abort_flag, p.status)) {
           ok = false;
@@ -326,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint64_t bdesc = kBmn ? smem_desc_sw128_mn(sb, kBox) : smem_desc_sw128(sb);
           // a step of 16: 32 bytes of K-major rows, or 16 rows of 128 bytes
           constexpr uint64_t kAstep = kAmn ? 128 : 2, kBstep = kBmn ? 128 : 2;
-          const int left = kW ? (int)(ti.end - ti.row) - kb * BK : p.contraction - kb * BK;
+          const int left = kW ? (ti.end - ti.row) - kb * BK : p.contraction - kb * BK;
 #pragma unroll
           for (int k = 0; k < BK / 16; k++)
             if (k * 16 < left)
@@ -353,17 +401,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------- tiles (leader)
-    if (lane == 0 && rank == 0 && p.next) {
-      for (int i = 0;; i++) {
-        const int s = i % kSlots;
-        int t = atomicAdd(p.next, 1);
-        if (t >= total) t = -1;
-        if (!mbar_wait_cluster(&s_free[s], ((i / kSlots) & 1) ^ 1, abort_flag, p.status)) break;
-        for (uint32_t r = 0; r < 2; r++) {
-          st_cluster_u32(mapa_shared(smem_u32(&s_tile[s]), r), (uint32_t)t);
-          mbar_arrive_cluster(mapa_shared(smem_u32(&s_have[s]), r));
+    if (rank == 0) {
+      make_order<kW>(s_order, p, kW ? p.mt * p.kt : p.mt);
+      if (lane == 0) {
+        const int64_t total = (int64_t)s_order.tiles[0] + s_order.tiles[1];
+        int64_t t = p.next ? atomicAdd(p.next, 1) : cluster;
+        for (int i = 0;; i++) {
+          const int s = i % kSlots;
+          const Tile ti = tile_of<DIR>(t, s_order, p);
+          if (!mbar_wait_cluster(&s_free[s], ((i / kSlots) & 1) ^ 1, abort_flag, p.status)) break;
+          for (uint32_t r = 0; r < 2; r++) {
+            const uint32_t to = mapa_shared(smem_u32(&s_tile[s]), r);
+            st_cluster_v4(to, ti.e, ti.m, ti.n, ti.row);
+            st_cluster_v4(to + 16, ti.end, ti.cols, ti.blocks, 0);
+            mbar_arrive_cluster(mapa_shared(smem_u32(&s_have[s]), r));
+          }
+          if (t >= total) break;
+          t = p.next ? atomicAdd(p.next, 1) : t + clusters;
         }
-        if (t < 0) break;
       }
     }
   } else if (warp == 3) {
@@ -372,19 +427,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phases = 0;  // bit s: parity of s_tail[s]
       for (int i = 0;; i++) {
-        int t = 0;
-        if (lane == 0) t = next_tile(i);
-        t = __shfl_sync(0xffffffffu, t, 0);
-        if (t < 0) break;
-        const Tile ti = tile_of<DIR>(t, s_prefix, p);
-        const int nkb = blocks_of(ti, DIR, p);
+        Tile ti;
+        if (!take_tile_warp(i, ti)) break;
+        const int nkb = ti.blocks;
         if (nkb && ragged(ti)) {
           const int s = (stage + nkb - 1) % kStages;
           int ok = 0;
           if (lane == 0) ok = mbar_wait(&s_tail[s], (phases >> s) & 1, abort_flag, p.status) ? 1 : 0;
           if (!__shfl_sync(0xffffffffu, ok, 0)) break;
           phases ^= 1u << s;
-          const int rows = (int)(ti.end - ti.row) - (nkb - 1) * BK, stop = (rows + 15) & ~15;
+          const int rows = (ti.end - ti.row) - (nkb - 1) * BK, stop = (rows + 15) & ~15;
           uint8_t* base = smem + (size_t)s * kStageBytes;
           for (int j = lane; j < (stop - rows) * 8 * 4; j += 32) {  // 16 bytes each of the four boxes' rows
             const int box = j & 3, at = j >> 2;
@@ -404,11 +456,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int i = 0;; i++) {
-      int t = 0;
-      if (lane == 0) t = next_tile(i);
-      t = __shfl_sync(0xffffffffu, t, 0);
-      if (t < 0) break;
-      const Tile ti = tile_of<DIR>(t, s_prefix, p);
+      Tile ti;
+      if (!take_tile_warp(i, ti)) break;
       int ok = 0;
       if (lane == 0) ok = mbar_wait(&s_tfull[acc], acc_phase, abort_flag, p.status) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -482,8 +531,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; j += 2) {
             const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
             const uint32_t w = odd ? pack2<T>(other, v[j + 1]) : pack2<T>(v[j], other);
-            const int64_t row = ti.row + c + j + (odd ? 1 : 0);
-            if (row < ti.end && f < p.features) *reinterpret_cast<uint32_t*>(out + row * p.sout) = w;
+            const int row = ti.row + c + j + (odd ? 1 : 0);
+            if (row < ti.end && f < p.features) *reinterpret_cast<uint32_t*>(out + (int64_t)row * p.sout) = w;
           }
         }
       }

@@ -362,8 +362,19 @@ MOE_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* 
   }
 }
 
-MOE_DEVICE void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+MOE_DEVICE void st_cluster_v4(uint32_t cluster_addr, int a, int b, int c, int d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// A read that is made where it stands, of what another CTA may have written.
+MOE_DEVICE int4 ld_shared_v4(const void* p) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(p))
+               : "memory");
+  return v;
 }
 
 // Shared-memory matrix descriptor for an operand whose rows run along the
