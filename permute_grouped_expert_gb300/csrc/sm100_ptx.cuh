@@ -314,20 +314,12 @@ MOE_DEVICE void tma_load_3d_pair(void* dst, const CUtensorMap* map, int32_t c0, 
       : "memory");
 }
 
-// Store of a box of a 3-D tensor from shared memory; what lies outside the tensor
-// is left out.  Completion is that of the issuing thread's bulk groups.
-MOE_DEVICE void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0, int32_t c1, int32_t c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+// 32 bytes, 32-byte aligned: a whole sector from one thread.
+MOE_DEVICE void st_global_v8(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-MOE_DEVICE void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-MOE_DEVICE void bulk_wait_read() {  // all but the N newest groups have read their source
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-MOE_DEVICE void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Generic writes to shared memory before, reads by copies and MMAs after.
 MOE_DEVICE void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -362,8 +354,23 @@ MOE_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* 
   }
 }
 
-MOE_DEVICE void st_cluster_v4(uint32_t cluster_addr, int a, int b, int c, int d) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d)
+// Arrive on an mbarrier of the cluster without ordering this thread's memory
+// accesses: an arrival that releases at cluster scope waits until all stores before
+// it, global ones too, have arrived.
+MOE_DEVICE void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 32 bytes written to shared memory of the cluster, and the mbarrier that counts
+// them there (one arrival, 32 bytes).
+MOE_DEVICE void send_32(uint32_t to, uint32_t bar, int4 a, int4 b) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 32;" ::"r"(bar) : "memory");
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(bar)
+               : "memory");
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   to + 16),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w), "r"(bar)
                : "memory");
 }
 
