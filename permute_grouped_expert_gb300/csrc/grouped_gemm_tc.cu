@@ -35,14 +35,18 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
-constexpr int kStages = 6, kSlots = 2;
+constexpr int kSlots = 2;
+template <GemmDir DIR>
+constexpr int kStagesOf = DIR == kWeight ? 5 : 6;
 constexpr int kBand = 8;                                // tiles of a band that share their operands in L2
 constexpr uint32_t kOperand = 128 * BK * 2;             // a CTA's half of an operand: 16 KB
 constexpr uint32_t kBox = 64 * BK * 2;                  // a box of an operand that is not K-major
 constexpr uint32_t kStageBytes = 2 * kOperand;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxE = 1024;
-constexpr size_t kDynSmem = 1024 + (size_t)kStages * kStageBytes;
+constexpr uint32_t kOutBytes = 32 * 128;                // kWeight: a warp's 32 rows of 128 bytes, twice
+template <GemmDir DIR>
+constexpr size_t kDynSmem = 1024 + (size_t)kStagesOf<DIR> * kStageBytes + (DIR == kWeight ? 8 * kOutBytes : 0);
 
 struct TcParams {
   const int32_t *offsets, *counts;
@@ -57,7 +61,6 @@ struct TcParams {
   int N, Kd;                  // kWeight
   int mt;                     // tiles of 256 features (kWeight: of N)
   int kt;                     // kWeight: tiles of 256 of Kd
-  bool sectors;               // kWeight: rows of the result in whole 32-byte sectors
 };
 
 // A tile as the pair's readers get it.
@@ -205,7 +208,8 @@ MOE_DEVICE void settle(uint64_t ns) {
 template <GemmDir DIR, typename T, typename OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
-                           TcParams p) {
+                           const __grid_constant__ CUtensorMap tm_out, TcParams p) {
+  constexpr int kStages = kStagesOf<DIR>;
   constexpr bool kW = DIR == kWeight, kAmn = DIR != kForward, kBmn = kW;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tail[kStages], s_tfull[2], s_tempty[2];
@@ -452,6 +456,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ---------------------------------------------------------- epilogue
     const int lane_base = 32 * (warp & 3);
+    uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (size_t)(warp & 3) * 2 * kOutBytes;  // kWeight
+    int out_at = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int i = 0;; i++) {
@@ -465,48 +471,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
       const int f_warp = ti.m * BM + (int)rank * 128 + lane_base;  // first feature of this warp
       if constexpr (kW) {
-        // this lane's row of the matrix, whole sectors of it at a time
+        // 128 bytes of this lane's row of the matrix at a time, through shared memory
+        constexpr int kCols = 128 / (int)sizeof(OUT);
         const bool none = ti.end == ti.row;
         const int n = f_warp + lane;
-        const int64_t first = ((int64_t)ti.e * p.N + n) * p.Kd + ti.n * BN;
-        OUT* to = static_cast<OUT*>(p.out) + first;
-        const float* add = p.addend ? p.addend + first : nullptr;
-        const int cols = p.Kd - ti.n * BN;  // of the matrix, from the tile's first on
-        for (int c = 0; c < min(cols, BN) && f_warp < p.N; c += 32) {
-          float v[32];
-          if (none) {
+        const float* add = p.addend ? p.addend + ((int64_t)ti.e * p.N + n) * p.Kd + ti.n * BN : nullptr;
+        const int cols = min(p.Kd - ti.n * BN, BN);
+        for (int c = 0; c < cols && f_warp < p.N; c += kCols) {
+          uint4 piece[8];
 #pragma unroll
-            for (int j = 0; j < 32; j++) v[j] = 0.0f;
-          } else {
-            tmem_ld32(taddr + c, v);
-          }
-          if (n >= p.N) continue;
-          constexpr int kPiece = 32 / (int)sizeof(OUT);
+          for (int h = 0; h < kCols / 32; h++) {
+            float v[32];
+            if (none) {
 #pragma unroll
-          for (int j = 0; j < 32; j += kPiece) {
-            if (sizeof(OUT) == 4 && add && c + j < cols) {
-#pragma unroll
-              for (int q = 0; q < kPiece; q += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(add + c + j + q);
-                v[j + q] += x.x, v[j + q + 1] += x.y, v[j + q + 2] += x.z, v[j + q + 3] += x.w;
-              }
-            }
-            uint32_t w[8];
-#pragma unroll
-            for (int q = 0; q < 8; q++) {
-              if constexpr (sizeof(OUT) == 4)
-                w[q] = __float_as_uint(v[j + q]);
-              else
-                w[q] = pack2<T>(v[j + 2 * q], v[j + 2 * q + 1]);
-            }
-            if (p.sectors && c + j + kPiece <= cols) {
-              st_global_v8(to + c + j, w);
+              for (int j = 0; j < 32; j++) v[j] = 0.0f;
             } else {
-              if (c + j < cols) *reinterpret_cast<uint4*>(to + c + j) = make_uint4(w[0], w[1], w[2], w[3]);
-              if (c + j + kPiece / 2 < cols)
-                *reinterpret_cast<uint4*>(to + c + j + kPiece / 2) = make_uint4(w[4], w[5], w[6], w[7]);
+              tmem_ld32(taddr + c + h * 32, v);
+            }
+            if constexpr (sizeof(OUT) == 4) {
+              if (add && n < p.N) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                  if (c + j < cols) {
+                    const float4 x = *reinterpret_cast<const float4*>(add + c + j);
+                    v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
+                  }
+              }
+#pragma unroll
+              for (int q = 0; q < 8; q++)
+                piece[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                      __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; q++)
+                piece[h * 4 + q] = make_uint4(pack2<T>(v[8 * q], v[8 * q + 1]), pack2<T>(v[8 * q + 2], v[8 * q + 3]),
+                                              pack2<T>(v[8 * q + 4], v[8 * q + 5]), pack2<T>(v[8 * q + 6], v[8 * q + 7]));
             }
           }
+          uint8_t* buf = s_out + out_at * kOutBytes;
+          if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this buffer
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; q++) *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) * 16)) = piece[q];
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm_out, buf, ti.n * BN + c, f_warp, ti.e);
+            bulk_commit();
+          }
+          out_at ^= 1;
         }
       } else {
         // columns are rows of the result, lanes features: neighbouring lanes exchange
@@ -537,6 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (kW && warp >= 4 && lane == 0) bulk_wait_all();
   tc_fence_before();
   __syncwarp();
   cluster_sync_all();
@@ -549,8 +563,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <GemmDir DIR, typename T, typename OUT>
-cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const TcParams& p, int64_t most_tiles, cudaStream_t st) {
-  constexpr size_t smem = kDynSmem;
+cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, const TcParams& p,
+                   int64_t most_tiles, cudaStream_t st) {
+  constexpr size_t smem = kDynSmem<DIR>;
   static int at_once[PerDeviceOnce::kMaxDevices];
   static PerDeviceOnce once;
   int dev = 0;
@@ -575,7 +590,7 @@ cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const TcParams& p, 
   if (e != cudaSuccess) return e;
   const int64_t clusters = at_once[dev] < 1 ? 1 : at_once[dev] < most_tiles ? at_once[dev] : most_tiles;
   if (p.next && (e = cudaMemsetAsync(p.next, 0, sizeof(int32_t), st)) != cudaSuccess) return e;
-  grouped_gemm_tc_kernel<DIR, T, OUT><<<(unsigned)(2 * clusters), kThreads, smem, st>>>(ta, tb, p);
+  grouped_gemm_tc_kernel<DIR, T, OUT><<<(unsigned)(2 * clusters), kThreads, smem, st>>>(ta, tb, to, p);
   return cudaGetLastError();
 }
 
@@ -594,7 +609,7 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
   p.E = (int)g.E;
   p.N = (int)g.N;
   p.Kd = (int)g.Kd;
-  CUtensorMap ta;
+  CUtensorMap ta, to = {};
   RowMaps tb = {};
   cudaError_t e;
   if (dir == kWeight) {
@@ -604,10 +619,12 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
     if ((e = make_tensor_map_rows(&ta, g.a, type, g.cap, g.N, g.sa, BK, 64)) != cudaSuccess) return e;
     if ((e = make_tensor_map_rows(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK, 64)) != cudaSuccess) return e;
     const bool f32 = g.out_dtype == MOE_ELEM_F32;
-    p.sectors = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.Kd * (f32 ? 4 : 2) % 32 == 0;
+    if ((e = make_tensor_map_matrices(&to, g.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, f32 ? 4 : 2, g.E, g.N,
+                                      g.Kd, 32, f32 ? 32 : 64)) != cudaSuccess)
+      return e;
     const int64_t tiles = g.E * p.mt * p.kt;
-    return f32 ? launch<kWeight, T, float>(ta, tb, p, tiles, st)
-               : launch<kWeight, T, T>(ta, tb, p, tiles, st);
+    return f32 ? launch<kWeight, T, float>(ta, tb, to, p, tiles, st)
+               : launch<kWeight, T, T>(ta, tb, to, p, tiles, st);
   }
   p.features = (int)(dir == kForward ? g.N : g.Kd);
   p.contraction = (int)(dir == kForward ? g.Kd : g.N);
@@ -622,7 +639,7 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
   // up to 256 routes no expert has a second tile and every tile costs its weights:
   // in turn, without the counter and its clearing
   if (routes > BN) p.next = static_cast<int32_t*>(g.workspace);
-  return fwd ? launch<kForward, T, T>(ta, tb, p, tiles, st) : launch<kData, T, T>(ta, tb, p, tiles, st);
+  return fwd ? launch<kForward, T, T>(ta, tb, to, p, tiles, st) : launch<kData, T, T>(ta, tb, to, p, tiles, st);
 }
 
 }  // namespace
