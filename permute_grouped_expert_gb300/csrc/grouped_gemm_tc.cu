@@ -15,11 +15,14 @@
 // may hold anything, NaN too).
 //
 // Per CTA, warp-specialised (rank 0 leads the pair):
-//   warp 0      TMA producer of its half of both operands, 64 of the contraction a stage
+//   warps 0, 3  TMA producers of its half of the first and of the second operand, 64 of
+//               the contraction a stage: one copy each (a thread issues a copy in about 120
+//               cycles, whatever its bytes; four of 8 KB a stage were what the weights'
+//               gradient waited for)
 //   warp 1      TMEM; on the leader one elected lane issues the MMAs
 //   warp 2      on the leader: claims tiles and hands their numbers to both CTAs
-//   warp 3      kWeight: zeros behind an expert's last row
 //   warps 4..7  epilogue of this CTA's 128 features, beside the next tile's MMAs
+//   warp 8      kWeight: zeros behind an expert's last row
 // Every wait is bounded (MOE_DEV_ERR_TIMEOUT, then a clean exit).
 #include <type_traits>
 
@@ -33,7 +36,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 256;
+template <GemmDir DIR>
+constexpr int kThreads = DIR == kWeight ? 288 : 256;
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
 constexpr int kSlots = 2;
 template <GemmDir DIR>
@@ -61,6 +65,7 @@ struct TcParams {
   int N, Kd;                  // kWeight
   int mt;                     // tiles of 256 features (kWeight: of N)
   int kt;                     // kWeight: tiles of 256 of Kd
+  bool a_groups, b_groups;    // the operand's map has columns in groups of 64
 };
 
 // A tile as the pair's readers get it.
@@ -206,7 +211,7 @@ MOE_DEVICE void settle(uint64_t ns) {
 
 // T: 16-bit type of the operands; OUT: of the result.
 template <GemmDir DIR, typename T, typename OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR>, 1)
     grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
                            const __grid_constant__ CUtensorMap tm_out, TcParams p) {
   constexpr int kStages = kStagesOf<DIR>;
@@ -240,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kSlots; s++) {
       mbar_init(&s_have[s], 1);
-      mbar_init(&s_free[s], kW ? 13 : 11);  // on the leader: every reader of both CTAs
+      mbar_init(&s_free[s], kW ? 15 : 13);  // on the leader: every reader of both CTAs
     }
     mbar_init(&s_drain, 1);
     fence_barrier_init();
@@ -279,9 +284,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return ti.e >= 0;
   };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- TMA producer
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------- TMA producers
     if (elect_one_lane()) {
+      const bool first = warp == 0;  // of the first operand; it announces both's bytes
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued_parity[kStages];
@@ -292,44 +298,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Tile ti;
         if (!take_tile(i, ti)) break;
         const int nkb = ti.blocks;
-        const int f0 = ti.m * BM + (int)rank * 128;             // first feature of this CTA
-        const int half = ti.cols / 2;                           // columns of this CTA
-        const int c0 = kW ? ti.n * BN + (int)rank * 128 : 0;    // kWeight: its first column
+        const int half = ti.cols / 2;  // columns of this CTA
+        // first feature of this CTA, or kWeight's second operand: its first column
+        const int f0 = (first ? ti.m * BM : ti.n * BN) + (int)rank * 128;
+        const int row = ti.row + (int)rank * half;
+        const CUtensorMap* map = first ? &tm_a : kW ? &tm_b.of[0] : &tm_b.of[half / 16 - 1];
         const uint32_t bytes = kW ? kStageBytes : kOperand + (uint32_t)half * BK * 2;
+        const bool groups = first ? p.a_groups : p.b_groups;
         for (int kb = 0; kb < nkb; kb++) {
           if (!mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          uint8_t* sa = smem + (size_t)stage * kStageBytes;
-          uint8_t* sb = sa + kOperand;
+          uint8_t* to = smem + (size_t)stage * kStageBytes + (first ? 0 : kOperand);
           const bool tail = kW && kb == nkb - 1 && ragged(ti);
           uint32_t bar;
           if (tail) {
             bar = mapa_shared(smem_u32(&s_tail[stage]), rank);
-            mbar_arrive_expect_tx(&s_tail[stage], bytes);
+            if (first) mbar_arrive_expect_tx(&s_tail[stage], bytes);
           } else {
             bar = mapa_shared(smem_u32(&s_full[stage]), 0);
-            if (rank == 0) {
+            if (first && rank == 0) {
               mbar_arrive_expect_tx(&s_full[stage], 2 * bytes);
               if (kW) mbar_arrive(&s_full[stage]);
             }
           }
           const int k0 = kb * BK;
           if (kW) {
-            const int r0 = ti.row + k0;
-            tma_load_2d_pair(sa, &tm_a, f0, r0, bar);
-            tma_load_2d_pair(sa + kBox, &tm_a, f0 + 64, r0, bar);
-            tma_load_2d_pair(sb, &tm_b.of[0], c0, r0, bar);
-            tma_load_2d_pair(sb + kBox, &tm_b.of[0], c0 + 64, r0, bar);
-          } else {
-            if (DIR == kForward) {
-              tma_load_3d_pair(sa, &tm_a, k0, f0, ti.e, bar);
+            if (groups) {
+              tma_load_3d_pair(to, map, 0, ti.row + k0, f0 / 64, bar);
             } else {
-              tma_load_3d_pair(sa, &tm_a, f0, k0, ti.e, bar);
-              tma_load_3d_pair(sa + kBox, &tm_a, f0 + 64, k0, ti.e, bar);
+              tma_load_2d_pair(to, map, f0, ti.row + k0, bar);
+              tma_load_2d_pair(to + kBox, map, f0 + 64, ti.row + k0, bar);
             }
-            tma_load_2d_pair(sb, &tm_b.of[half / 16 - 1], k0, ti.row + (int)rank * half, bar);
+          } else if (!first) {
+            tma_load_2d_pair(to, map, k0, row, bar);
+          } else if (DIR == kForward) {
+            tma_load_3d_pair(to, map, k0, f0, ti.e, bar);
+          } else if (groups) {
+            tma_load_4d_pair(to, map, 0, k0, f0 / 64, ti.e, bar);
+          } else {
+            tma_load_3d_pair(to, map, f0, k0, ti.e, bar);
+            tma_load_3d_pair(to + kBox, map, f0 + 64, k0, ti.e, bar);
           }
           issued[stage] = !tail;
           issued_parity[stage] = phase;
@@ -425,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 3) {
+  } else if (warp == 8) {
     // ---------------------------------------------------------- zeros (kWeight)
     if (kW) {
       int stage = 0;
@@ -550,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
 
-  if (kW && warp >= 4 && lane == 0) bulk_wait_all();
+  if (kW && warp >= 4 && warp < 8 && lane == 0) bulk_wait_all();
   tc_fence_before();
   __syncwarp();
   cluster_sync_all();
@@ -581,7 +591,7 @@ cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& 
     cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)device_sm_count() / 2 * 2);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads<DIR>);
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = &cluster;
     cfg.numAttrs = 1;
@@ -590,7 +600,7 @@ cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& 
   if (e != cudaSuccess) return e;
   const int64_t clusters = at_once[dev] < 1 ? 1 : at_once[dev] < most_tiles ? at_once[dev] : most_tiles;
   if (p.next && (e = cudaMemsetAsync(p.next, 0, sizeof(int32_t), st)) != cudaSuccess) return e;
-  grouped_gemm_tc_kernel<DIR, T, OUT><<<(unsigned)(2 * clusters), kThreads, smem, st>>>(ta, tb, to, p);
+  grouped_gemm_tc_kernel<DIR, T, OUT><<<(unsigned)(2 * clusters), kThreads<DIR>, smem, st>>>(ta, tb, to, p);
   return cudaGetLastError();
 }
 
@@ -616,8 +626,14 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
     p.mt = (int)((g.N + BM - 1) / BM);
     p.kt = (int)((g.Kd + BN - 1) / BN);
     p.next = static_cast<int32_t*>(g.workspace);
-    if ((e = make_tensor_map_rows(&ta, g.a, type, g.cap, g.N, g.sa, BK, 64)) != cudaSuccess) return e;
-    if ((e = make_tensor_map_rows(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK, 64)) != cudaSuccess) return e;
+    p.a_groups = g.N % 64 == 0;
+    p.b_groups = g.Kd % 64 == 0;
+    e = p.a_groups ? make_tensor_map_row_groups(&ta, g.a, type, g.cap, g.N, g.sa, BK)
+                   : make_tensor_map_rows(&ta, g.a, type, g.cap, g.N, g.sa, BK, 64);
+    if (e != cudaSuccess) return e;
+    e = p.b_groups ? make_tensor_map_row_groups(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK)
+                   : make_tensor_map_rows(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK, 64);
+    if (e != cudaSuccess) return e;
     const bool f32 = g.out_dtype == MOE_ELEM_F32;
     if ((e = make_tensor_map_matrices(&to, g.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, f32 ? 4 : 2, g.E, g.N,
                                       g.Kd, 32, f32 ? 32 : 64)) != cudaSuccess)
@@ -630,7 +646,10 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
   p.contraction = (int)(dir == kForward ? g.Kd : g.N);
   p.mt = (p.features + BM - 1) / BM;
   const bool fwd = dir == kForward;
-  if ((e = make_tensor_map_matrices(&ta, g.b, type, 2, g.E, g.N, g.Kd, fwd ? 128 : BK, 64)) != cudaSuccess) return e;
+  p.a_groups = !fwd && g.Kd % 64 == 0;
+  e = p.a_groups ? make_tensor_map_matrix_groups(&ta, g.b, type, g.E, g.N, g.Kd, BK)
+                 : make_tensor_map_matrices(&ta, g.b, type, 2, g.E, g.N, g.Kd, fwd ? 128 : BK, 64);
+  if (e != cudaSuccess) return e;
   const int64_t routes = g.T * g.K;
   for (int i = 0; i < 8 && (i == 0 || i * 32 < routes); i++)  // a tile has no more rows than there are routes
     if ((e = make_tensor_map_rows(&tb.of[i], g.a, type, g.cap, p.contraction, g.sa, 16 * (i + 1), BK)) != cudaSuccess)

@@ -314,6 +314,16 @@ MOE_DEVICE void tma_load_3d_pair(void* dst, const CUtensorMap* map, int32_t c0, 
       : "memory");
 }
 
+// The same for a box of a 4-D tensor.
+MOE_DEVICE void tma_load_4d_pair(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2, int32_t c3,
+                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar_cluster)
+      : "memory");
+}
+
 // Store of a box of a 3-D tensor from shared memory; what lies outside the tensor
 // is left out.  Completion is that of the issuing thread's bulk groups.
 MOE_DEVICE void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0, int32_t c1, int32_t c2) {

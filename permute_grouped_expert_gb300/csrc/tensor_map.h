@@ -39,18 +39,47 @@ inline cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, CUtens
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Tiled map of 16-bit elements with the 128-byte swizzle; strides in bytes, of all
+// dimensions but the innermost.
+inline cudaError_t make_tensor_map(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int rank,
+                                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(map, dtype, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Bytes between the rows of a row matrix (any multiple of 16 where there is one row).
+inline uint64_t row_bytes(uint64_t rows, uint64_t cols, uint64_t stride) {
+  return (rows > 1 ? stride : (cols + 7) / 8 * 8) * 2;
+}
+
 // Row matrix [rows][cols] of 16-bit elements whose rows lie `stride` elements apart.
 inline cudaError_t make_tensor_map_rows(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint64_t rows,
                                         uint64_t cols, uint64_t stride, uint32_t box_rows, uint32_t box_cols) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {(rows > 1 ? stride : (cols + 7) / 8 * 8) * 2};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {row_bytes(rows, cols, stride)};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  return make_tensor_map(map, base, dtype, 2, dims, strides, box);
+}
+
+// The same with columns in groups of 64 (cols a multiple of 64): boxes of two groups
+// of box_rows rows, one group after the other in shared memory.
+inline cudaError_t make_tensor_map_row_groups(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
+                                              uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows) {
+  const cuuint64_t dims[3] = {64, rows, cols / 64}, strides[2] = {row_bytes(rows, cols, stride), 128};
+  const cuuint32_t box[3] = {64, box_rows, 2};
+  return make_tensor_map(map, base, dtype, 3, dims, strides, box);
+}
+
+// Matrices [count][rows][cols] of 16-bit elements, contiguous, columns in groups of
+// 64: boxes of two groups of box_rows rows of one matrix.
+inline cudaError_t make_tensor_map_matrix_groups(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
+                                                 uint64_t count, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  const cuuint64_t dims[4] = {64, rows, cols / 64, count}, strides[3] = {cols * 2, 128, rows * cols * 2};
+  const cuuint32_t box[4] = {64, box_rows, 2, 1};
+  return make_tensor_map(map, base, dtype, 4, dims, strides, box);
 }
 
 // Matrices [count][rows][cols], contiguous; boxes within one matrix.
