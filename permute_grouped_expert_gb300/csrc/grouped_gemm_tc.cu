@@ -104,53 +104,63 @@ MOE_DEVICE int tile_rows(int64_t rows, int tiles) { return (int)((rows + tiles -
 struct Order {
   int tiles[2];            // of either kind: 0 products, 1 bytes
   int experts[2];
+  uint64_t share;          // of the second kind, in 2^-32
   int before[2][kMaxE];    // tiles of the kind's experts before
   uint16_t expert[2][kMaxE];
 };
 
-// Filled by one warp.  per: tiles of an expert that has rows (kForward, kData: for
-// each of its tiles of rows); kWeight has tiles without rows too.
+// Filled by one warp, whose lanes take a run of experts each: one scan, whatever
+// their number.  per: tiles of an expert (kForward, kData: of each of its tiles of
+// rows).
 template <bool WEIGHT>
 MOE_DEVICE void make_order(Order& o, const TcParams& p, int per) {
-  constexpr int kAhead = 8;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, run = (p.E + 31) / 32, e0 = lane * run, e1 = min(e0 + run, p.E);
+  auto rows_of = [&](int e) {
+    int64_t beg = 0, end = 0;
+    if (e < e1) gemm_segment(p.offsets, p.counts, p.cap, e, beg, end);
+    return (int)(end - beg);
+  };
   int tiles[2] = {0, 0}, experts[2] = {0, 0};
-  for (int e0 = 0; e0 < p.E; e0 += 32 * kAhead) {
-    int64_t rows[kAhead];
+  auto add = [&](int rows, int (&t)[2], int (&x)[2]) {
+    const int mine = WEIGHT ? per : row_tiles(rows) * per;
+    t[0] += rows > BN ? mine : 0;
+    t[1] += rows > BN ? 0 : mine;
+    x[0] += mine && rows > BN;
+    x[1] += mine && rows <= BN;
+  };
+  constexpr int kAhead = 8;
+  for (int e = e0; e < e0 + run; e += kAhead) {
+    int rows[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; j++) {
-      const int e = e0 + j * 32 + lane;
-      int64_t beg = 0, end = 0;
-      if (e < p.E) gemm_segment(p.offsets, p.counts, p.cap, e, beg, end);
-      rows[j] = end - beg;
-    }
+    for (int j = 0; j < kAhead; j++) rows[j] = rows_of(e + j);
 #pragma unroll
-    for (int j = 0; j < kAhead; j++) {
-      const int e = e0 + j * 32 + lane;
-      const int mine = e < p.E ? (WEIGHT ? per : row_tiles(rows[j]) * per) : 0;
-      const int kind = rows[j] <= BN;
-      const unsigned some = __ballot_sync(0xffffffffu, mine > 0), second = __ballot_sync(0xffffffffu, mine > 0 && kind);
-      int incl[2] = {kind ? 0 : mine, kind ? mine : 0};
+    for (int j = 0; j < kAhead; j++)
+      if (e + j < e1) add(rows[j], tiles, experts);
+  }
+  int t_sum[2] = {tiles[0], tiles[1]}, x_sum[2] = {experts[0], experts[1]};  // up to this lane
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, incl[0], d), b = __shfl_up_sync(0xffffffffu, incl[1], d);
-        if (lane >= d) incl[0] += a, incl[1] += b;
-      }
-      if (mine > 0) {
-        const unsigned same = kind ? second : some & ~second;
-        const int at = (kind ? experts[1] : experts[0]) + __popc(same & lanemask_lt());
-        o.expert[kind][at] = (uint16_t)e;
-        o.before[kind][at] = (kind ? tiles[1] + incl[1] : tiles[0] + incl[0]) - mine;
-      }
-      tiles[0] += __shfl_sync(0xffffffffu, incl[0], 31);
-      tiles[1] += __shfl_sync(0xffffffffu, incl[1], 31);
-      experts[0] += __popc(some & ~second);
-      experts[1] += __popc(second);
+  for (int d = 1; d < 32; d <<= 1) {
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const int a = __shfl_up_sync(0xffffffffu, t_sum[k], d), b = __shfl_up_sync(0xffffffffu, x_sum[k], d);
+      if (lane >= d) t_sum[k] += a, x_sum[k] += b;
     }
   }
-  if (lane == 0) {
+  if (lane == 31) {
 #pragma unroll
-    for (int k = 0; k < 2; k++) o.tiles[k] = tiles[k], o.experts[k] = experts[k];
+    for (int k = 0; k < 2; k++) o.tiles[k] = t_sum[k], o.experts[k] = x_sum[k];
+    // rounded up: after all tiles the second kind has had all of its
+    const uint64_t total = (uint64_t)t_sum[0] + t_sum[1];
+    o.share = total ? (((uint64_t)t_sum[1] << 32) + total - 1) / total : 0;
+  }
+  int t[2] = {t_sum[0] - tiles[0], t_sum[1] - tiles[1]}, x[2] = {x_sum[0] - experts[0], x_sum[1] - experts[1]};
+  for (int e = e0; e < e1; e++) {
+    const int rows = rows_of(e), kind = rows <= BN;
+    if (WEIGHT || rows > 0) {
+      o.expert[kind][kind ? x[1] : x[0]] = (uint16_t)e;
+      o.before[kind][kind ? x[1] : x[0]] = kind ? t[1] : t[0];
+    }
+    add(rows, t, x);
   }
   __syncwarp();
 }
@@ -163,8 +173,8 @@ MOE_DEVICE Tile tile_of(int64_t t, const Order& o, const TcParams& p) {
     i.e = -1;
     return i;
   }
-  const int64_t s = t * o.tiles[1] / total;  // bytes' tiles before t
-  const int kind = (t + 1) * o.tiles[1] / total > s ? 1 : 0;
+  const int64_t s = (int64_t)((uint64_t)t * o.share >> 32);  // bytes' tiles before t
+  const int kind = (int64_t)((uint64_t)(t + 1) * o.share >> 32) > s ? 1 : 0;
   const int at = (int)(kind ? s : t - s);
   const int x = expert_of_row(o.before[kind], o.experts[kind], at), local = at - o.before[kind][x];
   int64_t beg, end;
@@ -253,6 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR>, 1)
     tma_prefetch_desc(&tm_b.of[0]);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, kTmemCols);
+  if (warp == 2 && rank == 0) make_order<kW>(s_order, p, kW ? p.mt * p.kt : p.mt);
   tc_fence_before();
   __syncwarp();
   cluster_sync_all();
@@ -418,21 +429,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR>, 1)
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------- tiles (leader)
-    if (rank == 0) {
-      make_order<kW>(s_order, p, kW ? p.mt * p.kt : p.mt);
-      if (lane == 0) {
-        const int64_t total = (int64_t)s_order.tiles[0] + s_order.tiles[1];
-        int64_t t = p.next ? atomicAdd(p.next, 1) : cluster;
-        for (int i = 0;; i++) {
-          const int s = i % kSlots;
-          const Tile ti = tile_of<DIR>(t, s_order, p);
-          if (!mbar_wait_cluster(&s_free[s], ((i / kSlots) & 1) ^ 1, abort_flag, p.status)) break;
-          for (uint32_t r = 0; r < 2; r++)
-            send_32(mapa_shared(smem_u32(&s_tile[s]), r), mapa_shared(smem_u32(&s_have[s]), r),
-                    make_int4(ti.e, ti.m, ti.n, ti.row), make_int4(ti.end, ti.cols, ti.blocks, 0));
-          if (t >= total) break;
-          t = p.next ? atomicAdd(p.next, 1) : t + clusters;
-        }
+    if (lane == 0 && rank == 0) {
+      const int64_t total = (int64_t)s_order.tiles[0] + s_order.tiles[1];
+      int64_t t = p.next ? atomicAdd(p.next, 1) : cluster;
+      for (int i = 0;; i++) {
+        const int s = i % kSlots;
+        const int64_t then = p.next ? atomicAdd(p.next, 1) : t + clusters;  // on its way meanwhile
+        const Tile ti = tile_of<DIR>(t, s_order, p);
+        if (!mbar_wait_cluster(&s_free[s], ((i / kSlots) & 1) ^ 1, abort_flag, p.status)) break;
+        for (uint32_t r = 0; r < 2; r++)
+          send_32(mapa_shared(smem_u32(&s_tile[s]), r), mapa_shared(smem_u32(&s_have[s]), r),
+                  make_int4(ti.e, ti.m, ti.n, ti.row), make_int4(ti.end, ti.cols, ti.blocks, 0));
+        if (t >= total) break;
+        t = then;
       }
     }
   } else if (warp == 8) {
@@ -573,8 +582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR>, 1)
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <GemmDir DIR, typename T, typename OUT>
-cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, const TcParams& p,
-                   int64_t most_tiles, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, TcParams p, int64_t most_tiles,
+                   cudaStream_t st) {
   constexpr size_t smem = kDynSmem<DIR>;
   static int at_once[PerDeviceOnce::kMaxDevices];
   static PerDeviceOnce once;
@@ -599,6 +608,7 @@ cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& 
   });
   if (e != cudaSuccess) return e;
   const int64_t clusters = at_once[dev] < 1 ? 1 : at_once[dev] < most_tiles ? at_once[dev] : most_tiles;
+  if (most_tiles <= clusters) p.next = nullptr;  // a tile each: no counter to clear
   if (p.next && (e = cudaMemsetAsync(p.next, 0, sizeof(int32_t), st)) != cudaSuccess) return e;
   grouped_gemm_tc_kernel<DIR, T, OUT><<<(unsigned)(2 * clusters), kThreads<DIR>, smem, st>>>(ta, tb, to, p);
   return cudaGetLastError();

@@ -82,9 +82,11 @@ def swiglu(pre, p):
 
 
 def swiglu_tol(pre, p, dtype):
-    # exp to 2 ulp (4 U), 1 + z, the quotient, and three products: below 12 U of the result
+    # exp to 2 + 1.173 |g| ulp ((4 + 2.35 |g|) U, CUDA's bound of its fast one), 1 + z to U, the quotient to 2 ulp (4 U),
+    # and four products: below (14 + 2.4 |g|) U of the result
     a = swiglu(pre, p)
-    return 12 * U * a.abs() + bu.rounding(a, dtype) + 2.0 ** -140
+    g = pre.double()[:, pre.shape[1] // 2:].abs()
+    return (14 + 2.4 * g) * U * a.abs() + bu.rounding(a, dtype) + 2.0 ** -140
 
 
 def swiglu_backward(pre, p, ga):
@@ -96,10 +98,11 @@ def swiglu_backward(pre, p, ga):
     terms = d * act * u
     q = d if p is None else d * p.double()[:, None]
     gu, gg = q * act, q * u * s * (1 + g * (1 - s))
-    # s and 1 - s to 8 U; 1 + g (1 - s) may cancel: its error is that of its two parts
-    tg = (q * u * s).abs() * (12 * U + 14 * U * (1 + (g * (1 - s)).abs()))
-    tp = (12 + I / 32 + 24) * U * terms.abs().sum(1)
-    return torch.cat([gu, gg], 1), terms.sum(1), torch.cat([14 * U * gu.abs(), tg], 1) + 2.0 ** -140, tp
+    # s and 1 - s to (10 + 2.4 |g|) U, as in swiglu_tol; 1 + g (1 - s) may cancel: its error is that of its two parts
+    e = (10 + 2.4 * g.abs()) * U
+    tg = (q * u * s).abs() * (4 * U + e) * ((1 + g * (1 - s)).abs() + 1 + (g * (1 - s)).abs())
+    tp = ((4 * U + e) * terms.abs()).sum(1) + (I / 32 + 24) * U * terms.abs().sum(1)
+    return torch.cat([gu, gg], 1), terms.sum(1), torch.cat([(6 * U + e) * gu.abs(), tg], 1) + 2.0 ** -140, tp
 
 
 # ----------------------------------------------------------------- RMS norm
