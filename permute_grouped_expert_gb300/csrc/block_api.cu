@@ -163,6 +163,7 @@ moe_status grouped_rows(GemmDir dir, const moe_handle_dev* handle, const moe_sha
   if (!rows_ok(in, cap, kin, 2) || !rows_ok(out, cap, kout, 2)) return MOE_ERR_INVALID_ARG;
   if (overlap(in, kin, out, kout, cap, 2) || meet(bytes_of(out, cap, kout, 2), bytes_of(weight, w_bytes)))
     return MOE_ERR_INVALID_ARG;
+  if (!grouped_gemm_counts(*shape, *layout, kout)) return MOE_ERR_INVALID_ARG;
   const moe_status ws = check_gemm_workspace(gemm, shape, layout, workspace, workspace_bytes);
   if (ws != MOE_OK) return ws;
   if (shape->T == 0 || cap == 0) return MOE_OK;

@@ -1,14 +1,929 @@
-// grouped_gemm.cu -- which kernel a product grouped by expert runs on.
+// grouped_gemm.cu -- products grouped by expert on the tensor cores of pairs of
+// SMs (2-CTA clusters, tcgen05 cta_group::2, operands by TMA, sums in TMEM).
+//
+//   kForward  y[r]  = W x[r]            kData  gx[r] = W^T gy[r]
+//   kWeight   gW    = sum gy[r] x[r]^T (+ addend)
+//
+// Rows' products put the expert's matrix on the M side of the MMA and its rows on
+// the N side: a tile is 256 features (128 a CTA) by up to 256 rows, and an expert's
+// last rows cost what they are, in steps of 32, where rows as M would be filled up
+// to 256.  kData reads W as it lies, its features contiguous (an M-major operand),
+// so that no transposed copy exists.  The weights' gradient has 256 x 256 tiles of
+// the matrix and runs along the expert's rows, both operands with M and N
+// contiguous; its last 16 rows may reach into rows that are not the expert's: those
+// are overwritten with zeros in shared memory between the copy and the MMA (they
+// may hold anything, NaN too).
+//
+// Per CTA, warp-specialised (rank 0 leads the pair):
+//   warps 0, 3  TMA producers of its half of the first and of the second operand, 64 of
+//               the contraction a stage: one copy each (a thread issues a copy in about 120
+//               cycles, whatever its bytes; four of 8 KB a stage were what the weights'
+//               gradient waited for)
+//   warp 1      TMEM; on the leader one elected lane issues the MMAs
+//   warp 2      on the leader: claims tiles and hands their numbers to both CTAs
+//   warps 4..7  epilogue of this CTA's 128 features, beside the next tile's MMAs
+//   warp 8      kWeight: zeros behind an expert's last row
+// Every wait is bounded (MOE_DEV_ERR_TIMEOUT, then a clean exit).
+#include <type_traits>
+
+#include "block_common.cuh"
 #include "grouped_gemm.h"
+#include "sm100_ptx.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 
+namespace {
+
+using namespace sm100;
+
+constexpr int kPieceWarps = 8;  // that load what TMA cannot
+template <GemmDir DIR, bool PIECES>
+constexpr int kThreads = 256 + (PIECES ? 32 * kPieceWarps : DIR == kWeight ? 32 : 0);
+constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
+// Tiles that may be on their way to the readers: more where tiles are short, fewer
+// where the last ones would wait behind long ones.
+template <GemmDir DIR>
+constexpr int kSlotsOf = DIR == kWeight ? 4 : 2;
+template <GemmDir DIR, bool PIECES>
+constexpr int kStagesOf = DIR == kWeight && !PIECES ? 5 : 6;
+constexpr int kBand = 8;                                // tiles of a band that share their operands in L2
+constexpr uint32_t kOperand = 128 * BK * 2;             // a CTA's half of an operand: 16 KB
+constexpr uint32_t kBox = 64 * BK * 2;                  // a box of an operand that is not K-major
+constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxE = 1024;
+constexpr uint32_t kOutBytes = 32 * 128;                // kWeight: a warp's 32 rows of 128 bytes, twice
+constexpr int kTurn = 33;                               // and in pieces: a row of 32 results and a word between
+template <GemmDir DIR, bool PIECES>
+constexpr size_t kDynSmem = 1024 + (size_t)kStagesOf<DIR, PIECES> * kStageBytes +
+                            (DIR != kWeight ? 0 : PIECES ? 4 * 32 * kTurn * 4 : 8 * kOutBytes);
+
+struct TcParams {
+  const int32_t *offsets, *counts;
+  int32_t* status;
+  int32_t* next;  // tile counter, or NULL: tiles in turn
+  void* out;
+  const float* addend;
+  int64_t sout;
+  int64_t cap;
+  int E;
+  int features, contraction;  // rows' products
+  int N, Kd;                  // kWeight
+  int mt;                     // tiles of 256 features (kWeight: of N)
+  int kt;                     // kWeight: tiles of 256 of Kd
+  bool a_groups, b_groups;    // the operand's map has columns in groups of 64
+  // PIECES: the operands themselves, the bytes that hold them, strides of their rows
+  const uint16_t *a, *b, *a_end, *b_end;
+  int64_t sa, sb;
+};
+
+// Routed rows [beg, end) of expert e below the capacity; empty where the handle
+// holds no segment.
+MOE_DEVICE void gemm_segment(const int32_t* offsets, const int32_t* counts, int64_t cap, int e, int64_t& beg,
+                             int64_t& end) {
+  const int64_t off = offsets[e], cnt = counts[e];
+  beg = min64(max64(off, 0), cap);
+  end = off < 0 || cnt <= 0 ? beg : max64(min64(off + cnt, cap), beg);
+}
+
+// A tile as the pair's readers get it.
+struct alignas(16) Tile {
+  int e, m, n;   // expert, -1 behind the last tile; tile of features; kWeight: tile of Kd
+  int row, end;  // rows [row, end) of the tile, or of the expert (kWeight)
+  int cols;      // columns of the MMA
+  int blocks;    // stages along the contraction
+  int pad;
+};
+
+// Maps of the second operand: boxes of 16, 32, .. 128 rows, so that a tile's half of
+// a stage is one copy whatever its rows (as copies of 16 rows, 8192 x 8192 x 8192
+// over experts of about 1024 rows took 1031 us where whole tiles took 717); kWeight:
+// the first alone.
+struct RowMaps {
+  CUtensorMap of[8];
+};
+
+// Tiles of an expert in bands of kBand along one side, the other side outermost in
+// a band: tiles that run at once share few operands.
+MOE_DEVICE void banded(int local, int along, int across, int& a, int& c) {
+  const int band = local / (kBand * across), in = local - band * kBand * across;
+  const int width = min(kBand, along - band * kBand);
+  c = in / width;
+  a = band * kBand + in - c * width;
+}
+
+// Tiles of rows of an expert with `rows` rows, and rows of each.
+MOE_DEVICE int row_tiles(int64_t rows) { return (int)((rows + BN - 1) / BN); }
+MOE_DEVICE int tile_rows(int64_t rows, int tiles) { return (int)((rows + tiles - 1) / tiles + 31) & ~31; }
+
+// The order of the tiles.  Experts of up to BN rows cost their matrix's bytes, the
+// others products; one after another they would use HBM and the tensor cores in
+// turn, so the tiles of both kinds are dealt out evenly among each other.
+struct Order {
+  int tiles[2];            // of either kind: 0 products, 1 bytes
+  int experts[2];
+  uint64_t share;          // of the second kind, in 2^-32
+  int before[2][kMaxE];    // tiles of the kind's experts before
+  uint16_t expert[2][kMaxE];
+};
+
+// Filled by one warp, whose lanes take a run of experts each: one scan, whatever
+// their number.  per: tiles of an expert (kForward, kData: of each of its tiles of
+// rows).
+template <bool WEIGHT>
+MOE_DEVICE void make_order(Order& o, const TcParams& p, int per) {
+  const int lane = threadIdx.x & 31, run = (p.E + 31) / 32, e0 = lane * run, e1 = min(e0 + run, p.E);
+  auto rows_of = [&](int e) {
+    int64_t beg = 0, end = 0;
+    if (e < e1) gemm_segment(p.offsets, p.counts, p.cap, e, beg, end);
+    return (int)(end - beg);
+  };
+  int tiles[2] = {0, 0}, experts[2] = {0, 0};
+  auto add = [&](int rows, int (&t)[2], int (&x)[2]) {
+    const int mine = WEIGHT ? per : row_tiles(rows) * per;
+    t[0] += rows > BN ? mine : 0;
+    t[1] += rows > BN ? 0 : mine;
+    x[0] += mine && rows > BN;
+    x[1] += mine && rows <= BN;
+  };
+  constexpr int kAhead = 8;
+  for (int e = e0; e < e0 + run; e += kAhead) {
+    int rows[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) rows[j] = rows_of(e + j);
+#pragma unroll
+    for (int j = 0; j < kAhead; j++)
+      if (e + j < e1) add(rows[j], tiles, experts);
+  }
+  int t_sum[2] = {tiles[0], tiles[1]}, x_sum[2] = {experts[0], experts[1]};  // up to this lane
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const int a = __shfl_up_sync(0xffffffffu, t_sum[k], d), b = __shfl_up_sync(0xffffffffu, x_sum[k], d);
+      if (lane >= d) t_sum[k] += a, x_sum[k] += b;
+    }
+  }
+  if (lane == 31) {
+#pragma unroll
+    for (int k = 0; k < 2; k++) o.tiles[k] = t_sum[k], o.experts[k] = x_sum[k];
+    // rounded up: after all tiles the second kind has had all of its
+    const uint64_t total = (uint64_t)t_sum[0] + t_sum[1];
+    o.share = total ? (((uint64_t)t_sum[1] << 32) + total - 1) / total : 0;
+  }
+  int t[2] = {t_sum[0] - tiles[0], t_sum[1] - tiles[1]}, x[2] = {x_sum[0] - experts[0], x_sum[1] - experts[1]};
+  for (int e = e0; e < e1; e++) {
+    const int rows = rows_of(e), kind = rows <= BN;
+    if (WEIGHT || rows > 0) {
+      o.expert[kind][kind ? x[1] : x[0]] = (uint16_t)e;
+      o.before[kind][kind ? x[1] : x[0]] = kind ? t[1] : t[0];
+    }
+    add(rows, t, x);
+  }
+  __syncwarp();
+}
+
+template <GemmDir DIR>
+MOE_DEVICE Tile tile_of(int64_t t, const Order& o, const TcParams& p) {
+  Tile i = {};
+  const int64_t total = (int64_t)o.tiles[0] + o.tiles[1];
+  if (t >= total) {
+    i.e = -1;
+    return i;
+  }
+  const int64_t s = (int64_t)((uint64_t)t * o.share >> 32);  // bytes' tiles before t
+  const int kind = (int64_t)((uint64_t)(t + 1) * o.share >> 32) > s ? 1 : 0;
+  const int at = (int)(kind ? s : t - s);
+  const int x = expert_of_row(o.before[kind], o.experts[kind], at), local = at - o.before[kind][x];
+  int64_t beg, end;
+  i.e = o.expert[kind][x];
+  gemm_segment(p.offsets, p.counts, p.cap, i.e, beg, end);
+  if (DIR == kWeight) {
+    banded(local, p.mt, p.kt, i.m, i.n);
+    i.row = (int)beg;
+    i.end = (int)end;
+    i.cols = BN;
+    i.blocks = (int)((end - beg + BK - 1) / BK);
+  } else {
+    const int tiles = row_tiles(end - beg);
+    banded(local, tiles, p.mt, i.n, i.m);
+    i.cols = tile_rows(end - beg, tiles);
+    i.row = (int)(beg + (int64_t)i.n * i.cols);
+    i.end = (int)min64((int64_t)i.row + i.cols, end);
+    i.blocks = (p.contraction + BK - 1) / BK;
+  }
+  return i;
+}
+
+// Whether the last stage of a kWeight tile holds rows that are not the expert's
+// within its last 16.
+MOE_DEVICE bool ragged(const Tile& i) { return ((i.end - i.row) & 15) != 0; }
+
+template <typename T>
+MOE_DEVICE uint32_t pack2(float a, float b);
+template <>
+MOE_DEVICE uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+MOE_DEVICE uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+MOE_DEVICE void settle(uint64_t ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < ns) __nanosleep(1000);
+}
+
+// PIECES: operands that TMA does not take (odd widths, rows that start anywhere).
+// Eight elements of a row are the aligned 16-byte pieces that hold them, shifted into
+// place on their way to shared memory; a thread has a stage's loads on their way
+// while it waits for room.  Neighbours in the pieces, and what is beyond the rows or
+// the columns of the operand, are left out or zeros.
+struct Eight {
+  uint4 lo, hi;
+};
+
+// Elements [0, n) at p into e, n maybe below 1 or above 8; [begin, end) is the matrix.
+// Returns true where e.lo holds them in place already.
+MOE_DEVICE bool load_eight(Eight& e, const uint16_t* p, int n, const uint16_t* begin, const uint16_t* end) {
+  e.lo = e.hi = make_uint4(0, 0, 0, 0);
+  if (n <= 0) return true;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p), piece = at & ~uintptr_t(15);
+  const bool two = at != piece;
+  if (piece >= reinterpret_cast<uintptr_t>(begin) && piece + (two ? 32 : 16) <= reinterpret_cast<uintptr_t>(end)) {
+    e.lo = *reinterpret_cast<const uint4*>(piece);
+    if (two) e.hi = *reinterpret_cast<const uint4*>(piece + 16);
+    return false;
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < 8; k++)
+    if (k < n) w[k / 2] |= (uint32_t)p[k] << (16 * (k & 1));
+  e.lo = make_uint4(w[0], w[1], w[2], w[3]);
+  return true;
+}
+
+// The eight elements from byte `from` of the pieces on; zeros from the n-th on.
+MOE_DEVICE uint4 shifted(const Eight& e, uint32_t from, int n) {
+  uint32_t w[8] = {e.lo.x, e.lo.y, e.lo.z, e.lo.w, e.hi.x, e.hi.y, e.hi.z, e.hi.w};
+  if (from & 4) {
+#pragma unroll
+    for (int i = 0; i < 7; i++) w[i] = w[i + 1];
+  }
+  if (from & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; i++) w[i] = w[i + 2];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    w[i] = __funnelshift_r(w[i], w[i + 1], (from & 2) * 8);
+    if (n < 8) w[i] = 2 * i >= n ? 0u : 2 * i + 1 >= n ? w[i] & 0xffffu : w[i];
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A CTA's half of an operand, 64 of the contraction after 64: 128 rows of 64
+// elements in shared memory, of which a thread has eight elements of every 32nd.
+// KMAJOR: they are rows of the operand; otherwise two runs of 64 columns along 64 rows.
+template <bool KMAJOR>
+struct Half {
+  const uint16_t* p;  // this thread's first elements of the next stage
+  const uint16_t *begin, *end;
+  int64_t stride;
+  int n;      // elements from p on that are in the operand's columns
+  int valid;  // rows from this thread's first on: of the operand (KMAJOR), or of the contraction that are left
+  int count;  // rows in shared memory, of 32 each
+
+  // KMAJOR: rows [row, row + rows) of `cols` elements, `used` in shared memory;
+  // otherwise columns from `col` on of `cols`, along rows [row, row + rows).
+  MOE_DEVICE void begin_tile(const uint16_t* base, const uint16_t* stop, int64_t apart, int64_t row, int rows, int col,
+                             int cols, int used, int t) {
+    const int c = col + (t & 7) * 8, j = t >> 3;
+    p = base + (row + j) * apart + c;
+    begin = base;
+    end = stop;
+    stride = apart;
+    n = cols - c;
+    valid = rows - j;
+    count = (used + 31) / 32;
+  }
+
+  MOE_DEVICE const uint16_t* at(int i) const {
+    return KMAJOR ? p + 32 * i * stride : p + 32 * (i & 1) * stride + 64 * (i >> 1);
+  }
+  MOE_DEVICE int have(int i) const {
+    return valid > (KMAJOR ? 32 * i : 32 * (i & 1)) ? (KMAJOR ? n : n - 64 * (i >> 1)) : 0;
+  }
+
+  MOE_DEVICE void load(Eight (&e)[4], uint32_t& in_place) const {
+    in_place = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (i < count && load_eight(e[i], at(i), have(i), begin, end)) in_place |= 1u << i;
+  }
+
+  MOE_DEVICE void store(uint8_t* to, const Eight (&e)[4], uint32_t in_place, int t) const {
+    const int q = t & 7, j = t >> 3;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (i < count) {
+        const uint32_t from = in_place >> i & 1 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(at(i)) & 15);
+        *reinterpret_cast<uint4*>(to + (j + 32 * i) * 128 + ((q ^ (j & 7)) * 16)) = shifted(e[i], from, have(i));
+      }
+  }
+
+  MOE_DEVICE void advance() {
+    p += KMAJOR ? BK : BK * stride;
+    if (KMAJOR)
+      n -= BK;
+    else
+      valid -= BK;
+  }
+};
+
+// T: 16-bit type of the operands; OUT: of the result; PIECES: operands of any
+// alignment, without the maps.
+template <GemmDir DIR, typename T, typename OUT, bool PIECES>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES>, 1)
+    grouped_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
+                           const __grid_constant__ CUtensorMap tm_out, TcParams p) {
+  constexpr int kStages = kStagesOf<DIR, PIECES>, kSlots = kSlotsOf<DIR>;
+  constexpr bool kW = DIR == kWeight, kAmn = DIR != kForward, kBmn = kW;
+  extern __shared__ uint8_t dyn_smem[];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tail[kStages], s_tfull[2], s_tempty[2];
+  __shared__ __align__(8) uint64_t s_have[kSlots], s_free[kSlots], s_drain;
+  __shared__ Tile s_tile[kSlots];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ Order s_order;  // the leader's
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  volatile int* abort_flag = &s_abort;
+
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int s = 0; s < kStages; s++) {
+      // on the leader: its producer (and, kWeight, a second arrival) and both CTAs'
+      // bytes, or both CTAs' warp 8 after the zeros; PIECES: every loading warp of both
+      mbar_init(&s_full[s], PIECES ? 2 * kPieceWarps : kW ? 2 : 1);
+      mbar_init(&s_empty[s], 1);  // each CTA's own, by the leader's commit
+      mbar_init(&s_tail[s], 1);   // each CTA's own bytes of a stage that gets zeros
+    }
+    for (int a = 0; a < 2; a++) {
+      mbar_init(&s_tfull[a], 1);
+      mbar_init(&s_tempty[a], 8);  // on the leader: 4 epilogue warps of each CTA
+    }
+    for (int s = 0; s < kSlots; s++) {
+      mbar_init(&s_have[s], 1);
+      // MMA, 4 epilogue warps a CTA, and its producers (kWeight: and warp 8)
+      mbar_init(&s_free[s], 1 + 2 * (4 + (PIECES ? kPieceWarps : kW ? 3 : 2)));  // on the leader: every reader of both CTAs
+    }
+    mbar_init(&s_drain, 1);
+    fence_barrier_init();
+    if (!PIECES) {
+      tma_prefetch_desc(&tm_a);
+      tma_prefetch_desc(&tm_b.of[0]);
+    }
+  }
+  if (warp == 1) tmem_alloc_pair(&s_tmem, kTmemCols);
+  if (warp == 2 && rank == 0) make_order<kW>(s_order, p, kW ? p.mt * p.kt : p.mt);
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem;
+
+  // The i-th tile of this pair; waits for it, reads it and, once, says so.
+  auto next_tile = [&](int i, Tile& ti) {
+    const int s = i % kSlots;
+    if (!mbar_wait_cluster(&s_have[s], (i / kSlots) & 1, abort_flag, p.status)) return false;
+    const int4 a = ld_shared_v4(&s_tile[s]), b = ld_shared_v4(reinterpret_cast<const int4*>(&s_tile[s]) + 1);
+    ti.e = a.x, ti.m = a.y, ti.n = a.z, ti.row = a.w;
+    ti.end = b.x, ti.cols = b.y, ti.blocks = b.z;
+    return true;
+  };
+  // (after the values are there, which the branch asks for; it is always taken)
+  auto have_read = [&](int i, const Tile& ti) {
+    if ((ti.e | ti.blocks) >= -1) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&s_free[i % kSlots]), 0));
+  };
+  // one thread's, and a whole warp's
+  auto take_tile = [&](int i, Tile& ti) {
+    if (!next_tile(i, ti)) return false;
+    have_read(i, ti);
+    return ti.e >= 0;
+  };
+  auto take_tile_warp = [&](int i, Tile& ti) {
+    if (!__all_sync(0xffffffffu, next_tile(i, ti))) return false;
+    if (lane == 0) have_read(i, ti);
+    return ti.e >= 0;
+  };
+
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------- TMA producers
+    if (!PIECES && elect_one_lane()) {
+      const bool first = warp == 0;  // of the first operand; it announces both's bytes
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued_parity[kStages];
+      bool issued[kStages];
+      for (int s = 0; s < kStages; s++) issued[s] = false;
+      bool ok = true;
+      for (int i = 0; ok; i++) {
+        Tile ti;
+        if (!take_tile(i, ti)) break;
+        const int nkb = ti.blocks;
+        const int half = ti.cols / 2;  // columns of this CTA
+        // first feature of this CTA, or kWeight's second operand: its first column
+        const int f0 = (first ? ti.m * BM : ti.n * BN) + (int)rank * 128;
+        const int row = ti.row + (int)rank * half;
+        const CUtensorMap* map = first ? &tm_a : kW ? &tm_b.of[0] : &tm_b.of[half / 16 - 1];
+        const uint32_t bytes = kW ? kStageBytes : kOperand + (uint32_t)half * BK * 2;
+        const bool groups = first ? p.a_groups : p.b_groups;
+        for (int kb = 0; kb < nkb; kb++) {
+          if (!mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* to = smem + (size_t)stage * kStageBytes + (first ? 0 : kOperand);
+          const bool tail = kW && kb == nkb - 1 && ragged(ti);
+          uint32_t bar;
+          if (tail) {
+            bar = mapa_shared(smem_u32(&s_tail[stage]), rank);
+            if (first) mbar_arrive_expect_tx(&s_tail[stage], bytes);
+          } else {
+            bar = mapa_shared(smem_u32(&s_full[stage]), 0);
+            if (first && rank == 0) {
+              mbar_arrive_expect_tx(&s_full[stage], 2 * bytes);
+              if (kW) mbar_arrive(&s_full[stage]);
+            }
+          }
+          const int k0 = kb * BK;
+          if (kW) {
+            if (groups) {
+              tma_load_3d_pair(to, map, 0, ti.row + k0, f0 / 64, bar);
+            } else {
+              tma_load_2d_pair(to, map, f0, ti.row + k0, bar);
+              tma_load_2d_pair(to + kBox, map, f0 + 64, ti.row + k0, bar);
+            }
+          } else if (!first) {
+            tma_load_2d_pair(to, map, k0, row, bar);
+          } else if (DIR == kForward) {
+            tma_load_3d_pair(to, map, k0, f0, ti.e, bar);
+          } else if (groups) {
+            tma_load_4d_pair(to, map, 0, k0, f0 / 64, ti.e, bar);
+          } else {
+            tma_load_3d_pair(to, map, f0, k0, ti.e, bar);
+            tma_load_3d_pair(to + kBox, map, f0 + 64, k0, ti.e, bar);
+          }
+          issued[stage] = !tail;
+          issued_parity[stage] = phase;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        if (rank == 0) {
+          for (int s = 0; s < kStages; s++) {
+            if (!issued[s]) continue;
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(&s_full[s], issued_parity[s]) && globaltimer_ns() - t0 < kWaitLimitNs) {
+            }
+          }
+        }
+        settle(2000000);  // 2 ms: far longer than any single copy takes
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer (leader)
+    // One elected lane waits and issues, the others stay at the end: known to be one,
+    // it needs no care for others that might issue another MMA.
+    if (rank == 0 && elect_one_lane()) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int i = 0; ok; i++) {
+        Tile ti;
+        if (!take_tile(i, ti)) break;
+        const int nkb = ti.blocks;
+        const uint32_t idesc = idesc_16bit(BM, (uint32_t)ti.cols, std::is_same<T, __nv_bfloat16>::value, kAmn, kBmn);
+        if (!mbar_wait_cluster(&s_tempty[acc], acc_phase ^ 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        for (int kb = 0; kb < nkb; kb++) {
+          if (!mbar_wait_cluster(&s_full[stage], phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + (size_t)stage * kStageBytes), sb = sa + kOperand;
+          const uint64_t adesc = kAmn ? smem_desc_sw128_mn(sa, kBox) : smem_desc_sw128(sa);
+          const uint64_t bdesc = kBmn ? smem_desc_sw128_mn(sb, kBox) : smem_desc_sw128(sb);
+          // a step of 16: 32 bytes of K-major rows, or 16 rows of 128 bytes
+          constexpr uint64_t kAstep = kAmn ? 128 : 2, kBstep = kBmn ? 128 : 2;
+          const int left = kW ? (ti.end - ti.row) - kb * BK : p.contraction - kb * BK;
+#pragma unroll
+          for (int k = 0; k < BK / 16; k++)
+            if (k * 16 < left)
+              mma_bf16_pair(d_tmem, adesc + kAstep * k, bdesc + kBstep * k, idesc, (kb | k) != 0 ? 1u : 0u);
+          mma_commit_pair(&s_empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(&s_tfull[acc], 0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (!ok) {
+        mma_commit_pair(&s_drain, 0x1);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&s_drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- tiles (leader)
+    if (lane == 0 && rank == 0) {
+      const int64_t total = (int64_t)s_order.tiles[0] + s_order.tiles[1];
+      int64_t t = p.next ? atomicAdd(p.next, 1) : cluster;
+      for (int i = 0;; i++) {
+        const int s = i % kSlots;
+        const int64_t then = p.next ? atomicAdd(p.next, 1) : t + clusters;  // on its way meanwhile
+        const Tile ti = tile_of<DIR>(t, s_order, p);
+        if (!mbar_wait_cluster(&s_free[s], ((i / kSlots) & 1) ^ 1, abort_flag, p.status)) break;
+        for (uint32_t r = 0; r < 2; r++)
+          send_32(mapa_shared(smem_u32(&s_tile[s]), r), mapa_shared(smem_u32(&s_have[s]), r),
+                  make_int4(ti.e, ti.m, ti.n, ti.row), make_int4(ti.end, ti.cols, ti.blocks, 0));
+        if (t >= total) break;
+        t = then;
+      }
+    }
+  } else if (PIECES && warp >= 8) {
+    // ---------------------------------------------- producers without TMA
+    const int at = threadIdx.x - 256;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0, ok = 1; ok; i++) {
+      Tile ti;
+      if (!take_tile_warp(i, ti)) break;
+      const int half = ti.cols / 2, f0 = ti.m * BM + (int)rank * 128, c0 = ti.n * BN + (int)rank * 128;
+      Half<DIR == kForward> a;
+      Half<!kW> b;
+      if (kW) {
+        a.begin_tile(p.a, p.a_end, p.sa, ti.row, ti.end - ti.row, f0, p.N, 128, at);
+        b.begin_tile(p.b, p.b_end, p.sb, ti.row, ti.end - ti.row, c0, p.Kd, 128, at);
+      } else {
+        const int64_t w = (int64_t)ti.e * p.N;
+        if (DIR == kForward)
+          a.begin_tile(p.a, p.a_end, p.sa, w + f0, p.N - f0, 0, p.Kd, 128, at);
+        else
+          a.begin_tile(p.a, p.a_end, p.sa, w, p.N, f0, p.Kd, 128, at);
+        const int row = ti.row + (int)rank * half;
+        b.begin_tile(p.b, p.b_end, p.sb, row, min(half, ti.end - row), 0, p.contraction, half, at);
+      }
+      Eight ea[4], eb[4];
+      uint32_t ia, ib;
+      if (ti.blocks) a.load(ea, ia), b.load(eb, ib);
+      for (int kb = 0; kb < ti.blocks; kb++) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status))) {
+          ok = 0;
+          break;
+        }
+        uint8_t* to = smem + (size_t)stage * kStageBytes;
+        a.store(to, ea, ia, at);
+        b.store(to + kOperand, eb, ib, at);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_full[stage]), 0));
+        a.advance();
+        b.advance();
+        if (kb + 1 < ti.blocks) a.load(ea, ia), b.load(eb, ib);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------- zeros (kWeight)
+    if (kW) {
+      int stage = 0;
+      uint32_t phases = 0;  // bit s: parity of s_tail[s]
+      for (int i = 0;; i++) {
+        Tile ti;
+        if (!take_tile_warp(i, ti)) break;
+        const int nkb = ti.blocks;
+        if (nkb && ragged(ti)) {
+          const int s = (stage + nkb - 1) % kStages;
+          int ok = 0;
+          if (lane == 0) ok = mbar_wait(&s_tail[s], (phases >> s) & 1, abort_flag, p.status) ? 1 : 0;
+          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          phases ^= 1u << s;
+          const int rows = (ti.end - ti.row) - (nkb - 1) * BK, stop = (rows + 15) & ~15;
+          uint8_t* base = smem + (size_t)s * kStageBytes;
+          for (int j = lane; j < (stop - rows) * 8 * 4; j += 32) {  // 16 bytes each of the four boxes' rows
+            const int box = j & 3, at = j >> 2;
+            *reinterpret_cast<uint4*>(base + box * kBox + rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_full[s]), 0));
+        }
+        stage = (stage + nkb) % kStages;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    const int lane_base = 32 * (warp & 3);
+    uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (size_t)(warp & 3) * (PIECES ? 32 * kTurn * 4 : 2 * kOutBytes);  // kWeight
+    int out_at = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int i = 0;; i++) {
+      Tile ti;
+      if (!take_tile_warp(i, ti)) break;
+      int ok = 0;
+      if (lane == 0) ok = mbar_wait(&s_tfull[acc], acc_phase, abort_flag, p.status) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
+      const int f_warp = ti.m * BM + (int)rank * 128 + lane_base;  // first feature of this warp
+      if constexpr (kW && PIECES) {
+        // 32 columns of 32 rows at a time, turned in shared memory
+        float* turn = reinterpret_cast<float*>(s_out);
+        const bool none = ti.end == ti.row;
+        const int cols = min(p.Kd - ti.n * BN, BN), rows = min(p.N - f_warp, 32);
+        const int64_t first = ((int64_t)ti.e * p.N + f_warp) * p.Kd + ti.n * BN;
+        for (int c = 0; c < cols && rows > 0; c += 32) {
+          float v[32];
+          if (none) {
+#pragma unroll
+            for (int j = 0; j < 32; j++) v[j] = 0.0f;
+          } else {
+            tmem_ld32(taddr + c, v);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 32; j++) turn[lane * kTurn + j] = v[j];
+          __syncwarp();
+          if (c + lane < cols) {
+            const int64_t at = first + c + lane;
+            OUT* to = static_cast<OUT*>(p.out) + at;
+#pragma unroll 8
+            for (int r = 0; r < rows; r++) {
+              float x = turn[r * kTurn + lane];
+              if (sizeof(OUT) == 4 && p.addend) x += p.addend[at + (int64_t)r * p.Kd];
+              to[(int64_t)r * p.Kd] = from_float<OUT>(x);
+            }
+          }
+        }
+      } else if constexpr (kW) {
+        // 128 bytes of this lane's row of the matrix at a time, through shared memory
+        constexpr int kCols = 128 / (int)sizeof(OUT);
+        const bool none = ti.end == ti.row;
+        const int n = f_warp + lane;
+        const float* add = p.addend ? p.addend + ((int64_t)ti.e * p.N + n) * p.Kd + ti.n * BN : nullptr;
+        const int cols = min(p.Kd - ti.n * BN, BN);
+        for (int c = 0; c < cols && f_warp < p.N; c += kCols) {
+          uint4 piece[8];
+#pragma unroll
+          for (int h = 0; h < kCols / 32; h++) {
+            float v[32];
+            if (none) {
+#pragma unroll
+              for (int j = 0; j < 32; j++) v[j] = 0.0f;
+            } else {
+              tmem_ld32(taddr + c + h * 32, v);
+            }
+            if constexpr (sizeof(OUT) == 4) {
+              if (add && n < p.N) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                  if (c + j < cols) {
+                    const float4 x = *reinterpret_cast<const float4*>(add + c + j);
+                    v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
+                  }
+              }
+#pragma unroll
+              for (int q = 0; q < 8; q++)
+                piece[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                      __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; q++)
+                piece[h * 4 + q] = make_uint4(pack2<T>(v[8 * q], v[8 * q + 1]), pack2<T>(v[8 * q + 2], v[8 * q + 3]),
+                                              pack2<T>(v[8 * q + 4], v[8 * q + 5]), pack2<T>(v[8 * q + 6], v[8 * q + 7]));
+            }
+          }
+          uint8_t* buf = s_out + out_at * kOutBytes;
+          if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this buffer
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; q++) *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) * 16)) = piece[q];
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm_out, buf, ti.n * BN + c, f_warp, ti.e);
+            bulk_commit();
+          }
+          out_at ^= 1;
+        }
+      } else if constexpr (PIECES) {
+        // columns are rows of the result, lanes features
+        const int f = f_warp + lane;
+        T* out = static_cast<T*>(p.out) + f;
+        for (int c = 0; c < ti.cols; c += 32) {
+          float v[32];
+          tmem_ld32(taddr + c, v);
+#pragma unroll
+          for (int j = 0; j < 32; j++) {
+            const int row = ti.row + c + j;
+            if (row < ti.end && f < p.features) out[(int64_t)row * p.sout] = from_float<T>(v[j]);
+          }
+        }
+      } else {
+        // columns are rows of the result, lanes features: neighbouring lanes exchange
+        // one of two rows, so that each stores two features of one
+        const int f = f_warp + (lane & ~1);
+        const bool odd = lane & 1;
+        T* out = static_cast<T*>(p.out) + f;
+        for (int c = 0; c < ti.cols; c += 32) {
+          float v[32];
+          tmem_ld32(taddr + c, v);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const uint32_t w = odd ? pack2<T>(other, v[j + 1]) : pack2<T>(v[j], other);
+            const int row = ti.row + c + j + (odd ? 1 : 0);
+            if (row < ti.end && f < p.features) *reinterpret_cast<uint32_t*>(out + (int64_t)row * p.sout) = w;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      // the loads from TMEM are done; stores to memory may still be on their way
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&s_tempty[acc]), 0));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+
+  if (kW && !PIECES && warp >= 4 && warp < 8 && lane == 0) bulk_wait_all();
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <GemmDir DIR, typename T, typename OUT, bool PIECES>
+cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, TcParams p, int64_t most_tiles,
+                   cudaStream_t st) {
+  constexpr size_t smem = kDynSmem<DIR, PIECES>;
+  static int at_once[PerDeviceOnce::kMaxDevices];
+  static PerDeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run([&] {
+    cudaError_t r = cudaFuncSetAttribute(grouped_gemm_kernel<DIR, T, OUT, PIECES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (r != cudaSuccess) return r;
+    cudaLaunchAttribute cluster = {};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = 2;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)device_sm_count() / 2 * 2);
+    cfg.blockDim = dim3(kThreads<DIR, PIECES>);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(&at_once[dev], grouped_gemm_kernel<DIR, T, OUT, PIECES>, &cfg);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t clusters = at_once[dev] < 1 ? 1 : at_once[dev] < most_tiles ? at_once[dev] : most_tiles;
+  // one or two tiles each: in turn, without the counter, whose clearing takes 4 us
+  if (most_tiles <= 2 * clusters) p.next = nullptr;
+  if (p.next && (e = cudaMemsetAsync(p.next, 0, sizeof(int32_t), st)) != cudaSuccess) return e;
+  grouped_gemm_kernel<DIR, T, OUT, PIECES><<<(unsigned)(2 * clusters), kThreads<DIR, PIECES>, smem, st>>>(ta, tb, to, p);
+  return cudaGetLastError();
+}
+
+template <typename T, bool PIECES>
+cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
+  const CUtensorMapDataType type =
+      g.dtype == MOE_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  TcParams p = {};
+  p.offsets = g.offsets;
+  p.counts = g.counts;
+  p.status = g.status;
+  p.out = g.out;
+  p.addend = g.addend;
+  p.sout = g.sout;
+  p.cap = g.cap;
+  p.E = (int)g.E;
+  p.N = (int)g.N;
+  p.Kd = (int)g.Kd;
+  const uint16_t *rows_a = static_cast<const uint16_t*>(g.a), *b = static_cast<const uint16_t*>(g.b);
+  auto behind = [&](const uint16_t* m, int64_t stride, int64_t cols) {
+    return g.cap ? m + (g.cap - 1) * stride + cols : m;
+  };
+  CUtensorMap ta = {}, to = {};
+  RowMaps tb = {};
+  cudaError_t e;
+  if (dir == kWeight) {
+    p.mt = (int)((g.N + BM - 1) / BM);
+    p.kt = (int)((g.Kd + BN - 1) / BN);
+    p.next = static_cast<int32_t*>(g.workspace);
+    const bool f32 = g.out_dtype == MOE_ELEM_F32;
+    const int64_t tiles = g.E * p.mt * p.kt;
+    if constexpr (PIECES) {
+      p.a = rows_a, p.a_end = behind(rows_a, g.sa, g.N), p.sa = g.sa;
+      p.b = b, p.b_end = behind(b, g.sb, g.Kd), p.sb = g.sb;
+      return f32 ? launch<kWeight, T, float, true>(ta, tb, to, p, tiles, st)
+                 : launch<kWeight, T, T, true>(ta, tb, to, p, tiles, st);
+    }
+    p.a_groups = g.N % 64 == 0;
+    p.b_groups = g.Kd % 64 == 0;
+    e = p.a_groups ? make_tensor_map_row_groups(&ta, g.a, type, g.cap, g.N, g.sa, BK)
+                   : make_tensor_map_rows(&ta, g.a, type, g.cap, g.N, g.sa, BK, 64);
+    if (e != cudaSuccess) return e;
+    e = p.b_groups ? make_tensor_map_row_groups(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK)
+                   : make_tensor_map_rows(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK, 64);
+    if (e != cudaSuccess) return e;
+    if ((e = make_tensor_map_matrices(&to, g.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, f32 ? 4 : 2, g.E, g.N,
+                                      g.Kd, 32, f32 ? 32 : 64)) != cudaSuccess)
+      return e;
+    return f32 ? launch<kWeight, T, float, false>(ta, tb, to, p, tiles, st)
+               : launch<kWeight, T, T, false>(ta, tb, to, p, tiles, st);
+  }
+  p.features = (int)(dir == kForward ? g.N : g.Kd);
+  p.contraction = (int)(dir == kForward ? g.Kd : g.N);
+  p.mt = (p.features + BM - 1) / BM;
+  const bool fwd = dir == kForward;
+  const int64_t routes = g.T * g.K;
+  const int64_t tiles = (routes / BN + (routes < g.E ? routes : g.E)) * p.mt;
+  // up to 256 routes no expert has a second tile and every tile costs its weights:
+  // in turn, without the counter and its clearing
+  if (routes > BN) p.next = static_cast<int32_t*>(g.workspace);
+  if constexpr (PIECES) {
+    p.a = b, p.a_end = b + g.E * g.N * g.Kd, p.sa = g.Kd;
+    p.b = rows_a, p.b_end = behind(rows_a, g.sa, p.contraction), p.sb = g.sa;
+    return fwd ? launch<kForward, T, T, true>(ta, tb, to, p, tiles, st)
+               : launch<kData, T, T, true>(ta, tb, to, p, tiles, st);
+  }
+  p.a_groups = !fwd && g.Kd % 64 == 0;
+  e = p.a_groups ? make_tensor_map_matrix_groups(&ta, g.b, type, g.E, g.N, g.Kd, BK)
+                 : make_tensor_map_matrices(&ta, g.b, type, 2, g.E, g.N, g.Kd, fwd ? 128 : BK, 64);
+  if (e != cudaSuccess) return e;
+  for (int i = 0; i < 8 && (i == 0 || i * 32 < routes); i++)  // a tile has no more rows than there are routes
+    if ((e = make_tensor_map_rows(&tb.of[i], g.a, type, g.cap, p.contraction, g.sa, 16 * (i + 1), BK)) != cudaSuccess)
+      return e;
+  return fwd ? launch<kForward, T, T, false>(ta, tb, to, p, tiles, st)
+             : launch<kData, T, T, false>(ta, tb, to, p, tiles, st);
+}
+
+}  // namespace
+
 size_t grouped_gemm_workspace_bytes(const moe_shape& s, const moe_layout& l, int64_t N, int64_t Kd) {
-  return 256;
+  return 16;  // the tile counter
+}
+
+bool grouped_gemm_counts(const moe_shape& s, const moe_layout& l, int64_t features) {
+  return (l.capacity / BN + s.E) * ((features + BM - 1) / BM) < (int64_t(1) << 30);
 }
 
 cudaError_t launch_grouped_gemm(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
-  return grouped_gemm_tc_takes(dir, g) ? launch_grouped_gemm_tc(dir, g, st) : launch_grouped_gemm_any(dir, g, st);
+  const bool copies = g.cap > 0 && g.N % 8 == 0 && g.Kd % 8 == 0 && aligned16(g.a) && aligned16(g.b) &&
+                      aligned16(g.out) && aligned16(g.addend) &&
+                      (g.cap == 1 || (g.sa % 8 == 0 && (dir == kWeight ? g.sb % 8 == 0 : g.sout % 8 == 0)));
+  if (g.dtype == MOE_ELEM_BF16)
+    return copies ? run<__nv_bfloat16, false>(dir, g, st) : run<__nv_bfloat16, true>(dir, g, st);
+  return copies ? run<__half, false>(dir, g, st) : run<__half, true>(dir, g, st);
 }
 
 }  // namespace moe

@@ -26,14 +26,9 @@ struct GroupedGemm {
 };
 
 size_t grouped_gemm_workspace_bytes(const moe_shape& s, const moe_layout& l, int64_t N, int64_t Kd);
+// Whether the tiles of the rows' products can be counted (what does not fit is far
+// beyond any memory).
+bool grouped_gemm_counts(const moe_shape& s, const moe_layout& l, int64_t features);
 cudaError_t launch_grouped_gemm(GemmDir dir, const GroupedGemm& g, cudaStream_t st);
-
-// Matrices and rows that TMA copies take: 16-byte aligned, N, Kd and strides
-// multiples of 8 (grouped_gemm_tc.cu).
-bool grouped_gemm_tc_takes(GemmDir dir, const GroupedGemm& g);
-cudaError_t launch_grouped_gemm_tc(GemmDir dir, const GroupedGemm& g, cudaStream_t st);
-
-// Any size, stride and alignment (grouped_gemm_any.cu).
-cudaError_t launch_grouped_gemm_any(GemmDir dir, const GroupedGemm& g, cudaStream_t st);
 
 }  // namespace moe
