@@ -247,48 +247,51 @@ struct Eight {
   uint4 lo, hi;
 };
 
-// Elements [0, n) at p into e, n maybe below 1 or above 8; [begin, end) is the matrix.
-// Returns true where e.lo holds them in place already.
-MOE_DEVICE bool load_eight(Eight& e, const uint16_t* p, int n, const uint16_t* begin, const uint16_t* end) {
-  e.lo = e.hi = make_uint4(0, 0, 0, 0);
-  if (n <= 0) return true;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p), piece = at & ~uintptr_t(15);
-  const bool two = at != piece;
-  if (piece >= reinterpret_cast<uintptr_t>(begin) && piece + (two ? 32 : 16) <= reinterpret_cast<uintptr_t>(end)) {
-    e.lo = *reinterpret_cast<const uint4*>(piece);
-    if (two) e.hi = *reinterpret_cast<const uint4*>(piece + 16);
-    return false;
-  }
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int k = 0; k < 8; k++)
-    if (k < n) w[k / 2] |= (uint32_t)p[k] << (16 * (k & 1));
-  e.lo = make_uint4(w[0], w[1], w[2], w[3]);
-  return true;
+// Whether the pieces that hold p's eight elements are inside the matrix [begin, end).
+MOE_DEVICE bool inside(const uint16_t* p, const uint16_t* begin, const uint16_t* end) {
+  const uintptr_t piece = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+  return piece >= reinterpret_cast<uintptr_t>(begin) && piece + 32 <= reinterpret_cast<uintptr_t>(end);
 }
 
-// The eight elements from byte `from` of the pieces on; zeros from the n-th on.
-MOE_DEVICE uint4 shifted(const Eight& e, uint32_t from, int n) {
+// Elements [0, n) of the eight at p one by one, as pieces that hold them at p's place.
+MOE_DEVICE void load_singly(Eight& e, const uint16_t* p, int n) {
+  const uint32_t from = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15) / 2;
+  uint32_t w[8] = {};
+#pragma unroll
+  for (int i = 0; i < 15; i++) {
+    const int k = i - (int)from;
+    if (k >= 0 && k < 8 && k < n) w[i / 2] |= (uint32_t)p[k] << (16 * (i & 1));
+  }
+  e.lo = make_uint4(w[0], w[1], w[2], w[3]);
+  e.hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// The eight elements from byte `from` of the pieces on.
+MOE_DEVICE uint4 shifted(const Eight& e, uint32_t from) {
   uint32_t w[8] = {e.lo.x, e.lo.y, e.lo.z, e.lo.w, e.hi.x, e.hi.y, e.hi.z, e.hi.w};
-  if (from & 4) {
+  const bool one = from & 4, two = from & 8;
 #pragma unroll
-    for (int i = 0; i < 7; i++) w[i] = w[i + 1];
-  }
-  if (from & 8) {
+  for (int i = 0; i < 7; i++) w[i] = one ? w[i + 1] : w[i];
 #pragma unroll
-    for (int i = 0; i < 6; i++) w[i] = w[i + 2];
-  }
+  for (int i = 0; i < 5; i++) w[i] = two ? w[i + 2] : w[i];
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    w[i] = __funnelshift_r(w[i], w[i + 1], (from & 2) * 8);
-    if (n < 8) w[i] = 2 * i >= n ? 0u : 2 * i + 1 >= n ? w[i] & 0xffffu : w[i];
-  }
+  for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(w[i], w[i + 1], (from & 2) * 8);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Zeros from the n-th element on.
+MOE_DEVICE uint4 first_of(uint4 v, int n) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) w[i] = 2 * i >= n ? 0u : 2 * i + 1 >= n ? w[i] & 0xffffu : w[i];
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // A CTA's half of an operand, 64 of the contraction after 64: 128 rows of 64
 // elements in shared memory, of which a thread has eight elements of every 32nd.
 // KMAJOR: they are rows of the operand; otherwise two runs of 64 columns along 64 rows.
+// From row to row of a thread and from stage to stage lies a multiple of 64 elements,
+// so that a thread's elements keep their place in their pieces.
 template <bool KMAJOR>
 struct Half {
   const uint16_t* p;  // this thread's first elements of the next stage
@@ -319,20 +322,47 @@ struct Half {
     return valid > (KMAJOR ? 32 * i : 32 * (i & 1)) ? (KMAJOR ? n : n - 64 * (i >> 1)) : 0;
   }
 
-  MOE_DEVICE void load(Eight (&e)[4], uint32_t& in_place) const {
-    in_place = 0;
+  // Loads a stage's; true where a warp has whole eights alone.
+  MOE_DEVICE bool load(Eight (&e)[4]) const {
+    const bool eights = KMAJOR ? n >= 8 && valid > 32 * (count - 1) : n >= 72 && valid > 32;
+    // (pieces reach up to seven elements before the first and eight behind the last)
+    const bool whole = __all_sync(0xffffffffu, eights && p - begin >= 7 && end - at(KMAJOR ? count - 1 : 3) >= 16);
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-      if (i < count && load_eight(e[i], at(i), have(i), begin, end)) in_place |= 1u << i;
+      for (int i = 0; i < 4; i++)
+        if (i < count) {
+          const uint4* piece = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at(i)) & ~uintptr_t(15));
+          e[i].lo = piece[0];
+          e[i].hi = piece[1];
+        }
+      return true;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      e[i].lo = e[i].hi = make_uint4(0, 0, 0, 0);
+      if (i < count && have(i) > 0) {
+        if (inside(at(i), begin, end)) {
+          const uint4* piece = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at(i)) & ~uintptr_t(15));
+          e[i].lo = piece[0];
+          e[i].hi = piece[1];
+        } else {
+          load_singly(e[i], at(i), have(i));
+        }
+      }
+    }
+    return false;
   }
 
-  MOE_DEVICE void store(uint8_t* to, const Eight (&e)[4], uint32_t in_place, int t) const {
+  MOE_DEVICE void store(uint8_t* to, const Eight (&e)[4], bool whole, int t) const {
     const int q = t & 7, j = t >> 3;
+    const uint32_t from = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    to += j * 128 + ((q ^ (j & 7)) * 16);
 #pragma unroll
     for (int i = 0; i < 4; i++)
       if (i < count) {
-        const uint32_t from = in_place >> i & 1 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(at(i)) & 15);
-        *reinterpret_cast<uint4*>(to + (j + 32 * i) * 128 + ((q ^ (j & 7)) * 16)) = shifted(e[i], from, have(i));
+        uint4 v = shifted(e[i], from);
+        if (!whole) v = first_of(v, have(i));
+        *reinterpret_cast<uint4*>(to + 32 * i * 128) = v;
       }
   }
 
@@ -598,22 +628,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         b.begin_tile(p.b, p.b_end, p.sb, row, min(half, ti.end - row), 0, p.contraction, half, at);
       }
       Eight ea[4], eb[4];
-      uint32_t ia, ib;
-      if (ti.blocks) a.load(ea, ia), b.load(eb, ib);
+      bool wa = false, wb = false;  // whole eights
+      if (ti.blocks) wa = a.load(ea), wb = b.load(eb);
       for (int kb = 0; kb < ti.blocks; kb++) {
         if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status))) {
           ok = 0;
           break;
         }
         uint8_t* to = smem + (size_t)stage * kStageBytes;
-        a.store(to, ea, ia, at);
-        b.store(to + kOperand, eb, ib, at);
+        const bool more = kb + 1 < ti.blocks;
+        a.store(to, ea, wa, at);
+        a.advance();
+        if (more) wa = a.load(ea);
+        b.store(to + kOperand, eb, wb, at);
+        b.advance();
+        if (more) wb = b.load(eb);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_full[stage]), 0));
-        a.advance();
-        b.advance();
-        if (kb + 1 < ti.blocks) a.load(ea, ia), b.load(eb, ib);
+        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&s_full[stage]), 0));
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
@@ -643,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_full[s]), 0));
+          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&s_full[s]), 0));
         }
         stage = (stage + nkb) % kStages;
       }

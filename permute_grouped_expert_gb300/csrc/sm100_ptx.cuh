@@ -372,6 +372,12 @@ MOE_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* 
   }
 }
 
+// Arrive on an mbarrier of the cluster, behind this thread's writes to its own
+// CTA's shared memory.
+MOE_DEVICE void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Arrive on an mbarrier of the cluster without ordering this thread's memory
 // accesses: an arrival that releases at cluster scope waits until all stores before
 // it, global ones too, have arrived.
