@@ -291,87 +291,78 @@ MOE_DEVICE uint4 first_of(uint4 v, int n) {
 // elements in shared memory, of which a thread has eight elements of every 32nd.
 // KMAJOR: they are rows of the operand; otherwise two runs of 64 columns along 64 rows.
 // From row to row of a thread and from stage to stage lies a multiple of 64 elements,
-// so that a thread's elements keep their place in their pieces.
+// so that a thread's elements keep their place in their pieces.  Beyond the end of the
+// contraction are zeros; rows and columns beyond the operand's give results that are
+// not stored, whatever is there.
 template <bool KMAJOR>
 struct Half {
-  const uint16_t* p;  // this thread's first elements of the next stage
+  const uint8_t* piece;  // the piece where this thread's first elements of the next stage start
   const uint16_t *begin, *end;
-  int64_t stride;
-  int n;      // elements from p on that are in the operand's columns
-  int valid;  // rows from this thread's first on: of the operand (KMAJOR), or of the contraction that are left
-  int count;  // rows in shared memory, of 32 each
+  int64_t row32;  // bytes from a row to the 32nd behind
+  uint32_t from;  // byte of the piece
+  int k;          // of the contraction left: elements from this thread's first on, or rows
+  int other;      // of the other side: rows (KMAJOR) or columns
+  int count;      // rows in shared memory, of 32 each
 
   // KMAJOR: rows [row, row + rows) of `cols` elements, `used` in shared memory;
   // otherwise columns from `col` on of `cols`, along rows [row, row + rows).
   MOE_DEVICE void begin_tile(const uint16_t* base, const uint16_t* stop, int64_t apart, int64_t row, int rows, int col,
                              int cols, int used, int t) {
     const int c = col + (t & 7) * 8, j = t >> 3;
-    p = base + (row + j) * apart + c;
+    const uint16_t* p = base + (row + j) * apart + c;
+    from = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    piece = reinterpret_cast<const uint8_t*>(p) - from;
     begin = base;
     end = stop;
-    stride = apart;
-    n = cols - c;
-    valid = rows - j;
+    row32 = 64 * apart;
+    k = KMAJOR ? cols - c : rows - j;
+    other = KMAJOR ? rows - j : cols - c;
     count = (used + 31) / 32;
   }
 
-  MOE_DEVICE const uint16_t* at(int i) const {
-    return KMAJOR ? p + 32 * i * stride : p + 32 * (i & 1) * stride + 64 * (i >> 1);
-  }
-  MOE_DEVICE int have(int i) const {
-    return valid > (KMAJOR ? 32 * i : 32 * (i & 1)) ? (KMAJOR ? n : n - 64 * (i >> 1)) : 0;
-  }
+  MOE_DEVICE const uint8_t* at(int i) const { return KMAJOR ? piece + i * row32 : piece + (i & 1) * row32 + 128 * (i >> 1); }
+  MOE_DEVICE bool there(int i) const { return i < count && other > (KMAJOR ? 32 * i : 64 * (i >> 1)); }
 
-  // Loads a stage's; true where a warp has whole eights alone.
+  // Loads a stage's; true where a warp's are all of the contraction.
   MOE_DEVICE bool load(Eight (&e)[4]) const {
-    const bool eights = KMAJOR ? n >= 8 && valid > 32 * (count - 1) : n >= 72 && valid > 32;
-    // (pieces reach up to seven elements before the first and eight behind the last)
-    const bool whole = __all_sync(0xffffffffu, eights && p - begin >= 7 && end - at(KMAJOR ? count - 1 : 3) >= 16);
-    if (whole) {
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (i < count) {
-          const uint4* piece = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at(i)) & ~uintptr_t(15));
-          e[i].lo = piece[0];
-          e[i].hi = piece[1];
-        }
-      return true;
-    }
+    // the pieces from the first row's to the last's are inside the matrix
+    const bool safe = piece >= reinterpret_cast<const uint8_t*>(begin) &&
+                      at(KMAJOR ? count - 1 : 3) + 32 <= reinterpret_cast<const uint8_t*>(end);
+    const bool whole = __all_sync(0xffffffffu, safe && (KMAJOR ? k >= 8 : k > 32));
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      e[i].lo = e[i].hi = make_uint4(0, 0, 0, 0);
-      if (i < count && have(i) > 0) {
-        if (inside(at(i), begin, end)) {
-          const uint4* piece = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at(i)) & ~uintptr_t(15));
-          e[i].lo = piece[0];
-          e[i].hi = piece[1];
-        } else {
-          load_singly(e[i], at(i), have(i));
-        }
+      const uint4* q = reinterpret_cast<const uint4*>(at(i));
+      if (whole) {
+        if (there(i)) e[i].lo = q[0], e[i].hi = q[1];
+        continue;
       }
+      e[i].lo = e[i].hi = make_uint4(0, 0, 0, 0);
+      const int n = KMAJOR ? min(k, 8) : k > 32 * (i & 1) ? min(other - 64 * (i >> 1), 8) : 0;
+      if (!there(i) || n <= 0) continue;
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(at(i) + from);
+      if (inside(p, begin, end))
+        e[i].lo = q[0], e[i].hi = q[1];
+      else
+        load_singly(e[i], p, n);
     }
-    return false;
+    return whole;
   }
 
   MOE_DEVICE void store(uint8_t* to, const Eight (&e)[4], bool whole, int t) const {
     const int q = t & 7, j = t >> 3;
-    const uint32_t from = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
     to += j * 128 + ((q ^ (j & 7)) * 16);
 #pragma unroll
     for (int i = 0; i < 4; i++)
       if (i < count) {
         uint4 v = shifted(e[i], from);
-        if (!whole) v = first_of(v, have(i));
+        if (KMAJOR && !whole) v = first_of(v, k);
         *reinterpret_cast<uint4*>(to + 32 * i * 128) = v;
       }
   }
 
   MOE_DEVICE void advance() {
-    p += KMAJOR ? BK : BK * stride;
-    if (KMAJOR)
-      n -= BK;
-    else
-      valid -= BK;
+    piece += KMAJOR ? 2 * BK : 2 * row32;
+    k -= BK;
   }
 };
 
