@@ -37,7 +37,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kPieceWarps = 8;  // that load what TMA cannot
+constexpr int kPieceWarps = 8;  // that bring unaligned operands into place
 template <GemmDir DIR, bool PIECES>
 constexpr int kThreads = 256 + (PIECES ? 32 * kPieceWarps : DIR == kWeight ? 32 : 0);
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
@@ -46,7 +46,19 @@ constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
 template <GemmDir DIR>
 constexpr int kSlotsOf = DIR == kWeight ? 4 : 2;
 template <GemmDir DIR, bool PIECES>
-constexpr int kStagesOf = DIR == kWeight && !PIECES ? 5 : 6;
+constexpr int kStagesOf = PIECES ? 3 : DIR == kWeight ? 5 : 6;
+// PIECES: stages as they lie in memory, ahead of those; bytes of a row (64 or 128
+// elements that start anywhere in their first piece of 16 bytes), of the rows that
+// are eight apart, and of an operand.
+template <GemmDir DIR>
+constexpr int kRawOf = DIR == kWeight ? 2 : 3;
+template <bool KMAJOR>
+constexpr uint32_t kRawRow = KMAJOR ? 144 : 272;
+template <bool KMAJOR>
+constexpr uint32_t kRawRows = KMAJOR ? 16 : 8;
+template <bool KMAJOR>
+constexpr uint32_t kRawEighth = kRawRows<KMAJOR> * kRawRow<KMAJOR>;
+constexpr uint32_t kRawOperand = 8 * kRawEighth<true>;
 constexpr int kBand = 8;                                // tiles of a band that share their operands in L2
 constexpr uint32_t kOperand = 128 * BK * 2;             // a CTA's half of an operand: 16 KB
 constexpr uint32_t kBox = 64 * BK * 2;                  // a box of an operand that is not K-major
@@ -57,6 +69,7 @@ constexpr uint32_t kOutBytes = 32 * 128;                // kWeight: a warp's 32 
 constexpr int kTurn = 33;                               // and in pieces: a row of 32 results and a word between
 template <GemmDir DIR, bool PIECES>
 constexpr size_t kDynSmem = 1024 + (size_t)kStagesOf<DIR, PIECES> * kStageBytes +
+                            (PIECES ? 2 * kRawOf<DIR> * kRawOperand : 0) +
                             (DIR != kWeight ? 0 : PIECES ? 4 * 32 * kTurn * 4 : 8 * kOutBytes);
 
 struct TcParams {
@@ -73,8 +86,7 @@ struct TcParams {
   int mt;                     // tiles of 256 features (kWeight: of N)
   int kt;                     // kWeight: tiles of 256 of Kd
   bool a_groups, b_groups;    // the operand's map has columns in groups of 64
-  // PIECES: the operands themselves, the bytes that hold them, strides of their rows
-  const uint16_t *a, *b, *a_end, *b_end;
+  const uint16_t *a, *b;      // PIECES: the operands, strides of their rows
   int64_t sa, sb;
 };
 
@@ -96,12 +108,13 @@ struct alignas(16) Tile {
   int pad;
 };
 
-// Maps of the second operand: boxes of 16, 32, .. 128 rows, so that a tile's half of
-// a stage is one copy whatever its rows (as copies of 16 rows, 8192 x 8192 x 8192
-// over experts of about 1024 rows took 1031 us where whole tiles took 717); kWeight:
-// the first alone.
-struct RowMaps {
-  CUtensorMap of[8];
+// Maps of the operands.  The second's have boxes of 16, 32, .. 128 rows, so that a
+// tile's half of a stage is one copy whatever its rows (as copies of 16 rows, 8192 x
+// 8192 x 8192 over experts of about 1024 rows took 1031 us where whole tiles took
+// 717); kWeight and the first operand: one.  PIECES: the rows r of either with r % 8
+// equal to the index.
+struct Maps {
+  CUtensorMap a[8], b[8], out;
 };
 
 // Tiles of an expert in bands of kBand along one side, the other side outermost in
@@ -238,37 +251,17 @@ MOE_DEVICE void settle(uint64_t ns) {
   while (globaltimer_ns() - t0 < ns) __nanosleep(1000);
 }
 
-// PIECES: operands that TMA does not take (odd widths, rows that start anywhere).
-// Eight elements of a row are the aligned 16-byte pieces that hold them, shifted into
-// place on their way to shared memory; a thread has a stage's loads on their way
-// while it waits for room.  Neighbours in the pieces, and what is beyond the rows or
-// the columns of the operand, are left out or zeros.
-struct Eight {
-  uint4 lo, hi;
-};
+// PIECES: operands whose rows TMA does not take one after another (odd widths, rows
+// that start anywhere).  Rows that are eight apart lie a multiple of 16 bytes apart
+// whatever the stride, so that eight copies a stage bring an operand's rows to shared
+// memory as they lie; from there each eight elements are shifted into the place that
+// the MMA reads.  (Loaded by threads, a stage ahead, 8191 x 8191 x 8192 took 2.9 ms,
+// most of it in the loads' issue.)  Beyond the end of the contraction are zeros; rows
+// and columns beyond the operand's give results that are not stored, whatever is there.
 
-// Whether the pieces that hold p's eight elements are inside the matrix [begin, end).
-MOE_DEVICE bool inside(const uint16_t* p, const uint16_t* begin, const uint16_t* end) {
-  const uintptr_t piece = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
-  return piece >= reinterpret_cast<uintptr_t>(begin) && piece + 32 <= reinterpret_cast<uintptr_t>(end);
-}
-
-// Elements [0, n) of the eight at p one by one, as pieces that hold them at p's place.
-MOE_DEVICE void load_singly(Eight& e, const uint16_t* p, int n) {
-  const uint32_t from = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15) / 2;
-  uint32_t w[8] = {};
-#pragma unroll
-  for (int i = 0; i < 15; i++) {
-    const int k = i - (int)from;
-    if (k >= 0 && k < 8 && k < n) w[i / 2] |= (uint32_t)p[k] << (16 * (i & 1));
-  }
-  e.lo = make_uint4(w[0], w[1], w[2], w[3]);
-  e.hi = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
-// The eight elements from byte `from` of the pieces on.
-MOE_DEVICE uint4 shifted(const Eight& e, uint32_t from) {
-  uint32_t w[8] = {e.lo.x, e.lo.y, e.lo.z, e.lo.w, e.hi.x, e.hi.y, e.hi.z, e.hi.w};
+// The eight elements from byte `from` of two pieces of 16 bytes on.
+MOE_DEVICE uint4 shifted(uint4 lo, uint4 hi, uint32_t from) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   const bool one = from & 4, two = from & 8;
 #pragma unroll
   for (int i = 0; i < 7; i++) w[i] = one ? w[i + 1] : w[i];
@@ -287,95 +280,65 @@ MOE_DEVICE uint4 first_of(uint4 v, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A CTA's half of an operand, 64 of the contraction after 64: 128 rows of 64
-// elements in shared memory, of which a thread has eight elements of every 32nd.
-// KMAJOR: they are rows of the operand; otherwise two runs of 64 columns along 64 rows.
-// From row to row of a thread and from stage to stage lies a multiple of 64 elements,
-// so that a thread's elements keep their place in their pieces.  Beyond the end of the
-// contraction are zeros; rows and columns beyond the operand's give results that are
-// not stored, whatever is there.
+// A CTA's half of an operand in place: 128 rows of 64 elements in shared memory, of
+// which a thread has eight elements of every 32nd.  KMAJOR: they are rows of the
+// operand; otherwise two runs of 64 columns along 64 rows.  From row to row of a
+// thread and from stage to stage lie multiples of eight rows and of 64 elements, so
+// that a thread's elements keep their place in their pieces.
 template <bool KMAJOR>
 struct Half {
-  const uint8_t* piece;  // the piece where this thread's first elements of the next stage start
-  const uint16_t *begin, *end;
-  int64_t row32;  // bytes from a row to the 32nd behind
+  uint32_t raw;   // where this thread's first piece is in a stage
   uint32_t from;  // byte of the piece
   int k;          // of the contraction left: elements from this thread's first on, or rows
-  int other;      // of the other side: rows (KMAJOR) or columns
   int count;      // rows in shared memory, of 32 each
 
-  // KMAJOR: rows [row, row + rows) of `cols` elements, `used` in shared memory;
-  // otherwise columns from `col` on of `cols`, along rows [row, row + rows).
-  MOE_DEVICE void begin_tile(const uint16_t* base, const uint16_t* stop, int64_t apart, int64_t row, int rows, int col,
-                             int cols, int used, int t) {
-    const int c = col + (t & 7) * 8, j = t >> 3;
-    const uint16_t* p = base + (row + j) * apart + c;
-    from = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
-    piece = reinterpret_cast<const uint8_t*>(p) - from;
-    begin = base;
-    end = stop;
-    row32 = 64 * apart;
-    k = KMAJOR ? cols - c : rows - j;
-    other = KMAJOR ? rows - j : cols - c;
+  // KMAJOR: rows from `row` on, `used` of them, along k elements; otherwise columns
+  // from `col` on, along k rows from `row` on.
+  MOE_DEVICE void begin_tile(const uint16_t* base, int64_t stride, int64_t row, int col, int contraction, int used, int t) {
+    const int q = t & 7, j = t >> 3, eighth = (int)((row + j) & 7);
+    from = (uint32_t)(reinterpret_cast<uintptr_t>(base + (row + j) * stride) & 15);
+    raw = eighth * kRawEighth<KMAJOR> + (uint32_t)(((row + j) >> 3) - ((row - eighth + 7) >> 3)) * kRawRow<KMAJOR> + q * 16;
+    k = contraction - (KMAJOR ? q * 8 : j);
     count = (used + 31) / 32;
   }
 
-  MOE_DEVICE const uint8_t* at(int i) const { return KMAJOR ? piece + i * row32 : piece + (i & 1) * row32 + 128 * (i >> 1); }
-  MOE_DEVICE bool there(int i) const { return i < count && other > (KMAJOR ? 32 * i : 64 * (i >> 1)); }
-
-  // Loads a stage's; true where a warp's are all of the contraction.
-  MOE_DEVICE bool load(Eight (&e)[4]) const {
-    // the pieces from the first row's to the last's are inside the matrix
-    const bool safe = piece >= reinterpret_cast<const uint8_t*>(begin) &&
-                      at(KMAJOR ? count - 1 : 3) + 32 <= reinterpret_cast<const uint8_t*>(end);
-    const bool whole = __all_sync(0xffffffffu, safe && (KMAJOR ? k >= 8 : k > 32));
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint4* q = reinterpret_cast<const uint4*>(at(i));
-      if (whole) {
-        if (there(i)) e[i].lo = q[0], e[i].hi = q[1];
-        continue;
-      }
-      e[i].lo = e[i].hi = make_uint4(0, 0, 0, 0);
-      const int n = KMAJOR ? min(k, 8) : k > 32 * (i & 1) ? min(other - 64 * (i >> 1), 8) : 0;
-      if (!there(i) || n <= 0) continue;
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(at(i) + from);
-      if (inside(p, begin, end))
-        e[i].lo = q[0], e[i].hi = q[1];
-      else
-        load_singly(e[i], p, n);
-    }
-    return whole;
-  }
-
-  MOE_DEVICE void store(uint8_t* to, const Eight (&e)[4], bool whole, int t) const {
+  MOE_DEVICE void shift(uint8_t* to, const uint8_t* stage, int t) {
     const int q = t & 7, j = t >> 3;
     to += j * 128 + ((q ^ (j & 7)) * 16);
+    const uint8_t* at = stage + raw;
+    // a warp's elements are all of the contraction
+    const bool whole = __all_sync(0xffffffffu, KMAJOR ? k >= 8 : k > 32);
 #pragma unroll
     for (int i = 0; i < 4; i++)
       if (i < count) {
-        uint4 v = shifted(e[i], from);
-        if (KMAJOR && !whole) v = first_of(v, k);
+        const uint4* piece =
+            reinterpret_cast<const uint4*>(at + (KMAJOR ? 4 * i * kRawRow<true> : 4 * (i & 1) * kRawRow<false> + 128 * (i >> 1)));
+        uint4 v = shifted(piece[0], piece[1], from);
+        if (!whole) v = first_of(v, KMAJOR ? k : k > 32 * (i & 1) ? 8 : 0);
         *reinterpret_cast<uint4*>(to + 32 * i * 128) = v;
       }
-  }
-
-  MOE_DEVICE void advance() {
-    piece += KMAJOR ? 2 * BK : 2 * row32;
     k -= BK;
   }
 };
+
+// Copies of the rows of a stage, one for each that are eight apart.
+template <bool KMAJOR>
+MOE_DEVICE void copy_eighths(uint8_t* to, const CUtensorMap* maps, int64_t row, int col, uint64_t* bar) {
+#pragma unroll 1
+  for (int r = 0; r < 8; r++)
+    tma_load_2d(to + r * kRawEighth<KMAJOR>, maps + r, col, (int)((row - r + 7) >> 3), bar);
+}
 
 // T: 16-bit type of the operands; OUT: of the result; PIECES: operands of any
 // alignment, without the maps.
 template <GemmDir DIR, typename T, typename OUT, bool PIECES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES>, 1)
-    grouped_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
-                           const __grid_constant__ CUtensorMap tm_out, TcParams p) {
-  constexpr int kStages = kStagesOf<DIR, PIECES>, kSlots = kSlotsOf<DIR>;
+    grouped_gemm_kernel(const __grid_constant__ Maps maps, TcParams p) {
+  constexpr int kStages = kStagesOf<DIR, PIECES>, kSlots = kSlotsOf<DIR>, kRaw = PIECES ? kRawOf<DIR> : 1;
   constexpr bool kW = DIR == kWeight, kAmn = DIR != kForward, kBmn = kW;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tail[kStages], s_tfull[2], s_tempty[2];
+  __shared__ __align__(8) uint64_t s_raw[kRaw], s_raw_free[kRaw];  // PIECES, each CTA's own
   __shared__ __align__(8) uint64_t s_have[kSlots], s_free[kSlots], s_drain;
   __shared__ Tile s_tile[kSlots];
   __shared__ uint32_t s_tmem;
@@ -404,14 +367,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     for (int s = 0; s < kSlots; s++) {
       mbar_init(&s_have[s], 1);
       // MMA, 4 epilogue warps a CTA, and its producers (kWeight: and warp 8)
-      mbar_init(&s_free[s], 1 + 2 * (4 + (PIECES ? kPieceWarps : kW ? 3 : 2)));  // on the leader: every reader of both CTAs
+      mbar_init(&s_free[s], 1 + 2 * (6 + (PIECES ? kPieceWarps : kW)));  // on the leader: every reader of both CTAs
+    }
+    for (int s = 0; s < kRaw; s++) {
+      mbar_init(&s_raw[s], 1);
+      mbar_init(&s_raw_free[s], kPieceWarps);
     }
     mbar_init(&s_drain, 1);
     fence_barrier_init();
-    if (!PIECES) {
-      tma_prefetch_desc(&tm_a);
-      tma_prefetch_desc(&tm_b.of[0]);
-    }
+    tma_prefetch_desc(&maps.a[0]);
+    tma_prefetch_desc(&maps.b[0]);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, kTmemCols);
   if (warp == 2 && rank == 0) make_order<kW>(s_order, p, kW ? p.mt * p.kt : p.mt);
@@ -446,9 +411,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     return ti.e >= 0;
   };
 
-  if (warp == 0 || warp == 3) {
+  if (PIECES && (warp == 0 || warp == 3)) {
+    // --------------------------------- producers of the operands as they lie
+    if (elect_one_lane()) {
+      const bool first = warp == 0;  // of the first operand; it announces both's bytes
+      constexpr uint32_t kBytes = 8 * (kRawEighth<DIR == kForward> + kRawEighth<!kW>);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0; ok; i++) {
+        Tile ti;
+        if (!take_tile(i, ti)) break;
+        const int f0 = (first ? ti.m * BM : ti.n * BN) + (int)rank * 128;
+        const int64_t w = (int64_t)ti.e * p.N;
+        for (int kb = 0; kb < ti.blocks; kb++) {
+          if (!mbar_wait(&s_raw_free[stage], phase ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* to = smem + (size_t)kStages * kStageBytes + (size_t)(2 * stage + (first ? 0 : 1)) * kRawOperand;
+          const int k0 = kb * BK;
+          if (first) {
+            mbar_arrive_expect_tx(&s_raw[stage], kBytes);
+            if (DIR == kForward)
+              copy_eighths<true>(to, maps.a, w + f0, k0, &s_raw[stage]);
+            else
+              copy_eighths<false>(to, maps.a, (kW ? ti.row : w) + k0, f0, &s_raw[stage]);
+          } else if (kW) {
+            copy_eighths<false>(to, maps.b, ti.row + k0, f0, &s_raw[stage]);
+          } else {
+            copy_eighths<true>(to, maps.b, ti.row + (int)rank * (ti.cols / 2), k0, &s_raw[stage]);
+          }
+          if (++stage == kRaw) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) settle(2000000);  // 2 ms: far longer than any single copy takes
+    }
+  } else if (warp == 0 || warp == 3) {
     // ------------------------------------------------------- TMA producers
-    if (!PIECES && elect_one_lane()) {
+    if (elect_one_lane()) {
       const bool first = warp == 0;  // of the first operand; it announces both's bytes
       int stage = 0;
       uint32_t phase = 0;
@@ -464,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         // first feature of this CTA, or kWeight's second operand: its first column
         const int f0 = (first ? ti.m * BM : ti.n * BN) + (int)rank * 128;
         const int row = ti.row + (int)rank * half;
-        const CUtensorMap* map = first ? &tm_a : kW ? &tm_b.of[0] : &tm_b.of[half / 16 - 1];
+        const CUtensorMap* map = first ? maps.a : kW ? maps.b : maps.b + half / 16 - 1;
         const uint32_t bytes = kW ? kStageBytes : kOperand + (uint32_t)half * BK * 2;
         const bool groups = first ? p.a_groups : p.b_groups;
         for (int kb = 0; kb < nkb; kb++) {
@@ -596,10 +600,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
       }
     }
   } else if (PIECES && warp >= 8) {
-    // ---------------------------------------------- producers without TMA
+    // ------------------------------------------ operands brought into place
     const int at = threadIdx.x - 256;
-    int stage = 0;
-    uint32_t phase = 0;
+    int stage = 0, raw = 0;
+    uint32_t phase = 0, raw_phase = 0;
     for (int i = 0, ok = 1; ok; i++) {
       Tile ti;
       if (!take_tile_warp(i, ti)) break;
@@ -607,36 +611,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
       Half<DIR == kForward> a;
       Half<!kW> b;
       if (kW) {
-        a.begin_tile(p.a, p.a_end, p.sa, ti.row, ti.end - ti.row, f0, p.N, 128, at);
-        b.begin_tile(p.b, p.b_end, p.sb, ti.row, ti.end - ti.row, c0, p.Kd, 128, at);
+        a.begin_tile(p.a, p.sa, ti.row, f0, ti.end - ti.row, 128, at);
+        b.begin_tile(p.b, p.sb, ti.row, c0, ti.end - ti.row, 128, at);
       } else {
         const int64_t w = (int64_t)ti.e * p.N;
         if (DIR == kForward)
-          a.begin_tile(p.a, p.a_end, p.sa, w + f0, p.N - f0, 0, p.Kd, 128, at);
+          a.begin_tile(p.a, p.sa, w + f0, 0, p.contraction, 128, at);
         else
-          a.begin_tile(p.a, p.a_end, p.sa, w, p.N, f0, p.Kd, 128, at);
-        const int row = ti.row + (int)rank * half;
-        b.begin_tile(p.b, p.b_end, p.sb, row, min(half, ti.end - row), 0, p.contraction, half, at);
+          a.begin_tile(p.a, p.sa, w, f0, p.contraction, 128, at);
+        b.begin_tile(p.b, p.sb, ti.row + (int)rank * half, 0, p.contraction, half, at);
       }
-      Eight ea[4], eb[4];
-      bool wa = false, wb = false;  // whole eights
-      if (ti.blocks) wa = a.load(ea), wb = b.load(eb);
       for (int kb = 0; kb < ti.blocks; kb++) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status))) {
+        const bool both = mbar_wait(&s_raw[raw], raw_phase, abort_flag, p.status) &&
+                          mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status);
+        if (!__all_sync(0xffffffffu, both)) {
           ok = 0;
           break;
         }
         uint8_t* to = smem + (size_t)stage * kStageBytes;
-        const bool more = kb + 1 < ti.blocks;
-        a.store(to, ea, wa, at);
-        a.advance();
-        if (more) wa = a.load(ea);
-        b.store(to + kOperand, eb, wb, at);
-        b.advance();
-        if (more) wb = b.load(eb);
+        const uint8_t* from = smem + (size_t)kStages * kStageBytes + (size_t)(2 * raw) * kRawOperand;
+        a.shift(to, from, at);
+        b.shift(to + kOperand, from + kRawOperand, at);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&s_full[stage]), 0));
+        if (lane == 0) {
+          mbar_arrive(&s_raw_free[raw]);
+          mbar_arrive_remote(mapa_shared(smem_u32(&s_full[stage]), 0));
+        }
+        if (++raw == kRaw) {
+          raw = 0;
+          raw_phase ^= 1;
+        }
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
@@ -674,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
   } else {
     // ---------------------------------------------------------- epilogue
     const int lane_base = 32 * (warp & 3);
-    uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (size_t)(warp & 3) * (PIECES ? 32 * kTurn * 4 : 2 * kOutBytes);  // kWeight
+    uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (PIECES ? 2 * kRaw * kRawOperand : 0) + (size_t)(warp & 3) * (PIECES ? 32 * kTurn * 4 : 2 * kOutBytes);  // kWeight
     int out_at = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -763,7 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&tm_out, buf, ti.n * BN + c, f_warp, ti.e);
+            tma_store_3d(&maps.out, buf, ti.n * BN + c, f_warp, ti.e);
             bulk_commit();
           }
           out_at ^= 1;
@@ -823,8 +828,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <GemmDir DIR, typename T, typename OUT, bool PIECES>
-cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& to, TcParams p, int64_t most_tiles,
-                   cudaStream_t st) {
+cudaError_t launch(const Maps& maps, TcParams p, int64_t most_tiles, cudaStream_t st) {
   constexpr size_t smem = kDynSmem<DIR, PIECES>;
   static int at_once[PerDeviceOnce::kMaxDevices];
   static PerDeviceOnce once;
@@ -852,7 +856,7 @@ cudaError_t launch(const CUtensorMap& ta, const RowMaps& tb, const CUtensorMap& 
   // one or two tiles each: in turn, without the counter, whose clearing takes 4 us
   if (most_tiles <= 2 * clusters) p.next = nullptr;
   if (p.next && (e = cudaMemsetAsync(p.next, 0, sizeof(int32_t), st)) != cudaSuccess) return e;
-  grouped_gemm_kernel<DIR, T, OUT, PIECES><<<(unsigned)(2 * clusters), kThreads<DIR, PIECES>, smem, st>>>(ta, tb, to, p);
+  grouped_gemm_kernel<DIR, T, OUT, PIECES><<<(unsigned)(2 * clusters), kThreads<DIR, PIECES>, smem, st>>>(maps, p);
   return cudaGetLastError();
 }
 
@@ -871,12 +875,15 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
   p.E = (int)g.E;
   p.N = (int)g.N;
   p.Kd = (int)g.Kd;
-  const uint16_t *rows_a = static_cast<const uint16_t*>(g.a), *b = static_cast<const uint16_t*>(g.b);
-  auto behind = [&](const uint16_t* m, int64_t stride, int64_t cols) {
-    return g.cap ? m + (g.cap - 1) * stride + cols : m;
+  const uint16_t *rows = static_cast<const uint16_t*>(g.a), *b = static_cast<const uint16_t*>(g.b);
+  Maps maps = {};
+  auto eighths = [&](CUtensorMap (&of)[8], const uint16_t* m, int64_t count, int64_t cols, int64_t stride, bool kmajor) {
+    cudaError_t r = cudaSuccess;
+    for (int i = 0; i < 8 && r == cudaSuccess; i++)
+      r = make_tensor_map_eighth_rows(&of[i], m, type, count, cols, stride, i, kmajor ? kRawRows<true> : kRawRows<false>,
+                                      (kmajor ? kRawRow<true> : kRawRow<false>) / 2);
+    return r;
   };
-  CUtensorMap ta = {}, to = {};
-  RowMaps tb = {};
   cudaError_t e;
   if (dir == kWeight) {
     p.mt = (int)((g.N + BM - 1) / BM);
@@ -885,24 +892,28 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
     const bool f32 = g.out_dtype == MOE_ELEM_F32;
     const int64_t tiles = g.E * p.mt * p.kt;
     if constexpr (PIECES) {
-      p.a = rows_a, p.a_end = behind(rows_a, g.sa, g.N), p.sa = g.sa;
-      p.b = b, p.b_end = behind(b, g.sb, g.Kd), p.sb = g.sb;
-      return f32 ? launch<kWeight, T, float, true>(ta, tb, to, p, tiles, st)
-                 : launch<kWeight, T, T, true>(ta, tb, to, p, tiles, st);
+      p.a = rows, p.sa = g.sa;
+      p.b = b, p.sb = g.sb;
+      if (g.cap > 0) {  // (without rows no copy is made)
+        if ((e = eighths(maps.a, rows, g.cap, g.N, g.sa, false)) != cudaSuccess) return e;
+        if ((e = eighths(maps.b, b, g.cap, g.Kd, g.sb, false)) != cudaSuccess) return e;
+      }
+      return f32 ? launch<kWeight, T, float, true>(maps, p, tiles, st)
+                 : launch<kWeight, T, T, true>(maps, p, tiles, st);
     }
     p.a_groups = g.N % 64 == 0;
     p.b_groups = g.Kd % 64 == 0;
-    e = p.a_groups ? make_tensor_map_row_groups(&ta, g.a, type, g.cap, g.N, g.sa, BK)
-                   : make_tensor_map_rows(&ta, g.a, type, g.cap, g.N, g.sa, BK, 64);
+    e = p.a_groups ? make_tensor_map_row_groups(&maps.a[0], g.a, type, g.cap, g.N, g.sa, BK)
+                   : make_tensor_map_rows(&maps.a[0], g.a, type, g.cap, g.N, g.sa, BK, 64);
     if (e != cudaSuccess) return e;
-    e = p.b_groups ? make_tensor_map_row_groups(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK)
-                   : make_tensor_map_rows(&tb.of[0], g.b, type, g.cap, g.Kd, g.sb, BK, 64);
+    e = p.b_groups ? make_tensor_map_row_groups(&maps.b[0], g.b, type, g.cap, g.Kd, g.sb, BK)
+                   : make_tensor_map_rows(&maps.b[0], g.b, type, g.cap, g.Kd, g.sb, BK, 64);
     if (e != cudaSuccess) return e;
-    if ((e = make_tensor_map_matrices(&to, g.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, f32 ? 4 : 2, g.E, g.N,
+    if ((e = make_tensor_map_matrices(&maps.out, g.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, f32 ? 4 : 2, g.E, g.N,
                                       g.Kd, 32, f32 ? 32 : 64)) != cudaSuccess)
       return e;
-    return f32 ? launch<kWeight, T, float, false>(ta, tb, to, p, tiles, st)
-               : launch<kWeight, T, T, false>(ta, tb, to, p, tiles, st);
+    return f32 ? launch<kWeight, T, float, false>(maps, p, tiles, st)
+               : launch<kWeight, T, T, false>(maps, p, tiles, st);
   }
   p.features = (int)(dir == kForward ? g.N : g.Kd);
   p.contraction = (int)(dir == kForward ? g.Kd : g.N);
@@ -914,20 +925,22 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
   // in turn, without the counter and its clearing
   if (routes > BN) p.next = static_cast<int32_t*>(g.workspace);
   if constexpr (PIECES) {
-    p.a = b, p.a_end = b + g.E * g.N * g.Kd, p.sa = g.Kd;
-    p.b = rows_a, p.b_end = behind(rows_a, g.sa, p.contraction), p.sb = g.sa;
-    return fwd ? launch<kForward, T, T, true>(ta, tb, to, p, tiles, st)
-               : launch<kData, T, T, true>(ta, tb, to, p, tiles, st);
+    p.a = b, p.sa = g.Kd;
+    p.b = rows, p.sb = g.sa;
+    if ((e = eighths(maps.a, b, g.E * g.N, g.Kd, g.Kd, fwd)) != cudaSuccess) return e;
+    if ((e = eighths(maps.b, rows, g.cap, p.contraction, g.sa, true)) != cudaSuccess) return e;
+    return fwd ? launch<kForward, T, T, true>(maps, p, tiles, st)
+               : launch<kData, T, T, true>(maps, p, tiles, st);
   }
   p.a_groups = !fwd && g.Kd % 64 == 0;
-  e = p.a_groups ? make_tensor_map_matrix_groups(&ta, g.b, type, g.E, g.N, g.Kd, BK)
-                 : make_tensor_map_matrices(&ta, g.b, type, 2, g.E, g.N, g.Kd, fwd ? 128 : BK, 64);
+  e = p.a_groups ? make_tensor_map_matrix_groups(&maps.a[0], g.b, type, g.E, g.N, g.Kd, BK)
+                 : make_tensor_map_matrices(&maps.a[0], g.b, type, 2, g.E, g.N, g.Kd, fwd ? 128 : BK, 64);
   if (e != cudaSuccess) return e;
   for (int i = 0; i < 8 && (i == 0 || i * 32 < routes); i++)  // a tile has no more rows than there are routes
-    if ((e = make_tensor_map_rows(&tb.of[i], g.a, type, g.cap, p.contraction, g.sa, 16 * (i + 1), BK)) != cudaSuccess)
+    if ((e = make_tensor_map_rows(&maps.b[i], g.a, type, g.cap, p.contraction, g.sa, 16 * (i + 1), BK)) != cudaSuccess)
       return e;
-  return fwd ? launch<kForward, T, T, false>(ta, tb, to, p, tiles, st)
-             : launch<kData, T, T, false>(ta, tb, to, p, tiles, st);
+  return fwd ? launch<kForward, T, T, false>(maps, p, tiles, st)
+             : launch<kData, T, T, false>(maps, p, tiles, st);
 }
 
 }  // namespace

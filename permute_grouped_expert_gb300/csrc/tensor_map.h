@@ -42,12 +42,13 @@ inline cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, CUtens
 // Tiled map of 16-bit elements with the 128-byte swizzle; strides in bytes, of all
 // dimensions but the innermost.
 inline cudaError_t make_tensor_map(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int rank,
-                                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+                                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   CUresult r = enc(map, dtype, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -71,6 +72,23 @@ inline cudaError_t make_tensor_map_row_groups(CUtensorMap* map, const void* base
   const cuuint64_t dims[3] = {64, rows, cols / 64}, strides[2] = {row_bytes(rows, cols, stride), 128};
   const cuuint32_t box[3] = {64, box_rows, 2};
   return make_tensor_map(map, base, dtype, 3, dims, strides, box);
+}
+
+// Every eighth row of a row matrix that starts anywhere, from row `first` on: such
+// rows lie a multiple of 16 bytes apart.  The map starts at the aligned 16 bytes that
+// hold the first element, so that column c of it is column c minus their distance of
+// the matrix; boxes without swizzle.  Without such a row it is the first row's, which
+// no result depends on then.
+inline cudaError_t make_tensor_map_eighth_rows(CUtensorMap* map, const uint16_t* base, CUtensorMapDataType dtype,
+                                               uint64_t rows, uint64_t cols, uint64_t stride, uint64_t first,
+                                               uint32_t box_rows, uint32_t box_cols) {
+  if (first >= rows) first = 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(base + first * stride), start = at & ~uintptr_t(15);
+  const uint64_t count = (rows - first + 7) / 8, width = (at - start) / 2 + cols;
+  const cuuint64_t dims[2] = {width, count}, strides[1] = {count > 1 ? stride * 16 : (width + 7) / 8 * 16};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  return make_tensor_map(map, reinterpret_cast<const void*>(start), dtype, 2, dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // Matrices [count][rows][cols] of 16-bit elements, contiguous, columns in groups of
