@@ -152,7 +152,8 @@ _SIGNATURES = {
                                          ctypes.POINTER(_HandleDev), _P, ctypes.c_size_t, ctypes.c_int64, _P],
     "moe_quantize_fp8_blocks": [_P, _I64, _I64, _I64, _P, _P, _P],
     "moe_quantize_nvfp4_rows": [_P, _I64, _I64, _P, _P, _P, _P],
-    # descriptors (moe_norm, moe_router, moe_w4, moe_gemm, moe_rows) by address
+    # descriptors (moe_norm, moe_router, moe_w4, moe_gemm, moe_rows; of the calls on dispatched rows
+    # moe_handle_dev, moe_shape and moe_layout, too) by address
     "moe_layer_norm": [_P] * 10,
     "moe_layer_norm_workspace_size": [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
     "moe_layer_norm_backward": [_P] * 11 + [ctypes.c_size_t, _P],
@@ -167,16 +168,11 @@ _SIGNATURES = {
     "moe_rms_norm_backward": [_P] * 9 + [ctypes.c_size_t, _P],
     "moe_grouped_gemm_workspace_size": [ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _I64, _I64,
                                         ctypes.POINTER(ctypes.c_size_t)],
-    "moe_grouped_gemm": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _P, _P, _P, _P,
-                         _P, ctypes.c_size_t, _P],
-    "moe_grouped_gemm_backward_data": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout),
-                                       _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
-    "moe_grouped_gemm_backward_weight": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout),
-                                         _P, _P, _P, ctypes.c_int32, _P, _P, _P, ctypes.c_size_t, _P],
-    "moe_swiglu": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _I64, ctypes.c_int32,
-                   _P, _P, _P, _P],
-    "moe_swiglu_backward": [ctypes.POINTER(_HandleDev), ctypes.POINTER(_Shape), ctypes.POINTER(_Layout), _I64,
-                            ctypes.c_int32, _P, _P, _P, _P, _P, _P],
+    "moe_grouped_gemm": [_P] * 8 + [ctypes.c_size_t, _P],
+    "moe_grouped_gemm_backward_data": [_P] * 8 + [ctypes.c_size_t, _P],
+    "moe_grouped_gemm_backward_weight": [_P] * 6 + [ctypes.c_int32, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_swiglu": [_P] * 3 + [_I64, ctypes.c_int32] + [_P] * 4,
+    "moe_swiglu_backward": [_P] * 3 + [_I64, ctypes.c_int32] + [_P] * 6,
     "moe_ring_create": [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_P)],
     "moe_ring_acquire": [_P, _P, ctypes.POINTER(ctypes.c_int32)],
     "moe_ring_release": [_P, ctypes.c_int32, _P],
@@ -798,18 +794,36 @@ def moe_grouped_gemm_workspace_size(shape: Shape, layout: Layout, N: int, Kd: in
     return out.value
 
 
-_GEMM_CALL = struct.Struct("=qqi4x" + "qq" * 2)  # moe_gemm, then two moe_rows
-_GEMM_ROWS = 24
+# The calls on dispatched rows: moe_handle_dev (the arrays that they read), moe_shape
+# and moe_layout in front of the other descriptors.
+_ROUTED = "8Q5q2q"
+_SHAPE_AT, _LAYOUT_AT, _ROUTED_BYTES = 64, 104, 120
 
 
-def _gemm_call(layout: Layout, N: int, Kd: int, dtype: torch.dtype, rows):
+def _routed(handle: Handle, shape: Shape, layout: Layout):
+    arrays = []
+    for name in ("tokens_per_expert", "padded_offsets", "token_of", "status"):
+        t = getattr(handle, name)
+        if not (t.is_cuda and t.is_contiguous()):
+            raise ValueError(f"handle.{name}: contiguous device tensor expected")
+        arrays.append(t.data_ptr())
+    counts, offsets, token_of, status = arrays
+    return (counts, offsets, 0, token_of, 0, 0, 0, status, shape.T, shape.H, shape.E, shape.K, shape.I,
+            layout.pad_multiple, layout.capacity)
+
+
+_GEMM_CALL = struct.Struct("=" + _ROUTED + "qqi4x" + "qq" * 2)  # then moe_gemm and two moe_rows
+_GEMM_AT, _GEMM_ROWS = _ROUTED_BYTES, _ROUTED_BYTES + 24
+
+
+def _gemm_call(handle: Handle, shape: Shape, layout: Layout, N: int, Kd: int, dtype: torch.dtype, rows):
     """(buffer, its address); rows: (name, tensor, columns) of two row matrices."""
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"bfloat16 or float16 expected, got {dtype}")
     buf = bytearray(_GEMM_CALL.size)
     (n0, t0, c0), (n1, t1, c1) = rows
-    _GEMM_CALL.pack_into(buf, 0, N, Kd, _ELEM[dtype], *_rows(t0, n0, (layout.capacity, c0), dtype),
-                         *_rows(t1, n1, (layout.capacity, c1), dtype))
+    _GEMM_CALL.pack_into(buf, 0, *_routed(handle, shape, layout), N, Kd, _ELEM[dtype],
+                         *_rows(t0, n0, (layout.capacity, c0), dtype), *_rows(t1, n1, (layout.capacity, c1), dtype))
     return buf, _address(buf)
 
 
@@ -823,9 +837,9 @@ def moe_grouped_gemm(handle: Handle, shape: Shape, layout: Layout, weight: torch
                      y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """y[r] = weight[e] @ x[r] for the routed rows r of expert e: weight [E, N, Kd], x [cap, Kd], y [cap, N]."""
     N, Kd = _expert_matrices(weight, "weight", shape)
-    buf, a = _gemm_call(layout, N, Kd, weight.dtype, (("x", x, Kd), ("y", y, N)))
+    buf, a = _gemm_call(handle, shape, layout, N, Kd, weight.dtype, (("x", x, Kd), ("y", y, N)))
     r = a + _GEMM_ROWS
-    _check(_lib.moe_grouped_gemm(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), a,
+    _check(_lib.moe_grouped_gemm(a, a + _SHAPE_AT, a + _LAYOUT_AT, a + _GEMM_AT,
                                  _dense(weight, "weight", weight.shape, weight.dtype), r, r + _ROWS_BYTES,
                                  *_workspace(workspace), _stream(stream)), "moe_grouped_gemm")
 
@@ -835,10 +849,10 @@ def moe_grouped_gemm_backward_data(handle: Handle, shape: Shape, layout: Layout,
                                    stream=None) -> None:
     """grad_x[r] = weight[e].T @ grad_y[r] for the routed rows r of expert e: grad_y [cap, N], grad_x [cap, Kd]."""
     N, Kd = _expert_matrices(weight, "weight", shape)
-    buf, a = _gemm_call(layout, N, Kd, weight.dtype, (("grad_y", grad_y, N), ("grad_x", grad_x, Kd)))
+    buf, a = _gemm_call(handle, shape, layout, N, Kd, weight.dtype, (("grad_y", grad_y, N), ("grad_x", grad_x, Kd)))
     r = a + _GEMM_ROWS
     _check(_lib.moe_grouped_gemm_backward_data(
-        ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), a,
+        a, a + _SHAPE_AT, a + _LAYOUT_AT, a + _GEMM_AT,
         _dense(weight, "weight", weight.shape, weight.dtype), r, r + _ROWS_BYTES, *_workspace(workspace),
         _stream(stream)), "moe_grouped_gemm_backward_data")
 
@@ -849,16 +863,16 @@ def moe_grouped_gemm_backward_weight(handle: Handle, shape: Shape, layout: Layou
     """grad_weight[e] = sum of outer(grad_y[r], x[r]) over the routed rows r of e (+ addend[e]): grad_weight
     [E, N, Kd] of the rows' type or float; addend float, maybe grad_weight itself."""
     N, Kd = _expert_matrices(grad_weight, "grad_weight", shape)
-    buf, a = _gemm_call(layout, N, Kd, x.dtype, (("x", x, Kd), ("grad_y", grad_y, N)))
+    buf, a = _gemm_call(handle, shape, layout, N, Kd, x.dtype, (("x", x, Kd), ("grad_y", grad_y, N)))
     r = a + _GEMM_ROWS
     _check(_lib.moe_grouped_gemm_backward_weight(
-        ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), a, r, r + _ROWS_BYTES,
-        _elem(grad_weight), _dense(addend, "addend", grad_weight.shape, torch.float32),
+        a, a + _SHAPE_AT, a + _LAYOUT_AT, a + _GEMM_AT, r, r + _ROWS_BYTES, _elem(grad_weight),
+        _dense(addend, "addend", grad_weight.shape, torch.float32),
         _dense(grad_weight, "grad_weight", grad_weight.shape, grad_weight.dtype), *_workspace(workspace),
         _stream(stream)), "moe_grouped_gemm_backward_weight")
 
 
-_SWIGLU_CALL = struct.Struct("=" + "qq" * 3)  # three moe_rows
+_SWIGLU_CALL = struct.Struct("=" + _ROUTED + "qq" * 3)  # then three moe_rows
 
 
 def moe_swiglu(handle: Handle, shape: Shape, layout: Layout, pre: torch.Tensor, act: torch.Tensor,
@@ -866,11 +880,12 @@ def moe_swiglu(handle: Handle, shape: Shape, layout: Layout, pre: torch.Tensor, 
     """act[r] = probs[r] * silu(gate) * up for the routed rows: pre [cap, 2 I] = up columns, then gate; act [cap, I]."""
     cap, I = layout.capacity, _matrix(act, "act")[1]
     buf = bytearray(_SWIGLU_CALL.size)
-    _SWIGLU_CALL.pack_into(buf, 0, *_rows(pre, "pre", (cap, 2 * I), pre.dtype),
+    _SWIGLU_CALL.pack_into(buf, 0, *_routed(handle, shape, layout), *_rows(pre, "pre", (cap, 2 * I), pre.dtype),
                            *_rows(act, "act", (cap, I), pre.dtype), *_ABSENT)
     a = _address(buf)
-    _check(_lib.moe_swiglu(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), I, _elem(pre), a,
-                           _dense(probs, "probs", (cap,), torch.float32), a + _ROWS_BYTES, _stream(stream)),
+    r = a + _ROUTED_BYTES
+    _check(_lib.moe_swiglu(a, a + _SHAPE_AT, a + _LAYOUT_AT, I, _elem(pre), r,
+                           _dense(probs, "probs", (cap,), torch.float32), r + _ROWS_BYTES, _stream(stream)),
            "moe_swiglu")
 
 
@@ -880,13 +895,14 @@ def moe_swiglu_backward(handle: Handle, shape: Shape, layout: Layout, pre: torch
     """Gradients of moe_swiglu: grad_pre [cap, 2 I] (maybe pre itself) and grad_probs (float [cap])."""
     cap, I = layout.capacity, _matrix(grad_act, "grad_act")[1]
     buf = bytearray(_SWIGLU_CALL.size)
-    _SWIGLU_CALL.pack_into(buf, 0, *_rows(pre, "pre", (cap, 2 * I), pre.dtype),
+    _SWIGLU_CALL.pack_into(buf, 0, *_routed(handle, shape, layout), *_rows(pre, "pre", (cap, 2 * I), pre.dtype),
                            *_rows(grad_act, "grad_act", (cap, I), pre.dtype),
                            *_rows(grad_pre, "grad_pre", (cap, 2 * I), pre.dtype))
     a = _address(buf)
-    _check(_lib.moe_swiglu_backward(ctypes.byref(handle.c()), ctypes.byref(shape.c()), ctypes.byref(layout.c()), I,
-                                    _elem(pre), a, _dense(probs, "probs", (cap,), torch.float32), a + _ROWS_BYTES,
-                                    a + 2 * _ROWS_BYTES, _dense(grad_probs, "grad_probs", (cap,), torch.float32),
+    r = a + _ROUTED_BYTES
+    _check(_lib.moe_swiglu_backward(a, a + _SHAPE_AT, a + _LAYOUT_AT, I, _elem(pre), r,
+                                    _dense(probs, "probs", (cap,), torch.float32), r + _ROWS_BYTES,
+                                    r + 2 * _ROWS_BYTES, _dense(grad_probs, "grad_probs", (cap,), torch.float32),
                                     _stream(stream)), "moe_swiglu_backward")
 
 

@@ -38,8 +38,17 @@ namespace {
 using namespace sm100;
 
 constexpr int kPieceWarps = 8;  // that bring unaligned operands into place
+// Epilogue warps: with few steps along the contraction the rows' products wait for
+// them (5264 features of 64 for 15364 rows: four 123 us, eight @@).
 template <GemmDir DIR, bool PIECES>
-constexpr int kThreads = 256 + (PIECES ? 32 * kPieceWarps : DIR == kWeight ? 32 : 0);
+constexpr int kEpilogue = DIR == kWeight || PIECES ? 4 : 8;
+template <GemmDir DIR, bool PIECES>
+constexpr int kThreads = 128 + 32 * (kEpilogue<DIR, PIECES> + (PIECES ? kPieceWarps : DIR == kWeight));
+// An MMA adds to its fp32 sums by cutting off, so that a long sum is short by about
+// 2^-26 a step of 16.  fp32 gradients are sums of parts of at most this many stages
+// (768 rows), added by rounding: 512 rows are 5e-7 off, 8192 in one part @@.
+template <GemmDir DIR, typename OUT>
+constexpr int kPart = DIR == kWeight && sizeof(OUT) == 4 ? 12 : 1 << 30;
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
 // Tiles that may be on their way to the readers: more where tiles are short, fewer
 // where the last ones would wait behind long ones.
@@ -335,6 +344,7 @@ template <GemmDir DIR, typename T, typename OUT, bool PIECES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES>, 1)
     grouped_gemm_kernel(const __grid_constant__ Maps maps, TcParams p) {
   constexpr int kStages = kStagesOf<DIR, PIECES>, kSlots = kSlotsOf<DIR>, kRaw = PIECES ? kRawOf<DIR> : 1;
+  constexpr int kEpi = kEpilogue<DIR, PIECES>;
   constexpr bool kW = DIR == kWeight, kAmn = DIR != kForward, kBmn = kW;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tail[kStages], s_tfull[2], s_tempty[2];
@@ -362,12 +372,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     }
     for (int a = 0; a < 2; a++) {
       mbar_init(&s_tfull[a], 1);
-      mbar_init(&s_tempty[a], 8);  // on the leader: 4 epilogue warps of each CTA
+      mbar_init(&s_tempty[a], 2 * kEpi);  // on the leader: the epilogue warps of each CTA
     }
     for (int s = 0; s < kSlots; s++) {
       mbar_init(&s_have[s], 1);
-      // MMA, 4 epilogue warps a CTA, and its producers (kWeight: and warp 8)
-      mbar_init(&s_free[s], 1 + 2 * (6 + (PIECES ? kPieceWarps : kW)));  // on the leader: every reader of both CTAs
+      // the MMA's, and in each CTA the producers, the epilogue's and the others'
+      mbar_init(&s_free[s], 1 + 2 * (2 + kEpi + (PIECES ? kPieceWarps : kW)));  // on the leader: every reader of both CTAs
     }
     for (int s = 0; s < kRaw; s++) {
       mbar_init(&s_raw[s], 1);
@@ -409,6 +419,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     if (!__all_sync(0xffffffffu, next_tile(i, ti))) return false;
     if (lane == 0) have_read(i, ti);
     return ti.e >= 0;
+  };
+
+  // Parts of a tile's contraction that are summed on their own.
+  auto parts_of = [](int blocks) {
+    constexpr int kMost = kPart<DIR, OUT>;
+    return blocks <= kMost ? 1 : (blocks + kMost - 1) / kMost;
   };
 
   if (PIECES && (warp == 0 || warp == 3)) {
@@ -538,41 +554,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
       for (int i = 0; ok; i++) {
         Tile ti;
         if (!take_tile(i, ti)) break;
-        const int nkb = ti.blocks;
+        const int nkb = ti.blocks, parts = parts_of(nkb), part = (nkb + parts - 1) / parts;
         const uint32_t idesc = idesc_16bit(BM, (uint32_t)ti.cols, std::is_same<T, __nv_bfloat16>::value, kAmn, kBmn);
-        if (!mbar_wait_cluster(&s_tempty[acc], acc_phase ^ 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-        for (int kb = 0; kb < nkb; kb++) {
-          if (!mbar_wait_cluster(&s_full[stage], phase, abort_flag, p.status)) {
+        for (int kb0 = 0, done = 0; done < parts; kb0 += part, done++) {
+          if (!mbar_wait_cluster(&s_tempty[acc], acc_phase ^ 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + (size_t)stage * kStageBytes), sb = sa + kOperand;
-          const uint64_t adesc = kAmn ? smem_desc_sw128_mn(sa, kBox) : smem_desc_sw128(sa);
-          const uint64_t bdesc = kBmn ? smem_desc_sw128_mn(sb, kBox) : smem_desc_sw128(sb);
-          // a step of 16: 32 bytes of K-major rows, or 16 rows of 128 bytes
-          constexpr uint64_t kAstep = kAmn ? 128 : 2, kBstep = kBmn ? 128 : 2;
-          const int left = kW ? (ti.end - ti.row) - kb * BK : p.contraction - kb * BK;
+          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+          for (int kb = kb0; kb < min(kb0 + part, nkb); kb++) {
+            if (!mbar_wait_cluster(&s_full[stage], phase, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + (size_t)stage * kStageBytes), sb = sa + kOperand;
+            const uint64_t adesc = kAmn ? smem_desc_sw128_mn(sa, kBox) : smem_desc_sw128(sa);
+            const uint64_t bdesc = kBmn ? smem_desc_sw128_mn(sb, kBox) : smem_desc_sw128(sb);
+            // a step of 16: 32 bytes of K-major rows, or 16 rows of 128 bytes
+            constexpr uint64_t kAstep = kAmn ? 128 : 2, kBstep = kBmn ? 128 : 2;
+            const int left = kW ? (ti.end - ti.row) - kb * BK : p.contraction - kb * BK;
 #pragma unroll
-          for (int k = 0; k < BK / 16; k++)
-            if (k * 16 < left)
-              mma_bf16_pair(d_tmem, adesc + kAstep * k, bdesc + kBstep * k, idesc, (kb | k) != 0 ? 1u : 0u);
-          mma_commit_pair(&s_empty[stage], 0x3);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+            for (int k = 0; k < BK / 16; k++)
+              if (k * 16 < left)
+                mma_bf16_pair(d_tmem, adesc + kAstep * k, bdesc + kBstep * k, idesc, kb > kb0 || k > 0 ? 1u : 0u);
+            mma_commit_pair(&s_empty[stage], 0x3);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
-        }
-        if (!ok) break;
-        mma_commit_pair(&s_tfull[acc], 0x3);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1;
+          if (!ok) break;
+          mma_commit_pair(&s_tfull[acc], 0x3);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1;
+          }
         }
       }
       if (!ok) {
@@ -648,169 +666,191 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (kW && warp == 8) {
     // ---------------------------------------------------------- zeros (kWeight)
-    if (kW) {
-      int stage = 0;
-      uint32_t phases = 0;  // bit s: parity of s_tail[s]
-      for (int i = 0;; i++) {
-        Tile ti;
-        if (!take_tile_warp(i, ti)) break;
-        const int nkb = ti.blocks;
-        if (nkb && ragged(ti)) {
-          const int s = (stage + nkb - 1) % kStages;
-          int ok = 0;
-          if (lane == 0) ok = mbar_wait(&s_tail[s], (phases >> s) & 1, abort_flag, p.status) ? 1 : 0;
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-          phases ^= 1u << s;
-          const int rows = (ti.end - ti.row) - (nkb - 1) * BK, stop = (rows + 15) & ~15;
-          uint8_t* base = smem + (size_t)s * kStageBytes;
-          for (int j = lane; j < (stop - rows) * 8 * 4; j += 32) {  // 16 bytes each of the four boxes' rows
-            const int box = j & 3, at = j >> 2;
-            *reinterpret_cast<uint4*>(base + box * kBox + rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&s_full[s]), 0));
+    int stage = 0;
+    uint32_t phases = 0;  // bit s: parity of s_tail[s]
+    for (int i = 0;; i++) {
+      Tile ti;
+      if (!take_tile_warp(i, ti)) break;
+      const int nkb = ti.blocks;
+      if (nkb && ragged(ti)) {
+        const int s = (stage + nkb - 1) % kStages;
+        int ok = 0;
+        if (lane == 0) ok = mbar_wait(&s_tail[s], (phases >> s) & 1, abort_flag, p.status) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        phases ^= 1u << s;
+        const int rows = (ti.end - ti.row) - (nkb - 1) * BK, stop = (rows + 15) & ~15;
+        uint8_t* base = smem + (size_t)s * kStageBytes;
+        for (int j = lane; j < (stop - rows) * 8 * 4; j += 32) {  // 16 bytes each of the four boxes' rows
+          const int box = j & 3, at = j >> 2;
+          *reinterpret_cast<uint4*>(base + box * kBox + rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
         }
-        stage = (stage + nkb) % kStages;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&s_full[s]), 0));
       }
+      stage = (stage + nkb) % kStages;
     }
   } else {
     // ---------------------------------------------------------- epilogue
     const int lane_base = 32 * (warp & 3);
-    uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (PIECES ? 2 * kRaw * kRawOperand : 0) + (size_t)(warp & 3) * (PIECES ? 32 * kTurn * 4 : 2 * kOutBytes);  // kWeight
+    const int turn_of = (warp - 4) >> 2;  // of the warps with the same lanes
+    constexpr int kTurns = kEpi / 4;
+    uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (PIECES ? 2 * kRaw * kRawOperand : 0) +
+                     (size_t)(warp & 3) * (PIECES ? 32 * kTurn * 4 : 2 * kOutBytes);  // kWeight
     int out_at = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int i = 0;; i++) {
+    bool ok = true;
+    for (int i = 0; ok; i++) {
       Tile ti;
       if (!take_tile_warp(i, ti)) break;
-      int ok = 0;
-      if (lane == 0) ok = mbar_wait(&s_tfull[acc], acc_phase, abort_flag, p.status) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
+      const int parts = parts_of(ti.blocks);
       const int f_warp = ti.m * BM + (int)rank * 128 + lane_base;  // first feature of this warp
-      if constexpr (kW && PIECES) {
-        // 32 columns of 32 rows at a time, turned in shared memory
-        float* turn = reinterpret_cast<float*>(s_out);
-        const bool none = ti.end == ti.row;
-        const int cols = min(p.Kd - ti.n * BN, BN), rows = min(p.N - f_warp, 32);
-        const int64_t first = ((int64_t)ti.e * p.N + f_warp) * p.Kd + ti.n * BN;
-        for (int c = 0; c < cols && rows > 0; c += 32) {
-          float v[32];
-          if (none) {
-#pragma unroll
-            for (int j = 0; j < 32; j++) v[j] = 0.0f;
-          } else {
-            tmem_ld32(taddr + c, v);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 32; j++) turn[lane * kTurn + j] = v[j];
-          __syncwarp();
-          if (c + lane < cols) {
-            const int64_t at = first + c + lane;
-            OUT* to = static_cast<OUT*>(p.out) + at;
-#pragma unroll 8
-            for (int r = 0; r < rows; r++) {
-              float x = turn[r * kTurn + lane];
-              if (sizeof(OUT) == 4 && p.addend) x += p.addend[at + (int64_t)r * p.Kd];
-              to[(int64_t)r * p.Kd] = from_float<OUT>(x);
-            }
-          }
+      for (int done = 0; done < parts; done++) {
+        int there = 0;
+        if (lane == 0) there = mbar_wait(&s_tfull[acc], acc_phase, abort_flag, p.status) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, there, 0)) {
+          ok = false;
+          break;
         }
-      } else if constexpr (kW) {
-        // 128 bytes of this lane's row of the matrix at a time, through shared memory
-        constexpr int kCols = 128 / (int)sizeof(OUT);
-        const bool none = ti.end == ti.row;
-        const int n = f_warp + lane;
-        const float* add = p.addend ? p.addend + ((int64_t)ti.e * p.N + n) * p.Kd + ti.n * BN : nullptr;
-        const int cols = min(p.Kd - ti.n * BN, BN);
-        for (int c = 0; c < cols && f_warp < p.N; c += kCols) {
-          uint4 piece[8];
-#pragma unroll
-          for (int h = 0; h < kCols / 32; h++) {
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
+        if constexpr (kW && PIECES) {
+          // 32 columns of 32 rows at a time, turned in shared memory
+          float* turn = reinterpret_cast<float*>(s_out);
+          const bool none = ti.end == ti.row;
+          const int cols = min(p.Kd - ti.n * BN, BN), rows = min(p.N - f_warp, 32);
+          const int64_t first = ((int64_t)ti.e * p.N + f_warp) * p.Kd + ti.n * BN;
+          // the parts before this one, or the caller's
+          const float* add = done ? static_cast<const float*>(p.out) : p.addend;
+          for (int c = 0; c < cols && rows > 0; c += 32) {
             float v[32];
             if (none) {
 #pragma unroll
               for (int j = 0; j < 32; j++) v[j] = 0.0f;
             } else {
-              tmem_ld32(taddr + c + h * 32, v);
+              tmem_ld32(taddr + c, v);
             }
-            if constexpr (sizeof(OUT) == 4) {
-              if (add && n < p.N) {
+            __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                  if (c + j < cols) {
-                    const float4 x = *reinterpret_cast<const float4*>(add + c + j);
-                    v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
-                  }
+            for (int j = 0; j < 32; j++) turn[lane * kTurn + j] = v[j];
+            __syncwarp();
+            if (c + lane < cols) {
+              const int64_t at = first + c + lane;
+              OUT* to = static_cast<OUT*>(p.out) + at;
+#pragma unroll 8
+              for (int r = 0; r < rows; r++) {
+                float x = turn[r * kTurn + lane];
+                if (sizeof(OUT) == 4 && add) x += add[at + (int64_t)r * p.Kd];
+                to[(int64_t)r * p.Kd] = from_float<OUT>(x);
               }
-#pragma unroll
-              for (int q = 0; q < 8; q++)
-                piece[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                      __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; q++)
-                piece[h * 4 + q] = make_uint4(pack2<T>(v[8 * q], v[8 * q + 1]), pack2<T>(v[8 * q + 2], v[8 * q + 3]),
-                                              pack2<T>(v[8 * q + 4], v[8 * q + 5]), pack2<T>(v[8 * q + 6], v[8 * q + 7]));
             }
           }
-          uint8_t* buf = s_out + out_at * kOutBytes;
-          if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this buffer
-          __syncwarp();
-#pragma unroll
-          for (int q = 0; q < 8; q++) *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) * 16)) = piece[q];
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&maps.out, buf, ti.n * BN + c, f_warp, ti.e);
-            bulk_commit();
+        } else if constexpr (kW) {
+          // 128 bytes of this lane's row of the matrix at a time, through shared memory
+          constexpr int kCols = 128 / (int)sizeof(OUT);
+          const bool none = ti.end == ti.row;
+          const int n = f_warp + lane;
+          // the parts before this one, as this warp's copies left them, or the caller's
+          const float* add = done ? static_cast<const float*>(p.out) : p.addend;
+          if (add) add += ((int64_t)ti.e * p.N + n) * p.Kd + ti.n * BN;
+          if (done) {
+            if (lane == 0) {
+              bulk_wait_all();
+              fence_async_all();
+            }
+            __syncwarp();
           }
-          out_at ^= 1;
-        }
-      } else if constexpr (PIECES) {
-        // columns are rows of the result, lanes features
-        const int f = f_warp + lane;
-        T* out = static_cast<T*>(p.out) + f;
-        for (int c = 0; c < ti.cols; c += 32) {
-          float v[32];
-          tmem_ld32(taddr + c, v);
+          const int cols = min(p.Kd - ti.n * BN, BN);
+          for (int c = 0; c < cols && f_warp < p.N; c += kCols) {
+            uint4 piece[8];
 #pragma unroll
-          for (int j = 0; j < 32; j++) {
-            const int row = ti.row + c + j;
-            if (row < ti.end && f < p.features) out[(int64_t)row * p.sout] = from_float<T>(v[j]);
+            for (int h = 0; h < kCols / 32; h++) {
+              float v[32];
+              if (none) {
+#pragma unroll
+                for (int j = 0; j < 32; j++) v[j] = 0.0f;
+              } else {
+                tmem_ld32(taddr + c + h * 32, v);
+              }
+              if constexpr (sizeof(OUT) == 4) {
+                if (add && n < p.N) {
+#pragma unroll
+                  for (int j = 0; j < 32; j += 4)
+                    if (c + j < cols) {
+                      const float4 x = __ldcg(reinterpret_cast<const float4*>(add + c + j));
+                      v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 8; q++)
+                  piece[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+              } else {
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                  piece[h * 4 + q] =
+                      make_uint4(pack2<T>(v[8 * q], v[8 * q + 1]), pack2<T>(v[8 * q + 2], v[8 * q + 3]),
+                                 pack2<T>(v[8 * q + 4], v[8 * q + 5]), pack2<T>(v[8 * q + 6], v[8 * q + 7]));
+              }
+            }
+            uint8_t* buf = s_out + out_at * kOutBytes;
+            if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this buffer
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+              *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) * 16)) = piece[q];
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&maps.out, buf, ti.n * BN + c, f_warp, ti.e);
+              bulk_commit();
+            }
+            out_at ^= 1;
+          }
+        } else if constexpr (PIECES) {
+          // columns are rows of the result, lanes features
+          const int f = f_warp + lane;
+          T* out = static_cast<T*>(p.out) + f;
+          for (int c = 0; c < ti.cols; c += 32) {
+            float v[32];
+            tmem_ld32(taddr + c, v);
+#pragma unroll
+            for (int j = 0; j < 32; j++) {
+              const int row = ti.row + c + j;
+              if (row < ti.end && f < p.features) out[(int64_t)row * p.sout] = from_float<T>(v[j]);
+            }
+          }
+        } else {
+          // columns are rows of the result, lanes features: neighbouring lanes exchange
+          // one of two rows, so that each stores two features of one
+          const int f = f_warp + (lane & ~1);
+          const bool odd = lane & 1, mine = f < p.features;
+          for (int c = 32 * turn_of; c < ti.cols; c += 32 * kTurns) {
+            float v[32];
+            tmem_ld32(taddr + c, v);
+            T* out = static_cast<T*>(p.out) + (int64_t)(ti.row + c + (odd ? 1 : 0)) * p.sout + f;
+            const int64_t two = 2 * p.sout;
+            const int left = mine ? ti.end - ti.row - c - (odd ? 1 : 0) : 0;  // rows from this lane's first on
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+              const uint32_t w = odd ? pack2<T>(other, v[j + 1]) : pack2<T>(v[j], other);
+              if (j < left) *reinterpret_cast<uint32_t*>(out) = w;
+              out += two;
+            }
           }
         }
-      } else {
-        // columns are rows of the result, lanes features: neighbouring lanes exchange
-        // one of two rows, so that each stores two features of one
-        const int f = f_warp + (lane & ~1);
-        const bool odd = lane & 1;
-        T* out = static_cast<T*>(p.out) + f;
-        for (int c = 0; c < ti.cols; c += 32) {
-          float v[32];
-          tmem_ld32(taddr + c, v);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-            const uint32_t w = odd ? pack2<T>(other, v[j + 1]) : pack2<T>(v[j], other);
-            const int row = ti.row + c + j + (odd ? 1 : 0);
-            if (row < ti.end && f < p.features) *reinterpret_cast<uint32_t*>(out + (int64_t)row * p.sout) = w;
-          }
+        tc_fence_before();
+        __syncwarp();
+        // the loads from TMEM are done; stores to memory may still be on their way
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&s_tempty[acc]), 0));
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      // the loads from TMEM are done; stores to memory may still be on their way
-      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&s_tempty[acc]), 0));
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1;
       }
     }
   }

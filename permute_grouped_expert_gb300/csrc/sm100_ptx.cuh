@@ -342,6 +342,9 @@ MOE_DEVICE void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" :::
 // Generic writes to shared memory before, reads by copies and MMAs after.
 MOE_DEVICE void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// The same for all memory.
+MOE_DEVICE void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 // mbar_try_wait for arrivals from the other CTA of the cluster.
 MOE_DEVICE bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
