@@ -735,10 +735,12 @@ def moe_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, y:
     what the backward reads."""
     shape, dtype = _matrix(x, "x"), x.dtype
     pdtype = _param_dtype(x, weight, None)
+    x_rows = _rows(x, "x", shape, dtype)
+    _on_current_device(x, "x")
     if codes is not None and codes.dtype not in _CODES:
         raise ValueError(f"codes: float8_e4m3fn or uint8 expected, got {codes.dtype}")
     buf = bytearray(_NORM_CALL.size)
-    _NORM_CALL.pack_into(buf, 0, *shape, _elem(x), _ELEM[pdtype], eps, *_rows(x, "x", shape, dtype),
+    _NORM_CALL.pack_into(buf, 0, *shape, _elem(x), _ELEM[pdtype], eps, *x_rows,
                          *(_ABSENT if residual is None else _rows(residual, "residual", shape, dtype)),
                          *(_ABSENT if y is None else _rows(y, "y", shape, dtype)),
                          *(_ABSENT if sum_out is None else _rows(sum_out, "sum_out", shape, dtype)))
@@ -774,9 +776,11 @@ def moe_rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: Optiona
     the norm.  workspace is needed for grad_weight (float [H])."""
     shape, dtype, f32 = _matrix(h, "h"), h.dtype, torch.float32
     pdtype = _param_dtype(h, weight, None)
+    h_rows = _rows(h, "h", shape, dtype)
+    _on_current_device(h, "h")
     buf = bytearray(_NORM_CALL.size)
     _NORM_CALL.pack_into(buf, 0, *shape, _elem(h), _ELEM[pdtype], 0.0, *_rows(grad_y, "grad_y", shape, dtype),
-                         *_rows(h, "h", shape, dtype),
+                         *h_rows,
                          *(_ABSENT if grad_sum is None else _rows(grad_sum, "grad_sum", shape, dtype)),
                          *_rows(grad_x, "grad_x", shape, dtype))
     a = _address(buf)
@@ -800,6 +804,11 @@ _ROUTED = "8Q5q2q"
 _SHAPE_AT, _LAYOUT_AT, _ROUTED_BYTES = 64, 104, 120
 
 
+def _on_current_device(t: torch.Tensor, name: str):
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: a tensor of the current device expected, got {t.device}")
+
+
 def _routed(handle: Handle, shape: Shape, layout: Layout):
     arrays = []
     for name in ("tokens_per_expert", "padded_offsets", "token_of", "status"):
@@ -807,6 +816,7 @@ def _routed(handle: Handle, shape: Shape, layout: Layout):
         if not (t.is_cuda and t.is_contiguous()):
             raise ValueError(f"handle.{name}: contiguous device tensor expected")
         arrays.append(t.data_ptr())
+    _on_current_device(handle.padded_offsets, "handle.padded_offsets")
     counts, offsets, token_of, status = arrays
     return (counts, offsets, 0, token_of, 0, 0, 0, status, shape.T, shape.H, shape.E, shape.K, shape.I,
             layout.pad_multiple, layout.capacity)

@@ -39,14 +39,17 @@ using namespace sm100;
 
 constexpr int kPieceWarps = 8;  // that bring unaligned operands into place
 // Epilogue warps: with few steps along the contraction the rows' products wait for
-// them (5264 features of 64 for 15364 rows: four 123 us, eight @@).
+// them (5264 features of 64 for 15364 rows: four 124 us, eight 43).
 template <GemmDir DIR, bool PIECES>
 constexpr int kEpilogue = DIR == kWeight || PIECES ? 4 : 8;
 template <GemmDir DIR, bool PIECES>
 constexpr int kThreads = 128 + 32 * (kEpilogue<DIR, PIECES> + (PIECES ? kPieceWarps : DIR == kWeight));
 // An MMA adds to its fp32 sums by cutting off, so that a long sum is short by about
 // 2^-26 a step of 16.  fp32 gradients are sums of parts of at most this many stages
-// (768 rows), added by rounding: 512 rows are 5e-7 off, 8192 in one part @@.
+// (768 rows), added to one another by rounding on their way to memory: off by 7e-7 in
+// the 2-norm whatever the rows, where one part of 8192 rows would be by some 1e-5.
+// It costs 4 % of the time at 1024 rows an expert of 8192 x 8192 parts of 1536 rows,
+// 12 % parts of 768.
 template <GemmDir DIR, typename OUT>
 constexpr int kPart = DIR == kWeight && sizeof(OUT) == 4 ? 12 : 1 << 30;
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
@@ -753,16 +756,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           constexpr int kCols = 128 / (int)sizeof(OUT);
           const bool none = ti.end == ti.row;
           const int n = f_warp + lane;
-          // the parts before this one, as this warp's copies left them, or the caller's
-          const float* add = done ? static_cast<const float*>(p.out) : p.addend;
-          if (add) add += ((int64_t)ti.e * p.N + n) * p.Kd + ti.n * BN;
-          if (done) {
-            if (lane == 0) {
-              bulk_wait_all();
-              fence_async_all();
-            }
-            __syncwarp();
-          }
+          const float* add = p.addend && !done ? p.addend + ((int64_t)ti.e * p.N + n) * p.Kd + ti.n * BN : nullptr;
+          // this part is added to the one before, once that has been written
+          if (done && lane == 0) bulk_wait_all();
           const int cols = min(p.Kd - ti.n * BN, BN);
           for (int c = 0; c < cols && f_warp < p.N; c += kCols) {
             uint4 piece[8];
@@ -780,7 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
 #pragma unroll
                   for (int j = 0; j < 32; j += 4)
                     if (c + j < cols) {
-                      const float4 x = __ldcg(reinterpret_cast<const float4*>(add + c + j));
+                      const float4 x = *reinterpret_cast<const float4*>(add + c + j);
                       v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
                     }
                 }
@@ -805,7 +801,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
             fence_async_shared();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&maps.out, buf, ti.n * BN + c, f_warp, ti.e);
+              if (done)
+                tma_add_3d(&maps.out, buf, ti.n * BN + c, f_warp, ti.e);
+              else
+                tma_store_3d(&maps.out, buf, ti.n * BN + c, f_warp, ti.e);
               bulk_commit();
             }
             out_at ^= 1;

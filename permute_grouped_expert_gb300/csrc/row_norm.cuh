@@ -51,9 +51,8 @@ MOE_DEVICE float code_scale(float amax) {
 MOE_DEVICE bool plain_scale(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
 
 // Any width, stride and alignment: one CTA per row, three passes over the row
-// (the second and third mostly from L1 / L2), a fourth where codes are wanted,
-// a warp a block.
-template <typename T, typename P, bool RMS>
+// (the second and third mostly from L1 / L2).
+template <typename T, typename P>
 __global__ void __launch_bounds__(kThreads) row_norm_any_kernel(NormParams p) {
   __shared__ float2 red[2][kWarps];
   const P* w = static_cast<const P*>(p.w);
@@ -62,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) row_norm_any_kernel(NormParams p) {
     const T* x = static_cast<const T*>(p.x) + r * p.sx;
     const T* res = p.res ? static_cast<const T*>(p.res) + r * p.sres : nullptr;
     T* sum = p.sum ? static_cast<T*>(p.sum) + r * p.ssum : nullptr;
-    T* y = p.y ? static_cast<T*>(p.y) + r * p.sy : nullptr;
+    T* y = static_cast<T*>(p.y) + r * p.sy;
     // the residual sum as it is stored; a thread rereads only what it wrote
     auto h_at = [&](int64_t c) {
       if (!res) return to_float(x[c]);
@@ -74,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) row_norm_any_kernel(NormParams p) {
       if (sum) sum[c] = from_float<T>(to_float(x[c]) + to_float(res[c]));
       s += h_at(c);
     }
-    const float mean = RMS ? 0.0f : block_sum2(s, 0.0f, red[0]).x / (float)p.H;
+    const float mean = block_sum2(s, 0.0f, red[0]).x / (float)p.H;
     float q = 0.0f;
     for (int64_t c = threadIdx.x; c < p.H; c += kThreads) {
       const float d = h_at(c) - mean;
@@ -86,37 +85,85 @@ __global__ void __launch_bounds__(kThreads) row_norm_any_kernel(NormParams p) {
       float v = (h_at(c) - mean) * rstd;
       if (w) v *= to_float(w[c]);
       if (b) v += to_float(b[c]);
-      if (!RMS || y) y[c] = from_float<T>(v);
+      y[c] = from_float<T>(v);
     }
-    if (RMS && p.codes) {
-      __syncthreads();  // sum elements that other threads wrote
-      const int lane = threadIdx.x & 31;
-      const int64_t blocks = (p.H + kCodeBlock - 1) / kCodeBlock;
-      for (int64_t k = threadIdx.x >> 5; k < blocks; k += kWarps) {
-        float v[kCodeBlock / 32], amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kCodeBlock / 32; i++) {
-          const int64_t c = k * kCodeBlock + i * 32 + lane;
-          v[i] = 0.0f;
-          if (c < p.H) v[i] = h_at(c) * rstd * (w ? to_float(w[c]) : 1.0f);
-          amax = nan_max(amax, fabsf(v[i]));
-        }
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) amax = nan_max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        const float scale = code_scale(amax);
-#pragma unroll
-        for (int i = 0; i < kCodeBlock / 32; i++) {
-          const int64_t c = k * kCodeBlock + i * 32 + lane;
-          if (c < p.H) p.codes[r * p.H + c] = (uint8_t)e4m3x2(v[i] / scale, 0.0f);
-        }
-        if (lane == 0) p.scales[r * blocks + k] = scale;
-      }
-    }
-    if (RMS) __syncthreads();  // red[1] is written again without another barrier between
     if (threadIdx.x == 0) {
-      if (!RMS && p.mean) p.mean[r] = mean;
+      if (p.mean) p.mean[r] = mean;
       if (p.rstd) p.rstd[r] = rstd;
     }
+  }
+}
+
+// The same without a mean, and with codes: one CTA per row.  HELD: the row stays in
+// shared memory between its sum of squares and its results (22650 x 1641 bf16 codes
+// 131 us, read again element by element 174; instructions, about 100 an element and
+// warp, bound it); rows that it cannot hold are read again.  The results are
+// formed a block of codes at a time by a warp each.
+template <typename T, typename P, bool HELD>
+__global__ void __launch_bounds__(kThreads) rms_any_kernel(NormParams p) {
+  constexpr int kAhead = 8;  // elements of a thread on their way
+  __shared__ float2 red[2][kWarps];
+  extern __shared__ __align__(16) uint8_t staged[];
+  T* held = reinterpret_cast<T*>(staged);
+  const P* w = static_cast<const P*>(p.w);
+  const int lane = threadIdx.x & 31;
+  const int H = (int)p.H, blocks = (H + kCodeBlock - 1) / kCodeBlock;
+  int phase = 0;
+  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const T* x = static_cast<const T*>(p.x) + r * p.sx;
+    const T* res = p.res ? static_cast<const T*>(p.res) + r * p.sres : nullptr;
+    T* sum = p.sum ? static_cast<T*>(p.sum) + r * p.ssum : nullptr;
+    T* y = p.y ? static_cast<T*>(p.y) + r * p.sy : nullptr;
+    auto sum_of = [&](T a, T b) { return from_float<T>(to_float(a) + to_float(b)); };
+    float q = 0.0f;
+    for (int c0 = threadIdx.x; c0 < H; c0 += kAhead * kThreads) {
+      T a[kAhead], b[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) {
+        const int c = c0 + i * kThreads;
+        if (c < H) a[i] = x[c];
+        if (c < H && res) b[i] = res[c];
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) {
+        const int c = c0 + i * kThreads;
+        if (c >= H) continue;
+        const T h = res ? sum_of(a[i], b[i]) : a[i];
+        if (sum) sum[c] = h;
+        if (HELD) held[c] = h;
+        q = fmaf(to_float(h), to_float(h), q);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(block_sum2(q, 0.0f, red[phase]).x / (float)p.H + p.eps);  // (and the row is there)
+    phase ^= 1;
+    for (int k = threadIdx.x >> 5; k < blocks; k += kWarps) {
+      float v[kCodeBlock / 32], amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kCodeBlock / 32; i++) {
+        const int c = k * kCodeBlock + i * 32 + lane;
+        v[i] = 0.0f;
+        if (c < H) {
+          const T h = HELD ? held[c] : !res ? x[c] : sum ? sum[c] : sum_of(x[c], res[c]);
+          v[i] = to_float(h) * rstd * (w ? to_float(w[c]) : 1.0f);
+          if (y) y[c] = from_float<T>(v[i]);
+        }
+        amax = nan_max(amax, fabsf(v[i]));
+      }
+      if (!p.codes) continue;
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) amax = nan_max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      const float scale = code_scale(amax), inv = 1.0f / scale;
+      const bool plain = plain_scale(scale);
+      uint8_t* codes = p.codes + r * p.H;
+#pragma unroll
+      for (int i = 0; i < kCodeBlock / 32; i++) {
+        const int c = k * kCodeBlock + i * 32 + lane;
+        if (c < H) codes[c] = (uint8_t)e4m3x2(plain ? div_by_scale(v[i], scale, inv) : v[i] / scale, 0.0f);
+      }
+      if (lane == 0) p.scales[r * (int64_t)blocks + k] = scale;
+    }
+    if (threadIdx.x == 0 && p.rstd) p.rstd[r] = rstd;
+    __syncthreads();  // the row's place is written again
   }
 }
 
@@ -942,6 +989,22 @@ cudaError_t run_pieces(const NormParams& p, int64_t pieces, cudaStream_t st) {
   return run_vec<T, P, RMS, CODES, SHIFTED, 0, 1024, 4>(p, st);
 }
 
+template <typename T, typename P>
+cudaError_t run_rms_any(const NormParams& p, cudaStream_t st) {
+  const int64_t bytes = p.H * (int64_t)sizeof(T);
+  if (bytes > kMaxStaged) {
+    rms_any_kernel<T, P, false><<<row_grid(p.rows), kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  static PerDeviceOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(rms_any_kernel<T, P, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStaged);
+  });
+  if (e != cudaSuccess) return e;
+  rms_any_kernel<T, P, true><<<row_grid(p.rows), kThreads, (size_t)bytes, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename T, typename P, bool RMS>
 cudaError_t run_forward(NormParams p, cudaStream_t st) {
   const int b = sizeof(T), n = 16 / b;
@@ -955,8 +1018,7 @@ cudaError_t run_forward(NormParams p, cudaStream_t st) {
     // whole pieces of codes: as wide as a row's pieces are long
     if (vec && pieces <= 4096 && (reinterpret_cast<uintptr_t>(p.codes) & (n - 1)) == 0)
       return run_pieces<T, P, RMS, RMS, false>(p, pieces, st);
-    row_norm_any_kernel<T, P, RMS><<<row_grid(p.rows), kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return run_rms_any<T, P>(p, st);
   }
   if (vec && pieces <= 4096)
     return run_pieces<T, P, RMS, false, false>(p, pieces, st);
@@ -965,7 +1027,8 @@ cudaError_t run_forward(NormParams p, cudaStream_t st) {
     if (p.res) p.cut = std::min(p.cut, first_cut_row(p.rows, p.sres, n));
     return run_pieces<T, P, RMS, false, true>(p, pieces + 1, st);  // a row may touch one more
   }
-  row_norm_any_kernel<T, P, RMS><<<row_grid(p.rows), kThreads, 0, st>>>(p);
+  if constexpr (RMS) return run_rms_any<T, P>(p, st);
+  row_norm_any_kernel<T, P><<<row_grid(p.rows), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -332,6 +332,13 @@ MOE_DEVICE void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0
                "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
 }
+// The same, added to what the tensor holds (fp32: to nearest even).
+MOE_DEVICE void tma_add_3d(const CUtensorMap* map, const void* src, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 MOE_DEVICE void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int N>
 MOE_DEVICE void bulk_wait_read() {  // all but the N newest groups have read their source
@@ -341,9 +348,6 @@ MOE_DEVICE void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" :::
 
 // Generic writes to shared memory before, reads by copies and MMAs after.
 MOE_DEVICE void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// The same for all memory.
-MOE_DEVICE void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // mbar_try_wait for arrivals from the other CTA of the cluster.
 MOE_DEVICE bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
