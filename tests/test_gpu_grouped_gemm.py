@@ -105,6 +105,24 @@ def test_against_64_bits(T, E, K, m, N, Kd, dtype):
         bu.assert_within(weight(moe, r, gy, x, out), ref, tu.gemm_tol(ref, most, rows, out))
 
 
+@pytest.mark.parametrize("N,Kd", [(256, 192), (65, 130)])
+@pytest.mark.parametrize("rows", [700, 769, 6000])
+def test_long_sums(rows, N, Kd):
+    """fp32 gradients of many rows. An addition inside the tensor cores cuts at most 2^-23 off the sum so far, whose mean
+    square grows in proportion to the rows, so that 48 steps of 16 rows are off by 48 * 2/3 * 2^-23 = 3.8e-6 of their sum
+    at the most; parts of that length are joined by roundings of 2^-24. One sum of 6000 rows could be 3e-5 off."""
+    moe = moe_mod()
+    r = tu.Routed(moe, rows, 1, 1, 1)
+    x, gy = r.rows(Kd, BF, 1), r.rows(N, BF, 2)
+    ref = tu.gemm_weight(r, gy, x)
+    got = weight(moe, r, gy, x, F32)
+    assert float((bu.f64(got) - ref).norm() / ref.norm()) <= 48 * 2 / 3 * 2.0 ** -23 + 8 * 2.0 ** -24
+    add = torch.randn(1, N, Kd, generator=torch.Generator().manual_seed(3)) * 100
+    both = weight(moe, r, gy, x, F32, add)
+    assert float((bu.f64(both) - ref - add).norm() / ref.norm()) <= 5e-6 + 8 * 2.0 ** -24 * float(add.norm() / ref.norm())
+    assert all(torch.equal(weight(moe, r, gy, x, F32, add), both) for _ in range(3))
+
+
 @pytest.mark.parametrize("N,Kd", [(128, 192), (264, 136), (33, 50)])
 def test_addend(N, Kd):
     """The addend joins the fp32 sum; it may be the gradient itself, which then gathers several calls."""
