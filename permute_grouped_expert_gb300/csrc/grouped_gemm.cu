@@ -41,7 +41,7 @@ constexpr int kPieceWarps = 8;  // that bring unaligned operands into place
 // Epilogue warps: with few steps along the contraction the rows' products wait for
 // them (5264 features of 64 for 15364 rows: four 124 us, eight 43).
 template <GemmDir DIR, bool PIECES>
-constexpr int kEpilogue = DIR == kWeight || PIECES ? 4 : 8;
+constexpr int kEpilogue = DIR == kWeight && !PIECES ? 4 : 8;
 template <GemmDir DIR, bool PIECES>
 constexpr int kThreads = 128 + 32 * (kEpilogue<DIR, PIECES> + (PIECES ? kPieceWarps : DIR == kWeight));
 // An MMA adds to its fp32 sums by cutting off, so that a long sum is short by about
@@ -82,7 +82,7 @@ constexpr int kTurn = 33;                               // and in pieces: a row 
 template <GemmDir DIR, bool PIECES>
 constexpr size_t kDynSmem = 1024 + (size_t)kStagesOf<DIR, PIECES> * kStageBytes +
                             (PIECES ? 2 * kRawOf<DIR> * kRawOperand : 0) +
-                            (DIR != kWeight ? 0 : PIECES ? 4 * 32 * kTurn * 4 : 8 * kOutBytes);
+                            (DIR != kWeight ? 0 : PIECES ? 8 * 32 * kTurn * 4 : 8 * kOutBytes);
 
 struct TcParams {
   const int32_t *offsets, *counts;
@@ -143,8 +143,10 @@ MOE_DEVICE int row_tiles(int64_t rows) { return (int)((rows + BN - 1) / BN); }
 MOE_DEVICE int tile_rows(int64_t rows, int tiles) { return (int)((rows + tiles - 1) / tiles + 31) & ~31; }
 
 // The order of the tiles.  Experts of up to BN rows cost their matrix's bytes, the
-// others products; one after another they would use HBM and the tensor cores in
-// turn, so the tiles of both kinds are dealt out evenly among each other.
+// others products.  The rows' products deal the tiles of both kinds out evenly among
+// each other, so that HBM and the tensor cores work together (FC1 of 8192 tokens, one
+// kind behind the other 3550 us, so 3481; by expert 3499 when that was 3315); the
+// weights' gradient takes the long tiles first (FC2's 1192 us, mixed 1220).
 struct Order {
   int tiles[2];            // of either kind: 0 products, 1 bytes
   int experts[2];
@@ -217,8 +219,12 @@ MOE_DEVICE Tile tile_of(int64_t t, const Order& o, const TcParams& p) {
     i.e = -1;
     return i;
   }
-  const int64_t s = (int64_t)((uint64_t)t * o.share >> 32);  // bytes' tiles before t
-  const int kind = (int64_t)((uint64_t)(t + 1) * o.share >> 32) > s ? 1 : 0;
+  // bytes' tiles before t, and before t + 1
+  auto bytes = [&](int64_t n) {
+    return DIR == kWeight ? max64(n - o.tiles[0], 0) : (int64_t)((uint64_t)n * o.share >> 32);
+  };
+  const int64_t s = bytes(t);
+  const int kind = bytes(t + 1) > s ? 1 : 0;
   const int at = (int)(kind ? s : t - s);
   const int x = expert_of_row(o.before[kind], o.experts[kind], at), local = at - o.before[kind][x];
   int64_t beg, end;
@@ -620,9 +626,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         t = then;
       }
     }
-  } else if (PIECES && warp >= 8) {
+  } else if (PIECES && warp >= 4 + kEpi) {
     // ------------------------------------------ operands brought into place
-    const int at = threadIdx.x - 256;
+    const int at = threadIdx.x - 32 * (4 + kEpi);
     int stage = 0, raw = 0;
     uint32_t phase = 0, raw_phase = 0;
     for (int i = 0, ok = 1; ok; i++) {
@@ -669,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         }
       }
     }
-  } else if (kW && warp == 8) {
+  } else if (kW && !PIECES && warp == 8) {
     // ---------------------------------------------------------- zeros (kWeight)
     int stage = 0;
     uint32_t phases = 0;  // bit s: parity of s_tail[s]
@@ -701,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     const int turn_of = (warp - 4) >> 2;  // of the warps with the same lanes
     constexpr int kTurns = kEpi / 4;
     uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (PIECES ? 2 * kRaw * kRawOperand : 0) +
-                     (size_t)(warp & 3) * (PIECES ? 32 * kTurn * 4 : 2 * kOutBytes);  // kWeight
+                     (size_t)(warp - 4) * (PIECES ? 32 * kTurn * 4 : 2 * kOutBytes);  // kWeight
     int out_at = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -726,9 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           const bool none = ti.end == ti.row;
           const int cols = min(p.Kd - ti.n * BN, BN), rows = min(p.N - f_warp, 32);
           const int64_t first = ((int64_t)ti.e * p.N + f_warp) * p.Kd + ti.n * BN;
-          // the parts before this one, or the caller's
-          const float* add = done ? static_cast<const float*>(p.out) : p.addend;
-          for (int c = 0; c < cols && rows > 0; c += 32) {
+          for (int c = 32 * turn_of; c < cols && rows > 0; c += 32 * kTurns) {
             float v[32];
             if (none) {
 #pragma unroll
@@ -740,15 +744,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
 #pragma unroll
             for (int j = 0; j < 32; j++) turn[lane * kTurn + j] = v[j];
             __syncwarp();
-            if (c + lane < cols) {
-              const int64_t at = first + c + lane;
-              OUT* to = static_cast<OUT*>(p.out) + at;
-#pragma unroll 8
-              for (int r = 0; r < rows; r++) {
-                float x = turn[r * kTurn + lane];
-                if (sizeof(OUT) == 4 && add) x += add[at + (int64_t)r * p.Kd];
-                to[(int64_t)r * p.Kd] = from_float<OUT>(x);
+            const int64_t at = first + c + lane;
+            OUT* to = static_cast<OUT*>(p.out) + at;
+            const int here = c + lane < cols ? rows : 0;
+            if (sizeof(OUT) == 4 && done) {  // added to the parts before, in memory
+#pragma unroll
+              for (int r = 0; r < 32; r++, to += p.Kd)
+                if (r < here) atomicAdd(reinterpret_cast<float*>(to), turn[r * kTurn + lane]);
+            } else if (sizeof(OUT) == 4 && p.addend) {
+              const float* add = p.addend + at;
+              for (int r0 = 0; r0 < here; r0 += 8) {  // eight summands on their way before the first is stored
+                float x[8];
+#pragma unroll
+                for (int r = 0; r < 8; r++) x[r] = r0 + r < here ? add[(int64_t)(r0 + r) * p.Kd] : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 8; r++)
+                  if (r0 + r < here) to[(int64_t)(r0 + r) * p.Kd] = from_float<OUT>(turn[(r0 + r) * kTurn + lane] + x[r]);
               }
+            } else {
+#pragma unroll
+              for (int r = 0; r < 32; r++, to += p.Kd)
+                if (r < here) *to = from_float<OUT>(turn[r * kTurn + lane]);
             }
           }
         } else if constexpr (kW) {
@@ -813,14 +829,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           // columns are rows of the result, lanes features
           const int f = f_warp + lane;
           T* out = static_cast<T*>(p.out) + f;
-          for (int c = 0; c < ti.cols; c += 32) {
+          for (int c = 32 * turn_of; c < ti.cols; c += 32 * kTurns) {
             float v[32];
             tmem_ld32(taddr + c, v);
+            T* to = out + (int64_t)(ti.row + c) * p.sout;
+            const int left = f < p.features ? ti.end - ti.row - c : 0;
 #pragma unroll
-            for (int j = 0; j < 32; j++) {
-              const int row = ti.row + c + j;
-              if (row < ti.end && f < p.features) out[(int64_t)row * p.sout] = from_float<T>(v[j]);
-            }
+            for (int j = 0; j < 32; j++, to += p.sout)
+              if (j < left) *to = from_float<T>(v[j]);
           }
         } else {
           // columns are rows of the result, lanes features: neighbouring lanes exchange
