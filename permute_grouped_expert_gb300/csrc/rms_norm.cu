@@ -12,7 +12,14 @@
 // less, and y need not be written for them.
 //
 // The kernels are the layer norm's (row_norm.cuh) with one reduction a row less.
-// HBM bounds them.
+// HBM bounds them.  Device times on one GB300 (share of a copy's rate):
+//   forward   8192 x 7168 bf16, residual, y and codes   87 us, 90 %
+//             65536 x 1024 residual and y 89 us, 88 %; codes in the place of y 102 us, 68 % (instructions)
+//             4096 x 4096 fp32, residual, y and codes   48 us, 88 %
+//             8000 x 1001 bf16 y 11.7 us, 40 %; with codes, element by element, 36 us
+//             one row of 7168, residual, y and codes    3.5 us (launch, one row's chain)
+//   backward  8192 x 7168 bf16 with the residual's gradient 75 us, 92 %
+//             65536 x 1024 87 us, 91 %; 4096 x 4096 fp32 45 us, 88 %
 #include "row_norm.cuh"
 
 namespace moe {

@@ -14,7 +14,7 @@
 // left alone.  On one GB300, device time and share of a copy's rate: 65536 routed
 // rows of I = 2048 in bf16 123 us forward (96 %) and 204 backward (97 %), 16384 of
 // I = 4096 in fp32 121 and 198 (98 and 99 %); 64 tokens of 8 experts each among 256
-// (512 routed rows of 8192) 6 us, launch and two chains of loads.
+// (512 routed rows of 8192) 6 and 10 us, launch and two chains of loads.
 #include "block_common.cuh"
 #include "moe_internal.h"
 
