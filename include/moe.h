@@ -755,7 +755,8 @@ MOE_API moe_status moe_grouped_gemm_backward_data(const moe_handle_dev* handle, 
  * the addend) for an expert without rows.  addend: device
  * fp32, laid out as grad_weight, only with MOE_ELEM_F32; it may be grad_weight
  * itself, which then gathers the gradients of several steps, and must not overlap
- * it otherwise.  Pad rows take no part, whatever they hold. */
+ * it otherwise.  Pad rows take no part, whatever they hold.  capacity: up to 2^27
+ * rows (MOE_ERR_UNSUPPORTED above). */
 MOE_API moe_status moe_grouped_gemm_backward_weight(const moe_handle_dev* handle, const moe_shape* shape,
                                                     const moe_layout* layout, const moe_gemm* gemm,
                                                     const moe_rows* x, const moe_rows* grad_y, int32_t grad_dtype,

@@ -300,6 +300,91 @@ def test_streams_and_graphs():
     assert_rows(b, y, tu.gemm_forward(b, w, xs[1]))
 
 
+@pytest.mark.parametrize("N,Kd", [(512, 256), (257, 255)])
+def test_two_calls_at_once(N, Kd):
+    """Calls on two streams, each with a workspace of its own, while the other's run."""
+    moe = moe_mod()
+    rs = [tu.Routed(moe, 900, 6, 2, 8, seed=k) for k in (1, 2)]
+    w = matrices(6, N, Kd, BF, 1, ints=2)
+    xs, gs = [r.rows(Kd, BF, 2, ints=2) for r in rs], [r.rows(N, BF, 3, ints=2) for r in rs]
+    wd, streams = w.cuda(), [torch.cuda.Stream() for _ in rs]
+    d = [dict(x=x.cuda(), gy=g.cuda(), y=torch.full((r.cap, N), 7.0, dtype=BF, device="cuda"),
+              gx=torch.full((r.cap, Kd), 7.0, dtype=BF, device="cuda"), gw=torch.empty(6, N, Kd, device="cuda"),
+              ws=tu.workspace(moe, r, N, Kd)) for r, x, g in zip(rs, xs, gs)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for r, t, s in zip(rs, d, streams):
+            at = r.handle, r.shape, r.layout
+            moe.moe_grouped_gemm(*at, wd, t["x"], t["y"], t["ws"], stream=s)
+            moe.moe_grouped_gemm_backward_data(*at, wd, t["gy"], t["gx"], t["ws"], stream=s)
+            moe.moe_grouped_gemm_backward_weight(*at, t["x"], t["gy"], t["gw"], t["ws"], stream=s)
+    torch.cuda.synchronize()
+    for r, t, x, g in zip(rs, d, xs, gs):
+        assert_rows(r, t["y"], tu.gemm_forward(r, w, x))
+        assert_rows(r, t["gx"], tu.gemm_data(r, w, g))
+        assert torch.equal(t["gw"].cpu(), tu.gemm_weight(r, g, x).float())
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    """Nothing of the calls' own setup needs a call outside a capture first."""
+    import os
+    import subprocess
+    import sys
+
+    code = '''
+import torch, train_util as tu
+from gpu_util import moe_mod
+moe = moe_mod()
+r = tu.Routed(moe, 40, 4, 2, 8)
+outs = []
+for N, Kd in ((64, 128), (33, 50)):
+    x, gy = r.rows(Kd, tu.BF, 1, ints=2), r.rows(N, tu.BF, 2, ints=2)
+    w = torch.randint(-2, 3, (4, N, Kd)).to(tu.BF)
+    outs.append((w, x, gy, w.cuda(), x.cuda(), gy.cuda(), torch.zeros(r.cap, N, dtype=tu.BF, device="cuda"),
+                 torch.zeros(4, N, Kd, device="cuda"), tu.workspace(moe, r, N, Kd)))
+h = torch.randn(8, 256, device="cuda")
+n, c, s = torch.empty_like(h), torch.empty(8, 256, dtype=torch.uint8, device="cuda"), torch.empty(8, 2, device="cuda")
+pre, act = torch.zeros(r.cap, 64, device="cuda"), torch.zeros(r.cap, 32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for w, x, gy, wd, xd, gd, y, gw, ws in outs:
+        moe.moe_grouped_gemm(r.handle, r.shape, r.layout, wd, xd, y, ws)
+        moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, xd, gd, gw, ws)
+    moe.moe_rms_norm(h, None, 1e-6, n, codes=c, scales=s)
+    moe.moe_swiglu(r.handle, r.shape, r.layout, pre, act)
+g.replay()
+torch.cuda.synchronize()
+for w, x, gy, wd, xd, gd, y, gw, ws in outs:
+    assert torch.equal(y.cpu()[r.routed], tu.gemm_forward(r, w, x)[r.routed].to(tu.BF))
+    assert torch.equal(gw.cpu(), tu.gemm_weight(r, gy, x).float())
+assert bool((n - h * (h.square().mean(1, keepdim=True) + 1e-6) ** -0.5).abs().max() < 1e-5)
+print("captured")
+'''
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, timeout=300)
+    assert p.returncode == 0 and "captured" in p.stdout, p.stdout + p.stderr
+
+
+@pytest.mark.parametrize("N,Kd", [(40, 24), (33, 17)])
+def test_one_row_of_any_stride(N, Kd):
+    """A buffer of one row has no stride that matters, zero and odd ones among them."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 1, 1, 1, 1)
+    w, x, gy = matrices(1, N, Kd, BF, 1, ints=2), r.rows(Kd, BF, 2, ints=2), r.rows(N, BF, 3, ints=2)
+    for stride in (0, 1, N + Kd, 1000003):
+        at = lambda t: t.cuda().as_strided(t.shape, (stride, 1))
+        y, gx = at(torch.zeros(1, N, dtype=BF)), at(torch.zeros(1, Kd, dtype=BF))
+        gw, ws = torch.empty(1, N, Kd, device="cuda"), tu.workspace(moe, r, N, Kd)
+        moe.moe_grouped_gemm(r.handle, r.shape, r.layout, w.cuda(), at(x), y, ws)
+        moe.moe_grouped_gemm_backward_data(r.handle, r.shape, r.layout, w.cuda(), at(gy), gx, ws)
+        moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, at(x), at(gy), gw, ws)
+        assert torch.equal(y.cpu(), tu.gemm_forward(r, w, x).to(BF))
+        assert torch.equal(gx.cpu(), tu.gemm_data(r, w, gy).to(BF))
+        assert torch.equal(gw.cpu(), tu.gemm_weight(r, gy, x).float())
+
+
 def test_refusals():
     moe = moe_mod()
     r = tu.Routed(moe, 10, 2, 1, 8)

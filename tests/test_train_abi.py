@@ -127,6 +127,14 @@ def test_grouped_gemm_backward_weight_refusals(moe):
               dict(gy=0), dict(ws=None)):
         assert call(**b) == moe.MOE_ERR_INVALID_ARG, b
     assert call(nbytes=need - 1) == moe.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert call(r=routed(moe, layout=moe._Layout(1, (1 << 27) + 1)), x=0x1000, gy=1 << 50, gw=1 << 52) == \
+        moe.MOE_ERR_UNSUPPORTED
+
+
+def test_more_tiles_than_can_be_counted_are_refused(moe):
+    layout, g = moe._Layout(1, (1 << 31) - 1), moe._Gemm(1 << 20, 1, 1)
+    assert moe.library().moe_grouped_gemm(*routed(moe, layout=layout), byref(g), FAKE, rows(moe, 1 << 50, 1),
+                                          rows(moe, 1 << 54, 1 << 20), FAKE, 1 << 20, None) == moe.MOE_ERR_INVALID_ARG
 
 
 def test_grouped_gemm_workspace_size(moe):
