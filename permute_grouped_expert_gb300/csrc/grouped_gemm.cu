@@ -104,6 +104,7 @@ struct TcParams {
   const float* addend;
   int64_t sout;
   int64_t cap;
+  int64_t routes;  // of all tokens
   int E;
   int features, contraction;  // rows' products
   int N, Kd;                  // kWeight
@@ -115,12 +116,12 @@ struct TcParams {
 };
 
 // Routed rows [beg, end) of expert e below the capacity; empty where the handle
-// holds no segment.
-MOE_DEVICE void gemm_segment(const int32_t* offsets, const int32_t* counts, int64_t cap, int e, int64_t& beg,
-                             int64_t& end) {
-  const int64_t off = offsets[e], cnt = counts[e];
-  beg = min64(max64(off, 0), cap);
-  end = off < 0 || cnt <= 0 ? beg : max64(min64(off + cnt, cap), beg);
+// holds no segment, and no more than the shape has routes (there are maps for no
+// more), whatever the handle says.
+MOE_DEVICE void gemm_segment(const TcParams& p, int e, int64_t& beg, int64_t& end) {
+  const int64_t off = p.offsets[e], cnt = min64(p.counts[e], p.routes);
+  beg = min64(max64(off, 0), p.cap);
+  end = off < 0 || cnt <= 0 ? beg : max64(min64(off + cnt, p.cap), beg);
 }
 
 // A tile as the pair's readers get it.
@@ -175,7 +176,7 @@ MOE_DEVICE void make_order(Order& o, const TcParams& p, int per) {
   const int lane = threadIdx.x & 31, run = (p.E + 31) / 32, e0 = lane * run, e1 = min(e0 + run, p.E);
   auto rows_of = [&](int e) {
     int64_t beg = 0, end = 0;
-    if (e < e1) gemm_segment(p.offsets, p.counts, p.cap, e, beg, end);
+    if (e < e1) gemm_segment(p, e, beg, end);
     return (int)(end - beg);
   };
   int tiles[2] = {0, 0}, experts[2] = {0, 0};
@@ -241,7 +242,7 @@ MOE_DEVICE Tile tile_of(int64_t t, const Order& o, const TcParams& p) {
   const int x = expert_of_row(o.before[kind], o.experts[kind], at), local = at - o.before[kind][x];
   int64_t beg, end;
   i.e = o.expert[kind][x];
-  gemm_segment(p.offsets, p.counts, p.cap, i.e, beg, end);
+  gemm_segment(p, i.e, beg, end);
   if (DIR == kWeight) {
     banded(local, p.mt, p.kt, i.m, i.n);
     i.row = (int)beg;
@@ -939,6 +940,7 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
   p.addend = g.addend;
   p.sout = g.sout;
   p.cap = g.cap;
+  p.routes = g.T * g.K;
   p.E = (int)g.E;
   p.N = (int)g.N;
   p.Kd = (int)g.Kd;
@@ -986,7 +988,7 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
   p.contraction = (int)(dir == kForward ? g.Kd : g.N);
   p.mt = (p.features + BM - 1) / BM;
   const bool fwd = dir == kForward;
-  const int64_t routes = g.T * g.K;
+  const int64_t routes = p.routes;
   const int64_t tiles = (routes / BN + (routes < g.E ? routes : g.E)) * p.mt;
   // up to 256 routes no expert has a second tile and every tile costs its weights:
   // in turn, without the counter and its clearing

@@ -255,6 +255,23 @@ def test_a_damaged_handle(N, Kd):
     assert torch.equal(weight(moe, r, gy, x, F32), gw)
 
 
+@pytest.mark.parametrize("N,Kd", [(136, 72), (33, 50)])
+@pytest.mark.parametrize("T", [1, 20, 150])
+def test_a_handle_of_more_tokens_than_the_shape(T, N, Kd):
+    """Each expert's rows end after as many as the shape has routes."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 600, 4, 2, 8)
+    w, x, gy = matrices(4, N, Kd, BF, 1, ints=2), r.rows(Kd, BF, 2, ints=2), r.rows(N, BF, 3, ints=2)
+    r.shape = moe.Shape(T, 128, 4, 2)
+    r.segments = [(e, b, min(n, b + 2 * T)) for e, b, n in r.segments]
+    r.routed = torch.zeros(r.cap, dtype=torch.bool)
+    for e, b, n in r.segments:
+        r.routed[b:n] = True
+    assert_rows(r, forward(moe, r, w, x), tu.gemm_forward(r, w, x))
+    assert_rows(r, data(moe, r, w, gy), tu.gemm_data(r, w, gy))
+    assert torch.equal(weight(moe, r, gy, x, F32).cpu(), tu.gemm_weight(r, gy, x).float())
+
+
 def test_streams_and_graphs():
     """Captured and replayed with other inputs and another routing, and on a stream of its own."""
     moe = moe_mod()
