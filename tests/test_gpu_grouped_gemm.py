@@ -201,6 +201,28 @@ def test_strides_and_alignment(N, Kd, pad, shift):
     assert torch.equal(gw.cpu(), tu.gemm_weight(r, gy, x).float())
 
 
+@pytest.mark.parametrize("N,Kd,stride", [(136, 72, 1 << 25), (33, 17, (1 << 25) + 1)])
+def test_offsets_beyond_32_bits(N, Kd, stride):
+    """Rows so far apart that their offsets pass 2^31 elements, 2^32 bytes."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 40, 2, 2, 8)
+    w, x, gy = matrices(2, N, Kd, BF, 1, ints=2), r.rows(Kd, BF, 2, ints=2), r.rows(N, BF, 3, ints=2)
+    assert (r.cap - 8) * stride > 1 << 31
+
+    def apart(t):
+        v = torch.empty((r.cap - 1) * stride + t.shape[1], dtype=BF, device="cuda").as_strided(t.shape, (stride, 1))
+        return v.copy_(t)
+
+    xd, gd, ws = apart(x), apart(gy), tu.workspace(moe, r, N, Kd)
+    y, gw = apart(torch.full((r.cap, N), 7.0)), torch.empty(2, N, Kd, device="cuda")
+    moe.moe_grouped_gemm(r.handle, r.shape, r.layout, w.cuda(), xd, y, ws)
+    assert_rows(r, y, tu.gemm_forward(r, w, x))
+    moe.moe_grouped_gemm_backward_data(r.handle, r.shape, r.layout, w.cuda(), gd, xd.fill_(7.0), ws)
+    assert_rows(r, xd, tu.gemm_data(r, w, gy))
+    moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, xd.copy_(x), gd, gw, ws)
+    assert torch.equal(gw.cpu(), tu.gemm_weight(r, gy, x).float())
+
+
 @pytest.mark.parametrize("N,Kd", [(256, 128), (77, 50)])
 def test_nonfinite_rows_and_weights_stay_alone(N, Kd):
     moe = moe_mod()

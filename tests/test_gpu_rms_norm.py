@@ -114,6 +114,33 @@ def test_rows_of_zeros_and_no_weight(H):
         assert bool((c[2, :128].float() == 0).all()) and float(sc[2, 0]) == 1.0
 
 
+@pytest.mark.parametrize("H,stride", [(256, 1 << 27), (515, (1 << 27) + 1)])
+def test_offsets_beyond_32_bits(H, stride):
+    """Rows so far apart that their offsets pass 2^31 elements: as any others."""
+    moe = moe_mod()
+    rows, dtype = 34, torch.bfloat16
+    x, w = inputs(rows, H, dtype, dtype)
+    res, gy = (bu.randn(rows, H, seed=s).to(dtype) for s in (7, 8))
+
+    def apart(t):
+        v = torch.empty((rows - 1) * stride + H, dtype=dtype, device="cuda").as_strided(t.shape, (stride, 1))
+        return v.copy_(t)
+
+    xd, rd, yd, rstd = apart(x), apart(res), apart(x), torch.empty(rows, device="cuda")
+    c = torch.empty(rows, H, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    sc = torch.empty(rows, -(-H // 128), device="cuda")
+    moe.moe_rms_norm(xd, w.cuda(), EPS, yd, residual=rd, sum_out=rd, rstd=rstd, codes=c, scales=sc)
+    h = (x.float() + res.float()).to(dtype)
+    assert torch.equal(rd.cpu(), h)
+    check((yd, None, rstd, c, sc), h, w)
+    ws = torch.empty(moe.moe_rms_norm_workspace_size(rows, H), dtype=torch.uint8, device="cuda")
+    gw, gxd = torch.empty(H, device="cuda"), yd
+    moe.moe_rms_norm_backward(xd.copy_(gy), rd, w.cuda(), rstd, gxd, grad_weight=gw, workspace=ws)
+    refs, tols = (f(gy, h, w, rstd.cpu(), None, *a) for f, a in ((tu.rms_backward, ()), (tu.rms_backward_tol, (dtype,))))
+    bu.assert_within(gxd, refs[0], tols[0], "gx")
+    bu.assert_within(gw, refs[1], tols[1], "gw")
+
+
 @pytest.mark.parametrize("H", [100, 2048])
 def test_nonfinite_rows_stay_alone(H):
     moe = moe_mod()

@@ -76,6 +76,27 @@ def test_gradient_against_differences(dtype):
     assert bool(((gp - diff).abs() <= 1e-5 * (1 + diff.abs()))[r.routed].all())
 
 
+@pytest.mark.parametrize("I,stride", [(64, 1 << 26), (33, (1 << 26) + 1)])
+def test_offsets_beyond_32_bits(I, stride):
+    """Rows so far apart that their offsets pass 2^31 elements: as rows that are close."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 40, 2, 2, 2)
+    pre, ga, p, dtype = r.rows(2 * I, torch.bfloat16, 1), r.rows(I, torch.bfloat16, 2), probs_of(r), torch.bfloat16
+    assert (r.cap - 2) * stride > 1 << 32
+
+    def apart(t):
+        v = torch.empty((r.cap - 1) * stride + t.shape[1], dtype=dtype, device="cuda").as_strided(t.shape, (stride, 1))
+        return v.copy_(t)
+
+    prd, gad, act = apart(pre), apart(ga), apart(torch.full((r.cap, I), 7.0))
+    moe.moe_swiglu(r.handle, r.shape, r.layout, prd, act, p.cuda())
+    assert torch.equal(act, run(moe, r, pre, p, dtype))
+    gp = torch.full((r.cap,), 7.0, device="cuda")
+    moe.moe_swiglu_backward(r.handle, r.shape, r.layout, prd, gad, prd, p.cuda(), gp)
+    want, want_p = run_backward(moe, r, pre, p, ga)
+    assert torch.equal(prd[r.routed.cuda()], want[r.routed.cuda()]) and torch.equal(gp, want_p)
+
+
 @pytest.mark.parametrize("dtype", bu.DTYPES)
 def test_gates_at_the_ends(dtype):
     """Gates far out: exp neither overflows nor cancels, and the gate's slope there is 0 or 1."""
