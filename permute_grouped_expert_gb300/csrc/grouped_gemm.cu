@@ -34,7 +34,7 @@
 //     its weights' gradient in fp32                  275 us,  72 %  stores beside the copies
 //   8192 x 8192 x 8192 over 8 experts                692 us,  84 %  MMAs (power), last tiles
 //     its weights' gradient in bf16 / fp32           743 / 959 us
-//   the same of 8191 x 8191                         1.96 ms,  30 %  shifting into place
+//   the same of 8191 x 8191                         1.61 ms,  36 %  shifting into place
 // An SM takes in 64 bytes a cycle at the most, which is what a whole tile needs at the
 // MMAs' full rate: tiles of fewer rows wait for their copies.
 #include <type_traits>
@@ -290,17 +290,14 @@ MOE_DEVICE void settle(uint64_t ns) {
 // most of it in the loads' issue.)  Beyond the end of the contraction are zeros; rows
 // and columns beyond the operand's give results that are not stored, whatever is there.
 
-// The eight elements from byte `from` of two pieces of 16 bytes on.
-MOE_DEVICE uint4 shifted(uint4 lo, uint4 hi, uint32_t from) {
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  const bool one = from & 4, two = from & 8;
+// The eight elements of two pieces of 16 bytes from word WORDS and `half` bits (0 or 16) on.
+template <int WORDS>
+MOE_DEVICE uint4 shifted(int4 lo, int4 hi, uint32_t half) {
+  const int w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t v[4];
 #pragma unroll
-  for (int i = 0; i < 7; i++) w[i] = one ? w[i + 1] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; i++) w[i] = two ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(w[i], w[i + 1], (from & 2) * 8);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; i++) v[i] = __funnelshift_r(w[WORDS + i], w[WORDS + i + 1], half);
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // Zeros from the n-th element on.
@@ -315,39 +312,58 @@ MOE_DEVICE uint4 first_of(uint4 v, int n) {
 // which a thread has eight elements of every 32nd.  KMAJOR: they are rows of the
 // operand; otherwise two runs of 64 columns along 64 rows.  From row to row of a
 // thread and from stage to stage lie multiples of eight rows and of 64 elements, so
-// that a thread's elements keep their place in their pieces.
+// that a thread's elements keep their place in their pieces.  A warp's rows are eight
+// apart too, so that one branch a stage finds the words of all its pieces, and reads of
+// an operand's pieces all go out before the first is written (8191 x 8191 x 8192:
+// 1.61 ms; four rows next to each other in a warp, each thread selecting its words,
+// 1.70; reading and writing in turn besides, 1.96).
 template <bool KMAJOR>
 struct Half {
   uint32_t raw;   // where this thread's first piece is in a stage
-  uint32_t from;  // byte of the piece
+  uint32_t from;  // byte of the piece, the same in a warp
   int k;          // of the contraction left: elements from this thread's first on, or rows
-  int count;      // rows in shared memory, of 32 each
 
-  // KMAJOR: rows from `row` on, `used` of them, along k elements; otherwise columns
+  // Of a thread: its warp's, and eight apart.
+  static MOE_DEVICE int first_row(int t) { return (t >> 5) + (t & 24); }
+
+  // KMAJOR: rows from `row` on along k elements; otherwise columns
   // from `col` on, along k rows from `row` on.
-  MOE_DEVICE void begin_tile(const uint16_t* base, int64_t stride, int64_t row, int col, int contraction, int used, int t) {
-    const int q = t & 7, j = t >> 3, eighth = (int)((row + j) & 7);
-    from = (uint32_t)(reinterpret_cast<uintptr_t>(base + (row + j) * stride) & 15);
+  MOE_DEVICE void begin_tile(const uint16_t* base, int64_t stride, int64_t row, int col, int contraction, int t) {
+    const int q = t & 7, j = first_row(t), eighth = (int)((row + j) & 7);
+    from = __shfl_sync(0xffffffffu, (uint32_t)(reinterpret_cast<uintptr_t>(base + (row + j) * stride) & 15), 0);
     raw = eighth * kRawEighth<KMAJOR> + (uint32_t)(((row + j) >> 3) - ((row - eighth + 7) >> 3)) * kRawRow<KMAJOR> + q * 16;
     k = contraction - (KMAJOR ? q * 8 : j);
-    count = (used + 31) / 32;
+  }
+
+  // (all 128 rows whatever the tile's: a branch for fewer costs whole tiles 8 %)
+  template <int WORDS>
+  MOE_DEVICE void shift_by(uint8_t* to, const uint8_t* at, bool whole) {
+    int4 lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint8_t* piece = at + (KMAJOR ? 4 * i * kRawRow<true> : 4 * (i & 1) * kRawRow<false> + 128 * (i >> 1));
+      lo[i] = ld_shared_v4(piece), hi[i] = ld_shared_v4(piece + 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      uint4 v = shifted<WORDS>(lo[i], hi[i], (from & 2) * 8);
+      if (!whole) v = first_of(v, KMAJOR ? k : k > 32 * (i & 1) ? 8 : 0);
+      st_shared_v4(to + 32 * i * 128, v);
+    }
   }
 
   MOE_DEVICE void shift(uint8_t* to, const uint8_t* stage, int t) {
-    const int q = t & 7, j = t >> 3;
+    const int q = t & 7, j = first_row(t);
     to += j * 128 + ((q ^ (j & 7)) * 16);
     const uint8_t* at = stage + raw;
     // a warp's elements are all of the contraction
     const bool whole = __all_sync(0xffffffffu, KMAJOR ? k >= 8 : k > 32);
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-      if (i < count) {
-        const uint4* piece =
-            reinterpret_cast<const uint4*>(at + (KMAJOR ? 4 * i * kRawRow<true> : 4 * (i & 1) * kRawRow<false> + 128 * (i >> 1)));
-        uint4 v = shifted(piece[0], piece[1], from);
-        if (!whole) v = first_of(v, KMAJOR ? k : k > 32 * (i & 1) ? 8 : 0);
-        *reinterpret_cast<uint4*>(to + 32 * i * 128) = v;
-      }
+    switch (from >> 2) {
+      case 0: shift_by<0>(to, at, whole); break;
+      case 1: shift_by<1>(to, at, whole); break;
+      case 2: shift_by<2>(to, at, whole); break;
+      default: shift_by<3>(to, at, whole);
+    }
     k -= BK;
   }
 };
@@ -651,15 +667,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
       Half<DIR == kForward> a;
       Half<!kW> b;
       if (kW) {
-        a.begin_tile(p.a, p.sa, ti.row, f0, ti.end - ti.row, 128, at);
-        b.begin_tile(p.b, p.sb, ti.row, c0, ti.end - ti.row, 128, at);
+        a.begin_tile(p.a, p.sa, ti.row, f0, ti.end - ti.row, at);
+        b.begin_tile(p.b, p.sb, ti.row, c0, ti.end - ti.row, at);
       } else {
         const int64_t w = (int64_t)ti.e * p.N;
         if (DIR == kForward)
-          a.begin_tile(p.a, p.sa, w + f0, 0, p.contraction, 128, at);
+          a.begin_tile(p.a, p.sa, w + f0, 0, p.contraction, at);
         else
-          a.begin_tile(p.a, p.sa, w, f0, p.contraction, 128, at);
-        b.begin_tile(p.b, p.sb, ti.row + (int)rank * half, 0, p.contraction, half, at);
+          a.begin_tile(p.a, p.sa, w, f0, p.contraction, at);
+        b.begin_tile(p.b, p.sb, ti.row + (int)rank * half, 0, p.contraction, at);
       }
       for (int kb = 0; kb < ti.blocks; kb++) {
         const bool both = mbar_wait(&s_raw[raw], raw_phase, abort_flag, p.status) &&

@@ -392,6 +392,12 @@ MOE_DEVICE void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// A write to this CTA's shared memory, made where it stands.
+MOE_DEVICE void st_shared_v4(void* p, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(p)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // 32 bytes written to shared memory of the cluster, and the mbarrier that counts
 // them there (one arrival, 32 bytes).
 MOE_DEVICE void send_32(uint32_t to, uint32_t bar, int4 a, int4 b) {
