@@ -459,6 +459,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     return ti.e >= 0;
   };
 
+  // Waits until the MMAs have read every stage that was filled, `stage` being the next:
+  // the commits that say so arrive by themselves, in the other CTA of the pair too, and
+  // neither may leave before its last one has (a stage that was never filled counts as
+  // read).
+  auto all_consumed = [&](int stage, uint32_t phase) {
+    for (int s = 0; s < kStages; s++) {
+      if (!mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status)) return false;
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    return true;
+  };
+
   // Parts of a tile's contraction that are summed on their own.
   auto parts_of = [](int blocks) {
     constexpr int kMost = kPart<DIR, OUT>;
@@ -502,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           }
         }
       }
-      if (!ok) settle(2000000);  // 2 ms: far longer than any single copy takes
+      if (!ok || *abort_flag) settle(2000000);  // 2 ms: far longer than any single copy takes
     }
   } else if (warp == 0 || warp == 3) {
     // ------------------------------------------------------- TMA producers
@@ -569,6 +584,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           }
         }
       }
+      ok = ok && !*abort_flag;
+      if (first) ok = ok && all_consumed(stage, phase);
       if (!ok) {
         if (rank == 0) {
           for (int s = 0; s < kStages; s++) {
@@ -631,11 +648,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           }
         }
       }
-      if (!ok) {
+      if (!ok || *abort_flag) {
         mma_commit_pair(&s_drain, 0x1);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(&s_drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
+        settle(2000000);  // the arrivals of the commits before it, in the other CTA too
       }
     }
   } else if (warp == 2) {
@@ -704,6 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         }
       }
     }
+    if (warp == 4 + kEpi && !*abort_flag) all_consumed(stage, phase);
   } else if (kW && !PIECES && warp == 8) {
     // ---------------------------------------------------------- zeros (kWeight)
     int stage = 0;

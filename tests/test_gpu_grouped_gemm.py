@@ -364,6 +364,28 @@ def test_two_calls_at_once(N, Kd):
         assert torch.equal(t["gw"].cpu(), tu.gemm_weight(r, g, x).float())
 
 
+@pytest.mark.parametrize("N,Kd", [(264, 136), (65, 33)])
+def test_short_calls_behind_one_another(N, Kd):
+    """Calls of a tile or two, each pair of SMs leaving as soon as its last results are stored: the commits of its last
+    stages have arrived in both CTAs by then."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 40, 3, 2, 8, empty=(1,))
+    w = matrices(3, N, Kd, BF, 1, ints=2)
+    x, gy = r.rows(Kd, BF, 2, ints=2), r.rows(N, BF, 3, ints=2)
+    wd, xd, gd, ws = w.cuda(), x.cuda(), gy.cuda(), tu.workspace(moe, r, N, Kd)
+    y, gx = (torch.full((r.cap, c), 7.0, dtype=BF, device="cuda") for c in (N, Kd))
+    gw = torch.empty(3, N, Kd, device="cuda")
+    for _ in range(200):
+        moe.moe_grouped_gemm(r.handle, r.shape, r.layout, wd, xd, y, ws)
+        moe.moe_grouped_gemm_backward_data(r.handle, r.shape, r.layout, wd, gd, gx, ws)
+        moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, xd, gd, gw, ws)
+    torch.cuda.synchronize()
+    assert int(r.handle.status.item()) == 0
+    assert_rows(r, y, tu.gemm_forward(r, w, x))
+    assert_rows(r, gx, tu.gemm_data(r, w, gy))
+    assert torch.equal(gw.cpu(), tu.gemm_weight(r, gy, x).float())
+
+
 def test_first_calls_of_a_process_in_a_capture():
     """Nothing of the calls' own setup needs a call outside a capture first."""
     import os
