@@ -10,9 +10,8 @@
 // to 256.  kData reads W as it lies, its features contiguous (an M-major operand),
 // so that no transposed copy exists.  The weights' gradient has 256 x 256 tiles of
 // the matrix and runs along the expert's rows, both operands with M and N
-// contiguous; its last 16 rows may reach into rows that are not the expert's: those
-// are overwritten with zeros in shared memory between the copy and the MMA (they
-// may hold anything, NaN too).
+// contiguous; rows that are not the expert's (they may hold anything, NaN too) are
+// never read: the copies of an expert's last rows end with them, zeros in front.
 //
 // Per CTA, warp-specialised (rank 0 leads the pair):
 //   warps 0, 3  TMA producers of its half of the first and of the second operand, 64 of
@@ -21,8 +20,8 @@
 //               gradient waited for)
 //   warp 1      TMEM; on the leader one elected lane issues the MMAs
 //   warp 2      on the leader: claims tiles and hands their numbers to both CTAs
-//   warps 4..7  epilogue of this CTA's 128 features, beside the next tile's MMAs
-//   warp 8      kWeight: zeros behind an expert's last row
+//   warps 4..   epilogue of this CTA's 128 features, beside the next tile's MMAs
+//   PIECES: the last eight warps bring operands into place
 // Every wait is bounded (MOE_DEV_ERR_TIMEOUT, then a clean exit).
 //
 // Device times on one GB300, beside the floor by a copy's 6796 GB/s or 1880 TFLOP/s
@@ -56,7 +55,7 @@ constexpr int kPieceWarps = 8;  // that bring unaligned operands into place
 template <GemmDir DIR, bool PIECES>
 constexpr int kEpilogue = DIR == kWeight && !PIECES ? 4 : 8;
 template <GemmDir DIR, bool PIECES>
-constexpr int kThreads = 128 + 32 * (kEpilogue<DIR, PIECES> + (PIECES ? kPieceWarps : DIR == kWeight));
+constexpr int kThreads = 128 + 32 * (kEpilogue<DIR, PIECES> + (PIECES ? kPieceWarps : 0));
 // An MMA adds to its fp32 sums by cutting off, so that a long sum is short by about
 // 2^-26 a step of 16.  fp32 gradients are sums of parts of at most this many stages
 // (768 rows), added to one another by rounding on their way to memory: off by 7e-7 in
@@ -260,10 +259,6 @@ MOE_DEVICE Tile tile_of(int64_t t, const Order& o, const TcParams& p) {
   return i;
 }
 
-// Whether the last stage of a kWeight tile holds rows that are not the expert's
-// within its last 16.
-MOE_DEVICE bool ragged(const Tile& i) { return ((i.end - i.row) & 15) != 0; }
-
 template <typename T>
 MOE_DEVICE uint32_t pack2(float a, float b);
 template <>
@@ -385,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
   constexpr int kEpi = kEpilogue<DIR, PIECES>;
   constexpr bool kW = DIR == kWeight, kAmn = DIR != kForward, kBmn = kW;
   extern __shared__ uint8_t dyn_smem[];
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tail[kStages], s_tfull[2], s_tempty[2];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tfull[2], s_tempty[2];
   __shared__ __align__(8) uint64_t s_raw[kRaw], s_raw_free[kRaw];  // PIECES, each CTA's own
   __shared__ __align__(8) uint64_t s_have[kSlots], s_free[kSlots], s_drain;
   __shared__ Tile s_tile[kSlots];
@@ -402,11 +397,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int s = 0; s < kStages; s++) {
-      // on the leader: its producer (and, kWeight, a second arrival) and both CTAs'
-      // bytes, or both CTAs' warp 8 after the zeros; PIECES: every loading warp of both
-      mbar_init(&s_full[s], PIECES ? 2 * kPieceWarps : kW ? 2 : 1);
+      // on the leader: its producer and both CTAs' bytes; PIECES: every warp that fills it
+      mbar_init(&s_full[s], PIECES ? 2 * kPieceWarps : 1);
       mbar_init(&s_empty[s], 1);  // each CTA's own, by the leader's commit
-      mbar_init(&s_tail[s], 1);   // each CTA's own bytes of a stage that gets zeros
     }
     for (int a = 0; a < 2; a++) {
       mbar_init(&s_tfull[a], 1);
@@ -414,8 +407,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     }
     for (int s = 0; s < kSlots; s++) {
       mbar_init(&s_have[s], 1);
-      // the MMA's, and in each CTA the producers, the epilogue's and the others'
-      mbar_init(&s_free[s], 1 + 2 * (2 + kEpi + (PIECES ? kPieceWarps : kW)));  // on the leader: every reader of both CTAs
+      // on the leader, every reader of both CTAs: its warp 1, and in each the producers,
+      // the epilogue's and the pieces' warps
+      mbar_init(&s_free[s], 1 + 2 * (2 + kEpi + (PIECES ? kPieceWarps : 0)));
     }
     for (int s = 0; s < kRaw; s++) {
       mbar_init(&s_raw[s], 1);
@@ -546,25 +540,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
             break;
           }
           uint8_t* to = smem + (size_t)stage * kStageBytes + (first ? 0 : kOperand);
-          const bool tail = kW && kb == nkb - 1 && ragged(ti);
-          uint32_t bar;
-          if (tail) {
-            bar = mapa_shared(smem_u32(&s_tail[stage]), rank);
-            if (first) mbar_arrive_expect_tx(&s_tail[stage], bytes);
-          } else {
-            bar = mapa_shared(smem_u32(&s_full[stage]), 0);
-            if (first && rank == 0) {
-              mbar_arrive_expect_tx(&s_full[stage], 2 * bytes);
-              if (kW) mbar_arrive(&s_full[stage]);
-            }
-          }
+          const uint32_t bar = mapa_shared(smem_u32(&s_full[stage]), 0);
+          if (first && rank == 0) mbar_arrive_expect_tx(&s_full[stage], 2 * bytes);
           const int k0 = kb * BK;
           if (kW) {
+            const int from = ti.row + k0, before = min(ti.end - from - BK, 0);  // rows of zeros in front, negative
             if (groups) {
-              tma_load_3d_pair(to, map, 0, ti.row + k0, f0 / 64, bar);
+              tma_load_4d_pair(to, map, 0, before, from, f0 / 64, bar);
             } else {
-              tma_load_2d_pair(to, map, f0, ti.row + k0, bar);
-              tma_load_2d_pair(to + kBox, map, f0 + 64, ti.row + k0, bar);
+              tma_load_3d_pair(to, map, f0, before, from, bar);
+              tma_load_3d_pair(to + kBox, map, f0 + 64, before, from, bar);
             }
           } else if (!first) {
             tma_load_2d_pair(to, map, k0, row, bar);
@@ -576,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
             tma_load_3d_pair(to, map, f0, k0, ti.e, bar);
             tma_load_3d_pair(to + kBox, map, f0 + 64, k0, ti.e, bar);
           }
-          issued[stage] = !tail;
+          issued[stage] = true;
           issued_parity[stage] = phase;
           if (++stage == kStages) {
             stage = 0;
@@ -629,11 +614,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
             const uint64_t bdesc = kBmn ? smem_desc_sw128_mn(sb, kBox) : smem_desc_sw128(sb);
             // a step of 16: 32 bytes of K-major rows, or 16 rows of 128 bytes
             constexpr uint64_t kAstep = kAmn ? 128 : 2, kBstep = kBmn ? 128 : 2;
+            // the last stage's steps that hold anything: its first ones, or (kWeight,
+            // not PIECES) those behind the zeros
             const int left = kW ? (ti.end - ti.row) - kb * BK : p.contraction - kb * BK;
+            constexpr bool kZerosFirst = kW && !PIECES;
+            const int begin = kZerosFirst && left < BK ? (BK - left) / 16 : 0;
 #pragma unroll
             for (int k = 0; k < BK / 16; k++)
-              if (k * 16 < left)
-                mma_bf16_pair(d_tmem, adesc + kAstep * k, bdesc + kBstep * k, idesc, kb > kb0 || k > 0 ? 1u : 0u);
+              if (kZerosFirst ? k >= begin : k * 16 < left)
+                mma_bf16_pair(d_tmem, adesc + kAstep * k, bdesc + kBstep * k, idesc, kb > kb0 || k > begin ? 1u : 0u);
             mma_commit_pair(&s_empty[stage], 0x3);
             if (++stage == kStages) {
               stage = 0;
@@ -710,7 +699,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&s_raw_free[raw]);
-          mbar_arrive_remote(mapa_shared(smem_u32(&s_full[stage]), 0));
+          if (rank == 0)
+            mbar_arrive(&s_full[stage]);
+          else
+            mbar_arrive_leader(mapa_shared(smem_u32(&s_full[stage]), 0));
         }
         if (++raw == kRaw) {
           raw = 0;
@@ -723,32 +715,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
       }
     }
     if (warp == 4 + kEpi && !*abort_flag) all_consumed(stage, phase);
-  } else if (kW && !PIECES && warp == 8) {
-    // ---------------------------------------------------------- zeros (kWeight)
-    int stage = 0;
-    uint32_t phases = 0;  // bit s: parity of s_tail[s]
-    for (int i = 0;; i++) {
-      Tile ti;
-      if (!take_tile_warp(i, ti)) break;
-      const int nkb = ti.blocks;
-      if (nkb && ragged(ti)) {
-        const int s = (stage + nkb - 1) % kStages;
-        int ok = 0;
-        if (lane == 0) ok = mbar_wait(&s_tail[s], (phases >> s) & 1, abort_flag, p.status) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        phases ^= 1u << s;
-        const int rows = (ti.end - ti.row) - (nkb - 1) * BK, stop = (rows + 15) & ~15;
-        uint8_t* base = smem + (size_t)s * kStageBytes;
-        for (int j = lane; j < (stop - rows) * 8 * 4; j += 32) {  // 16 bytes each of the four boxes' rows
-          const int box = j & 3, at = j >> 2;
-          *reinterpret_cast<uint4*>(base + box * kBox + rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&s_full[s]), 0));
-      }
-      stage = (stage + nkb) % kStages;
-    }
   } else {
     // ---------------------------------------------------------- epilogue
     const int lane_base = 32 * (warp & 3);
@@ -1007,12 +973,8 @@ cudaError_t run(GemmDir dir, const GroupedGemm& g, cudaStream_t st) {
     }
     p.a_groups = g.N % 64 == 0;
     p.b_groups = g.Kd % 64 == 0;
-    e = p.a_groups ? make_tensor_map_row_groups(&maps.a[0], g.a, type, g.cap, g.N, g.sa, BK)
-                   : make_tensor_map_rows(&maps.a[0], g.a, type, g.cap, g.N, g.sa, BK, 64);
-    if (e != cudaSuccess) return e;
-    e = p.b_groups ? make_tensor_map_row_groups(&maps.b[0], g.b, type, g.cap, g.Kd, g.sb, BK)
-                   : make_tensor_map_rows(&maps.b[0], g.b, type, g.cap, g.Kd, g.sb, BK, 64);
-    if (e != cudaSuccess) return e;
+    if ((e = make_tensor_map_row_windows(&maps.a[0], g.a, type, g.cap, g.N, g.sa, BK)) != cudaSuccess) return e;
+    if ((e = make_tensor_map_row_windows(&maps.b[0], g.b, type, g.cap, g.Kd, g.sb, BK)) != cudaSuccess) return e;
     if ((e = make_tensor_map_matrices(&maps.out, g.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, f32 ? 4 : 2, g.E, g.N,
                                       g.Kd, 32, f32 ? 32 : 64)) != cudaSuccess)
       return e;

@@ -379,10 +379,14 @@ MOE_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* 
   }
 }
 
-// Arrive on an mbarrier of the cluster, behind this thread's writes to its own
-// CTA's shared memory.
-MOE_DEVICE void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrive on an mbarrier of the cluster behind the writes to this CTA's shared memory
+// that this thread made or met at a barrier, and nothing else: unlike
+// mbar_arrive_cluster it does not wait for accesses to global memory.
+MOE_DEVICE void mbar_arrive_leader(uint32_t cluster_addr) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
 }
 
 // Arrive on an mbarrier of the cluster without ordering this thread's memory

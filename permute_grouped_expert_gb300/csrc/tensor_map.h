@@ -65,13 +65,19 @@ inline cudaError_t make_tensor_map_rows(CUtensorMap* map, const void* base, CUte
   return make_tensor_map(map, base, dtype, 2, dims, strides, box);
 }
 
-// The same with columns in groups of 64 (cols a multiple of 64): boxes of two groups
-// of box_rows rows, one group after the other in shared memory.
-inline cudaError_t make_tensor_map_row_groups(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
-                                              uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows) {
-  const cuuint64_t dims[3] = {64, rows, cols / 64}, strides[2] = {row_bytes(rows, cols, stride), 128};
-  const cuuint32_t box[3] = {64, box_rows, 2};
-  return make_tensor_map(map, base, dtype, 3, dims, strides, box);
+// The same as windows of box_rows rows, one from each row on: coordinates (column,
+// row of the window, first row).  A box that begins at a negative row of its window
+// has zeros in front of the rows from the first on, and ends where the window would
+// go on: no row behind is read.  Boxes of 64 columns, or, where cols is a multiple of
+// 64, columns in groups of 64 (their number is a fourth coordinate) and boxes of two
+// groups, one after the other in shared memory.
+inline cudaError_t make_tensor_map_row_windows(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
+                                               uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows) {
+  const bool groups = cols % 64 == 0;
+  const uint64_t apart = row_bytes(rows, cols, stride);
+  const cuuint64_t dims[4] = {groups ? 64 : cols, box_rows, rows, cols / 64}, strides[3] = {apart, apart, 128};
+  const cuuint32_t box[4] = {64, box_rows, 1, 2};
+  return make_tensor_map(map, base, dtype, groups ? 4 : 3, dims, strides, box);
 }
 
 // Every eighth row of a row matrix that starts anywhere, from row `first` on: such

@@ -87,6 +87,52 @@ def test_more_tiles_than_run_at_once(T, E, K, m, N, Kd, skew):
     assert torch.equal(weight(moe, r, gy, x, F32).cpu(), gw.float())
 
 
+@pytest.mark.parametrize("T,E,K,m,N,Kd,skew,empty", [(3000, 16, 4, 32, 1025, 513, 0.0, (5,)), (2500, 3, 1, 8, 2311, 329, 0.0, ()),
+                                                     (5000, 40, 2, 1, 521, 265, 1.2, (0, 39)), (9000, 7, 1, 1, 1537, 1001, 0.0, (3,)),
+                                                     (2000, 200, 3, 4, 515, 259, 0.5, (7, 8))])
+def test_unaligned_more_tiles_than_run_at_once(T, E, K, m, N, Kd, skew, empty):
+    """Operands shifted into place in several tiles of each pair of SMs, some dealt from the counter: odd and even numbers
+    of stages a tile, so that every ring goes on in the next tile where it stood, and experts without rows between."""
+    moe = moe_mod()
+    r = tu.Routed(moe, T, E, K, m, skew=skew, empty=empty)
+    w = matrices(E, N, Kd, BF, 1, ints=2)
+    x, gy = r.rows(Kd, BF, 2, ints=2), r.rows(N, BF, 3, ints=2)
+    assert_rows(r, forward(moe, r, w, x), tu.gemm_forward(r, w, x))
+    assert_rows(r, data(moe, r, w, gy), tu.gemm_data(r, w, gy))
+    gw = tu.gemm_weight(r, gy, x)
+    assert torch.equal(weight(moe, r, gy, x, BF).cpu(), gw.to(BF))
+    assert torch.equal(weight(moe, r, gy, x, F32).cpu(), gw.float())
+    assert int(r.handle.status.item()) == 0
+
+
+@pytest.mark.parametrize("N,Kd", [(128, 64), (264, 136), (320, 520), (65, 33)])
+def test_every_length_of_an_expert(N, Kd):
+    """Experts of 0 to 150 rows, with and without pad rows between (NaN in all of those): every number of rows in the last
+    stage along an expert's rows, the buffer's first rows and its last ones among them."""
+    moe = moe_mod()
+    E = 151
+    counts, pads = np.arange(E)[::-1].copy(), np.arange(E) % 3
+    counts[0], counts[-1] = 1, 37  # the first rows, and the last ones of the buffer
+    pads[-1] = 0
+    r = tu.Routed(moe, int(counts.sum()) + 8, E, 1, 2)
+    off = np.concatenate([[0], np.cumsum(counts + pads)]).astype(np.int32)
+    r.cap = int(off[-1])
+    r.layout = moe.Layout(1, r.cap)
+    r.handle.padded_offsets.copy_(torch.from_numpy(off))
+    r.handle.tokens_per_expert.copy_(torch.from_numpy(counts.astype(np.int32)))
+    r.segments = [(e, int(off[e]), int(off[e] + counts[e])) for e in range(E)]
+    r.routed = torch.zeros(r.cap, dtype=torch.bool)
+    for _, b, n in r.segments:
+        r.routed[b:n] = True
+    w = matrices(E, N, Kd, BF, 1, ints=2)
+    x, gy = r.rows(Kd, BF, 2, ints=2), r.rows(N, BF, 3, ints=2)
+    gw = tu.gemm_weight(r, gy, x)
+    assert torch.equal(weight(moe, r, gy, x, F32).cpu(), gw.float())
+    assert torch.equal(weight(moe, r, gy, x, BF).cpu(), gw.to(BF))
+    assert_rows(r, forward(moe, r, w, x), tu.gemm_forward(r, w, x))
+    assert_rows(r, data(moe, r, w, gy), tu.gemm_data(r, w, gy))
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("T,E,K,m,N,Kd", [(1, 8, 2, 32, 264, 2048), (50, 6, 2, 8, 384, 512), (333, 4, 2, 1, 129, 257),
                                           (900, 2, 1, 32, 256, 640)])
