@@ -409,7 +409,7 @@ moe_status moe_grouped_gemm_backward_weight(const moe_handle_dev* handle, const 
   if (grad_dtype != gemm->dtype && grad_dtype != MOE_ELEM_F32) return MOE_ERR_INVALID_ARG;
   const int gb = elem_bytes(grad_dtype);
   const int64_t cap = layout->capacity, n = shape->E * gemm->N * gemm->Kd;
-  // a tile runs along all of an expert's rows, and the kernel's waits for it are bounded
+  // a tile runs along all of an expert's rows: two seconds on its pair of SMs at this many
   if (cap > (int64_t(1) << 27)) return MOE_ERR_UNSUPPORTED;
   if (!rows_ok(x, cap, gemm->Kd, 2) || !rows_ok(grad_y, cap, gemm->N, 2)) return MOE_ERR_INVALID_ARG;
   if (!grad_weight || !aligned_to(grad_weight, gb)) return MOE_ERR_INVALID_ARG;

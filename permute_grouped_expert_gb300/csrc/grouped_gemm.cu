@@ -22,7 +22,8 @@
 //   warp 2      on the leader: claims tiles and hands their numbers to both CTAs
 //   warps 4..   epilogue of this CTA's 128 features, beside the next tile's MMAs
 //   PIECES: the last eight warps bring operands into place
-// Every wait is bounded (MOE_DEV_ERR_TIMEOUT, then a clean exit).
+// Every wait is bounded (MOE_DEV_ERR_TIMEOUT, then a clean exit); those that a whole
+// tile may take go on as long as its stages do.
 //
 // Device times on one GB300, beside the floor by a copy's 6796 GB/s or 1880 TFLOP/s
 // and what bounds them:
@@ -385,17 +386,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
   __shared__ __align__(8) uint64_t s_have[kSlots], s_free[kSlots], s_drain;
   __shared__ Tile s_tile[kSlots];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_filled;  // s_filled: stages copied by warp 0, ever
   __shared__ Order s_order;  // the leader's
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  volatile int* abort_flag = &s_abort;
+  volatile int *abort_flag = &s_abort, *filled = &s_filled;
 
   if (threadIdx.x == 0) {
-    s_abort = 0;
+    s_abort = s_filled = 0;
     for (int s = 0; s < kStages; s++) {
       // on the leader: its producer and both CTAs' bytes; PIECES: every warp that fills it
       mbar_init(&s_full[s], PIECES ? 2 * kPieceWarps : 1);
@@ -431,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
   // The i-th tile of this pair; waits for it, reads it and, once, says so.
   auto next_tile = [&](int i, Tile& ti) {
     const int s = i % kSlots;
-    if (!mbar_wait_cluster(&s_have[s], (i / kSlots) & 1, abort_flag, p.status)) return false;
+    if (!mbar_wait_cluster(&s_have[s], (i / kSlots) & 1, abort_flag, p.status, filled)) return false;
     const int4 a = ld_shared_v4(&s_tile[s]), b = ld_shared_v4(reinterpret_cast<const int4*>(&s_tile[s]) + 1);
     ti.e = a.x, ti.m = a.y, ti.n = a.z, ti.row = a.w;
     ti.end = b.x, ti.cols = b.y, ti.blocks = b.z;
@@ -495,6 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           uint8_t* to = smem + (size_t)kStages * kStageBytes + (size_t)(2 * stage + (first ? 0 : 1)) * kRawOperand;
           const int k0 = kb * BK;
           if (first) {
+            *filled = *filled + 1;
             mbar_arrive_expect_tx(&s_raw[stage], kBytes);
             if (DIR == kForward)
               copy_eighths<true>(to, maps.a, w + f0, k0, &s_raw[stage]);
@@ -541,6 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           }
           uint8_t* to = smem + (size_t)stage * kStageBytes + (first ? 0 : kOperand);
           const uint32_t bar = mapa_shared(smem_u32(&s_full[stage]), 0);
+          if (first) *filled = *filled + 1;
           if (first && rank == 0) mbar_arrive_expect_tx(&s_full[stage], 2 * bytes);
           const int k0 = kb * BK;
           if (kW) {
@@ -654,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         const int s = i % kSlots;
         const int64_t then = p.next ? atomicAdd(p.next, 1) : t + clusters;  // on its way meanwhile
         const Tile ti = tile_of<DIR>(t, s_order, p);
-        if (!mbar_wait_cluster(&s_free[s], ((i / kSlots) & 1) ^ 1, abort_flag, p.status)) break;
+        if (!mbar_wait_cluster(&s_free[s], ((i / kSlots) & 1) ^ 1, abort_flag, p.status, filled)) break;
         for (uint32_t r = 0; r < 2; r++)
           send_32(mapa_shared(smem_u32(&s_tile[s]), r), mapa_shared(smem_u32(&s_have[s]), r),
                   make_int4(ti.e, ti.m, ti.n, ti.row), make_int4(ti.end, ti.cols, ti.blocks, 0));
@@ -733,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
       const int f_warp = ti.m * BM + (int)rank * 128 + lane_base;  // first feature of this warp
       for (int done = 0; done < parts; done++) {
         int there = 0;
-        if (lane == 0) there = mbar_wait(&s_tfull[acc], acc_phase, abort_flag, p.status) ? 1 : 0;
+        if (lane == 0) there = mbar_wait(&s_tfull[acc], acc_phase, abort_flag, p.status, filled) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, there, 0)) {
           ok = false;
           break;

@@ -17,7 +17,10 @@ namespace moe {
 
 // Bounded waits give up after this many nanoseconds of %globaltimer; the wait
 // then records MOE_DEV_ERR_TIMEOUT and returns, so no kernel can hang the GPU.
-constexpr uint64_t kWaitLimitNs = 2000ull * 1000ull * 1000ull;
+#ifndef MOE_WAIT_LIMIT_NS
+#define MOE_WAIT_LIMIT_NS 2000000000ull
+#endif
+constexpr uint64_t kWaitLimitNs = MOE_WAIT_LIMIT_NS;
 
 MOE_DEVICE int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 MOE_DEVICE int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }

@@ -45,23 +45,37 @@ MOE_DEVICE bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Wait for the phase of `bar` with the given parity to complete.  Gives up
-// after kWaitLimitNs, or as soon as another role raised *abort; on giving up it
-// raises *abort, records MOE_DEV_ERR_TIMEOUT in *status and returns false.
-MOE_DEVICE bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+template <typename F>
+MOE_DEVICE bool wait_bounded(F&& done, volatile int* abort, int32_t* status, const volatile int* progress) {
+  uint64_t t0 = globaltimer_ns();
+  int seen = progress ? *progress : 0;
   for (uint32_t it = 1;; it++) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (done()) return true;
     if ((it & 63) == 0) {
       if (*abort) return false;
       if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (progress && *progress != seen) {
+          seen = *progress;
+          t0 = globaltimer_ns();
+          continue;
+        }
         *abort = 1;
         set_status(status, MOE_DEV_ERR_TIMEOUT);
         return false;
       }
     }
   }
+}
+
+// Wait for the phase of `bar` with the given parity to complete.  Gives up
+// after kWaitLimitNs, or as soon as another role raised *abort; on giving up it
+// raises *abort, records MOE_DEV_ERR_TIMEOUT in *status and returns false.  With
+// `progress`, which other roles count up in steps that are short and come to an end,
+// the limit is that of the time since it last changed.
+MOE_DEVICE bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
+                          const volatile int* progress = nullptr) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_bounded([&] { return mbar_try_wait(bar, parity); }, abort, status, progress);
 }
 
 // mbar_wait for long waits: sleeps `sleep_ns` between polls instead of spinning,
@@ -363,20 +377,10 @@ MOE_DEVICE bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
 }
 
 // mbar_wait for arrivals from the other CTA of the cluster.
-MOE_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+MOE_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
+                                  const volatile int* progress = nullptr) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; it++) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 63) == 0) {
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        set_status(status, MOE_DEV_ERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
+  return wait_bounded([&] { return mbar_try_wait_cluster(bar, parity); }, abort, status, progress);
 }
 
 // Arrive on an mbarrier of the cluster behind the writes to this CTA's shared memory

@@ -474,6 +474,74 @@ print("captured")
     assert p.returncode == 0 and "captured" in p.stdout, p.stdout + p.stderr
 
 
+def test_tiles_that_take_longer_than_a_wait_may(tmp_path):
+    """Built with a limit of 3 ms on a wait without progress, gradients whose tile of 2^21 rows takes 10 ms (aligned) to
+    30 ms are whole: the roles that wait for the tile go on while its stages do. (With the limit of 2 s that is a tile of
+    2^27 rows, which the call accepts.)"""
+    import concurrent.futures as cf
+    import os
+    import subprocess
+    import sys
+
+    from permute_grouped_expert_gb300 import _build as b
+
+    def compile_one(src):
+        short = os.path.basename(src) == "grouped_gemm.cu"
+        kept = os.path.join(b.BUILD, os.path.basename(src) + ".o")
+        if not short and os.path.exists(kept) and os.path.getmtime(kept) >= max(map(os.path.getmtime, b._deps())):
+            return kept
+        obj = str(tmp_path / (os.path.basename(src) + ".o"))
+        limit = ["-DMOE_WAIT_LIMIT_NS=3000000ull"] if short else []
+        subprocess.run([b.nvcc(), *b.ARCH, *b.FLAGS, *limit, "-c", src, "-o", obj], check=True)
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        objs = list(ex.map(compile_one, b._sources()))
+    lib = str(tmp_path / "libmoe_short_waits.so")
+    subprocess.run([b.nvcc(), *b.ARCH, "-shared", "-o", lib, *objs, "-lcudart"], check=True)
+    code = """
+import ctypes, sys
+real = ctypes.CDLL
+ctypes.CDLL = lambda path, *a, **k: real(sys.argv[1] if str(path).endswith("libmoe_gb300.so") else path, *a, **k)
+import numpy as np, torch, train_util as tu
+from gpu_util import moe_mod
+moe = moe_mod()
+rows, few, E = 1 << 21, 100, 5
+r = tu.Routed(moe, 64, E, 1, 1)
+counts = np.array([0, rows, 0, few, 0], np.int32)
+off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+cap = int(off[-1])
+shape, layout = moe.Shape(cap, 128, E, 1), moe.Layout(1, cap)
+r.handle.padded_offsets.copy_(torch.from_numpy(off))
+r.handle.tokens_per_expert.copy_(torch.from_numpy(counts))
+r.handle.status.zero_()
+g = torch.Generator(device="cuda").manual_seed(1)
+for N, Kd in ((33, 17), (64, 40), (257, 24)):
+    x, gy = (torch.randint(-1, 2, (cap, c), generator=g, device="cuda").to(tu.BF) for c in (Kd, N))
+    ref = torch.zeros(E, N, Kd, dtype=torch.float64, device="cuda")
+    for e in (1, 3):
+        ref[e] = gy[off[e]:off[e + 1]].double().T @ x[off[e]:off[e + 1]].double()
+    ws = torch.empty(moe.moe_grouped_gemm_workspace_size(shape, layout, N, Kd), dtype=torch.uint8, device="cuda")
+    for dtype in (tu.BF, tu.F32):
+        gw = torch.empty(E, N, Kd, dtype=dtype, device="cuda")
+        moe.moe_grouped_gemm_backward_weight(r.handle, shape, layout, x, gy, gw, ws)
+        torch.cuda.synchronize()
+        a, z = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        moe.moe_grouped_gemm_backward_weight(r.handle, shape, layout, x, gy, gw, ws)
+        z.record()
+        torch.cuda.synchronize()
+        assert int(r.handle.status.item()) == 0, (N, Kd, dtype)
+        assert torch.equal(gw, ref.to(dtype)), (N, Kd, dtype)
+        assert a.elapsed_time(z) > 3.0, "a tile shorter than the limit shows nothing"
+print("whole")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    p = subprocess.run([sys.executable, "-c", code, lib], capture_output=True, text=True, env=env, timeout=300)
+    assert p.returncode == 0 and "whole" in p.stdout, p.stdout + p.stderr
+
+
 @pytest.mark.parametrize("N,Kd", [(40, 24), (33, 17)])
 def test_one_row_of_any_stride(N, Kd):
     """A buffer of one row has no stride that matters, zero and odd ones among them."""
