@@ -725,7 +725,10 @@ MOE_API moe_status moe_grouped_gemm_workspace_size(const moe_shape* shape, const
 /* y[r] = W[e] x[r] for every routed row r of expert e below the capacity: FC1
  * (whose output moe_swiglu_backward needs, and which moe_grouped_mlp does not
  * keep) or FC2 of an expert MLP.  Sums in fp32, rounded to dtype once, in an
- * order fixed by the sizes and the routing: repeated calls agree bit for bit.
+ * order fixed by the sizes and the routing: repeated calls agree bit for bit.  The
+ * tensor cores cut what an addition cannot hold, so that a sum of numbers of one sign
+ * comes out short, by 5e-5 of itself at 8192 numbers (f16; bf16 by less); longer sums
+ * are made of parts of up to 8192, added by rounding, and are short by no more.
  * x: capacity rows of Kd, y: capacity rows of N.  shape: T, E and K are read.  Pad
  * rows take no part and are not written, nor are rows at or beyond the capacity;
  * any segment may be empty.  A NaN or infinity of a row stays in it, one of a weight
@@ -749,9 +752,10 @@ MOE_API moe_status moe_grouped_gemm_backward_data(const moe_handle_dev* handle, 
 /* Gradient of the weights:
  *   grad_weight[e][n][k] = sum over the routed rows r of e below the capacity of
  *                          grad_y[r][n] * x[r][k]  (+ addend[e][n][k])
- * Sums in fp32, rounded to grad_dtype (dtype or MOE_ELEM_F32) once; fp32 gradients
- * are summed 768 rows at a time, and these parts added in order by roundings to
- * nearest (a subnormal part may count as zero).  Every element is written, zeros (or
+ * Sums in fp32, rounded to grad_dtype (dtype or MOE_ELEM_F32) once, in parts as in
+ * moe_grouped_gemm; fp32 gradients are summed 768 rows at a time (short by 4e-6), and
+ * these parts added in order by roundings to nearest (a subnormal part may count as
+ * zero).  Every element is written, zeros (or
  * the addend) for an expert without rows.  addend: device
  * fp32, laid out as grad_weight, only with MOE_ELEM_F32; it may be grad_weight
  * itself, which then gathers the gradients of several steps, and must not overlap

@@ -57,13 +57,18 @@ template <GemmDir DIR, bool PIECES>
 constexpr int kEpilogue = DIR == kWeight && !PIECES ? 4 : 8;
 template <GemmDir DIR, bool PIECES>
 constexpr int kThreads = 128 + 32 * (kEpilogue<DIR, PIECES> + (PIECES ? kPieceWarps : 0));
-// An MMA adds to its fp32 sums by cutting off, so that a long sum is short by about
-// 2^-26 a step of 16.  fp32 gradients are sums of parts of at most this many stages
-// (768 rows), added to one another by rounding on their way to memory: off by 7e-7 in
-// the 2-norm whatever the rows, where one part of 8192 rows would be by some 1e-5.
-// 8192 x 8192 of 1024 rows an expert take 959 us so, 867 in one part.
+// An MMA cuts off what its fp32 sum cannot hold, of each product too: 768 numbers of
+// one sign come out short by 5e-7 in bf16 and 4e-6 in f16 (whose products have more
+// bits to lose), 8192 by 4e-5 and 5e-5.  So sums are made of parts, added to one another
+// by rounding, and no shorter however long they are.  fp32 gradients: parts of at most
+// 12 stages (768 rows), added on their way to memory; 8192 x 8192 of 1024 rows an expert
+// take 959 us so, 867 in one part.  Results of 16 bits: parts of 128 stages, a tenth of
+// f16's rounding each, joined in TMEM by the epilogue (one sum of 2^20 was short by
+// 7e-3; 2048 x 2048 x 65536 over 2 experts: 363 us, in one part 358).
 template <GemmDir DIR, typename OUT>
-constexpr int kPart = DIR == kWeight && sizeof(OUT) == 4 ? 12 : 1 << 30;
+constexpr bool kJoin = DIR != kWeight || sizeof(OUT) == 2;
+template <GemmDir DIR, typename OUT>
+constexpr int kPart = kJoin<DIR, OUT> ? 128 : 12;
 constexpr int BM = 256, BN = 256, BK = 64;  // of a pair's tile; BK: of a stage
 // Tiles that may be on their way to the readers: more where tiles are short, fewer
 // where the last ones would wait behind long ones.
@@ -273,6 +278,17 @@ MOE_DEVICE uint32_t pack2<__half>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 32 columns of TMEM added to 32 others, by a warp whose lanes they are.
+MOE_DEVICE void add_columns(uint32_t to, uint32_t from) {
+  float a[32], b[32];
+  uint32_t sum[32];
+  tmem_ld32(to, a);
+  tmem_ld32(from, b);
+#pragma unroll
+  for (int j = 0; j < 32; j++) sum[j] = __float_as_uint(a[j] + b[j]);
+  tmem_st32(to, sum);
+}
+
 MOE_DEVICE void settle(uint64_t ns) {
   const uint64_t t0 = globaltimer_ns();
   while (globaltimer_ns() - t0 < ns) __nanosleep(1000);
@@ -474,6 +490,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     constexpr int kMost = kPart<DIR, OUT>;
     return blocks <= kMost ? 1 : (blocks + kMost - 1) / kMost;
   };
+  // TMEM buffer of a part, `first` being that of the tile's first: the other one in turn,
+  // or, where parts are joined there, the first keeps the sum and the others meet the
+  // epilogue in the other.  The next tile begins in the one that the last part left free.
+  auto buffer_of = [](int first, int part) {
+    return kJoin<DIR, OUT> ? first ^ (part > 0 ? 1 : 0) : first ^ (part & 1);
+  };
 
   if (PIECES && (warp == 0 || warp == 3)) {
     // --------------------------------- producers of the operands as they lie
@@ -591,8 +613,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     // One elected lane waits and issues, the others stay at the end: known to be one,
     // it needs no care for others that might issue another MMA.
     if (rank == 0 && elect_one_lane()) {
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      int stage = 0, acc = 0;  // acc: of the tile's first part
+      uint32_t phase = 0, acc_phases = 0;
       bool ok = true;
       for (int i = 0; ok; i++) {
         Tile ti;
@@ -600,12 +622,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         const int nkb = ti.blocks, parts = parts_of(nkb), part = (nkb + parts - 1) / parts;
         const uint32_t idesc = idesc_16bit(BM, (uint32_t)ti.cols, std::is_same<T, __nv_bfloat16>::value, kAmn, kBmn);
         for (int kb0 = 0, done = 0; done < parts; kb0 += part, done++) {
-          if (!mbar_wait_cluster(&s_tempty[acc], acc_phase ^ 1, abort_flag, p.status)) {
+          const int now = buffer_of(acc, done);
+          if (!mbar_wait_cluster(&s_tempty[now], (acc_phases >> now & 1) ^ 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+          const uint32_t d_tmem = tmem_base + (uint32_t)(now * BN);
           for (int kb = kb0; kb < min(kb0 + part, nkb); kb++) {
             if (!mbar_wait_cluster(&s_full[stage], phase, abort_flag, p.status)) {
               ok = false;
@@ -633,12 +656,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
             }
           }
           if (!ok) break;
-          mma_commit_pair(&s_tfull[acc], 0x3);
-          if (++acc == 2) {
-            acc = 0;
-            acc_phase ^= 1;
-          }
+          mma_commit_pair(&s_tfull[now], 0x3);
+          acc_phases ^= 1u << now;
         }
+        acc = buffer_of(acc, parts - 1) ^ 1;
       }
       if (!ok || *abort_flag) {
         mma_commit_pair(&s_drain, 0x1);
@@ -726,23 +747,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     uint8_t* s_out = smem + (size_t)kStages * kStageBytes + (PIECES ? 2 * kRaw * kRawOperand : 0) +
                      (size_t)(warp - 4) * (PIECES ? 32 * kTurn * 4 : 2 * kOutBytes);  // kWeight
     int out_at = 0;
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    int acc = 0;  // of the tile's first part
+    uint32_t acc_phases = 0;
+    // the loads from this buffer are done; stores to memory may still be on their way
+    auto release = [&](int at) {
+      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&s_tempty[at]), 0));
+    };
     bool ok = true;
     for (int i = 0; ok; i++) {
       Tile ti;
       if (!take_tile_warp(i, ti)) break;
       const int parts = parts_of(ti.blocks);
+      const uint32_t tsum = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
       const int f_warp = ti.m * BM + (int)rank * 128 + lane_base;  // first feature of this warp
       for (int done = 0; done < parts; done++) {
         int there = 0;
-        if (lane == 0) there = mbar_wait(&s_tfull[acc], acc_phase, abort_flag, p.status, filled) ? 1 : 0;
+        const int now = buffer_of(acc, done);
+        if (lane == 0) there = mbar_wait(&s_tfull[now], acc_phases >> now & 1, abort_flag, p.status, filled) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, there, 0)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
+        acc_phases ^= 1u << now;
+        uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(now * BN);
+        if (kJoin<DIR, OUT> && parts > 1) {
+          if (done) {
+            for (int c = 32 * turn_of; c < ti.cols; c += 32 * kTurns) add_columns(tsum + c, taddr + c);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            release(now);
+          }
+          if (done < parts - 1) continue;
+          taddr = tsum;
+        }
         if constexpr (kW && PIECES) {
           // 32 columns of 32 rows at a time, turned in shared memory
           float* turn = reinterpret_cast<float*>(s_out);
@@ -791,7 +830,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
           const int n = f_warp + lane;
           const float* add = p.addend && !done ? p.addend + ((int64_t)ti.e * p.N + n) * p.Kd + ti.n * BN : nullptr;
           // this part is added to the one before, once that has been written
-          if (done && lane == 0) bulk_wait_all();
+          if (!kJoin<DIR, OUT> && done && lane == 0) bulk_wait_all();
           const int cols = min(p.Kd - ti.n * BN, BN);
           for (int c = 0; c < cols && f_warp < p.N; c += kCols) {
             uint4 piece[8];
@@ -834,7 +873,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
             fence_async_shared();
             __syncwarp();
             if (lane == 0) {
-              if (done)
+              if (!kJoin<DIR, OUT> && done)
                 tma_add_3d(&maps.out, buf, ti.n * BN + c, f_warp, ti.e);
               else
                 tma_store_3d(&maps.out, buf, ti.n * BN + c, f_warp, ti.e);
@@ -877,13 +916,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         }
         tc_fence_before();
         __syncwarp();
-        // the loads from TMEM are done; stores to memory may still be on their way
-        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&s_tempty[acc]), 0));
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1;
-        }
+        release(kJoin<DIR, OUT> ? acc : now);
       }
+      acc = buffer_of(acc, parts - 1) ^ 1;
     }
   }
 

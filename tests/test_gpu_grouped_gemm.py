@@ -169,6 +169,79 @@ def test_long_sums(rows, N, Kd):
     assert all(torch.equal(weight(moe, r, gy, x, F32, add), both) for _ in range(3))
 
 
+def one_expert(moe, rows):
+    """A routing of `rows` rows of one expert, without the arrays that the products do not read."""
+    r = tu.Routed(moe, 8, 1, 1, 1)
+    r.cap, r.shape, r.layout = rows, moe.Shape(rows, 128, 1, 1), moe.Layout(1, rows)
+    r.handle.padded_offsets.copy_(torch.tensor([0, rows], dtype=torch.int32))
+    r.handle.tokens_per_expert.fill_(rows)
+    return r
+
+
+def positive(rows, cols, dtype, seed, long_rows):
+    """Numbers between 2^-5 and 2^-3, with a scale of its own for each line that is summed along: sums as wide apart as
+    a power of two, so that their roundings to 16 bits are spread evenly."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    u = torch.rand(rows, cols, generator=g, device="cuda") * 0.5 + 0.5
+    line = torch.exp2(torch.rand(rows if long_rows else cols, generator=g, device="cuda"))
+    return (u * (line[:, None] if long_rows else line[None]) * 2.0 ** -4).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n,few,cols", [(1 << 20, 24, 40), ((1 << 20) - 1, 19, 33), (40000, 300, 264)])
+def test_long_sums_in_16_bits(n, few, cols, dtype):
+    """Sums of n numbers of one sign, rounded to 16 bits once: parts of 8192, each addition inside the tensor cores cutting
+    at most 2^-23 off the part's sum so far, which is half the part on average, so that 2^-11 of the result may be
+    missing; up to 128 parts are joined by roundings of 2^-24, half of which reach the whole sum. The mean over the
+    results has that bound without their own rounding, up to four of its standard deviations. (One sum of 2^20 may be
+    short by 2^-4 by the same bound, and was by 2^-7.)"""
+    moe = moe_mod()
+    short = 2.0 ** -11 + 64 * 2.0 ** -24
+
+    def check(got, ref):
+        assert bool(((bu.f64(got) - bu.f64(ref)).abs() <= short * bu.f64(ref) + bu.rounding(bu.f64(ref), dtype)).all())
+        rel = (got.double() / ref - 1).mean().abs().item()
+        assert rel <= short + 4 * torch.finfo(dtype).eps / 2 / 3 ** 0.5 / ref.numel() ** 0.5, rel
+
+    r = one_expert(moe, n)  # the weights' gradient, along n rows
+    x, gy = positive(n, cols, dtype, 1, False), positive(n, few, dtype, 2, False)
+    gw = torch.empty(1, few, cols, dtype=dtype, device="cuda")
+    ws = tu.workspace(moe, r, few, cols)
+    moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, x, gy, gw, ws)
+    check(gw[0], gy.double().T @ x.double())
+    r = one_expert(moe, few)
+    x, w = positive(few, n, dtype, 3, True), positive(cols, n, dtype, 4, True)[None]
+    y = torch.empty(few, cols, dtype=dtype, device="cuda")
+    moe.moe_grouped_gemm(r.handle, r.shape, r.layout, w, x, y, ws)
+    check(y, x.double() @ w[0].double().T)
+    w = w[0].T.contiguous()[None]
+    moe.moe_grouped_gemm_backward_data(r.handle, r.shape, r.layout, w, x, y, ws)
+    check(y, x.double() @ w[0].double())
+
+
+@pytest.mark.parametrize("rows,wide,n", [(600, 8192, 33000), (600, 8191, 33001), (300, 20000, 16385), (40, 19000, 49160)])
+def test_long_sums_of_more_tiles_than_run_at_once(rows, wide, n):
+    """Sums in three to seven parts, of several tiles a pair of SMs, on whole numbers: parts joined beside the next tile."""
+    moe = moe_mod()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").to(BF)
+    times = lambda a, b: (a.float() @ b.float()).to(BF)  # whole numbers below 2^24: exact in any order
+    r = one_expert(moe, rows)
+    ws = tu.workspace(moe, r, wide, n)
+    w, x, y = ints(1, wide, n), ints(rows, n), torch.empty(rows, wide, dtype=BF, device="cuda")
+    moe.moe_grouped_gemm(r.handle, r.shape, r.layout, w, x, y, ws)
+    assert torch.equal(y, times(x, w[0].T))
+    w = w[0].T.contiguous()[None]
+    moe.moe_grouped_gemm_backward_data(r.handle, r.shape, r.layout, w, x, y, ws)
+    assert torch.equal(y, times(x, w[0]))
+    del w, x, y
+    r = one_expert(moe, n)
+    x, gy = ints(n, 2056 + wide % 2), ints(n, 2312 + wide % 2)
+    gw = torch.empty(1, gy.shape[1], x.shape[1], dtype=BF, device="cuda")
+    moe.moe_grouped_gemm_backward_weight(r.handle, r.shape, r.layout, x, gy, gw, ws)
+    assert torch.equal(gw[0], times(gy.T, x))
+
+
 @pytest.mark.parametrize("N,Kd", [(128, 192), (264, 136), (33, 50)])
 def test_addend(N, Kd):
     """The addend joins the fp32 sum; it may be the gradient itself, which then gathers several calls."""
