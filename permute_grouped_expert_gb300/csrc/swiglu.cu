@@ -12,7 +12,7 @@
 // Each element is read and written once (3 values forward, 5 backward): HBM bounds
 // both.  A team of threads takes a routed row; pad rows are known by token_of and
 // left alone.  On one GB300, device time and share of a copy's rate: 65536 routed
-// rows of I = 2048 in bf16 123 us forward (96 %) and 204 backward (97 %), 16384 of
+// rows of I = 2048 in bf16 123 us forward (96 %) and 207 backward (95 %), 16384 of
 // I = 4096 in fp32 121 and 198 (98 and 99 %); 64 tokens of 8 experts each among 256
 // (512 routed rows of 8192) 6 and 10 us, launch and two chains of loads.
 #include "block_common.cuh"
@@ -74,13 +74,17 @@ struct Gate {
 };
 
 // For 16-bit rows the exponential and the quotient are CUDA's fast ones, below
-// (10 + 2.4 |g|) 2^-24 of s together, far below the result's rounding; the full ones
-// would be what bounds the kernels (65536 x 2048 bf16: 215 us, so 132; backward 282
-// and 228).  fp32 rows have half the elements a byte and take the full ones.
-template <typename T>
+// (10 + 2.4 |g|) 2^-24 of s together, far below the rounding of the 16-bit results; the
+// full ones would be what bounds the kernels (65536 x 2048 bf16: 215 us, so 132; backward
+// 282 and 228).  Backward the exponential is the full one all the same: the gradient of
+// the probabilities is fp32 whatever the rows, and has 12 2^-24 of s so whatever g (with
+// the fast one 55 2^-24 was seen at g = -60; 206.5 us for 204, 4096 x 8 x 1024 60 for
+// 56; with the full quotient too 252).  fp32 rows have half the elements a byte and take
+// both.
+template <typename T, bool FULL_EXP>
 MOE_DEVICE Gate gate_of(float g) {
   constexpr bool kFast = sizeof(T) == 2;
-  const float z = kFast ? __expf(-fabsf(g)) : expf(-fabsf(g));
+  const float z = kFast && !FULL_EXP ? __expf(-fabsf(g)) : expf(-fabsf(g));
   const float r = kFast ? __fdividef(1.0f, 1.0f + z) : 1.0f / (1.0f + z);
   const float zr = z * r;
   return g < 0.0f ? Gate{zr, r} : Gate{r, zr};
@@ -107,7 +111,7 @@ MOE_DEVICE void routed_rows(const SwigluParams& p, int64_t first, int64_t step, 
 // TEAM threads a row: a warp, or the CTA.  A thread's loads of a batch of pieces are
 // all on their way before it stores the first result, which the compiler may not do
 // by itself.  Pieces of a batch: two of a 16-bit row forward (65536 x 2048: 123 us,
-// four 129) and four of the others (backward 204, two 231; fp32 forward 121 and 131).
+// four 129) and four of the others (backward 204 then, two 231; fp32 forward 121 and 131).
 template <typename T, int N, int TEAM>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluParams p) {
   using R = typename Raw<T, N>::type;
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(SwigluParams p) {
           unpack<T, N>(u, ru[j]);
           unpack<T, N>(g, rg[j]);
 #pragma unroll
-          for (int i = 0; i < N; i++) u[i] = prob * (g[i] * gate_of<T>(g[i]).s * u[i]);
+          for (int i = 0; i < N; i++) u[i] = prob * (g[i] * gate_of<T, false>(g[i]).s * u[i]);
           *reinterpret_cast<R*>(a + c0 + j * kStep) = pack<T, N>(u);
         }
     }
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(SwigluParams p) {
           unpack<T, N>(d, rd[j]);
 #pragma unroll
           for (int i = 0; i < N; i++) {
-            const Gate q = gate_of<T>(g[i]);
+            const Gate q = gate_of<T, true>(g[i]);
             const float act = g[i] * q.s;
             sum = fmaf(d[i], act * u[i], sum);
             d[i] *= prob;

@@ -55,6 +55,24 @@ def test_forward_and_backward(T, E, K, m, I, dtype):
 
 
 @pytest.mark.parametrize("dtype", bu.DTYPES)
+@pytest.mark.parametrize("I", [1, 8, 40])
+def test_gradient_of_the_probabilities_at_any_gate(I, dtype):
+    """fp32 whatever the rows: sums of one term, exact but for it. The term's error does not grow with the gate: the full
+    exponential to 2 ulp (4 U), 1 + z to U and z's 2 U, the quotient to 2 ulp (4 U) and its product to U (s to 12 U), then
+    three products: 15 U, and U for terms of the second order."""
+    moe = moe_mod()
+    r = tu.Routed(moe, 3000, 4, 1, 1)
+    g = torch.Generator().manual_seed(1)
+    pre, ga = torch.zeros(r.cap, 2 * I), torch.rand(r.cap, I, generator=g) + 1
+    pre[:, 0] = torch.rand(r.cap, generator=g) + 1
+    pre[:, I:] = torch.rand(r.cap, I, generator=g) * 90 - 70
+    pre, ga = pre.to(dtype), ga.to(dtype)
+    _, ref, _, _ = tu.swiglu_backward(pre, None, ga)
+    gp = run_backward(moe, r, pre, None, ga)[1]
+    check(r, gp, ref, 16 * bu.U * ref.abs())
+
+
+@pytest.mark.parametrize("dtype", bu.DTYPES)
 def test_gradient_against_differences(dtype):
     """Central differences of the 64-bit forward: the gradient is that of what the forward computes."""
     moe = moe_mod()
