@@ -496,10 +496,18 @@ def _address(buf: bytearray) -> int:
     return ctypes.addressof(ctypes.c_char.from_buffer(buf))
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype):
+def _on_device(t: torch.Tensor, name: str, device: Optional[int]):
+    """device: the current one, where a call wants its tensors there; None: any."""
+    if device is None:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: device tensor expected")
+    elif t.get_device() != device:
+        raise ValueError(f"{name}: a tensor of the current device (cuda:{device}) expected, got {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: Optional[int] = None):
     """Address and row stride of a 2-D tensor with unit column stride; its rows may lie apart."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: device tensor expected")
+    _on_device(t, name, device)
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     if t.dtype is not dtype:
@@ -513,14 +521,13 @@ def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype):
 _ABSENT = (0, 0)
 
 
-def _dense(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
+def _dense(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, device: Optional[int] = None):
     """Address of a contiguous tensor of this shape and type."""
     if t is None:
         return None
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: device tensor expected")
+    _on_device(t, name, device)
     if not t.is_contiguous():
         raise ValueError(f"{name}: contiguous tensor expected")
     return t.data_ptr()
@@ -721,6 +728,7 @@ def moe_quantize_w4_rows(w: torch.Tensor, group: int, codes: torch.Tensor, scale
 
 
 # ------------------------------------- root-mean-square norm, expert training
+# These calls run on the current device and refuse tensors of another one.
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
@@ -735,21 +743,22 @@ def moe_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, y:
     what the backward reads."""
     shape, dtype = _matrix(x, "x"), x.dtype
     pdtype = _param_dtype(x, weight, None)
-    x_rows = _rows(x, "x", shape, dtype)
-    _on_current_device(x, "x")
+    device = torch.cuda.current_device()
+    x_rows = _rows(x, "x", shape, dtype, device)
     if codes is not None and codes.dtype not in _CODES:
         raise ValueError(f"codes: float8_e4m3fn or uint8 expected, got {codes.dtype}")
     buf = bytearray(_NORM_CALL.size)
     _NORM_CALL.pack_into(buf, 0, *shape, _elem(x), _ELEM[pdtype], eps, *x_rows,
-                         *(_ABSENT if residual is None else _rows(residual, "residual", shape, dtype)),
-                         *(_ABSENT if y is None else _rows(y, "y", shape, dtype)),
-                         *(_ABSENT if sum_out is None else _rows(sum_out, "sum_out", shape, dtype)))
+                         *(_ABSENT if residual is None else _rows(residual, "residual", shape, dtype, device)),
+                         *(_ABSENT if y is None else _rows(y, "y", shape, dtype, device)),
+                         *(_ABSENT if sum_out is None else _rows(sum_out, "sum_out", shape, dtype, device)))
     a = _address(buf)
     r = a + _NORM_ROWS
-    _check(_lib.moe_rms_norm(a, r, r + _ROWS_BYTES, _dense(weight, "weight", shape[1:], pdtype), r + 2 * _ROWS_BYTES,
-                             r + 3 * _ROWS_BYTES, _dense(rstd, "rstd", shape[:1], torch.float32),
-                             None if codes is None else _dense(codes, "codes", shape, codes.dtype),
-                             _dense(scales, "scales", (shape[0], -(-shape[1] // 128)), torch.float32),
+    _check(_lib.moe_rms_norm(a, r, r + _ROWS_BYTES, _dense(weight, "weight", shape[1:], pdtype, device),
+                             r + 2 * _ROWS_BYTES, r + 3 * _ROWS_BYTES,
+                             _dense(rstd, "rstd", shape[:1], torch.float32, device),
+                             None if codes is None else _dense(codes, "codes", shape, codes.dtype, device),
+                             _dense(scales, "scales", (shape[0], -(-shape[1] // 128)), torch.float32, device),
                              _stream(stream)), "moe_rms_norm")
 
 
@@ -759,11 +768,12 @@ def moe_rms_norm_workspace_size(rows: int, H: int) -> int:
     return out.value
 
 
-def _workspace(workspace: Optional[torch.Tensor]):
+def _workspace(workspace: Optional[torch.Tensor], device: int):
     if workspace is None:
         return None, 0
-    if not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace: contiguous device tensor expected")
+    _on_device(workspace, "workspace", device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous tensor expected")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -776,19 +786,19 @@ def moe_rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: Optiona
     the norm.  workspace is needed for grad_weight (float [H])."""
     shape, dtype, f32 = _matrix(h, "h"), h.dtype, torch.float32
     pdtype = _param_dtype(h, weight, None)
-    h_rows = _rows(h, "h", shape, dtype)
-    _on_current_device(h, "h")
+    device = torch.cuda.current_device()
+    h_rows = _rows(h, "h", shape, dtype, device)
     buf = bytearray(_NORM_CALL.size)
-    _NORM_CALL.pack_into(buf, 0, *shape, _elem(h), _ELEM[pdtype], 0.0, *_rows(grad_y, "grad_y", shape, dtype),
-                         *h_rows,
-                         *(_ABSENT if grad_sum is None else _rows(grad_sum, "grad_sum", shape, dtype)),
-                         *_rows(grad_x, "grad_x", shape, dtype))
+    _NORM_CALL.pack_into(buf, 0, *shape, _elem(h), _ELEM[pdtype], 0.0,
+                         *_rows(grad_y, "grad_y", shape, dtype, device), *h_rows,
+                         *(_ABSENT if grad_sum is None else _rows(grad_sum, "grad_sum", shape, dtype, device)),
+                         *_rows(grad_x, "grad_x", shape, dtype, device))
     a = _address(buf)
     r = a + _NORM_ROWS
-    _check(_lib.moe_rms_norm_backward(a, r, r + _ROWS_BYTES, _dense(weight, "weight", shape[1:], pdtype),
-                                      _dense(rstd, "rstd", shape[:1], f32), r + 2 * _ROWS_BYTES, r + 3 * _ROWS_BYTES,
-                                      _dense(grad_weight, "grad_weight", shape[1:], f32), *_workspace(workspace),
-                                      _stream(stream)), "moe_rms_norm_backward")
+    _check(_lib.moe_rms_norm_backward(a, r, r + _ROWS_BYTES, _dense(weight, "weight", shape[1:], pdtype, device),
+                                      _dense(rstd, "rstd", shape[:1], f32, device), r + 2 * _ROWS_BYTES,
+                                      r + 3 * _ROWS_BYTES, _dense(grad_weight, "grad_weight", shape[1:], f32, device),
+                                      *_workspace(workspace, device), _stream(stream)), "moe_rms_norm_backward")
 
 
 def moe_grouped_gemm_workspace_size(shape: Shape, layout: Layout, N: int, Kd: int) -> int:
@@ -804,19 +814,13 @@ _ROUTED = "8Q5q2q"
 _SHAPE_AT, _LAYOUT_AT, _ROUTED_BYTES = 64, 104, 120
 
 
-def _on_current_device(t: torch.Tensor, name: str):
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: a tensor of the current device expected, got {t.device}")
-
-
-def _routed(handle: Handle, shape: Shape, layout: Layout):
+def _routed(handle: Handle, shape: Shape, layout: Layout, device: int):
     arrays = []
     for name in ("tokens_per_expert", "padded_offsets", "token_of", "status"):
         t = getattr(handle, name)
-        if not (t.is_cuda and t.is_contiguous()):
-            raise ValueError(f"handle.{name}: contiguous device tensor expected")
+        if t.get_device() != device or not t.is_contiguous():
+            raise ValueError(f"handle.{name}: contiguous tensor of the current device (cuda:{device}) expected")
         arrays.append(t.data_ptr())
-    _on_current_device(handle.padded_offsets, "handle.padded_offsets")
     counts, offsets, token_of, status = arrays
     return (counts, offsets, 0, token_of, 0, 0, 0, status, shape.T, shape.H, shape.E, shape.K, shape.I,
             layout.pad_multiple, layout.capacity)
@@ -827,14 +831,15 @@ _GEMM_AT, _GEMM_ROWS = _ROUTED_BYTES, _ROUTED_BYTES + 24
 
 
 def _gemm_call(handle: Handle, shape: Shape, layout: Layout, N: int, Kd: int, dtype: torch.dtype, rows):
-    """(buffer, its address); rows: (name, tensor, columns) of two row matrices."""
+    """(buffer, its address, current device); rows: (name, tensor, columns) of two row matrices."""
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"bfloat16 or float16 expected, got {dtype}")
-    buf = bytearray(_GEMM_CALL.size)
+    buf, device = bytearray(_GEMM_CALL.size), torch.cuda.current_device()
     (n0, t0, c0), (n1, t1, c1) = rows
-    _GEMM_CALL.pack_into(buf, 0, *_routed(handle, shape, layout), N, Kd, _ELEM[dtype],
-                         *_rows(t0, n0, (layout.capacity, c0), dtype), *_rows(t1, n1, (layout.capacity, c1), dtype))
-    return buf, _address(buf)
+    _GEMM_CALL.pack_into(buf, 0, *_routed(handle, shape, layout, device), N, Kd, _ELEM[dtype],
+                         *_rows(t0, n0, (layout.capacity, c0), dtype, device),
+                         *_rows(t1, n1, (layout.capacity, c1), dtype, device))
+    return buf, _address(buf), device
 
 
 def _expert_matrices(weight: torch.Tensor, name: str, shape: Shape):
@@ -847,11 +852,11 @@ def moe_grouped_gemm(handle: Handle, shape: Shape, layout: Layout, weight: torch
                      y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """y[r] = weight[e] @ x[r] for the routed rows r of expert e: weight [E, N, Kd], x [cap, Kd], y [cap, N]."""
     N, Kd = _expert_matrices(weight, "weight", shape)
-    buf, a = _gemm_call(handle, shape, layout, N, Kd, weight.dtype, (("x", x, Kd), ("y", y, N)))
+    buf, a, device = _gemm_call(handle, shape, layout, N, Kd, weight.dtype, (("x", x, Kd), ("y", y, N)))
     r = a + _GEMM_ROWS
     _check(_lib.moe_grouped_gemm(a, a + _SHAPE_AT, a + _LAYOUT_AT, a + _GEMM_AT,
-                                 _dense(weight, "weight", weight.shape, weight.dtype), r, r + _ROWS_BYTES,
-                                 *_workspace(workspace), _stream(stream)), "moe_grouped_gemm")
+                                 _dense(weight, "weight", weight.shape, weight.dtype, device), r, r + _ROWS_BYTES,
+                                 *_workspace(workspace, device), _stream(stream)), "moe_grouped_gemm")
 
 
 def moe_grouped_gemm_backward_data(handle: Handle, shape: Shape, layout: Layout, weight: torch.Tensor,
@@ -859,12 +864,13 @@ def moe_grouped_gemm_backward_data(handle: Handle, shape: Shape, layout: Layout,
                                    stream=None) -> None:
     """grad_x[r] = weight[e].T @ grad_y[r] for the routed rows r of expert e: grad_y [cap, N], grad_x [cap, Kd]."""
     N, Kd = _expert_matrices(weight, "weight", shape)
-    buf, a = _gemm_call(handle, shape, layout, N, Kd, weight.dtype, (("grad_y", grad_y, N), ("grad_x", grad_x, Kd)))
+    buf, a, device = _gemm_call(handle, shape, layout, N, Kd, weight.dtype,
+                                (("grad_y", grad_y, N), ("grad_x", grad_x, Kd)))
     r = a + _GEMM_ROWS
     _check(_lib.moe_grouped_gemm_backward_data(
         a, a + _SHAPE_AT, a + _LAYOUT_AT, a + _GEMM_AT,
-        _dense(weight, "weight", weight.shape, weight.dtype), r, r + _ROWS_BYTES, *_workspace(workspace),
-        _stream(stream)), "moe_grouped_gemm_backward_data")
+        _dense(weight, "weight", weight.shape, weight.dtype, device), r, r + _ROWS_BYTES,
+        *_workspace(workspace, device), _stream(stream)), "moe_grouped_gemm_backward_data")
 
 
 def moe_grouped_gemm_backward_weight(handle: Handle, shape: Shape, layout: Layout, x: torch.Tensor,
@@ -873,13 +879,13 @@ def moe_grouped_gemm_backward_weight(handle: Handle, shape: Shape, layout: Layou
     """grad_weight[e] = sum of outer(grad_y[r], x[r]) over the routed rows r of e (+ addend[e]): grad_weight
     [E, N, Kd] of the rows' type or float; addend float, maybe grad_weight itself."""
     N, Kd = _expert_matrices(grad_weight, "grad_weight", shape)
-    buf, a = _gemm_call(handle, shape, layout, N, Kd, x.dtype, (("x", x, Kd), ("grad_y", grad_y, N)))
+    buf, a, device = _gemm_call(handle, shape, layout, N, Kd, x.dtype, (("x", x, Kd), ("grad_y", grad_y, N)))
     r = a + _GEMM_ROWS
     _check(_lib.moe_grouped_gemm_backward_weight(
         a, a + _SHAPE_AT, a + _LAYOUT_AT, a + _GEMM_AT, r, r + _ROWS_BYTES, _elem(grad_weight),
-        _dense(addend, "addend", grad_weight.shape, torch.float32),
-        _dense(grad_weight, "grad_weight", grad_weight.shape, grad_weight.dtype), *_workspace(workspace),
-        _stream(stream)), "moe_grouped_gemm_backward_weight")
+        _dense(addend, "addend", grad_weight.shape, torch.float32, device),
+        _dense(grad_weight, "grad_weight", grad_weight.shape, grad_weight.dtype, device),
+        *_workspace(workspace, device), _stream(stream)), "moe_grouped_gemm_backward_weight")
 
 
 _SWIGLU_CALL = struct.Struct("=" + _ROUTED + "qq" * 3)  # then three moe_rows
@@ -889,13 +895,14 @@ def moe_swiglu(handle: Handle, shape: Shape, layout: Layout, pre: torch.Tensor, 
                probs: Optional[torch.Tensor] = None, stream=None) -> None:
     """act[r] = probs[r] * silu(gate) * up for the routed rows: pre [cap, 2 I] = up columns, then gate; act [cap, I]."""
     cap, I = layout.capacity, _matrix(act, "act")[1]
-    buf = bytearray(_SWIGLU_CALL.size)
-    _SWIGLU_CALL.pack_into(buf, 0, *_routed(handle, shape, layout), *_rows(pre, "pre", (cap, 2 * I), pre.dtype),
-                           *_rows(act, "act", (cap, I), pre.dtype), *_ABSENT)
+    buf, device = bytearray(_SWIGLU_CALL.size), torch.cuda.current_device()
+    _SWIGLU_CALL.pack_into(buf, 0, *_routed(handle, shape, layout, device),
+                           *_rows(pre, "pre", (cap, 2 * I), pre.dtype, device),
+                           *_rows(act, "act", (cap, I), pre.dtype, device), *_ABSENT)
     a = _address(buf)
     r = a + _ROUTED_BYTES
     _check(_lib.moe_swiglu(a, a + _SHAPE_AT, a + _LAYOUT_AT, I, _elem(pre), r,
-                           _dense(probs, "probs", (cap,), torch.float32), r + _ROWS_BYTES, _stream(stream)),
+                           _dense(probs, "probs", (cap,), torch.float32, device), r + _ROWS_BYTES, _stream(stream)),
            "moe_swiglu")
 
 
@@ -904,16 +911,18 @@ def moe_swiglu_backward(handle: Handle, shape: Shape, layout: Layout, pre: torch
                         grad_probs: Optional[torch.Tensor] = None, stream=None) -> None:
     """Gradients of moe_swiglu: grad_pre [cap, 2 I] (maybe pre itself) and grad_probs (float [cap])."""
     cap, I = layout.capacity, _matrix(grad_act, "grad_act")[1]
-    buf = bytearray(_SWIGLU_CALL.size)
-    _SWIGLU_CALL.pack_into(buf, 0, *_routed(handle, shape, layout), *_rows(pre, "pre", (cap, 2 * I), pre.dtype),
-                           *_rows(grad_act, "grad_act", (cap, I), pre.dtype),
-                           *_rows(grad_pre, "grad_pre", (cap, 2 * I), pre.dtype))
+    buf, device = bytearray(_SWIGLU_CALL.size), torch.cuda.current_device()
+    _SWIGLU_CALL.pack_into(buf, 0, *_routed(handle, shape, layout, device),
+                           *_rows(pre, "pre", (cap, 2 * I), pre.dtype, device),
+                           *_rows(grad_act, "grad_act", (cap, I), pre.dtype, device),
+                           *_rows(grad_pre, "grad_pre", (cap, 2 * I), pre.dtype, device))
     a = _address(buf)
     r = a + _ROUTED_BYTES
     _check(_lib.moe_swiglu_backward(a, a + _SHAPE_AT, a + _LAYOUT_AT, I, _elem(pre), r,
-                                    _dense(probs, "probs", (cap,), torch.float32), r + _ROWS_BYTES,
-                                    r + 2 * _ROWS_BYTES, _dense(grad_probs, "grad_probs", (cap,), torch.float32),
-                                    _stream(stream)), "moe_swiglu_backward")
+                                    _dense(probs, "probs", (cap,), torch.float32, device), r + _ROWS_BYTES,
+                                    r + 2 * _ROWS_BYTES,
+                                    _dense(grad_probs, "grad_probs", (cap,), torch.float32, device), _stream(stream)),
+           "moe_swiglu_backward")
 
 
 class Ring:
