@@ -208,6 +208,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // every stage that was filled has been read: no commit of the pair is still on its
+      // way to either CTA when they leave
+      for (int s = 0; s < kStages && ok; s++) {
+        if (!mbar_wait(&s_empty[stage], phase ^ 1, abort_flag, p.status)) ok = false;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
       if (!ok) {
         if (rank == 0) {
           for (int s = 0; s < kStages; s++) {

@@ -76,6 +76,27 @@ def test_grouped_mlp_bf16_all_rows(oracle, moe, name, w):
     assert layer_rel_err(oracle.bf16_to_f64(bits(r["out"])), oracle.bf16_to_f64(ref), o_rows, wts) <= TOL_BF16
 
 
+def test_pairs_behind_one_another(moe):
+    """The kernels on pairs of SMs, one call behind the other: both CTAs of a pair stay until the commits of their last
+    stages have arrived, and every call gives the first one's bits."""
+    w = _case("tiny", T=4160, H=512, E=2, K=2, I=256)
+    r = run_layer_bf16(moe, w, seed=21)
+    shape, layout = moe.Shape(w.T, w.H, w.E, w.K, w.I), moe.Layout(w.m, r["cap"])
+    assert moe.moe_grouped_mlp_kernel_count(shape, layout, moe.DTYPE_BF16) == 2
+    y = torch.zeros(r["cap"], w.H, dtype=torch.bfloat16, device="cuda")
+    yp = torch.empty(r["cap"], device="cuda")
+    routing = moe.Routing(r["fmt"], torch.from_numpy(r["rmap"]).cuda(), torch.from_numpy(r["probs"]).cuda())
+    moe.moe_dispatch_permute(r["handle"], shape, layout, moe.DTYPE_BF16, r["x"].cuda(), None, routing, y, yp)
+    ws = torch.empty(moe.moe_grouped_mlp_workspace_size(shape, layout, moe.DTYPE_BF16), dtype=torch.uint8, device="cuda")
+    valid = int(r["handle"].total_rows.item())
+    for _ in range(100):
+        o = torch.zeros(r["cap"], w.H, dtype=torch.bfloat16, device="cuda")
+        moe.moe_grouped_mlp(r["handle"], shape, layout, moe.DTYPE_BF16, y, None, r["w13"], None, r["w2"], None, None, ws, o)
+    torch.cuda.synchronize()
+    assert int(r["handle"].status.item()) == 0
+    assert torch.equal(o[:valid], r["o"][:valid])
+
+
 def _sampled_check(oracle, w, r, n_tokens=48, seed=0, edges=False):
     """Oracle on a sample of tokens (all their routes) at full size; with
     edges, also the first and last valid row of every expert segment."""
