@@ -18,7 +18,8 @@
 //               the contraction a stage: one copy each (a thread issues a copy in about 120
 //               cycles, whatever its bytes; four of 8 KB a stage were what the weights'
 //               gradient waited for)
-//   warp 1      TMEM; on the leader one elected lane issues the MMAs
+//   warp 1      TMEM; on the leader one elected lane issues the MMAs (PIECES: on the
+//               other CTA one tells the leader of the stages that were filled there)
 //   warp 2      on the leader: claims tiles and hands their numbers to both CTAs
 //   warps 4..   epilogue of this CTA's 128 features, beside the next tile's MMAs
 //   PIECES: the last eight warps bring operands into place
@@ -397,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
   constexpr int kEpi = kEpilogue<DIR, PIECES>;
   constexpr bool kW = DIR == kWeight, kAmn = DIR != kForward, kBmn = kW;
   extern __shared__ uint8_t dyn_smem[];
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_tfull[2], s_tempty[2];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_placed[kStages], s_tfull[2], s_tempty[2];
   __shared__ __align__(8) uint64_t s_raw[kRaw], s_raw_free[kRaw];  // PIECES, each CTA's own
   __shared__ __align__(8) uint64_t s_have[kSlots], s_free[kSlots], s_drain;
   __shared__ Tile s_tile[kSlots];
@@ -415,8 +416,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     s_abort = s_filled = 0;
     for (int s = 0; s < kStages; s++) {
       // on the leader: its producer and both CTAs' bytes; PIECES: every warp that fills it
-      mbar_init(&s_full[s], PIECES ? 2 * kPieceWarps : 1);
-      mbar_init(&s_empty[s], 1);  // each CTA's own, by the leader's commit
+      // there, and the other CTA's warp 1 for all that do here
+      mbar_init(&s_full[s], PIECES ? kPieceWarps + 1 : 1);
+      mbar_init(&s_empty[s], 1);             // each CTA's own, by the leader's commit
+      mbar_init(&s_placed[s], kPieceWarps);  // PIECES, the other CTA's own
     }
     for (int a = 0; a < 2; a++) {
       mbar_init(&s_tfull[a], 1);
@@ -424,9 +427,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
     }
     for (int s = 0; s < kSlots; s++) {
       mbar_init(&s_have[s], 1);
-      // on the leader, every reader of both CTAs: its warp 1, and in each the producers,
-      // the epilogue's and the pieces' warps
-      mbar_init(&s_free[s], 1 + 2 * (2 + kEpi + (PIECES ? kPieceWarps : 0)));
+      // on the leader, every reader of both CTAs: its warp 1 (PIECES: both CTAs'), and in
+      // each the producers, the epilogue's and the pieces' warps
+      mbar_init(&s_free[s], (PIECES ? 2 : 1) + 2 * (2 + kEpi + (PIECES ? kPieceWarps : 0)));
     }
     for (int s = 0; s < kRaw; s++) {
       mbar_init(&s_raw[s], 1);
@@ -608,6 +611,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         settle(2000000);  // 2 ms: far longer than any single copy takes
       }
     }
+  } else if (PIECES && rank == 1 && warp == 1) {
+    // ------------------------------ tells the leader of the stages filled here
+    // The warps that fill a stage arrive in their own CTA, which orders their writes
+    // before this lane's one arrival in the leader, at the cluster's scope, and so before
+    // the MMAs that read them (8191 x 8191 x 8192: 1584 us; each warp arriving there by
+    // itself 1681; an arrival that orders accesses to global memory too 2154).
+    if (elect_one_lane()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0; ok; i++) {
+        Tile ti;
+        if (!take_tile(i, ti)) break;
+        for (int kb = 0; kb < ti.blocks; kb++) {
+          if (!mbar_wait(&s_placed[stage], phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_leader(mapa_shared(smem_u32(&s_full[stage]), 0));
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer (leader)
     // One elected lane waits and issues, the others stay at the end: known to be one,
@@ -723,10 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<DIR, PIECES
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&s_raw_free[raw]);
-          if (rank == 0)
-            mbar_arrive(&s_full[stage]);
-          else
-            mbar_arrive_leader(mapa_shared(smem_u32(&s_full[stage]), 0));
+          mbar_arrive(rank == 0 ? &s_full[stage] : &s_placed[stage]);
         }
         if (++raw == kRaw) {
           raw = 0;
