@@ -734,8 +734,8 @@ MOE_API moe_status moe_grouped_gemm_workspace_size(const moe_shape* shape, const
  * any segment may be empty.  A NaN or infinity of a row stays in it, one of a weight
  * in its output feature.  Rows and weights may begin at any element: where bases
  * are 16-byte aligned and strides, N and Kd multiples of 8 the copies bring them into
- * place by themselves, others are shifted on the way (at two to three times the
- * time where products bind).  y overlaps neither x nor the weights.  (capacity / 256 +
+ * place by themselves, others are shifted on the way (at about twice the time, more
+ * for small calls).  y overlaps neither x nor the weights.  (capacity / 256 +
  * E) * (N / 256 + 1) has to stay below 2^30, as it does in any memory. */
 MOE_API moe_status moe_grouped_gemm(const moe_handle_dev* handle, const moe_shape* shape, const moe_layout* layout,
                                     const moe_gemm* gemm, const void* weight, const moe_rows* x, const moe_rows* y,
@@ -755,9 +755,8 @@ MOE_API moe_status moe_grouped_gemm_backward_data(const moe_handle_dev* handle, 
  * Sums in fp32, rounded to grad_dtype (dtype or MOE_ELEM_F32) once, in parts as in
  * moe_grouped_gemm; fp32 gradients are summed 768 rows at a time (short by 4e-6), and
  * these parts added in order by roundings to nearest (a subnormal part may count as
- * zero).  Every element is written, zeros (or
- * the addend) for an expert without rows.  addend: device
- * fp32, laid out as grad_weight, only with MOE_ELEM_F32; it may be grad_weight
+ * zero).  Every element is written, zeros (or the addend) for an expert without rows.
+ * addend: device fp32, laid out as grad_weight, only with MOE_ELEM_F32; it may be grad_weight
  * itself, which then gathers the gradients of several steps, and must not overlap
  * it otherwise.  Pad rows take no part, whatever they hold.  capacity: up to 2^27
  * rows (MOE_ERR_UNSUPPORTED above). */

@@ -28,14 +28,17 @@
 //
 // Device times on one GB300, beside the floor by a copy's 6796 GB/s or 1880 TFLOP/s
 // and what bounds them:
-//   1 token, 8 of 256 experts, 7168 x 2048 bf16       42 us,  83 %  launch, HBM
-//   64 tokens, the same                              940 us, 100 %  HBM
-//   8192 tokens, 256 experts, 4096 x 7168, uneven   3.3 ms,  73 %  HBM and MMAs, not together
-//   4096 tokens, 64 experts, 2048 x 2048             204 us,  72 %  copies into shared memory
-//     its weights' gradient in fp32                  275 us,  72 %  stores beside the copies
-//   8192 x 8192 x 8192 over 8 experts                692 us,  84 %  MMAs (power), last tiles
-//     its weights' gradient in bf16 / fp32           743 / 959 us
-//   the same of 8191 x 8191                         1.61 ms,  36 %  shifting into place
+//   1 token, 8 of 256 experts, 7168 x 2048 bf16       42 us,  82 %  launch, HBM
+//   64 tokens, the same                              950 us, 101 %  HBM
+//   8192 tokens, 256 experts, 4096 x 7168, uneven   3.4 ms,  72 %  HBM and MMAs, not together
+//     its weights' gradient in bf16 / fp32           4.0 / 5.8 ms, 61 / 79 %; added to itself 20.7 ms
+//   4096 tokens, 64 experts, 2048 x 2048             210 us,  70 %  copies into shared memory
+//     its weights' gradient in fp32                  266 us,  74 %  stores beside the copies
+//       added to itself                              730 us,  49 %  reads of the old one
+//   8192 x 8192 x 8192 over 8 experts                700 us,  84 %  MMAs (power), last tiles
+//     its weights' gradient in bf16 / fp32           720 / 948 us
+//   the same of 8191 x 8191                         1.59 ms,  37 %  shifting into place
+// (the middle of several boxes, which differ by up to 3 %)
 // An SM takes in 64 bytes a cycle at the most, which is what a whole tile needs at the
 // MMAs' full rate: tiles of fewer rows wait for their copies.
 #include <type_traits>
@@ -63,7 +66,7 @@ constexpr int kThreads = 128 + 32 * (kEpilogue<DIR, PIECES> + (PIECES ? kPieceWa
 // bits to lose), 8192 by 4e-5 and 5e-5.  So sums are made of parts, added to one another
 // by rounding, and no shorter however long they are.  fp32 gradients: parts of at most
 // 12 stages (768 rows), added on their way to memory; 8192 x 8192 of 1024 rows an expert
-// take 959 us so, 867 in one part.  Results of 16 bits: parts of 128 stages, a tenth of
+// took 959 us so, 867 in one part.  Results of 16 bits: parts of 128 stages, a tenth of
 // f16's rounding each, joined in TMEM by the epilogue (one sum of 2^20 was short by
 // 7e-3; 2048 x 2048 x 65536 over 2 experts: 363 us, in one part 358).
 template <GemmDir DIR, typename OUT>
@@ -327,7 +330,7 @@ MOE_DEVICE uint4 first_of(uint4 v, int n) {
 // thread and from stage to stage lie multiples of eight rows and of 64 elements, so
 // that a thread's elements keep their place in their pieces.  A warp's rows are eight
 // apart too, so that one branch a stage finds the words of all its pieces, and reads of
-// an operand's pieces all go out before the first is written (8191 x 8191 x 8192:
+// an operand's pieces all go out before the first is written (8191 x 8191 x 8192, then:
 // 1.61 ms; four rows next to each other in a warp, each thread selecting its words,
 // 1.70; reading and writing in turn besides, 1.96).
 template <bool KMAJOR>
